@@ -324,6 +324,128 @@ int moe_layer_forward(const moe_desc* desc, const void* x, const void* Wg,
                       void* stream);
 
 /*
+ * Training.  The gradient of the layer in its steps, for a program that ran
+ * the forward pass with the separate calls above and kept what they wrote:
+ *   moe_combine_backward -> moe_expert_ffn_backward -> moe_dispatch_backward
+ * and the optimiser's step, moe_adamw_step.  The pages describe inference and
+ * name training only in passing; these are the calculus of the formulas above.
+ */
+
+/*
+ * Gradient of moe_combine: from dout, the gradient of out,
+ *   dy_perm[pos[s]] = w[s] * dout[t]            for each kept slot s = t*K + j
+ *   dw[s]           = <dout[t], y_perm[pos[s]]> in fp32; 0 for a dropped slot
+ *   dout [T, H] dtype; y_perm [moe_max_rows, H] dtype (the forward pass's; not
+ *   read if dw is NULL, may be NULL then); pos [T*K] int32; w [T, K] fp32
+ *   dy_perm [moe_max_rows, H] dtype out or NULL: rows that no slot holds are
+ *   left as they are
+ *   dw [T, K] fp32 out or NULL
+ * Deterministic.
+ */
+int moe_combine_backward(const moe_desc* desc, const void* dout, const void* y_perm, const int32_t* pos,
+                         const float* w, void* dy_perm, float* dw, void* stream);
+
+/*
+ * Gradient of moe_dispatch's copy x_perm[pos[s]] = x[t]:
+ *   dx[t] = sum_j dx_perm[pos[t*K + j]] (+ dx_add[t])
+ * summed in fp32 over the kept slots in the order j = 0..K-1, then dx_add.
+ *   dx_perm [moe_max_rows, H] dtype; pos [T*K] int32
+ *   dx_add [T, H] dtype or NULL: what other paths of the same x have (the
+ *   residual's, the gate's); may be dx itself
+ *   dx [T, H] dtype out; a token without a kept slot gets dx_add, or zeros
+ */
+int moe_dispatch_backward(const moe_desc* desc, const void* dx_perm, const int32_t* pos, const void* dx_add,
+                          void* dx, void* stream);
+
+/* Bytes of device workspace moe_expert_ffn_backward needs for `desc`: the
+ * error word (moe_get_device_error reads it; clear its 256 bytes once) and the
+ * hidden gradients, which a call writes before it reads them.  Returns
+ * MOE_ERR_INVALID for a bad desc. */
+int moe_backward_workspace_size(const moe_desc* desc, size_t* bytes);
+
+/*
+ * Gradient of moe_expert_ffn.  For each expert e and its rows r in
+ * [offs[e], offs[e+1]), with a = W1[e] x_perm[r] + b1[e] computed again:
+ *   dh  = W2[e]^T dy_perm[r],  da = dh * GELU'(a)
+ *   dx_perm[r] = W1[e]^T da
+ *   dW1[e] = sum_r da x_perm[r]^T,     db1[e] = sum_r da
+ *   dW2[e] = sum_r dy_perm[r] h_perm[r]^T,  db2[e] = sum_r dy_perm[r]
+ * (zeros for an expert without a row).  With MOE_FLAG_SWIGLU a holds the
+ * gate's and the up projection's columns, W1, b1, dW1 and db1 are stacked as
+ * in moe_expert_ffn, and h = SiLU(gate) * up is what is differentiated.
+ *   x_perm [moe_max_rows, H], h_perm [moe_max_rows, F] (as moe_expert_ffn wrote
+ *   it; NULL if dW2 is), dy_perm [moe_max_rows, H] dtype; rows from offs[E] on
+ *   may hold anything
+ *   W1, b1 (nullable), W2: the forward pass's
+ *   dx_perm [moe_max_rows, H] dtype out or NULL; rows from offs[E] on are left
+ *   as they are
+ *   dW1, dW2 dtype out, shaped as W1 and W2, or NULL; db1, db2 fp32 out
+ *   ([E, F] or [E, 2F], and [E, H]) or NULL.  Results are written, not added.
+ * On the bf16 path products are accumulated in fp32; da is rounded to bf16 as
+ * an operand of the products after it, the bias gradients sum it before that.
+ * Deterministic.  bf16 runs on the tensor cores, fp32 (and MOE_FLAG_SIMT_FFN)
+ * on CUDA cores.
+ */
+int moe_expert_ffn_backward(const moe_desc* desc, const void* x_perm, const void* h_perm, const void* dy_perm,
+                            const int32_t* offs, const void* W1, const float* b1, const void* W2, void* dx_perm,
+                            void* dW1, float* db1, void* dW2, float* db2, void* ws, size_t ws_bytes, void* stream);
+
+/* Elements that share a scale in 8-bit moments. */
+#define MOE_ADAMW_BLOCK 256
+
+/*
+ * One parameter tensor of moe_adamw_step: device pointers, n elements each,
+ * aligned to their element (vector accesses are used where p, p_bf16, grad, m
+ * and v are all 16-byte aligned).  Tensors of one call must not overlap.
+ *   p [n] fp32; p_bf16 [n] bf16 or NULL: receives p rounded to bf16
+ *   grad [n]: fp32 or bf16 (grad_dtype of the call)
+ *   state_bits 32: m, v [n] fp32; m_scale, v_scale NULL
+ *   state_bits 8: m, v [n] e4m3 codes of m and of sqrt(v); m_scale, v_scale
+ *     [ceil(n / MOE_ADAMW_BLOCK)] fp32: a value is its code times the scale of
+ *     its block of MOE_ADAMW_BLOCK elements.  Zeroed buffers are the start.
+ *   weight_decay: decoupled, for this tensor
+ */
+typedef struct moe_adamw_tensor {
+  float* p;
+  void* p_bf16;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  float weight_decay;
+  int32_t reserved;      /* 0 */
+} moe_adamw_tensor;
+
+/* lr >= 0, 0 <= beta1, beta2 < 1, eps >= 0, all finite; step = 1 for the first. */
+typedef struct moe_adamw_params {
+  double lr;
+  double beta1;
+  double beta2;
+  double eps;
+  int64_t step;
+} moe_adamw_params;
+
+/*
+ * One AdamW step over `count` tensors, in place, in one launch for up to 400
+ * of them:
+ *   g = grad * (grad_scale ? *grad_scale : 1)
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, the moments of this step before they are rounded to 8 bits.
+ *   tensors: host array, read during the call only
+ *   grad_dtype: moe_dtype of every grad; state_bits: 32 or 8, for every tensor
+ *   grad_scale [1] fp32 device or NULL (a clipping or loss-scale factor)
+ *   skip [1] int32 device or NULL: nothing is changed if it is not 0
+ * 8-bit moments are rounded to nearest; a block of moments with a NaN or an
+ * infinity reads back as NaN throughout (guard it with skip).
+ */
+int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t grad_dtype, int32_t state_bits,
+                   const moe_adamw_params* params, const float* grad_scale, const int32_t* skip, void* stream);
+
+/*
  * How many kernels one moe_layer_forward with this description launches
  * (no counterpart on the pages; it lets a caller or a benchmark account for
  * the launches it issues).  Depends on the shape only: the path taken

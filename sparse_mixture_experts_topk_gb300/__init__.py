@@ -26,6 +26,9 @@ __all__ = [
     "MOE_FFN_STREAM", "MOE_FFN_SIMT", "MOE_FFN_TC_SINGLE", "MOE_FFN_TC_PAIRS", "MOE_FFN_TC_FUSED",
     "MOE_FFN_STREAM_SPLIT", "workspace", "MOE_OK", "MOE_ERR_INVALID", "MOE_ERR_UNSUPPORTED", "MOE_ERR_WORKSPACE",
     "MOE_ERR_CUDA", "MOE_ERR_TIMEOUT", "MOE_ERR_DEVICE",
+    "moe_combine_backward", "moe_dispatch_backward", "moe_backward_workspace_size", "backward_workspace",
+    "moe_expert_ffn_backward", "moe_adamw_step", "MOE_ADAMW_BLOCK", "MoeAdamwTensor", "MoeAdamwParams",
+    "AdamwTensors", "adamw_tensors", "make_adamw",
 ]
 
 MOE_F32, MOE_BF16 = 0, 1
@@ -45,6 +48,8 @@ MOE_FLAG_DECODE_SPLIT = 1 << 12
 MOE_FLAG_GATHER_GEMM = 1 << 13
 # moe_ffn_kernel results
 MOE_FFN_STREAM, MOE_FFN_SIMT, MOE_FFN_TC_SINGLE, MOE_FFN_TC_PAIRS, MOE_FFN_TC_FUSED, MOE_FFN_STREAM_SPLIT = 0, 1, 2, 3, 4, 5
+
+MOE_ADAMW_BLOCK = 256   # elements that share a scale in 8-bit moments
 
 # status codes (MoeError.code)
 MOE_OK = 0
@@ -67,6 +72,18 @@ class MoeDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("temperature", ctypes.c_float)]
 
 
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("p_bf16", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class MoeAdamwParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -86,6 +103,12 @@ _SIGS = {
     "moe_layer_launches": (ctypes.c_int, [ctypes.POINTER(MoeDesc)]),
     "moe_ffn_kernel": (ctypes.c_int, [ctypes.POINTER(MoeDesc)]),
     "moe_layer_decode_fused": (ctypes.c_int, [ctypes.POINTER(MoeDesc)]),
+    "moe_combine_backward": (ctypes.c_int, [ctypes.POINTER(MoeDesc)] + [_P] * 7),
+    "moe_dispatch_backward": (ctypes.c_int, [ctypes.POINTER(MoeDesc)] + [_P] * 5),
+    "moe_backward_workspace_size": (ctypes.c_int, [ctypes.POINTER(MoeDesc), ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_expert_ffn_backward": (ctypes.c_int, [ctypes.POINTER(MoeDesc)] + [_P] * 13 + [ctypes.c_size_t, _P]),
+    "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(MoeAdamwTensor), ctypes.c_int32, ctypes.c_int32,
+                                      ctypes.c_int32, ctypes.POINTER(MoeAdamwParams), _P, _P, _P]),
 }
 
 _lib = None
@@ -241,6 +264,110 @@ def moe_get_device_error(ws, stream=None) -> int:
     _check("moe_get_device_error", lib().moe_get_device_error(_ptr(ws), ctypes.byref(code),
                                                               _stream(stream)))
     return int(code.value)
+
+
+def moe_combine_backward(desc, dout, y_perm, pos, w, dy_perm, dw, stream=None):
+    _check("moe_combine_backward", lib().moe_combine_backward(
+        ctypes.byref(desc), _ptr(dout), _ptr(y_perm), _ptr(pos), _ptr(w), _ptr(dy_perm), _ptr(dw),
+        _stream(stream)))
+
+
+def moe_dispatch_backward(desc, dx_perm, pos, dx_add, dx, stream=None):
+    _check("moe_dispatch_backward", lib().moe_dispatch_backward(
+        ctypes.byref(desc), _ptr(dx_perm), _ptr(pos), _ptr(dx_add), _ptr(dx), _stream(stream)))
+
+
+def moe_backward_workspace_size(desc: MoeDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_backward_workspace_size", lib().moe_backward_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return int(n.value)
+
+
+def backward_workspace(desc: MoeDesc, device=None):
+    """A device workspace of ``moe_backward_workspace_size(desc)`` bytes, its error word cleared."""
+    import torch
+    ws = torch.empty(moe_backward_workspace_size(desc), dtype=torch.uint8,
+                     device=device if device is not None else "cuda")
+    ws[:256].zero_()
+    return ws
+
+
+def moe_expert_ffn_backward(desc, x_perm, h_perm, dy_perm, offs, W1, b1, W2, dx_perm, dW1, db1, dW2, db2, ws,
+                            stream=None):
+    _check("moe_expert_ffn_backward", lib().moe_expert_ffn_backward(
+        ctypes.byref(desc), _ptr(x_perm), _ptr(h_perm), _ptr(dy_perm), _ptr(offs), _ptr(W1), _ptr(b1), _ptr(W2),
+        _ptr(dx_perm), _ptr(dW1), _ptr(db1), _ptr(dW2), _ptr(db2), _ptr(ws), ws.numel() if ws is not None else 0,
+        _stream(stream)))
+
+
+class AdamwTensors:
+    """The tensors of a ``moe_adamw_step``, kept by the caller from step to step."""
+
+    def __init__(self, array, count, grad_dtype, state_bits, held):
+        self.array, self.count, self.grad_dtype, self.state_bits = array, count, grad_dtype, state_bits
+        self.held = held          # the tensors the addresses belong to
+
+
+def adamw_tensors(tensors) -> AdamwTensors:
+    """Describe the parameter tensors of an AdamW step once.
+
+    ``tensors``: one dict per parameter tensor with contiguous device tensors
+    ``p`` (fp32), ``g`` (fp32 or bf16, the same for all), ``m`` and ``v`` (both
+    fp32, or both ``torch.float8_e4m3fn`` with fp32 ``m_scale`` and ``v_scale``
+    of one value per ``MOE_ADAMW_BLOCK`` elements), and optionally ``p16``
+    (bf16 copy of p) and ``weight_decay``.  The addresses are read here, so the
+    same tensors have to stay in place for every step that uses the result."""
+    import torch
+    tensors = list(tensors)
+    array = (MoeAdamwTensor * max(1, len(tensors)))()
+    held, grad_dtype, bits = [], None, None
+
+    def need(ok, what):
+        if not ok:
+            raise ValueError(f"adamw_tensors: {what}")
+
+    for i, d in enumerate(tensors):
+        unknown = set(d) - {"p", "p16", "g", "m", "v", "m_scale", "v_scale", "weight_decay"}
+        need(not unknown, f"tensor {i}: unknown fields {sorted(unknown)}")
+        p, g, m, v = d["p"], d["g"], d["m"], d["v"]
+        p16, ms, vs = d.get("p16"), d.get("m_scale"), d.get("v_scale")
+        n = p.numel()
+        need(p.dtype == torch.float32, f"tensor {i}: p is not fp32")
+        need(g.dtype in (torch.float32, torch.bfloat16), f"tensor {i}: g is neither fp32 nor bf16")
+        need(m.dtype == v.dtype and m.dtype in (torch.float32, torch.float8_e4m3fn),
+             f"tensor {i}: m and v are neither both fp32 nor both float8_e4m3fn")
+        b = 8 if m.dtype == torch.float8_e4m3fn else 32
+        gd = MOE_BF16 if g.dtype == torch.bfloat16 else MOE_F32
+        need(grad_dtype in (None, gd) and bits in (None, b), f"tensor {i}: another gradient or moment type than before")
+        grad_dtype, bits = gd, b
+        need((b == 8) == (ms is not None) and (b == 8) == (vs is not None), f"tensor {i}: scales go with 8-bit moments")
+        if b == 8:
+            blocks = -(-n // MOE_ADAMW_BLOCK)
+            need(ms.dtype == vs.dtype == torch.float32 and ms.numel() == vs.numel() == blocks,
+                 f"tensor {i}: scales are not {blocks} fp32 values")
+        need(p16 is None or p16.dtype == torch.bfloat16, f"tensor {i}: p16 is not bf16")
+        for t in (p, g, m, v) + (() if p16 is None else (p16,)):
+            need(t.numel() == n, f"tensor {i}: sizes differ")
+        for t in (p, g, m, v, p16, ms, vs):
+            need(t is None or (t.is_contiguous() and t.device == p.device and t.is_cuda),
+                 f"tensor {i}: not contiguous on one device")
+        array[i] = MoeAdamwTensor(_ptr(p), _ptr(p16), _ptr(g), _ptr(m), _ptr(v), _ptr(ms), _ptr(vs), n,
+                                  float(d.get("weight_decay", 0.0)), 0)
+        held.append(d)
+    return AdamwTensors(array, len(tensors), MOE_F32 if grad_dtype is None else grad_dtype, bits or 32, held)
+
+
+def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1) -> MoeAdamwParams:
+    """The hyperparameters of one step; ``step`` counts from 1."""
+    return MoeAdamwParams(float(lr), float(beta1), float(beta2), float(eps), int(step))
+
+
+def moe_adamw_step(tensors: AdamwTensors, params: MoeAdamwParams, grad_scale=None, skip=None, stream=None):
+    """One AdamW step in place over ``adamw_tensors(...)``; ``grad_scale`` (fp32)
+    and ``skip`` (int32) are one-element device tensors or ``None``."""
+    _check("moe_adamw_step", lib().moe_adamw_step(
+        tensors.array, tensors.count, tensors.grad_dtype, tensors.state_bits, ctypes.byref(params),
+        _ptr(grad_scale), _ptr(skip), _stream(stream)))
 
 
 _prof_events = None

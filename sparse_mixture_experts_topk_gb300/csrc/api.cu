@@ -755,4 +755,104 @@ int moe_get_device_error(void* ws, int32_t* code, void* stream) {
   return MOE_OK;
 }
 
+// ---------------------------------------------------------------- training
+
+int moe_combine_backward(const moe_desc* desc, const void* dout, const void* y_perm, const int32_t* pos,
+                         const float* w, void* dy_perm, float* dw, void* stream) {
+  int rc = check_desc(desc);
+  if (rc) return rc;
+  const moe_desc& d = *desc;
+  if (d.T > 0 && (!dout || !pos || !w || (dw && !y_perm) || (!dy_perm && !dw))) return MOE_ERR_INVALID;
+  if (!aligned16(dout) || !aligned16(dy_perm) || (dw && !aligned16(y_perm))) return MOE_ERR_INVALID;
+  return cuda_status(launch_combine_backward(shape_of(d), dout, y_perm, pos, w, dy_perm, dw, (cudaStream_t)stream));
+}
+
+int moe_dispatch_backward(const moe_desc* desc, const void* dx_perm, const int32_t* pos, const void* dx_add,
+                          void* dx, void* stream) {
+  int rc = check_desc(desc);
+  if (rc) return rc;
+  const moe_desc& d = *desc;
+  if (d.T > 0 && (!dx_perm || !pos || !dx)) return MOE_ERR_INVALID;
+  if (!aligned16(dx_perm) || !aligned16(dx_add) || !aligned16(dx)) return MOE_ERR_INVALID;
+  return cuda_status(launch_dispatch_backward(shape_of(d), dx_perm, pos, dx_add, dx, (cudaStream_t)stream));
+}
+
+namespace moe {
+namespace {
+
+// The backward workspace: error word | da (fp32 on CUDA cores).
+struct BackwardLayout {
+  size_t err, da, total;
+  int64_t rows;
+};
+
+BackwardLayout backward_layout(const moe_desc& d) {
+  BackwardLayout L;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  L.rows = rows_for(d);
+  const size_t hidden = (size_t)L.rows * d.F * ((d.flags & MOE_FLAG_SWIGLU) ? 2 : 1);
+  L.err = take(256);
+  L.da = take(hidden * 4);
+  L.total = off;
+  return L;
+}
+
+}  // namespace
+}  // namespace moe
+
+int moe_backward_workspace_size(const moe_desc* desc, size_t* bytes) {
+  if (check_desc(desc) != MOE_OK || !bytes) return MOE_ERR_INVALID;
+  *bytes = backward_layout(*desc).total;
+  return MOE_OK;
+}
+
+int moe_expert_ffn_backward(const moe_desc* desc, const void* x_perm, const void* h_perm, const void* dy_perm,
+                            const int32_t* offs, const void* W1, const float* b1, const void* W2, void* dx_perm,
+                            void* dW1, float* db1, void* dW2, float* db2, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_desc(desc);
+  if (rc) return rc;
+  const moe_desc& d = *desc;
+  const BackwardLayout L = backward_layout(d);
+  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  const bool hidden = dx_perm || dW1 || db1;   // what needs da
+  if (!offs || !(hidden || dW2 || db2)) return MOE_ERR_INVALID;
+  if (L.rows > 0 && (!dy_perm || (hidden && (!x_perm || !W1 || !W2)) || (dW2 && !h_perm))) return MOE_ERR_INVALID;
+  for (const void* p : {x_perm, h_perm, dy_perm, W1, W2, (const void*)dx_perm, (const void*)dW1, (const void*)dW2})
+    if (!aligned16(p)) return MOE_ERR_INVALID;
+  const FfnBackward b{x_perm, h_perm, dy_perm, offs, W1, b1, W2, dx_perm, dW1, db1, dW2, db2};
+  return cuda_status(launch_ffn_backward_simt(shape_of(d), L.rows, b, at<float>(ws, L.da), (cudaStream_t)stream));
+}
+
+int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t grad_dtype, int32_t state_bits,
+                   const moe_adamw_params* params, const float* grad_scale, const int32_t* skip, void* stream) {
+  if (count < 0 || (count > 0 && !tensors) || !params) return MOE_ERR_INVALID;
+  if ((grad_dtype != MOE_F32 && grad_dtype != MOE_BF16) || (state_bits != 32 && state_bits != 8))
+    return MOE_ERR_INVALID;
+  const moe_adamw_params& h = *params;
+  // every comparison is false for a NaN
+  if (!(h.lr >= 0 && h.lr < 1e30 && h.eps >= 0 && h.eps < 1e30 && h.beta1 >= 0 && h.beta1 < 1 && h.beta2 >= 0 &&
+        h.beta2 < 1 && h.step >= 1))
+    return MOE_ERR_INVALID;
+  const bool eight = state_bits == 8;
+  auto off = [](const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; };
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.reserved != 0 || !(t.weight_decay >= -1e30f && t.weight_decay <= 1e30f)) return MOE_ERR_INVALID;
+    if ((uint64_t)t.n > (uint64_t)MOE_ADAMW_BLOCK << 31) return MOE_ERR_UNSUPPORTED;
+    if (t.n == 0) continue;
+    if (!t.p || !t.grad || !t.m || !t.v || (eight != (t.m_scale != nullptr)) || (eight != (t.v_scale != nullptr)))
+      return MOE_ERR_INVALID;
+    if (off(t.p, 4) || off(t.p_bf16, 2) || off(t.grad, grad_dtype == MOE_BF16 ? 2 : 4) || off(t.m_scale, 4) ||
+        off(t.v_scale, 4) || (!eight && (off(t.m, 4) || off(t.v, 4))))
+      return MOE_ERR_INVALID;
+  }
+  if (count == 0) return MOE_OK;
+  return cuda_status(launch_adamw(tensors, count, grad_dtype, state_bits, h, grad_scale, skip, (cudaStream_t)stream));
+}
+
 }  // extern "C"

@@ -189,6 +189,36 @@ cudaError_t launch_aux(const Shape& s, const float* psum, const int32_t* count, 
 // acc [T, H] fp32 = 0, and out [T, H] = bf16(acc) (the fused combine's two ends)
 cudaError_t launch_zero_acc(const Shape& s, float* acc, cudaStream_t st);
 cudaError_t launch_acc_to_out(const Shape& s, const float* acc, void* out, cudaStream_t st);
+// ---------------------------------------------------------------- training
+cudaError_t launch_combine_backward(const Shape& s, const void* dout, const void* y_perm, const int32_t* pos,
+                                    const float* w, void* dy_perm, float* dw, cudaStream_t st);
+cudaError_t launch_dispatch_backward(const Shape& s, const void* dx_perm, const int32_t* pos, const void* add,
+                                     void* dx, cudaStream_t st);
+// The expert FFN's gradient: what moe_expert_ffn_backward is given (the
+// results nullable, one by one).
+struct FfnBackward {
+  const void* x_perm;
+  const void* h_perm;
+  const void* dy_perm;
+  const int32_t* offs;
+  const void* W1;
+  const float* b1;
+  const void* W2;
+  void* dx_perm;
+  void* dW1;
+  float* db1;
+  void* dW2;
+  float* db2;
+};
+// da: [max_rows, F or 2F] fp32 scratch
+cudaError_t launch_ffn_backward_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, float* da,
+                                     cudaStream_t st);
+// out[e, :] = the sum of A's [rows, N] rows of expert e, in fp32
+cudaError_t launch_row_sums(int dtype, const void* A, const int32_t* offs, int E, int N, float* out,
+                            cudaStream_t st);
+cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int count, int grad_dtype, int state_bits,
+                         const moe_adamw_params& h, const float* grad_scale, const int32_t* skip, cudaStream_t st);
+
 // The statistics of a layer run in pieces of tokens: count[e] and psum[e]
 // summed over the n pieces in order, then the loss of the whole batch (s.T
 // tokens); count_copy, aux and dropped (0: no capacity) are nullable.
