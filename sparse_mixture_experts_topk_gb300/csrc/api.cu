@@ -84,6 +84,18 @@ bool tma_map_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tma_map_bf16_3d(CUtensorMap* m, const void* ptr, uint64_t d2, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cols, rows, d2};
+  cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
   static int cached[64] = {0};
   int dev = 0;
@@ -780,9 +792,12 @@ int moe_dispatch_backward(const moe_desc* desc, const void* dx_perm, const int32
 namespace moe {
 namespace {
 
-// The backward workspace: error word | da (fp32 on CUDA cores).
+bool backward_on_tensor_cores(const moe_desc& d) { return d.dtype == MOE_BF16 && !(d.flags & MOE_FLAG_SIMT_FFN); }
+
+// The backward workspace: error word | da (fp32 on CUDA cores, else bf16) |
+// tensor cores: dh (fp32), partial sums of da for db1.
 struct BackwardLayout {
-  size_t err, da, total;
+  size_t err, da, dh, part, total;
   int64_t rows;
 };
 
@@ -794,10 +809,13 @@ BackwardLayout backward_layout(const moe_desc& d) {
     off += (bytes + 255) / 256 * 256;
     return o;
   };
+  const bool tc = backward_on_tensor_cores(d);
   L.rows = rows_for(d);
-  const size_t hidden = (size_t)L.rows * d.F * ((d.flags & MOE_FLAG_SWIGLU) ? 2 : 1);
+  const size_t N = (size_t)d.F * ((d.flags & MOE_FLAG_SWIGLU) ? 2 : 1);
   L.err = take(256);
-  L.da = take(hidden * 4);
+  L.da = take((size_t)L.rows * N * (tc ? 2 : 4));
+  L.dh = take(tc ? (size_t)L.rows * d.F * 4 : 0);
+  L.part = take(tc ? (size_t)backward_blocks(L.rows, d.E) * 8 * N * 4 : 0);
   L.total = off;
   return L;
 }
@@ -825,7 +843,11 @@ int moe_expert_ffn_backward(const moe_desc* desc, const void* x_perm, const void
   for (const void* p : {x_perm, h_perm, dy_perm, W1, W2, (const void*)dx_perm, (const void*)dW1, (const void*)dW2})
     if (!aligned16(p)) return MOE_ERR_INVALID;
   const FfnBackward b{x_perm, h_perm, dy_perm, offs, W1, b1, W2, dx_perm, dW1, db1, dW2, db2};
-  return cuda_status(launch_ffn_backward_simt(shape_of(d), L.rows, b, at<float>(ws, L.da), (cudaStream_t)stream));
+  cudaStream_t st = (cudaStream_t)stream;
+  if (backward_on_tensor_cores(d))
+    return cuda_status(launch_ffn_backward_tc(shape_of(d), L.rows, b, at<void>(ws, L.da), at<float>(ws, L.dh),
+                                              at<float>(ws, L.part), at<int>(ws, L.err), st));
+  return cuda_status(launch_ffn_backward_simt(shape_of(d), L.rows, b, at<float>(ws, L.da), st));
 }
 
 int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t grad_dtype, int32_t state_bits,

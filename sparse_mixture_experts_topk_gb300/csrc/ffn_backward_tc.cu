@@ -1,0 +1,814 @@
+// Gradient of the expert FFN on the tensor cores: grouped products on SM
+// pairs (tcgen05 .cta_group::2, tiles of 256 x 256, fp32 accumulators in
+// TMEM, operands staged by TMA).
+//
+// For expert e and its rows r (formulas as in ffn_backward_simt.cu):
+//   dh = dy W2[e]           [rows, F]    tokens K-major, weights read along their rows
+//   a  = x W1[e]^T (+ b1)   [rows, G F]  both K-major; the epilogue reads dh and writes da
+//   dx = da W1[e]           [rows, H]    tokens K-major, weights read along their rows
+//   dW1[e] = da^T x, dW2[e] = dy^T h     reduction over the rows, both operands read along their rows
+// Nothing is transposed in memory: an operand whose reduction index runs
+// along the rows of its matrix ("MN-major") is staged as it lies, and the MMA
+// descriptors say so.
+//
+// dh goes through fp32 scratch between its product and the one that uses it.
+// Computing both products of a da tile together would spare that traffic
+// (4 bytes a value, written and read once), but two accumulators of 256
+// columns fill TMEM, so the epilogue could not overlap the next tile, and two
+// of 128 columns would raise the operand bytes per MMA by half, which bounds
+// a tile already.  da is rounded to bf16, as an operand of the next products.
+//
+// Rows kernel (dh, da, dx).  A block of 256 rows has its rows on the MMA's M
+// side; an expert's last block of at most 128 rows runs swapped (256 weight
+// columns on M, the rows on N rounded up to 16), so that few rows do not cost
+// a full tile.  Weights kernel (dW1, dW2): the reduction runs over an
+// expert's rows in blocks of 64, 16 to an MMA.  Its last block usually ends
+// inside a group of 16, where TMA has brought rows of the next expert (or
+// memory nobody wrote): a warp of each CTA zeroes those rows of both operands
+// in shared memory before the MMAs may read the stage, since 0 x NaN is NaN.
+//
+// Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader CTA of the
+// pair), warps 2-5 epilogue, warp 6 (weights kernel) the zeroing.  Every wait
+// is bounded: on expiry the kernel records a timeout in the workspace's error
+// word, drains what it has in flight, frees its tensor memory and returns.
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "ffn_backward.cuh"
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBM = 128;                  // operand rows (or columns) per CTA: the pair covers 256
+constexpr int kTile = 2 * kBM;            // rows and columns of a pair's tile
+constexpr int kBK = 64;                   // reduction elements per stage
+constexpr int kBoxRows = 32;              // swapped: token rows per box
+constexpr int kSwapRows = 128;            // a last block of at most this many rows runs swapped
+constexpr int kOperand = kBM * kBK * 2;   // bytes of one operand in a stage
+constexpr int kHalf = kOperand / 2;       // an MN-major operand is two boxes of 64 columns x 64 rows
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kStages = 6;
+constexpr int kTmemCols = 512;            // two accumulators of 256 columns
+constexpr int kStoreBytes = 32 * 128;     // an epilogue warp's store tile: 32 rows of 128 bytes
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes;
+constexpr size_t kSmemW = kSmem + 8 * kStoreBytes;   // two store tiles for each of 4 warps
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+enum Product { kDh, kDaGelu, kDaSwiglu, kDx };
+
+// Shared-memory descriptor of an MN-major operand of 128 x 64: two boxes (64
+// columns of 128 bytes, 64 rows, 128-byte swizzle) one after the other.
+//   bits 16-29: bytes >> 4 between groups of 64 columns; bits 32-45: between groups of 8 rows
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(kHalf >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;   // instruction descriptor: operand is MN-major
+// 16 reduction elements on: along a K-major row, or two groups of 8 rows
+constexpr int kStepK = 32, kStepMN = 2048;
+
+// Per-expert tile counts' prefix into tstart [E + 1] and a copy of offs; one warp.
+template <typename Count>
+__device__ __forceinline__ void tile_table(const int32_t* __restrict__ offs, int E, int lane, int* s_offs, int* tstart,
+                                           Count count) {
+  int loc[8], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = lane * 8 + i;
+    loc[i] = 0;
+    if (e < E) {
+      const int o0 = offs[e], o1 = offs[e + 1];
+      loc[i] = count(o1 - o0);
+      s_offs[e] = o0;
+      if (e == E - 1) s_offs[E] = o1;
+    }
+    sum += loc[i];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int run = incl - sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = lane * 8 + i;
+    if (e < E) tstart[e] = run;
+    run += loc[i];
+  }
+  if (lane == 31) tstart[E] = incl;
+}
+
+// The last expert whose first tile is at or before t.
+__device__ __forceinline__ int expert_of(const int* tstart, int E, int t) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tstart[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void advance(int& stage, uint32_t& phase) {
+  if (++stage == kStages) {
+    stage = 0;
+    phase ^= 1u;
+  }
+}
+
+// What the rows kernel's epilogue reads and writes.
+struct RowsOut {
+  float* dh;            // [rows, F] fp32: written by kDh, read by kDa*
+  bf16* da;             // [rows, G F]
+  bf16* dx;             // [rows, H]
+  const float* bias;    // b1 or null
+  float* part;          // [blocks * 8, G F] partial sums of da over rows, or null
+};
+
+// Sum over the warp's lanes of 32 values each: lane l returns the sum of v[l].
+__device__ __forceinline__ float column_sum(float* v, int lane) {
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    const bool up = (lane & w) != 0;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float keep = up ? v[i + w] : v[i], give = up ? v[i] : v[i + w];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+    }
+  }
+  return v[0];
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row(T* dst, const float* v, int n) {   // n values, a multiple of 8, at most 32
+#pragma unroll
+  for (int g = 0; g < 32 / Vec<T>::N; ++g)
+    if (g * Vec<T>::N < n) reinterpret_cast<uint4*>(dst)[g] = Vec<T>::pack(v + g * Vec<T>::N);
+}
+
+// One tile of the rows kernel.  Row orientation: this thread's row, 32
+// columns at a time.  Swapped: this thread's column, 32 rows at a time.
+template <int kKind>
+__device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, int row_base, int nrows, int n0,
+                                              int block, int rank, int q, int lane, int N, const RowsOut& o) {
+  constexpr bool kSwi = kKind == kDaSwiglu, kDa = kKind == kDaGelu || kSwi;
+  constexpr int kOut = kSwi ? kBM : kTile;
+  const int wide = kSwi ? 2 * N : N;     // columns of da and of the bias
+  const float* be = kDa && o.bias ? o.bias + (int64_t)e * wide : nullptr;
+  if (swap) {
+    const int f = n0 + rank * kBM + q * 32 + lane;
+    const bool ok = f < N;
+    const float bf = be && ok ? be[f] : 0.f;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c * 32 < nrows; ++c) {
+      uint32_t r[32];
+      tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
+      tc::tmem_wait_ld();
+      if (ok) {
+        const int64_t at = (int64_t)(row_base + c * 32) * N + f;
+        const int left = nrows - c * 32;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j < left) {
+            const float v = __uint_as_float(r[j]);
+            if (kKind == kDh) {
+              o.dh[at + (int64_t)j * N] = v;
+            } else if (kKind == kDx) {
+              o.dx[at + (int64_t)j * N] = __float2bfloat16_rn(v);
+            } else {
+              const float d = o.dh[at + (int64_t)j * N] * gelu_slope(v + bf);
+              sum += d;
+              o.da[at + (int64_t)j * N] = __float2bfloat16_rn(d);
+            }
+          }
+        }
+      }
+    }
+    if (kDa && o.part && ok) o.part[(int64_t)block * 8 * wide + f] = sum;
+    return;
+  }
+  const int r0 = rank * kBM + q * 32;          // this warp's first row of the block
+  const int64_t row = row_base + r0 + lane;
+  const bool ok = r0 + lane < nrows;
+#pragma unroll 1
+  for (int c = 0; c < kOut / 32; ++c) {
+    const int col = n0 + c * 32;
+    if (col >= N) break;
+    const int left = min(32, N - col);
+    uint32_t r[32], u[kSwi ? 32 : 1];
+    tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
+    if (kSwi) tc::tmem_ld_32x32b_x32(tbase + kBM + c * 32, u);
+    tc::tmem_wait_ld();
+    float v[32];
+    if (!kDa) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+      if (ok) {
+        if (kKind == kDh) store_row(o.dh + row * N + col, v, left);
+        else store_row(o.dx + row * N + col, v, left);
+      }
+    } else {
+      float w[kSwi ? 32 : 1];
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ok && g * 4 < left) d = __ldcs(reinterpret_cast<const float4*>(o.dh + row * N + col + g * 4));
+        const float dh[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = g * 4 + i;
+          float a = __uint_as_float(r[j]);
+          if (be && j < left) a += be[col + j];
+          if (kSwi) {
+            float b = __uint_as_float(u[j % (kSwi ? 32 : 1)]);
+            if (be && j < left) b += be[N + col + j];
+            swiglu_gradient(a, b, dh[i], &v[j], &w[j % (kSwi ? 32 : 1)]);
+          } else {
+            v[j] = dh[i] * gelu_slope(a);
+          }
+        }
+      }
+      if (ok) {
+        store_row(o.da + row * wide + col, v, left);
+        if (kSwi) store_row(o.da + row * wide + N + col, w, left);
+      }
+      if (o.part) {
+        // rows past the block's end and columns past N are other data: they count as zeros
+        const int64_t p = ((int64_t)block * 8 + rank * 4 + q) * wide + col + lane;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (!ok || j >= left) {
+            v[j] = 0.f;
+            if (kSwi) w[j % (kSwi ? 32 : 1)] = 0.f;
+          }
+        const float s = column_sum(v, lane);
+        if (lane < left) o.part[p] = s;
+        if (kSwi) {
+          const float s2 = column_sum(w, lane);
+          if (lane < left) o.part[p + N] = s2;
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ int row_blocks(int rows) { return (rows + kTile - 1) / kTile; }
+
+// Barriers of a CTA: full and empty per stage, full and empty per accumulator, the end.
+struct Bars {
+  uint32_t base;
+  __device__ uint32_t full(int s) const { return base + 8 * s; }
+  __device__ uint32_t empty(int s) const { return base + 8 * (kStages + s); }
+  __device__ uint32_t tfull(int a) const { return base + 8 * (2 * kStages + a); }
+  __device__ uint32_t tempty(int a) const { return base + 8 * (2 * kStages + 2 + a); }
+  __device__ uint32_t done() const { return base + 8 * (2 * kStages + 4); }
+  __device__ uint32_t fix(int s) const { return base + 8 * (2 * kStages + 5 + s); }
+};
+
+__device__ __forceinline__ void give_up(int* err, volatile int* abort) {
+  set_error(err, kDevTimeout);
+  *abort = 1;
+}
+
+// tmX, tmXs: token rows [rows, K] in boxes of 128 and 32 rows.  tmW: weights
+// K-major [E N, K] (kDa*) or [E, K, N] in 64 x 64 boxes (kDh, kDx).
+template <int kKind>
+__global__ void __launch_bounds__(192, 1)
+backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
+                     const __grid_constant__ CUtensorMap tmW, const int32_t* __restrict__ offs, int E, int N, int K,
+                     RowsOut out, int* err) {
+  constexpr bool kSwi = kKind == kDaSwiglu, kMN = kKind == kDh || kKind == kDx;
+  constexpr int kOut = kSwi ? kBM : kTile;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_offs[257], s_tstart[257];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
+  const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sB = sA + kStages * kOperand;
+  const Bars bar{tc::smem_u32(s_bar)};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)tc::cluster_ctarank();
+  const int nt = (N + kOut - 1) / kOut, nk = (K + kBK - 1) / kBK;
+
+  if (warp == 0) {
+    pdl_enter();
+    tile_table(offs, E, lane, s_offs, s_tstart, [&](int rows) { return row_blocks(rows) * nt; });
+    if (lane == 0) {
+      for (int s = 0; s < kStages; ++s) {
+        tc::mbar_init(bar.full(s), 1);
+        tc::mbar_init(bar.empty(s), 1);
+      }
+      for (int a = 0; a < 2; ++a) {
+        tc::mbar_init(bar.tfull(a), 1);
+        tc::mbar_init(bar.tempty(a), 2 * 128);
+      }
+      tc::mbar_init(bar.done(), 1);
+      s_abort = 0;
+      tc::fence_barrier_init();
+      tc::fence_proxy_async_smem();
+      tc::prefetch_tmap(&tmX);
+      tc::prefetch_tmap(&tmXs);
+      tc::prefetch_tmap(&tmW);
+    }
+  } else if (warp == 1) {
+    tc::tmem_alloc_pair(tc::smem_u32(&s_tmem), kTmemCols);
+    tc::tmem_relinquish_pair();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::tc_fence_after();
+  if (warp != 0) pdl_wait();
+  const uint32_t tmem = s_tmem;
+  const int total = s_tstart[E], first = blockIdx.x / 2, step = gridDim.x / 2;
+
+  struct Tile {
+    int e, row_base, nrows, mma_n, n0, block;
+    bool swap;
+  };
+  auto decode = [&](int t) {
+    Tile d;
+    d.e = expert_of(s_tstart, E, t);
+    const int mt = row_blocks(s_offs[d.e + 1] - s_offs[d.e]);
+    const int local = t - s_tstart[d.e], rb = local % mt;
+    d.row_base = s_offs[d.e] + rb * kTile;
+    d.nrows = min(kTile, s_offs[d.e + 1] - d.row_base);
+    d.swap = !kSwi && d.nrows <= kSwapRows;
+    d.mma_n = d.swap ? (d.nrows + 15) / 16 * 16 : kTile;
+    d.n0 = (local / mt) * kOut;
+    d.block = (s_offs[d.e] >> 8) + d.e + rb;
+    return d;
+  };
+
+  uint32_t filled = 0, fill_par = 0;
+  bool producer = false;
+  if (warp == 0) {
+    if (tc::elect_one()) {
+      producer = true;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; t < total && ok; t += step) {
+        const Tile d = decode(t);
+        const int half = d.mma_n / 2, nbox = d.swap ? (half + kBoxRows - 1) / kBoxRows : 0;
+        const uint32_t tx = 2u * (uint32_t)(kOperand + (d.swap ? nbox * kBoxRows * 128 : kOperand));
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!tc::mbar_wait(bar.empty(stage), phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
+          const uint32_t fbar = tc::map_peer(bar.full(stage), 0);
+          if (rank == 0) tc::mbar_arrive_expect_tx(bar.full(stage), tx);
+          const uint32_t tok = (d.swap ? sB : sA) + stage * kOperand, wgt = (d.swap ? sA : sB) + stage * kOperand;
+          const int n = d.n0 + rank * kBM;
+          if (kMN) {
+            tc::tma_load_3d_pair(wgt, &tmW, fbar, n, kb * kBK, d.e);
+            tc::tma_load_3d_pair(wgt + kHalf, &tmW, fbar, n + 64, kb * kBK, d.e);
+          } else {
+            tc::tma_load_2d_pair(wgt, &tmW, fbar, kb * kBK, kSwi ? (2 * d.e + rank) * N + d.n0 : d.e * N + n);
+          }
+          if (d.swap) {
+            for (int i = 0; i < nbox; ++i)
+              tc::tma_load_2d_pair(tok + i * kBoxRows * 128, &tmXs, fbar, kb * kBK,
+                                   d.row_base + rank * half + i * kBoxRows);
+          } else {
+            tc::tma_load_2d_pair(tok, &tmX, fbar, kb * kBK, d.row_base + rank * kBM);
+          }
+          filled |= 1u << stage;
+          fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
+          advance(stage, phase);
+        }
+      }
+      if (!ok) give_up(err, &s_abort);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && tc::elect_one()) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = first; t < total && ok; t += step) {
+        const Tile d = decode(t);
+        const uint32_t idesc = tc::idesc_bf16_f32(kTile, d.mma_n) | (kMN ? (d.swap ? kMajorA : kMajorB) : 0u);
+        if (!tc::mbar_wait(bar.tempty(acc), acc_phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
+        tc::tc_fence_after();
+        const uint32_t dst = tmem + (uint32_t)(acc * kTile);
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!tc::mbar_wait(bar.full(stage), phase, &s_abort, kWaitNs)) { ok = false; break; }
+          tc::tc_fence_after();
+          const uint32_t a0 = sA + stage * kOperand, b0 = sB + stage * kOperand;
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k) {
+            uint64_t da, db;
+            if (kMN && d.swap) da = sdesc_mn128(a0 + k * kStepMN);
+            else da = tc::sdesc_k128(a0 + k * kStepK);
+            if (kMN && !d.swap) db = sdesc_mn128(b0 + k * kStepMN);
+            else db = tc::sdesc_k128(b0 + k * kStepK);
+            tc::mma_bf16_pair(dst, da, db, idesc, (kb | k) != 0);
+          }
+          tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
+          advance(stage, phase);
+        }
+        if (!ok) break;
+        tc::tc_commit_pair_mc(bar.tfull(acc), 0x3);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!ok) give_up(err, &s_abort);
+      tc::tc_commit_pair_mc(bar.done(), 0x3);   // both CTAs learn when every MMA has finished
+    }
+    __syncwarp();
+    if (lane == 0 && !tc::mbar_wait(bar.done(), 0, nullptr, kWaitNs)) set_error(err, kDevTimeout);
+    __syncwarp();
+  } else {
+    const int q = warp & 3;   // TMEM lanes 32 q .. 32 q + 31 belong to this warp
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = first; t < total; t += step) {
+      const Tile d = decode(t);
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.tfull(acc), acc_phase, &s_abort, kWaitNs))) {
+        give_up(err, &s_abort);
+        break;
+      }
+      tc::tc_fence_after();
+      rows_epilogue<kKind>(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile), d.swap, d.e, d.row_base,
+                           d.nrows, d.n0, d.block, rank, q, lane, N, out);
+      tc::tc_fence_before();
+      if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
+      else tc::mbar_arrive_remote(tc::map_peer(bar.tempty(acc), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (producer && rank == 0 && s_abort)
+    for (int s = 0; s < kStages; ++s)
+      if ((filled >> s) & 1u) tc::mbar_wait(bar.full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
+  tc::cluster_sync();   // neither CTA leaves while the other may still signal it
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// One weight gradient: out [E, M, N] = sum over an expert's rows of A's row
+// (M columns) times B's row (N columns).
+struct WeightProduct {
+  int M, N;
+};
+
+// tmA, tmB: the operands' rows in 64 x 64 boxes; tmO: out [E, M, N] in boxes
+// of 32 rows x 64 columns.  Products 0 and 1 follow one another.
+__global__ void __launch_bounds__(224, 1)
+backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
+                        const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmA1,
+                        const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmO1,
+                        const int32_t* __restrict__ offs, int E, WeightProduct P0, WeightProduct P1, int* err) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_offs[257];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ __align__(8) uint64_t s_bar[3 * kStages + 5];
+  const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sB = sA + kStages * kOperand;
+  const uint32_t sOut = sB + kStages * kOperand;
+  uint8_t* gOut = smem_raw + (sOut - tc::smem_u32(smem_raw));
+  const Bars bar{tc::smem_u32(s_bar)};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)tc::cluster_ctarank();
+  auto tiles = [](int n) { return (n + kTile - 1) / kTile; };
+  const int per0 = tiles(P0.M) * tiles(P0.N), per1 = tiles(P1.M) * tiles(P1.N);
+
+  if (warp == 0) {
+    pdl_enter();
+    for (int e = lane; e <= E; e += 32) s_offs[e] = offs[e];
+    if (lane == 0) {
+      for (int s = 0; s < kStages; ++s) {
+        tc::mbar_init(bar.full(s), 2);    // used in the leader: one arrival for each CTA
+        tc::mbar_init(bar.empty(s), 1);
+        tc::mbar_init(bar.fix(s), 1);     // this CTA's loads of a stage that is zeroed in part
+      }
+      for (int a = 0; a < 2; ++a) {
+        tc::mbar_init(bar.tfull(a), 1);
+        tc::mbar_init(bar.tempty(a), 2 * 128);
+      }
+      tc::mbar_init(bar.done(), 1);
+      s_abort = 0;
+      tc::fence_barrier_init();
+      tc::fence_proxy_async_smem();
+      tc::prefetch_tmap(&tmA0);
+      tc::prefetch_tmap(&tmB0);
+      tc::prefetch_tmap(&tmO0);
+      tc::prefetch_tmap(&tmA1);
+      tc::prefetch_tmap(&tmB1);
+      tc::prefetch_tmap(&tmO1);
+    }
+  } else if (warp == 1) {
+    tc::tmem_alloc_pair(tc::smem_u32(&s_tmem), kTmemCols);
+    tc::tmem_relinquish_pair();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::tc_fence_after();
+  if (warp != 0) pdl_wait();
+  const uint32_t tmem = s_tmem;
+  const int total0 = E * per0, total = total0 + E * per1, first = blockIdx.x / 2, step = gridDim.x / 2;
+
+  struct Tile {
+    int p, e, m0, n0, row0, rows, nk;
+  };
+  auto decode = [&](int t) {
+    Tile d;
+    d.p = t >= total0 ? 1 : 0;
+    const int tl = t - (d.p ? total0 : 0), per = d.p ? per1 : per0, nt = tiles(d.p ? P1.N : P0.N);
+    d.e = tl / per;
+    const int local = tl % per;
+    d.m0 = (local / nt) * kTile;
+    d.n0 = (local % nt) * kTile;
+    d.row0 = s_offs[d.e];
+    d.rows = s_offs[d.e + 1] - d.row0;
+    d.nk = (d.rows + kBK - 1) / kBK;
+    return d;
+  };
+  // the last block of an expert's rows is zeroed in part unless it ends with a group of 16
+  auto zeroed = [](const Tile& d, int kb) { return kb == d.nk - 1 && d.rows % 16 != 0; };
+
+  uint32_t filled = 0, fill_par = 0, fixed = 0, fix_par = 0, last_fix = 0;
+  bool producer = false;
+  if (warp == 0) {
+    if (tc::elect_one()) {
+      producer = true;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; t < total && ok; t += step) {
+        const Tile d = decode(t);
+        const CUtensorMap* mA = d.p ? &tmA1 : &tmA0;
+        const CUtensorMap* mB = d.p ? &tmB1 : &tmB0;
+        const int m = d.m0 + rank * kBM, n = d.n0 + rank * kBM;
+        for (int kb = 0; kb < d.nk; ++kb) {
+          if (!tc::mbar_wait(bar.empty(stage), phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
+          const bool z = zeroed(d, kb);
+          // a stage to be zeroed is signalled by the zeroing warps once they are done
+          const uint32_t lbar = z ? tc::map_peer(bar.fix(stage), rank) : tc::map_peer(bar.full(stage), 0);
+          if (z) tc::mbar_arrive_expect_tx(bar.fix(stage), kStageBytes);
+          else if (rank == 0) tc::mbar_arrive_expect_tx(bar.full(stage), 2 * kStageBytes);
+          else tc::mbar_arrive_remote(lbar);
+          const int r = d.row0 + kb * kBK;
+          const uint32_t a = sA + stage * kOperand, b = sB + stage * kOperand;
+          tc::tma_load_2d_pair(a, mA, lbar, m, r);
+          tc::tma_load_2d_pair(a + kHalf, mA, lbar, m + 64, r);
+          tc::tma_load_2d_pair(b, mB, lbar, n, r);
+          tc::tma_load_2d_pair(b + kHalf, mB, lbar, n + 64, r);
+          const uint32_t bit = 1u << stage;
+          filled |= bit;
+          fill_par = (fill_par & ~bit) | (phase << stage);
+          last_fix = z ? last_fix | bit : last_fix & ~bit;
+          if (z) {
+            fix_par ^= (fixed & bit);     // the first use completes phase 0, each later one the other
+            fixed |= bit;
+          }
+          advance(stage, phase);
+        }
+      }
+      if (!ok) give_up(err, &s_abort);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && tc::elect_one()) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      const uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | kMajorA | kMajorB;
+      for (int t = first; t < total && ok; t += step) {
+        const Tile d = decode(t);
+        if (!tc::mbar_wait(bar.tempty(acc), acc_phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
+        tc::tc_fence_after();
+        const uint32_t dst = tmem + (uint32_t)(acc * kTile);
+        for (int kb = 0; kb < d.nk; ++kb) {
+          if (!tc::mbar_wait<true>(bar.full(stage), phase, &s_abort, kWaitNs)) { ok = false; break; }
+          tc::tc_fence_after();
+          const uint32_t a0 = sA + stage * kOperand, b0 = sB + stage * kOperand;
+          const int groups = min(kBK / 16, (d.rows - kb * kBK + 15) / 16);
+          for (int k = 0; k < groups; ++k)
+            tc::mma_bf16_pair(dst, sdesc_mn128(a0 + k * kStepMN), sdesc_mn128(b0 + k * kStepMN), idesc, (kb | k) != 0);
+          tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
+          advance(stage, phase);
+        }
+        if (!ok) break;
+        tc::tc_commit_pair_mc(bar.tfull(acc), 0x3);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!ok) give_up(err, &s_abort);
+      tc::tc_commit_pair_mc(bar.done(), 0x3);
+    }
+    __syncwarp();
+    if (lane == 0 && !tc::mbar_wait(bar.done(), 0, nullptr, kWaitNs)) set_error(err, kDevTimeout);
+    __syncwarp();
+  } else if (warp == 6) {
+    // zero the rows past the expert's end in both operands of its last block:
+    // row k of a box is the 128 bytes at 128 k, whatever the swizzle does within them
+    int stage = 0;
+    uint32_t phase = 0, seen = 0;
+    for (int t = first; t < total; t += step) {
+      const Tile d = decode(t);
+      if (d.nk == 0) continue;
+      int last = stage + d.nk - 1;
+      last %= kStages;
+      if (zeroed(d, d.nk - 1)) {
+        const uint32_t par = (seen >> last) & 1u;
+        seen ^= 1u << last;
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.fix(last), par, &s_abort, kWaitNs))) {
+          if (lane == 0) give_up(err, &s_abort);
+          break;
+        }
+        const int r0 = d.rows - (d.nk - 1) * kBK, r1 = (r0 + 15) / 16 * 16;
+        const uint32_t part = lane >> 3, chunk = lane & 7;   // 8 lanes to a row of each of the four boxes
+        const uint32_t box = (part < 2 ? sA : sB) + last * kOperand + (part & 1) * kHalf + chunk * 16;
+        for (int r = r0; r < r1; ++r)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(box + r * 128), "r"(0) : "memory");
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(bar.full(last), 0));
+      }
+      for (int i = 0; i < d.nk % kStages; ++i) advance(stage, phase);
+    }
+  } else {
+    const int q = warp & 3;
+    const uint32_t buf0 = sOut + q * 2 * kStoreBytes;
+    int acc = 0, turn = 0;
+    uint32_t acc_phase = 0;
+    for (int t = first; t < total; t += step) {
+      const Tile d = decode(t);
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.tfull(acc), acc_phase, &s_abort, kWaitNs))) {
+        give_up(err, &s_abort);
+        break;
+      }
+      tc::tc_fence_after();
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile);
+      const int M = d.p ? P1.M : P0.M, N = d.p ? P1.N : P0.N;
+      const int m = d.m0 + rank * kBM + q * 32;
+      if (m < M) {
+#pragma unroll 1
+        for (int c = 0; c < kTile / 64; ++c) {
+          const int n = d.n0 + c * 64;
+          if (n >= N) break;
+          const uint32_t buf = buf0 + turn * kStoreBytes;
+          turn ^= 1;
+          uint8_t* g = gOut + (buf - sOut);
+          if (lane == 0) tc::bulk_wait_read<1>();   // this buffer's previous store has been read
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[32];
+            if (d.nk > 0) {
+              uint32_t r[32];
+              tc::tmem_ld_32x32b_x32(tbase + c * 64 + h * 32, r);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(g + lane * 128 + (((h * 4 + j) ^ (lane & 7)) << 4)) =
+                  Vec<bf16>::pack(v + j * 8);
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::tma_store_3d(d.p ? &tmO1 : &tmO0, buf, n, m, d.e);
+        }
+      }
+      tc::tc_fence_before();
+      if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
+      else tc::mbar_arrive_remote(tc::map_peer(bar.tempty(acc), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (lane == 0) tc::bulk_wait_all();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (producer && s_abort)
+    for (int s = 0; s < kStages; ++s) {
+      if ((fixed >> s) & 1u) tc::mbar_wait(bar.fix(s), (fix_par >> s) & 1u, nullptr, kWaitNs);
+      if (rank == 0 && ((filled & ~last_fix) >> s) & 1u)
+        tc::mbar_wait(bar.full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
+    }
+  tc::cluster_sync();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// db1[e, c]: the row blocks' partial sums in order.  A swapped block has one
+// partial, another eight.
+__global__ void __launch_bounds__(128)
+bias_reduce_kernel(const float* __restrict__ part, const int32_t* __restrict__ offs, int n, int swaps,
+                   float* __restrict__ db) {
+  pdl_enter();
+  const int e = blockIdx.y, c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= n) return;
+  const int r0 = offs[e], rows = offs[e + 1] - r0, mt = row_blocks(rows);
+  const int64_t first = (int64_t)((r0 >> 8) + e) * 8;
+  float sum = 0.f;
+  for (int b = 0; b < mt; ++b) {
+    const int parts = swaps && rows - b * kTile <= kSwapRows ? 1 : 8;
+    for (int i = 0; i < parts; ++i) sum += part[(first + b * 8 + i) * n + c];
+  }
+  db[(int64_t)e * n + c] = sum;
+}
+
+// One persistent launch of CTA pairs, never more than fit at once.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pairs(void (*kern)(KArgs...), int threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (r != cudaSuccess) return r;
+  return launch_kernel(kern, dim3((unsigned)(sm_count() / 2 * 2)), dim3(threads), smem, st, 2, args...);
+}
+
+template <int kKind>
+cudaError_t run_rows(const void* tokens, int64_t rows, int K, const void* W, int E, int N, const int32_t* offs,
+                     const RowsOut& out, int* err, cudaStream_t st) {
+  constexpr bool kMN = kKind == kDh || kKind == kDx;
+  CUtensorMap mx, mxs, mw;
+  if (!tma_map_bf16(&mx, tokens, (uint64_t)rows, (uint64_t)K, kBM) ||
+      !tma_map_bf16(&mxs, tokens, (uint64_t)rows, (uint64_t)K, kBoxRows))
+    return cudaErrorNotSupported;
+  if (kMN ? !tma_map_bf16_3d(&mw, W, (uint64_t)E, (uint64_t)K, (uint64_t)N, kBK)
+          : !tma_map_bf16(&mw, W, (uint64_t)E * N * (kKind == kDaSwiglu ? 2 : 1), (uint64_t)K, kBM))
+    return cudaErrorNotSupported;
+  return launch_pairs(backward_rows_kernel<kKind>, 192, kSmem, st, mx, mxs, mw, offs, E, N, K, out, err);
+}
+
+}  // namespace
+
+int64_t backward_blocks(int64_t rows, int E) { return rows / kTile + E + 1; }
+
+cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBackward& b, void* da, float* dh,
+                                   float* part, int* err, cudaStream_t st) {
+  const bool swi = (s.flags & MOE_FLAG_SWIGLU) != 0;
+  const int G = swi ? 2 : 1, N = G * s.F;
+  const int64_t lim = (int64_t)1 << 31;
+  if (max_rows + kTile >= lim || (int64_t)s.E * N >= lim || (int64_t)s.E * s.H >= lim) return cudaErrorNotSupported;
+  cudaError_t e = cudaSuccess;
+  if (max_rows == 0) {
+    // no row of any expert: every gradient is zero
+    if (b.dW1) e = cudaMemsetAsync(b.dW1, 0, (size_t)s.E * N * s.H * 2, st);
+    if (e == cudaSuccess && b.dW2) e = cudaMemsetAsync(b.dW2, 0, (size_t)s.E * s.F * s.H * 2, st);
+    if (e == cudaSuccess && b.db1) e = cudaMemsetAsync(b.db1, 0, (size_t)s.E * N * 4, st);
+    if (e == cudaSuccess && b.db2) e = cudaMemsetAsync(b.db2, 0, (size_t)s.E * s.H * 4, st);
+    return e;
+  }
+  const RowsOut out{dh, (bf16*)da, (bf16*)b.dx_perm, b.b1, b.db1 ? part : nullptr};
+  if (b.dx_perm || b.dW1 || b.db1) {
+    e = run_rows<kDh>(b.dy_perm, max_rows, s.H, b.W2, s.E, s.F, b.offs, out, err, st);
+    if (e == cudaSuccess)
+      e = swi ? run_rows<kDaSwiglu>(b.x_perm, max_rows, s.H, b.W1, s.E, s.F, b.offs, out, err, st)
+              : run_rows<kDaGelu>(b.x_perm, max_rows, s.H, b.W1, s.E, s.F, b.offs, out, err, st);
+    if (e == cudaSuccess && b.db1)
+      e = launch_kernel(bias_reduce_kernel, dim3((unsigned)((N + 127) / 128), (unsigned)s.E), dim3(128), 0, st, 1,
+                        (const float*)part, b.offs, N, swi ? 0 : 1, b.db1);
+    if (e == cudaSuccess && b.dx_perm)
+      e = run_rows<kDx>(da, max_rows, N, b.W1, s.E, s.H, b.offs, out, err, st);
+  }
+  if (e == cudaSuccess && (b.dW1 || b.dW2)) {
+    CUtensorMap m[6];
+    WeightProduct P[2];
+    int n = 0;
+    auto add = [&](const void* A, int M, const void* Bm, int Nn, void* dW) {
+      P[n] = {M, Nn};
+      const bool ok = tma_map_bf16(&m[3 * n], A, (uint64_t)max_rows, (uint64_t)M, kBK) &&
+                      tma_map_bf16(&m[3 * n + 1], Bm, (uint64_t)max_rows, (uint64_t)Nn, kBK) &&
+                      tma_map_bf16_3d(&m[3 * n + 2], dW, (uint64_t)s.E, (uint64_t)M, (uint64_t)Nn, 32);
+      ++n;
+      return ok;
+    };
+    if (b.dW1 && !add(da, N, b.x_perm, s.H, b.dW1)) return cudaErrorNotSupported;
+    if (b.dW2 && !add(b.dy_perm, s.H, b.h_perm, s.F, b.dW2)) return cudaErrorNotSupported;
+    if (n == 1) {
+      for (int i = 0; i < 3; ++i) m[3 + i] = m[i];
+      P[1] = {0, 0};
+    }
+    e = launch_pairs(backward_weights_kernel, 224, kSmemW, st, m[0], m[1], m[2], m[3], m[4], m[5], b.offs, s.E, P[0],
+                     P[1], err);
+  }
+  if (e == cudaSuccess && b.db2) e = launch_row_sums(MOE_BF16, b.dy_perm, b.offs, s.E, s.H, b.db2, st);
+  return e;
+}
+
+}  // namespace moe

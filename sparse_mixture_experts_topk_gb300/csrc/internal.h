@@ -66,6 +66,11 @@ void prof_mark(int mark, cudaStream_t st);
 // 64 columns (128 bytes, 128-byte swizzle) x box_rows rows; false on failure.
 bool tma_map_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);
 
+// Row-major bf16 [d2, rows, cols] as a 3D tensor map with a box of 1 x box_rows
+// x 64 columns (128-byte swizzle): what lies outside a [rows, cols] matrix
+// reads as zero and is not written.
+bool tma_map_bf16_3d(CUtensorMap* m, const void* ptr, uint64_t d2, uint64_t rows, uint64_t cols, uint32_t box_rows);
+
 // ---------------------------------------------------------------- router
 // Upper bound of the rows of per-block probability partial sums the router
 // writes (workspace sizing), and the rows the chosen router writes.
@@ -213,6 +218,11 @@ struct FfnBackward {
 // da: [max_rows, F or 2F] fp32 scratch
 cudaError_t launch_ffn_backward_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, float* da,
                                      cudaStream_t st);
+// bf16 on SM pairs.  da: [max_rows, F or 2F] bf16, dh: [max_rows, F] fp32,
+// part: [8 * backward_blocks(max_rows, E), F or 2F] fp32 scratch.
+int64_t backward_blocks(int64_t rows, int E);
+cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBackward& b, void* da, float* dh,
+                                   float* part, int* err, cudaStream_t st);
 // out[e, :] = the sum of A's [rows, N] rows of expert e, in fp32
 cudaError_t launch_row_sums(int dtype, const void* A, const int32_t* offs, int E, int N, float* out,
                             cudaStream_t st);
