@@ -273,6 +273,7 @@ struct Bars {
   __device__ uint32_t tempty(int a) const { return base + 8 * (2 * kStages + 2 + a); }
   __device__ uint32_t done() const { return base + 8 * (2 * kStages + 4); }
   __device__ uint32_t fix(int s) const { return base + 8 * (2 * kStages + 5 + s); }
+  __device__ uint32_t fixed(int s) const { return base + 8 * (3 * kStages + 5 + s); }
 };
 
 __device__ __forceinline__ void give_up(int* err, volatile int* abort) {
@@ -477,7 +478,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   __shared__ int s_offs[257];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ __align__(8) uint64_t s_bar[3 * kStages + 5];
+  __shared__ __align__(8) uint64_t s_bar[4 * kStages + 5];
   const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sB = sA + kStages * kOperand;
   const uint32_t sOut = sB + kStages * kOperand;
@@ -493,9 +494,10 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
     for (int e = lane; e <= E; e += 32) s_offs[e] = offs[e];
     if (lane == 0) {
       for (int s = 0; s < kStages; ++s) {
-        tc::mbar_init(bar.full(s), 2);    // used in the leader: one arrival for each CTA
+        tc::mbar_init(bar.full(s), 1);
         tc::mbar_init(bar.empty(s), 1);
         tc::mbar_init(bar.fix(s), 1);     // this CTA's loads of a stage that is zeroed in part
+        tc::mbar_init(bar.fixed(s), 2);   // used in the leader: both CTAs have zeroed
       }
       for (int a = 0; a < 2; ++a) {
         tc::mbar_init(bar.tfull(a), 1);
@@ -543,7 +545,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   // the last block of an expert's rows is zeroed in part unless it ends with a group of 16
   auto zeroed = [](const Tile& d, int kb) { return kb == d.nk - 1 && d.rows % 16 != 0; };
 
-  uint32_t filled = 0, fill_par = 0, fixed = 0, fix_par = 0, last_fix = 0;
+  uint32_t filled = 0, fill_par = 0, fixed = 0, fix_par = 0;
   bool producer = false;
   if (warp == 0) {
     if (tc::elect_one()) {
@@ -559,11 +561,11 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
         for (int kb = 0; kb < d.nk; ++kb) {
           if (!tc::mbar_wait(bar.empty(stage), phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
           const bool z = zeroed(d, kb);
-          // a stage to be zeroed is signalled by the zeroing warps once they are done
+          // the loads of a stage to be zeroed complete in their own CTA, for its zeroing warp;
+          // the leader's full barrier only turns over then
           const uint32_t lbar = z ? tc::map_peer(bar.fix(stage), rank) : tc::map_peer(bar.full(stage), 0);
           if (z) tc::mbar_arrive_expect_tx(bar.fix(stage), kStageBytes);
-          else if (rank == 0) tc::mbar_arrive_expect_tx(bar.full(stage), 2 * kStageBytes);
-          else tc::mbar_arrive_remote(lbar);
+          if (rank == 0) tc::mbar_arrive_expect_tx(bar.full(stage), z ? 0u : 2 * kStageBytes);
           const int r = d.row0 + kb * kBK;
           const uint32_t a = sA + stage * kOperand, b = sB + stage * kOperand;
           tc::tma_load_2d_pair(a, mA, lbar, m, r);
@@ -573,7 +575,6 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
           const uint32_t bit = 1u << stage;
           filled |= bit;
           fill_par = (fill_par & ~bit) | (phase << stage);
-          last_fix = z ? last_fix | bit : last_fix & ~bit;
           if (z) {
             fix_par ^= (fixed & bit);     // the first use completes phase 0, each later one the other
             fixed |= bit;
@@ -587,7 +588,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   } else if (warp == 1) {
     if (rank == 0 && tc::elect_one()) {
       int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t phase = 0, acc_phase = 0, seen = 0;
       bool ok = true;
       const uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | kMajorA | kMajorB;
       for (int t = first; t < total && ok; t += step) {
@@ -596,7 +597,13 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
         tc::tc_fence_after();
         const uint32_t dst = tmem + (uint32_t)(acc * kTile);
         for (int kb = 0; kb < d.nk; ++kb) {
-          if (!tc::mbar_wait<true>(bar.full(stage), phase, &s_abort, kWaitNs)) { ok = false; break; }
+          if (!tc::mbar_wait(bar.full(stage), phase, &s_abort, kWaitNs)) { ok = false; break; }
+          if (zeroed(d, kb)) {
+            // the other CTA's zeroing reaches this thread by a release and an acquire at cluster
+            // scope; both cost about 0.7 us, so only these stages pay for them
+            if (!tc::mbar_wait<true>(bar.fixed(stage), (seen >> stage) & 1u, &s_abort, kWaitNs)) { ok = false; break; }
+            seen ^= 1u << stage;
+          }
           tc::tc_fence_after();
           const uint32_t a0 = sA + stage * kOperand, b0 = sB + stage * kOperand;
           const int groups = min(kBK / 16, (d.rows - kb * kBK + 15) / 16);
@@ -640,7 +647,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(box + r * 128), "r"(0) : "memory");
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(bar.full(last), 0));
+        if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(bar.fixed(last), 0));
       }
       for (int i = 0; i < d.nk % kStages; ++i) advance(stage, phase);
     }
@@ -705,7 +712,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   if (producer && s_abort)
     for (int s = 0; s < kStages; ++s) {
       if ((fixed >> s) & 1u) tc::mbar_wait(bar.fix(s), (fix_par >> s) & 1u, nullptr, kWaitNs);
-      if (rank == 0 && ((filled & ~last_fix) >> s) & 1u)
+      if (rank == 0 && (filled >> s) & 1u)
         tc::mbar_wait(bar.full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
     }
   tc::cluster_sync();
