@@ -28,7 +28,9 @@
 // in shared memory before the MMAs may read the stage, since 0 x NaN is NaN.
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader CTA of the
-// pair), warps 2-5 epilogue, warp 6 (weights kernel) the zeroing.  Every wait
+// pair), warps 2-9 epilogue, warp 10 (weights kernel) the zeroing.  Two
+// epilogue warps share a quarter of the TMEM lanes and halve its columns: with
+// one, the slopes of a da tile took longer than its MMAs.  Every wait
 // is bounded: on expiry the kernel records a timeout in the workspace's error
 // word, drains what it has in flight, frees its tensor memory and returns.
 #include <cudaTypedefs.h>
@@ -52,9 +54,11 @@ constexpr int kHalf = kOperand / 2;       // an MN-major operand is two boxes of
 constexpr int kStageBytes = 2 * kOperand;
 constexpr int kStages = 6;
 constexpr int kTmemCols = 512;            // two accumulators of 256 columns
+constexpr int kEpiWarps = 8;              // per CTA: two for each quarter of the TMEM lanes
 constexpr int kStoreBytes = 32 * 128;     // an epilogue warp's store tile: 32 rows of 128 bytes
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes;
-constexpr size_t kSmemW = kSmem + 8 * kStoreBytes;   // two store tiles for each of 4 warps
+constexpr size_t kSmemW = kSmem + kEpiWarps * kStoreBytes;
+constexpr int kRowsThreads = 64 + 32 * kEpiWarps, kWeightsThreads = kRowsThreads + 32;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 enum Product { kDh, kDaGelu, kDaSwiglu, kDx };
@@ -155,11 +159,13 @@ __device__ __forceinline__ void store_row(T* dst, const float* v, int n) {   // 
     if (g * Vec<T>::N < n) reinterpret_cast<uint4*>(dst)[g] = Vec<T>::pack(v + g * Vec<T>::N);
 }
 
-// One tile of the rows kernel.  Row orientation: this thread's row, 32
-// columns at a time.  Swapped: this thread's column, 32 rows at a time.
+// One tile of the rows kernel, this warp's half of it.  Row orientation: this
+// thread's row, 32 columns at a time, the tile's left or right half.  Swapped:
+// this thread's column, every other group of 32 rows.
 template <int kKind>
 __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, int row_base, int nrows, int n0,
-                                              int block, int rank, int q, int lane, int N, const RowsOut& o) {
+                                              int block, int rank, int q, int half, int lane, int N,
+                                              const RowsOut& o) {
   constexpr bool kSwi = kKind == kDaSwiglu, kDa = kKind == kDaGelu || kSwi;
   constexpr int kOut = kSwi ? kBM : kTile;
   const int wide = kSwi ? 2 * N : N;     // columns of da and of the bias
@@ -170,41 +176,53 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
     const float bf = be && ok ? be[f] : 0.f;
     float sum = 0.f;
 #pragma unroll 1
-    for (int c = 0; c * 32 < nrows; ++c) {
+    for (int c = half; c * 32 < nrows; c += 2) {
+      const int64_t at = (int64_t)(row_base + c * 32) * N + f;
+      const int left = ok ? nrows - c * 32 : 0;
+      float dh[kDa ? 32 : 1];
+      if (kDa) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) dh[j % (kDa ? 32 : 1)] = j < left ? __ldcs(o.dh + at + (int64_t)j * N) : 0.f;
+      }
       uint32_t r[32];
       tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
       tc::tmem_wait_ld();
-      if (ok) {
-        const int64_t at = (int64_t)(row_base + c * 32) * N + f;
-        const int left = nrows - c * 32;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j < left) {
-            const float v = __uint_as_float(r[j]);
-            if (kKind == kDh) {
-              o.dh[at + (int64_t)j * N] = v;
-            } else if (kKind == kDx) {
-              o.dx[at + (int64_t)j * N] = __float2bfloat16_rn(v);
-            } else {
-              const float d = o.dh[at + (int64_t)j * N] * gelu_slope(v + bf);
-              sum += d;
-              o.da[at + (int64_t)j * N] = __float2bfloat16_rn(d);
-            }
+      for (int j = 0; j < 32; ++j) {
+        if (j < left) {
+          const float v = __uint_as_float(r[j]);
+          if (kKind == kDh) {
+            o.dh[at + (int64_t)j * N] = v;
+          } else if (kKind == kDx) {
+            o.dx[at + (int64_t)j * N] = __float2bfloat16_rn(v);
+          } else {
+            const float d = dh[j % (kDa ? 32 : 1)] * gelu_slope(v + bf);
+            sum += d;
+            o.da[at + (int64_t)j * N] = __float2bfloat16_rn(d);
           }
         }
       }
     }
-    if (kDa && o.part && ok) o.part[(int64_t)block * 8 * wide + f] = sum;
+    if (kDa && o.part && ok) o.part[((int64_t)block * 8 + half) * wide + f] = sum;
     return;
   }
   const int r0 = rank * kBM + q * 32;          // this warp's first row of the block
   const int64_t row = row_base + r0 + lane;
   const bool ok = r0 + lane < nrows;
 #pragma unroll 1
-  for (int c = 0; c < kOut / 32; ++c) {
+  for (int c = half * (kOut / 64); c < (half + 1) * (kOut / 64); ++c) {
     const int col = n0 + c * 32;
     if (col >= N) break;
-    const int left = min(32, N - col);
+    const int left = min(32, N - col);     // a multiple of 8
+    float4 d[kDa ? 8 : 1];
+    if (kDa) {
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        d[g % (kDa ? 8 : 1)] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ok && g * 4 < left)
+          d[g % (kDa ? 8 : 1)] = __ldcs(reinterpret_cast<const float4*>(o.dh + row * N + col + g * 4));
+      }
+    }
     uint32_t r[32], u[kSwi ? 32 : 1];
     tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
     if (kSwi) tc::tmem_ld_32x32b_x32(tbase + kBM + c * 32, u);
@@ -221,21 +239,25 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
       float w[kSwi ? 32 : 1];
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
-        float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ok && g * 4 < left) d = __ldcs(reinterpret_cast<const float4*>(o.dh + row * N + col + g * 4));
-        const float dh[4] = {d.x, d.y, d.z, d.w};
+        float ba[4] = {0.f, 0.f, 0.f, 0.f}, bb[4] = {0.f, 0.f, 0.f, 0.f};
+        if (be && g * 4 < left) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ba[i] = be[col + g * 4 + i];
+            if (kSwi) bb[i] = be[N + col + g * 4 + i];
+          }
+        }
+        const float4 dg = d[g % (kDa ? 8 : 1)];
+        const float dh[4] = {dg.x, dg.y, dg.z, dg.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int j = g * 4 + i;
-          float a = __uint_as_float(r[j]);
-          if (be && j < left) a += be[col + j];
-          if (kSwi) {
-            float b = __uint_as_float(u[j % (kSwi ? 32 : 1)]);
-            if (be && j < left) b += be[N + col + j];
-            swiglu_gradient(a, b, dh[i], &v[j], &w[j % (kSwi ? 32 : 1)]);
-          } else {
+          const float a = __uint_as_float(r[j]) + ba[i];
+          if (kSwi)
+            swiglu_gradient(a, __uint_as_float(u[j % (kSwi ? 32 : 1)]) + bb[i], dh[i], &v[j],
+                            &w[j % (kSwi ? 32 : 1)]);
+          else
             v[j] = dh[i] * gelu_slope(a);
-          }
         }
       }
       if (ok) {
@@ -273,7 +295,7 @@ struct Bars {
   __device__ uint32_t tempty(int a) const { return base + 8 * (2 * kStages + 2 + a); }
   __device__ uint32_t done() const { return base + 8 * (2 * kStages + 4); }
   __device__ uint32_t fix(int s) const { return base + 8 * (2 * kStages + 5 + s); }
-  __device__ uint32_t fixed(int s) const { return base + 8 * (3 * kStages + 5 + s); }
+  __device__ uint32_t peer(int s) const { return base + 8 * (3 * kStages + 5 + s); }
 };
 
 __device__ __forceinline__ void give_up(int* err, volatile int* abort) {
@@ -284,7 +306,7 @@ __device__ __forceinline__ void give_up(int* err, volatile int* abort) {
 // tmX, tmXs: token rows [rows, K] in boxes of 128 and 32 rows.  tmW: weights
 // K-major [E N, K] (kDa*) or [E, K, N] in 64 x 64 boxes (kDh, kDx).
 template <int kKind>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(kRowsThreads, 1)
 backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                      const __grid_constant__ CUtensorMap tmW, const int32_t* __restrict__ offs, int E, int N, int K,
                      RowsOut out, int* err) {
@@ -312,7 +334,7 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
       }
       for (int a = 0; a < 2; ++a) {
         tc::mbar_init(bar.tfull(a), 1);
-        tc::mbar_init(bar.tempty(a), 2 * 128);
+        tc::mbar_init(bar.tempty(a), 2 * 32 * kEpiWarps);
       }
       tc::mbar_init(bar.done(), 1);
       s_abort = 0;
@@ -430,7 +452,7 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
     if (lane == 0 && !tc::mbar_wait(bar.done(), 0, nullptr, kWaitNs)) set_error(err, kDevTimeout);
     __syncwarp();
   } else {
-    const int q = warp & 3;   // TMEM lanes 32 q .. 32 q + 31 belong to this warp
+    const int q = warp & 3, half = (warp - 2) >> 2;   // TMEM lanes 32 q .. 32 q + 31 belong to this warp
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = first; t < total; t += step) {
@@ -441,7 +463,7 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
       }
       tc::tc_fence_after();
       rows_epilogue<kKind>(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile), d.swap, d.e, d.row_base,
-                           d.nrows, d.n0, d.block, rank, q, lane, N, out);
+                           d.nrows, d.n0, d.block, rank, q, half, lane, N, out);
       tc::tc_fence_before();
       if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
       else tc::mbar_arrive_remote(tc::map_peer(bar.tempty(acc), 0));
@@ -469,7 +491,7 @@ struct WeightProduct {
 
 // tmA, tmB: the operands' rows in 64 x 64 boxes; tmO: out [E, M, N] in boxes
 // of 32 rows x 64 columns.  Products 0 and 1 follow one another.
-__global__ void __launch_bounds__(224, 1)
+__global__ void __launch_bounds__(kWeightsThreads, 1)
 backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
                         const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmA1,
                         const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmO1,
@@ -497,11 +519,11 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
         tc::mbar_init(bar.full(s), 1);
         tc::mbar_init(bar.empty(s), 1);
         tc::mbar_init(bar.fix(s), 1);     // this CTA's loads of a stage that is zeroed in part
-        tc::mbar_init(bar.fixed(s), 2);   // used in the leader: both CTAs have zeroed
+        tc::mbar_init(bar.peer(s), 1);    // used in the leader: the other CTA has zeroed
       }
       for (int a = 0; a < 2; ++a) {
         tc::mbar_init(bar.tfull(a), 1);
-        tc::mbar_init(bar.tempty(a), 2 * 128);
+        tc::mbar_init(bar.tempty(a), 2 * 32 * kEpiWarps);
       }
       tc::mbar_init(bar.done(), 1);
       s_abort = 0;
@@ -545,7 +567,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   // the last block of an expert's rows is zeroed in part unless it ends with a group of 16
   auto zeroed = [](const Tile& d, int kb) { return kb == d.nk - 1 && d.rows % 16 != 0; };
 
-  uint32_t filled = 0, fill_par = 0, fixed = 0, fix_par = 0;
+  uint32_t filled = 0, fill_par = 0, fixed = 0, fix_par = 0, last_fix = 0;
   bool producer = false;
   if (warp == 0) {
     if (tc::elect_one()) {
@@ -561,11 +583,11 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
         for (int kb = 0; kb < d.nk; ++kb) {
           if (!tc::mbar_wait(bar.empty(stage), phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
           const bool z = zeroed(d, kb);
-          // the loads of a stage to be zeroed complete in their own CTA, for its zeroing warp;
-          // the leader's full barrier only turns over then
+          // the loads of a stage to be zeroed complete in their own CTA, for its
+          // zeroing warp; the leader's then completes the full barrier
           const uint32_t lbar = z ? tc::map_peer(bar.fix(stage), rank) : tc::map_peer(bar.full(stage), 0);
           if (z) tc::mbar_arrive_expect_tx(bar.fix(stage), kStageBytes);
-          if (rank == 0) tc::mbar_arrive_expect_tx(bar.full(stage), z ? 0u : 2 * kStageBytes);
+          else if (rank == 0) tc::mbar_arrive_expect_tx(bar.full(stage), 2 * kStageBytes);
           const int r = d.row0 + kb * kBK;
           const uint32_t a = sA + stage * kOperand, b = sB + stage * kOperand;
           tc::tma_load_2d_pair(a, mA, lbar, m, r);
@@ -575,6 +597,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
           const uint32_t bit = 1u << stage;
           filled |= bit;
           fill_par = (fill_par & ~bit) | (phase << stage);
+          last_fix = z ? last_fix | bit : last_fix & ~bit;
           if (z) {
             fix_par ^= (fixed & bit);     // the first use completes phase 0, each later one the other
             fixed |= bit;
@@ -588,7 +611,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   } else if (warp == 1) {
     if (rank == 0 && tc::elect_one()) {
       int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0, seen = 0;
+      uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       const uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | kMajorA | kMajorB;
       for (int t = first; t < total && ok; t += step) {
@@ -598,12 +621,6 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
         const uint32_t dst = tmem + (uint32_t)(acc * kTile);
         for (int kb = 0; kb < d.nk; ++kb) {
           if (!tc::mbar_wait(bar.full(stage), phase, &s_abort, kWaitNs)) { ok = false; break; }
-          if (zeroed(d, kb)) {
-            // the other CTA's zeroing reaches this thread by a release and an acquire at cluster
-            // scope; both cost about 0.7 us, so only these stages pay for them
-            if (!tc::mbar_wait<true>(bar.fixed(stage), (seen >> stage) & 1u, &s_abort, kWaitNs)) { ok = false; break; }
-            seen ^= 1u << stage;
-          }
           tc::tc_fence_after();
           const uint32_t a0 = sA + stage * kOperand, b0 = sB + stage * kOperand;
           const int groups = min(kBK / 16, (d.rows - kb * kBK + 15) / 16);
@@ -623,7 +640,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
     __syncwarp();
     if (lane == 0 && !tc::mbar_wait(bar.done(), 0, nullptr, kWaitNs)) set_error(err, kDevTimeout);
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == 2 + kEpiWarps) {
     // zero the rows past the expert's end in both operands of its last block:
     // row k of a box is the 128 bytes at 128 k, whatever the swizzle does within them
     int stage = 0;
@@ -647,14 +664,27 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(box + r * 128), "r"(0) : "memory");
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(bar.fixed(last), 0));
+        // The other CTA's zeroing reaches the MMA thread through the leader's
+        // zeroing warp: a release and an acquire at cluster scope hold up the
+        // thread that makes them (on every stage they made the kernel 1.6
+        // times as long), and this warp has the ring's depth to spare.
+        if (rank != 0) {
+          if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(bar.peer(last), 0));
+        } else {
+          if (!__all_sync(0xffffffffu, tc::mbar_wait<true>(bar.peer(last), par, &s_abort, kWaitNs))) {
+            if (lane == 0) give_up(err, &s_abort);
+            break;
+          }
+          if (lane == 0) tc::mbar_arrive(bar.full(last));
+        }
       }
       for (int i = 0; i < d.nk % kStages; ++i) advance(stage, phase);
     }
   } else {
-    const int q = warp & 3;
-    const uint32_t buf0 = sOut + q * 2 * kStoreBytes;
-    int acc = 0, turn = 0;
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t buf = sOut + (warp - 2) * kStoreBytes;
+    uint8_t* g = gOut + (buf - sOut);
+    int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = first; t < total; t += step) {
       const Tile d = decode(t);
@@ -668,13 +698,10 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
       const int m = d.m0 + rank * kBM + q * 32;
       if (m < M) {
 #pragma unroll 1
-        for (int c = 0; c < kTile / 64; ++c) {
+        for (int c = half * (kTile / 128); c < (half + 1) * (kTile / 128); ++c) {
           const int n = d.n0 + c * 64;
           if (n >= N) break;
-          const uint32_t buf = buf0 + turn * kStoreBytes;
-          turn ^= 1;
-          uint8_t* g = gOut + (buf - sOut);
-          if (lane == 0) tc::bulk_wait_read<1>();   // this buffer's previous store has been read
+          if (lane == 0) tc::bulk_wait_read<0>();   // the buffer's previous store has been read
           __syncwarp();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -712,7 +739,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   if (producer && s_abort)
     for (int s = 0; s < kStages; ++s) {
       if ((fixed >> s) & 1u) tc::mbar_wait(bar.fix(s), (fix_par >> s) & 1u, nullptr, kWaitNs);
-      if (rank == 0 && (filled >> s) & 1u)
+      if (rank == 0 && ((filled & ~last_fix) >> s) & 1u)
         tc::mbar_wait(bar.full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
     }
   tc::cluster_sync();
@@ -722,22 +749,30 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   }
 }
 
-// db1[e, c]: the row blocks' partial sums in order.  A swapped block has one
-// partial, another eight.
-__global__ void __launch_bounds__(128)
+// db1[e, c]: the row blocks' partial sums, added in a fixed order.  A swapped
+// block has two partials, another eight; 8 threads of a column take them in turn.
+constexpr int kRedCols = 32, kRedGroups = 8;
+__global__ void __launch_bounds__(kRedCols * kRedGroups)
 bias_reduce_kernel(const float* __restrict__ part, const int32_t* __restrict__ offs, int n, int swaps,
                    float* __restrict__ db) {
+  __shared__ float s[kRedGroups][kRedCols];
   pdl_enter();
-  const int e = blockIdx.y, c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= n) return;
+  const int e = blockIdx.y, g = threadIdx.x / kRedCols, c = blockIdx.x * kRedCols + threadIdx.x % kRedCols;
   const int r0 = offs[e], rows = offs[e + 1] - r0, mt = row_blocks(rows);
-  const int64_t first = (int64_t)((r0 >> 8) + e) * 8;
+  const int last = mt > 0 ? rows - (mt - 1) * kTile : 0;
+  const int parts = 8 * mt - (swaps && mt > 0 && last <= kSwapRows ? 6 : 0);
+  const float* p = part + ((int64_t)(r0 >> 8) + e) * 8 * n + c;
   float sum = 0.f;
-  for (int b = 0; b < mt; ++b) {
-    const int parts = swaps && rows - b * kTile <= kSwapRows ? 1 : 8;
-    for (int i = 0; i < parts; ++i) sum += part[(first + b * 8 + i) * n + c];
+  if (c < n) {
+#pragma unroll 4
+    for (int i = g; i < parts; i += kRedGroups) sum += p[(int64_t)i * n];
   }
-  db[(int64_t)e * n + c] = sum;
+  s[g][threadIdx.x % kRedCols] = sum;
+  __syncthreads();
+  if (g == 0 && c < n) {
+    for (int i = 1; i < kRedGroups; ++i) sum += s[i][threadIdx.x];
+    db[(int64_t)e * n + c] = sum;
+  }
 }
 
 // One persistent launch of CTA pairs, never more than fit at once.
@@ -759,7 +794,7 @@ cudaError_t run_rows(const void* tokens, int64_t rows, int K, const void* W, int
   if (kMN ? !tma_map_bf16_3d(&mw, W, (uint64_t)E, (uint64_t)K, (uint64_t)N, kBK)
           : !tma_map_bf16(&mw, W, (uint64_t)E * N * (kKind == kDaSwiglu ? 2 : 1), (uint64_t)K, kBM))
     return cudaErrorNotSupported;
-  return launch_pairs(backward_rows_kernel<kKind>, 192, kSmem, st, mx, mxs, mw, offs, E, N, K, out, err);
+  return launch_pairs(backward_rows_kernel<kKind>, kRowsThreads, kSmem, st, mx, mxs, mw, offs, E, N, K, out, err);
 }
 
 }  // namespace
@@ -788,7 +823,8 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
       e = swi ? run_rows<kDaSwiglu>(b.x_perm, max_rows, s.H, b.W1, s.E, s.F, b.offs, out, err, st)
               : run_rows<kDaGelu>(b.x_perm, max_rows, s.H, b.W1, s.E, s.F, b.offs, out, err, st);
     if (e == cudaSuccess && b.db1)
-      e = launch_kernel(bias_reduce_kernel, dim3((unsigned)((N + 127) / 128), (unsigned)s.E), dim3(128), 0, st, 1,
+      e = launch_kernel(bias_reduce_kernel, dim3((unsigned)((N + kRedCols - 1) / kRedCols), (unsigned)s.E),
+                        dim3(kRedCols * kRedGroups), 0, st, 1,
                         (const float*)part, b.offs, N, swi ? 0 : 1, b.db1);
     if (e == cudaSuccess && b.dx_perm)
       e = run_rows<kDx>(da, max_rows, N, b.W1, s.E, s.H, b.offs, out, err, st);
@@ -811,7 +847,7 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
       for (int i = 0; i < 3; ++i) m[3 + i] = m[i];
       P[1] = {0, 0};
     }
-    e = launch_pairs(backward_weights_kernel, 224, kSmemW, st, m[0], m[1], m[2], m[3], m[4], m[5], b.offs, s.E, P[0],
+    e = launch_pairs(backward_weights_kernel, kWeightsThreads, kSmemW, st, m[0], m[1], m[2], m[3], m[4], m[5], b.offs, s.E, P[0],
                      P[1], err);
   }
   if (e == cudaSuccess && b.db2) e = launch_row_sums(MOE_BF16, b.dy_perm, b.offs, s.E, s.H, b.db2, st);
