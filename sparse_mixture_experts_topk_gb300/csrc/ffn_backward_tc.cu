@@ -22,14 +22,16 @@
 // side; an expert's last block of at most 128 rows runs swapped (256 weight
 // columns on M, the rows on N rounded up to 16), so that few rows do not cost
 // a full tile.  Weights kernel (dW1, dW2): the reduction runs over an
-// expert's rows in blocks of 64, 16 to an MMA.  Its last block usually ends
-// inside a group of 16, where TMA has brought rows of the next expert (or
-// memory nobody wrote): a warp of each CTA zeroes those rows of both operands
-// in shared memory before the MMAs may read the stage, since 0 x NaN is NaN.
+// expert's rows in blocks of 64, 16 to an MMA.  The rows that do not fill a
+// group of 16 come from copies of them, padded with zeros to 16, that a small
+// kernel makes first: in place the group goes on with rows of the next expert
+// or with memory that nobody wrote, in both operands, and 0 x NaN is NaN.
+// (Zeroing those rows in shared memory was measured: the second CTA's zeroing
+// has to reach the MMA thread through a release and an acquire at cluster
+// scope, 2300 cycles of a tile's 4300.)
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader CTA of the
-// pair), warps 2-9 epilogue, warp 10 (weights kernel) the zeroing.  Two
-// epilogue warps share a quarter of the TMEM lanes and halve its columns: with
+// pair), warps 2-9 epilogue.  Two epilogue warps share a quarter of the TMEM lanes and halve its columns: with
 // one, the slopes of a da tile took longer than its MMAs.  Every wait
 // is bounded: on expiry the kernel records a timeout in the workspace's error
 // word, drains what it has in flight, frees its tensor memory and returns.
@@ -52,13 +54,11 @@ constexpr int kSwapRows = 128;            // a last block of at most this many r
 constexpr int kOperand = kBM * kBK * 2;   // bytes of one operand in a stage
 constexpr int kHalf = kOperand / 2;       // an MN-major operand is two boxes of 64 columns x 64 rows
 constexpr int kStageBytes = 2 * kOperand;
-constexpr int kStages = 6;
+constexpr int kRowsStages = 6, kWeightsStages = 7;   // the rows kernel's tile tables leave no room for a seventh
 constexpr int kTmemCols = 512;            // two accumulators of 256 columns
 constexpr int kEpiWarps = 8;              // per CTA: two for each quarter of the TMEM lanes
-constexpr int kStoreBytes = 32 * 128;     // an epilogue warp's store tile: 32 rows of 128 bytes
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes;
-constexpr size_t kSmemW = kSmem + kEpiWarps * kStoreBytes;
-constexpr int kRowsThreads = 64 + 32 * kEpiWarps, kWeightsThreads = kRowsThreads + 32;
+constexpr size_t smem_bytes(int stages) { return 1024 + (size_t)stages * kStageBytes; }
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 enum Product { kDh, kDaGelu, kDaSwiglu, kDx };
@@ -122,6 +122,7 @@ __device__ __forceinline__ int expert_of(const int* tstart, int E, int t) {
   return lo;
 }
 
+template <int kStages>
 __device__ __forceinline__ void advance(int& stage, uint32_t& phase) {
   if (++stage == kStages) {
     stage = 0;
@@ -136,6 +137,7 @@ struct RowsOut {
   bf16* dx;             // [rows, H]
   const float* bias;    // b1 or null
   float* part;          // [blocks * 8, G F] partial sums of da over rows, or null
+  bool sectors;         // what this product writes has rows that start on 32 bytes
 };
 
 // Sum over the warp's lanes of 32 values each: lane l returns the sum of v[l].
@@ -152,11 +154,21 @@ __device__ __forceinline__ float column_sum(float* v, int lane) {
   return v[0];
 }
 
+// n of 32 values (n a multiple of 8) to a row; whole 32-byte sectors where
+// every row starts on one (`sectors`), else 16 bytes at a time.
 template <typename T>
-__device__ __forceinline__ void store_row(T* dst, const float* v, int n) {   // n values, a multiple of 8, at most 32
+__device__ __forceinline__ void store_row(T* dst, const float* v, int n, bool sectors) {
+  constexpr int V = Vec<T>::N;
 #pragma unroll
-  for (int g = 0; g < 32 / Vec<T>::N; ++g)
-    if (g * Vec<T>::N < n) reinterpret_cast<uint4*>(dst)[g] = Vec<T>::pack(v + g * Vec<T>::N);
+  for (int g = 0; g < 32 / (2 * V); ++g) {
+    const uint4 lo = Vec<T>::pack(v + 2 * g * V), hi = Vec<T>::pack(v + (2 * g + 1) * V);
+    if (sectors && (2 * g + 2) * V <= n) {
+      tc::st_global_32(dst + 2 * g * V, lo, hi);
+    } else {
+      if (2 * g * V < n) *reinterpret_cast<uint4*>(dst + 2 * g * V) = lo;
+      if ((2 * g + 1) * V < n) *reinterpret_cast<uint4*>(dst + (2 * g + 1) * V) = hi;
+    }
+  }
 }
 
 // One tile of the rows kernel, this warp's half of it.  Row orientation: this
@@ -232,8 +244,8 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
       if (ok) {
-        if (kKind == kDh) store_row(o.dh + row * N + col, v, left);
-        else store_row(o.dx + row * N + col, v, left);
+        if (kKind == kDh) store_row(o.dh + row * N + col, v, left, o.sectors);
+        else store_row(o.dx + row * N + col, v, left, o.sectors);
       }
     } else {
       float w[kSwi ? 32 : 1];
@@ -261,8 +273,8 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
         }
       }
       if (ok) {
-        store_row(o.da + row * wide + col, v, left);
-        if (kSwi) store_row(o.da + row * wide + N + col, w, left);
+        store_row(o.da + row * wide + col, v, left, o.sectors);
+        if (kSwi) store_row(o.da + row * wide + N + col, w, left, o.sectors);
       }
       if (o.part) {
         // rows past the block's end and columns past N are other data: they count as zeros
@@ -287,6 +299,7 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
 __device__ __forceinline__ int row_blocks(int rows) { return (rows + kTile - 1) / kTile; }
 
 // Barriers of a CTA: full and empty per stage, full and empty per accumulator, the end.
+template <int kStages>
 struct Bars {
   uint32_t base;
   __device__ uint32_t full(int s) const { return base + 8 * s; }
@@ -294,8 +307,6 @@ struct Bars {
   __device__ uint32_t tfull(int a) const { return base + 8 * (2 * kStages + a); }
   __device__ uint32_t tempty(int a) const { return base + 8 * (2 * kStages + 2 + a); }
   __device__ uint32_t done() const { return base + 8 * (2 * kStages + 4); }
-  __device__ uint32_t fix(int s) const { return base + 8 * (2 * kStages + 5 + s); }
-  __device__ uint32_t peer(int s) const { return base + 8 * (3 * kStages + 5 + s); }
 };
 
 __device__ __forceinline__ void give_up(int* err, volatile int* abort) {
@@ -306,12 +317,13 @@ __device__ __forceinline__ void give_up(int* err, volatile int* abort) {
 // tmX, tmXs: token rows [rows, K] in boxes of 128 and 32 rows.  tmW: weights
 // K-major [E N, K] (kDa*) or [E, K, N] in 64 x 64 boxes (kDh, kDx).
 template <int kKind>
-__global__ void __launch_bounds__(kRowsThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                      const __grid_constant__ CUtensorMap tmW, const int32_t* __restrict__ offs, int E, int N, int K,
                      RowsOut out, int* err) {
   constexpr bool kSwi = kKind == kDaSwiglu, kMN = kKind == kDh || kKind == kDx;
   constexpr int kOut = kSwi ? kBM : kTile;
+  constexpr int kStages = kRowsStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_offs[257], s_tstart[257];
   __shared__ uint32_t s_tmem;
@@ -319,7 +331,7 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sB = sA + kStages * kOperand;
-  const Bars bar{tc::smem_u32(s_bar)};
+  const Bars<kStages> bar{tc::smem_u32(s_bar)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)tc::cluster_ctarank();
   const int nt = (N + kOut - 1) / kOut, nk = (K + kBK - 1) / kBK;
@@ -407,7 +419,7 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
           }
           filled |= 1u << stage;
           fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
-          advance(stage, phase);
+          advance<kStages>(stage, phase);
         }
       }
       if (!ok) give_up(err, &s_abort);
@@ -438,7 +450,7 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
             tc::mma_bf16_pair(dst, da, db, idesc, (kb | k) != 0);
           }
           tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
-          advance(stage, phase);
+          advance<kStages>(stage, phase);
         }
         if (!ok) break;
         tc::tc_commit_pair_mc(bar.tfull(acc), 0x3);
@@ -483,29 +495,58 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   }
 }
 
+// The rows of each expert past its last whole group of 16, padded with zeros
+// to 16: tails [E, 16, cols] for each of up to four operands.
+struct Operand {
+  const uint4* rows;
+  uint4* tails;
+  int vec;              // 16-byte vectors in a row
+};
+struct Operands {
+  Operand o[4];
+};
+constexpr int kTailRows = 16, kTailSplit = 4;
+__global__ void __launch_bounds__(256)
+expert_tails_kernel(const __grid_constant__ Operands ops, const int32_t* __restrict__ offs) {
+  pdl_enter();
+  const int e = blockIdx.x;
+  const Operand& o = ops.o[blockIdx.y];
+  const int r0 = offs[e], rows = offs[e + 1] - r0, whole = rows / kTailRows * kTailRows;
+  if (rows == whole) return;   // no tail: never read
+  const int per = kTailRows / kTailSplit * o.vec;
+  for (int i = threadIdx.x; i < per; i += blockDim.x) {
+    const int r = blockIdx.z * (kTailRows / kTailSplit) + i / o.vec, v = i % o.vec;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (whole + r < rows) x = o.rows[(int64_t)(r0 + whole + r) * o.vec + v];
+    o.tails[((int64_t)e * kTailRows + r) * o.vec + v] = x;
+  }
+}
+
 // One weight gradient: out [E, M, N] = sum over an expert's rows of A's row
 // (M columns) times B's row (N columns).
 struct WeightProduct {
   int M, N;
+  bf16* out;
+  bool sectors;    // out's rows start on 32 bytes
 };
 
-// tmA, tmB: the operands' rows in 64 x 64 boxes; tmO: out [E, M, N] in boxes
-// of 32 rows x 64 columns.  Products 0 and 1 follow one another.
-__global__ void __launch_bounds__(kWeightsThreads, 1)
+// tmA, tmB: an operand's rows in boxes of 64 x 64; tmAt, tmBt: its tails in
+// boxes of 64 columns x 16 rows.  Products 0 and 1 follow one another.
+__global__ void __launch_bounds__(kThreads, 1)
 backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
-                        const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmA1,
-                        const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmO1,
+                        const __grid_constant__ CUtensorMap tmAt0, const __grid_constant__ CUtensorMap tmBt0,
+                        const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
+                        const __grid_constant__ CUtensorMap tmAt1, const __grid_constant__ CUtensorMap tmBt1,
                         const int32_t* __restrict__ offs, int E, WeightProduct P0, WeightProduct P1, int* err) {
+  constexpr int kStages = kWeightsStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_offs[257];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ __align__(8) uint64_t s_bar[4 * kStages + 5];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sB = sA + kStages * kOperand;
-  const uint32_t sOut = sB + kStages * kOperand;
-  uint8_t* gOut = smem_raw + (sOut - tc::smem_u32(smem_raw));
-  const Bars bar{tc::smem_u32(s_bar)};
+  const Bars<kStages> bar{tc::smem_u32(s_bar)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)tc::cluster_ctarank();
   auto tiles = [](int n) { return (n + kTile - 1) / kTile; };
@@ -518,8 +559,6 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
       for (int s = 0; s < kStages; ++s) {
         tc::mbar_init(bar.full(s), 1);
         tc::mbar_init(bar.empty(s), 1);
-        tc::mbar_init(bar.fix(s), 1);     // this CTA's loads of a stage that is zeroed in part
-        tc::mbar_init(bar.peer(s), 1);    // used in the leader: the other CTA has zeroed
       }
       for (int a = 0; a < 2; ++a) {
         tc::mbar_init(bar.tfull(a), 1);
@@ -529,12 +568,6 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
       s_abort = 0;
       tc::fence_barrier_init();
       tc::fence_proxy_async_smem();
-      tc::prefetch_tmap(&tmA0);
-      tc::prefetch_tmap(&tmB0);
-      tc::prefetch_tmap(&tmO0);
-      tc::prefetch_tmap(&tmA1);
-      tc::prefetch_tmap(&tmB1);
-      tc::prefetch_tmap(&tmO1);
     }
   } else if (warp == 1) {
     tc::tmem_alloc_pair(tc::smem_u32(&s_tmem), kTmemCols);
@@ -549,25 +582,26 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   const int total0 = E * per0, total = total0 + E * per1, first = blockIdx.x / 2, step = gridDim.x / 2;
 
   struct Tile {
-    int p, e, m0, n0, row0, rows, nk;
+    int p, e, m0, n0, row0, groups, nk;   // groups of 16 rows, the tail's included; stages
+    bool tail;                            // the last stage is the tail's, one group
   };
   auto decode = [&](int t) {
     Tile d;
     d.p = t >= total0 ? 1 : 0;
     const int tl = t - (d.p ? total0 : 0), per = d.p ? per1 : per0, nt = tiles(d.p ? P1.N : P0.N);
     d.e = tl / per;
-    const int local = tl % per;
-    d.m0 = (local / nt) * kTile;
-    d.n0 = (local % nt) * kTile;
+    const int local = tl - d.e * per, mi = local / nt;
+    d.m0 = mi * kTile;
+    d.n0 = (local - mi * nt) * kTile;
     d.row0 = s_offs[d.e];
-    d.rows = s_offs[d.e + 1] - d.row0;
-    d.nk = (d.rows + kBK - 1) / kBK;
+    const int rows = s_offs[d.e + 1] - d.row0, whole = rows / kTailRows;
+    d.tail = rows % kTailRows != 0;
+    d.nk = (whole * kTailRows + kBK - 1) / kBK + (d.tail ? 1 : 0);
+    d.groups = whole + (d.tail ? 1 : 0);
     return d;
   };
-  // the last block of an expert's rows is zeroed in part unless it ends with a group of 16
-  auto zeroed = [](const Tile& d, int kb) { return kb == d.nk - 1 && d.rows % 16 != 0; };
 
-  uint32_t filled = 0, fill_par = 0, fixed = 0, fix_par = 0, last_fix = 0;
+  uint32_t filled = 0, fill_par = 0;
   bool producer = false;
   if (warp == 0) {
     if (tc::elect_one()) {
@@ -582,27 +616,24 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
         const int m = d.m0 + rank * kBM, n = d.n0 + rank * kBM;
         for (int kb = 0; kb < d.nk; ++kb) {
           if (!tc::mbar_wait(bar.empty(stage), phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
-          const bool z = zeroed(d, kb);
-          // the loads of a stage to be zeroed complete in their own CTA, for its
-          // zeroing warp; the leader's then completes the full barrier
-          const uint32_t lbar = z ? tc::map_peer(bar.fix(stage), rank) : tc::map_peer(bar.full(stage), 0);
-          if (z) tc::mbar_arrive_expect_tx(bar.fix(stage), kStageBytes);
-          else if (rank == 0) tc::mbar_arrive_expect_tx(bar.full(stage), 2 * kStageBytes);
-          const int r = d.row0 + kb * kBK;
-          const uint32_t a = sA + stage * kOperand, b = sB + stage * kOperand;
-          tc::tma_load_2d_pair(a, mA, lbar, m, r);
-          tc::tma_load_2d_pair(a + kHalf, mA, lbar, m + 64, r);
-          tc::tma_load_2d_pair(b, mB, lbar, n, r);
-          tc::tma_load_2d_pair(b + kHalf, mB, lbar, n + 64, r);
-          const uint32_t bit = 1u << stage;
-          filled |= bit;
-          fill_par = (fill_par & ~bit) | (phase << stage);
-          last_fix = z ? last_fix | bit : last_fix & ~bit;
-          if (z) {
-            fix_par ^= (fixed & bit);     // the first use completes phase 0, each later one the other
-            fixed |= bit;
+          const uint32_t fbar = tc::map_peer(bar.full(stage), 0);
+          const bool tail = d.tail && kb == d.nk - 1;
+          int r = d.row0 + kb * kBK;
+          if (tail) {
+            mA = d.p ? &tmAt1 : &tmAt0;
+            mB = d.p ? &tmBt1 : &tmBt0;
+            r = d.e * kTailRows;
           }
-          advance(stage, phase);
+          if (rank == 0)
+            tc::mbar_arrive_expect_tx(bar.full(stage), tail ? 2 * kStageBytes * kTailRows / kBK : 2 * kStageBytes);
+          const uint32_t a = sA + stage * kOperand, b = sB + stage * kOperand;
+          tc::tma_load_2d_pair(a, mA, fbar, m, r);
+          tc::tma_load_2d_pair(a + kHalf, mA, fbar, m + 64, r);
+          tc::tma_load_2d_pair(b, mB, fbar, n, r);
+          tc::tma_load_2d_pair(b + kHalf, mB, fbar, n + 64, r);
+          filled |= 1u << stage;
+          fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
+          advance<kStages>(stage, phase);
         }
       }
       if (!ok) give_up(err, &s_abort);
@@ -614,8 +645,9 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       const uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | kMajorA | kMajorB;
+      Tile next = first < total ? decode(first) : Tile{};
       for (int t = first; t < total && ok; t += step) {
-        const Tile d = decode(t);
+        const Tile d = next;
         if (!tc::mbar_wait(bar.tempty(acc), acc_phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
         tc::tc_fence_after();
         const uint32_t dst = tmem + (uint32_t)(acc * kTile);
@@ -623,14 +655,18 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
           if (!tc::mbar_wait(bar.full(stage), phase, &s_abort, kWaitNs)) { ok = false; break; }
           tc::tc_fence_after();
           const uint32_t a0 = sA + stage * kOperand, b0 = sB + stage * kOperand;
-          const int groups = min(kBK / 16, (d.rows - kb * kBK + 15) / 16);
+          // the tail's stage holds the last group alone, the one before it what is left of the whole ones
+          const bool tail = d.tail && kb == d.nk - 1;
+          const int groups = tail ? 1 : min(kBK / 16, d.groups - (d.tail ? 1 : 0) - kb * (kBK / 16));
           for (int k = 0; k < groups; ++k)
             tc::mma_bf16_pair(dst, sdesc_mn128(a0 + k * kStepMN), sdesc_mn128(b0 + k * kStepMN), idesc, (kb | k) != 0);
           tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
-          advance(stage, phase);
+          advance<kStages>(stage, phase);
+          if (kb == 0 && t + step < total) next = decode(t + step);   // its divisions run beside the MMAs
         }
         if (!ok) break;
         tc::tc_commit_pair_mc(bar.tfull(acc), 0x3);
+        if (d.nk == 0 && t + step < total) next = decode(t + step);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
@@ -640,50 +676,8 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
     __syncwarp();
     if (lane == 0 && !tc::mbar_wait(bar.done(), 0, nullptr, kWaitNs)) set_error(err, kDevTimeout);
     __syncwarp();
-  } else if (warp == 2 + kEpiWarps) {
-    // zero the rows past the expert's end in both operands of its last block:
-    // row k of a box is the 128 bytes at 128 k, whatever the swizzle does within them
-    int stage = 0;
-    uint32_t phase = 0, seen = 0;
-    for (int t = first; t < total; t += step) {
-      const Tile d = decode(t);
-      if (d.nk == 0) continue;
-      int last = stage + d.nk - 1;
-      last %= kStages;
-      if (zeroed(d, d.nk - 1)) {
-        const uint32_t par = (seen >> last) & 1u;
-        seen ^= 1u << last;
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.fix(last), par, &s_abort, kWaitNs))) {
-          if (lane == 0) give_up(err, &s_abort);
-          break;
-        }
-        const int r0 = d.rows - (d.nk - 1) * kBK, r1 = (r0 + 15) / 16 * 16;
-        const uint32_t part = lane >> 3, chunk = lane & 7;   // 8 lanes to a row of each of the four boxes
-        const uint32_t box = (part < 2 ? sA : sB) + last * kOperand + (part & 1) * kHalf + chunk * 16;
-        for (int r = r0; r < r1; ++r)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(box + r * 128), "r"(0) : "memory");
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        // The other CTA's zeroing reaches the MMA thread through the leader's
-        // zeroing warp: a release and an acquire at cluster scope hold up the
-        // thread that makes them (on every stage they made the kernel 1.6
-        // times as long), and this warp has the ring's depth to spare.
-        if (rank != 0) {
-          if (lane == 0) tc::mbar_arrive_remote(tc::map_peer(bar.peer(last), 0));
-        } else {
-          if (!__all_sync(0xffffffffu, tc::mbar_wait<true>(bar.peer(last), par, &s_abort, kWaitNs))) {
-            if (lane == 0) give_up(err, &s_abort);
-            break;
-          }
-          if (lane == 0) tc::mbar_arrive(bar.full(last));
-        }
-      }
-      for (int i = 0; i < d.nk % kStages; ++i) advance(stage, phase);
-    }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t buf = sOut + (warp - 2) * kStoreBytes;
-    uint8_t* g = gOut + (buf - sOut);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = first; t < total; t += step) {
@@ -695,36 +689,25 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
       tc::tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile);
       const int M = d.p ? P1.M : P0.M, N = d.p ? P1.N : P0.N;
-      const int m = d.m0 + rank * kBM + q * 32;
-      if (m < M) {
+      const int m = d.m0 + rank * kBM + q * 32 + lane;
+      bf16* row = (d.p ? P1.out : P0.out) + ((int64_t)d.e * M + m) * N;
+      const bool sectors = d.p ? P1.sectors : P0.sectors;
 #pragma unroll 1
-        for (int c = half * (kTile / 128); c < (half + 1) * (kTile / 128); ++c) {
-          const int n = d.n0 + c * 64;
-          if (n >= N) break;
-          if (lane == 0) tc::bulk_wait_read<0>();   // the buffer's previous store has been read
-          __syncwarp();
+      for (int c = half * (kTile / 64); c < (half + 1) * (kTile / 64); ++c) {
+        const int n = d.n0 + c * 32;
+        if (n >= N) break;
+        float v[32];
+        if (d.nk > 0) {
+          uint32_t r[32];
+          tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
+          tc::tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float v[32];
-            if (d.nk > 0) {
-              uint32_t r[32];
-              tc::tmem_ld_32x32b_x32(tbase + c * 64 + h * 32, r);
-              tc::tmem_wait_ld();
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(g + lane * 128 + (((h * 4 + j) ^ (lane & 7)) << 4)) =
-                  Vec<bf16>::pack(v + j * 8);
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::tma_store_3d(d.p ? &tmO1 : &tmO0, buf, n, m, d.e);
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
         }
+        if (m < M) store_row(row + n, v, min(32, N - n), sectors);
       }
       tc::tc_fence_before();
       if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
@@ -732,16 +715,12 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
-    if (lane == 0) tc::bulk_wait_all();
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (producer && s_abort)
-    for (int s = 0; s < kStages; ++s) {
-      if ((fixed >> s) & 1u) tc::mbar_wait(bar.fix(s), (fix_par >> s) & 1u, nullptr, kWaitNs);
-      if (rank == 0 && ((filled & ~last_fix) >> s) & 1u)
-        tc::mbar_wait(bar.full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
-    }
+  if (producer && rank == 0 && s_abort)
+    for (int s = 0; s < kStages; ++s)
+      if ((filled >> s) & 1u) tc::mbar_wait(bar.full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
   tc::cluster_sync();
   if (warp == 1) {
     tc::tc_fence_after();
@@ -777,10 +756,15 @@ bias_reduce_kernel(const float* __restrict__ part, const int32_t* __restrict__ o
 
 // One persistent launch of CTA pairs, never more than fit at once.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pairs(void (*kern)(KArgs...), int threads, size_t smem, cudaStream_t st, Args... args) {
+cudaError_t launch_pairs(void (*kern)(KArgs...), size_t smem, cudaStream_t st, Args... args) {
   cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (r != cudaSuccess) return r;
-  return launch_kernel(kern, dim3((unsigned)(sm_count() / 2 * 2)), dim3(threads), smem, st, 2, args...);
+  return launch_kernel(kern, dim3((unsigned)(sm_count() / 2 * 2)), dim3(kThreads), smem, st, 2, args...);
+}
+
+// Whether every row of [.., cols] elements of `size` bytes starts on a 32-byte sector.
+bool starts_on_sectors(const void* p, int cols, int size) {
+  return ((uintptr_t)p % 32 == 0) && ((int64_t)cols * size % 32 == 0);
 }
 
 template <int kKind>
@@ -794,15 +778,18 @@ cudaError_t run_rows(const void* tokens, int64_t rows, int K, const void* W, int
   if (kMN ? !tma_map_bf16_3d(&mw, W, (uint64_t)E, (uint64_t)K, (uint64_t)N, kBK)
           : !tma_map_bf16(&mw, W, (uint64_t)E * N * (kKind == kDaSwiglu ? 2 : 1), (uint64_t)K, kBM))
     return cudaErrorNotSupported;
-  return launch_pairs(backward_rows_kernel<kKind>, kRowsThreads, kSmem, st, mx, mxs, mw, offs, E, N, K, out, err);
+  return launch_pairs(backward_rows_kernel<kKind>, smem_bytes(kRowsStages), st, mx, mxs, mw, offs, E, N, K, out, err);
 }
 
 }  // namespace
 
 int64_t backward_blocks(int64_t rows, int E) { return rows / kTile + E + 1; }
+size_t backward_tail_bytes(int E, int H, int N, int F) {
+  return (size_t)E * kTailRows * ((size_t)N + 2 * (size_t)H + (size_t)F) * sizeof(bf16);
+}
 
 cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBackward& b, void* da, float* dh,
-                                   float* part, int* err, cudaStream_t st) {
+                                   float* part, void* tails, int* err, cudaStream_t st) {
   const bool swi = (s.flags & MOE_FLAG_SWIGLU) != 0;
   const int G = swi ? 2 : 1, N = G * s.F;
   const int64_t lim = (int64_t)1 << 31;
@@ -816,39 +803,49 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
     if (e == cudaSuccess && b.db2) e = cudaMemsetAsync(b.db2, 0, (size_t)s.E * s.H * 4, st);
     return e;
   }
-  const RowsOut out{dh, (bf16*)da, (bf16*)b.dx_perm, b.b1, b.db1 ? part : nullptr};
+  RowsOut out{dh, (bf16*)da, (bf16*)b.dx_perm, b.b1, b.db1 ? part : nullptr, false};
   if (b.dx_perm || b.dW1 || b.db1) {
+    out.sectors = starts_on_sectors(dh, s.F, 4);
     e = run_rows<kDh>(b.dy_perm, max_rows, s.H, b.W2, s.E, s.F, b.offs, out, err, st);
+    out.sectors = starts_on_sectors(da, s.F, 2);
     if (e == cudaSuccess)
       e = swi ? run_rows<kDaSwiglu>(b.x_perm, max_rows, s.H, b.W1, s.E, s.F, b.offs, out, err, st)
               : run_rows<kDaGelu>(b.x_perm, max_rows, s.H, b.W1, s.E, s.F, b.offs, out, err, st);
     if (e == cudaSuccess && b.db1)
       e = launch_kernel(bias_reduce_kernel, dim3((unsigned)((N + kRedCols - 1) / kRedCols), (unsigned)s.E),
-                        dim3(kRedCols * kRedGroups), 0, st, 1,
-                        (const float*)part, b.offs, N, swi ? 0 : 1, b.db1);
+                        dim3(kRedCols * kRedGroups), 0, st, 1, (const float*)part, b.offs, N, swi ? 0 : 1, b.db1);
+    out.sectors = starts_on_sectors(b.dx_perm, s.H, 2);
     if (e == cudaSuccess && b.dx_perm)
       e = run_rows<kDx>(da, max_rows, N, b.W1, s.E, s.H, b.offs, out, err, st);
   }
   if (e == cudaSuccess && (b.dW1 || b.dW2)) {
-    CUtensorMap m[6];
-    WeightProduct P[2];
+    CUtensorMap m[8];
+    WeightProduct P[2] = {{0, 0, nullptr, false}, {0, 0, nullptr, false}};
+    Operands ops = {};
     int n = 0;
+    bf16* at = (bf16*)tails;
+    auto add_operand = [&](int i, const void* rows, int cols) {   // operand i of product n
+      bf16* t = at;
+      at += (int64_t)s.E * kTailRows * cols;
+      ops.o[2 * n + i] = {(const uint4*)rows, (uint4*)t, cols / 8};
+      return tma_map_bf16(&m[4 * n + i], rows, (uint64_t)max_rows, (uint64_t)cols, kBK) &&
+             tma_map_bf16(&m[4 * n + 2 + i], t, (uint64_t)s.E * kTailRows, (uint64_t)cols, kTailRows);
+    };
     auto add = [&](const void* A, int M, const void* Bm, int Nn, void* dW) {
-      P[n] = {M, Nn};
-      const bool ok = tma_map_bf16(&m[3 * n], A, (uint64_t)max_rows, (uint64_t)M, kBK) &&
-                      tma_map_bf16(&m[3 * n + 1], Bm, (uint64_t)max_rows, (uint64_t)Nn, kBK) &&
-                      tma_map_bf16_3d(&m[3 * n + 2], dW, (uint64_t)s.E, (uint64_t)M, (uint64_t)Nn, 32);
+      P[n] = {M, Nn, (bf16*)dW, starts_on_sectors(dW, Nn, 2)};
+      const bool ok = add_operand(0, A, M) && add_operand(1, Bm, Nn);
       ++n;
       return ok;
     };
     if (b.dW1 && !add(da, N, b.x_perm, s.H, b.dW1)) return cudaErrorNotSupported;
     if (b.dW2 && !add(b.dy_perm, s.H, b.h_perm, s.F, b.dW2)) return cudaErrorNotSupported;
-    if (n == 1) {
-      for (int i = 0; i < 3; ++i) m[3 + i] = m[i];
-      P[1] = {0, 0};
-    }
-    e = launch_pairs(backward_weights_kernel, kWeightsThreads, kSmemW, st, m[0], m[1], m[2], m[3], m[4], m[5], b.offs, s.E, P[0],
-                     P[1], err);
+    e = launch_kernel(expert_tails_kernel, dim3((unsigned)s.E, (unsigned)(2 * n), kTailSplit), dim3(256), 0, st, 1, ops,
+                      b.offs);
+    if (n == 1)
+      for (int i = 0; i < 4; ++i) m[4 + i] = m[i];
+    if (e == cudaSuccess)
+      e = launch_pairs(backward_weights_kernel, smem_bytes(kWeightsStages), st, m[0], m[1], m[2], m[3], m[4], m[5],
+                       m[6], m[7], b.offs, s.E, P[0], P[1], err);
   }
   if (e == cudaSuccess && b.db2) e = launch_row_sums(MOE_BF16, b.dy_perm, b.offs, s.E, s.H, b.db2, st);
   return e;

@@ -219,10 +219,12 @@ struct FfnBackward {
 cudaError_t launch_ffn_backward_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, float* da,
                                      cudaStream_t st);
 // bf16 on SM pairs.  da: [max_rows, F or 2F] bf16, dh: [max_rows, F] fp32,
-// part: [8 * backward_blocks(max_rows, E), F or 2F] fp32 scratch.
+// part: [8 * backward_blocks(max_rows, E), F or 2F] fp32, tails:
+// backward_tail_bytes (N = F or 2F), 128-byte aligned: scratch.
 int64_t backward_blocks(int64_t rows, int E);
+size_t backward_tail_bytes(int E, int H, int N, int F);
 cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBackward& b, void* da, float* dh,
-                                   float* part, int* err, cudaStream_t st);
+                                   float* part, void* tails, int* err, cudaStream_t st);
 // out[e, :] = the sum of A's [rows, N] rows of expert e, in fp32
 cudaError_t launch_row_sums(int dtype, const void* A, const int32_t* offs, int E, int N, float* out,
                             cudaStream_t st);

@@ -253,6 +253,8 @@ FFN = [
     ([15, 16, 17, 63, 64, 65], 128, 192), ([127, 128, 129, 0, 255, 256, 257], 256, 136),
     # sizes that are no multiple of a tile, rows of several tiles
     ([300, 7, 513], 520, 264), ([33, 48, 49], 1000, 328), ([31, 96, 160], 72, 648),
+    # more tiles than SM pairs: every pair works through several, of experts of all lengths
+    ([20, 300, 0, 64, 5, 257] * 7, 520, 528),
 ]
 
 
