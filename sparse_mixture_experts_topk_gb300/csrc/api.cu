@@ -814,7 +814,7 @@ BackwardLayout backward_layout(const moe_desc& d) {
   const size_t N = (size_t)d.F * ((d.flags & MOE_FLAG_SWIGLU) ? 2 : 1);
   L.err = take(256);
   L.da = take((size_t)L.rows * N * (tc ? 2 : 4));
-  L.dh = take(tc ? (size_t)L.rows * d.F * 4 : 0);
+  L.dh = take(tc ? backward_dh_floats(L.rows, d.E, d.F) * 4 : 0);
   L.part = take(tc ? (size_t)backward_blocks(L.rows, d.E) * 8 * N * 4 : 0);
   L.tails = take(tc ? backward_tail_bytes(d.E, d.H, (int)N, d.F) : 0);
   L.total = off;

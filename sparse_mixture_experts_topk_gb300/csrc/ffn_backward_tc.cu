@@ -11,7 +11,9 @@
 // along the rows of its matrix ("MN-major") is staged as it lies, and the MMA
 // descriptors say so.
 //
-// dh goes through fp32 scratch between its product and the one that uses it.
+// dh goes through fp32 scratch between its product and the one that uses it,
+// tile by tile in the order in which the epilogue's threads hold it, so that
+// every access of a warp is 512 bytes in a row.
 // Computing both products of a da tile together would spare that traffic
 // (4 bytes a value, written and read once), but two accumulators of 256
 // columns fill TMEM, so the epilogue could not overlap the next tile, and two
@@ -132,13 +134,19 @@ __device__ __forceinline__ void advance(int& stage, uint32_t& phase) {
 
 // What the rows kernel's epilogue reads and writes.
 struct RowsOut {
-  float* dh;            // [rows, F] fp32: written by kDh, read by kDa*
+  float* dh;            // kTile x kTile fp32 for each dh tile (see dh_at): written by kDh, read by kDa*
   bf16* da;             // [rows, G F]
   bf16* dx;             // [rows, H]
   const float* bias;    // b1 or null
   float* part;          // [blocks * 8, G F] partial sums of da over rows, or null
   bool sectors;         // what this product writes has rows that start on 32 bytes
 };
+
+// Where a dh tile holds row r, column f: 32 x 32 blocks, in each of them the
+// 32 rows' first four columns, then the next four, ...
+__device__ __forceinline__ int dh_at(int r, int f) {
+  return ((r >> 5) * (kTile / 32) + (f >> 5)) * 1024 + ((f & 31) >> 2) * 128 + (r & 31) * 4 + (f & 3);
+}
 
 // Sum over the warp's lanes of 32 values each: lane l returns the sum of v[l].
 __device__ __forceinline__ float column_sum(float* v, int lane) {
@@ -173,11 +181,12 @@ __device__ __forceinline__ void store_row(T* dst, const float* v, int n, bool se
 
 // One tile of the rows kernel, this warp's half of it.  Row orientation: this
 // thread's row, 32 columns at a time, the tile's left or right half.  Swapped:
-// this thread's column, every other group of 32 rows.
+// this thread's column, every other group of 32 rows.  dh: the dh tile of
+// these rows, f0 this tile's first column in it.
 template <int kKind>
 __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, int row_base, int nrows, int n0,
-                                              int block, int rank, int q, int half, int lane, int N,
-                                              const RowsOut& o) {
+                                              int block, float* dh, int f0, int rank, int q, int half, int lane,
+                                              int N, const RowsOut& o) {
   constexpr bool kSwi = kKind == kDaSwiglu, kDa = kKind == kDaGelu || kSwi;
   constexpr int kOut = kSwi ? kBM : kTile;
   const int wide = kSwi ? 2 * N : N;     // columns of da and of the bias
@@ -191,10 +200,11 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
     for (int c = half; c * 32 < nrows; c += 2) {
       const int64_t at = (int64_t)(row_base + c * 32) * N + f;
       const int left = ok ? nrows - c * 32 : 0;
-      float dh[kDa ? 32 : 1];
+      float* dt = dh + dh_at(c * 32, f0 + rank * kBM + q * 32 + lane);   // row c * 32 + j at + 4 j
+      float g[kDa ? 32 : 1];
       if (kDa) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) dh[j % (kDa ? 32 : 1)] = j < left ? __ldcs(o.dh + at + (int64_t)j * N) : 0.f;
+        for (int j = 0; j < 32; ++j) g[j % (kDa ? 32 : 1)] = j < left ? __ldcs(dt + 4 * j) : 0.f;
       }
       uint32_t r[32];
       tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
@@ -204,11 +214,11 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
         if (j < left) {
           const float v = __uint_as_float(r[j]);
           if (kKind == kDh) {
-            o.dh[at + (int64_t)j * N] = v;
+            dt[4 * j] = v;
           } else if (kKind == kDx) {
             o.dx[at + (int64_t)j * N] = __float2bfloat16_rn(v);
           } else {
-            const float d = dh[j % (kDa ? 32 : 1)] * gelu_slope(v + bf);
+            const float d = g[j % (kDa ? 32 : 1)] * gelu_slope(v + bf);
             sum += d;
             o.da[at + (int64_t)j * N] = __float2bfloat16_rn(d);
           }
@@ -226,13 +236,13 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
     const int col = n0 + c * 32;
     if (col >= N) break;
     const int left = min(32, N - col);     // a multiple of 8
+    float4* dt = reinterpret_cast<float4*>(dh + dh_at(r0 + lane, f0 + c * 32));   // columns 4 g .. 4 g + 3 at + 32 g
     float4 d[kDa ? 8 : 1];
     if (kDa) {
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         d[g % (kDa ? 8 : 1)] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ok && g * 4 < left)
-          d[g % (kDa ? 8 : 1)] = __ldcs(reinterpret_cast<const float4*>(o.dh + row * N + col + g * 4));
+        if (ok && g * 4 < left) d[g % (kDa ? 8 : 1)] = __ldcs(dt + 32 * g);
       }
     }
     uint32_t r[32], u[kSwi ? 32 : 1];
@@ -243,9 +253,12 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
     if (!kDa) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-      if (ok) {
-        if (kKind == kDh) store_row(o.dh + row * N + col, v, left, o.sectors);
-        else store_row(o.dx + row * N + col, v, left, o.sectors);
+      if (kKind == kDh) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+          if (ok && g * 4 < left) dt[32 * g] = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+      } else if (ok) {
+        store_row(o.dx + row * N + col, v, left, o.sectors);
       }
     } else {
       float w[kSwi ? 32 : 1];
@@ -369,9 +382,10 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   const int total = s_tstart[E], first = blockIdx.x / 2, step = gridDim.x / 2;
 
   struct Tile {
-    int e, row_base, nrows, mma_n, n0, block;
+    int e, row_base, nrows, mma_n, n0, block, dh_tile;
     bool swap;
   };
+  const int dh_nt = (N + kTile - 1) / kTile;   // kDh, kDa*: N = F
   auto decode = [&](int t) {
     Tile d;
     d.e = expert_of(s_tstart, E, t);
@@ -383,6 +397,7 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
     d.mma_n = d.swap ? (d.nrows + 15) / 16 * 16 : kTile;
     d.n0 = (local / mt) * kOut;
     d.block = (s_offs[d.e] >> 8) + d.e + rb;
+    d.dh_tile = s_tstart[d.e] / nt * dh_nt + d.n0 / kTile * mt + rb;
     return d;
   };
 
@@ -475,7 +490,8 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
       }
       tc::tc_fence_after();
       rows_epilogue<kKind>(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile), d.swap, d.e, d.row_base,
-                           d.nrows, d.n0, d.block, rank, q, half, lane, N, out);
+                           d.nrows, d.n0, d.block, out.dh + (int64_t)d.dh_tile * kTile * kTile, d.n0 % kTile, rank, q, half,
+                           lane, N, out);
       tc::tc_fence_before();
       if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
       else tc::mbar_arrive_remote(tc::map_peer(bar.tempty(acc), 0));
@@ -784,6 +800,10 @@ cudaError_t run_rows(const void* tokens, int64_t rows, int K, const void* W, int
 }  // namespace
 
 int64_t backward_blocks(int64_t rows, int E) { return rows / kTile + E + 1; }
+size_t backward_dh_floats(int64_t rows, int E, int F) {
+  const int64_t blocks = rows / kTile + (rows < E ? rows : E);   // at most: one partial block for each expert with rows
+  return (size_t)blocks * ((F + kTile - 1) / kTile) * kTile * kTile;
+}
 size_t backward_tail_bytes(int E, int H, int N, int F) {
   return (size_t)E * kTailRows * ((size_t)N + 2 * (size_t)H + (size_t)F) * sizeof(bf16);
 }
@@ -805,7 +825,6 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
   }
   RowsOut out{dh, (bf16*)da, (bf16*)b.dx_perm, b.b1, b.db1 ? part : nullptr, false};
   if (b.dx_perm || b.dW1 || b.db1) {
-    out.sectors = starts_on_sectors(dh, s.F, 4);
     e = run_rows<kDh>(b.dy_perm, max_rows, s.H, b.W2, s.E, s.F, b.offs, out, err, st);
     out.sectors = starts_on_sectors(da, s.F, 2);
     if (e == cudaSuccess)

@@ -218,9 +218,10 @@ struct FfnBackward {
 // da: [max_rows, F or 2F] fp32 scratch
 cudaError_t launch_ffn_backward_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, float* da,
                                      cudaStream_t st);
-// bf16 on SM pairs.  da: [max_rows, F or 2F] bf16, dh: [max_rows, F] fp32,
+// bf16 on SM pairs.  da: [max_rows, F or 2F] bf16, dh: backward_dh_floats,
 // part: [8 * backward_blocks(max_rows, E), F or 2F] fp32, tails:
 // backward_tail_bytes (N = F or 2F), 128-byte aligned: scratch.
+size_t backward_dh_floats(int64_t rows, int E, int F);
 int64_t backward_blocks(int64_t rows, int E);
 size_t backward_tail_bytes(int E, int H, int N, int F);
 cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBackward& b, void* da, float* dh,
