@@ -139,10 +139,28 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """The current device's current stream as an address.  The stream object
+    that torch's public call makes costs more than a small kernel's launch, so
+    its raw getter is used where this torch has it."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if get is not None and device is not None:
+            _raw_stream = lambda: get(device())
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+    return _raw_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

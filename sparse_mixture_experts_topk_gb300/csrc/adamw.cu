@@ -22,7 +22,6 @@
 // bf16 copy of p) or 16 bytes and 16 / 256 of scales.
 #include <cuda_fp8.h>
 #include <math.h>
-#include <string.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -63,8 +62,10 @@ struct Step {
   float beta1, one_minus_beta1, beta2, one_minus_beta2, inv_sqrt_c2, eps, lr_c1;
 };
 
-// The largest launch: its kernel parameters have to stay below 32764 bytes.
-constexpr int kSmallCap = 40, kLargeCap = 400;
+// Tensors a launch can take.  Its parameters travel with it, so that few
+// tensors take a short list (40: 3 KB, 128: 9 KB, 400: 29 KB; a launch costs
+// about 3 us more with the longest); they have to stay below 32764 bytes.
+constexpr int kSmallCap = 40, kMiddleCap = 128, kLargeCap = 400;
 static_assert(sizeof(Slots<kLargeCap>) + sizeof(Step) + 32 < 32764, "kernel parameters");
 
 __device__ __forceinline__ float warp_max_bits(uint32_t v) {
@@ -294,7 +295,7 @@ cudaError_t run_adamw(const moe_adamw_tensor* tensors, int count, const Step& q,
   int i = 0;
   while (i < count) {
     Slots<kCap> t;
-    memset(&t, 0, sizeof(t));
+    t.count = 0;
     uint64_t blocks = 0;
     for (; i < count && t.count < kCap; ++i) {
       const moe_adamw_tensor& x = tensors[i];
@@ -317,8 +318,17 @@ cudaError_t run_adamw(const moe_adamw_tensor* tensors, int count, const Step& q,
     if (t.count == 0) break;
     t.blocks = (uint32_t)blocks;
     const uint64_t need = (blocks + kWarps - 1) / kWarps, cap = (uint64_t)sm_count() * 8;
-    const cudaError_t e = launch_kernel(adamw_kernel<kCap, TG, kEight>, dim3((unsigned)(need < cap ? need : cap)),
-                                        dim3(32 * kWarps), 0, st, 1, t, q, grad_scale, skip);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(need < cap ? need : cap));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    void* args[] = {&t, const_cast<Step*>(&q), &grad_scale, &skip};   // the list is copied once, by the launch
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, (const void*)adamw_kernel<kCap, TG, kEight>, args);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -346,10 +356,9 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int count, int grad_dt
   q.inv_sqrt_c2 = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)h.step)));
   q.eps = (float)h.eps;
   q.lr_c1 = (float)(h.lr / (1.0 - pow(h.beta1, (double)h.step)));
-  // few tensors take the launch whose parameters are short
-  return count <= kSmallCap
-             ? pick_adamw<kSmallCap>(tensors, count, grad_dtype, state_bits, q, h.lr, grad_scale, skip, st)
-             : pick_adamw<kLargeCap>(tensors, count, grad_dtype, state_bits, q, h.lr, grad_scale, skip, st);
+  auto pick = count <= kSmallCap ? pick_adamw<kSmallCap>
+                                 : count <= kMiddleCap ? pick_adamw<kMiddleCap> : pick_adamw<kLargeCap>;
+  return pick(tensors, count, grad_dtype, state_bits, q, h.lr, grad_scale, skip, st);
 }
 
 }  // namespace moe

@@ -511,30 +511,103 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   }
 }
 
-// The rows of each expert past its last whole group of 16, padded with zeros
-// to 16: tails [E, 16, cols] for each of up to four operands.
+// What is left of the smaller work, in one launch beside one another.
+//
+// Tails: the rows of each expert past its last whole group of 16, padded with
+// zeros to 16, [E, 16, cols] for each of up to four operands.
 struct Operand {
   const uint4* rows;
   uint4* tails;
   int vec;              // 16-byte vectors in a row
 };
-struct Operands {
+constexpr int kTailRows = 16, kTailSplit = 4;   // blocks for an expert's tail of one operand
+constexpr int kRedCols = 32, kRedGroups = 8, kSumVecs = 8, kSumGroups = 32;
+struct Extras {
   Operand o[4];
+  int tails;            // blocks of tails
+  const float* part;    // db1's partial sums, n columns
+  float* db1;
+  int n, swaps, cols1;  // columns of blocks
+  int db1_blocks;
+  const uint4* dy;      // db2 = the sum of an expert's dy rows, h columns
+  float* db2;
+  int h, cols2;
 };
-constexpr int kTailRows = 16, kTailSplit = 4;
-__global__ void __launch_bounds__(256)
-expert_tails_kernel(const __grid_constant__ Operands ops, const int32_t* __restrict__ offs) {
-  pdl_enter();
-  const int e = blockIdx.x;
-  const Operand& o = ops.o[blockIdx.y];
+
+// One expert's rows past its last whole group of 16, a quarter of them.
+__device__ __forceinline__ void copy_tail(const Operand& o, const int32_t* __restrict__ offs, int e, int part) {
   const int r0 = offs[e], rows = offs[e + 1] - r0, whole = rows / kTailRows * kTailRows;
   if (rows == whole) return;   // no tail: never read
   const int per = kTailRows / kTailSplit * o.vec;
   for (int i = threadIdx.x; i < per; i += blockDim.x) {
-    const int r = blockIdx.z * (kTailRows / kTailSplit) + i / o.vec, v = i % o.vec;
+    const int r = part * (kTailRows / kTailSplit) + i / o.vec, v = i % o.vec;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (whole + r < rows) x = o.rows[(int64_t)(r0 + whole + r) * o.vec + v];
     o.tails[((int64_t)e * kTailRows + r) * o.vec + v] = x;
+  }
+}
+
+// db1[e, c]: the row blocks' partial sums, added in a fixed order.  A swapped
+// block has two partials, another eight; 8 threads of a column take them in turn.
+__device__ __forceinline__ void reduce_bias(const Extras& x, const int32_t* __restrict__ offs, int e, int col,
+                                            float* s) {
+  const int g = threadIdx.x / kRedCols, c = col * kRedCols + threadIdx.x % kRedCols;
+  const int r0 = offs[e], rows = offs[e + 1] - r0, mt = row_blocks(rows);
+  const int last = mt > 0 ? rows - (mt - 1) * kTile : 0;
+  const int parts = 8 * mt - (x.swaps && mt > 0 && last <= kSwapRows ? 6 : 0);
+  const float* p = x.part + ((int64_t)(r0 >> 8) + e) * 8 * x.n + c;
+  float sum = 0.f;
+  if (c < x.n) {
+#pragma unroll 4
+    for (int i = g; i < parts; i += kRedGroups) sum += p[(int64_t)i * x.n];
+  }
+  s[threadIdx.x] = sum;
+  __syncthreads();
+  if (g == 0 && c < x.n) {
+    for (int i = 1; i < kRedGroups; ++i) sum += s[i * kRedCols + threadIdx.x];
+    x.db1[(int64_t)e * x.n + c] = sum;
+  }
+}
+
+// db2[e, 64 columns]: 32 threads of a 16-byte vector take the rows in turn,
+// their sums are added in order.
+__device__ __forceinline__ void sum_rows(const Extras& x, const int32_t* __restrict__ offs, int e, int col, float* s) {
+  const int g = threadIdx.x / kSumVecs, v = col * kSumVecs + threadIdx.x % kSumVecs, vec = x.h / 8;
+  const int r1 = offs[e + 1];
+  float sum[8] = {};
+  if (v < vec) {
+#pragma unroll 4
+    for (int r = offs[e] + g; r < r1; r += kSumGroups) {
+      float f[8];
+      Vec<bf16>::unpack(__ldg(x.dy + (int64_t)r * vec + v), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += f[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[(g * kSumVecs + threadIdx.x % kSumVecs) * 8 + i] = sum[i];
+  __syncthreads();
+  const int c = threadIdx.x;   // one column of the block's 64
+  if (c < kSumVecs * 8 && col * kSumVecs * 8 + c < x.h) {
+    float total = 0.f;
+    for (int i = 0; i < kSumGroups; ++i) total += s[i * kSumVecs * 8 + c];
+    x.db2[(int64_t)e * x.h + col * kSumVecs * 8 + c] = total;
+  }
+}
+
+__global__ void __launch_bounds__(256)
+backward_extras_kernel(const __grid_constant__ Extras x, const int32_t* __restrict__ offs, int E) {
+  __shared__ float s[256 * 8];
+  pdl_enter();
+  int i = blockIdx.x;
+  if (i < x.tails) {
+    const int e = i % E, k = i / E;
+    copy_tail(x.o[k / kTailSplit], offs, e, k % kTailSplit);
+  } else if ((i -= x.tails) < x.db1_blocks) {
+    reduce_bias(x, offs, i / x.cols1, i % x.cols1, s);
+  } else {
+    i -= x.db1_blocks;
+    sum_rows(x, offs, i / x.cols2, i % x.cols2, s);
   }
 }
 
@@ -744,32 +817,6 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   }
 }
 
-// db1[e, c]: the row blocks' partial sums, added in a fixed order.  A swapped
-// block has two partials, another eight; 8 threads of a column take them in turn.
-constexpr int kRedCols = 32, kRedGroups = 8;
-__global__ void __launch_bounds__(kRedCols * kRedGroups)
-bias_reduce_kernel(const float* __restrict__ part, const int32_t* __restrict__ offs, int n, int swaps,
-                   float* __restrict__ db) {
-  __shared__ float s[kRedGroups][kRedCols];
-  pdl_enter();
-  const int e = blockIdx.y, g = threadIdx.x / kRedCols, c = blockIdx.x * kRedCols + threadIdx.x % kRedCols;
-  const int r0 = offs[e], rows = offs[e + 1] - r0, mt = row_blocks(rows);
-  const int last = mt > 0 ? rows - (mt - 1) * kTile : 0;
-  const int parts = 8 * mt - (swaps && mt > 0 && last <= kSwapRows ? 6 : 0);
-  const float* p = part + ((int64_t)(r0 >> 8) + e) * 8 * n + c;
-  float sum = 0.f;
-  if (c < n) {
-#pragma unroll 4
-    for (int i = g; i < parts; i += kRedGroups) sum += p[(int64_t)i * n];
-  }
-  s[g][threadIdx.x % kRedCols] = sum;
-  __syncthreads();
-  if (g == 0 && c < n) {
-    for (int i = 1; i < kRedGroups; ++i) sum += s[i][threadIdx.x];
-    db[(int64_t)e * n + c] = sum;
-  }
-}
-
 // One persistent launch of CTA pairs, never more than fit at once.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pairs(void (*kern)(KArgs...), size_t smem, cudaStream_t st, Args... args) {
@@ -823,50 +870,55 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
     if (e == cudaSuccess && b.db2) e = cudaMemsetAsync(b.db2, 0, (size_t)s.E * s.H * 4, st);
     return e;
   }
-  RowsOut out{dh, (bf16*)da, (bf16*)b.dx_perm, b.b1, b.db1 ? part : nullptr, false};
+  CUtensorMap m[8];
+  WeightProduct P[2] = {{0, 0, nullptr, false}, {0, 0, nullptr, false}};
+  Extras x = {};
+  int n = 0;   // weight products
+  bf16* at = (bf16*)tails;
+  auto add_operand = [&](int i, const void* rows, int cols) {   // operand i of product n
+    bf16* t = at;
+    at += (int64_t)s.E * kTailRows * cols;
+    x.o[2 * n + i] = {(const uint4*)rows, (uint4*)t, cols / 8};
+    return tma_map_bf16(&m[4 * n + i], rows, (uint64_t)max_rows, (uint64_t)cols, kBK) &&
+           tma_map_bf16(&m[4 * n + 2 + i], t, (uint64_t)s.E * kTailRows, (uint64_t)cols, kTailRows);
+  };
+  auto add = [&](const void* A, int M, const void* Bm, int Nn, void* dW) {
+    P[n] = {M, Nn, (bf16*)dW, starts_on_sectors(dW, Nn, 2)};
+    const bool ok = add_operand(0, A, M) && add_operand(1, Bm, Nn);
+    ++n;
+    return ok;
+  };
+  if (b.dW1 && !add(da, N, b.x_perm, s.H, b.dW1)) return cudaErrorNotSupported;
+  if (b.dW2 && !add(b.dy_perm, s.H, b.h_perm, s.F, b.dW2)) return cudaErrorNotSupported;
+  x.tails = 2 * n * kTailSplit * s.E;
+  RowsOut out{dh, (bf16*)da, (bf16*)b.dx_perm, b.b1, b.db1 ? part : nullptr, starts_on_sectors(da, s.F, 2)};
   if (b.dx_perm || b.dW1 || b.db1) {
     e = run_rows<kDh>(b.dy_perm, max_rows, s.H, b.W2, s.E, s.F, b.offs, out, err, st);
-    out.sectors = starts_on_sectors(da, s.F, 2);
     if (e == cudaSuccess)
       e = swi ? run_rows<kDaSwiglu>(b.x_perm, max_rows, s.H, b.W1, s.E, s.F, b.offs, out, err, st)
               : run_rows<kDaGelu>(b.x_perm, max_rows, s.H, b.W1, s.E, s.F, b.offs, out, err, st);
-    if (e == cudaSuccess && b.db1)
-      e = launch_kernel(bias_reduce_kernel, dim3((unsigned)((N + kRedCols - 1) / kRedCols), (unsigned)s.E),
-                        dim3(kRedCols * kRedGroups), 0, st, 1, (const float*)part, b.offs, N, swi ? 0 : 1, b.db1);
-    out.sectors = starts_on_sectors(b.dx_perm, s.H, 2);
-    if (e == cudaSuccess && b.dx_perm)
-      e = run_rows<kDx>(da, max_rows, N, b.W1, s.E, s.H, b.offs, out, err, st);
+    x.part = part;
+    x.db1 = b.db1;
+    x.n = N;
+    x.swaps = swi ? 0 : 1;
+    x.cols1 = (N + kRedCols - 1) / kRedCols;
+    x.db1_blocks = b.db1 ? x.cols1 * s.E : 0;
   }
-  if (e == cudaSuccess && (b.dW1 || b.dW2)) {
-    CUtensorMap m[8];
-    WeightProduct P[2] = {{0, 0, nullptr, false}, {0, 0, nullptr, false}};
-    Operands ops = {};
-    int n = 0;
-    bf16* at = (bf16*)tails;
-    auto add_operand = [&](int i, const void* rows, int cols) {   // operand i of product n
-      bf16* t = at;
-      at += (int64_t)s.E * kTailRows * cols;
-      ops.o[2 * n + i] = {(const uint4*)rows, (uint4*)t, cols / 8};
-      return tma_map_bf16(&m[4 * n + i], rows, (uint64_t)max_rows, (uint64_t)cols, kBK) &&
-             tma_map_bf16(&m[4 * n + 2 + i], t, (uint64_t)s.E * kTailRows, (uint64_t)cols, kTailRows);
-    };
-    auto add = [&](const void* A, int M, const void* Bm, int Nn, void* dW) {
-      P[n] = {M, Nn, (bf16*)dW, starts_on_sectors(dW, Nn, 2)};
-      const bool ok = add_operand(0, A, M) && add_operand(1, Bm, Nn);
-      ++n;
-      return ok;
-    };
-    if (b.dW1 && !add(da, N, b.x_perm, s.H, b.dW1)) return cudaErrorNotSupported;
-    if (b.dW2 && !add(b.dy_perm, s.H, b.h_perm, s.F, b.dW2)) return cudaErrorNotSupported;
-    e = launch_kernel(expert_tails_kernel, dim3((unsigned)s.E, (unsigned)(2 * n), kTailSplit), dim3(256), 0, st, 1, ops,
-                      b.offs);
-    if (n == 1)
-      for (int i = 0; i < 4; ++i) m[4 + i] = m[i];
-    if (e == cudaSuccess)
-      e = launch_pairs(backward_weights_kernel, smem_bytes(kWeightsStages), st, m[0], m[1], m[2], m[3], m[4], m[5],
-                       m[6], m[7], b.offs, s.E, P[0], P[1], err);
-  }
-  if (e == cudaSuccess && b.db2) e = launch_row_sums(MOE_BF16, b.dy_perm, b.offs, s.E, s.H, b.db2, st);
+  x.dy = (const uint4*)b.dy_perm;
+  x.db2 = b.db2;
+  x.h = s.H;
+  x.cols2 = (s.H / 8 + kSumVecs - 1) / kSumVecs;
+  const int64_t extras = (int64_t)x.tails + x.db1_blocks + (b.db2 ? (int64_t)x.cols2 * s.E : 0);
+  if (e == cudaSuccess && extras > 0)
+    e = launch_kernel(backward_extras_kernel, dim3((unsigned)extras), dim3(256), 0, st, 1, x, b.offs, s.E);
+  out.sectors = starts_on_sectors(b.dx_perm, s.H, 2);
+  if (e == cudaSuccess && b.dx_perm)
+    e = run_rows<kDx>(da, max_rows, N, b.W1, s.E, s.H, b.offs, out, err, st);
+  if (n == 1)
+    for (int i = 0; i < 4; ++i) m[4 + i] = m[i];
+  if (e == cudaSuccess && n > 0)
+    e = launch_pairs(backward_weights_kernel, smem_bytes(kWeightsStages), st, m[0], m[1], m[2], m[3], m[4], m[5], m[6],
+                     m[7], b.offs, s.E, P[0], P[1], err);
   return e;
 }
 

@@ -226,9 +226,6 @@ int64_t backward_blocks(int64_t rows, int E);
 size_t backward_tail_bytes(int E, int H, int N, int F);
 cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBackward& b, void* da, float* dh,
                                    float* part, void* tails, int* err, cudaStream_t st);
-// out[e, :] = the sum of A's [rows, N] rows of expert e, in fp32
-cudaError_t launch_row_sums(int dtype, const void* A, const int32_t* offs, int E, int N, float* out,
-                            cudaStream_t st);
 cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int count, int grad_dtype, int state_bits,
                          const moe_adamw_params& h, const float* grad_scale, const int32_t* skip, cudaStream_t st);
 
