@@ -15,12 +15,15 @@
 // Two launches: the tiles of da, then those of dx, dW1 and dW2 side by side
 // (they need da and nothing of each other).  The bias gradients are the
 // column sums of the weight gradients' left operand, added up by the blocks
-// of the first column of tiles.  A block computes a kB x kB tile, the next 32
-// reduction elements on their way to registers while it multiplies the last
-// 32 in shared memory.  These layers are small (the fp32 ones are for
-// checking): 32 x 32 tiles spread them over more SMs, and are used while
-// 64 x 64 ones would not fill two rounds of blocks.  Measured on a layer of
-// 64 tokens (H = 256, E = 8, F = 512): 12 us with tiles of 32, 21 with 64.
+// of the first column of tiles.  While a block multiplies 32 reduction
+// elements in shared memory, the next 32 are on their way to registers.
+//
+// A row product's tile has 64 columns and 64 or 16 rows; a thread always
+// holds 4 x 4 values (two 16-byte reads of shared memory for 16
+// multiply-adds), so that with 16 rows four groups of 64 threads take a
+// quarter of the reduction each, added up at the end.  These layers are small
+// (the fp32 ones are for checking) and their experts have few rows: 16 is
+// used while the experts have less than 32 rows on average.
 #include "common.cuh"
 #include "ffn_backward.cuh"
 #include "internal.h"
@@ -29,16 +32,16 @@ namespace moe {
 
 namespace {
 
-constexpr int kBK = 32, kThreads = 256;
+constexpr int kN = 64, kBK = 32, kThreads = 256;
 
-// Row tile `tile` of kB rows: its expert, first row and the expert's end;
+// Row tile `tile` of kM rows: its expert, first row and the expert's end;
 // false past the last tile.  A whole warp.
-template <int kB>
+template <int kM>
 __device__ __forceinline__ bool row_tile(const int32_t* __restrict__ offs, int E, int tile, int* e, int* r0, int* r1) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int base = 0; base < E; base += 32) {
-    const int i = base + lane, a = i < E ? offs[i] : 0, b = i < E ? offs[i + 1] : 0, n = (b - a + kB - 1) / kB;
+    const int i = base + lane, a = i < E ? offs[i] : 0, b = i < E ? offs[i + 1] : 0, n = (b - a + kM - 1) / kM;
     int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -50,7 +53,7 @@ __device__ __forceinline__ bool row_tile(const int32_t* __restrict__ offs, int E
     if (hit) {
       const int src = __ffs(hit) - 1;
       *e = base + src;
-      *r0 = __shfl_sync(0xffffffffu, a + (tile - (incl - n)) * kB, src);
+      *r0 = __shfl_sync(0xffffffffu, a + (tile - (incl - n)) * kM, src);
       *r1 = __shfl_sync(0xffffffffu, b, src);
       return true;
     }
@@ -66,89 +69,126 @@ __device__ __forceinline__ float4 load4(const bf16* p) {
   const float2 b = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(&u)[1]);
   return make_float4(a.x, a.y, b.x, b.y);
 }
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(bf16* p, float4 v) {
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(bf16* p, const float (&v)[4]) {
   uint2 u;
-  reinterpret_cast<__nv_bfloat162*>(&u)[0] = __floats2bfloat162_rn(v.x, v.y);
-  reinterpret_cast<__nv_bfloat162*>(&u)[1] = __floats2bfloat162_rn(v.z, v.w);
+  reinterpret_cast<__nv_bfloat162*>(&u)[0] = __floats2bfloat162_rn(v[0], v[1]);
+  reinterpret_cast<__nv_bfloat162*>(&u)[1] = __floats2bfloat162_rn(v[2], v[3]);
   *reinterpret_cast<uint2*>(p) = u;
 }
 
-// An operand of a tile, kB indices i by kBK reduction indices k, in shared
+// An operand of a tile, kI indices i by kBK reduction indices k, in shared
 // memory as [k][i].  In memory either k runs along a row (kAlongK: element
 // i, k at i * stride + k) or i does (k * stride + i).  Rows start on 16 bytes
 // and the dimension along them is a multiple of 8, so four elements are
 // inside or outside together; outside (i >= ni, k >= nk) is zero.
-template <int kB, bool kAlongK>
+template <int kI, bool kAlongK>
 struct Stage {
-  static constexpr int kLoads = kB * kBK / 4 / kThreads;
+  static constexpr int kVecs = kI * kBK / 4, kLoads = (kVecs + kThreads - 1) / kThreads;
   float4 v[kLoads];
+  __device__ __forceinline__ static int at(int c) { return c * kThreads + threadIdx.x; }
   template <typename T>
   __device__ __forceinline__ void fetch(const T* __restrict__ src, int64_t stride, int ni, int nk) {
 #pragma unroll
     for (int c = 0; c < kLoads; ++c) {
-      const int at = c * kThreads + threadIdx.x;
-      const int i = kAlongK ? at / (kBK / 4) : at % (kB / 4) * 4, k = kAlongK ? at % (kBK / 4) * 4 : at / (kB / 4);
+      const int i = kAlongK ? at(c) / (kBK / 4) : at(c) % (kI / 4) * 4;
+      const int k = kAlongK ? at(c) % (kBK / 4) * 4 : at(c) / (kI / 4);
       v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < ni && k < nk) v[c] = load4(src + (kAlongK ? i * stride + k : k * stride + i));
     }
   }
-  __device__ __forceinline__ void put(float (*s)[kB + 4]) const {
+  __device__ __forceinline__ void put(float (*s)[kI + 4]) const {
 #pragma unroll
     for (int c = 0; c < kLoads; ++c) {
-      const int at = c * kThreads + threadIdx.x;
+      if (at(c) >= kVecs) break;
       if (kAlongK) {
-        const int i = at / (kBK / 4), k = at % (kBK / 4) * 4;
+        const int i = at(c) / (kBK / 4), k = at(c) % (kBK / 4) * 4;
         s[k][i] = v[c].x;
         s[k + 1][i] = v[c].y;
         s[k + 2][i] = v[c].z;
         s[k + 3][i] = v[c].w;
       } else {
-        *reinterpret_cast<float4*>(&s[at / (kB / 4)][at % (kB / 4) * 4]) = v[c];
+        *reinterpret_cast<float4*>(&s[at(c) / (kI / 4)][at(c) % (kI / 4) * 4]) = v[c];
       }
     }
   }
 };
 
-// acc += A^T B over the staged reduction: thread (ty, tx) holds R x R values.
-template <int kB, int R>
-__device__ __forceinline__ void multiply(float (&acc)[R][R], const float (*A)[kB + 4], const float (*B)[kB + 4], int ty,
-                                         int tx) {
+// This thread's 4 x 4 values of a kM x 64 tile, and its share of the reduction.
+template <int kM>
+struct Place {
+  static constexpr int kTileThreads = kM / 4 * (kN / 4), kGroups = kThreads / kTileThreads;
+  int ty, tx, group;
+  __device__ Place() {
+    const int i = threadIdx.x % kTileThreads;
+    ty = i / (kN / 4);
+    tx = i % (kN / 4);
+    group = threadIdx.x / kTileThreads;
+  }
+};
+
+// acc += A^T B over this group's share of the first nk staged elements.
+template <int kM>
+__device__ __forceinline__ void multiply(float (&acc)[4][4], const float (*A)[kM + 4], const float (*B)[kN + 4],
+                                         const Place<kM>& at, int nk) {
 #pragma unroll 8
-  for (int k = 0; k < kBK; ++k) {
-    float a[R], b[R];
+  for (int k = at.group; k < nk; k += Place<kM>::kGroups) {
+    const float4 a4 = *reinterpret_cast<const float4*>(&A[k][at.ty * 4]);
+    const float4 b4 = *reinterpret_cast<const float4*>(&B[k][at.tx * 4]);
+    const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      a[i] = A[k][ty * R + i];
-      b[i] = B[k][tx * R + i];
-    }
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int j = 0; j < R; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
   }
 }
 
-// da for one kB-row x kB-column tile: the products a (one, or gate and up)
+// The groups' accumulators added up, in order, in group 0's.
+template <int kM>
+__device__ __forceinline__ void gather(float (&acc)[4][4], const Place<kM>& at, float* s) {
+  constexpr int kG = Place<kM>::kGroups, kT = Place<kM>::kTileThreads;
+  if (kG == 1) return;
+  __syncthreads();
+  const int me = threadIdx.x % kT;
+  if (at.group > 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[((at.group - 1) * 16 + i) * kT + me] = acc[i / 4][i % 4];
+  }
+  __syncthreads();
+  if (at.group == 0) {
+    for (int g = 1; g < kG; ++g)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i / 4][i % 4] += s[((g - 1) * 16 + i) * kT + me];
+  }
+}
+// Shared memory of gather: three groups' accumulators of 64 threads.
+constexpr int kGatherFloats = 3 * 16 * 64;
+
+// da for one kM-row x 64-column tile: the products a (one, or gate and up)
 // and dh, all of length H, then the activation's slope.
-template <typename T, bool kSwi, int kB>
+template <typename T, bool kSwi, int kM>
 __global__ void __launch_bounds__(kThreads)
 hidden_gradient_simt_kernel(const T* __restrict__ x, const T* __restrict__ dy, const int32_t* __restrict__ offs,
                             int E, const T* __restrict__ W1, const float* __restrict__ b1, const T* __restrict__ W2,
                             int H, int F, float* __restrict__ da) {
-  constexpr int G = kSwi ? 2 : 1, R = kB / 16;
-  __shared__ float sx[kBK][kB + 4], sdy[kBK][kB + 4], sg[kBK][kB + 4], su[kSwi ? kBK : 1][kB + 4], s2[kBK][kB + 4];
+  constexpr int G = kSwi ? 2 : 1;
+  __shared__ __align__(16) float sx[kBK][kM + 4], sdy[kBK][kM + 4];
+  __shared__ __align__(16) float sw[2 + (kSwi ? 1 : 0)][kBK][kN + 4];   // gate, W2, up
+  static_assert(kM == 64 || sizeof(sw) >= kGatherFloats * sizeof(float), "the groups' sums reuse the weights' stage");
   pdl_enter();
   int e, r0, r1;
-  if (!row_tile<kB>(offs, E, blockIdx.y, &e, &r0, &r1)) return;
-  const int f0 = blockIdx.x * kB, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const int nr = min(kB, r1 - r0), nf = min(kB, F - f0);
+  if (!row_tile<kM>(offs, E, blockIdx.y, &e, &r0, &r1)) return;
+  const Place<kM> at;
+  const int f0 = blockIdx.x * kN, nr = min(kM, r1 - r0), nf = min(kN, F - f0);
   const T* px = x + (int64_t)r0 * H;
   const T* pdy = dy + (int64_t)r0 * H;
   const T* pg = W1 + ((int64_t)e * G * F + f0) * H;
   const T* p2 = W2 + (int64_t)e * H * F + f0;
-  Stage<kB, true> vx, vdy, vg, vu;
-  Stage<kB, false> v2;
+  Stage<kM, true> vx, vdy;
+  Stage<kN, true> vg, vu;
+  Stage<kN, false> v2;
   auto fetch = [&](int k0) {
     const int nk = min(kBK, H - k0);
     vx.fetch(px + k0, H, nr, nk);
@@ -157,124 +197,124 @@ hidden_gradient_simt_kernel(const T* __restrict__ x, const T* __restrict__ dy, c
     if (kSwi) vu.fetch(pg + (int64_t)F * H + k0, H, nf, nk);
     v2.fetch(p2 + (int64_t)k0 * F, F, nf, nk);
   };
-  float ag[R][R] = {}, au[R][R] = {}, ah[R][R] = {};
+  float ag[4][4] = {}, au[4][4] = {}, ah[4][4] = {};
   fetch(0);
   for (int k0 = 0; k0 < H; k0 += kBK) {
     vx.put(sx);
     vdy.put(sdy);
-    vg.put(sg);
-    if (kSwi) vu.put(su);
-    v2.put(s2);
+    vg.put(sw[0]);
+    v2.put(sw[1]);
+    if (kSwi) vu.put(sw[kSwi ? 2 : 0]);
     __syncthreads();
+    const int nk = min(kBK, H - k0);
     if (k0 + kBK < H) fetch(k0 + kBK);
-    multiply<kB, R>(ag, sx, sg, ty, tx);
-    if (kSwi) multiply<kB, R>(au, sx, su, ty, tx);
-    multiply<kB, R>(ah, sdy, s2, ty, tx);
+    multiply<kM>(ag, sx, sw[0], at, nk);
+    multiply<kM>(ah, sdy, sw[1], at, nk);
+    if (kSwi) multiply<kM>(au, sx, sw[kSwi ? 2 : 0], at, nk);
     __syncthreads();
   }
+  gather<kM>(ag, at, &sw[0][0][0]);
+  gather<kM>(ah, at, &sw[0][0][0]);
+  if (kSwi) gather<kM>(au, at, &sw[0][0][0]);
+  if (at.group > 0 || at.tx * 4 >= nf) return;
+  const int f = f0 + at.tx * 4;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int r = ty * R + i;
+  for (int i = 0; i < 4; ++i) {
+    const int r = at.ty * 4 + i;
     if (r >= nr) continue;
+    float dg[4], du[4];
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int f = f0 + tx * R + j;
-      if (f >= F) continue;
-      float* d = da + (int64_t)(r0 + r) * G * F + f;
-      const float a = ag[i][j] + (b1 ? b1[(int64_t)e * G * F + f] : 0.f);
-      if (kSwi) {
-        const float u = au[i][j] + (b1 ? b1[(int64_t)e * G * F + F + f] : 0.f);
-        swiglu_gradient(a, u, ah[i][j], d, d + F);
-      } else {
-        *d = ah[i][j] * gelu_slope(a);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const float a = ag[i][j] + (b1 ? b1[(int64_t)e * G * F + f + j] : 0.f);
+      if (kSwi)
+        swiglu_gradient(a, au[i][j] + (b1 ? b1[(int64_t)e * G * F + F + f + j] : 0.f), ah[i][j], &dg[j], &du[j]);
+      else
+        dg[j] = ah[i][j] * gelu_slope(a);
     }
+    float* d = da + (int64_t)(r0 + r) * G * F + f;
+    store4(d, dg);
+    if (kSwi) store4(d + F, du);
   }
 }
 
-// out[i, j] for i < ni, j < nj (nj a multiple of 8) of this block's tile.
-template <typename T, int R>
-__device__ __forceinline__ void store_tile(T* out, int64_t stride, const float (&acc)[R][R], int ni, int nj, int ty,
-                                           int tx) {
+// acc[i][j] to out at row ty * 4 + i < ni, column tx * 4 + j < nj (a multiple of 8).
+template <typename T, int kM>
+__device__ __forceinline__ void store_tile(T* out, int64_t stride, const float (&acc)[4][4], int ni, int nj,
+                                           const Place<kM>& at) {
+  if (at.group > 0 || at.tx * 4 >= nj) return;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (ty * R + i >= ni || tx * R >= nj) continue;
-    T* p = out + (int64_t)(ty * R + i) * stride + tx * R;
-    if constexpr (R == 4) {
-      store4(p, make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]));
-    } else {
-#pragma unroll
-      for (int j = 0; j < R; ++j) p[j] = from_f32<T>(acc[i][j]);
-    }
-  }
+  for (int i = 0; i < 4; ++i)
+    if (at.ty * 4 + i < ni) store4(out + (int64_t)(at.ty * 4 + i) * stride + at.tx * 4, acc[i]);
 }
+
+union Shared {
+  struct { float a[kBK][64 + 4], b[kBK][kN + 4]; } w;
+  struct { float a[kBK][16 + 4], b[kBK][kN + 4]; } r;
+  float sums[kGatherFloats];
+};
 
 // dx tile: da [rows, N] times W1[e] [N, H].
-template <typename T, int kB>
+template <typename T, int kM>
 __device__ __forceinline__ void input_tile(const float* __restrict__ da, const int32_t* __restrict__ offs, int E,
                                            const T* __restrict__ W1, int N, int H, T* __restrict__ dx, int row, int col,
-                                           float (*sa)[kB + 4], float (*sb)[kB + 4]) {
-  constexpr int R = kB / 16;
+                                           float (*sa)[kM + 4], float (*sb)[kN + 4], float* sums) {
   int e, r0, r1;
-  if (!row_tile<kB>(offs, E, row, &e, &r0, &r1)) return;
-  const int h0 = col * kB, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const int nr = min(kB, r1 - r0), nh = min(kB, H - h0);
+  if (!row_tile<kM>(offs, E, row, &e, &r0, &r1)) return;
+  const Place<kM> at;
+  const int h0 = col * kN, nr = min(kM, r1 - r0), nh = min(kN, H - h0);
   const float* pa = da + (int64_t)r0 * N;
   const T* pw = W1 + (int64_t)e * N * H + h0;
-  Stage<kB, true> va;
-  Stage<kB, false> vw;
-  float acc[R][R] = {};
-  va.fetch(pa, N, nr, min(kBK, N));
-  vw.fetch(pw, H, nh, min(kBK, N));
+  Stage<kM, true> va;
+  Stage<kN, false> vw;
+  float acc[4][4] = {};
+  auto fetch = [&](int k0) {
+    va.fetch(pa + k0, N, nr, min(kBK, N - k0));
+    vw.fetch(pw + (int64_t)k0 * H, H, nh, min(kBK, N - k0));
+  };
+  fetch(0);
   for (int k0 = 0; k0 < N; k0 += kBK) {
     va.put(sa);
     vw.put(sb);
     __syncthreads();
-    const int next = k0 + kBK;
-    if (next < N) {
-      va.fetch(pa + next, N, nr, min(kBK, N - next));
-      vw.fetch(pw + (int64_t)next * H, H, nh, min(kBK, N - next));
-    }
-    multiply<kB, R>(acc, sa, sb, ty, tx);
+    if (k0 + kBK < N) fetch(k0 + kBK);
+    multiply<kM>(acc, sa, sb, at, min(kBK, N - k0));
     __syncthreads();
   }
-  store_tile<T, R>(dx + (int64_t)r0 * H + h0, H, acc, nr, nh, ty, tx);
+  gather<kM>(acc, at, sums);
+  store_tile<T, kM>(dx + (int64_t)r0 * H + h0, H, acc, nr, nh, at);
 }
 
 // One tile of dW[e] [M, N] = sum over expert e's rows of a_r b_r^T (zeros for
 // an expert with no row); with n0 = 0 also db[e] = sum of a_r.  dW, db nullable.
-template <typename TA, typename T, int kB>
+template <typename TA, typename T>
 __device__ __forceinline__ void weight_tile(const TA* __restrict__ A, const T* __restrict__ B,
                                             const int32_t* __restrict__ offs, int M, int N, T* __restrict__ dW,
-                                            float* __restrict__ db, int e, int m0, int n0, float (*sa)[kB + 4],
-                                            float (*sb)[kB + 4]) {
-  constexpr int R = kB / 16;
-  const int r0 = offs[e], rows = offs[e + 1] - r0, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const int nm = min(kB, M - m0), nn = min(kB, N - n0);
+                                            float* __restrict__ db, int e, int m0, int n0, float (*sa)[64 + 4],
+                                            float (*sb)[kN + 4]) {
+  const Place<64> at;
+  const int r0 = offs[e], rows = offs[e + 1] - r0, nm = min(64, M - m0), nn = min(kN, N - n0);
   const TA* pa = A + (int64_t)r0 * M + m0;
   const T* pb = B + (int64_t)r0 * N + n0;
-  Stage<kB, false> va, vb;
-  float acc[R][R] = {}, sum = 0.f;
+  Stage<64, false> va, vb;
+  float acc[4][4] = {}, sum = 0.f;
   const bool sums = db && n0 == 0;
-  if (rows > 0) {
-    va.fetch(pa, M, nm, min(kBK, rows));
-    if (dW) vb.fetch(pb, N, nn, min(kBK, rows));
-  }
+  auto fetch = [&](int k0) {
+    va.fetch(pa + (int64_t)k0 * M, M, nm, min(kBK, rows - k0));
+    if (dW) vb.fetch(pb + (int64_t)k0 * N, N, nn, min(kBK, rows - k0));
+  };
+  if (rows > 0) fetch(0);
   for (int k0 = 0; k0 < rows; k0 += kBK) {
+    const int nk = min(kBK, rows - k0);
     va.put(sa);
     if (dW) vb.put(sb);
     __syncthreads();
-    const int next = k0 + kBK;
-    if (next < rows) {
-      va.fetch(pa + (int64_t)next * M, M, nm, min(kBK, rows - next));
-      if (dW) vb.fetch(pb + (int64_t)next * N, N, nn, min(kBK, rows - next));
-    }
-    if (dW) multiply<kB, R>(acc, sa, sb, ty, tx);
-    if (sums && threadIdx.x < kB)
-      for (int k = 0; k < kBK; ++k) sum += sa[k][threadIdx.x];
+    if (k0 + kBK < rows) fetch(k0 + kBK);
+    if (dW) multiply<64>(acc, sa, sb, at, nk);
+    if (sums && threadIdx.x < 64)
+      for (int k = 0; k < nk; ++k) sum += sa[k][threadIdx.x];
     __syncthreads();
   }
-  if (dW) store_tile<T, R>(dW + ((int64_t)e * M + m0) * N + n0, N, acc, nm, nn, ty, tx);
+  if (dW) store_tile<T, 64>(dW + ((int64_t)e * M + m0) * N + n0, N, acc, nm, nn, at);
   if (sums && (int)threadIdx.x < nm) db[(int64_t)e * M + m0 + threadIdx.x] = sum;
 }
 
@@ -284,37 +324,43 @@ struct Tiles {
   int w1, w1_cols, w1_per;    // blocks of dW1, columns of tiles, tiles of an expert
   int w2_cols, w2_per;
 };
-template <typename T, int kB>
+template <typename T, int kM>
 __global__ void __launch_bounds__(kThreads)
-gradients_simt_kernel(const float* __restrict__ da, FfnBackward b, int E, int H, int F, int N, Tiles t) {
-  __shared__ float sa[kBK][kB + 4], sb[kBK][kB + 4];
+gradients_simt_kernel(const float* __restrict__ da, const __grid_constant__ FfnBackward b, int E, int H, int F, int N,
+                      Tiles t) {
+  __shared__ __align__(16) Shared s;
   pdl_enter();
   int i = blockIdx.x;
   if (i < t.dx) {
-    input_tile<T, kB>(da, b.offs, E, (const T*)b.W1, N, H, (T*)b.dx_perm, i / t.dx_cols, i % t.dx_cols, sa, sb);
+    if constexpr (kM == 64)
+      input_tile<T, kM>(da, b.offs, E, (const T*)b.W1, N, H, (T*)b.dx_perm, i / t.dx_cols, i % t.dx_cols, s.w.a, s.w.b,
+                        s.sums);
+    else
+      input_tile<T, kM>(da, b.offs, E, (const T*)b.W1, N, H, (T*)b.dx_perm, i / t.dx_cols, i % t.dx_cols, s.r.a, s.r.b,
+                        s.sums);
   } else if ((i -= t.dx) < t.w1) {
     const int e = i / t.w1_per, l = i % t.w1_per;
-    weight_tile<float, T, kB>(da, (const T*)b.x_perm, b.offs, N, H, (T*)b.dW1, b.db1, e, l / t.w1_cols * kB,
-                              l % t.w1_cols * kB, sa, sb);
+    weight_tile(da, (const T*)b.x_perm, b.offs, N, H, (T*)b.dW1, b.db1, e, l / t.w1_cols * 64, l % t.w1_cols * kN,
+                s.w.a, s.w.b);
   } else {
     i -= t.w1;
     const int e = i / t.w2_per, l = i % t.w2_per;
-    weight_tile<T, T, kB>((const T*)b.dy_perm, (const T*)b.h_perm, b.offs, H, F, (T*)b.dW2, b.db2, e,
-                          l / t.w2_cols * kB, l % t.w2_cols * kB, sa, sb);
+    weight_tile((const T*)b.dy_perm, (const T*)b.h_perm, b.offs, H, F, (T*)b.dW2, b.db2, e, l / t.w2_cols * 64,
+                l % t.w2_cols * kN, s.w.a, s.w.b);
   }
 }
 
-template <typename T, int kB>
+template <typename T, int kM>
 cudaError_t run_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, float* da, cudaStream_t st) {
   const bool swi = (s.flags & MOE_FLAG_SWIGLU) != 0;
   const int N = swi ? 2 * s.F : s.F;
-  auto tiles = [](int64_t n) { return (n + kB - 1) / kB; };
+  auto tiles = [](int64_t n) { return (n + kN - 1) / kN; };
   // at most one part-filled row tile for each expert with rows
-  const int64_t mtiles = max_rows / kB + (max_rows < s.E ? max_rows : s.E);
+  const int64_t mtiles = max_rows / kM + (max_rows < s.E ? max_rows : s.E);
   if (mtiles > 65535) return cudaErrorNotSupported;
   const bool hidden = max_rows > 0 && (b.dx_perm || b.dW1 || b.db1);
   if (hidden) {
-    auto k = swi ? hidden_gradient_simt_kernel<T, true, kB> : hidden_gradient_simt_kernel<T, false, kB>;
+    auto k = swi ? hidden_gradient_simt_kernel<T, true, kM> : hidden_gradient_simt_kernel<T, false, kM>;
     const cudaError_t e =
         launch_kernel(k, dim3((unsigned)tiles(s.F), (unsigned)mtiles), dim3(kThreads), 0, st, 1, (const T*)b.x_perm,
                       (const T*)b.dy_perm, b.offs, s.E, (const T*)b.W1, b.b1, (const T*)b.W2, s.H, s.F, da);
@@ -327,14 +373,13 @@ cudaError_t run_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, flo
   if (all == 0) return cudaSuccess;
   if (all >= ((int64_t)1 << 31)) return cudaErrorNotSupported;
   const Tiles t{(int)dx, (int)tiles(s.H), (int)w1, (int)w1_cols, (int)w1_per, (int)w2_cols, (int)w2_per};
-  return launch_kernel(gradients_simt_kernel<T, kB>, dim3((unsigned)all), dim3(kThreads), 0, st, 1, (const float*)da,
+  return launch_kernel(gradients_simt_kernel<T, kM>, dim3((unsigned)all), dim3(kThreads), 0, st, 1, (const float*)da,
                        b, s.E, s.H, s.F, N, t);
 }
 
 template <typename T>
 cudaError_t pick_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, float* da, cudaStream_t st) {
-  const int64_t big = (max_rows / 64 + s.E) * ((s.F + 63) / 64);   // tiles of da
-  return big < 2 * sm_count() ? run_simt<T, 32>(s, max_rows, b, da, st) : run_simt<T, 64>(s, max_rows, b, da, st);
+  return max_rows < 32 * (int64_t)s.E ? run_simt<T, 16>(s, max_rows, b, da, st) : run_simt<T, 64>(s, max_rows, b, da, st);
 }
 
 }  // namespace
