@@ -56,10 +56,11 @@ constexpr int kSwapRows = 128;            // a last block of at most this many r
 constexpr int kOperand = kBM * kBK * 2;   // bytes of one operand in a stage
 constexpr int kHalf = kOperand / 2;       // an MN-major operand is two boxes of 64 columns x 64 rows
 constexpr int kStageBytes = 2 * kOperand;
-constexpr int kRowsStages = 6, kWeightsStages = 7;   // the rows kernel's tile tables leave no room for a seventh
+constexpr int kStages = 6;
 constexpr int kTmemCols = 512;            // two accumulators of 256 columns
 constexpr int kEpiWarps = 8;              // per CTA: two for each quarter of the TMEM lanes
-constexpr size_t smem_bytes(int stages) { return 1024 + (size_t)stages * kStageBytes; }
+constexpr int kStoreBytes = 32 * 128;     // weights kernel: an epilogue warp's 32 rows of 64 columns
+constexpr size_t kSmemRows = 1024 + (size_t)kStages * kStageBytes, kSmemWeights = kSmemRows + kEpiWarps * kStoreBytes;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -124,7 +125,6 @@ __device__ __forceinline__ int expert_of(const int* tstart, int E, int t) {
   return lo;
 }
 
-template <int kStages>
 __device__ __forceinline__ void advance(int& stage, uint32_t& phase) {
   if (++stage == kStages) {
     stage = 0;
@@ -218,7 +218,7 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
           } else if (kKind == kDx) {
             o.dx[at + (int64_t)j * N] = __float2bfloat16_rn(v);
           } else {
-            const float d = g[j % (kDa ? 32 : 1)] * gelu_slope(v + bf);
+            const float d = g[j % (kDa ? 32 : 1)] * gelu_slope_fast(v + bf);
             sum += d;
             o.da[at + (int64_t)j * N] = __float2bfloat16_rn(d);
           }
@@ -279,10 +279,10 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
           const int j = g * 4 + i;
           const float a = __uint_as_float(r[j]) + ba[i];
           if (kSwi)
-            swiglu_gradient(a, __uint_as_float(u[j % (kSwi ? 32 : 1)]) + bb[i], dh[i], &v[j],
+            swiglu_gradient_fast(a, __uint_as_float(u[j % (kSwi ? 32 : 1)]) + bb[i], dh[i], &v[j],
                             &w[j % (kSwi ? 32 : 1)]);
           else
-            v[j] = dh[i] * gelu_slope(a);
+            v[j] = dh[i] * gelu_slope_fast(a);
         }
       }
       if (ok) {
@@ -312,7 +312,6 @@ __device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, 
 __device__ __forceinline__ int row_blocks(int rows) { return (rows + kTile - 1) / kTile; }
 
 // Barriers of a CTA: full and empty per stage, full and empty per accumulator, the end.
-template <int kStages>
 struct Bars {
   uint32_t base;
   __device__ uint32_t full(int s) const { return base + 8 * s; }
@@ -336,7 +335,6 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
                      RowsOut out, int* err) {
   constexpr bool kSwi = kKind == kDaSwiglu, kMN = kKind == kDh || kKind == kDx;
   constexpr int kOut = kSwi ? kBM : kTile;
-  constexpr int kStages = kRowsStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_offs[257], s_tstart[257];
   __shared__ uint32_t s_tmem;
@@ -344,7 +342,7 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sB = sA + kStages * kOperand;
-  const Bars<kStages> bar{tc::smem_u32(s_bar)};
+  const Bars bar{tc::smem_u32(s_bar)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)tc::cluster_ctarank();
   const int nt = (N + kOut - 1) / kOut, nk = (K + kBK - 1) / kBK;
@@ -434,7 +432,7 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
           }
           filled |= 1u << stage;
           fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
-          advance<kStages>(stage, phase);
+          advance(stage, phase);
         }
       }
       if (!ok) give_up(err, &s_abort);
@@ -465,7 +463,7 @@ backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
             tc::mma_bf16_pair(dst, da, db, idesc, (kb | k) != 0);
           }
           tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
-          advance<kStages>(stage, phase);
+          advance(stage, phase);
         }
         if (!ok) break;
         tc::tc_commit_pair_mc(bar.tfull(acc), 0x3);
@@ -615,27 +613,29 @@ backward_extras_kernel(const __grid_constant__ Extras x, const int32_t* __restri
 // (M columns) times B's row (N columns).
 struct WeightProduct {
   int M, N;
-  bf16* out;
-  bool sectors;    // out's rows start on 32 bytes
 };
 
 // tmA, tmB: an operand's rows in boxes of 64 x 64; tmAt, tmBt: its tails in
-// boxes of 64 columns x 16 rows.  Products 0 and 1 follow one another.
+// boxes of 64 columns x 16 rows; tmO: out in boxes of 32 rows x 64 columns.
+// Products 0 and 1 follow one another.  An accumulator leaves through shared
+// memory by TMA: stored by its threads, a row each, it took 594 us instead of
+// 440 at the prefill layer with 16 bytes a store (450 with 32, which needs
+// rows that start on 32 bytes).
 __global__ void __launch_bounds__(kThreads, 1)
 backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
                         const __grid_constant__ CUtensorMap tmAt0, const __grid_constant__ CUtensorMap tmBt0,
                         const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
                         const __grid_constant__ CUtensorMap tmAt1, const __grid_constant__ CUtensorMap tmBt1,
+                        const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
                         const int32_t* __restrict__ offs, int E, WeightProduct P0, WeightProduct P1, int* err) {
-  constexpr int kStages = kWeightsStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_offs[257];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sB = sA + kStages * kOperand;
-  const Bars<kStages> bar{tc::smem_u32(s_bar)};
+  const uint32_t sB = sA + kStages * kOperand, sOut = sB + kStages * kOperand;
+  const Bars bar{tc::smem_u32(s_bar)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)tc::cluster_ctarank();
   auto tiles = [](int n) { return (n + kTile - 1) / kTile; };
@@ -722,7 +722,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
           tc::tma_load_2d_pair(b + kHalf, mB, fbar, n + 64, r);
           filled |= 1u << stage;
           fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
-          advance<kStages>(stage, phase);
+          advance(stage, phase);
         }
       }
       if (!ok) give_up(err, &s_abort);
@@ -750,7 +750,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
           for (int k = 0; k < groups; ++k)
             tc::mma_bf16_pair(dst, sdesc_mn128(a0 + k * kStepMN), sdesc_mn128(b0 + k * kStepMN), idesc, (kb | k) != 0);
           tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
-          advance<kStages>(stage, phase);
+          advance(stage, phase);
           if (kb == 0 && t + step < total) next = decode(t + step);   // its divisions run beside the MMAs
         }
         if (!ok) break;
@@ -767,6 +767,8 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
     __syncwarp();
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t buf = sOut + (warp - 2) * kStoreBytes;
+    uint8_t* g = smem_raw + (buf - tc::smem_u32(smem_raw)) + lane * 128;   // this thread's row of it
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = first; t < total; t += step) {
@@ -777,26 +779,35 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
       }
       tc::tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile);
-      const int M = d.p ? P1.M : P0.M, N = d.p ? P1.N : P0.N;
-      const int m = d.m0 + rank * kBM + q * 32 + lane;
-      bf16* row = (d.p ? P1.out : P0.out) + ((int64_t)d.e * M + m) * N;
-      const bool sectors = d.p ? P1.sectors : P0.sectors;
+      const int m = d.m0 + rank * kBM + q * 32;
+      if (m < (d.p ? P1.M : P0.M)) {
 #pragma unroll 1
-      for (int c = half * (kTile / 64); c < (half + 1) * (kTile / 64); ++c) {
-        const int n = d.n0 + c * 32;
-        if (n >= N) break;
-        float v[32];
-        if (d.nk > 0) {
-          uint32_t r[32];
-          tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
-          tc::tmem_wait_ld();
+        for (int c = half * (kTile / 128); c < (half + 1) * (kTile / 128); ++c) {
+          const int n = d.n0 + c * 64;
+          if (n >= (d.p ? P1.N : P0.N)) break;
+          if (lane == 0) tc::bulk_wait_read();   // the buffer's previous store has been read
+          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        } else {
+          for (int h = 0; h < 2; ++h) {
+            float v[32];
+            if (d.nk > 0) {
+              uint32_t r[32];
+              tc::tmem_ld_32x32b_x32(tbase + c * 64 + h * 32, r);
+              tc::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)   // 16 bytes at the place that the 128-byte swizzle gives them
+              *reinterpret_cast<uint4*>(g + (((h * 4 + j) ^ (lane & 7)) << 4)) = Vec<bf16>::pack(v + j * 8);
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::tma_store_3d(d.p ? &tmO1 : &tmO0, buf, n, m, d.e);
         }
-        if (m < M) store_row(row + n, v, min(32, N - n), sectors);
       }
       tc::tc_fence_before();
       if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
@@ -804,6 +815,7 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
+    if (lane == 0) tc::bulk_wait_all();
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -841,7 +853,7 @@ cudaError_t run_rows(const void* tokens, int64_t rows, int K, const void* W, int
   if (kMN ? !tma_map_bf16_3d(&mw, W, (uint64_t)E, (uint64_t)K, (uint64_t)N, kBK)
           : !tma_map_bf16(&mw, W, (uint64_t)E * N * (kKind == kDaSwiglu ? 2 : 1), (uint64_t)K, kBM))
     return cudaErrorNotSupported;
-  return launch_pairs(backward_rows_kernel<kKind>, smem_bytes(kRowsStages), st, mx, mxs, mw, offs, E, N, K, out, err);
+  return launch_pairs(backward_rows_kernel<kKind>, kSmemRows, st, mx, mxs, mw, offs, E, N, K, out, err);
 }
 
 }  // namespace
@@ -871,7 +883,8 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
     return e;
   }
   CUtensorMap m[8];
-  WeightProduct P[2] = {{0, 0, nullptr, false}, {0, 0, nullptr, false}};
+  CUtensorMap mo[2];
+  WeightProduct P[2] = {{0, 0}, {0, 0}};
   Extras x = {};
   int n = 0;   // weight products
   bf16* at = (bf16*)tails;
@@ -883,8 +896,9 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
            tma_map_bf16(&m[4 * n + 2 + i], t, (uint64_t)s.E * kTailRows, (uint64_t)cols, kTailRows);
   };
   auto add = [&](const void* A, int M, const void* Bm, int Nn, void* dW) {
-    P[n] = {M, Nn, (bf16*)dW, starts_on_sectors(dW, Nn, 2)};
-    const bool ok = add_operand(0, A, M) && add_operand(1, Bm, Nn);
+    P[n] = {M, Nn};
+    const bool ok = add_operand(0, A, M) && add_operand(1, Bm, Nn) &&
+                    tma_map_bf16_3d(&mo[n], dW, (uint64_t)s.E, (uint64_t)M, (uint64_t)Nn, 32);
     ++n;
     return ok;
   };
@@ -914,11 +928,13 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
   out.sectors = starts_on_sectors(b.dx_perm, s.H, 2);
   if (e == cudaSuccess && b.dx_perm)
     e = run_rows<kDx>(da, max_rows, N, b.W1, s.E, s.H, b.offs, out, err, st);
-  if (n == 1)
+  if (n == 1) {
     for (int i = 0; i < 4; ++i) m[4 + i] = m[i];
+    mo[1] = mo[0];
+  }
   if (e == cudaSuccess && n > 0)
-    e = launch_pairs(backward_weights_kernel, smem_bytes(kWeightsStages), st, m[0], m[1], m[2], m[3], m[4], m[5], m[6],
-                     m[7], b.offs, s.E, P[0], P[1], err);
+    e = launch_pairs(backward_weights_kernel, kSmemWeights, st, m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], mo[0],
+                     mo[1], b.offs, s.E, P[0], P[1], err);
   return e;
 }
 
