@@ -418,7 +418,8 @@ typedef struct moe_adamw_tensor {
   int32_t reserved;      /* 0 */
 } moe_adamw_tensor;
 
-/* lr >= 0, 0 <= beta1, beta2 < 1, eps >= 0, all finite; step = 1 for the first. */
+/* lr >= 0, 0 <= beta1, beta2 < 1, eps >= 0 (below 1e-30: taken as 0), all
+ * finite; step = 1 for the first. */
 typedef struct moe_adamw_params {
   double lr;
   double beta1;

@@ -10,16 +10,28 @@
 // block, code = e4m3(x 448 / A) rounded to nearest even and scale = A / 448.
 // A non-zero r keeps a non-zero code (at least 2^-9), so that no element's
 // divisor falls to eps alone by rounding.  A block with A < 2^-100 is held as
-// zeros.  A block with a NaN or an infinity gets that A as its scale and zero
-// codes, so that all of it reads back as NaN: loud, not silently clipped.
+// zeros.  A block with a NaN or an infinity gets that A as its scale and codes
+// of 0 and NaN, so that all of it reads back as NaN: loud, not silently clipped.
 //
 // Every operation of the moments rounds by itself (no fused multiply-add), in
 // the order written above, so that a code is a function of its inputs alone.
+// The parameter's own update may fuse, and its quotient is the fast one (2
+// units of the last place of an update that is itself a small part of p): with
+// IEEE quotients the 8-bit step was bound by instructions, 1719 us for 587 M
+// elements.  (A divisor is eps or at least 3e-23, the square root of the
+// smallest fp32 number.)
 //
-// One warp takes a block of 256 elements: lane l holds elements 4 l .. 4 l + 3
+// A warp takes one block of 256 elements: lane l holds elements 4 l .. 4 l + 3
 // of both halves, so each load of the warp is contiguous; A is a warp maximum.
+// The eight warps of a thread block take consecutive blocks, whose scales fill
+// one 32-byte sector.  (Several blocks to a warp, one after the other, were
+// slower by a third: 2.1 ms.  A grid that fits the GPU once, striding, took
+// 647 us instead of 578 with moments in 32 bits.)
+//
 // Bound by memory: 28 bytes an element (moments in 32 bits, bf16 gradient, a
-// bf16 copy of p) or 16 bytes and 16 / 256 of scales.
+// bf16 copy of p) or 16 bytes and 16 / 256 of scales.  Measured: 578 us for
+// 147 M elements (7.1 TB/s), in 8 bits 1545 us for 587 M (6.1 TB/s; two thirds
+// of the issue slots are taken too).
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -37,7 +49,7 @@ static_assert(kBlock == 32 * kPer, "a warp holds a block");
 constexpr uint32_t kTinyBits = (127u - 100u) << 23;   // 2^-100
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-// One tensor of a launch; first = the number of 256-element blocks before it.
+// One tensor of a launch.
 struct Slot {
   float* p;
   bf16* p16;
@@ -47,13 +59,13 @@ struct Slot {
   float* m_scale;
   float* v_scale;
   int64_t n;
-  uint32_t first;
   float keep;      // 1 - lr * weight decay
 };
 
 template <int kCap>
 struct Slots {
   Slot s[kCap];
+  uint32_t first[kCap];   // the number of blocks before a tensor's
   int count;
   uint32_t blocks;
 };
@@ -67,12 +79,6 @@ struct Step {
 // about 3 us more with the longest); they have to stay below 32764 bytes.
 constexpr int kSmallCap = 40, kMiddleCap = 128, kLargeCap = 400;
 static_assert(sizeof(Slots<kLargeCap>) + sizeof(Step) + 32 < 32764, "kernel parameters");
-
-__device__ __forceinline__ float warp_max_bits(uint32_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return __uint_as_float(v);
-}
 
 // Element 4 l + i of half h: the lane's value h * 4 + i.
 template <bool kFull>
@@ -199,22 +205,30 @@ __device__ __forceinline__ void store(uint8_t* dst, int lane, int left, const fl
   }
 }
 
+// The largest magnitude of three; NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // The block's values as codes and its scale (lane 0 writes it).  Elements
 // past the tensor's end are zeros and do not count.
 template <bool kFull, bool kKeepNonZero>
 __device__ __forceinline__ void encode(const float* x, uint8_t* codes, float* scale, int lane, int left) {
-  uint32_t top = 0;
+  float top = 0.f;
 #pragma unroll
-  for (int c = 0; c < kPer; ++c) top = max(top, __float_as_uint(x[c]) & 0x7fffffffu);   // NaN > infinity > finite
-  const float A = warp_max_bits(top);
-  const uint32_t bits = __float_as_uint(A);
+  for (int c = 0; c < kPer; c += 2) top = max_abs(top, x[c], x[c + 1]);
+  const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // as bits: NaN > infinity > finite
+  const float A = __uint_as_float(bits);
   const bool finite = bits < kInfBits, big = bits >= kTinyBits && finite;
   const float inv = big ? __fdiv_rn(448.f, A) : 0.f;
+  const float least = big ? 0.001953125f : 0.f;   // 2^-9, the smallest code
   float y[kPer];
 #pragma unroll
   for (int c = 0; c < kPer; ++c) {
-    y[c] = big ? __fmul_rn(x[c], inv) : 0.f;
-    if (kKeepNonZero && big && x[c] > 0.f) y[c] = fmaxf(y[c], 0.001953125f);   // 2^-9, the smallest code
+    y[c] = __fmul_rn(x[c], inv);
+    if (kKeepNonZero && x[c] > 0.f) y[c] = fmaxf(y[c], least);
   }
   store<kFull>(codes, lane, left, y);
   if (lane == 0) *scale = big ? __fmul_rn(A, 1.0f / 448.0f) : (finite ? 0.f : A);
@@ -247,8 +261,7 @@ __device__ __forceinline__ void update_block(const Slot& s, uint32_t block, cons
     m[c] = __fadd_rn(__fmul_rn(m[c], q.beta1), __fmul_rn(gc, q.one_minus_beta1));
     v[c] = __fadd_rn(__fmul_rn(v[c], q.beta2), __fmul_rn(__fmul_rn(gc, gc), q.one_minus_beta2));
     const float r = __fsqrt_rn(v[c]);
-    p[c] = __fsub_rn(__fmul_rn(p[c], s.keep),
-                     __fmul_rn(__fdiv_rn(m[c], __fadd_rn(__fmul_rn(r, q.inv_sqrt_c2), q.eps)), q.lr_c1));
+    p[c] = fmaf(p[c], s.keep, -q.lr_c1 * __fdividef(m[c], fmaf(r, q.inv_sqrt_c2, q.eps)));
     if (kEight) v[c] = r;
   }
   store<kFull>(s.p + at, lane, left, p);
@@ -270,23 +283,21 @@ adamw_kernel(const __grid_constant__ Slots<kCap> t, const __grid_constant__ Step
   if (skip && *skip != 0) return;
   const float gs = grad_scale ? *grad_scale : 1.0f;
   const int lane = threadIdx.x & 31;
-  const uint32_t stride = gridDim.x * kWarps;
-  int cur = 0;
-  for (uint32_t b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < t.blocks; b += stride) {
-    int hi = t.count - 1;
-    while (cur < hi) {   // the last tensor that starts at or before b; b only grows
-      const int mid = (cur + hi + 1) >> 1;
-      if (t.s[mid].first <= b) cur = mid; else hi = mid - 1;
-    }
-    const Slot& s = t.s[cur];
-    const uint32_t block = b - s.first;
-    // vector loads and stores need 16-byte aligned tensors and a whole block
-    const uintptr_t all = (uintptr_t)s.p | (uintptr_t)s.p16 | (uintptr_t)s.g | (uintptr_t)s.m | (uintptr_t)s.v;
-    if ((all & 15u) == 0 && ((int64_t)block + 1) * kBlock <= s.n)
-      update_block<true, TG, kEight>(s, block, q, gs, lane);
-    else
-      update_block<false, TG, kEight>(s, block, q, gs, lane);
+  const uint32_t at = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (at >= t.blocks) return;
+  int cur = 0, hi = t.count - 1;
+  while (cur < hi) {   // the last tensor that starts at or before this block
+    const int mid = (cur + hi + 1) >> 1;
+    if (t.first[mid] <= at) cur = mid; else hi = mid - 1;
   }
+  const Slot& s = t.s[cur];
+  const uint32_t block = at - t.first[cur];
+  // vector loads and stores need 16-byte aligned tensors and a whole block
+  const uintptr_t all = (uintptr_t)s.p | (uintptr_t)s.p16 | (uintptr_t)s.g | (uintptr_t)s.m | (uintptr_t)s.v;
+  if ((all & 15u) == 0 && ((int64_t)block + 1) * kBlock <= s.n)
+    update_block<true, TG, kEight>(s, block, q, gs, lane);
+  else
+    update_block<false, TG, kEight>(s, block, q, gs, lane);
 }
 
 template <int kCap, typename TG, bool kEight>
@@ -300,7 +311,7 @@ cudaError_t run_adamw(const moe_adamw_tensor* tensors, int count, const Step& q,
     for (; i < count && t.count < kCap; ++i) {
       const moe_adamw_tensor& x = tensors[i];
       if (x.n == 0) continue;
-      const uint64_t nb = (uint64_t)(x.n + kBlock - 1) / kBlock;
+      const uint64_t nb = ((uint64_t)x.n + kBlock - 1) / kBlock;
       if (t.count > 0 && blocks + nb >= (1ull << 31)) break;   // block numbers stay in 32 bits
       Slot& s = t.s[t.count++];
       s.p = x.p;
@@ -311,15 +322,14 @@ cudaError_t run_adamw(const moe_adamw_tensor* tensors, int count, const Step& q,
       s.m_scale = x.m_scale;
       s.v_scale = x.v_scale;
       s.n = x.n;
-      s.first = (uint32_t)blocks;
+      t.first[t.count - 1] = (uint32_t)blocks;
       s.keep = (float)(1.0 - lr * (double)x.weight_decay);
       blocks += nb;
     }
     if (t.count == 0) break;
     t.blocks = (uint32_t)blocks;
-    const uint64_t need = (blocks + kWarps - 1) / kWarps, cap = (uint64_t)sm_count() * 8;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(need < cap ? need : cap));
+    cfg.gridDim = dim3((unsigned)((blocks + kWarps - 1) / kWarps));
     cfg.blockDim = dim3(32 * kWarps);
     cfg.stream = st;
     cudaLaunchAttribute attr;
@@ -354,7 +364,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int count, int grad_dt
   q.beta2 = (float)h.beta2;
   q.one_minus_beta2 = (float)(1.0 - h.beta2);
   q.inv_sqrt_c2 = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)h.step)));
-  q.eps = (float)h.eps;
+  q.eps = h.eps < 1e-30 ? 0.f : (float)h.eps;   // the fast quotient wants a divisor whose reciprocal is a normal number
   q.lr_c1 = (float)(h.lr / (1.0 - pow(h.beta1, (double)h.step)));
   auto pick = count <= kSmallCap ? pick_adamw<kSmallCap>
                                  : count <= kMiddleCap ? pick_adamw<kMiddleCap> : pick_adamw<kLargeCap>;

@@ -11,6 +11,11 @@
 //   dx[t] = sum_j dx_perm[pos[t, j]] (+ add[t])
 // summed in fp32 in slot order, then the addend; both results are
 // deterministic.
+//
+// Both are bound by memory.  Measured: combine 44.5 us for the prefill layer
+// (8192 tokens, H = 3584, top-2, bf16: 294 MB, 6.6 TB/s), 76.6 us for 16384
+// tokens of which a capacity keeps 26 k of 65 k slots; dispatch 168 us for
+// 32768 tokens, H = 4096, top-2 with an addend (1.07 GB, 6.4 TB/s).
 #include "common.cuh"
 #include "internal.h"
 
@@ -21,14 +26,16 @@ namespace {
 constexpr int kThreads = 128;
 
 // kWarps warps take a token: dout is read once for its K slots, and the K
-// partial dot products are reduced over the warps in a fixed order.  KP: K
-// rounded up to 2, 4 or 8 so the slot arrays stay in registers.
+// partial dot products are reduced over the warps in a fixed order.  A token
+// without a kept slot reads no dout.  KP: K rounded up to 2, 4 or 8 so the
+// slot arrays stay in registers.  All loads of a step (kUnroll vectors of dout
+// and of every slot's row) are issued before the first is used.
 template <typename T, int KP, int kWarps>
 __global__ void __launch_bounds__(kThreads)
 combine_backward_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ y_perm,
                         const int32_t* __restrict__ pos, const float* __restrict__ w, int64_t Tn, int K,
                         int vec_per_row, uint4* __restrict__ dy_perm, float* __restrict__ dw) {
-  constexpr int V = Vec<T>::N;
+  constexpr int V = Vec<T>::N, kUnroll = KP <= 4 ? 2 : 1, kStep = 32 * kWarps;
   __shared__ float s_part[kWarps][KP];
   pdl_enter();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -37,30 +44,46 @@ combine_backward_kernel(const uint4* __restrict__ dout, const uint4* __restrict_
   const int first = kWarps == 1 ? lane : (int)threadIdx.x;
   int p[KP];
   float wt[KP], dot[KP];
+  bool any = false;
 #pragma unroll
   for (int j = 0; j < KP; ++j) {
     p[j] = j < K ? pos[t * K + j] : -1;
     wt[j] = j < K ? w[t * K + j] : 0.f;
     dot[j] = 0.f;
+    any |= p[j] >= 0;
   }
-  for (int v = first; v < vec_per_row; v += 32 * kWarps) {
-    float g[V];
-    Vec<T>::unpack(__ldcs(dout + t * vec_per_row + v), g);
+  const int end = any ? vec_per_row : 0;
+  for (int v0 = first; v0 < end; v0 += kStep * kUnroll) {
+    uint4 gr[kUnroll], yr[kUnroll][KP];
 #pragma unroll
-    for (int j = 0; j < KP; ++j) {
-      if (p[j] < 0) continue;
-      const int64_t at = (int64_t)p[j] * vec_per_row + v;
-      if (dw) {
-        float y[V];
-        Vec<T>::unpack(__ldcs(y_perm + at), y);
+    for (int u = 0; u < kUnroll; ++u) {
+      const int v = v0 + u * kStep;
+      if (v < end) gr[u] = __ldcs(dout + t * vec_per_row + v);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dot[j] = fmaf(g[i], y[i], dot[j]);
-      }
-      if (dy_perm) {
-        float d[V];
+      for (int j = 0; j < KP; ++j)
+        if (dw && p[j] >= 0 && v < end) yr[u][j] = __ldcs(y_perm + (int64_t)p[j] * vec_per_row + v);
+    }
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = wt[j] * g[i];
-        dy_perm[at] = Vec<T>::pack(d);
+    for (int u = 0; u < kUnroll; ++u) {
+      const int v = v0 + u * kStep;
+      if (v >= end) break;
+      float g[V];
+      Vec<T>::unpack(gr[u], g);
+#pragma unroll
+      for (int j = 0; j < KP; ++j) {
+        if (p[j] < 0) continue;
+        if (dw) {
+          float y[V];
+          Vec<T>::unpack(yr[u][j], y);
+#pragma unroll
+          for (int i = 0; i < V; ++i) dot[j] = fmaf(g[i], y[i], dot[j]);
+        }
+        if (dy_perm) {
+          float d[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) d[i] = wt[j] * g[i];
+          __stcs(dy_perm + (int64_t)p[j] * vec_per_row + v, Vec<T>::pack(d));
+        }
       }
     }
   }
