@@ -402,7 +402,8 @@ int moe_expert_ffn_backward(const moe_desc* desc, const void* x_perm, const void
  *   state_bits 32: m, v [n] fp32; m_scale, v_scale NULL
  *   state_bits 8: m, v [n] e4m3 codes of m and of sqrt(v); m_scale, v_scale
  *     [ceil(n / MOE_ADAMW_BLOCK)] fp32: a value is its code times the scale of
- *     its block of MOE_ADAMW_BLOCK elements.  Zeroed buffers are the start.
+ *     its block of MOE_ADAMW_BLOCK elements, which is the block's largest
+ *     magnitude / 448.  Zeroed buffers are the start.
  *   weight_decay: decoupled, for this tensor
  */
 typedef struct moe_adamw_tensor {

@@ -7,7 +7,7 @@
 //
 // 8-bit moments hold m and r = sqrt(v) (a square root halves v's exponent
 // range) as e4m3 codes: with A the largest magnitude of the 256 elements of a
-// block, code = e4m3(x 448 / A) rounded to nearest even and scale = A / 448.
+// block, code = e4m3(x (1 / A) 448) rounded to nearest even and scale = A / 448.
 // A non-zero r keeps a non-zero code (at least 2^-9), so that no element's
 // divisor falls to eps alone by rounding.  A block with A < 2^-100 is held as
 // zeros.  A block with a NaN or an infinity gets that A as its scale and codes
@@ -222,7 +222,7 @@ __device__ __forceinline__ void encode(const float* x, uint8_t* codes, float* sc
   const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // as bits: NaN > infinity > finite
   const float A = __uint_as_float(bits);
   const bool finite = bits < kInfBits, big = bits >= kTinyBits && finite;
-  const float inv = big ? __fdiv_rn(448.f, A) : 0.f;
+  const float inv = big ? __fmul_rn(__frcp_rn(A), 448.f) : 0.f;
   const float least = big ? 0.001953125f : 0.f;   // 2^-9, the smallest code
   float y[kPer];
 #pragma unroll

@@ -379,7 +379,7 @@ def encode(x, keep_non_zero):
     top = np.abs(b).max(1)
     big = top >= f32(2.0 ** -100)
     with np.errstate(divide="ignore", over="ignore", invalid="ignore"):
-        inv = np.where(big, f32(448) / top, f32(0)).astype(f32)
+        inv = np.where(big, (f32(1) / top) * f32(448), f32(0)).astype(f32)
         y = (b * inv[:, None]).astype(f32)
     y = np.where(big[:, None], y, f32(0))
     if keep_non_zero:
