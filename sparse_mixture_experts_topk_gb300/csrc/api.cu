@@ -795,9 +795,10 @@ namespace {
 bool backward_on_tensor_cores(const moe_desc& d) { return d.dtype == MOE_BF16 && !(d.flags & MOE_FLAG_SIMT_FFN); }
 
 // The backward workspace: error word | da (fp32 on CUDA cores, else bf16) |
-// tensor cores: dh (fp32), partial sums of da for db1, the experts' tails.
+// tensor cores: dh of the tiles at hand, partial sums of da for db1, the
+// experts' tails.
 struct BackwardLayout {
-  size_t err, da, dh, part, tails, total;
+  size_t err, da, stash, part, tails, total;
   int64_t rows;
 };
 
@@ -814,7 +815,7 @@ BackwardLayout backward_layout(const moe_desc& d) {
   const size_t N = (size_t)d.F * ((d.flags & MOE_FLAG_SWIGLU) ? 2 : 1);
   L.err = take(256);
   L.da = take((size_t)L.rows * N * (tc ? 2 : 4));
-  L.dh = take(tc ? backward_dh_floats(L.rows, d.E, d.F) * 4 : 0);
+  L.stash = take(tc ? backward_stash_floats() * 4 : 0);
   L.part = take(tc ? (size_t)backward_blocks(L.rows, d.E) * 8 * N * 4 : 0);
   L.tails = take(tc ? backward_tail_bytes(d.E, d.H, (int)N, d.F) : 0);
   L.total = off;
@@ -846,7 +847,7 @@ int moe_expert_ffn_backward(const moe_desc* desc, const void* x_perm, const void
   const FfnBackward b{x_perm, h_perm, dy_perm, offs, W1, b1, W2, dx_perm, dW1, db1, dW2, db2};
   cudaStream_t st = (cudaStream_t)stream;
   if (backward_on_tensor_cores(d))
-    return cuda_status(launch_ffn_backward_tc(shape_of(d), L.rows, b, at<void>(ws, L.da), at<float>(ws, L.dh),
+    return cuda_status(launch_ffn_backward_tc(shape_of(d), L.rows, b, at<void>(ws, L.da), at<float>(ws, L.stash),
                                               at<float>(ws, L.part), at<void>(ws, L.tails), at<int>(ws, L.err), st));
   return cuda_status(launch_ffn_backward_simt(shape_of(d), L.rows, b, at<float>(ws, L.da), st));
 }

@@ -4,39 +4,42 @@
 //
 // For expert e and its rows r (formulas as in ffn_backward_simt.cu):
 //   dh = dy W2[e]           [rows, F]    tokens K-major, weights read along their rows
-//   a  = x W1[e]^T (+ b1)   [rows, G F]  both K-major; the epilogue reads dh and writes da
+//   a  = x W1[e]^T (+ b1)   [rows, G F]  both K-major
 //   dx = da W1[e]           [rows, H]    tokens K-major, weights read along their rows
 //   dW1[e] = da^T x, dW2[e] = dy^T h     reduction over the rows, both operands read along their rows
 // Nothing is transposed in memory: an operand whose reduction index runs
 // along the rows of its matrix ("MN-major") is staged as it lies, and the MMA
 // descriptors say so.
 //
-// dh goes through fp32 scratch between its product and the one that uses it,
-// tile by tile in the order in which the epilogue's threads hold it, so that
-// every access of a warp is 512 bytes in a row.
-// Computing both products of a da tile together would spare that traffic
-// (4 bytes a value, written and read once), but two accumulators of 256
-// columns fill TMEM, so the epilogue could not overlap the next tile, and two
-// of 128 columns would raise the operand bytes per MMA by half, which bounds
-// a tile already.  da is rounded to bf16, as an operand of the next products.
+// Three launches.  (1) da: a pair computes a tile of dh and then the same
+// tile of a (with SwiGLU its two halves, gate and up side by side), and the
+// epilogue of the second turns both into da, rounded to bf16 as an operand of
+// what follows.  dh waits in a scratch of 128 KB for each CTA, where every
+// thread reads back what it wrote itself: it stays in L2 and needs no
+// synchronisation.  (Both accumulators of a tile side by side would fill TMEM,
+// and no epilogue could overlap the next tile; through memory, with a launch
+// for each product, the two took 435 us instead of @H@ at the prefill layer.)
+// (2) The smaller work: see Extras.  (3) dx, dW1 and dW2, which need nothing of
+// one another, the long tiles of dx first.
 //
-// Rows kernel (dh, da, dx).  A block of 256 rows has its rows on the MMA's M
+// Row products (dh, a, dx).  A block of 256 rows has its rows on the MMA's M
 // side; an expert's last block of at most 128 rows runs swapped (256 weight
 // columns on M, the rows on N rounded up to 16), so that few rows do not cost
-// a full tile.  Weights kernel (dW1, dW2): the reduction runs over an
-// expert's rows in blocks of 64, 16 to an MMA.  The rows that do not fill a
-// group of 16 come from copies of them, padded with zeros to 16, that a small
-// kernel makes first: in place the group goes on with rows of the next expert
-// or with memory that nobody wrote, in both operands, and 0 x NaN is NaN.
-// (Zeroing those rows in shared memory was measured: the second CTA's zeroing
-// has to reach the MMA thread through a release and an acquire at cluster
-// scope, 2300 cycles of a tile's 4300.)
+// a full tile (not with SwiGLU, where a tile pairs gate with up columns).
+// Weight products: the reduction runs over an expert's rows in blocks of 64,
+// 16 to an MMA.  The rows that do not fill a group of 16 come from copies of
+// them, padded with zeros to 16, that the second launch makes: in place the
+// group goes on with rows of the next expert or with memory that nobody wrote,
+// in both operands, and 0 x NaN is NaN.  (Zeroing those rows in shared memory
+// was measured: the second CTA's zeroing has to reach the MMA thread through a
+// release and an acquire at cluster scope, 2300 cycles of a tile's 4300.)
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader CTA of the
-// pair), warps 2-9 epilogue.  Two epilogue warps share a quarter of the TMEM lanes and halve its columns: with
-// one, the slopes of a da tile took longer than its MMAs.  Every wait
-// is bounded: on expiry the kernel records a timeout in the workspace's error
-// word, drains what it has in flight, frees its tensor memory and returns.
+// pair), warps 2-9 epilogue.  Two epilogue warps share a quarter of the TMEM
+// lanes and halve its columns: with one, the slopes of a da tile took longer
+// than its MMAs.  Tiles go round the pairs by number.  Every wait is bounded:
+// on expiry the kernel records a timeout in the workspace's error word, drains
+// what it has in flight, frees its tensor memory and returns.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
@@ -51,6 +54,7 @@ namespace {
 constexpr int kBM = 128;                  // operand rows (or columns) per CTA: the pair covers 256
 constexpr int kTile = 2 * kBM;            // rows and columns of a pair's tile
 constexpr int kBK = 64;                   // reduction elements per stage
+constexpr int kGroup = 16;                // reduction elements per MMA
 constexpr int kBoxRows = 32;              // swapped: token rows per box
 constexpr int kSwapRows = 128;            // a last block of at most this many rows runs swapped
 constexpr int kOperand = kBM * kBK * 2;   // bytes of one operand in a stage
@@ -59,12 +63,12 @@ constexpr int kStageBytes = 2 * kOperand;
 constexpr int kStages = 6;
 constexpr int kTmemCols = 512;            // two accumulators of 256 columns
 constexpr int kEpiWarps = 8;              // per CTA: two for each quarter of the TMEM lanes
-constexpr int kStoreBytes = 32 * 128;     // weights kernel: an epilogue warp's 32 rows of 64 columns
-constexpr size_t kSmemRows = 1024 + (size_t)kStages * kStageBytes, kSmemWeights = kSmemRows + kEpiWarps * kStoreBytes;
+constexpr int kStoreBytes = 32 * 128;     // an epilogue warp's 32 rows of 64 columns on their way to TMA
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * kStoreBytes;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kMaxPairs = 80;             // bounds the dh scratch: 128 KB for each CTA
+constexpr int kStash = kBM * kTile;       // its fp32 values
 constexpr uint64_t kWaitNs = 2000000000ull;
-
-enum Product { kDh, kDaGelu, kDaSwiglu, kDx };
 
 // Shared-memory descriptor of an MN-major operand of 128 x 64: two boxes (64
 // columns of 128 bytes, 64 rows, 128-byte swizzle) one after the other.
@@ -82,21 +86,15 @@ constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;   // instruction desc
 // 16 reduction elements on: along a K-major row, or two groups of 8 rows
 constexpr int kStepK = 32, kStepMN = 2048;
 
-// Per-expert tile counts' prefix into tstart [E + 1] and a copy of offs; one warp.
+// Per-expert tile counts' prefix into tstart [E + 1]; one warp.
 template <typename Count>
-__device__ __forceinline__ void tile_table(const int32_t* __restrict__ offs, int E, int lane, int* s_offs, int* tstart,
+__device__ __forceinline__ void tile_table(const int32_t* __restrict__ offs, int E, int lane, int* tstart,
                                            Count count) {
   int loc[8], sum = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int e = lane * 8 + i;
-    loc[i] = 0;
-    if (e < E) {
-      const int o0 = offs[e], o1 = offs[e + 1];
-      loc[i] = count(o1 - o0);
-      s_offs[e] = o0;
-      if (e == E - 1) s_offs[E] = o1;
-    }
+    loc[i] = e < E ? count(offs[e + 1] - offs[e]) : 0;
     sum += loc[i];
   }
   int incl = sum;
@@ -132,22 +130,6 @@ __device__ __forceinline__ void advance(int& stage, uint32_t& phase) {
   }
 }
 
-// What the rows kernel's epilogue reads and writes.
-struct RowsOut {
-  float* dh;            // kTile x kTile fp32 for each dh tile (see dh_at): written by kDh, read by kDa*
-  bf16* da;             // [rows, G F]
-  bf16* dx;             // [rows, H]
-  const float* bias;    // b1 or null
-  float* part;          // [blocks * 8, G F] partial sums of da over rows, or null
-  bool sectors;         // what this product writes has rows that start on 32 bytes
-};
-
-// Where a dh tile holds row r, column f: 32 x 32 blocks, in each of them the
-// 32 rows' first four columns, then the next four, ...
-__device__ __forceinline__ int dh_at(int r, int f) {
-  return ((r >> 5) * (kTile / 32) + (f >> 5)) * 1024 + ((f & 31) >> 2) * 128 + (r & 31) * 4 + (f & 3);
-}
-
 // Sum over the warp's lanes of 32 values each: lane l returns the sum of v[l].
 __device__ __forceinline__ float column_sum(float* v, int lane) {
 #pragma unroll
@@ -179,136 +161,6 @@ __device__ __forceinline__ void store_row(T* dst, const float* v, int n, bool se
   }
 }
 
-// One tile of the rows kernel, this warp's half of it.  Row orientation: this
-// thread's row, 32 columns at a time, the tile's left or right half.  Swapped:
-// this thread's column, every other group of 32 rows.  dh: the dh tile of
-// these rows, f0 this tile's first column in it.
-template <int kKind>
-__device__ __forceinline__ void rows_epilogue(uint32_t tbase, bool swap, int e, int row_base, int nrows, int n0,
-                                              int block, float* dh, int f0, int rank, int q, int half, int lane,
-                                              int N, const RowsOut& o) {
-  constexpr bool kSwi = kKind == kDaSwiglu, kDa = kKind == kDaGelu || kSwi;
-  constexpr int kOut = kSwi ? kBM : kTile;
-  const int wide = kSwi ? 2 * N : N;     // columns of da and of the bias
-  const float* be = kDa && o.bias ? o.bias + (int64_t)e * wide : nullptr;
-  if (swap) {
-    const int f = n0 + rank * kBM + q * 32 + lane;
-    const bool ok = f < N;
-    const float bf = be && ok ? be[f] : 0.f;
-    float sum = 0.f;
-#pragma unroll 1
-    for (int c = half; c * 32 < nrows; c += 2) {
-      const int64_t at = (int64_t)(row_base + c * 32) * N + f;
-      const int left = ok ? nrows - c * 32 : 0;
-      float* dt = dh + dh_at(c * 32, f0 + rank * kBM + q * 32 + lane);   // row c * 32 + j at + 4 j
-      float g[kDa ? 32 : 1];
-      if (kDa) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) g[j % (kDa ? 32 : 1)] = j < left ? __ldcs(dt + 4 * j) : 0.f;
-      }
-      uint32_t r[32];
-      tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
-      tc::tmem_wait_ld();
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        if (j < left) {
-          const float v = __uint_as_float(r[j]);
-          if (kKind == kDh) {
-            dt[4 * j] = v;
-          } else if (kKind == kDx) {
-            o.dx[at + (int64_t)j * N] = __float2bfloat16_rn(v);
-          } else {
-            const float d = g[j % (kDa ? 32 : 1)] * gelu_slope_fast(v + bf);
-            sum += d;
-            o.da[at + (int64_t)j * N] = __float2bfloat16_rn(d);
-          }
-        }
-      }
-    }
-    if (kDa && o.part && ok) o.part[((int64_t)block * 8 + half) * wide + f] = sum;
-    return;
-  }
-  const int r0 = rank * kBM + q * 32;          // this warp's first row of the block
-  const int64_t row = row_base + r0 + lane;
-  const bool ok = r0 + lane < nrows;
-#pragma unroll 1
-  for (int c = half * (kOut / 64); c < (half + 1) * (kOut / 64); ++c) {
-    const int col = n0 + c * 32;
-    if (col >= N) break;
-    const int left = min(32, N - col);     // a multiple of 8
-    float4* dt = reinterpret_cast<float4*>(dh + dh_at(r0 + lane, f0 + c * 32));   // columns 4 g .. 4 g + 3 at + 32 g
-    float4 d[kDa ? 8 : 1];
-    if (kDa) {
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        d[g % (kDa ? 8 : 1)] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ok && g * 4 < left) d[g % (kDa ? 8 : 1)] = __ldcs(dt + 32 * g);
-      }
-    }
-    uint32_t r[32], u[kSwi ? 32 : 1];
-    tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
-    if (kSwi) tc::tmem_ld_32x32b_x32(tbase + kBM + c * 32, u);
-    tc::tmem_wait_ld();
-    float v[32];
-    if (!kDa) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-      if (kKind == kDh) {
-#pragma unroll
-        for (int g = 0; g < 8; ++g)
-          if (ok && g * 4 < left) dt[32 * g] = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
-      } else if (ok) {
-        store_row(o.dx + row * N + col, v, left, o.sectors);
-      }
-    } else {
-      float w[kSwi ? 32 : 1];
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        float ba[4] = {0.f, 0.f, 0.f, 0.f}, bb[4] = {0.f, 0.f, 0.f, 0.f};
-        if (be && g * 4 < left) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            ba[i] = be[col + g * 4 + i];
-            if (kSwi) bb[i] = be[N + col + g * 4 + i];
-          }
-        }
-        const float4 dg = d[g % (kDa ? 8 : 1)];
-        const float dh[4] = {dg.x, dg.y, dg.z, dg.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = g * 4 + i;
-          const float a = __uint_as_float(r[j]) + ba[i];
-          if (kSwi)
-            swiglu_gradient_fast(a, __uint_as_float(u[j % (kSwi ? 32 : 1)]) + bb[i], dh[i], &v[j],
-                            &w[j % (kSwi ? 32 : 1)]);
-          else
-            v[j] = dh[i] * gelu_slope_fast(a);
-        }
-      }
-      if (ok) {
-        store_row(o.da + row * wide + col, v, left, o.sectors);
-        if (kSwi) store_row(o.da + row * wide + N + col, w, left, o.sectors);
-      }
-      if (o.part) {
-        // rows past the block's end and columns past N are other data: they count as zeros
-        const int64_t p = ((int64_t)block * 8 + rank * 4 + q) * wide + col + lane;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (!ok || j >= left) {
-            v[j] = 0.f;
-            if (kSwi) w[j % (kSwi ? 32 : 1)] = 0.f;
-          }
-        const float s = column_sum(v, lane);
-        if (lane < left) o.part[p] = s;
-        if (kSwi) {
-          const float s2 = column_sum(w, lane);
-          if (lane < left) o.part[p + N] = s2;
-        }
-      }
-    }
-  }
-}
-
 __device__ __forceinline__ int row_blocks(int rows) { return (rows + kTile - 1) / kTile; }
 
 // Barriers of a CTA: full and empty per stage, full and empty per accumulator, the end.
@@ -326,189 +178,6 @@ __device__ __forceinline__ void give_up(int* err, volatile int* abort) {
   *abort = 1;
 }
 
-// tmX, tmXs: token rows [rows, K] in boxes of 128 and 32 rows.  tmW: weights
-// K-major [E N, K] (kDa*) or [E, K, N] in 64 x 64 boxes (kDh, kDx).
-template <int kKind>
-__global__ void __launch_bounds__(kThreads, 1)
-backward_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
-                     const __grid_constant__ CUtensorMap tmW, const int32_t* __restrict__ offs, int E, int N, int K,
-                     RowsOut out, int* err) {
-  constexpr bool kSwi = kKind == kDaSwiglu, kMN = kKind == kDh || kKind == kDx;
-  constexpr int kOut = kSwi ? kBM : kTile;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_offs[257], s_tstart[257];
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
-  const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sB = sA + kStages * kOperand;
-  const Bars bar{tc::smem_u32(s_bar)};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)tc::cluster_ctarank();
-  const int nt = (N + kOut - 1) / kOut, nk = (K + kBK - 1) / kBK;
-
-  if (warp == 0) {
-    pdl_enter();
-    tile_table(offs, E, lane, s_offs, s_tstart, [&](int rows) { return row_blocks(rows) * nt; });
-    if (lane == 0) {
-      for (int s = 0; s < kStages; ++s) {
-        tc::mbar_init(bar.full(s), 1);
-        tc::mbar_init(bar.empty(s), 1);
-      }
-      for (int a = 0; a < 2; ++a) {
-        tc::mbar_init(bar.tfull(a), 1);
-        tc::mbar_init(bar.tempty(a), 2 * 32 * kEpiWarps);
-      }
-      tc::mbar_init(bar.done(), 1);
-      s_abort = 0;
-      tc::fence_barrier_init();
-      tc::fence_proxy_async_smem();
-      tc::prefetch_tmap(&tmX);
-      tc::prefetch_tmap(&tmXs);
-      tc::prefetch_tmap(&tmW);
-    }
-  } else if (warp == 1) {
-    tc::tmem_alloc_pair(tc::smem_u32(&s_tmem), kTmemCols);
-    tc::tmem_relinquish_pair();
-  }
-  tc::tc_fence_before();
-  __syncthreads();
-  tc::cluster_sync();
-  tc::tc_fence_after();
-  if (warp != 0) pdl_wait();
-  const uint32_t tmem = s_tmem;
-  const int total = s_tstart[E], first = blockIdx.x / 2, step = gridDim.x / 2;
-
-  struct Tile {
-    int e, row_base, nrows, mma_n, n0, block, dh_tile;
-    bool swap;
-  };
-  const int dh_nt = (N + kTile - 1) / kTile;   // kDh, kDa*: N = F
-  auto decode = [&](int t) {
-    Tile d;
-    d.e = expert_of(s_tstart, E, t);
-    const int mt = row_blocks(s_offs[d.e + 1] - s_offs[d.e]);
-    const int local = t - s_tstart[d.e], rb = local % mt;
-    d.row_base = s_offs[d.e] + rb * kTile;
-    d.nrows = min(kTile, s_offs[d.e + 1] - d.row_base);
-    d.swap = !kSwi && d.nrows <= kSwapRows;
-    d.mma_n = d.swap ? (d.nrows + 15) / 16 * 16 : kTile;
-    d.n0 = (local / mt) * kOut;
-    d.block = (s_offs[d.e] >> 8) + d.e + rb;
-    d.dh_tile = s_tstart[d.e] / nt * dh_nt + d.n0 / kTile * mt + rb;
-    return d;
-  };
-
-  uint32_t filled = 0, fill_par = 0;
-  bool producer = false;
-  if (warp == 0) {
-    if (tc::elect_one()) {
-      producer = true;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = first; t < total && ok; t += step) {
-        const Tile d = decode(t);
-        const int half = d.mma_n / 2, nbox = d.swap ? (half + kBoxRows - 1) / kBoxRows : 0;
-        const uint32_t tx = 2u * (uint32_t)(kOperand + (d.swap ? nbox * kBoxRows * 128 : kOperand));
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!tc::mbar_wait(bar.empty(stage), phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
-          const uint32_t fbar = tc::map_peer(bar.full(stage), 0);
-          if (rank == 0) tc::mbar_arrive_expect_tx(bar.full(stage), tx);
-          const uint32_t tok = (d.swap ? sB : sA) + stage * kOperand, wgt = (d.swap ? sA : sB) + stage * kOperand;
-          const int n = d.n0 + rank * kBM;
-          if (kMN) {
-            tc::tma_load_3d_pair(wgt, &tmW, fbar, n, kb * kBK, d.e);
-            tc::tma_load_3d_pair(wgt + kHalf, &tmW, fbar, n + 64, kb * kBK, d.e);
-          } else {
-            tc::tma_load_2d_pair(wgt, &tmW, fbar, kb * kBK, kSwi ? (2 * d.e + rank) * N + d.n0 : d.e * N + n);
-          }
-          if (d.swap) {
-            for (int i = 0; i < nbox; ++i)
-              tc::tma_load_2d_pair(tok + i * kBoxRows * 128, &tmXs, fbar, kb * kBK,
-                                   d.row_base + rank * half + i * kBoxRows);
-          } else {
-            tc::tma_load_2d_pair(tok, &tmX, fbar, kb * kBK, d.row_base + rank * kBM);
-          }
-          filled |= 1u << stage;
-          fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
-          advance(stage, phase);
-        }
-      }
-      if (!ok) give_up(err, &s_abort);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (rank == 0 && tc::elect_one()) {
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int t = first; t < total && ok; t += step) {
-        const Tile d = decode(t);
-        const uint32_t idesc = tc::idesc_bf16_f32(kTile, d.mma_n) | (kMN ? (d.swap ? kMajorA : kMajorB) : 0u);
-        if (!tc::mbar_wait(bar.tempty(acc), acc_phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
-        tc::tc_fence_after();
-        const uint32_t dst = tmem + (uint32_t)(acc * kTile);
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!tc::mbar_wait(bar.full(stage), phase, &s_abort, kWaitNs)) { ok = false; break; }
-          tc::tc_fence_after();
-          const uint32_t a0 = sA + stage * kOperand, b0 = sB + stage * kOperand;
-#pragma unroll
-          for (int k = 0; k < kBK / 16; ++k) {
-            uint64_t da, db;
-            if (kMN && d.swap) da = sdesc_mn128(a0 + k * kStepMN);
-            else da = tc::sdesc_k128(a0 + k * kStepK);
-            if (kMN && !d.swap) db = sdesc_mn128(b0 + k * kStepMN);
-            else db = tc::sdesc_k128(b0 + k * kStepK);
-            tc::mma_bf16_pair(dst, da, db, idesc, (kb | k) != 0);
-          }
-          tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
-          advance(stage, phase);
-        }
-        if (!ok) break;
-        tc::tc_commit_pair_mc(bar.tfull(acc), 0x3);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
-      }
-      if (!ok) give_up(err, &s_abort);
-      tc::tc_commit_pair_mc(bar.done(), 0x3);   // both CTAs learn when every MMA has finished
-    }
-    __syncwarp();
-    if (lane == 0 && !tc::mbar_wait(bar.done(), 0, nullptr, kWaitNs)) set_error(err, kDevTimeout);
-    __syncwarp();
-  } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;   // TMEM lanes 32 q .. 32 q + 31 belong to this warp
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int t = first; t < total; t += step) {
-      const Tile d = decode(t);
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.tfull(acc), acc_phase, &s_abort, kWaitNs))) {
-        give_up(err, &s_abort);
-        break;
-      }
-      tc::tc_fence_after();
-      rows_epilogue<kKind>(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile), d.swap, d.e, d.row_base,
-                           d.nrows, d.n0, d.block, out.dh + (int64_t)d.dh_tile * kTile * kTile, d.n0 % kTile, rank, q, half,
-                           lane, N, out);
-      tc::tc_fence_before();
-      if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
-      else tc::mbar_arrive_remote(tc::map_peer(bar.tempty(acc), 0));
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
-    }
-  }
-  tc::tc_fence_before();
-  __syncthreads();
-  if (producer && rank == 0 && s_abort)
-    for (int s = 0; s < kStages; ++s)
-      if ((filled >> s) & 1u) tc::mbar_wait(bar.full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
-  tc::cluster_sync();   // neither CTA leaves while the other may still signal it
-  if (warp == 1) {
-    tc::tc_fence_after();
-    tc::tmem_dealloc_pair(tmem, kTmemCols);
-  }
-}
-
 // What is left of the smaller work, in one launch beside one another.
 //
 // Tails: the rows of each expert past its last whole group of 16, padded with
@@ -518,7 +187,7 @@ struct Operand {
   uint4* tails;
   int vec;              // 16-byte vectors in a row
 };
-constexpr int kTailRows = 16, kTailSplit = 4;   // blocks for an expert's tail of one operand
+constexpr int kTailSplit = 4;   // blocks for an expert's tail of one operand
 constexpr int kRedCols = 32, kRedGroups = 8, kSumVecs = 8, kSumGroups = 32;
 struct Extras {
   Operand o[4];
@@ -534,14 +203,14 @@ struct Extras {
 
 // One expert's rows past its last whole group of 16, a quarter of them.
 __device__ __forceinline__ void copy_tail(const Operand& o, const int32_t* __restrict__ offs, int e, int part) {
-  const int r0 = offs[e], rows = offs[e + 1] - r0, whole = rows / kTailRows * kTailRows;
+  const int r0 = offs[e], rows = offs[e + 1] - r0, whole = rows / kGroup * kGroup;
   if (rows == whole) return;   // no tail: never read
-  const int per = kTailRows / kTailSplit * o.vec;
+  const int per = kGroup / kTailSplit * o.vec;
   for (int i = threadIdx.x; i < per; i += blockDim.x) {
-    const int r = part * (kTailRows / kTailSplit) + i / o.vec, v = i % o.vec;
+    const int r = part * (kGroup / kTailSplit) + i / o.vec, v = i % o.vec;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (whole + r < rows) x = o.rows[(int64_t)(r0 + whole + r) * o.vec + v];
-    o.tails[((int64_t)e * kTailRows + r) * o.vec + v] = x;
+    o.tails[((int64_t)e * kGroup + r) * o.vec + v] = x;
   }
 }
 
@@ -609,27 +278,240 @@ backward_extras_kernel(const __grid_constant__ Extras x, const int32_t* __restri
   }
 }
 
-// One weight gradient: out [E, M, N] = sum over an expert's rows of A's row
-// (M columns) times B's row (N columns).
-struct WeightProduct {
-  int M, N;
+// The kernels: da of GELU or SwiGLU experts, or the gradients that need it.
+enum Job { kDaGelu, kDaSwiglu, kGradients };
+
+struct Params {
+  // kDa*: dy and x rows (boxes of 128 and of 32 rows), W2 [E, H, F], W1 [E G F, H]
+  // kGradients: da rows (128, 32), W1 [E, G F, H]; the operands of dW1 and dW2
+  // (A, B, and their tails in boxes of 16 rows); dW1 and dW2 (boxes of 32 rows)
+  CUtensorMap map[13];
+  const int32_t* offs;
+  int E, H, F, N;          // N = G F
+  float* stash;            // kDa*: dh of the tile at hand, kStash for each CTA
+  bf16* da;                // [rows, N]
+  const float* b1;         // [E, N] or null
+  float* part;             // [blocks * 8, N] partial sums of da over rows, or null
+  bf16* dx;                // [rows, H] or null
+  int wm[2], wn[2];        // the weight products' M and N, 0 for none
+  bool sectors;            // the rows of da or dx start on 32 bytes
+  int* err;
+};
+enum Map { kDy = 0, kDyBox, kW2, kX, kXBox, kW1, kDaRows = 0, kDaBox, kW1MN, kWeightMaps, kOutMaps = 11 };
+
+// A tile: a row product's (expert e, rows row0 .. row0 + nrows, columns n0 ..),
+// or a weight product's (p, rows m0 .., columns n0 ..).
+struct Tile {
+  int e, row0, nrows, n0, block, m0, p;
+  bool rows, swap;
 };
 
-// tmA, tmB: an operand's rows in boxes of 64 x 64; tmAt, tmBt: its tails in
-// boxes of 64 columns x 16 rows; tmO: out in boxes of 32 rows x 64 columns.
-// Products 0 and 1 follow one another.  An accumulator leaves through shared
-// memory by TMA: stored by its threads, a row each, it took 594 us instead of
-// 440 at the prefill layer with 16 bytes a store (450 with 32, which needs
-// rows that start on 32 bytes).
-__global__ void __launch_bounds__(kThreads, 1)
-backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
-                        const __grid_constant__ CUtensorMap tmAt0, const __grid_constant__ CUtensorMap tmBt0,
-                        const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
-                        const __grid_constant__ CUtensorMap tmAt1, const __grid_constant__ CUtensorMap tmBt1,
-                        const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
-                        const int32_t* __restrict__ offs, int E, WeightProduct P0, WeightProduct P1, int* err) {
+// This thread's dh values, in groups of four: group k at [32 k].
+__device__ __forceinline__ float4* stash_of(float* stash, int epi_warp, int lane) {
+  return reinterpret_cast<float4*>(stash + (int64_t)blockIdx.x * kStash) + epi_warp * 32 * 32 + lane;
+}
+
+// The i-th of the four groups of 32 columns that an epilogue warp has of a dh
+// tile.  SwiGLU: two of each half of the tile, those that it will have of
+// that half's gate and up columns.
+template <bool kSwi>
+__device__ __forceinline__ int dh_chunk(int i, int half) {
+  return kSwi ? (i >> 1) * 4 + half * 2 + (i & 1) : half * 4 + i;
+}
+
+// dh of a tile: from the accumulator to this thread's scratch.
+template <bool kSwi>
+__device__ __forceinline__ void stash_dh(uint32_t tbase, const Tile& d, int half, int F, float4* st) {
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const int c = d.swap ? half + 2 * i : dh_chunk<kSwi>(i, half);
+    if (d.swap ? c * 32 >= d.nrows : d.n0 + c * 32 >= F) continue;
+    uint32_t r[32];
+    tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      st[(i * 8 + g) * 32] = make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
+                                         __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
+  }
+}
+
+// da of a GELU tile that runs swapped: this thread's column, every other group of 32 rows.
+__device__ __forceinline__ void da_swapped(uint32_t tbase, const Tile& d, int rank, int q, int half, int lane,
+                                           const Params& P, const float4* st) {
+  const int f = d.n0 + rank * kBM + q * 32 + lane;
+  const bool ok = f < P.F;
+  const float bf = P.b1 && ok ? P.b1[(int64_t)d.e * P.F + f] : 0.f;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int i = 0; (half + 2 * i) * 32 < d.nrows; ++i) {
+    const int c = half + 2 * i, left = ok ? d.nrows - c * 32 : 0;
+    float4 dh[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) dh[g] = __ldcg(st + (i * 8 + g) * 32);
+    uint32_t r[32];
+    tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
+    tc::tmem_wait_ld();
+    bf16* out = P.da + (int64_t)(d.row0 + c * 32) * P.F + f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float4 v = dh[j >> 2];
+      const float h = (j & 3) == 0 ? v.x : (j & 3) == 1 ? v.y : (j & 3) == 2 ? v.z : v.w;
+      if (j < left) {
+        const float g = h * gelu_slope_fast(__uint_as_float(r[j]) + bf);
+        sum += g;
+        out[(int64_t)j * P.F] = __float2bfloat16_rn(g);
+      }
+    }
+  }
+  if (P.part && ok) P.part[((int64_t)d.block * 8 + half) * P.F + f] = sum;
+}
+
+// da of a tile in row orientation: this thread's row, 32 columns at a time.
+// SwiGLU: `sub` is the half of the dh tile whose gate and up columns the
+// accumulator holds.
+template <bool kSwi>
+__device__ __forceinline__ void da_rows(uint32_t tbase, const Tile& d, int sub, int rank, int q, int half, int lane,
+                                        const Params& P, const float4* st) {
+  const int F = P.F, r0 = rank * kBM + q * 32;
+  const int64_t row = d.row0 + r0 + lane;
+  const bool ok = r0 + lane < d.nrows;
+  const float* be = P.b1 ? P.b1 + (int64_t)d.e * P.N : nullptr;
+#pragma unroll 1
+  for (int k = 0; k < (kSwi ? 2 : 4); ++k) {
+    const int i = kSwi ? sub * 2 + k : k, c = dh_chunk<kSwi>(i, half);   // of the dh tile
+    const int acc = kSwi ? c - sub * 4 : c;                               // of the accumulator
+    const int col = d.n0 + c * 32;
+    if (col >= F) break;
+    const int left = min(32, F - col);     // a multiple of 8
+    float4 dh[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) dh[g] = __ldcg(st + (i * 8 + g) * 32);
+    uint32_t r[32], u[kSwi ? 32 : 1];
+    tc::tmem_ld_32x32b_x32(tbase + acc * 32, r);
+    if (kSwi) tc::tmem_ld_32x32b_x32(tbase + kBM + acc * 32, u);
+    tc::tmem_wait_ld();
+    float v[32], w[kSwi ? 32 : 1];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      float ba[4] = {0.f, 0.f, 0.f, 0.f}, bb[4] = {0.f, 0.f, 0.f, 0.f};
+      if (be && g * 4 < left) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          ba[x] = be[col + g * 4 + x];
+          if (kSwi) bb[x] = be[F + col + g * 4 + x];
+        }
+      }
+      const float h[4] = {dh[g].x, dh[g].y, dh[g].z, dh[g].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int j = g * 4 + x;
+        const float a = __uint_as_float(r[j]) + ba[x];
+        if (kSwi)
+          swiglu_gradient_fast(a, __uint_as_float(u[j % (kSwi ? 32 : 1)]) + bb[x], h[x], &v[j],
+                               &w[j % (kSwi ? 32 : 1)]);
+        else
+          v[j] = h[x] * gelu_slope_fast(a);
+      }
+    }
+    if (ok) {
+      store_row(P.da + row * P.N + col, v, left, P.sectors);
+      if (kSwi) store_row(P.da + row * P.N + F + col, w, left, P.sectors);
+    }
+    if (P.part) {
+      // rows past the block's end and columns past F are other data: they count as zeros
+      const int64_t p = ((int64_t)d.block * 8 + rank * 4 + q) * P.N + col + lane;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (!ok || j >= left) {
+          v[j] = 0.f;
+          if (kSwi) w[j % (kSwi ? 32 : 1)] = 0.f;
+        }
+      const float s = column_sum(v, lane);
+      if (lane < left) P.part[p] = s;
+      if (kSwi) {
+        const float s2 = column_sum(w, lane);
+        if (lane < left) P.part[p + F] = s2;
+      }
+    }
+  }
+}
+
+// A tile of dx, in either orientation.
+__device__ __forceinline__ void dx_tile(uint32_t tbase, const Tile& d, int rank, int q, int half, int lane,
+                                        const Params& P) {
+  if (d.swap) {
+    const int f = d.n0 + rank * kBM + q * 32 + lane;
+#pragma unroll 1
+    for (int c = half; c * 32 < d.nrows; c += 2) {
+      uint32_t r[32];
+      tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
+      tc::tmem_wait_ld();
+      bf16* out = P.dx + (int64_t)(d.row0 + c * 32) * P.H + f;
+      const int left = f < P.H ? d.nrows - c * 32 : 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < left) out[(int64_t)j * P.H] = __float2bfloat16_rn(__uint_as_float(r[j]));
+    }
+    return;
+  }
+  const int r0 = rank * kBM + q * 32 + lane;
+#pragma unroll 1
+  for (int c = half * 4; c < half * 4 + 4; ++c) {
+    const int col = d.n0 + c * 32;
+    if (col >= P.H) break;
+    uint32_t r[32];
+    tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
+    tc::tmem_wait_ld();
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+    if (r0 < d.nrows) store_row(P.dx + (int64_t)(d.row0 + r0) * P.H + col, v, min(32, P.H - col), P.sectors);
+  }
+}
+
+// A tile of a weight gradient, zeros for an expert without rows.  It leaves
+// through shared memory by TMA: stored by its threads, a row each, the
+// products took 594 us instead of 440 at the prefill layer with 16 bytes a
+// store (450 with 32, which needs rows that start on 32 bytes).
+__device__ __forceinline__ void weight_tile(uint32_t tbase, const Tile& d, bool zero, int rank, int q, int half,
+                                            int lane, const Params& P, uint32_t buf, uint8_t* g) {
+  const int m = d.m0 + rank * kBM + q * 32;
+  if (m >= P.wm[d.p]) return;
+#pragma unroll 1
+  for (int c = half * 2; c < half * 2 + 2; ++c) {
+    const int n = d.n0 + c * 64;
+    if (n >= P.wn[d.p]) break;
+    if (lane == 0) tc::bulk_wait_read();   // the buffer's previous store has been read
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[32];
+      if (!zero) {
+        uint32_t r[32];
+        tc::tmem_ld_32x32b_x32(tbase + c * 64 + h * 32, r);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)   // 16 bytes at the place that the 128-byte swizzle gives them
+        *reinterpret_cast<uint4*>(g + (((h * 4 + j) ^ (lane & 7)) << 4)) = Vec<bf16>::pack(v + j * 8);
+    }
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) tc::tma_store_3d(&P.map[kOutMaps + d.p], buf, n, m, d.e);
+  }
+}
+
+template <int kJob>
+__global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid_constant__ Params P) {
+  constexpr bool kSwi = kJob == kDaSwiglu, kDa = kJob != kGradients;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_offs[257];
+  __shared__ int s_tstart[257];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
@@ -639,11 +521,12 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)tc::cluster_ctarank();
   auto tiles = [](int n) { return (n + kTile - 1) / kTile; };
-  const int per0 = tiles(P0.M) * tiles(P0.N), per1 = tiles(P1.M) * tiles(P1.N);
+  const int E = P.E, nt = kDa ? tiles(P.F) : P.dx ? tiles(P.H) : 0;   // columns of a row product's tiles
+  const int per0 = kDa ? 0 : tiles(P.wm[0]) * tiles(P.wn[0]), per1 = kDa ? 0 : tiles(P.wm[1]) * tiles(P.wn[1]);
 
   if (warp == 0) {
     pdl_enter();
-    for (int e = lane; e <= E; e += 32) s_offs[e] = offs[e];
+    tile_table(P.offs, E, lane, s_tstart, [&](int rows) { return row_blocks(rows) * nt; });
     if (lane == 0) {
       for (int s = 0; s < kStages; ++s) {
         tc::mbar_init(bar.full(s), 1);
@@ -668,209 +551,244 @@ backward_weights_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_c
   tc::tc_fence_after();
   if (warp != 0) pdl_wait();
   const uint32_t tmem = s_tmem;
-  const int total0 = E * per0, total = total0 + E * per1, first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int total_rows = s_tstart[E], total0 = total_rows + E * per0, total = total0 + E * per1;
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
-  struct Tile {
-    int p, e, m0, n0, row0, groups, nk;   // groups of 16 rows, the tail's included; stages
-    bool tail;                            // the last stage is the tail's, one group
-  };
   auto decode = [&](int t) {
-    Tile d;
-    d.p = t >= total0 ? 1 : 0;
-    const int tl = t - (d.p ? total0 : 0), per = d.p ? per1 : per0, nt = tiles(d.p ? P1.N : P0.N);
-    d.e = tl / per;
-    const int local = tl - d.e * per, mi = local / nt;
-    d.m0 = mi * kTile;
-    d.n0 = (local - mi * nt) * kTile;
-    d.row0 = s_offs[d.e];
-    const int rows = s_offs[d.e + 1] - d.row0, whole = rows / kTailRows;
-    d.tail = rows % kTailRows != 0;
-    d.nk = (whole * kTailRows + kBK - 1) / kBK + (d.tail ? 1 : 0);
-    d.groups = whole + (d.tail ? 1 : 0);
+    Tile d = {};
+    if (kDa || t < total_rows) {
+      d.rows = true;
+      d.e = expert_of(s_tstart, E, t);
+      const int r0 = P.offs[d.e], r1 = P.offs[d.e + 1], mt = row_blocks(r1 - r0);
+      const int local = t - s_tstart[d.e], col = local / mt, rb = local - col * mt;
+      d.row0 = r0 + rb * kTile;
+      d.nrows = min(kTile, r1 - d.row0);
+      d.swap = !kSwi && d.nrows <= kSwapRows;
+      d.n0 = col * kTile;
+      d.block = (r0 >> 8) + d.e + rb;
+    } else {
+      d.p = t >= total0 ? 1 : 0;
+      const int tl = t - (d.p ? total0 : total_rows), per = d.p ? per1 : per0, cols = tiles(P.wn[d.p]);
+      d.e = tl / per;
+      const int local = tl - d.e * per, mi = local / cols;
+      d.m0 = mi * kTile;
+      d.n0 = (local - mi * cols) * kTile;
+      d.row0 = P.offs[d.e];
+      d.nrows = P.offs[d.e + 1] - d.row0;
+    }
     return d;
+  };
+  // The products of a tile, one accumulator after the other (SwiGLU: dh, then
+  // a's halves as far as F goes), their stages, and the MMAs of a stage.
+  auto products = [&](const Tile& d) { return kSwi ? (P.F - d.n0 > kBM ? 3 : 2) : kDa ? 2 : 1; };
+  auto has_tail = [&](const Tile& d) { return !d.rows && d.nrows % kGroup != 0; };
+  const int row_k = kDa ? P.H : P.N;   // a row product's reduction
+  auto stages = [&](const Tile& d) {
+    return d.rows ? (row_k + kBK - 1) / kBK
+                  : (d.nrows / kGroup * kGroup + kBK - 1) / kBK + (has_tail(d) ? 1 : 0);
+  };
+  auto groups = [&](const Tile& d, int kb, int nk) {
+    if (d.rows) return min(kBK / kGroup, (row_k - kb * kBK + kGroup - 1) / kGroup);
+    if (has_tail(d) && kb == nk - 1) return 1;   // the tail's stage holds its group alone
+    return min(kBK / kGroup, d.nrows / kGroup - kb * (kBK / kGroup));
   };
 
   uint32_t filled = 0, fill_par = 0;
   bool producer = false;
   if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
     if (tc::elect_one()) {
       producer = true;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = first; t < total && ok; t += step) {
-        const Tile d = decode(t);
-        const CUtensorMap* mA = d.p ? &tmA1 : &tmA0;
-        const CUtensorMap* mB = d.p ? &tmB1 : &tmB0;
-        const int m = d.m0 + rank * kBM, n = d.n0 + rank * kBM;
-        for (int kb = 0; kb < d.nk; ++kb) {
-          if (!tc::mbar_wait(bar.empty(stage), phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
-          const uint32_t fbar = tc::map_peer(bar.full(stage), 0);
-          const bool tail = d.tail && kb == d.nk - 1;
-          int r = d.row0 + kb * kBK;
-          if (tail) {
-            mA = d.p ? &tmAt1 : &tmAt0;
-            mB = d.p ? &tmBt1 : &tmBt0;
-            r = d.e * kTailRows;
-          }
-          if (rank == 0)
-            tc::mbar_arrive_expect_tx(bar.full(stage), tail ? 2 * kStageBytes * kTailRows / kBK : 2 * kStageBytes);
-          const uint32_t a = sA + stage * kOperand, b = sB + stage * kOperand;
-          tc::tma_load_2d_pair(a, mA, fbar, m, r);
-          tc::tma_load_2d_pair(a + kHalf, mA, fbar, m + 64, r);
-          tc::tma_load_2d_pair(b, mB, fbar, n, r);
-          tc::tma_load_2d_pair(b + kHalf, mB, fbar, n + 64, r);
+      // Waits for a free stage, arms the leader's barrier for the pair's bytes
+      // and has `load` fill the stage.  The kinds of loads have loops of their
+      // own: what a stage costs this thread bounds the kernel.
+      auto fill = [&](int nk, uint32_t bytes, auto load) {
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!tc::mbar_wait(bar.empty(stage), phase ^ 1u, &s_abort, kWaitNs)) return false;
+          if (rank == 0) tc::mbar_arrive_expect_tx(bar.full(stage), bytes);
+          load(kb, sA + stage * kOperand, sB + stage * kOperand, tc::map_peer(bar.full(stage), 0));
           filled |= 1u << stage;
           fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
           advance(stage, phase);
         }
+        return true;
+      };
+      for (int t = first; t < total && ok; t += step) {
+        const Tile d = decode(t);
+        const int nk = stages(d), n = d.n0 + rank * kBM;
+        if (!d.rows) {
+          const CUtensorMap* m = &P.map[kWeightMaps + 4 * d.p];
+          const int ma = d.m0 + rank * kBM, whole = nk - (has_tail(d) ? 1 : 0);
+          auto load = [&](const CUtensorMap* op, int r, uint32_t a, uint32_t b, uint32_t fbar) {
+            tc::tma_load_2d_pair(a, op, fbar, ma, r);
+            tc::tma_load_2d_pair(a + kHalf, op, fbar, ma + 64, r);
+            tc::tma_load_2d_pair(b, op + 1, fbar, n, r);
+            tc::tma_load_2d_pair(b + kHalf, op + 1, fbar, n + 64, r);
+          };
+          ok = fill(whole, 2 * kStageBytes, [&](int kb, uint32_t a, uint32_t b, uint32_t fbar) {
+                 load(m, d.row0 + kb * kBK, a, b, fbar);
+               }) &&
+               fill(nk - whole, 2 * kStageBytes * kGroup / kBK, [&](int, uint32_t a, uint32_t b, uint32_t fbar) {
+                 load(m + 2, d.e * kGroup, a, b, fbar);
+               });
+          continue;
+        }
+        const int tokens = d.swap ? (d.nrows + 15) / 16 * 8 : kBM;   // this CTA's token rows
+        const int nbox = d.swap ? (tokens + kBoxRows - 1) / kBoxRows : 1, row = d.row0 + rank * tokens;
+        const uint32_t bytes = 2 * (kOperand + (d.swap ? nbox * kBoxRows * 128 : kOperand));
+        auto load_tokens = [&](const CUtensorMap* m, int kb, uint32_t dst, uint32_t fbar) {
+          for (int i = 0; i < nbox; ++i) tc::tma_load_2d_pair(dst + i * kBoxRows * 128, m, fbar, kb * kBK, row + i * kBoxRows);
+        };
+        // a product with the weights read along their rows (dh, dx) ...
+        const CUtensorMap* mt = &P.map[(kDa ? kDy : kDaRows) + (d.swap ? 1 : 0)];
+        const CUtensorMap* mw = &P.map[kDa ? kW2 : kW1MN];
+        ok = fill(nk, bytes, [&](int kb, uint32_t a, uint32_t b, uint32_t fbar) {
+          const uint32_t tok = d.swap ? b : a, wgt = d.swap ? a : b;
+          tc::tma_load_3d_pair(wgt, mw, fbar, n, kb * kBK, d.e);
+          tc::tma_load_3d_pair(wgt + kHalf, mw, fbar, n + 64, kb * kBK, d.e);
+          load_tokens(mt, kb, tok, fbar);
+        });
+        // ... and those with both operands K-major (a)
+        if (kDa) {
+          const CUtensorMap* mx = &P.map[kX + (d.swap ? 1 : 0)];
+          for (int sub = 1; sub < products(d) && ok; ++sub) {
+            const int wrow = kSwi ? (2 * d.e + rank) * P.F + d.n0 + (sub - 1) * kBM : d.e * P.F + n;
+            ok = fill(nk, bytes, [&](int kb, uint32_t a, uint32_t b, uint32_t fbar) {
+              tc::tma_load_2d_pair(d.swap ? a : b, &P.map[kW1], fbar, kb * kBK, wrow);
+              load_tokens(mx, kb, d.swap ? b : a, fbar);
+            });
+          }
+        }
       }
-      if (!ok) give_up(err, &s_abort);
+      if (!ok) give_up(P.err, &s_abort);
     }
     __syncwarp();
   } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader)
     if (rank == 0 && tc::elect_one()) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      const uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | kMajorA | kMajorB;
       Tile next = first < total ? decode(first) : Tile{};
       for (int t = first; t < total && ok; t += step) {
         const Tile d = next;
-        if (!tc::mbar_wait(bar.tempty(acc), acc_phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
-        tc::tc_fence_after();
-        const uint32_t dst = tmem + (uint32_t)(acc * kTile);
-        for (int kb = 0; kb < d.nk; ++kb) {
-          if (!tc::mbar_wait(bar.full(stage), phase, &s_abort, kWaitNs)) { ok = false; break; }
+        if (t + step < total) next = decode(t + step);   // beside the MMAs issued last
+        const int nk = stages(d), np = products(d), mma_n = d.swap ? (d.nrows + 15) / 16 * 16 : kTile;
+        for (int sub = 0; sub < np && ok; ++sub) {
+          const bool weights_mn = kDa ? sub == 0 : true;
+          const bool a_mn = !d.rows || (d.swap && weights_mn), b_mn = !d.rows || (!d.swap && weights_mn);
+          const uint32_t idesc = tc::idesc_bf16_f32(kTile, mma_n) | (a_mn ? kMajorA : 0u) | (b_mn ? kMajorB : 0u);
+          if (!tc::mbar_wait(bar.tempty(acc), acc_phase ^ 1u, &s_abort, kWaitNs)) { ok = false; break; }
           tc::tc_fence_after();
-          const uint32_t a0 = sA + stage * kOperand, b0 = sB + stage * kOperand;
-          // the tail's stage holds the last group alone, the one before it what is left of the whole ones
-          const bool tail = d.tail && kb == d.nk - 1;
-          const int groups = tail ? 1 : min(kBK / 16, d.groups - (d.tail ? 1 : 0) - kb * (kBK / 16));
-          for (int k = 0; k < groups; ++k)
-            tc::mma_bf16_pair(dst, sdesc_mn128(a0 + k * kStepMN), sdesc_mn128(b0 + k * kStepMN), idesc, (kb | k) != 0);
-          tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
-          advance(stage, phase);
-          if (kb == 0 && t + step < total) next = decode(t + step);   // its divisions run beside the MMAs
+          const uint32_t dst = tmem + (uint32_t)(acc * kTile);
+          // a descriptor's address is in units of 16 bytes, and no operand leaves its field
+          const uint64_t a0 = a_mn ? sdesc_mn128(sA) : tc::sdesc_k128(sA), as = (a_mn ? kStepMN : kStepK) >> 4;
+          const uint64_t b0 = b_mn ? sdesc_mn128(sB) : tc::sdesc_k128(sB), bs = (b_mn ? kStepMN : kStepK) >> 4;
+          for (int kb = 0; kb < nk; ++kb) {
+            const int ng = groups(d, kb, nk);
+            if (!tc::mbar_wait(bar.full(stage), phase, &s_abort, kWaitNs)) { ok = false; break; }
+            tc::tc_fence_after();
+            const uint64_t at = (uint64_t)(stage * (kOperand >> 4)), a = a0 + at, b = b0 + at;
+            tc::mma_bf16_pair(dst, a, b, idesc, kb != 0);
+#pragma unroll
+            for (int k = 1; k < kBK / kGroup; ++k)
+              if (k < ng) tc::mma_bf16_pair(dst, a + k * as, b + k * bs, idesc, 1);
+            tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
+            advance(stage, phase);
+          }
+          if (!ok) break;
+          tc::tc_commit_pair_mc(bar.tfull(acc), 0x3);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
         }
-        if (!ok) break;
-        tc::tc_commit_pair_mc(bar.tfull(acc), 0x3);
-        if (d.nk == 0 && t + step < total) next = decode(t + step);
+      }
+      if (!ok) give_up(P.err, &s_abort);
+      tc::tc_commit_pair_mc(bar.done(), 0x3);   // both CTAs learn when every MMA has finished
+    }
+    __syncwarp();
+    if (lane == 0 && !tc::mbar_wait(bar.done(), 0, nullptr, kWaitNs)) set_error(P.err, kDevTimeout);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3, half = (warp - 2) >> 2;   // TMEM lanes 32 q .. 32 q + 31 belong to this warp
+    const uint32_t buf = sOut + (warp - 2) * kStoreBytes;
+    uint8_t* row = smem_raw + (buf - tc::smem_u32(smem_raw)) + lane * 128;
+    float4* st = kDa ? stash_of(P.stash, warp - 2, lane) : nullptr;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step) {
+      const Tile d = decode(t);
+      const int np = products(d);
+      for (int sub = 0; sub < np; ++sub) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.tfull(acc), acc_phase, &s_abort, kWaitNs))) {
+          give_up(P.err, &s_abort);
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile);
+        if (kDa) {
+          if (sub == 0) stash_dh<kSwi>(tbase, d, half, P.F, st);
+          else if (!kSwi && d.swap) da_swapped(tbase, d, rank, q, half, lane, P, st);
+          else da_rows<kSwi>(tbase, d, sub - 1, rank, q, half, lane, P, st);
+        } else if (d.rows) {
+          dx_tile(tbase, d, rank, q, half, lane, P);
+        } else {
+          weight_tile(tbase, d, d.nrows == 0, rank, q, half, lane, P, buf, row);
+        }
+        tc::tc_fence_before();
+        if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
+        else tc::mbar_arrive_remote(tc::map_peer(bar.tempty(acc), 0));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      if (!ok) give_up(err, &s_abort);
-      tc::tc_commit_pair_mc(bar.done(), 0x3);
-    }
-    __syncwarp();
-    if (lane == 0 && !tc::mbar_wait(bar.done(), 0, nullptr, kWaitNs)) set_error(err, kDevTimeout);
-    __syncwarp();
-  } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t buf = sOut + (warp - 2) * kStoreBytes;
-    uint8_t* g = smem_raw + (buf - tc::smem_u32(smem_raw)) + lane * 128;   // this thread's row of it
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int t = first; t < total; t += step) {
-      const Tile d = decode(t);
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.tfull(acc), acc_phase, &s_abort, kWaitNs))) {
-        give_up(err, &s_abort);
-        break;
-      }
-      tc::tc_fence_after();
-      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile);
-      const int m = d.m0 + rank * kBM + q * 32;
-      if (m < (d.p ? P1.M : P0.M)) {
-#pragma unroll 1
-        for (int c = half * (kTile / 128); c < (half + 1) * (kTile / 128); ++c) {
-          const int n = d.n0 + c * 64;
-          if (n >= (d.p ? P1.N : P0.N)) break;
-          if (lane == 0) tc::bulk_wait_read();   // the buffer's previous store has been read
-          __syncwarp();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float v[32];
-            if (d.nk > 0) {
-              uint32_t r[32];
-              tc::tmem_ld_32x32b_x32(tbase + c * 64 + h * 32, r);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)   // 16 bytes at the place that the 128-byte swizzle gives them
-              *reinterpret_cast<uint4*>(g + (((h * 4 + j) ^ (lane & 7)) << 4)) = Vec<bf16>::pack(v + j * 8);
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::tma_store_3d(d.p ? &tmO1 : &tmO0, buf, n, m, d.e);
-        }
-      }
-      tc::tc_fence_before();
-      if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
-      else tc::mbar_arrive_remote(tc::map_peer(bar.tempty(acc), 0));
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
     }
     if (lane == 0) tc::bulk_wait_all();
   }
   tc::tc_fence_before();
   __syncthreads();
+  // after an abort the leader drains its stage barriers, on which both CTAs'
+  // loads complete, before either CTA may leave
   if (producer && rank == 0 && s_abort)
     for (int s = 0; s < kStages; ++s)
       if ((filled >> s) & 1u) tc::mbar_wait(bar.full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
-  tc::cluster_sync();
+  tc::cluster_sync();   // neither CTA leaves while the other may still signal it
   if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
-// One persistent launch of CTA pairs, never more than fit at once.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pairs(void (*kern)(KArgs...), size_t smem, cudaStream_t st, Args... args) {
-  cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// One persistent launch of CTA pairs.
+template <int kJob>
+cudaError_t launch_pairs(const Params& P, cudaStream_t st) {
+  auto kern = backward_pair_kernel<kJob>;
+  const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (r != cudaSuccess) return r;
-  return launch_kernel(kern, dim3((unsigned)(sm_count() / 2 * 2)), dim3(kThreads), smem, st, 2, args...);
+  const int pairs = sm_count() / 2;
+  return launch_kernel(kern, dim3((unsigned)(2 * (pairs < kMaxPairs ? pairs : kMaxPairs))), dim3(kThreads), kSmem, st, 2,
+                       P);
 }
 
-// Whether every row of [.., cols] elements of `size` bytes starts on a 32-byte sector.
-bool starts_on_sectors(const void* p, int cols, int size) {
-  return ((uintptr_t)p % 32 == 0) && ((int64_t)cols * size % 32 == 0);
-}
-
-template <int kKind>
-cudaError_t run_rows(const void* tokens, int64_t rows, int K, const void* W, int E, int N, const int32_t* offs,
-                     const RowsOut& out, int* err, cudaStream_t st) {
-  constexpr bool kMN = kKind == kDh || kKind == kDx;
-  CUtensorMap mx, mxs, mw;
-  if (!tma_map_bf16(&mx, tokens, (uint64_t)rows, (uint64_t)K, kBM) ||
-      !tma_map_bf16(&mxs, tokens, (uint64_t)rows, (uint64_t)K, kBoxRows))
-    return cudaErrorNotSupported;
-  if (kMN ? !tma_map_bf16_3d(&mw, W, (uint64_t)E, (uint64_t)K, (uint64_t)N, kBK)
-          : !tma_map_bf16(&mw, W, (uint64_t)E * N * (kKind == kDaSwiglu ? 2 : 1), (uint64_t)K, kBM))
-    return cudaErrorNotSupported;
-  return launch_pairs(backward_rows_kernel<kKind>, kSmemRows, st, mx, mxs, mw, offs, E, N, K, out, err);
-}
+// Whether every row of [.., cols] bf16 elements starts on a 32-byte sector.
+bool starts_on_sectors(const void* p, int cols) { return ((uintptr_t)p % 32 == 0) && (cols % 16 == 0); }
 
 }  // namespace
 
 int64_t backward_blocks(int64_t rows, int E) { return rows / kTile + E + 1; }
-size_t backward_dh_floats(int64_t rows, int E, int F) {
-  const int64_t blocks = rows / kTile + (rows < E ? rows : E);   // at most: one partial block for each expert with rows
-  return (size_t)blocks * ((F + kTile - 1) / kTile) * kTile * kTile;
-}
+size_t backward_stash_floats() { return (size_t)2 * kMaxPairs * kStash; }
 size_t backward_tail_bytes(int E, int H, int N, int F) {
-  return (size_t)E * kTailRows * ((size_t)N + 2 * (size_t)H + (size_t)F) * sizeof(bf16);
+  return (size_t)E * kGroup * ((size_t)N + 2 * (size_t)H + (size_t)F) * sizeof(bf16);
 }
 
-cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBackward& b, void* da, float* dh,
+cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBackward& b, void* da, float* stash,
                                    float* part, void* tails, int* err, cudaStream_t st) {
   const bool swi = (s.flags & MOE_FLAG_SWIGLU) != 0;
-  const int G = swi ? 2 : 1, N = G * s.F;
+  const int N = swi ? 2 * s.F : s.F;
   const int64_t lim = (int64_t)1 << 31;
   if (max_rows + kTile >= lim || (int64_t)s.E * N >= lim || (int64_t)s.E * s.H >= lim) return cudaErrorNotSupported;
   cudaError_t e = cudaSuccess;
@@ -882,60 +800,70 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
     if (e == cudaSuccess && b.db2) e = cudaMemsetAsync(b.db2, 0, (size_t)s.E * s.H * 4, st);
     return e;
   }
-  CUtensorMap m[8];
-  CUtensorMap mo[2];
-  WeightProduct P[2] = {{0, 0}, {0, 0}};
+  const uint64_t R = (uint64_t)max_rows, E = (uint64_t)s.E, H = (uint64_t)s.H, F = (uint64_t)s.F, n = (uint64_t)N;
+  Params P = {};
+  P.offs = b.offs;
+  P.E = s.E;
+  P.H = s.H;
+  P.F = s.F;
+  P.N = N;
+  P.da = (bf16*)da;
+  P.err = err;
+  const bool hidden = b.dx_perm || b.dW1 || b.db1;   // what needs da
+  if (hidden) {
+    P.stash = stash;
+    P.b1 = b.b1;
+    P.part = b.db1 ? part : nullptr;
+    P.sectors = starts_on_sectors(da, s.F);
+    if (!tma_map_bf16(&P.map[kDy], b.dy_perm, R, H, kBM) || !tma_map_bf16(&P.map[kDyBox], b.dy_perm, R, H, kBoxRows) ||
+        !tma_map_bf16_3d(&P.map[kW2], b.W2, E, H, F, kBK) || !tma_map_bf16(&P.map[kX], b.x_perm, R, H, kBM) ||
+        !tma_map_bf16(&P.map[kXBox], b.x_perm, R, H, kBoxRows) || !tma_map_bf16(&P.map[kW1], b.W1, E * n, H, kBM))
+      return cudaErrorNotSupported;
+    e = swi ? launch_pairs<kDaSwiglu>(P, st) : launch_pairs<kDaGelu>(P, st);
+    if (e != cudaSuccess) return e;
+  }
   Extras x = {};
-  int n = 0;   // weight products
+  int nw = 0;   // weight products
   bf16* at = (bf16*)tails;
-  auto add_operand = [&](int i, const void* rows, int cols) {   // operand i of product n
-    bf16* t = at;
-    at += (int64_t)s.E * kTailRows * cols;
-    x.o[2 * n + i] = {(const uint4*)rows, (uint4*)t, cols / 8};
-    return tma_map_bf16(&m[4 * n + i], rows, (uint64_t)max_rows, (uint64_t)cols, kBK) &&
-           tma_map_bf16(&m[4 * n + 2 + i], t, (uint64_t)s.E * kTailRows, (uint64_t)cols, kTailRows);
-  };
   auto add = [&](const void* A, int M, const void* Bm, int Nn, void* dW) {
-    P[n] = {M, Nn};
-    const bool ok = add_operand(0, A, M) && add_operand(1, Bm, Nn) &&
-                    tma_map_bf16_3d(&mo[n], dW, (uint64_t)s.E, (uint64_t)M, (uint64_t)Nn, 32);
-    ++n;
+    const void* rows[2] = {A, Bm};
+    const int cols[2] = {M, Nn};
+    CUtensorMap* m = &P.map[kWeightMaps + 4 * nw];
+    bool ok = tma_map_bf16_3d(&P.map[kOutMaps + nw], dW, E, (uint64_t)M, (uint64_t)Nn, 32);
+    for (int i = 0; i < 2; ++i) {
+      x.o[2 * nw + i] = {(const uint4*)rows[i], (uint4*)at, cols[i] / 8};
+      ok = ok && tma_map_bf16(m + i, rows[i], R, (uint64_t)cols[i], kBK) &&
+           tma_map_bf16(m + 2 + i, at, E * kGroup, (uint64_t)cols[i], kGroup);
+      at += (int64_t)s.E * kGroup * cols[i];
+    }
+    P.wm[nw] = M;
+    P.wn[nw] = Nn;
+    ++nw;
     return ok;
   };
   if (b.dW1 && !add(da, N, b.x_perm, s.H, b.dW1)) return cudaErrorNotSupported;
   if (b.dW2 && !add(b.dy_perm, s.H, b.h_perm, s.F, b.dW2)) return cudaErrorNotSupported;
-  x.tails = 2 * n * kTailSplit * s.E;
-  RowsOut out{dh, (bf16*)da, (bf16*)b.dx_perm, b.b1, b.db1 ? part : nullptr, starts_on_sectors(da, s.F, 2)};
-  if (b.dx_perm || b.dW1 || b.db1) {
-    e = run_rows<kDh>(b.dy_perm, max_rows, s.H, b.W2, s.E, s.F, b.offs, out, err, st);
-    if (e == cudaSuccess)
-      e = swi ? run_rows<kDaSwiglu>(b.x_perm, max_rows, s.H, b.W1, s.E, s.F, b.offs, out, err, st)
-              : run_rows<kDaGelu>(b.x_perm, max_rows, s.H, b.W1, s.E, s.F, b.offs, out, err, st);
-    x.part = part;
-    x.db1 = b.db1;
-    x.n = N;
-    x.swaps = swi ? 0 : 1;
-    x.cols1 = (N + kRedCols - 1) / kRedCols;
-    x.db1_blocks = b.db1 ? x.cols1 * s.E : 0;
-  }
+  x.tails = 2 * nw * kTailSplit * s.E;
+  x.part = part;
+  x.db1 = b.db1;
+  x.n = N;
+  x.swaps = swi ? 0 : 1;
+  x.cols1 = (N + kRedCols - 1) / kRedCols;
+  x.db1_blocks = b.db1 ? x.cols1 * s.E : 0;
   x.dy = (const uint4*)b.dy_perm;
   x.db2 = b.db2;
   x.h = s.H;
   x.cols2 = (s.H / 8 + kSumVecs - 1) / kSumVecs;
   const int64_t extras = (int64_t)x.tails + x.db1_blocks + (b.db2 ? (int64_t)x.cols2 * s.E : 0);
-  if (e == cudaSuccess && extras > 0)
+  if (extras > 0)
     e = launch_kernel(backward_extras_kernel, dim3((unsigned)extras), dim3(256), 0, st, 1, x, b.offs, s.E);
-  out.sectors = starts_on_sectors(b.dx_perm, s.H, 2);
-  if (e == cudaSuccess && b.dx_perm)
-    e = run_rows<kDx>(da, max_rows, N, b.W1, s.E, s.H, b.offs, out, err, st);
-  if (n == 1) {
-    for (int i = 0; i < 4; ++i) m[4 + i] = m[i];
-    mo[1] = mo[0];
-  }
-  if (e == cudaSuccess && n > 0)
-    e = launch_pairs(backward_weights_kernel, kSmemWeights, st, m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], mo[0],
-                     mo[1], b.offs, s.E, P[0], P[1], err);
-  return e;
+  if (e != cudaSuccess || !(b.dx_perm || nw > 0)) return e;
+  P.dx = (bf16*)b.dx_perm;
+  P.sectors = starts_on_sectors(b.dx_perm, s.H);
+  if (b.dx_perm && (!tma_map_bf16(&P.map[kDaRows], da, R, n, kBM) || !tma_map_bf16(&P.map[kDaBox], da, R, n, kBoxRows) ||
+                    !tma_map_bf16_3d(&P.map[kW1MN], b.W1, E, n, H, kBK)))
+    return cudaErrorNotSupported;
+  return launch_pairs<kGradients>(P, st);
 }
 
 }  // namespace moe

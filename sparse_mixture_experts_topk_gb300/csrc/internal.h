@@ -218,13 +218,13 @@ struct FfnBackward {
 // da: [max_rows, F or 2F] fp32 scratch
 cudaError_t launch_ffn_backward_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, float* da,
                                      cudaStream_t st);
-// bf16 on SM pairs.  da: [max_rows, F or 2F] bf16, dh: backward_dh_floats,
-// part: [8 * backward_blocks(max_rows, E), F or 2F] fp32, tails:
-// backward_tail_bytes (N = F or 2F), 128-byte aligned: scratch.
-size_t backward_dh_floats(int64_t rows, int E, int F);
+// bf16 on SM pairs.  da: [max_rows, F or 2F] bf16, stash:
+// backward_stash_floats, part: [8 * backward_blocks(max_rows, E), F or 2F]
+// fp32, tails: backward_tail_bytes (N = F or 2F), 128-byte aligned: scratch.
+size_t backward_stash_floats();
 int64_t backward_blocks(int64_t rows, int E);
 size_t backward_tail_bytes(int E, int H, int N, int F);
-cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBackward& b, void* da, float* dh,
+cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBackward& b, void* da, float* stash,
                                    float* part, void* tails, int* err, cudaStream_t st);
 cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int count, int grad_dtype, int state_bits,
                          const moe_adamw_params& h, const float* grad_scale, const int32_t* skip, cudaStream_t st);
