@@ -25,7 +25,8 @@
 // Row products (dh, a, dx).  A block of 256 rows has its rows on the MMA's M
 // side; an expert's last block of at most 128 rows runs swapped (256 weight
 // columns on M, the rows on N rounded up to 16), so that few rows do not cost
-// a full tile (not with SwiGLU, where a tile pairs gate with up columns).
+// a full tile.  (With SwiGLU it then has three products of 256 columns, dh,
+// gate and up, and the gate waits in the scratch as dh does.)
 // Weight products: the reduction runs over an expert's rows in blocks of 64,
 // 16 to an MMA.  The rows that do not fill a group of 16 come from copies of
 // them, padded with zeros to 16, that the second launch makes: in place the
@@ -60,11 +61,11 @@ constexpr int kSwapRows = 128;            // a last block of at most this many r
 constexpr int kOperand = kBM * kBK * 2;   // bytes of one operand in a stage
 constexpr int kHalf = kOperand / 2;       // an MN-major operand is two boxes of 64 columns x 64 rows
 constexpr int kStageBytes = 2 * kOperand;
-constexpr int kStages = 6;
 constexpr int kTmemCols = 512;            // two accumulators of 256 columns
 constexpr int kEpiWarps = 8;              // per CTA: two for each quarter of the TMEM lanes
 constexpr int kStoreBytes = 32 * 128;     // an epilogue warp's 32 rows of 64 columns on their way to TMA
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * kStoreBytes;
+constexpr size_t kSmem = 1024 + (size_t)7 * kStageBytes;   // seven stages, or six and the eight store tiles
+static_assert(kEpiWarps * kStoreBytes == kStageBytes, "the store tiles take a stage's place");
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxPairs = 80;             // bounds the dh scratch: 128 KB for each CTA
 constexpr int kStash = kBM * kTile;       // its fp32 values
@@ -123,6 +124,7 @@ __device__ __forceinline__ int expert_of(const int* tstart, int E, int t) {
   return lo;
 }
 
+template <int kStages>
 __device__ __forceinline__ void advance(int& stage, uint32_t& phase) {
   if (++stage == kStages) {
     stage = 0;
@@ -164,6 +166,7 @@ __device__ __forceinline__ void store_row(T* dst, const float* v, int n, bool se
 __device__ __forceinline__ int row_blocks(int rows) { return (rows + kTile - 1) / kTile; }
 
 // Barriers of a CTA: full and empty per stage, full and empty per accumulator, the end.
+template <int kStages>
 struct Bars {
   uint32_t base;
   __device__ uint32_t full(int s) const { return base + 8 * s; }
@@ -194,7 +197,7 @@ struct Extras {
   int tails;            // blocks of tails
   const float* part;    // db1's partial sums, n columns
   float* db1;
-  int n, swaps, cols1;  // columns of blocks
+  int n, cols1;         // columns of blocks
   int db1_blocks;
   const uint4* dy;      // db2 = the sum of an expert's dy rows, h columns
   float* db2;
@@ -221,7 +224,7 @@ __device__ __forceinline__ void reduce_bias(const Extras& x, const int32_t* __re
   const int g = threadIdx.x / kRedCols, c = col * kRedCols + threadIdx.x % kRedCols;
   const int r0 = offs[e], rows = offs[e + 1] - r0, mt = row_blocks(rows);
   const int last = mt > 0 ? rows - (mt - 1) * kTile : 0;
-  const int parts = 8 * mt - (x.swaps && mt > 0 && last <= kSwapRows ? 6 : 0);
+  const int parts = 8 * mt - (mt > 0 && last <= kSwapRows ? 6 : 0);
   const float* p = x.part + ((int64_t)(r0 >> 8) + e) * 8 * x.n + c;
   float sum = 0.f;
   if (c < x.n) {
@@ -319,52 +322,80 @@ __device__ __forceinline__ int dh_chunk(int i, int half) {
   return kSwi ? (i >> 1) * 4 + half * 2 + (i & 1) : half * 4 + i;
 }
 
-// dh of a tile: from the accumulator to this thread's scratch.
+// 32 values of this thread's from an accumulator to its scratch.
+__device__ __forceinline__ void stash32(uint32_t taddr, float4* st) {
+  uint32_t r[32];
+  tc::tmem_ld_32x32b_x32(taddr, r);
+  tc::tmem_wait_ld();
+#pragma unroll
+  for (int g = 0; g < 8; ++g)
+    st[g * 32] = make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]), __uint_as_float(r[4 * g + 2]),
+                             __uint_as_float(r[4 * g + 3]));
+}
+// dh of a tile in row orientation.
 template <bool kSwi>
-__device__ __forceinline__ void stash_dh(uint32_t tbase, const Tile& d, int half, int F, float4* st) {
+__device__ __forceinline__ void stash_rows(uint32_t tbase, const Tile& d, int half, int F, float4* st) {
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
-    const int c = d.swap ? half + 2 * i : dh_chunk<kSwi>(i, half);
-    if (d.swap ? c * 32 >= d.nrows : d.n0 + c * 32 >= F) continue;
-    uint32_t r[32];
-    tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
-    tc::tmem_wait_ld();
-#pragma unroll
-    for (int g = 0; g < 8; ++g)
-      st[(i * 8 + g) * 32] = make_float4(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]),
-                                         __uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
+    const int c = dh_chunk<kSwi>(i, half);
+    if (d.n0 + c * 32 < F) stash32(tbase + c * 32, st + i * 8 * 32);
   }
 }
+// dh (which = 0) or the gate (1) of a swapped tile: at most two groups of 32 rows.
+__device__ __forceinline__ void stash_swapped(uint32_t tbase, const Tile& d, int half, int which, float4* st) {
+#pragma unroll 1
+  for (int i = 0; (half + 2 * i) * 32 < d.nrows; ++i)
+    stash32(tbase + (half + 2 * i) * 32, st + (which * 2 + i) * 8 * 32);
+}
+__device__ __forceinline__ float part_of(const float4& v, int j) {
+  return (j & 3) == 0 ? v.x : (j & 3) == 1 ? v.y : (j & 3) == 2 ? v.z : v.w;
+}
 
-// da of a GELU tile that runs swapped: this thread's column, every other group of 32 rows.
+// da of a swapped tile: this thread's column, every other group of 32 rows.
+template <bool kSwi>
 __device__ __forceinline__ void da_swapped(uint32_t tbase, const Tile& d, int rank, int q, int half, int lane,
                                            const Params& P, const float4* st) {
   const int f = d.n0 + rank * kBM + q * 32 + lane;
   const bool ok = f < P.F;
-  const float bf = P.b1 && ok ? P.b1[(int64_t)d.e * P.F + f] : 0.f;
-  float sum = 0.f;
+  const float* be = P.b1 && ok ? P.b1 + (int64_t)d.e * P.N + f : nullptr;
+  const float bf = be ? be[0] : 0.f, bu = be && kSwi ? be[P.F] : 0.f;
+  float sum = 0.f, sum_up = 0.f;
 #pragma unroll 1
   for (int i = 0; (half + 2 * i) * 32 < d.nrows; ++i) {
     const int c = half + 2 * i, left = ok ? d.nrows - c * 32 : 0;
-    float4 dh[8];
+    float4 dh[8], gate[kSwi ? 8 : 1];
 #pragma unroll
-    for (int g = 0; g < 8; ++g) dh[g] = __ldcg(st + (i * 8 + g) * 32);
+    for (int g = 0; g < 8; ++g) {
+      dh[g] = __ldcg(st + (i * 8 + g) * 32);
+      if (kSwi) gate[g % (kSwi ? 8 : 1)] = __ldcg(st + ((2 + i) * 8 + g) * 32);
+    }
     uint32_t r[32];
     tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
     tc::tmem_wait_ld();
-    bf16* out = P.da + (int64_t)(d.row0 + c * 32) * P.F + f;
+    bf16* out = P.da + (int64_t)(d.row0 + c * 32) * P.N + f;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      const float4 v = dh[j >> 2];
-      const float h = (j & 3) == 0 ? v.x : (j & 3) == 1 ? v.y : (j & 3) == 2 ? v.z : v.w;
       if (j < left) {
-        const float g = h * gelu_slope_fast(__uint_as_float(r[j]) + bf);
+        const float h = part_of(dh[j >> 2], j), v = __uint_as_float(r[j]);
+        float g;
+        if (kSwi) {
+          float u;
+          swiglu_gradient_fast(part_of(gate[(j >> 2) % (kSwi ? 8 : 1)], j) + bf, v + bu, h, &g, &u);
+          sum_up += u;
+          out[(int64_t)j * P.N + P.F] = __float2bfloat16_rn(u);
+        } else {
+          g = h * gelu_slope_fast(v + bf);
+        }
         sum += g;
-        out[(int64_t)j * P.F] = __float2bfloat16_rn(g);
+        out[(int64_t)j * P.N] = __float2bfloat16_rn(g);
       }
     }
   }
-  if (P.part && ok) P.part[((int64_t)d.block * 8 + half) * P.F + f] = sum;
+  if (P.part && ok) {
+    float* p = P.part + ((int64_t)d.block * 8 + half) * P.N + f;
+    p[0] = sum;
+    if (kSwi) p[P.F] = sum_up;
+  }
 }
 
 // da of a tile in row orientation: this thread's row, 32 columns at a time.
@@ -510,6 +541,7 @@ __device__ __forceinline__ void weight_tile(uint32_t tbase, const Tile& d, bool 
 template <int kJob>
 __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid_constant__ Params P) {
   constexpr bool kSwi = kJob == kDaSwiglu, kDa = kJob != kGradients;
+  constexpr int kStages = kDa ? 7 : 6;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_tstart[257];
   __shared__ uint32_t s_tmem;
@@ -517,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sB = sA + kStages * kOperand, sOut = sB + kStages * kOperand;
-  const Bars bar{tc::smem_u32(s_bar)};
+  const Bars<kStages> bar{tc::smem_u32(s_bar)};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)tc::cluster_ctarank();
   auto tiles = [](int n) { return (n + kTile - 1) / kTile; };
@@ -563,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
       const int local = t - s_tstart[d.e], col = local / mt, rb = local - col * mt;
       d.row0 = r0 + rb * kTile;
       d.nrows = min(kTile, r1 - d.row0);
-      d.swap = !kSwi && d.nrows <= kSwapRows;
+      d.swap = d.nrows <= kSwapRows;
       d.n0 = col * kTile;
       d.block = (r0 >> 8) + d.e + rb;
     } else {
@@ -579,8 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
     return d;
   };
   // The products of a tile, one accumulator after the other (SwiGLU: dh, then
-  // a's halves as far as F goes), their stages, and the MMAs of a stage.
-  auto products = [&](const Tile& d) { return kSwi ? (P.F - d.n0 > kBM ? 3 : 2) : kDa ? 2 : 1; };
+  // a's halves as far as F goes, or gate and up), their stages, and the MMAs
+  // of a stage.
+  auto products = [&](const Tile& d) { return kSwi ? (d.swap || P.F - d.n0 > kBM ? 3 : 2) : kDa ? 2 : 1; };
   auto has_tail = [&](const Tile& d) { return !d.rows && d.nrows % kGroup != 0; };
   const int row_k = kDa ? P.H : P.N;   // a row product's reduction
   auto stages = [&](const Tile& d) {
@@ -612,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
           load(kb, sA + stage * kOperand, sB + stage * kOperand, tc::map_peer(bar.full(stage), 0));
           filled |= 1u << stage;
           fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
-          advance(stage, phase);
+          advance<kStages>(stage, phase);
         }
         return true;
       };
@@ -655,7 +688,9 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
         if (kDa) {
           const CUtensorMap* mx = &P.map[kX + (d.swap ? 1 : 0)];
           for (int sub = 1; sub < products(d) && ok; ++sub) {
-            const int wrow = kSwi ? (2 * d.e + rank) * P.F + d.n0 + (sub - 1) * kBM : d.e * P.F + n;
+            const int wrow = !kSwi ? d.e * P.F + n
+                                   : d.swap ? (2 * d.e + sub - 1) * P.F + n
+                                            : (2 * d.e + rank) * P.F + d.n0 + (sub - 1) * kBM;
             ok = fill(nk, bytes, [&](int kb, uint32_t a, uint32_t b, uint32_t fbar) {
               tc::tma_load_2d_pair(d.swap ? a : b, &P.map[kW1], fbar, kb * kBK, wrow);
               load_tokens(mx, kb, d.swap ? b : a, fbar);
@@ -675,7 +710,6 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
       Tile next = first < total ? decode(first) : Tile{};
       for (int t = first; t < total && ok; t += step) {
         const Tile d = next;
-        if (t + step < total) next = decode(t + step);   // beside the MMAs issued last
         const int nk = stages(d), np = products(d), mma_n = d.swap ? (d.nrows + 15) / 16 * 16 : kTile;
         for (int sub = 0; sub < np && ok; ++sub) {
           const bool weights_mn = kDa ? sub == 0 : true;
@@ -697,9 +731,12 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
             for (int k = 1; k < kBK / kGroup; ++k)
               if (k < ng) tc::mma_bf16_pair(dst, a + k * as, b + k * bs, idesc, 1);
             tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
-            advance(stage, phase);
+            advance<kStages>(stage, phase);
+            // the next tile's divisions run beside the MMAs issued so far
+            if (sub == 0 && kb == min(2, nk - 1) && t + step < total) next = decode(t + step);
           }
           if (!ok) break;
+          if (nk == 0 && t + step < total) next = decode(t + step);
           tc::tc_commit_pair_mc(bar.tfull(acc), 0x3);
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1u;
@@ -732,8 +769,9 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
         tc::tc_fence_after();
         const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile);
         if (kDa) {
-          if (sub == 0) stash_dh<kSwi>(tbase, d, half, P.F, st);
-          else if (!kSwi && d.swap) da_swapped(tbase, d, rank, q, half, lane, P, st);
+          if (d.swap && sub < np - 1) stash_swapped(tbase, d, half, sub, st);
+          else if (d.swap) da_swapped<kSwi>(tbase, d, rank, q, half, lane, P, st);
+          else if (sub == 0) stash_rows<kSwi>(tbase, d, half, P.F, st);
           else da_rows<kSwi>(tbase, d, sub - 1, rank, q, half, lane, P, st);
         } else if (d.rows) {
           dx_tile(tbase, d, rank, q, half, lane, P);
@@ -847,7 +885,6 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
   x.part = part;
   x.db1 = b.db1;
   x.n = N;
-  x.swaps = swi ? 0 : 1;
   x.cols1 = (N + kRedCols - 1) / kRedCols;
   x.db1_blocks = b.db1 ? x.cols1 * s.E : 0;
   x.dy = (const uint4*)b.dy_perm;
