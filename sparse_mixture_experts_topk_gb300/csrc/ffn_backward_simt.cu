@@ -15,15 +15,18 @@
 // Two launches: the tiles of da, then those of dx, dW1 and dW2 side by side
 // (they need da and nothing of each other).  The bias gradients are the
 // column sums of the weight gradients' left operand, added up by the blocks
-// of the first column of tiles.  While a block multiplies 32 reduction
-// elements in shared memory, the next 32 are on their way to registers.
+// of the first column of tiles.  While a block multiplies the reduction
+// elements in shared memory, the next are on their way to registers.
 //
-// A row product's tile has 64 columns and 64 or 16 rows; a thread always
-// holds 4 x 4 values (two 16-byte reads of shared memory for 16
-// multiply-adds), so that with 16 rows four groups of 64 threads take a
-// quarter of the reduction each, added up at the end.  These layers are small
-// (the fp32 ones are for checking) and their experts have few rows: 16 is
-// used while the experts have less than 32 rows on average.
+// A thread always holds 4 x 4 values (two 16-byte reads of shared memory for
+// 16 multiply-adds).  A tile has 64 x 64 values, or 16 rows and 32 columns: eight
+// warps then take an eighth of the reduction each, added up at the end.  These
+// layers are small (the fp32 ones are for checking) and their experts have few
+// rows: the small tiles are used while the experts have less than 32 rows on
+// average, or while tiles of 64 would not be four for every three SMs.
+// Measured, small against large: 64 tokens, H = 256, E = 8, top-2, F = 512:
+// 25.5 us against 59.8; 250 tokens, H = 384, F = 640: 80 against 104, with top-4
+// 137 against 121.
 #include "common.cuh"
 #include "ffn_backward.cuh"
 #include "internal.h"
@@ -32,7 +35,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kN = 64, kBK = 32, kThreads = 256;
+constexpr int kThreads = 256;
+// Columns of a row product's tile of kM rows, and the reduction elements staged at a time.
+template <int kM> constexpr int kCols = kM == 16 ? 32 : 64;
+template <int kM> constexpr int kDepth = kM == 16 ? 64 : 32;
 
 // Row tile `tile` of kM rows: its expert, first row and the expert's end;
 // false past the last tile.  A whole warp.
@@ -84,7 +90,7 @@ __device__ __forceinline__ void store4(bf16* p, const float (&v)[4]) {
 // i, k at i * stride + k) or i does (k * stride + i).  Rows start on 16 bytes
 // and the dimension along them is a multiple of 8, so four elements are
 // inside or outside together; outside (i >= ni, k >= nk) is zero.
-template <int kI, bool kAlongK>
+template <int kI, int kBK, bool kAlongK>
 struct Stage {
   static constexpr int kVecs = kI * kBK / 4, kLoads = (kVecs + kThreads - 1) / kThreads;
   float4 v[kLoads];
@@ -116,9 +122,10 @@ struct Stage {
   }
 };
 
-// This thread's 4 x 4 values of a kM x 64 tile, and its share of the reduction.
+// This thread's 4 x 4 values of a kM-row tile, and its share of the reduction.
 template <int kM>
 struct Place {
+  static constexpr int kN = kCols<kM>;
   static constexpr int kTileThreads = kM / 4 * (kN / 4), kGroups = kThreads / kTileThreads;
   int ty, tx, group;
   __device__ Place() {
@@ -131,7 +138,7 @@ struct Place {
 
 // acc += A^T B over this group's share of the first nk staged elements.
 template <int kM>
-__device__ __forceinline__ void multiply(float (&acc)[4][4], const float (*A)[kM + 4], const float (*B)[kN + 4],
+__device__ __forceinline__ void multiply(float (&acc)[4][4], const float (*A)[kM + 4], const float (*B)[kCols<kM> + 4],
                                          const Place<kM>& at, int nk) {
 #pragma unroll 8
   for (int k = at.group; k < nk; k += Place<kM>::kGroups) {
@@ -163,17 +170,17 @@ __device__ __forceinline__ void gather(float (&acc)[4][4], const Place<kM>& at, 
       for (int i = 0; i < 16; ++i) acc[i / 4][i % 4] += s[((g - 1) * 16 + i) * kT + me];
   }
 }
-// Shared memory of gather: three groups' accumulators of 64 threads.
-constexpr int kGatherFloats = 3 * 16 * 64;
+// Shared memory of gather: seven groups' accumulators of 32 threads.
+constexpr int kGatherFloats = 7 * 16 * 32;
 
-// da for one kM-row x 64-column tile: the products a (one, or gate and up)
+// da for one tile: the products a (one, or gate and up)
 // and dh, all of length H, then the activation's slope.
 template <typename T, bool kSwi, int kM>
 __global__ void __launch_bounds__(kThreads)
 hidden_gradient_simt_kernel(const T* __restrict__ x, const T* __restrict__ dy, const int32_t* __restrict__ offs,
                             int E, const T* __restrict__ W1, const float* __restrict__ b1, const T* __restrict__ W2,
                             int H, int F, float* __restrict__ da) {
-  constexpr int G = kSwi ? 2 : 1;
+  constexpr int G = kSwi ? 2 : 1, kN = kCols<kM>, kBK = kDepth<kM>;
   __shared__ __align__(16) float sx[kBK][kM + 4], sdy[kBK][kM + 4];
   __shared__ __align__(16) float sw[2 + (kSwi ? 1 : 0)][kBK][kN + 4];   // gate, W2, up
   static_assert(kM == 64 || sizeof(sw) >= kGatherFloats * sizeof(float), "the groups' sums reuse the weights' stage");
@@ -186,9 +193,9 @@ hidden_gradient_simt_kernel(const T* __restrict__ x, const T* __restrict__ dy, c
   const T* pdy = dy + (int64_t)r0 * H;
   const T* pg = W1 + ((int64_t)e * G * F + f0) * H;
   const T* p2 = W2 + (int64_t)e * H * F + f0;
-  Stage<kM, true> vx, vdy;
-  Stage<kN, true> vg, vu;
-  Stage<kN, false> v2;
+  Stage<kM, kBK, true> vx, vdy;
+  Stage<kN, kBK, true> vg, vu;
+  Stage<kN, kBK, false> v2;
   auto fetch = [&](int k0) {
     const int nk = min(kBK, H - k0);
     vx.fetch(px + k0, H, nr, nk);
@@ -248,8 +255,8 @@ __device__ __forceinline__ void store_tile(T* out, int64_t stride, const float (
 }
 
 union Shared {
-  struct { float a[kBK][64 + 4], b[kBK][kN + 4]; } w;
-  struct { float a[kBK][16 + 4], b[kBK][kN + 4]; } r;
+  struct { float a[kDepth<64>][64 + 4], b[kDepth<64>][kCols<64> + 4]; } w;
+  struct { float a[kDepth<16>][16 + 4], b[kDepth<16>][kCols<16> + 4]; } r;
   float sums[kGatherFloats];
 };
 
@@ -257,15 +264,16 @@ union Shared {
 template <typename T, int kM>
 __device__ __forceinline__ void input_tile(const float* __restrict__ da, const int32_t* __restrict__ offs, int E,
                                            const T* __restrict__ W1, int N, int H, T* __restrict__ dx, int row, int col,
-                                           float (*sa)[kM + 4], float (*sb)[kN + 4], float* sums) {
+                                           float (*sa)[kM + 4], float (*sb)[kCols<kM> + 4], float* sums) {
+  constexpr int kN = kCols<kM>, kBK = kDepth<kM>;
   int e, r0, r1;
   if (!row_tile<kM>(offs, E, row, &e, &r0, &r1)) return;
   const Place<kM> at;
   const int h0 = col * kN, nr = min(kM, r1 - r0), nh = min(kN, H - h0);
   const float* pa = da + (int64_t)r0 * N;
   const T* pw = W1 + (int64_t)e * N * H + h0;
-  Stage<kM, true> va;
-  Stage<kN, false> vw;
+  Stage<kM, kBK, true> va;
+  Stage<kN, kBK, false> vw;
   float acc[4][4] = {};
   auto fetch = [&](int k0) {
     va.fetch(pa + k0, N, nr, min(kBK, N - k0));
@@ -290,12 +298,13 @@ template <typename TA, typename T>
 __device__ __forceinline__ void weight_tile(const TA* __restrict__ A, const T* __restrict__ B,
                                             const int32_t* __restrict__ offs, int M, int N, T* __restrict__ dW,
                                             float* __restrict__ db, int e, int m0, int n0, float (*sa)[64 + 4],
-                                            float (*sb)[kN + 4]) {
+                                            float (*sb)[64 + 4]) {
+  constexpr int kN = 64, kBK = kDepth<64>;
   const Place<64> at;
   const int r0 = offs[e], rows = offs[e + 1] - r0, nm = min(64, M - m0), nn = min(kN, N - n0);
   const TA* pa = A + (int64_t)r0 * M + m0;
   const T* pb = B + (int64_t)r0 * N + n0;
-  Stage<64, false> va, vb;
+  Stage<64, kBK, false> va, vb;
   float acc[4][4] = {}, sum = 0.f;
   const bool sums = db && n0 == 0;
   auto fetch = [&](int k0) {
@@ -340,13 +349,13 @@ gradients_simt_kernel(const float* __restrict__ da, const __grid_constant__ FfnB
                         s.sums);
   } else if ((i -= t.dx) < t.w1) {
     const int e = i / t.w1_per, l = i % t.w1_per;
-    weight_tile(da, (const T*)b.x_perm, b.offs, N, H, (T*)b.dW1, b.db1, e, l / t.w1_cols * 64, l % t.w1_cols * kN,
+    weight_tile(da, (const T*)b.x_perm, b.offs, N, H, (T*)b.dW1, b.db1, e, l / t.w1_cols * 64, l % t.w1_cols * 64,
                 s.w.a, s.w.b);
   } else {
     i -= t.w1;
     const int e = i / t.w2_per, l = i % t.w2_per;
     weight_tile((const T*)b.dy_perm, (const T*)b.h_perm, b.offs, H, F, (T*)b.dW2, b.db2, e, l / t.w2_cols * 64,
-                l % t.w2_cols * kN, s.w.a, s.w.b);
+                l % t.w2_cols * 64, s.w.a, s.w.b);
   }
 }
 
@@ -354,7 +363,8 @@ template <typename T, int kM>
 cudaError_t run_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, float* da, cudaStream_t st) {
   const bool swi = (s.flags & MOE_FLAG_SWIGLU) != 0;
   const int N = swi ? 2 * s.F : s.F;
-  auto tiles = [](int64_t n) { return (n + kN - 1) / kN; };
+  auto tiles = [](int64_t n) { return (n + 63) / 64; };            // weight products
+  auto cols = [](int64_t n) { return (n + kCols<kM> - 1) / kCols<kM>; };   // row products
   // at most one part-filled row tile for each expert with rows
   const int64_t mtiles = max_rows / kM + (max_rows < s.E ? max_rows : s.E);
   if (mtiles > 65535) return cudaErrorNotSupported;
@@ -362,24 +372,26 @@ cudaError_t run_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, flo
   if (hidden) {
     auto k = swi ? hidden_gradient_simt_kernel<T, true, kM> : hidden_gradient_simt_kernel<T, false, kM>;
     const cudaError_t e =
-        launch_kernel(k, dim3((unsigned)tiles(s.F), (unsigned)mtiles), dim3(kThreads), 0, st, 1, (const T*)b.x_perm,
+        launch_kernel(k, dim3((unsigned)cols(s.F), (unsigned)mtiles), dim3(kThreads), 0, st, 1, (const T*)b.x_perm,
                       (const T*)b.dy_perm, b.offs, s.E, (const T*)b.W1, b.b1, (const T*)b.W2, s.H, s.F, da);
     if (e != cudaSuccess) return e;
   }
   // a bias gradient alone takes the first column of tiles
   const int64_t w1_cols = b.dW1 ? tiles(s.H) : b.db1 ? 1 : 0, w2_cols = b.dW2 ? tiles(s.F) : b.db2 ? 1 : 0;
   const int64_t w1_per = w1_cols * tiles(N), w2_per = w2_cols * tiles(s.H);
-  const int64_t dx = hidden && b.dx_perm ? mtiles * tiles(s.H) : 0, w1 = w1_per * s.E, all = dx + w1 + w2_per * s.E;
+  const int64_t dx = hidden && b.dx_perm ? mtiles * cols(s.H) : 0, w1 = w1_per * s.E, all = dx + w1 + w2_per * s.E;
   if (all == 0) return cudaSuccess;
   if (all >= ((int64_t)1 << 31)) return cudaErrorNotSupported;
-  const Tiles t{(int)dx, (int)tiles(s.H), (int)w1, (int)w1_cols, (int)w1_per, (int)w2_cols, (int)w2_per};
+  const Tiles t{(int)dx, (int)cols(s.H), (int)w1, (int)w1_cols, (int)w1_per, (int)w2_cols, (int)w2_per};
   return launch_kernel(gradients_simt_kernel<T, kM>, dim3((unsigned)all), dim3(kThreads), 0, st, 1, (const float*)da,
                        b, s.E, s.H, s.F, N, t);
 }
 
 template <typename T>
 cudaError_t pick_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, float* da, cudaStream_t st) {
-  return max_rows < 32 * (int64_t)s.E ? run_simt<T, 16>(s, max_rows, b, da, st) : run_simt<T, 64>(s, max_rows, b, da, st);
+  const int64_t large = (max_rows / 64 + s.E) * ((s.F + 63) / 64);   // da's tiles of 64 rows, about
+  const bool small = max_rows < 32 * (int64_t)s.E || large * 3 < (int64_t)sm_count() * 4;
+  return small ? run_simt<T, 16>(s, max_rows, b, da, st) : run_simt<T, 64>(s, max_rows, b, da, st);
 }
 
 }  // namespace
