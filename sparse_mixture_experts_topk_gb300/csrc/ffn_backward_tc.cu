@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
       }
       for (int a = 0; a < 2; ++a) {
         tc::mbar_init(bar.tfull(a), 1);
-        tc::mbar_init(bar.tempty(a), 2 * 32 * kEpiWarps);
+        tc::mbar_init(bar.tempty(a), 2 * kEpiWarps);   // one arrival for each epilogue warp of the pair
       }
       tc::mbar_init(bar.done(), 1);
       s_abort = 0;
@@ -779,8 +779,11 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
           weight_tile(tbase, d, d.nrows == 0, rank, q, half, lane, P, buf, row);
         }
         tc::tc_fence_before();
-        if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
-        else tc::mbar_arrive_remote(tc::map_peer(bar.tempty(acc), 0));
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
+          else tc::mbar_arrive_remote(tc::map_peer(bar.tempty(acc), 0));
+        }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
