@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
         __syncwarp();
         if (lane == 0) {
           if (rank == 0) tc::mbar_arrive(bar.tempty(acc));
-          else tc::mbar_arrive_remote(tc::map_peer(bar.tempty(acc), 0));
+          else tc::mbar_arrive_remote_relaxed(tc::map_peer(bar.tempty(acc), 0));
         }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;

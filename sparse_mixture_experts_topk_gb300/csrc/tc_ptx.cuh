@@ -342,6 +342,11 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// Arrive on an mbarrier of another CTA of the cluster without releasing
+// anything: for a consumer that has only read (tensor memory, into registers).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
 // TMA 3D store of a shared-memory tile (elements outside the tensor are not
 // written), as a group of its own of this thread's bulk copies.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
