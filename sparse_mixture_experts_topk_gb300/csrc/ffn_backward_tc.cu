@@ -35,8 +35,9 @@
 // was measured: the second CTA's zeroing has to reach the MMA thread through a
 // release and an acquire at cluster scope, 2300 cycles of a tile's 4300.)
 //
-// Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader CTA of the
-// pair), warps 2-9 epilogue.  Two epilogue warps share a quarter of the TMEM
+// Roles per CTA: warps 0 and 10 TMA producers, one for each operand (a thread
+// takes 600 cycles to fill a stage by itself, more than its MMAs take), warp 1
+// MMA issuer (leader CTA of the pair), warps 2-9 epilogue.  Two epilogue warps share a quarter of the TMEM
 // lanes and halve its columns: with one, the slopes of a da tile took longer
 // than its MMAs.  Tiles go round the pairs by number.  Every wait is bounded:
 // on expiry the kernel records a timeout in the workspace's error word, drains
@@ -66,7 +67,7 @@ constexpr int kEpiWarps = 8;              // per CTA: two for each quarter of th
 constexpr int kStoreBytes = 32 * 128;     // an epilogue warp's 32 rows of 64 columns on their way to TMA
 constexpr size_t kSmem = 1024 + (size_t)7 * kStageBytes;   // seven stages, or six and the eight store tiles
 static_assert(kEpiWarps * kStoreBytes == kStageBytes, "the store tiles take a stage's place");
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 64 + 32 * kEpiWarps + 32, kSecondProducer = 2 + kEpiWarps;
 constexpr int kMaxPairs = 80;             // bounds the dh scratch: 128 KB for each CTA
 constexpr int kStash = kBM * kTile;       // its fp32 values
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -628,21 +629,23 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
 
   uint32_t filled = 0, fill_par = 0;
   bool producer = false;
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer (both CTAs)
+  if (warp == 0 || warp == kSecondProducer) {
+    // ------------------------------------------------------------ TMA producers (both CTAs)
+    const bool second = warp == kSecondProducer;   // this warp's operand: tokens or B; else weights or A
     if (tc::elect_one()) {
-      producer = true;
+      producer = !second;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      // Waits for a free stage, arms the leader's barrier for the pair's bytes
-      // and has `load` fill the stage.  The kinds of loads have loops of their
-      // own: what a stage costs this thread bounds the kernel.
+      // Waits for a free stage and has `load` fill this warp's operand; the
+      // first producer arms the leader's barrier for the pair's bytes.  The
+      // kinds of loads have loops of their own: what a stage costs this thread
+      // bounds the kernel.
       auto fill = [&](int nk, uint32_t bytes, auto load) {
         for (int kb = 0; kb < nk; ++kb) {
           if (!tc::mbar_wait(bar.empty(stage), phase ^ 1u, &s_abort, kWaitNs)) return false;
-          if (rank == 0) tc::mbar_arrive_expect_tx(bar.full(stage), bytes);
-          load(kb, sA + stage * kOperand, sB + stage * kOperand, tc::map_peer(bar.full(stage), 0));
+          if (rank == 0 && !second) tc::mbar_arrive_expect_tx(bar.full(stage), bytes);
+          load(kb, stage * kOperand, tc::map_peer(bar.full(stage), 0));
           filled |= 1u << stage;
           fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
           advance<kStages>(stage, phase);
@@ -653,47 +656,49 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
         const Tile d = decode(t);
         const int nk = stages(d), n = d.n0 + rank * kBM;
         if (!d.rows) {
-          const CUtensorMap* m = &P.map[kWeightMaps + 4 * d.p];
-          const int ma = d.m0 + rank * kBM, whole = nk - (has_tail(d) ? 1 : 0);
-          auto load = [&](const CUtensorMap* op, int r, uint32_t a, uint32_t b, uint32_t fbar) {
-            tc::tma_load_2d_pair(a, op, fbar, ma, r);
-            tc::tma_load_2d_pair(a + kHalf, op, fbar, ma + 64, r);
-            tc::tma_load_2d_pair(b, op + 1, fbar, n, r);
-            tc::tma_load_2d_pair(b + kHalf, op + 1, fbar, n + 64, r);
+          const CUtensorMap* m = &P.map[kWeightMaps + 4 * d.p + (second ? 1 : 0)];
+          const int c = second ? n : d.m0 + rank * kBM, whole = nk - (has_tail(d) ? 1 : 0);
+          const uint32_t to = second ? sB : sA;
+          auto load = [&](const CUtensorMap* op, int r, uint32_t at, uint32_t fbar) {
+            tc::tma_load_2d_pair(to + at, op, fbar, c, r);
+            tc::tma_load_2d_pair(to + at + kHalf, op, fbar, c + 64, r);
           };
-          ok = fill(whole, 2 * kStageBytes, [&](int kb, uint32_t a, uint32_t b, uint32_t fbar) {
-                 load(m, d.row0 + kb * kBK, a, b, fbar);
-               }) &&
-               fill(nk - whole, 2 * kStageBytes * kGroup / kBK, [&](int, uint32_t a, uint32_t b, uint32_t fbar) {
-                 load(m + 2, d.e * kGroup, a, b, fbar);
-               });
+          ok = fill(whole, 2 * kStageBytes,
+                    [&](int kb, uint32_t at, uint32_t fbar) { load(m, d.row0 + kb * kBK, at, fbar); }) &&
+               fill(nk - whole, 2 * kStageBytes * kGroup / kBK,
+                    [&](int, uint32_t at, uint32_t fbar) { load(m + 2, d.e * kGroup, at, fbar); });
           continue;
         }
         const int tokens = d.swap ? (d.nrows + 15) / 16 * 8 : kBM;   // this CTA's token rows
-        const int nbox = d.swap ? (tokens + kBoxRows - 1) / kBoxRows : 1, row = d.row0 + rank * tokens;
+        const int nbox = d.swap ? (tokens + kBoxRows - 1) / kBoxRows : 1;
         const uint32_t bytes = 2 * (kOperand + (d.swap ? nbox * kBoxRows * 128 : kOperand));
-        auto load_tokens = [&](const CUtensorMap* m, int kb, uint32_t dst, uint32_t fbar) {
-          for (int i = 0; i < nbox; ++i) tc::tma_load_2d_pair(dst + i * kBoxRows * 128, m, fbar, kb * kBK, row + i * kBoxRows);
-        };
-        // a product with the weights read along their rows (dh, dx) ...
-        const CUtensorMap* mt = &P.map[(kDa ? kDy : kDaRows) + (d.swap ? 1 : 0)];
+        if (second) {
+          const int row = d.row0 + rank * tokens;
+          const uint32_t to = d.swap ? sB : sA;
+          for (int sub = 0; sub < products(d) && ok; ++sub) {
+            const CUtensorMap* m = &P.map[(!kDa ? kDaRows : sub == 0 ? kDy : kX) + (d.swap ? 1 : 0)];
+            ok = fill(nk, bytes, [&](int kb, uint32_t at, uint32_t fbar) {
+              for (int i = 0; i < nbox; ++i)
+                tc::tma_load_2d_pair(to + at + i * kBoxRows * 128, m, fbar, kb * kBK, row + i * kBoxRows);
+            });
+          }
+          continue;
+        }
+        // the weights: read along their rows (dh, dx) ...
+        const uint32_t to = d.swap ? sA : sB;
         const CUtensorMap* mw = &P.map[kDa ? kW2 : kW1MN];
-        ok = fill(nk, bytes, [&](int kb, uint32_t a, uint32_t b, uint32_t fbar) {
-          const uint32_t tok = d.swap ? b : a, wgt = d.swap ? a : b;
-          tc::tma_load_3d_pair(wgt, mw, fbar, n, kb * kBK, d.e);
-          tc::tma_load_3d_pair(wgt + kHalf, mw, fbar, n + 64, kb * kBK, d.e);
-          load_tokens(mt, kb, tok, fbar);
+        ok = fill(nk, bytes, [&](int kb, uint32_t at, uint32_t fbar) {
+          tc::tma_load_3d_pair(to + at, mw, fbar, n, kb * kBK, d.e);
+          tc::tma_load_3d_pair(to + at + kHalf, mw, fbar, n + 64, kb * kBK, d.e);
         });
-        // ... and those with both operands K-major (a)
+        // ... or K-major (a)
         if (kDa) {
-          const CUtensorMap* mx = &P.map[kX + (d.swap ? 1 : 0)];
           for (int sub = 1; sub < products(d) && ok; ++sub) {
             const int wrow = !kSwi ? d.e * P.F + n
                                    : d.swap ? (2 * d.e + sub - 1) * P.F + n
                                             : (2 * d.e + rank) * P.F + d.n0 + (sub - 1) * kBM;
-            ok = fill(nk, bytes, [&](int kb, uint32_t a, uint32_t b, uint32_t fbar) {
-              tc::tma_load_2d_pair(d.swap ? a : b, &P.map[kW1], fbar, kb * kBK, wrow);
-              load_tokens(mx, kb, d.swap ? b : a, fbar);
+            ok = fill(nk, bytes, [&](int kb, uint32_t at, uint32_t fbar) {
+              tc::tma_load_2d_pair(to + at, &P.map[kW1], fbar, kb * kBK, wrow);
             });
           }
         }
