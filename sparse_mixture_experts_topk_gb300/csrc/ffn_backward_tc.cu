@@ -711,11 +711,30 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
     if (rank == 0 && tc::elect_one()) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
+      bool ok = true, ready = false;   // ready: the stage at hand was seen full
+      // A stage's MMAs.  This thread's own latency bounds the kernel: a wait
+      // takes 200 cycles even on a barrier that is complete, so the next
+      // stage's is looked at while this one's MMAs are issued, and what does
+      // not change from stage to stage is kept out of here.
+      auto issue = [&](uint32_t dst, uint64_t a0, uint64_t b0, uint64_t as, uint64_t bs, uint32_t idesc, int ng,
+                       uint32_t accumulate) {
+        if (!ready && !tc::mbar_wait(bar.full(stage), phase, &s_abort, kWaitNs)) return false;
+        const int here = stage;
+        advance<kStages>(stage, phase);
+        ready = tc::mbar_try_wait(bar.full(stage), phase);
+        const uint64_t a = a0 + (uint32_t)(here * (kOperand >> 4)), b = b0 + (uint32_t)(here * (kOperand >> 4));
+        tc::mma_bf16_pair(dst, a, b, idesc, accumulate);
+#pragma unroll
+        for (int k = 1; k < kBK / kGroup; ++k)
+          if (k < ng) tc::mma_bf16_pair(dst, a + k * as, b + k * bs, idesc, 1);
+        tc::tc_commit_pair_mc(bar.empty(here), 0x3);
+        return true;
+      };
       Tile next = first < total ? decode(first) : Tile{};
       for (int t = first; t < total && ok; t += step) {
         const Tile d = next;
         const int nk = stages(d), np = products(d), mma_n = d.swap ? (d.nrows + 15) / 16 * 16 : kTile;
+        const int full = d.rows ? row_k / kBK : d.nrows / kBK;   // stages of four groups
         for (int sub = 0; sub < np && ok; ++sub) {
           const bool weights_mn = kDa ? sub == 0 : true;
           const bool a_mn = !d.rows || (d.swap && weights_mn), b_mn = !d.rows || (!d.swap && weights_mn);
@@ -726,22 +745,14 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
           // a descriptor's address is in units of 16 bytes, and no operand leaves its field
           const uint64_t a0 = a_mn ? sdesc_mn128(sA) : tc::sdesc_k128(sA), as = (a_mn ? kStepMN : kStepK) >> 4;
           const uint64_t b0 = b_mn ? sdesc_mn128(sB) : tc::sdesc_k128(sB), bs = (b_mn ? kStepMN : kStepK) >> 4;
-          for (int kb = 0; kb < nk; ++kb) {
-            const int ng = groups(d, kb, nk);
-            if (!tc::mbar_wait(bar.full(stage), phase, &s_abort, kWaitNs)) { ok = false; break; }
-            tc::tc_fence_after();
-            const uint64_t at = (uint64_t)(stage * (kOperand >> 4)), a = a0 + at, b = b0 + at;
-            tc::mma_bf16_pair(dst, a, b, idesc, kb != 0);
-#pragma unroll
-            for (int k = 1; k < kBK / kGroup; ++k)
-              if (k < ng) tc::mma_bf16_pair(dst, a + k * as, b + k * bs, idesc, 1);
-            tc::tc_commit_pair_mc(bar.empty(stage), 0x3);
-            advance<kStages>(stage, phase);
-            // the next tile's divisions run beside the MMAs issued so far
-            if (sub == 0 && kb == min(2, nk - 1) && t + step < total) next = decode(t + step);
-          }
+          int kb = 0;
+#pragma unroll 1
+          for (; kb < full && ok; ++kb) ok = issue(dst, a0, b0, as, bs, idesc, kBK / kGroup, kb != 0);
+          // the next tile's divisions run beside the MMAs issued so far
+          if (sub == np - 1 && t + step < total) next = decode(t + step);
+#pragma unroll 1
+          for (; kb < nk && ok; ++kb) ok = issue(dst, a0, b0, as, bs, idesc, groups(d, kb, nk), kb != 0);
           if (!ok) break;
-          if (nk == 0 && t + step < total) next = decode(t + step);
           tc::tc_commit_pair_mc(bar.tfull(acc), 0x3);
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1u;
