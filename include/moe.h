@@ -1,6 +1,7 @@
 /*
- * moe.h -- C ABI of the top-k gated Mixture-of-Experts FFN layer, forward pass,
- * for one NVIDIA GB300 GPU (sm_103a).
+ * moe.h -- C ABI of the top-k gated Mixture-of-Experts FFN layer for one NVIDIA
+ * GB300 GPU (sm_103a): its forward pass, the gradients of its steps, and an
+ * AdamW step.
  *
  * The layer (sources: "Qwen2-MoE代码解析：MoE架构原理、工程实现与部署避坑指南",
  * jsqmd.com, sections 3.1, 3.3, 3.4; the Qwen2-MoE module article, mlqm.cn,
@@ -329,6 +330,7 @@ int moe_layer_forward(const moe_desc* desc, const void* x, const void* Wg,
  *   moe_combine_backward -> moe_expert_ffn_backward -> moe_dispatch_backward
  * and the optimiser's step, moe_adamw_step.  The pages describe inference and
  * name training only in passing; these are the calculus of the formulas above.
+ * Results must not overlap inputs, unless a call says otherwise.
  */
 
 /*
@@ -382,7 +384,8 @@ int moe_backward_workspace_size(const moe_desc* desc, size_t* bytes);
  *   dW1, dW2 dtype out, shaped as W1 and W2, or NULL; db1, db2 fp32 out
  *   ([E, F] or [E, 2F], and [E, H]) or NULL.  Results are written, not added.
  * On the bf16 path products are accumulated in fp32; da is rounded to bf16 as
- * an operand of the products after it, the bias gradients sum it before that.
+ * an operand of the products after it, the bias gradients sum it before that
+ * (the tensor cores' fp32 sums round towards zero: db1 is about 1e-6 small).
  * Deterministic.  bf16 runs on the tensor cores, fp32 (and MOE_FLAG_SIMT_FFN)
  * on CUDA cores.
  */

@@ -18,7 +18,7 @@
 // thread reads back what it wrote itself: it stays in L2 and needs no
 // synchronisation.  (Both accumulators of a tile side by side would fill TMEM,
 // and no epilogue could overlap the next tile; through memory, with a launch
-// for each product, the two took 435 us instead of @H@ at the prefill layer.)
+// for each product, the two took 435 us instead of 425 at the prefill layer.)
 // (2) The smaller work: see Extras.  (3) dx, dW1 and dW2, which need nothing of
 // one another, the long tiles of dx first.
 //
@@ -39,9 +39,19 @@
 // takes 600 cycles to fill a stage by itself, more than its MMAs take), warp 1
 // MMA issuer (leader CTA of the pair), warps 2-9 epilogue.  Two epilogue warps share a quarter of the TMEM
 // lanes and halve its columns: with one, the slopes of a da tile took longer
-// than its MMAs.  Tiles go round the pairs by number.  Every wait is bounded:
+// than its MMAs.  The other CTA's arrivals that free an accumulator release
+// nothing (only tensor memory was read): with a release each of its tiles
+// took 1000 cycles more, and a layer of 512 tokens and 32 experts (H = 2048,
+// F = 1024) 162 us instead of 140.  Tiles go round the pairs by number.  Every wait is bounded:
 // on expiry the kernel records a timeout in the workspace's error word, drains
 // what it has in flight, frees its tensor memory and returns.
+//
+// Bound by the tensor cores (active 77 % of the cycles in launch 1 and 83 % in
+// 3, on 4096 tokens of 8 experts: 1.6 PFLOP/s) and, in a long run, by the power
+// cap.  Measured: the prefill layer (8192 tokens, H = 3584, E = 32, top-2, F =
+// 2560, 1.5 TFLOP) 425 + 7 + 589 us launch by launch, 1.12 to 1.23 ms in a
+// program that runs nothing else (SM clock 1.7 of 2.07 GHz); with SwiGLU
+// 617 + 9 + 986 us, 1.77 to 1.92 ms.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
@@ -809,10 +819,16 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
   tc::tc_fence_before();
   __syncthreads();
   // after an abort the leader drains its stage barriers, on which both CTAs'
-  // loads complete, before either CTA may leave
-  if (producer && rank == 0 && s_abort)
-    for (int s = 0; s < kStages; ++s)
-      if ((filled >> s) & 1u) tc::mbar_wait(bar.full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
+  // loads complete, before either CTA may leave; loads into a stage that it
+  // had not armed yet are given a millisecond to land
+  if (producer && s_abort) {
+    if (rank == 0)
+      for (int s = 0; s < kStages; ++s)
+        if ((filled >> s) & 1u) tc::mbar_wait(bar.full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
+    const uint64_t t0 = tc::globaltimer();
+    while (tc::globaltimer() - t0 < 1000000ull) {
+    }
+  }
   tc::cluster_sync();   // neither CTA leaves while the other may still signal it
   if (warp == 1) {
     tc::tc_fence_after();
