@@ -16,7 +16,7 @@
 // (they need da and nothing of each other).  The bias gradients are the
 // column sums of the weight gradients' left operand, added up by the blocks
 // of the first column of tiles.  While a block multiplies the reduction
-// elements in shared memory, the next are on their way to registers.
+// elements in shared memory, the next (or the next two) are on their way to registers.
 //
 // A thread always holds 4 x 4 values (two 16-byte reads of shared memory for
 // 16 multiply-adds).  A tile has 64 x 64 values, or 16 rows and 32 columns: eight
@@ -25,7 +25,7 @@
 // rows: the small tiles are used while the experts have less than 32 rows on
 // average, or while tiles of 64 would not be four for every three SMs.
 // Measured, small against large: 64 tokens, H = 256, E = 8, top-2, F = 512:
-// 25.5 us against 59.8; 250 tokens, H = 384, F = 640: 80 against 104, with top-4
+// 23.7 us against 59.8; 250 tokens, H = 384, F = 640: 78 against 104, with top-4
 // 137 against 121.
 #include "common.cuh"
 #include "ffn_backward.cuh"
@@ -39,6 +39,9 @@ constexpr int kThreads = 256;
 // Columns of a row product's tile of kM rows, and the reduction elements staged at a time.
 template <int kM> constexpr int kCols = kM == 16 ? 32 : 64;
 template <int kM> constexpr int kDepth = kM == 16 ? 64 : 32;
+// Stages of dx's operands on their way to registers: a stage of the small tiles has too little to
+// multiply to cover a load's time.
+template <int kM> constexpr int kAhead = kM == 16 ? 2 : 1;
 
 // Row tile `tile` of kM rows: its expert, first row and the expert's end;
 // false past the last tile.  A whole warp.
@@ -90,17 +93,28 @@ __device__ __forceinline__ void store4(bf16* p, const float (&v)[4]) {
 // i, k at i * stride + k) or i does (k * stride + i).  Rows start on 16 bytes
 // and the dimension along them is a multiple of 8, so four elements are
 // inside or outside together; outside (i >= ni, k >= nk) is zero.
+// The transposed writes of a 16-row operand would meet eight at a time in a bank
+// with a warp's lanes along k.  It takes all 16 rows and two vectors along k
+// instead (kSpread): rows of s have 20 floats, four rows are 16 banks apart.
+// (64 tokens, H = 256, E = 8, top-2, F = 512: 25.5 -> 23.9 us, 16 tokens, H = 1024,
+// E = 16: 68.5 -> 60.2; 64-row operands lose 9 % to loads that touch 16 rows.)
 template <int kI, int kBK, bool kAlongK>
 struct Stage {
+  static constexpr bool kSpread = kAlongK && kI == 16;
   static constexpr int kVecs = kI * kBK / 4, kLoads = (kVecs + kThreads - 1) / kThreads;
   float4 v[kLoads];
   __device__ __forceinline__ static int at(int c) { return c * kThreads + threadIdx.x; }
+  __device__ __forceinline__ static int i_of(int c) {
+    return kSpread ? at(c) % 16 : kAlongK ? at(c) / (kBK / 4) : at(c) % (kI / 4) * 4;
+  }
+  __device__ __forceinline__ static int k_of(int c) {
+    return kSpread ? at(c) / 16 * 4 : kAlongK ? at(c) % (kBK / 4) * 4 : at(c) / (kI / 4);
+  }
   template <typename T>
   __device__ __forceinline__ void fetch(const T* __restrict__ src, int64_t stride, int ni, int nk) {
 #pragma unroll
     for (int c = 0; c < kLoads; ++c) {
-      const int i = kAlongK ? at(c) / (kBK / 4) : at(c) % (kI / 4) * 4;
-      const int k = kAlongK ? at(c) % (kBK / 4) * 4 : at(c) / (kI / 4);
+      const int i = i_of(c), k = k_of(c);
       v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < ni && k < nk) v[c] = load4(src + (kAlongK ? i * stride + k : k * stride + i));
     }
@@ -109,14 +123,14 @@ struct Stage {
 #pragma unroll
     for (int c = 0; c < kLoads; ++c) {
       if (at(c) >= kVecs) break;
+      const int i = i_of(c), k = k_of(c);
       if (kAlongK) {
-        const int i = at(c) / (kBK / 4), k = at(c) % (kBK / 4) * 4;
         s[k][i] = v[c].x;
         s[k + 1][i] = v[c].y;
         s[k + 2][i] = v[c].z;
         s[k + 3][i] = v[c].w;
       } else {
-        *reinterpret_cast<float4*>(&s[at(c) / (kI / 4)][at(c) % (kI / 4) * 4]) = v[c];
+        *reinterpret_cast<float4*>(&s[k][i]) = v[c];
       }
     }
   }
@@ -272,21 +286,31 @@ __device__ __forceinline__ void input_tile(const float* __restrict__ da, const i
   const int h0 = col * kN, nr = min(kM, r1 - r0), nh = min(kN, H - h0);
   const float* pa = da + (int64_t)r0 * N;
   const T* pw = W1 + (int64_t)e * N * H + h0;
-  Stage<kM, kBK, true> va;
-  Stage<kN, kBK, false> vw;
+  struct {
+    Stage<kM, kBK, true> a;
+    Stage<kN, kBK, false> w;
+  } v[kAhead<kM>];
   float acc[4][4] = {};
-  auto fetch = [&](int k0) {
-    va.fetch(pa + k0, N, nr, min(kBK, N - k0));
-    vw.fetch(pw + (int64_t)k0 * H, H, nh, min(kBK, N - k0));
+  auto fetch = [&](auto& s, int k0) {
+    const int nk = min(kBK, N - k0);
+    if (nk <= 0) return;
+    s.a.fetch(pa + k0, N, nr, nk);
+    s.w.fetch(pw + (int64_t)k0 * H, H, nh, nk);
   };
-  fetch(0);
-  for (int k0 = 0; k0 < N; k0 += kBK) {
-    va.put(sa);
-    vw.put(sb);
-    __syncthreads();
-    if (k0 + kBK < N) fetch(k0 + kBK);
-    multiply<kM>(acc, sa, sb, at, min(kBK, N - k0));
-    __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kAhead<kM>; ++j) fetch(v[j], j * kBK);
+  for (int kj = 0; kj < N; kj += kAhead<kM> * kBK) {
+#pragma unroll
+    for (int j = 0; j < kAhead<kM>; ++j) {
+      const int k0 = kj + j * kBK, nk = min(kBK, N - k0);
+      if (nk <= 0) break;
+      v[j].a.put(sa);
+      v[j].w.put(sb);
+      __syncthreads();
+      fetch(v[j], k0 + kAhead<kM> * kBK);
+      multiply<kM>(acc, sa, sb, at, nk);
+      __syncthreads();
+    }
   }
   gather<kM>(acc, at, sums);
   store_tile<T, kM>(dx + (int64_t)r0 * H + h0, H, acc, nr, nh, at);
