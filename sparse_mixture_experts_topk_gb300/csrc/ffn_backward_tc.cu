@@ -784,8 +784,6 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
       tc::tc_commit_pair_mc(bar.done(), 0x3);   // both CTAs learn when every MMA has finished
     }
     __syncwarp();
-    if (lane == 0 && !tc::mbar_wait(bar.done(), 0, nullptr, kWaitNs)) set_error(P.err, kDevTimeout);
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, half = (warp - 2) >> 2;   // TMEM lanes 32 q .. 32 q + 31 belong to this warp
@@ -830,6 +828,13 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
   }
   tc::tc_fence_before();
   __syncthreads();
+  // Every MMA has finished before the CTAs part.  Asked for only now that this
+  // CTA's roles are done: warp 1 of the pair's other CTA has no role, and
+  // waiting from the start it would hold the launch, not a wait, to the limit.
+  if (warp == 1) {
+    if (lane == 0 && !tc::mbar_wait(bar.done(), 0, nullptr, kWaitNs)) set_error(P.err, kDevTimeout);
+    __syncwarp();
+  }
   // after an abort the leader drains its stage barriers, on which both CTAs'
   // loads complete, before either CTA may leave; loads into a stage that it
   // had not armed yet are given a millisecond to land

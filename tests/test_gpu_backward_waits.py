@@ -1,0 +1,67 @@
+"""The bounded waits of the expert gradient's tensor-core kernels."""
+import numpy as np
+import pytest
+
+import sparse_mixture_experts_topk_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_mixture_experts_topk_gb300 import build
+    build.build()
+    moe.lib()
+
+
+def test_a_launch_may_take_longer_than_one_wait():
+    """A wait may take two seconds, a launch any number of them.  Tiles go round
+    the SM pairs by number, and with H = F = 8 an expert's dW2 is one tile, so
+    that with rows in every `pairs`-th expert alone one pair computes them all.
+    The rows are chosen for 0.8 s a tile, 3.2 s the launch.  Their values are
+    zero but for a few, at both ends of an expert's rows too, so that the sums
+    are exact."""
+    import torch
+    pairs = min(torch.cuda.get_device_properties(0).multi_processor_count // 2, 80)
+    busy = list(range(0, 256, pairs))[:4]
+    assert len(busy) == 4
+
+    def call(rows):
+        """(seconds, dW2, what it has to be, error word) with `rows` rows an expert."""
+        count = np.zeros(256, np.int64)
+        count[busy] = rows
+        offs = np.concatenate([[0], np.cumsum(count)])
+        desc = moe.make_desc(4 * rows, 8, 256, 1, 8)
+        ws = moe.backward_workspace(desc)
+        dy = torch.zeros((4 * rows, 8), dtype=torch.bfloat16, device="cuda")
+        want = np.zeros((256, 8, 8))
+        rng = np.random.default_rng(rows)
+        for e in busy:
+            for r in (0, 1, rows // 3, rows // 2, rows - 2, rows - 1):
+                v = rng.integers(-4, 5, 8)
+                dy[int(offs[e]) + r] = torch.from_numpy(v).to("cuda", torch.bfloat16)
+                want[e] += np.outer(v, v)
+        dW2 = torch.full((256, 8, 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+        W = torch.zeros(8, dtype=torch.bfloat16, device="cuda")
+        at = torch.from_numpy(offs.astype(np.int32)).cuda()
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        moe.moe_expert_ffn_backward(desc, dy, dy, dy, at, W, None, W, None, None, None, dW2, None, ws)
+        end.record()
+        end.synchronize()
+        return start.elapsed_time(end) / 1e3, dW2.double().cpu().numpy(), want, moe.moe_get_device_error(ws)
+
+    few = (4 << 20) + 5
+    call(few)                                           # the first call of a process, and the clocks
+    took, got, want, error = call(few)
+    assert error == 0 and (got == want).all()           # at most 6 x 16 an entry: exact in bf16
+    rows = int(few * 0.8 / (took / 4)) | 1
+    assert 4 * rows < 2 ** 31 - 256
+    took, got, want, error = call(rows)
+    torch.cuda.empty_cache()
+    assert 2.4 < took < 6.0, took                       # longer than a wait may take, a tile shorter
+    assert (got == want).all()
+    assert error == 0
