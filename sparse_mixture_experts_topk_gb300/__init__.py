@@ -371,7 +371,7 @@ def adamw_tensors(tensors) -> AdamwTensors:
                  f"tensor {i}: not contiguous on one device")
         array[i] = MoeAdamwTensor(_ptr(p), _ptr(p16), _ptr(g), _ptr(m), _ptr(v), _ptr(ms), _ptr(vs), n,
                                   float(d.get("weight_decay", 0.0)), 0)
-        held.append(d)
+        held.append((p, p16, g, m, v, ms, vs))   # not the dict, which is the caller's to change
     return AdamwTensors(array, len(tensors), MOE_F32 if grad_dtype is None else grad_dtype, bits or 32, held)
 
 
