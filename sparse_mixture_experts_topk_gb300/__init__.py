@@ -383,6 +383,12 @@ def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1) -> MoeAdamwParams:
 def moe_adamw_step(tensors: AdamwTensors, params: MoeAdamwParams, grad_scale=None, skip=None, stream=None):
     """One AdamW step in place over ``adamw_tensors(...)``; ``grad_scale`` (fp32)
     and ``skip`` (int32) are one-element device tensors or ``None``."""
+    import torch
+    for name, t, dtype in (("grad_scale", grad_scale, torch.float32), ("skip", skip, torch.int32)):
+        if t is None or isinstance(t, int):     # an address is taken as it is
+            continue
+        if t.dtype != dtype or t.numel() != 1 or not t.is_cuda:
+            raise ValueError(f"moe_adamw_step: {name} is not one {dtype} value on a GPU")
     _check("moe_adamw_step", lib().moe_adamw_step(
         tensors.array, tensors.count, tensors.grad_dtype, tensors.state_bits, ctypes.byref(params),
         _ptr(grad_scale), _ptr(skip), _stream(stream)))

@@ -10,6 +10,12 @@ import sparse_mixture_experts_topk_gb300 as moe
 torch = pytest.importorskip("torch")
 
 
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sparse_mixture_experts_topk_gb300 import build
+    build.build()
+
+
 class OnDevice(torch.Tensor):
     is_cuda = True
 
@@ -39,3 +45,19 @@ def test_a_description_keeps_its_tensors(bits):
     del plan, a
     gc.collect()
     assert all(ref() is None for ref in alive.values())     # and no longer
+
+
+def test_the_steps_two_scalars_are_what_the_kernel_reads():
+    """The kernel reads four bytes of each: a factor in fp32, a flag in int32,
+    on the device.  (With no tensor in the description the call launches nothing.)"""
+    plan, params = moe.adamw_tensors([]), moe.make_adamw(1e-3)
+    scale, skip = t(1), t(1, torch.int32)
+    for ok in ((None, None), (scale, None), (None, skip), (scale, skip), (scale[0], skip[0]), (1 << 20, 1 << 20)):
+        moe.moe_adamw_step(plan, params, *ok, stream=0)
+    for bad in (t(1, torch.bfloat16), t(1, torch.float64), t(1, torch.int32), t(2), t(0), torch.zeros(1)):
+        with pytest.raises(ValueError, match="grad_scale"):
+            moe.moe_adamw_step(plan, params, bad, skip, stream=0)
+    for bad in (t(1, torch.bool), t(1, torch.int64), t(1, torch.uint8), t(1), t(2, torch.int32), t(0, torch.int32),
+                torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="skip"):
+            moe.moe_adamw_step(plan, params, scale, bad, stream=0)
