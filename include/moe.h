@@ -387,7 +387,8 @@ int moe_backward_workspace_size(const moe_desc* desc, size_t* bytes);
  * an operand of the products after it, the bias gradients sum it before that
  * (the tensor cores' fp32 sums round towards zero: db1 is about 1e-6 small).
  * Deterministic.  bf16 runs on the tensor cores, fp32 (and MOE_FLAG_SIMT_FFN)
- * on CUDA cores.
+ * on CUDA cores.  moe_max_rows + 256 (on CUDA cores + 64) has to stay below
+ * 2^31: MOE_ERR_UNSUPPORTED.
  */
 int moe_expert_ffn_backward(const moe_desc* desc, const void* x_perm, const void* h_perm, const void* dy_perm,
                             const int32_t* offs, const void* W1, const float* b1, const void* W2, void* dx_perm,

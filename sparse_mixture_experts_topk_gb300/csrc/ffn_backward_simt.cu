@@ -200,7 +200,8 @@ hidden_gradient_simt_kernel(const T* __restrict__ x, const T* __restrict__ dy, c
   static_assert(kM == 64 || sizeof(sw) >= kGatherFloats * sizeof(float), "the groups' sums reuse the weights' stage");
   pdl_enter();
   int e, r0, r1;
-  if (!row_tile<kM>(offs, E, blockIdx.y, &e, &r0, &r1)) return;
+  // row tiles go on in the grid's third dimension where its second is full
+  if (!row_tile<kM>(offs, E, blockIdx.z * gridDim.y + blockIdx.y, &e, &r0, &r1)) return;
   const Place<kM> at;
   const int f0 = blockIdx.x * kN, nr = min(kM, r1 - r0), nf = min(kN, F - f0);
   const T* px = x + (int64_t)r0 * H;
@@ -391,13 +392,17 @@ cudaError_t run_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, flo
   auto cols = [](int64_t n) { return (n + kCols<kM> - 1) / kCols<kM>; };   // row products
   // at most one part-filled row tile for each expert with rows
   const int64_t mtiles = max_rows / kM + (max_rows < s.E ? max_rows : s.E);
-  if (mtiles > 65535) return cudaErrorNotSupported;
+  const int64_t lim = (int64_t)1 << 31;
+  if (max_rows + 64 >= lim) return cudaErrorNotSupported;   // row numbers go a stage or tile past an expert's end
   const bool hidden = max_rows > 0 && (b.dx_perm || b.dW1 || b.db1);
   if (hidden) {
+    constexpr int64_t kMost = 65535;   // of a grid's second and third dimensions; 2^31 / 16 tiles take 2048 layers
+    const int64_t layers = (mtiles + kMost - 1) / kMost;
     auto k = swi ? hidden_gradient_simt_kernel<T, true, kM> : hidden_gradient_simt_kernel<T, false, kM>;
     const cudaError_t e =
-        launch_kernel(k, dim3((unsigned)cols(s.F), (unsigned)mtiles), dim3(kThreads), 0, st, 1, (const T*)b.x_perm,
-                      (const T*)b.dy_perm, b.offs, s.E, (const T*)b.W1, b.b1, (const T*)b.W2, s.H, s.F, da);
+        launch_kernel(k, dim3((unsigned)cols(s.F), (unsigned)(mtiles < kMost ? mtiles : kMost), (unsigned)layers),
+                      dim3(kThreads), 0, st, 1, (const T*)b.x_perm, (const T*)b.dy_perm, b.offs, s.E,
+                      (const T*)b.W1, b.b1, (const T*)b.W2, s.H, s.F, da);
     if (e != cudaSuccess) return e;
   }
   // a bias gradient alone takes the first column of tiles
@@ -405,7 +410,7 @@ cudaError_t run_simt(const Shape& s, int64_t max_rows, const FfnBackward& b, flo
   const int64_t w1_per = w1_cols * tiles(N), w2_per = w2_cols * tiles(s.H);
   const int64_t dx = hidden && b.dx_perm ? mtiles * cols(s.H) : 0, w1 = w1_per * s.E, all = dx + w1 + w2_per * s.E;
   if (all == 0) return cudaSuccess;
-  if (all >= ((int64_t)1 << 31)) return cudaErrorNotSupported;
+  if (all >= lim) return cudaErrorNotSupported;
   const Tiles t{(int)dx, (int)cols(s.H), (int)w1, (int)w1_cols, (int)w1_per, (int)w2_cols, (int)w2_per};
   return launch_kernel(gradients_simt_kernel<T, kM>, dim3((unsigned)all), dim3(kThreads), 0, st, 1, (const float*)da,
                        b, s.E, s.H, s.F, N, t);
