@@ -380,15 +380,26 @@ def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1) -> MoeAdamwParams:
     return MoeAdamwParams(float(lr), float(beta1), float(beta2), float(eps), int(step))
 
 
+_dtypes = {}
+
+
+def _need_one(name, t, dtype):
+    want = _dtypes.get(dtype)
+    if want is None:
+        import torch
+        want = _dtypes[dtype] = getattr(torch, dtype)
+    if not (t.dtype is want and t.is_cuda and t.numel() == 1):
+        raise ValueError(f"moe_adamw_step: {name} is not one {dtype} value on a GPU")
+
+
 def moe_adamw_step(tensors: AdamwTensors, params: MoeAdamwParams, grad_scale=None, skip=None, stream=None):
     """One AdamW step in place over ``adamw_tensors(...)``; ``grad_scale`` (fp32)
     and ``skip`` (int32) are one-element device tensors or ``None``."""
-    import torch
-    for name, t, dtype in (("grad_scale", grad_scale, torch.float32), ("skip", skip, torch.int32)):
-        if t is None or isinstance(t, int):     # an address is taken as it is
-            continue
-        if t.dtype != dtype or t.numel() != 1 or not t.is_cuda:
-            raise ValueError(f"moe_adamw_step: {name} is not one {dtype} value on a GPU")
+    # an address is taken as it is
+    if grad_scale is not None and not isinstance(grad_scale, int):
+        _need_one("grad_scale", grad_scale, "float32")
+    if skip is not None and not isinstance(skip, int):
+        _need_one("skip", skip, "int32")
     _check("moe_adamw_step", lib().moe_adamw_step(
         tensors.array, tensors.count, tensors.grad_dtype, tensors.state_bits, ctypes.byref(params),
         _ptr(grad_scale), _ptr(skip), _stream(stream)))
