@@ -68,7 +68,10 @@ typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
  * product withholds its first operand load, so the MMA's bounded wait runs
  * out (about 2 s): the kernel records MOE_ERR_TIMEOUT in the workspace error
  * word, drains the loads it issued, frees its tensor memory and returns;
- * outputs are undefined.  It exercises the timeout path without a fault. */
+ * outputs are undefined.  It exercises the timeout path without a fault.
+ * moe_expert_ffn_backward on the tensor cores does the same: the barrier of
+ * each kernel's first stage waits for an arrival that nobody makes (about 4 s
+ * a kernel, the drain's own wait running out too). */
 #define MOE_FLAG_TEST_WAIT_TIMEOUT (1u << 7)
 /* bf16 with SM pairs: every block of an expert's token rows runs with the
  * rows on the MMA's M side (padded to 256), instead of the default where an

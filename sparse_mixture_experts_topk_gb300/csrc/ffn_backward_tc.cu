@@ -322,6 +322,7 @@ struct Params {
   int wm[2], wn[2];        // the weight products' M and N, 0 for none
   bool sectors;            // the rows of da or dx start on 32 bytes
   int* err;
+  int stall;               // testing: 1 = the first stage's barrier waits for an arrival that nobody makes
 };
 enum Map { kDy = 0, kDyBox, kW2, kX, kXBox, kW1, kDaRows = 0, kDaBox, kW1MN, kWeightMaps, kOutMaps = 11 };
 
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
     tile_table(P.offs, E, lane, s_tstart, [&](int rows) { return row_blocks(rows) * nt; });
     if (lane == 0) {
       for (int s = 0; s < kStages; ++s) {
-        tc::mbar_init(bar.full(s), 1);
+        tc::mbar_init(bar.full(s), s == 0 ? 1 + P.stall : 1);
         tc::mbar_init(bar.empty(s), 1);
       }
       for (int a = 0; a < 2; ++a) {
@@ -846,6 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
     while (tc::globaltimer() - t0 < 1000000ull) {
     }
   }
+  __syncwarp();         // the cluster's barrier takes whole warps
   tc::cluster_sync();   // neither CTA leaves while the other may still signal it
   if (warp == 1) {
     tc::tc_fence_after();
@@ -899,6 +901,7 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
   P.N = N;
   P.da = (bf16*)da;
   P.err = err;
+  P.stall = (s.flags & MOE_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
   const bool hidden = b.dx_perm || b.dW1 || b.db1;   // what needs da
   if (hidden) {
     P.stash = stash;

@@ -1,8 +1,13 @@
 """The bounded waits of the expert gradient's tensor-core kernels."""
+import time
+
 import numpy as np
 import pytest
 
 import sparse_mixture_experts_topk_gb300 as moe
+
+from harness import to_dev
+from test_gpu_training import check_ffn, ffn_case, run_ffn, with_tail
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +70,27 @@ def test_a_launch_may_take_longer_than_one_wait():
     assert 2.4 < took < 6.0, took                       # longer than a wait may take, a tile shorter
     assert (got == want).all()
     assert error == 0
+
+
+@pytest.mark.parametrize("act,want", [("gelu", ("dx", "dW1", "db1", "dW2", "db2")), ("swiglu", ("db1",))])
+def test_expired_wait_reports_timeout_and_context_survives(act, want):
+    """The barrier of each kernel's first stage waits for an arrival that nobody
+    makes: every role gives up, what is in flight lands, tensor memory is freed
+    and the error word says so.  The next call, in the same workspace, is right."""
+    import torch
+    c = ffn_case([300, 0, 20, 129], 520, 264, act, True, "bf16", 41)     # full, short and more stages than the ring
+    flags = moe.MOE_FLAG_SWIGLU if act == "swiglu" else 0
+    ws = moe.backward_workspace(moe.make_desc(c["R"], c["H"], c["E"], 1, c["F"], flags=flags))
+    desc = moe.make_desc(c["R"], c["H"], c["E"], 1, c["F"], flags=flags | moe.MOE_FLAG_TEST_WAIT_TIMEOUT)
+    x, h, dy = (with_tail(c[k], c["R"], "bf16") for k in ("x", "h", "dy"))
+    W1, b1, W2 = to_dev(c["W1"], "bf16"), to_dev(c["b1"], "f32"), to_dev(c["W2"], "bf16")
+    o = dict(dx=torch.empty_like(x), dW1=torch.empty_like(W1), db1=torch.empty_like(b1), dW2=torch.empty_like(W2),
+             db2=torch.empty((c["E"], c["H"]), device="cuda"))
+    start = time.time()
+    moe.moe_expert_ffn_backward(desc, x, h, dy, to_dev(c["offs"], "i32"), W1, b1, W2,
+                                *(o[k] if k in want else None for k in o), ws)
+    torch.cuda.synchronize()
+    took = time.time() - start
+    assert moe.moe_get_device_error(ws) == moe.MOE_ERR_TIMEOUT
+    assert took < 30.0
+    check_ffn(c, run_ffn(c, ws=ws))                 # the read cleared the error word
