@@ -80,7 +80,10 @@ static_assert(kEpiWarps * kStoreBytes == kStageBytes, "the store tiles take a st
 constexpr int kThreads = 64 + 32 * kEpiWarps + 32, kSecondProducer = 2 + kEpiWarps;
 constexpr int kMaxPairs = 80;             // bounds the dh scratch: 128 KB for each CTA
 constexpr int kStash = kBM * kTile;       // its fp32 values
-constexpr uint64_t kWaitNs = 2000000000ull;
+// The limit of a wait, and what the epilogue's wait for a tile has on top for
+// each stage of its reduction: a weight product's goes over all of an expert's
+// rows (264 ns a stage of 64 rows at H = F = 8: two seconds are 485 M rows).
+constexpr uint64_t kWaitNs = 2000000000ull, kStageNs = 2000;
 
 // Shared-memory descriptor of an MN-major operand of 128 x 64: two boxes (64
 // columns of 128 bytes, 64 rows, 128-byte swizzle) one after the other.
@@ -797,8 +800,9 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
     for (int t = first; t < total && ok; t += step) {
       const Tile d = decode(t);
       const int np = products(d);
+      const uint64_t limit = kWaitNs + (uint64_t)stages(d) * kStageNs;
       for (int sub = 0; sub < np; ++sub) {
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.tfull(acc), acc_phase, &s_abort, kWaitNs))) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(bar.tfull(acc), acc_phase, &s_abort, limit))) {
           give_up(P.err, &s_abort);
           ok = false;
           break;

@@ -22,54 +22,70 @@ def _built():
     moe.lib()
 
 
-def test_a_launch_may_take_longer_than_one_wait():
-    """A wait may take two seconds, a launch any number of them.  Tiles go round
-    the SM pairs by number, and with H = F = 8 an expert's dW2 is one tile, so
-    that with rows in every `pairs`-th expert alone one pair computes them all.
-    The rows are chosen for 0.8 s a tile, 3.2 s the launch.  Their values are
-    zero but for a few, at both ends of an expert's rows too, so that the sums
-    are exact."""
+def second_weight_gradient(counts):
+    """dW2 alone of experts with these rows, H = F = 8: (seconds, dW2, what it has
+    to be, error word).  The rows are zero but for a few, at both ends of an
+    expert's rows too, so that the sums are exact."""
+    import torch
+    E, total = len(counts), int(np.sum(counts))
+    offs = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+    desc = moe.make_desc(total, 8, E, 1, 8)
+    ws = moe.backward_workspace(desc)
+    dy = torch.zeros((total, 8), dtype=torch.bfloat16, device="cuda")
+    want = np.zeros((E, 8, 8))
+    rng = np.random.default_rng(total)
+    for e in np.flatnonzero(counts):
+        n = int(counts[e])
+        for r in (0, 1, n // 3, n // 2, n - 2, n - 1):
+            v = rng.integers(-4, 5, 8)
+            dy[int(offs[e]) + r] = torch.from_numpy(v).to("cuda", torch.bfloat16)
+            want[e] += np.outer(v, v)                    # at most 6 x 16 an entry: exact in bf16
+    dW2 = torch.full((E, 8, 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    W = torch.zeros(8, dtype=torch.bfloat16, device="cuda")
+    at = torch.from_numpy(offs.astype(np.int32)).cuda()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    moe.moe_expert_ffn_backward(desc, dy, dy, dy, at, W, None, W, None, None, None, dW2, None, ws)
+    end.record()
+    end.synchronize()
+    return start.elapsed_time(end) / 1e3, dW2.double().cpu().numpy(), want, moe.moe_get_device_error(ws)
+
+
+def long_tile(tiles, seconds):
+    """`tiles` experts of one tile each, which one SM pair computes one after
+    another, `seconds` each: tiles go round the pairs by number, and with H = F =
+    8 an expert's dW2 is one tile.  The total has to be longer than a wait may take."""
     import torch
     pairs = min(torch.cuda.get_device_properties(0).multi_processor_count // 2, 80)
-    busy = list(range(0, 256, pairs))[:4]
-    assert len(busy) == 4
+    busy = list(range(0, 256, pairs))[:tiles]
+    assert len(busy) == tiles
 
-    def call(rows):
-        """(seconds, dW2, what it has to be, error word) with `rows` rows an expert."""
-        count = np.zeros(256, np.int64)
-        count[busy] = rows
-        offs = np.concatenate([[0], np.cumsum(count)])
-        desc = moe.make_desc(4 * rows, 8, 256, 1, 8)
-        ws = moe.backward_workspace(desc)
-        dy = torch.zeros((4 * rows, 8), dtype=torch.bfloat16, device="cuda")
-        want = np.zeros((256, 8, 8))
-        rng = np.random.default_rng(rows)
-        for e in busy:
-            for r in (0, 1, rows // 3, rows // 2, rows - 2, rows - 1):
-                v = rng.integers(-4, 5, 8)
-                dy[int(offs[e]) + r] = torch.from_numpy(v).to("cuda", torch.bfloat16)
-                want[e] += np.outer(v, v)
-        dW2 = torch.full((256, 8, 8), float("nan"), dtype=torch.bfloat16, device="cuda")
-        W = torch.zeros(8, dtype=torch.bfloat16, device="cuda")
-        at = torch.from_numpy(offs.astype(np.int32)).cuda()
-        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
-        start.record()
-        moe.moe_expert_ffn_backward(desc, dy, dy, dy, at, W, None, W, None, None, None, dW2, None, ws)
-        end.record()
-        end.synchronize()
-        return start.elapsed_time(end) / 1e3, dW2.double().cpu().numpy(), want, moe.moe_get_device_error(ws)
+    def counts(rows):
+        c = np.zeros(256 if tiles > 1 else 1, np.int64)
+        c[busy] = rows
+        return c
 
     few = (4 << 20) + 5
-    call(few)                                           # the first call of a process, and the clocks
-    took, got, want, error = call(few)
-    assert error == 0 and (got == want).all()           # at most 6 x 16 an entry: exact in bf16
-    rows = int(few * 0.8 / (took / 4)) | 1
-    assert 4 * rows < 2 ** 31 - 256
-    took, got, want, error = call(rows)
+    second_weight_gradient(counts(few))                  # the first call of a process, and the clocks
+    took, got, want, error = second_weight_gradient(counts(few))
+    assert error == 0 and (got == want).all()
+    rows = int(few * seconds / (took / tiles)) | 1
+    assert tiles * rows < 2 ** 31 - 256
+    took, got, want, error = second_weight_gradient(counts(rows))
     torch.cuda.empty_cache()
-    assert 2.4 < took < 6.0, took                       # longer than a wait may take, a tile shorter
+    assert 2.3 < took < 6.0, took
     assert (got == want).all()
     assert error == 0
+
+
+def test_a_launch_may_take_longer_than_one_wait():
+    """A wait may take two seconds, a launch any number of them."""
+    long_tile(4, 0.8)
+
+
+def test_a_tile_may_take_longer_than_two_seconds():
+    """The wait for an accumulator lasts as long as its tile's reduction."""
+    long_tile(1, 2.8)
 
 
 @pytest.mark.parametrize("act,want", [("gelu", ("dx", "dW1", "db1", "dW2", "db2")), ("swiglu", ("db1",))])
