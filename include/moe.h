@@ -387,8 +387,10 @@ int moe_backward_workspace_size(const moe_desc* desc, size_t* bytes);
  *   dW1, dW2 dtype out, shaped as W1 and W2, or NULL; db1, db2 fp32 out
  *   ([E, F] or [E, 2F], and [E, H]) or NULL.  Results are written, not added.
  * On the bf16 path products are accumulated in fp32; da is rounded to bf16 as
- * an operand of the products after it, the bias gradients sum it before that
- * (the tensor cores' fp32 sums round towards zero: db1 is about 1e-6 small).
+ * an operand of the products after it (on CUDA cores it stays in fp32), the
+ * bias gradients sum it before that.  The tensor cores' fp32 sums round
+ * towards zero: db1, which is not rounded to bf16 after them, is about 1e-6
+ * small.
  * Deterministic.  bf16 runs on the tensor cores, fp32 (and MOE_FLAG_SIMT_FFN)
  * on CUDA cores.  moe_max_rows + 256 (on CUDA cores + 64) has to stay below
  * 2^31: MOE_ERR_UNSUPPORTED.
@@ -448,8 +450,14 @@ typedef struct moe_adamw_params {
  *   grad_dtype: moe_dtype of every grad; state_bits: 32 or 8, for every tensor
  *   grad_scale [1] fp32 device or NULL (a clipping or loss-scale factor)
  *   skip [1] int32 device or NULL: nothing is changed if it is not 0
- * 8-bit moments are rounded to nearest; a block of moments with a NaN or an
- * infinity reads back as NaN throughout (guard it with skip).
+ * p's quotient is within 2 units of its last place.
+ * 8-bit moments are rounded to nearest, code = e4m3(x * (1 / largest) * 448); a
+ * block of moments with a NaN or an infinity reads back as NaN throughout
+ * (guard it with skip).  A code moves only where one step changes its value,
+ * as a share of its block's largest, by half a code (3 to 6 %).  For sqrt(v)
+ * that takes a gradient of 8 to 11 times sqrt(v) with beta2 = 0.999, of 1.5 to
+ * 1.9 times with 0.95, and it decays only as fast as its block's largest does:
+ * 8 bits go with a beta2 of about 0.95 or below.
  */
 int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t grad_dtype, int32_t state_bits,
                    const moe_adamw_params* params, const float* grad_scale, const int32_t* skip, void* stream);

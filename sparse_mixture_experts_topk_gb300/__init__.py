@@ -376,7 +376,8 @@ def adamw_tensors(tensors) -> AdamwTensors:
 
 
 def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1) -> MoeAdamwParams:
-    """The hyperparameters of one step; ``step`` counts from 1."""
+    """The hyperparameters of one step; ``step`` counts from 1.  8-bit moments
+    want ``beta2`` of about 0.95: with 0.999 most steps round to no change of v."""
     return MoeAdamwParams(float(lr), float(beta1), float(beta2), float(eps), int(step))
 
 

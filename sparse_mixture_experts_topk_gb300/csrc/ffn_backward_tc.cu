@@ -46,12 +46,15 @@
 // on expiry the kernel records a timeout in the workspace's error word, drains
 // what it has in flight, frees its tensor memory and returns.
 //
-// Bound by the tensor cores (active 77 % of the cycles in launch 1 and 83 % in
-// 3, on 4096 tokens of 8 experts: 1.6 PFLOP/s) and, in a long run, by the power
-// cap.  Measured: the prefill layer (8192 tokens, H = 3584, E = 32, top-2, F =
-// 2560, 1.5 TFLOP) 425 + 7 + 589 us launch by launch, 1.12 to 1.23 ms in a
-// program that runs nothing else (SM clock 1.7 of 2.07 GHz); with SwiGLU
-// 617 + 9 + 986 us, 1.77 to 1.92 ms.
+// What bounds it is what a stage costs whatever its MMAs take: 590 to 605
+// cycles where a row product's take 512, 570 where a swapped block's take 64,
+// 610 to 700 for a weight product.  (The tensor pipe is active 77 % of the
+// cycles in launch 1 and 83 % in 3 on 4096 tokens of 8 experts, where there are
+// few short blocks: 1.6 PFLOP/s.)  Measured: the prefill layer (8192 tokens, H =
+// 3584, E = 32, top-2, F = 2560, 1.5 TFLOP) 425 + 7 + 589 us launch by launch,
+// 1.12 to 1.23 ms in a program that runs nothing else (SM clock 1.7 of 2.07 GHz,
+// at which 1.27 PFLOP/s are 60 % of what the tensor cores could do, so the power
+// cap is not the limit); with SwiGLU 617 + 9 + 986 us, 1.77 to 1.92 ms.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
@@ -283,7 +286,7 @@ __device__ __forceinline__ void sum_rows(const Extras& x, const int32_t* __restr
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[(g * kSumVecs + threadIdx.x % kSumVecs) * 8 + i] = sum[i];
   __syncthreads();
-  const int c = threadIdx.x;   // one column of the block's 64
+  const int c = threadIdx.x;   // one column of the block's 32
   if (c < kSumVecs * 8 && col * kSumVecs * 8 + c < x.h) {
     float total = 0.f;
     for (int i = 0; i < kSumGroups; ++i) total += s[i * kSumVecs * 8 + c];
@@ -738,10 +741,13 @@ __global__ void __launch_bounds__(kThreads, 1) backward_pair_kernel(const __grid
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, ready = false;   // ready: the stage at hand was seen full
-      // A stage's MMAs.  This thread's own latency bounds the kernel: a wait
-      // takes 200 cycles even on a barrier that is complete, so the next
-      // stage's is looked at while this one's MMAs are issued, and what does
-      // not change from stage to stage is kept out of here.
+      // A stage's MMAs.  This thread's own latency counts: a wait takes 200
+      // cycles even on a barrier that is complete, so the next stage's is
+      // looked at before this one's MMAs are issued, under those still running
+      // (1 to 2 % at every size), and what does not change from stage to stage
+      // is kept out of here.  The look may suspend the thread for a while: when
+      // the ring is dry, and at a pair's last stage, which no other follows,
+      // MMAs that could start wait with it.
       auto issue = [&](uint32_t dst, uint64_t a0, uint64_t b0, uint64_t as, uint64_t bs, uint32_t idesc, int ng,
                        uint32_t accumulate) {
         if (!ready && !tc::mbar_wait(bar.full(stage), phase, &s_abort, kWaitNs)) return false;
