@@ -463,6 +463,140 @@ int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t grad_
                    const moe_adamw_params* params, const float* grad_scale, const int32_t* skip, void* stream);
 
 /*
+ * Load-balancing loss over the tokens that count, and the statistics that its
+ * gradient needs: with p = softmax(logits / temperature),
+ *   tokens = the number n of tokens with mask[t] != 0 (T without a mask)
+ *   count[e] = their slots with ids = e;  psum[e] = the sum of their p[t, e]
+ *   loss = E * sum_e count[e] / (n K) * psum[e] / n       (0 if n = 0)
+ * moe_aux_loss of a whole batch is the same number.  A token with mask[t] = 0
+ * (the padding of a batch of sequences) takes no part, whatever its scores
+ * and ids hold.
+ *   logits [T, E] fp32; ids [T, K] int32: moe_router_topk's (an id of -1 counts
+ *   for no expert)
+ *   mask [T] bytes or NULL
+ *   psum [E] fp32 out, count [E] int32 out, tokens [1] int32 out, loss [1] fp32
+ *   out, or NULL each.  Ranks of a data-parallel batch add up the first three
+ *   before they take the loss (moe_aux_loss) or its gradient.
+ *   ws: of moe_router_backward_workspace_size() bytes
+ * psum is summed in a fixed order, in fp32 over at most 2^13 tokens and in fp64
+ * beyond.  An id outside [-1, E) of a token that counts sets MOE_ERR_DEVICE in
+ * the workspace error word and counts for no expert.  Deterministic.
+ */
+int moe_balance_loss(const moe_desc* desc, const float* logits, const int32_t* ids, const uint8_t* mask,
+                     float* psum, int32_t* count, int32_t* tokens, float* loss, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* Bytes of device workspace moe_balance_loss and moe_router_backward need for
+ * `desc`; its first 256 bytes (the error word among them) have to be zeros
+ * before the first call.  Returns MOE_ERR_INVALID for a bad desc. */
+int moe_router_backward_workspace_size(const moe_desc* desc, size_t* bytes);
+
+/*
+ * Gradient of moe_router_topk's weights w and of moe_balance_loss, through the
+ * softmax to the scores and through the gate's product to its matrix and x:
+ *   dlogits[t, e] = 1 / temperature * (
+ *       sum over j with ids[t, j] = e of w_j (dw[t, j] - sum_i w_i dw[t, i])
+ *       + p_e (c_e - sum_i p_i c_i) ),   c_e = dloss E count[e] / (n^2 K)
+ *   dWg = dlogits^T x,  dgate_bias = sum_t dlogits[t],  dx = dlogits Wg
+ * with w computed again as the softmax over the scores of the token's ids.
+ * Tokens with mask[t] = 0 have dlogits and dx of zeros and add nothing to dWg
+ * and dgate_bias, whatever x, logits, ids and dw hold for them.
+ *   x [T, H] dtype (not read if dWg is NULL, may be NULL then)
+ *   Wg [E, H] dtype (not read if dx is NULL, may be NULL then)
+ *   logits [T, E] fp32, ids [T, K] int32: the forward pass's; an id of -1 has
+ *   no weight, an id outside [-1, E) the same, with MOE_ERR_DEVICE in the
+ *   workspace error word
+ *   dw [T, K] fp32 or NULL (no gradient of the weights): moe_combine_backward's
+ *   dloss [1] fp32 device or NULL (no gradient of the loss): the loss' factor
+ *   in what is minimised; then count [E] and tokens [1] (device): those of the
+ *   loss, over every rank's tokens if the loss is; they may be NULL without it
+ *   dlogits [T, E] fp32 out, dWg [E, H] fp32 out, dgate_bias [E] fp32 out,
+ *   dx [T, H] dtype out, or NULL each, not all.  Results are written, not added:
+ *   dx goes to moe_dispatch_backward as dx_add.
+ * bf16: the products run on the tensor cores, dlogits split in three bf16 parts
+ * for dWg (24 bits) and two for dx (16 bits, which is rounded to 8), fp32 sums.
+ * fp32 and MOE_FLAG_SIMT_ROUTER: CUDA cores.  Deterministic.
+ */
+int moe_router_backward(const moe_desc* desc, const void* x, const void* Wg, const float* logits,
+                        const int32_t* ids, const float* dw, const float* dloss, const int32_t* count,
+                        const int32_t* tokens, const uint8_t* mask, float* dlogits, float* dWg, float* dgate_bias,
+                        void* dx, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Orthogonalised updates.  A matrix u [rows, cols] is made nearly orthogonal by
+ * Newton-Schulz products: with X = u / |u| (Frobenius norm; zeros for a zero
+ * matrix), transposed if rows > cols so that its rows are the short side,
+ *   `iterations` times: A = X X^T;  X = (a I + b A + c A A) X
+ *   (a, b, c) = (3.4445, -4.7750, 2.0315)
+ * which takes every singular value that is not tiny into about [0.7, 1.2] (five
+ * iterations: those above 1/500 of |u|).  X and the products are held in fp16
+ * times 2^12, their sums in fp32: the result is within about 2e-3 of the exact
+ * iteration's, relative, in the 2-norm of the elements.  A matrix with a NaN or
+ * an infinity becomes NaN throughout; the others of its batch do not.
+ */
+#define MOE_ORTHOGONALIZE_MAX_SIDE 32768       /* rows, cols <= this */
+#define MOE_ORTHOGONALIZE_MAX_ITERATIONS 16
+
+/* Bytes of device workspace moe_orthogonalize needs for `batch` matrices (a
+ * large batch runs in parts); its first 256 bytes have to be zeros before the
+ * first call. */
+int moe_orthogonalize_workspace_size(int64_t batch, int32_t rows, int32_t cols, size_t* bytes);
+
+/*
+ * out[i] = x[i] made nearly orthogonal, for each of `batch` matrices.
+ *   x, out [batch, rows, cols], of dtype x_dtype and out_dtype (moe_dtype),
+ *   aligned to their element; out may be x if the dtypes are the same
+ */
+int moe_orthogonalize(const void* x, int32_t x_dtype, int64_t batch, int32_t rows, int32_t cols, int32_t iterations,
+                      void* out, int32_t out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One parameter tensor of moe_muon_step: `batch` matrices [rows, cols] one
+ * after the other (an expert's W1 each, say; SwiGLU's stacked W1 is 2 E
+ * matrices [F, H]), each orthogonalised by itself.  Device pointers, aligned to
+ * their element.  Tensors of one call must not overlap.
+ */
+typedef struct moe_muon_tensor {
+  float* p;            /* [batch, rows, cols] fp32                             */
+  void* p_bf16;        /* the same in bf16, or NULL: receives p rounded        */
+  const void* grad;    /* fp32 or bf16 (grad_dtype of the call)                */
+  float* m;            /* fp32 momentum; zeros are the start                   */
+  int64_t batch;
+  int32_t rows, cols;
+  float weight_decay;  /* decoupled, for this tensor                           */
+  float scale;         /* of its orthogonalised update, e.g. 0.2 sqrt(max(rows, cols)) */
+} moe_muon_tensor;
+
+/* lr >= 0, 0 <= momentum < 1, finite; nesterov 0 or 1; 1 <= iterations <=
+ * MOE_ORTHOGONALIZE_MAX_ITERATIONS. */
+typedef struct moe_muon_params {
+  double lr;
+  double momentum;
+  int32_t nesterov;
+  int32_t iterations;
+} moe_muon_params;
+
+/* Bytes of device workspace moe_muon_step needs for these tensors; its first
+ * 256 bytes have to be zeros before the first call. */
+int moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count, size_t* bytes);
+
+/*
+ * One Muon step over `count` tensors, in place:
+ *   g = grad * (grad_scale ? *grad_scale : 1)
+ *   m = momentum m + g;   u = nesterov ? g + momentum m : m
+ *   p = p (1 - lr weight_decay) - lr scale orthogonalize(u)
+ * in fp32 but for the orthogonalisation (see above).  Matrices of one size,
+ * whichever way round they lie, run together.
+ *   tensors: host array, read during the call only
+ *   grad_dtype: moe_dtype of every grad
+ *   grad_scale [1] fp32 device or NULL; skip [1] int32 device or NULL: nothing
+ *   is changed if it is not 0
+ * Deterministic.
+ */
+int moe_muon_step(const moe_muon_tensor* tensors, int32_t count, int32_t grad_dtype, const moe_muon_params* params,
+                  const float* grad_scale, const int32_t* skip, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * How many kernels one moe_layer_forward with this description launches
  * (no counterpart on the pages; it lets a caller or a benchmark account for
  * the launches it issues).  Depends on the shape only: the path taken

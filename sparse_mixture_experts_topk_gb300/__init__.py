@@ -29,6 +29,10 @@ __all__ = [
     "moe_combine_backward", "moe_dispatch_backward", "moe_backward_workspace_size", "backward_workspace",
     "moe_expert_ffn_backward", "moe_adamw_step", "MOE_ADAMW_BLOCK", "MoeAdamwTensor", "MoeAdamwParams",
     "AdamwTensors", "adamw_tensors", "make_adamw",
+    "moe_balance_loss", "moe_router_backward", "moe_router_backward_workspace_size", "router_backward_workspace",
+    "moe_orthogonalize", "moe_orthogonalize_workspace_size", "orthogonalize_workspace",
+    "MOE_ORTHOGONALIZE_MAX_SIDE", "MOE_ORTHOGONALIZE_MAX_ITERATIONS", "moe_muon_step", "moe_muon_workspace_size",
+    "MoeMuonTensor", "MoeMuonParams", "MuonTensors", "muon_tensors", "make_muon", "muon_workspace",
 ]
 
 MOE_F32, MOE_BF16 = 0, 1
@@ -50,6 +54,9 @@ MOE_FLAG_GATHER_GEMM = 1 << 13
 MOE_FFN_STREAM, MOE_FFN_SIMT, MOE_FFN_TC_SINGLE, MOE_FFN_TC_PAIRS, MOE_FFN_TC_FUSED, MOE_FFN_STREAM_SPLIT = 0, 1, 2, 3, 4, 5
 
 MOE_ADAMW_BLOCK = 256   # elements that share a scale in 8-bit moments
+
+MOE_ORTHOGONALIZE_MAX_SIDE = 32768
+MOE_ORTHOGONALIZE_MAX_ITERATIONS = 16
 
 # status codes (MoeError.code)
 MOE_OK = 0
@@ -84,6 +91,17 @@ class MoeAdamwParams(ctypes.Structure):
                 ("eps", ctypes.c_double), ("step", ctypes.c_int64)]
 
 
+class MoeMuonTensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("p_bf16", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("batch", ctypes.c_int64), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("weight_decay", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class MoeMuonParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("nesterov", ctypes.c_int32),
+                ("iterations", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -109,6 +127,17 @@ _SIGS = {
     "moe_expert_ffn_backward": (ctypes.c_int, [ctypes.POINTER(MoeDesc)] + [_P] * 13 + [ctypes.c_size_t, _P]),
     "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(MoeAdamwTensor), ctypes.c_int32, ctypes.c_int32,
                                       ctypes.c_int32, ctypes.POINTER(MoeAdamwParams), _P, _P, _P]),
+    "moe_balance_loss": (ctypes.c_int, [ctypes.POINTER(MoeDesc)] + [_P] * 8 + [ctypes.c_size_t, _P]),
+    "moe_router_backward_workspace_size": (ctypes.c_int, [ctypes.POINTER(MoeDesc), ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_router_backward": (ctypes.c_int, [ctypes.POINTER(MoeDesc)] + [_P] * 14 + [ctypes.c_size_t, _P]),
+    "moe_orthogonalize_workspace_size": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                                        ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_orthogonalize": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                         ctypes.c_int32, _P, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "moe_muon_workspace_size": (ctypes.c_int, [ctypes.POINTER(MoeMuonTensor), ctypes.c_int32,
+                                               ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_muon_step": (ctypes.c_int, [ctypes.POINTER(MoeMuonTensor), ctypes.c_int32, ctypes.c_int32,
+                                     ctypes.POINTER(MoeMuonParams), _P, _P, _P, ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -384,13 +413,13 @@ def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1) -> MoeAdamwParams:
 _dtypes = {}
 
 
-def _need_one(name, t, dtype):
+def _need_one(name, t, dtype, fn="moe_adamw_step"):
     want = _dtypes.get(dtype)
     if want is None:
         import torch
         want = _dtypes[dtype] = getattr(torch, dtype)
     if not (t.dtype is want and t.is_cuda and t.numel() == 1):
-        raise ValueError(f"moe_adamw_step: {name} is not one {dtype} value on a GPU")
+        raise ValueError(f"{fn}: {name} is not one {dtype} value on a GPU")
 
 
 def moe_adamw_step(tensors: AdamwTensors, params: MoeAdamwParams, grad_scale=None, skip=None, stream=None):
@@ -404,6 +433,159 @@ def moe_adamw_step(tensors: AdamwTensors, params: MoeAdamwParams, grad_scale=Non
     _check("moe_adamw_step", lib().moe_adamw_step(
         tensors.array, tensors.count, tensors.grad_dtype, tensors.state_bits, ctypes.byref(params),
         _ptr(grad_scale), _ptr(skip), _stream(stream)))
+
+
+def moe_balance_loss(desc, logits, ids, mask, psum, count, tokens, loss, ws, stream=None):
+    """The load-balancing loss over the tokens that ``mask`` ([T] ``bool`` or
+    ``uint8``, or ``None``) keeps, with its counts and probability sums."""
+    _check("moe_balance_loss", lib().moe_balance_loss(
+        ctypes.byref(desc), _ptr(logits), _ptr(ids), _ptr(mask), _ptr(psum), _ptr(count), _ptr(tokens), _ptr(loss),
+        _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def moe_router_backward_workspace_size(desc: MoeDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_router_backward_workspace_size",
+           lib().moe_router_backward_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _cleared(nbytes, device):
+    import torch
+    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device if device is not None else "cuda")
+    ws[:256].zero_()
+    return ws
+
+
+def router_backward_workspace(desc: MoeDesc, device=None):
+    """A device workspace for ``moe_balance_loss`` and ``moe_router_backward``, its first 256 bytes cleared."""
+    return _cleared(moe_router_backward_workspace_size(desc), device)
+
+
+def moe_router_backward(desc, x, Wg, logits, ids, dw, dloss, count, tokens, mask, dlogits, dWg, dgate_bias, dx, ws,
+                        stream=None):
+    _check("moe_router_backward", lib().moe_router_backward(
+        ctypes.byref(desc), _ptr(x), _ptr(Wg), _ptr(logits), _ptr(ids), _ptr(dw), _ptr(dloss), _ptr(count),
+        _ptr(tokens), _ptr(mask), _ptr(dlogits), _ptr(dWg), _ptr(dgate_bias), _ptr(dx), _ptr(ws),
+        ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def moe_orthogonalize_workspace_size(batch: int, rows: int, cols: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_orthogonalize_workspace_size",
+           lib().moe_orthogonalize_workspace_size(int(batch), int(rows), int(cols), ctypes.byref(n)))
+    return int(n.value)
+
+
+def orthogonalize_workspace(batch: int, rows: int, cols: int, device=None):
+    """A device workspace for ``moe_orthogonalize`` of ``batch`` matrices, its first 256 bytes cleared."""
+    return _cleared(moe_orthogonalize_workspace_size(batch, rows, cols), device)
+
+
+def _moe_dtype(t, fn, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return MOE_BF16
+    if t.dtype == torch.float32:
+        return MOE_F32
+    raise ValueError(f"{fn}: {name} is neither fp32 nor bf16")
+
+
+def moe_orthogonalize(x, out, iterations, ws, stream=None):
+    """``out[i] = x[i]`` made nearly orthogonal by ``iterations`` Newton-Schulz
+    steps, for one matrix [rows, cols] or a batch [..., rows, cols]; ``out`` of
+    the same shape, each fp32 or bf16."""
+    if x.dim() < 2 or x.shape != out.shape:
+        raise ValueError("moe_orthogonalize: x and out are not matrices of one shape")
+    if not (x.is_cuda and out.is_cuda and x.device == out.device and x.is_contiguous() and out.is_contiguous()):
+        raise ValueError("moe_orthogonalize: not contiguous on one device")
+    rows, cols = x.shape[-2:]
+    if x.numel() == 0:
+        return
+    _check("moe_orthogonalize", lib().moe_orthogonalize(
+        _ptr(x), _moe_dtype(x, "moe_orthogonalize", "x"), x.numel() // (rows * cols), rows, cols, int(iterations),
+        _ptr(out), _moe_dtype(out, "moe_orthogonalize", "out"), _ptr(ws), ws.numel() if ws is not None else 0,
+        _stream(stream)))
+
+
+class MuonTensors:
+    """The tensors of a ``moe_muon_step``, kept by the caller from step to step."""
+
+    def __init__(self, array, count, grad_dtype, held):
+        self.array, self.count, self.grad_dtype = array, count, grad_dtype
+        self.held = held          # the tensors the addresses belong to
+
+
+def muon_tensors(tensors) -> MuonTensors:
+    """Describe the parameter tensors of a Muon step once.
+
+    ``tensors``: one dict per parameter tensor with contiguous device tensors
+    ``p`` (fp32, [rows, cols] or a batch of such matrices [..., rows, cols]),
+    ``g`` (fp32 or bf16, the same for all), ``m`` (fp32) of the same shape, and
+    optionally ``p16`` (bf16 copy of p), ``weight_decay`` and ``scale`` (of the
+    orthogonalised update; 0.2 sqrt(max(rows, cols)) by default, which gives it
+    the size of an AdamW step's).  The addresses are read here, so the same
+    tensors have to stay in place for every step that uses the result."""
+    import torch
+    tensors = list(tensors)
+    array = (MoeMuonTensor * max(1, len(tensors)))()
+    held, grad_dtype = [], None
+
+    def need(ok, what):
+        if not ok:
+            raise ValueError(f"muon_tensors: {what}")
+
+    for i, d in enumerate(tensors):
+        unknown = set(d) - {"p", "p16", "g", "m", "weight_decay", "scale"}
+        need(not unknown, f"tensor {i}: unknown fields {sorted(unknown)}")
+        p, g, m, p16 = d["p"], d["g"], d["m"], d.get("p16")
+        need(p.dim() >= 2, f"tensor {i}: p is not a matrix or a batch of matrices")
+        need(p.dtype == torch.float32, f"tensor {i}: p is not fp32")
+        need(m.dtype == torch.float32, f"tensor {i}: m is not fp32")
+        need(g.dtype in (torch.float32, torch.bfloat16), f"tensor {i}: g is neither fp32 nor bf16")
+        need(p16 is None or p16.dtype == torch.bfloat16, f"tensor {i}: p16 is not bf16")
+        gd = MOE_BF16 if g.dtype == torch.bfloat16 else MOE_F32
+        need(grad_dtype in (None, gd), f"tensor {i}: another gradient type than before")
+        grad_dtype = gd
+        for t in (p, g, m) + (() if p16 is None else (p16,)):
+            need(t.shape == p.shape, f"tensor {i}: shapes differ")
+            need(t.is_contiguous() and t.device == p.device and t.is_cuda, f"tensor {i}: not contiguous on one device")
+        rows, cols = p.shape[-2:]
+        batch = p.numel() // (rows * cols) if rows and cols else 0
+        scale = float(d.get("scale", 0.2 * max(rows, cols) ** 0.5))
+        array[i] = MoeMuonTensor(_ptr(p), _ptr(p16), _ptr(g), _ptr(m), batch, rows, cols,
+                                 float(d.get("weight_decay", 0.0)), scale)
+        held.append((p, p16, g, m))   # not the dict, which is the caller's to change
+    return MuonTensors(array, len(tensors), MOE_F32 if grad_dtype is None else grad_dtype, held)
+
+
+def make_muon(lr, momentum=0.95, nesterov=True, iterations=5) -> MoeMuonParams:
+    """The hyperparameters of one step."""
+    return MoeMuonParams(float(lr), float(momentum), 1 if nesterov else 0, int(iterations))
+
+
+def moe_muon_workspace_size(tensors: MuonTensors) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_muon_workspace_size", lib().moe_muon_workspace_size(tensors.array, tensors.count, ctypes.byref(n)))
+    return int(n.value)
+
+
+def muon_workspace(tensors: MuonTensors, device=None):
+    """A device workspace for ``moe_muon_step`` over these tensors, its first 256 bytes cleared."""
+    return _cleared(moe_muon_workspace_size(tensors), device)
+
+
+def moe_muon_step(tensors: MuonTensors, params: MoeMuonParams, grad_scale=None, skip=None, ws=None, stream=None):
+    """One Muon step in place over ``muon_tensors(...)``; ``grad_scale`` (fp32)
+    and ``skip`` (int32) are one-element device tensors or ``None``."""
+    # an address is taken as it is
+    if grad_scale is not None and not isinstance(grad_scale, int):
+        _need_one("grad_scale", grad_scale, "float32", "moe_muon_step")
+    if skip is not None and not isinstance(skip, int):
+        _need_one("skip", skip, "int32", "moe_muon_step")
+    _check("moe_muon_step", lib().moe_muon_step(
+        tensors.array, tensors.count, tensors.grad_dtype, ctypes.byref(params), _ptr(grad_scale), _ptr(skip),
+        _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
 
 
 _prof_events = None

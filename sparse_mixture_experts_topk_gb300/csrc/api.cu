@@ -96,6 +96,19 @@ bool tma_map_bf16_3d(CUtensorMap* m, const void* ptr, uint64_t d2, uint64_t rows
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tma_map_16bit_3d(CUtensorMap* m, const void* ptr, uint64_t d2, uint64_t rows, uint64_t cols, uint64_t pitch,
+                      uint64_t plane, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cols, rows, d2};
+  cuuint64_t strides[2] = {pitch * 2, plane * 2};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
   static int cached[64] = {0};
   int dev = 0;
@@ -877,6 +890,165 @@ int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t grad_
   }
   if (count == 0) return MOE_OK;
   return cuda_status(launch_adamw(tensors, count, grad_dtype, state_bits, h, grad_scale, skip, (cudaStream_t)stream));
+}
+
+namespace moe {
+namespace {
+
+// The workspace of the loss and the router's gradient: error word | scores'
+// gradient | partial sums of tokens (loss or bias) and counts | of dWg.
+struct RouterLayout {
+  size_t err, dl, part, count, part_w, total;
+};
+
+RouterLayout router_layout(const moe_desc& d) {
+  const Shape s = shape_of(d);
+  RouterLayout L;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  const size_t rows = (size_t)balance_partials(s);
+  L.err = take(256);
+  L.dl = take((size_t)s.T * s.E * 4);
+  L.part = take(rows * s.E * 4);
+  L.count = take(rows * (s.E + 1) * 4);
+  L.part_w = take((size_t)router_weight_partials(s) * 4);
+  L.total = off;
+  return L;
+}
+
+bool finite_float(double v) { return v >= -3.4e38 && v <= 3.4e38; }
+
+// The matrices of a Muon step: MOE_OK, or why they are refused.
+int check_matrices(const moe_muon_tensor* tensors, int32_t count) {
+  if (count < 0 || (count > 0 && !tensors)) return MOE_ERR_INVALID;
+  for (int i = 0; i < count; ++i) {
+    const moe_muon_tensor& t = tensors[i];
+    if (t.batch < 0 || t.rows < 0 || t.cols < 0) return MOE_ERR_INVALID;
+    if (t.rows > MOE_ORTHOGONALIZE_MAX_SIDE || t.cols > MOE_ORTHOGONALIZE_MAX_SIDE || t.batch >= (int64_t)1 << 24)
+      return MOE_ERR_UNSUPPORTED;
+  }
+  return MOE_OK;
+}
+
+bool off_by(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
+
+}  // namespace
+}  // namespace moe
+
+int moe_router_backward_workspace_size(const moe_desc* desc, size_t* bytes) {
+  if (check_desc(desc) != MOE_OK || !bytes) return MOE_ERR_INVALID;
+  *bytes = router_layout(*desc).total;
+  return MOE_OK;
+}
+
+int moe_balance_loss(const moe_desc* desc, const float* logits, const int32_t* ids, const uint8_t* mask,
+                     float* psum, int32_t* count, int32_t* tokens, float* loss, void* ws, size_t ws_bytes,
+                     void* stream) {
+  int rc = check_desc(desc);
+  if (rc) return rc;
+  const moe_desc& d = *desc;
+  const RouterLayout L = router_layout(d);
+  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (!(psum || count || tokens || loss) || (d.T > 0 && (!logits || !ids))) return MOE_ERR_INVALID;
+  if (!aligned16(logits) || off_by(ids, 4) || off_by(psum, 4) || off_by(count, 4) || off_by(tokens, 4) ||
+      off_by(loss, 4))
+    return MOE_ERR_INVALID;
+  return cuda_status(launch_balance(shape_of(d), logits, ids, mask, BalanceOut{psum, count, tokens, loss},
+                                    at<float>(ws, L.part), at<int32_t>(ws, L.count), at<int>(ws, L.err),
+                                    (cudaStream_t)stream));
+}
+
+int moe_router_backward(const moe_desc* desc, const void* x, const void* Wg, const float* logits,
+                        const int32_t* ids, const float* dw, const float* dloss, const int32_t* count,
+                        const int32_t* tokens, const uint8_t* mask, float* dlogits, float* dWg, float* dgate_bias,
+                        void* dx, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_desc(desc);
+  if (rc) return rc;
+  const moe_desc& d = *desc;
+  const RouterLayout L = router_layout(d);
+  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (!(dlogits || dWg || dgate_bias || dx) || (dloss && (!count || !tokens))) return MOE_ERR_INVALID;
+  if (d.T > 0 && (!logits || !ids || (dWg && !x) || (dx && !Wg))) return MOE_ERR_INVALID;
+  for (const void* p : {x, Wg, (const void*)logits, (const void*)dlogits, (const void*)dWg, (const void*)dx})
+    if (!aligned16(p)) return MOE_ERR_INVALID;
+  for (const void* p : {(const void*)ids, (const void*)dw, (const void*)dloss, (const void*)count,
+                        (const void*)tokens, (const void*)dgate_bias})
+    if (off_by(p, 4)) return MOE_ERR_INVALID;
+  const RouterBackward b{x, Wg, logits, ids, dw, dloss, count, tokens, mask, dlogits, dWg, dgate_bias, dx};
+  return cuda_status(launch_router_backward(shape_of(d), b, at<float>(ws, L.dl), at<float>(ws, L.part),
+                                            at<float>(ws, L.part_w), at<int>(ws, L.err), (cudaStream_t)stream));
+}
+
+int moe_orthogonalize_workspace_size(int64_t batch, int32_t rows, int32_t cols, size_t* bytes) {
+  moe_muon_tensor t = {};
+  t.batch = batch;
+  t.rows = rows;
+  t.cols = cols;
+  if (!bytes) return MOE_ERR_INVALID;
+  const int rc = check_matrices(&t, 1);
+  if (rc) return rc;
+  *bytes = orthogonal_workspace(&t, 1);
+  return MOE_OK;
+}
+
+int moe_orthogonalize(const void* x, int32_t x_dtype, int64_t batch, int32_t rows, int32_t cols, int32_t iterations,
+                      void* out, int32_t out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  moe_muon_tensor t = {};
+  t.batch = batch;
+  t.rows = rows;
+  t.cols = cols;
+  const int rc = check_matrices(&t, 1);
+  if (rc) return rc;
+  if ((x_dtype != MOE_F32 && x_dtype != MOE_BF16) || (out_dtype != MOE_F32 && out_dtype != MOE_BF16) ||
+      iterations < 1 || iterations > MOE_ORTHOGONALIZE_MAX_ITERATIONS)
+    return MOE_ERR_INVALID;
+  if (batch == 0 || rows == 0 || cols == 0) return MOE_OK;
+  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < orthogonal_workspace(&t, 1)) return MOE_ERR_WORKSPACE;
+  if (!x || !out || off_by(x, x_dtype == MOE_BF16 ? 2 : 4) || off_by(out, out_dtype == MOE_BF16 ? 2 : 4) ||
+      (x == out && x_dtype != out_dtype))
+    return MOE_ERR_INVALID;
+  const OrthogonalRaw raw{x, x_dtype, out, out_dtype};
+  const moe_muon_params h{0.0, 0.0, 0, iterations};
+  return cuda_status(launch_orthogonal(&t, 1, x_dtype, h, &raw, nullptr, nullptr, ws, (cudaStream_t)stream));
+}
+
+int moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID;
+  const int rc = check_matrices(tensors, count);
+  if (rc) return rc;
+  *bytes = orthogonal_workspace(tensors, count);
+  return MOE_OK;
+}
+
+int moe_muon_step(const moe_muon_tensor* tensors, int32_t count, int32_t grad_dtype, const moe_muon_params* params,
+                  const float* grad_scale, const int32_t* skip, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_matrices(tensors, count);
+  if (rc) return rc;
+  if (!params || (grad_dtype != MOE_F32 && grad_dtype != MOE_BF16) || off_by(grad_scale, 4) || off_by(skip, 4))
+    return MOE_ERR_INVALID;
+  const moe_muon_params& h = *params;
+  // every comparison is false for a NaN
+  if (!(h.lr >= 0 && h.lr < 1e30 && h.momentum >= 0 && h.momentum < 1) || (h.nesterov != 0 && h.nesterov != 1) ||
+      h.iterations < 1 || h.iterations > MOE_ORTHOGONALIZE_MAX_ITERATIONS)
+    return MOE_ERR_INVALID;
+  bool any = false;
+  for (int i = 0; i < count; ++i) {
+    const moe_muon_tensor& t = tensors[i];
+    if (!finite_float(t.weight_decay) || !finite_float(t.scale)) return MOE_ERR_INVALID;
+    if (t.batch == 0 || t.rows == 0 || t.cols == 0) continue;
+    any = true;
+    if (!t.p || !t.grad || !t.m) return MOE_ERR_INVALID;
+    if (off_by(t.p, 4) || off_by(t.p_bf16, 2) || off_by(t.grad, grad_dtype == MOE_BF16 ? 2 : 4) || off_by(t.m, 4))
+      return MOE_ERR_INVALID;
+  }
+  if (!any) return MOE_OK;
+  if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < orthogonal_workspace(tensors, count)) return MOE_ERR_WORKSPACE;
+  return cuda_status(launch_orthogonal(tensors, count, grad_dtype, h, nullptr, grad_scale, skip, ws,
+                                       (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -71,6 +71,11 @@ bool tma_map_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
 // reads as zero and is not written.
 bool tma_map_bf16_3d(CUtensorMap* m, const void* ptr, uint64_t d2, uint64_t rows, uint64_t cols, uint32_t box_rows);
 
+// The same for 16-bit elements whose rows are `pitch` and matrices `plane`
+// elements apart (multiples of 8).
+bool tma_map_16bit_3d(CUtensorMap* m, const void* ptr, uint64_t d2, uint64_t rows, uint64_t cols, uint64_t pitch,
+                      uint64_t plane, uint32_t box_rows);
+
 // ---------------------------------------------------------------- router
 // Upper bound of the rows of per-block probability partial sums the router
 // writes (workspace sizing), and the rows the chosen router writes.
@@ -228,6 +233,53 @@ cudaError_t launch_ffn_backward_tc(const Shape& s, int64_t max_rows, const FfnBa
                                    float* part, void* tails, int* err, cudaStream_t st);
 cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int count, int grad_dtype, int state_bits,
                          const moe_adamw_params& h, const float* grad_scale, const int32_t* skip, cudaStream_t st);
+
+
+// The load-balancing loss and the router's gradient.  blocks: partial sums of
+// the tokens' kernels; the products' scratch follows from the shape.
+int64_t balance_partials(const Shape& s);
+struct BalanceOut {
+  float* psum;
+  int32_t* count;
+  int32_t* tokens;
+  float* loss;
+};
+// part_p: [balance_partials, E] floats, part_c: [balance_partials, E + 1] ints
+cudaError_t launch_balance(const Shape& s, const float* logits, const int32_t* ids, const uint8_t* mask,
+                           const BalanceOut& o, float* part_p, int32_t* part_c, int* err, cudaStream_t st);
+struct RouterBackward {
+  const void* x;
+  const void* Wg;
+  const float* logits;
+  const int32_t* ids;
+  const float* dw;
+  const float* dloss;
+  const int32_t* count;
+  const int32_t* tokens;
+  const uint8_t* mask;
+  float* dlogits;
+  float* dWg;
+  float* dbias;
+  void* dx;
+};
+// dl: [T, E] fp32 scratch (unused with dlogits), part_b: [balance_partials, E]
+// floats, part_w: router_weight_partials floats
+int64_t router_weight_partials(const Shape& s);
+cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, float* dl, float* part_b, float* part_w,
+                                   int* err, cudaStream_t st);
+
+// Orthogonalised updates.  With `tensors` of one matrix each way round in
+// `raw`: moe_orthogonalize; else a Muon step.
+struct OrthogonalRaw {
+  const void* x;
+  int x_dtype;
+  void* out;
+  int out_dtype;
+};
+size_t orthogonal_workspace(const moe_muon_tensor* tensors, int count);
+cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int grad_dtype, const moe_muon_params& h,
+                              const OrthogonalRaw* raw, const float* grad_scale, const int32_t* skip, void* ws,
+                              cudaStream_t st);
 
 // The statistics of a layer run in pieces of tokens: count[e] and psum[e]
 // summed over the n pieces in order, then the loss of the whole batch (s.T

@@ -1,0 +1,415 @@
+// The load-balancing loss over the tokens that count, and the router's
+// gradient (Qwen2-MoE code walkthrough, jsqmd.com, sections 3.1 and 3.3).
+//
+//   p = softmax(l / tau),  w = p[ids] / sum_j p[ids_j] = softmax(l[ids] / tau)
+//   loss = E sum_e f_e P_e,  f_e = count_e / (n K),  P_e = sum_t p[t, e] / n
+// over the n tokens that the mask keeps.  Backwards, with c_e = dloss E f_e / n
+// the loss' derivative by p[t, e] (the counts have none):
+//   dl[t, e] = 1/tau ( sum_{ids_j = e} w_j (dw_j - <w, dw>) + p_e (c_e - <p, c>) )
+//   dWg = dl^T x,  dbias = sum_t dl,  dx = dl Wg
+//
+// A group of 8, 16 or 32 lanes takes a token, each lane 4 experts at a time,
+// so that a token's scores are one vector load a lane and every sum over them
+// stays in the group.  What is summed over tokens leaves a block as one row of
+// partial sums; the rows are added in their order, so results are
+// deterministic.
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Lanes for a token and experts for a lane, by the number of experts.
+template <int kLanes, int kVecs>
+struct Group {
+  static constexpr int kTokens = kThreads / kLanes;   // at a time in a block
+  static constexpr int kN = 4 * kVecs;
+  // expert i of this lane
+  __device__ static int expert(int lane, int i) { return (i / 4) * kLanes * 4 + lane * 4 + i % 4; }
+  __device__ static float sum(float v) {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  __device__ static float max(float v) {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+  // This lane's scores of a token times 1 / tau, -infinity past the last expert.
+  __device__ static void load(const float* __restrict__ row, int lane, int E, float inv_tau, bool live, float* l) {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int e = expert(lane, 4 * v);
+      if (E % 4 == 0) {
+        const float4 q = live && e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        l[4 * v] = q.x;
+        l[4 * v + 1] = q.y;
+        l[4 * v + 2] = q.z;
+        l[4 * v + 3] = q.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[4 * v + i] = live && e + i < E ? row[e + i] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[4 * v + i] = e + i < E ? l[4 * v + i] * inv_tau : -INFINITY;
+    }
+  }
+  // Softmax in place over the group's scores.  A NaN among them makes all NaN.
+  __device__ static void softmax(float* l) {
+    float top = l[0];
+#pragma unroll
+    for (int i = 1; i < kN; ++i) top = fmaxf(top, l[i]);
+    top = max(top);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      l[i] = expf(l[i] - top);
+      s += l[i];
+    }
+    const float inv = 1.f / sum(s);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) l[i] *= inv;
+  }
+};
+
+// The groups' sums of each expert over a block's tokens, added in order and
+// written as the block's row of partial sums.
+template <typename G>
+__device__ __forceinline__ void block_sums(const float* acc, float* s, int lane, int group, int E, float* row) {
+  constexpr int kWidth = G::kN * (kThreads / G::kTokens);
+#pragma unroll
+  for (int i = 0; i < G::kN; ++i) s[group * kWidth + G::expert(lane, i)] = acc[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    float v = 0.f;
+    for (int g = 0; g < G::kTokens; ++g) v += s[g * kWidth + e];
+    row[e] = v;
+  }
+}
+
+template <int kLanes, int kVecs>
+__global__ void __launch_bounds__(kThreads)
+balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
+               int64_t T, int E, int K, float inv_tau, float* __restrict__ part_p, int32_t* __restrict__ part_c,
+               int* err) {
+  using G = Group<kLanes, kVecs>;
+  __shared__ float s_p[kThreads * 4 * kVecs];
+  __shared__ int s_count[257];
+  for (int i = threadIdx.x; i <= E; i += kThreads) s_count[i] = 0;
+  __syncthreads();
+  pdl_enter();
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  float acc[G::kN] = {};
+  int n = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * G::kTokens; t0 < T; t0 += (int64_t)gridDim.x * G::kTokens) {
+    const int64_t t = t0 + group;
+    const bool live = t < T && (!mask || mask[t]);
+    float l[G::kN];
+    G::load(logits + t * E, lane, E, inv_tau, live, l);
+    G::softmax(l);
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < G::kN; ++i) acc[i] += l[i];
+      ++n;
+      if (lane < K) {
+        const int e = ids[t * K + lane];
+        if (e >= 0 && e < E) atomicAdd(&s_count[e], 1);
+        else if (e != -1) set_error(err, kDevBadIndex);
+      }
+    }
+  }
+  if (lane == 0 && n) atomicAdd(&s_count[E], n);
+  block_sums<G>(acc, s_p, lane, group, E, part_p + (int64_t)blockIdx.x * E);   // its barrier ends the counting too
+  for (int i = threadIdx.x; i <= E; i += kThreads) part_c[(int64_t)blockIdx.x * (E + 1) + i] = s_count[i];
+}
+
+// One block: the partial rows added up, four threads to an expert, and the loss.
+__global__ void __launch_bounds__(1024)
+balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_c, int rows, int E, int K,
+                      BalanceOut o) {
+  __shared__ double s_p[4][256], s_term[256];
+  __shared__ int s_c[4][256];
+  __shared__ int s_n;
+  pdl_enter();
+  const int e = threadIdx.x % 256, q = threadIdx.x / 256;
+  double p = 0.0;
+  int c = 0;
+  if (e < E)
+    for (int r = q; r < rows; r += 4) {
+      p += part_p[(int64_t)r * E + e];
+      c += part_c[(int64_t)r * (E + 1) + e];
+    }
+  s_p[q][e] = p;
+  s_c[q][e] = c;
+  if (threadIdx.x < 32) {
+    int n = 0;
+    for (int r = threadIdx.x; r < rows; r += 32) n += part_c[(int64_t)r * (E + 1) + E];
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) n += __shfl_xor_sync(0xffffffffu, n, w);
+    if (threadIdx.x == 0) s_n = n;
+  }
+  __syncthreads();
+  if (q == 0) {
+    const double ps = (s_p[0][e] + s_p[1][e]) + (s_p[2][e] + s_p[3][e]);
+    const int ct = s_c[0][e] + s_c[1][e] + s_c[2][e] + s_c[3][e];
+    if (e < E) {
+      if (o.psum) o.psum[e] = (float)ps;
+      if (o.count) o.count[e] = ct;
+    }
+    s_term[e] = e < E ? ps * ct : 0.0;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    double v = 0.0;
+    for (int i = threadIdx.x; i < 256; i += 32) v += s_term[i];
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
+    if (threadIdx.x == 0) {
+      const double n = s_n;
+      if (o.tokens) *o.tokens = s_n;
+      if (o.loss) *o.loss = s_n ? (float)(E * v / (n * K * n)) : 0.f;
+    }
+  }
+}
+
+// The scores' gradient, [T, E] fp32, and its sum over each block's tokens.
+template <int kLanes, int kVecs>
+__global__ void __launch_bounds__(kThreads)
+dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* __restrict__ dl,
+               float* __restrict__ part_b, int* err) {
+  using G = Group<kLanes, kVecs>;
+  __shared__ float s_b[kThreads * 4 * kVecs];
+  pdl_enter();
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  float c[G::kN], acc[G::kN] = {};
+  if (b.dloss) {
+    const int n = *b.tokens;
+    const double f = n > 0 ? (double)*b.dloss * E / ((double)n * n * K) : 0.0;
+#pragma unroll
+    for (int i = 0; i < G::kN; ++i) {
+      const int e = G::expert(lane, i);
+      c[i] = e < E ? (float)(f * b.count[e]) : 0.f;
+    }
+  }
+  for (int64_t t0 = (int64_t)blockIdx.x * G::kTokens; t0 < T; t0 += (int64_t)gridDim.x * G::kTokens) {
+    const int64_t t = t0 + group;
+    const bool live = t < T && (!b.mask || b.mask[t]);
+    float d[G::kN] = {};
+    if (b.dloss) {
+      float p[G::kN], dot = 0.f;
+      G::load(b.logits + t * E, lane, E, inv_tau, live, p);
+      G::softmax(p);
+#pragma unroll
+      for (int i = 0; i < G::kN; ++i) dot = fmaf(p[i], c[i], dot);
+      dot = G::sum(dot);
+#pragma unroll
+      for (int i = 0; i < G::kN; ++i) d[i] = p[i] * (c[i] - dot);
+    }
+    if (b.dw) {
+      // lane j has choice j
+      int id = -1;
+      float z = -INFINITY, g = 0.f;
+      if (live && lane < K) {
+        id = b.ids[t * K + lane];
+        if (id >= 0 && id < E) {
+          z = b.logits[t * E + id] * inv_tau;
+          g = b.dw[t * K + lane];
+        } else {
+          if (id != -1) set_error(err, kDevBadIndex);
+          id = -1;
+        }
+      }
+      const float top = G::max(z), x = id >= 0 ? expf(z - top) : 0.f, s = G::sum(x);
+      const float w = s != 0.f ? x / s : 0.f, dot = G::sum(w * g), v = w * (g - dot);
+      for (int j = 0; j < K; ++j) {
+        const int e = __shfl_sync(0xffffffffu, id, j, kLanes);
+        const float vj = __shfl_sync(0xffffffffu, v, j, kLanes);
+#pragma unroll
+        for (int i = 0; i < G::kN; ++i)
+          if (G::expert(lane, i) == e) d[i] += vj;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < G::kN; ++i) {
+      d[i] = live ? d[i] * inv_tau : 0.f;
+      acc[i] += d[i];
+    }
+    if (t < T) {
+      float* row = dl + t * E;
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        const int e = G::expert(lane, 4 * v);
+        if (E % 4 == 0) {
+          if (e < E) *reinterpret_cast<float4*>(row + e) = make_float4(d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (e + i < E) row[e + i] = d[4 * v + i];
+        }
+      }
+    }
+  }
+  if (b.dbias) block_sums<G>(acc, s_b, lane, group, E, part_b + (int64_t)blockIdx.x * E);
+}
+
+// dx[t, h] = sum_e dl[t, e] Wg[e, h] on CUDA cores: 16 tokens, a thread a column.
+constexpr int kTokTile = 16;
+template <typename T>
+__global__ void __launch_bounds__(128)
+dx_simt_kernel(const float* __restrict__ dl, const T* __restrict__ Wg, int64_t Tn, int E, int H, T* __restrict__ dx) {
+  __shared__ float s_dl[256][kTokTile];
+  pdl_enter();
+  const int64_t t0 = (int64_t)blockIdx.x * kTokTile;
+  for (int i = threadIdx.x; i < E * kTokTile; i += 128) {
+    const int tt = i / E, e = i % E;
+    s_dl[e][tt] = t0 + tt < Tn ? dl[(t0 + tt) * E + e] : 0.f;
+  }
+  __syncthreads();
+  const int h = blockIdx.y * 128 + threadIdx.x;
+  if (h >= H) return;
+  float acc[kTokTile] = {};
+  for (int e = 0; e < E; ++e) {
+    const float w = to_f32(Wg[(int64_t)e * H + h]);
+#pragma unroll
+    for (int i = 0; i < kTokTile; ++i) acc[i] = fmaf(s_dl[e][i], w, acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kTokTile; ++i)
+    if (t0 + i < Tn) dx[(t0 + i) * H + h] = from_f32<T>(acc[i]);
+}
+
+// dWg on CUDA cores: partial sums over a share of the tokens, 16 experts, a
+// thread a column.  A masked token's x is not read: it may hold anything.
+constexpr int kExpTile = 16, kTokStep = 32;
+template <typename T>
+__global__ void __launch_bounds__(128)
+dwg_simt_kernel(const float* __restrict__ dl, const T* __restrict__ x, const uint8_t* __restrict__ mask, int64_t Tn,
+                int E, int H, float* __restrict__ part) {
+  __shared__ float s_dl[kTokStep][kExpTile];
+  pdl_enter();
+  const int h = blockIdx.x * 128 + threadIdx.x, e0 = blockIdx.y * kExpTile;
+  const int64_t a = Tn * blockIdx.z / gridDim.z, z = Tn * (blockIdx.z + 1) / gridDim.z;
+  float acc[kExpTile] = {};
+  for (int64_t t0 = a; t0 < z; t0 += kTokStep) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTokStep * kExpTile; i += 128) {
+      const int tt = i / kExpTile, e = e0 + i % kExpTile;
+      s_dl[tt][i % kExpTile] = t0 + tt < z && e < E ? dl[(t0 + tt) * E + e] : 0.f;
+    }
+    __syncthreads();
+    if (h < H) {
+      const int n = (int)(z - t0 < kTokStep ? z - t0 : kTokStep);
+#pragma unroll 4
+      for (int tt = 0; tt < n; ++tt) {
+        if (mask && !mask[t0 + tt]) continue;
+        const float v = to_f32(x[(t0 + tt) * H + h]);
+#pragma unroll
+        for (int i = 0; i < kExpTile; ++i) acc[i] = fmaf(s_dl[tt][i], v, acc[i]);
+      }
+    }
+  }
+  if (h < H)
+#pragma unroll
+    for (int i = 0; i < kExpTile; ++i)
+      if (e0 + i < E) part[((int64_t)blockIdx.z * E + e0 + i) * H + h] = acc[i];
+}
+
+// out[i] = the sum of `rows` rows of n, in order.
+__global__ void __launch_bounds__(256)
+row_sums_kernel(const float* __restrict__ part, int64_t rows, int64_t n, float* __restrict__ out) {
+  pdl_enter();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float v = 0.f;
+#pragma unroll 8
+  for (int64_t r = 0; r < rows; ++r) v += part[r * n + i];
+  out[i] = v;
+}
+
+int simt_splits(const Shape& s) {
+  const int64_t blocks = (int64_t)((s.H + 127) / 128) * ((s.E + kExpTile - 1) / kExpTile);
+  const int64_t want = (2 * (int64_t)sm_count() + blocks - 1) / blocks, most = (s.T + 63) / 64;
+  const int64_t n = want < most ? want : most;
+  return (int)(n < 1 ? 1 : n);
+}
+
+template <typename T>
+cudaError_t products_simt(const Shape& s, const RouterBackward& b, const float* dl, float* part_w, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  const unsigned cols = (unsigned)((s.H + 127) / 128);
+  if (b.dx)
+    e = launch_kernel(dx_simt_kernel<T>, dim3((unsigned)((s.T + kTokTile - 1) / kTokTile), cols), dim3(128), 0, st, 1,
+                      dl, (const T*)b.Wg, s.T, s.E, s.H, (T*)b.dx);
+  if (e == cudaSuccess && b.dWg) {
+    const int splits = simt_splits(s);
+    e = launch_kernel(dwg_simt_kernel<T>, dim3(cols, (unsigned)((s.E + kExpTile - 1) / kExpTile), (unsigned)splits),
+                      dim3(128), 0, st, 1, dl, (const T*)b.x, b.mask, s.T, s.E, s.H, part_w);
+    const int64_t n = (int64_t)s.E * s.H;
+    if (e == cudaSuccess)
+      e = launch_kernel(row_sums_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, 1, part_w,
+                        (int64_t)splits, n, b.dWg);
+  }
+  return e;
+}
+
+// Runs f with the lanes of a token and the vectors of a lane that E takes.
+template <typename F>
+cudaError_t by_experts(int E, F f) {
+  if (E <= 32) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+  if (E <= 64) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
+  if (E <= 128) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
+  return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
+}
+
+}  // namespace
+
+// Two blocks an SM at most while a block has no more than 2^13 tokens, and four rounds of tokens a block at least.
+int64_t balance_partials(const Shape& s) {
+  const int64_t tokens = kThreads / (s.E <= 32 ? 8 : s.E <= 64 ? 16 : 32);
+  const int64_t want = (s.T + 4 * tokens - 1) / (4 * tokens), cap = 2 * (int64_t)sm_count();
+  const int64_t least = (s.T + 8191) / 8192;
+  int64_t n = want < cap ? want : cap;
+  if (n < least) n = least;
+  return n < 1 ? 1 : n;
+}
+
+int64_t router_weight_partials(const Shape& s) { return (int64_t)simt_splits(s) * s.E * s.H; }
+
+cudaError_t launch_balance(const Shape& s, const float* logits, const int32_t* ids, const uint8_t* mask,
+                           const BalanceOut& o, float* part_p, int32_t* part_c, int* err, cudaStream_t st) {
+  const int rows = (int)balance_partials(s);
+  cudaError_t e = by_experts(s.E, [&](auto lanes, auto vecs) {
+    return launch_kernel(balance_kernel<decltype(lanes)::value, decltype(vecs)::value>, dim3((unsigned)rows),
+                         dim3(kThreads), 0, st, 1, logits, ids, mask, s.T, s.E, s.K, s.inv_tau, part_p, part_c, err);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_kernel(balance_finish_kernel, dim3(1), dim3(1024), 0, st, 1, part_p, part_c, rows, s.E, s.K, o);
+}
+
+cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, float* dl, float* part_b, float* part_w,
+                                   int* err, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (s.T == 0) {
+    if (b.dWg) e = cudaMemsetAsync(b.dWg, 0, (size_t)s.E * s.H * 4, st);
+    if (e == cudaSuccess && b.dbias) e = cudaMemsetAsync(b.dbias, 0, (size_t)s.E * 4, st);
+    return e;
+  }
+  float* out = b.dlogits ? b.dlogits : dl;
+  const int64_t rows = balance_partials(s);
+  e = by_experts(s.E, [&](auto lanes, auto vecs) {
+    return launch_kernel(dlogits_kernel<decltype(lanes)::value, decltype(vecs)::value>, dim3((unsigned)rows),
+                         dim3(kThreads), 0, st, 1, b, s.T, s.E, s.K, s.inv_tau, out, part_b, err);
+  });
+  if (e == cudaSuccess && b.dbias)
+    e = launch_kernel(row_sums_kernel, dim3(1), dim3(256), 0, st, 1, part_b, rows, (int64_t)s.E, b.dbias);
+  if (e != cudaSuccess || !(b.dx || b.dWg)) return e;
+  return s.dtype == MOE_BF16 ? products_simt<bf16>(s, b, out, part_w, st) : products_simt<float>(s, b, out, part_w, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,230 @@
+"""Newton-Schulz orthogonalisation and the Muon step against a plain
+implementation in 64 bits."""
+import numpy as np
+import pytest
+
+import sparse_mixture_experts_topk_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+
+NS = (3.4445, -4.7750, 2.0315)
+U32, U16 = 2.0 ** -24, 2.0 ** -8      # half a step of fp32 and of bf16, relative
+
+
+def t_():
+    import torch
+    return torch
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sparse_mixture_experts_topk_gb300 import build
+    build.build()
+
+
+def newton_schulz(u, iterations, held=lambda v: v):
+    """The iteration in 64 bits; ``held`` rounds what the kernels hold."""
+    a, b, c = NS
+    u = np.asarray(u, np.float64)
+    norm = np.linalg.norm(u)
+    if norm == 0:
+        return np.zeros_like(u)
+    x = held((u.T if u.shape[0] > u.shape[1] else u) / norm)
+    for _ in range(iterations):
+        A = held(x @ x.T)
+        x = held(held(a * np.eye(len(x)) + b * A + c * (A @ A)) @ x)
+    return x.T if u.shape[0] > u.shape[1] else x
+
+
+def fp16(v):
+    return (v * 4096.0).astype(np.float16).astype(np.float64) / 4096.0
+
+
+def check(got, u, iterations, out_step):
+    """Within twice the distance that the same iteration with every held value rounded to fp16 has (the kernels'
+    sums are in fp32, 2^-24 a term, and short products of products may be rounded once more), and the result's own
+    rounding; a matrix of one element has no averaging, hence the floor of 16 fp16 half steps."""
+    want = newton_schulz(u, iterations)
+    norm = np.linalg.norm(want)
+    model = np.linalg.norm(newton_schulz(u, iterations, fp16) - want)
+    assert np.linalg.norm(got - want) <= 2 * model + (out_step + 16 * 2.0 ** -12) * norm
+
+
+def update_like(r, *shape):
+    u = r.standard_normal(shape)
+    k = min(4, *shape[-2:])
+    return (u + r.standard_normal(shape[:-1] + (k,)) @ r.standard_normal(shape[:-2] + (k, shape[-1]))) * 1e-3
+
+
+def dev(a, dtype="f32"):
+    t = t_()
+    return t.from_numpy(np.ascontiguousarray(a)).to("cuda").to(t.bfloat16 if dtype == "bf16" else t.float32)
+
+
+def run(x, out_dtype, iterations=5):
+    t = t_()
+    b = int(np.prod(x.shape[:-2], dtype=np.int64))
+    ws = moe.orthogonalize_workspace(b, x.shape[-2], x.shape[-1])
+    out = t.full(x.shape, 7.0, device="cuda").to(t.bfloat16 if out_dtype == "bf16" else t.float32)
+    moe.moe_orthogonalize(x, out, iterations, ws)
+    t.cuda.synchronize()
+    assert moe.moe_get_device_error(ws) == 0
+    return out
+
+
+SHAPES = [(1, 1, 1), (2, 1, 7), (1, 5, 1), (3, 2, 2), (1, 64, 96), (2, 96, 64), (1, 17, 1000), (2, 257, 300),
+          (1, 255, 256), (1, 1001, 130), (2, 520, 520), (1, 384, 1537), (1, 640, 768), (5, 129, 511)]
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_orthogonalize(shape, dtype, out_dtype):
+    x = dev(update_like(np.random.default_rng(shape), *shape), dtype)
+    out = run(x, out_dtype).double().cpu().numpy()
+    for i in range(shape[0]):
+        check(out[i], x[i].double().cpu().numpy(), 5, U16 if out_dtype == "bf16" else U32)
+
+
+@pytest.mark.parametrize("iterations", [1, 2, 3, 4, 6])
+@pytest.mark.parametrize("shape", [(200, 300), (300, 200), (264, 1100)])
+def test_number_of_iterations(shape, iterations):
+    x = dev(update_like(np.random.default_rng(iterations), *shape))
+    check(run(x, "f32", iterations).double().cpu().numpy(), x.double().cpu().numpy(), iterations, U32)
+
+
+def test_result_is_nearly_orthogonal():
+    """Singular values of a Gaussian 200 x 800 are within (0.5, 1.5) / sqrt(200) of |u|: five iterations take them
+    into the band that the quintic leaves, [0.68, 1.21]."""
+    x = dev(np.random.default_rng(1).standard_normal((200, 800)))
+    s = np.linalg.svd(run(x, "f32").double().cpu().numpy(), compute_uv=False)
+    assert s.min() > 0.66 and s.max() < 1.22
+
+
+def test_transposes_batches_and_repeats():
+    """The same bits again, alone as in a batch, in place and off the 16-byte grid.  A transpose's norm is summed in
+    another order, and a last bit of it moves roundings of X: the same result within the bound."""
+    r = np.random.default_rng(2)
+    x = dev(update_like(r, 7, 300, 200))
+    out = run(x, "f32")
+    assert (out == run(x, "f32")).all()
+    flipped = run(x.mT.contiguous(), "f32").mT.double().cpu().numpy()
+    for i in range(7):
+        check(flipped[i], x[i].double().cpu().numpy(), 5, U32)
+    for i in (0, 3, 6):
+        assert (out[i] == run(x[i], "f32")).all()
+    t = t_()
+    flat = t.zeros(x.numel() + 1, device="cuda")
+    y = flat[1:].view(x.shape)
+    y.copy_(x)
+    ws = moe.orthogonalize_workspace(7, 300, 200)
+    moe.moe_orthogonalize(y, y, 5, ws)
+    assert (y == out).all() and flat[0] == 0
+
+
+@pytest.mark.parametrize("power", [-130, -70, -20, 20, 60, 120])
+def test_scale_does_not_matter(power):
+    """u and u 2^k have the same X but for values that vanish at the ends of fp32's range."""
+    r = np.random.default_rng(3)
+    u = update_like(r, 2, 60, 80) * 1e3
+    x = dev(u)
+    assert (run(x * 2.0 ** power, "f32") == run(x, "f32")).all() or power == -130
+    if power == -130:     # subnormal inputs: bits are lost before the call
+        y = x * 2.0 ** power
+        got = run(y, "f32").double().cpu().numpy()
+        for i in range(2):
+            check(got[i], y[i].double().cpu().numpy() * 2.0 ** 130, 5, U32)
+
+
+def test_a_zero_matrix_and_a_matrix_with_nan_keep_to_themselves():
+    r = np.random.default_rng(4)
+    x = dev(update_like(r, 5, 130, 270))
+    clean = run(x, "f32")
+    x[1] = 0
+    x[2, 3, 4] = float("nan")
+    x[3, 129, 269] = float("inf")
+    out = run(x, "f32")
+    assert (out[1] == 0).all()
+    assert out[2].isnan().all() and out[3].isnan().all()
+    assert (out[0] == clean[0]).all() and (out[4] == clean[4]).all()
+
+
+# ------------------------------------------------------------------ the step
+
+def step_case(shapes, grad, seed, p16=True):
+    r = np.random.default_rng(seed)
+    t = t_()
+    out = []
+    for i, s in enumerate(shapes):
+        p = dev(r.standard_normal(s) * 0.02)
+        d = {"p": p, "g": dev(update_like(r, *s), grad), "m": dev(update_like(r, *s) * 3), "weight_decay": 0.1 * (i % 2)}
+        if p16:
+            d["p16"] = t.zeros(s, dtype=t.bfloat16, device="cuda")
+        out.append(d)
+    return out
+
+
+def check_step(before, after, lr, mu, nesterov, iterations, factor):
+    for b, a in zip(before, after):
+        g = b["g"].astype(np.float64) * factor
+        m = mu * b["m"] + g
+        assert (abs(a["m"] - m) <= 4 * U32 * (abs(mu * b["m"]) + abs(g))).all()
+        u = g + mu * m if nesterov else m
+        size = b["p"].shape[-2:]
+        scale = b.get("scale", 0.2 * np.sqrt(max(size)))
+        keep = 1 - lr * b["weight_decay"]
+        moved = (b["p"] * keep - a["p"]) / (lr * scale)
+        noise = np.linalg.norm(b["p"]) * 4 * U32 / (lr * scale)      # p's own rounding, seen through the quotient
+        for got, ui in zip(moved.reshape((-1,) + size), u.reshape((-1,) + size)):
+            want = newton_schulz(ui, iterations)
+            model = np.linalg.norm(newton_schulz(ui, iterations, fp16) - want)
+            assert np.linalg.norm(got - want) <= 2 * model + 16 * 2.0 ** -12 * np.linalg.norm(want) + noise
+        if "p16" in a:
+            assert (a["p16"] == t_().from_numpy(a["p"]).float().to(t_().bfloat16).double().numpy()).all()
+
+
+def numbers(tensors):
+    return [{k: v.double().cpu().numpy() if hasattr(v, "cpu") else v for k, v in d.items()} for d in tensors]
+
+
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("nesterov", [True, False])
+def test_muon_step(grad, nesterov):
+    """Tensors of several sizes, two of one size the other way round, batches, a single matrix, one element."""
+    shapes = [(3, 96, 160), (2, 160, 96), (130, 257), (1, 1), (4, 8, 8), (2, 2, 24, 40)]
+    tensors = step_case(shapes, grad, 5, p16=nesterov)
+    t = t_()
+    plan, params = moe.muon_tensors(tensors), moe.make_muon(0.02, 0.9, nesterov, 5)
+    ws = moe.muon_workspace(plan)
+    factor = t.full((1,), 0.5, device="cuda")
+    for _ in range(2):
+        before = numbers(tensors)
+        moe.moe_muon_step(plan, params, factor, None, ws)
+        check_step(before, numbers(tensors), 0.02, np.float64(np.float32(0.9)), nesterov, 5, 0.5)
+    assert moe.moe_get_device_error(ws) == 0
+
+
+def test_muon_step_skips_and_takes_no_tensor():
+    tensors = step_case([(2, 40, 60)], "f32", 6)
+    t = t_()
+    plan, params = moe.muon_tensors(tensors), moe.make_muon(0.1)
+    ws = moe.muon_workspace(plan)
+    before = numbers(tensors)
+    tensors[0]["g"][0, 1, 2] = float("nan")
+    moe.moe_muon_step(plan, params, None, t.ones(1, dtype=t.int32, device="cuda"), ws)
+    for b, a in zip(before, numbers(tensors)):
+        for k in ("p", "m", "p16"):
+            assert (a[k] == b[k]).all(), k
+    moe.moe_muon_step(plan, params, None, t.zeros(1, dtype=t.int32, device="cuda"), ws)
+    assert tensors[0]["p"][0].isnan().all() and not tensors[0]["p"][1].isnan().any()
+    empty = moe.muon_tensors([])
+    moe.moe_muon_step(empty, params, None, None, moe.muon_workspace(empty))
+
+
+def test_more_tensors_than_a_launch_takes():
+    tensors = step_case([(1 + i % 3, 24, 40) if i % 2 else (40, 24) for i in range(61)], "f32", 7)
+    plan, params = moe.muon_tensors(tensors), moe.make_muon(0.02, 0.95, True, 3)
+    ws = moe.muon_workspace(plan)
+    before = numbers(tensors)
+    moe.moe_muon_step(plan, params, None, None, ws)
+    check_step(before, numbers(tensors), 0.02, np.float64(np.float32(0.95)), True, 3, 1.0)
