@@ -912,7 +912,7 @@ RouterLayout router_layout(const moe_desc& d) {
   };
   const size_t rows = (size_t)balance_partials(s);
   L.err = take(256);
-  L.dl = take((size_t)s.T * s.E * 4);
+  L.dl = take(router_scratch_bytes(s));
   L.part = take(rows * s.E * 4);
   L.count = take(rows * (s.E + 1) * 4);
   L.part_w = take((size_t)router_weight_partials(s) * 4);
@@ -979,7 +979,7 @@ int moe_router_backward(const moe_desc* desc, const void* x, const void* Wg, con
                         (const void*)tokens, (const void*)dgate_bias})
     if (off_by(p, 4)) return MOE_ERR_INVALID;
   const RouterBackward b{x, Wg, logits, ids, dw, dloss, count, tokens, mask, dlogits, dWg, dgate_bias, dx};
-  return cuda_status(launch_router_backward(shape_of(d), b, at<float>(ws, L.dl), at<float>(ws, L.part),
+  return cuda_status(launch_router_backward(shape_of(d), b, at<void>(ws, L.dl), at<float>(ws, L.part),
                                             at<float>(ws, L.part_w), at<int>(ws, L.err), (cudaStream_t)stream));
 }
 

@@ -262,10 +262,19 @@ struct RouterBackward {
   float* dbias;
   void* dx;
 };
-// dl: [T, E] fp32 scratch (unused with dlogits), part_b: [balance_partials, E]
-// floats, part_w: router_weight_partials floats
+// dl: router_scratch_bytes: the scores' gradient, [T, E] fp32, or in bf16
+// parts; part_b: [balance_partials, E] floats, part_w: router_weight_partials
+// floats
+bool router_gate_on_tensor_cores(const Shape& s);
+size_t router_scratch_bytes(const Shape& s);
 int64_t router_weight_partials(const Shape& s);
-cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, float* dl, float* part_b, float* part_w,
+// The gate's products on the tensor cores, and the sum of part_b's rows_b rows
+// into dbias.  panels: [T, gate_panel_cols] bf16 as dlogits_kernel writes them.
+int gate_panel_cols(int E);
+int64_t gate_part_floats(const Shape& s);
+cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* panels, float* part,
+                           const float* part_b, int rows_b, int* err, cudaStream_t st);
+cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, void* dl, float* part_b, float* part_w,
                                    int* err, cudaStream_t st);
 
 // Orthogonalised updates.  With `tensors` of one matrix each way round in

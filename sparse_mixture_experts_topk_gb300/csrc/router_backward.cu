@@ -178,11 +178,31 @@ balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restric
   }
 }
 
-// The scores' gradient, [T, E] fp32, and its sum over each block's tokens.
+// Four values as bf16 parts: v = high + middle + low, each rounded from what
+// the ones before it leave (exactly, but for values below 2^-110).
+__device__ __forceinline__ void split4(const float* v, uint2* parts) {
+  float rest[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(rest[0], rest[1]), b = __floats2bfloat162_rn(rest[2], rest[3]);
+    parts[k] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    const float2 fa = __bfloat1622float2(a), fb = __bfloat1622float2(b);
+    rest[0] -= fa.x;
+    rest[1] -= fa.y;
+    rest[2] -= fb.x;
+    rest[3] -= fb.y;
+  }
+}
+
+// The scores' gradient, and its sum over each block's tokens.  It is written
+// as [T, E] fp32 (dl) and as bf16 parts (panels), where these are not null.
+// Panels are 64 columns wide and zero past the last expert: the high parts of
+// all experts, the middle ones, the low ones; up to 32 experts: [high | middle],
+// [low | 0].
 template <int kLanes, int kVecs>
 __global__ void __launch_bounds__(kThreads)
 dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* __restrict__ dl,
-               float* __restrict__ part_b, int* err) {
+               bf16* __restrict__ panels, int panel_cols, float* __restrict__ part_b, int* err) {
   using G = Group<kLanes, kVecs>;
   __shared__ float s_b[kThreads * 4 * kVecs];
   pdl_enter();
@@ -240,7 +260,23 @@ dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* 
       d[i] = live ? d[i] * inv_tau : 0.f;
       acc[i] += d[i];
     }
-    if (t < T) {
+    if (t < T && panels) {
+      bf16* row = panels + t * panel_cols;
+      const bool packed = kLanes == 8;
+      const int width = packed ? 32 : panel_cols / 3;
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        const int e = G::expert(lane, 4 * v);
+        uint2 parts[3];
+        split4(d + 4 * v, parts);
+        if (e < width) {
+#pragma unroll
+          for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2*>(row + k * width + e) = parts[k];
+          if (packed) *reinterpret_cast<uint2*>(row + 96 + e) = make_uint2(0u, 0u);
+        }
+      }
+    }
+    if (t < T && dl) {
       float* row = dl + t * E;
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
@@ -379,7 +415,15 @@ int64_t balance_partials(const Shape& s) {
   return n < 1 ? 1 : n;
 }
 
-int64_t router_weight_partials(const Shape& s) { return (int64_t)simt_splits(s) * s.E * s.H; }
+bool router_gate_on_tensor_cores(const Shape& s) {
+  return s.dtype == MOE_BF16 && !(s.flags & MOE_FLAG_SIMT_ROUTER);
+}
+size_t router_scratch_bytes(const Shape& s) {
+  return (size_t)s.T * (router_gate_on_tensor_cores(s) ? (size_t)gate_panel_cols(s.E) * 2 : (size_t)s.E * 4);
+}
+int64_t router_weight_partials(const Shape& s) {
+  return router_gate_on_tensor_cores(s) ? gate_part_floats(s) : (int64_t)simt_splits(s) * s.E * s.H;
+}
 
 cudaError_t launch_balance(const Shape& s, const float* logits, const int32_t* ids, const uint8_t* mask,
                            const BalanceOut& o, float* part_p, int32_t* part_c, int* err, cudaStream_t st) {
@@ -392,7 +436,7 @@ cudaError_t launch_balance(const Shape& s, const float* logits, const int32_t* i
   return launch_kernel(balance_finish_kernel, dim3(1), dim3(1024), 0, st, 1, part_p, part_c, rows, s.E, s.K, o);
 }
 
-cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, float* dl, float* part_b, float* part_w,
+cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, void* dl, float* part_b, float* part_w,
                                    int* err, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (s.T == 0) {
@@ -400,13 +444,18 @@ cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, floa
     if (e == cudaSuccess && b.dbias) e = cudaMemsetAsync(b.dbias, 0, (size_t)s.E * 4, st);
     return e;
   }
-  float* out = b.dlogits ? b.dlogits : dl;
+  const bool tc = router_gate_on_tensor_cores(s), products = b.dx || b.dWg;
+  float* out = b.dlogits || tc || !products ? b.dlogits : (float*)dl;
+  bf16* panels = tc && products ? (bf16*)dl : nullptr;
   const int64_t rows = balance_partials(s);
   e = by_experts(s.E, [&](auto lanes, auto vecs) {
     return launch_kernel(dlogits_kernel<decltype(lanes)::value, decltype(vecs)::value>, dim3((unsigned)rows),
-                         dim3(kThreads), 0, st, 1, b, s.T, s.E, s.K, s.inv_tau, out, part_b, err);
+                         dim3(kThreads), 0, st, 1, b, s.T, s.E, s.K, s.inv_tau, out, panels, gate_panel_cols(s.E),
+                         part_b, err);
   });
-  if (e == cudaSuccess && b.dbias)
+  if (e != cudaSuccess) return e;
+  if (tc) return launch_gate_tc(s, b, panels, part_w, part_b, (int)rows, err, st);
+  if (b.dbias)
     e = launch_kernel(row_sums_kernel, dim3(1), dim3(256), 0, st, 1, part_b, rows, (int64_t)s.E, b.dbias);
   if (e != cudaSuccess || !(b.dx || b.dWg)) return e;
   return s.dtype == MOE_BF16 ? products_simt<bf16>(s, b, out, part_w, st) : products_simt<float>(s, b, out, part_w, st);

@@ -1,0 +1,506 @@
+// The gate's products of the router's gradient on the tensor cores: from the
+// scores' gradient dl [T, E] (router_backward.cu)
+//   dWg = dl^T x  [E, H],   dx = dl Wg  [T, H]
+// in one pass over x and dx, which are what it has to read and write: the
+// products themselves are E wide.
+//
+// dl comes in bf16 parts whose sum it is: high + middle for dx (16 bits, which
+// is rounded to 8), and low too for dWg (24 bits: dl itself).  A part times a
+// bf16 value is exact in the tensor cores' fp32 sums.  The parts of 64 experts
+// are a panel of 64 columns; up to 32 experts high and middle share one.
+//
+// A CTA takes 128 columns of H (a chunk) and walks over tiles of 128 tokens:
+//   D1 [128 columns, E]   += x^T dl   x read along its rows ("MN-major"), the panels too
+//   D2 [128 tokens, 128]   = dl Wg    the panels K-major, Wg's columns in shared memory
+// so the same panel in shared memory serves both.  The tensor cores' fp32 sums
+// round towards zero, half a last place low each on average: over all of a
+// CTA's tokens dWg would be 1e-4 small (32768 tokens).  So D1 starts anew every
+// tile (every four above 128 experts), small parts first, and the epilogue adds
+// it to sums in registers, which leave as partial ones when the chunk ends for
+// this CTA; a last kernel adds those of a chunk in order.  D2 is double-buffered
+// and leaves through shared memory by TMA.  The (chunk, tile) pairs are dealt
+// out evenly, chunk by chunk, in one stretch for each CTA.
+//
+// Roles: warp 0 producer of x and Wg, warp 1 of the panels, warp 2 MMA issuer,
+// warp 3 zeroes the rows of tokens that the mask leaves out (0 x NaN is NaN),
+// warps 4-11 epilogue, two
+// for a quarter of the TMEM lanes, each with half of the columns.  Every wait is bounded: on expiry the kernel records a
+// timeout in the workspace's error word, drains what it has in flight, frees
+// its tensor memory and returns.
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTok = 128, kCols = 128;        // tokens of a tile, columns of a chunk
+constexpr int kHalf = kTok * 128;             // bytes of 64 columns of an x tile, and of a panel
+constexpr int kXBytes = 2 * kHalf;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kStoreBytes = 32 * 128;         // an epilogue warp's 32 rows of 64 columns
+constexpr int kOut = kEpiWarps * kStoreBytes;
+constexpr int kMaxX = 3, kMaxPanels = 5;
+constexpr uint32_t kD2 = 256;                 // TMEM columns: D1 at 0 (and 128), D2 twice 128
+constexpr int kTmemCols = 512;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// How E experts are held: `groups` of 64 columns of D1; panels of a tile.
+struct Plan {
+  int E, groups, panels;
+  bool packed;      // up to 32 experts: panels [high | middle] and [low | 0]
+  int nx, np;       // ring sizes
+  int bufs, run;    // buffers of D1, and tiles that it sums
+  __host__ __device__ explicit Plan(int e)
+      : E(e), groups((e + 63) / 64), panels(e <= 32 ? 2 : 3 * ((e + 63) / 64)), packed(e <= 32),
+        nx(e <= 128 ? 3 : 2), np(e <= 64 || (e > 128 && e <= 192) ? 5 : 4),
+        bufs(e <= 128 ? 2 : 1), run(e <= 128 ? 1 : 4) {}
+  __host__ __device__ int wg_bytes() const { return groups * 2 * 64 * 128; }
+  size_t smem() const { return 1024 + (size_t)wg_bytes() + nx * kXBytes + np * kHalf + kOut; }
+};
+
+struct Params {
+  CUtensorMap x, wg, panel, dx;   // boxes of 128, 32, 128 and 32 rows
+  const uint8_t* mask;
+  int64_t T;
+  int tiles, chunks;
+  int E, H;
+  float* part;     // [CTAs + chunks (packed: twice), E, 128] or null: no dWg
+  bool dx_on;
+  int* err;
+};
+
+// First item of CTA i of n items dealt to g CTAs.
+__host__ __device__ inline int64_t item_begin(int64_t i, int64_t n, int64_t g) { return i * n / g; }
+
+struct Ring {
+  int n, at;
+  uint32_t phase;
+  __device__ explicit Ring(int count) : n(count), at(0), phase(0) {}
+  __device__ void next() {
+    if (++at == n) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ void give_up(int* err, volatile int* abort) {
+  set_error(err, kDevTimeout);
+  *abort = 1;
+}
+
+// Descriptor of an MN-major operand whose groups of 64 columns are `group` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t group) {
+  return tc::sdesc_k128(saddr) | ((uint64_t)(group >> 4) << 16);
+}
+constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;
+
+// kGroups: of 64 experts.
+template <int kGroups>
+__global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant__ Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ __align__(8) uint64_t s_bar[3 * kMaxX + 2 * kMaxPanels + 11];
+  const Plan plan(P.E);
+  const uint32_t sW = (tc::smem_u32(smem_raw) + 1023u) & ~1023u, sX = sW + plan.wg_bytes();
+  const uint32_t sP = sX + plan.nx * kXBytes, sOut = sP + plan.np * kHalf;
+  const uint32_t bars = tc::smem_u32(s_bar);
+  auto x_full = [&](int s) { return bars + 8 * s; };
+  auto x_clean = [&](int s) { return bars + 8 * (kMaxX + s); };      // masked rows zeroed
+  auto x_empty = [&](int s) { return bars + 8 * (2 * kMaxX + s); };
+  auto p_full = [&](int s) { return bars + 8 * (3 * kMaxX + s); };
+  auto p_empty = [&](int s) { return bars + 8 * (3 * kMaxX + kMaxPanels + s); };
+  const uint32_t more = bars + 8 * (3 * kMaxX + 2 * kMaxPanels);
+  const uint32_t w_full = more, w_empty = more + 8, done = more + 16;
+  auto d1_full = [&](int a) { return more + 24 + 8 * a; };
+  auto d1_empty = [&](int a) { return more + 40 + 8 * a; };
+  auto d2_full = [&](int a) { return more + 56 + 8 * a; };
+  auto d2_empty = [&](int a) { return more + 72 + 8 * a; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int s = 0; s < kMaxX; ++s) {
+        tc::mbar_init(x_full(s), 1);
+        tc::mbar_init(x_clean(s), 1);
+        tc::mbar_init(x_empty(s), 1);
+      }
+      for (int s = 0; s < kMaxPanels; ++s) {
+        tc::mbar_init(p_full(s), 1);
+        tc::mbar_init(p_empty(s), 1);
+      }
+      tc::mbar_init(w_full, 1);
+      tc::mbar_init(w_empty, 1);
+      for (int a = 0; a < 2; ++a) {
+        tc::mbar_init(d1_full(a), 1);
+        tc::mbar_init(d1_empty(a), kEpiWarps);
+        tc::mbar_init(d2_full(a), 1);
+        tc::mbar_init(d2_empty(a), kEpiWarps);
+      }
+      tc::mbar_init(done, 1);
+      s_abort = 0;
+      tc::fence_barrier_init();
+      tc::fence_proxy_async_smem();
+    }
+  } else if (warp == 1) {
+    tc::tmem_alloc(tc::smem_u32(&s_tmem), kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  pdl_enter();
+  const uint32_t tmem = s_tmem;
+  const int64_t items = (int64_t)P.tiles * P.chunks;
+  const int64_t first = item_begin(blockIdx.x, items, gridDim.x), last = item_begin(blockIdx.x + 1, items, gridDim.x);
+  const bool dwg = P.part != nullptr;
+  // whether D1 starts with item i, and whether it is complete after it
+  auto starts = [&](int64_t i) { return i == first || i % P.tiles == 0 || (i % P.tiles) % plan.run == 0; };
+  auto ends = [&](int64_t i) { return i + 1 == last || starts(i + 1); };
+  // the producers' copies: stages filled and the parity of each one's latest
+  uint32_t filled = 0, fill_par = 0, w_phase = 0;
+  bool w_loaded = false;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ x and Wg
+    if (lane == 0) {
+      Ring r(plan.nx);
+      bool ok = true;
+      int chunk = -1;
+      for (int64_t i = first; i < last && ok; ++i) {
+        const int c = (int)(i / P.tiles), t0 = (int)(i - (int64_t)c * P.tiles) * kTok, h0 = c * kCols;
+        if (P.dx_on && c != chunk) {
+          ok = tc::mbar_wait(w_empty, w_phase ^ 1u, &s_abort, kWaitNs);
+          if (!ok) break;
+          tc::mbar_arrive_expect_tx(w_full, (uint32_t)plan.wg_bytes());
+          for (int half = 0; half < 2; ++half)
+            for (int e = 0; e < plan.groups * 64; e += 32)
+              tc::tma_load_2d(sW + half * plan.groups * 64 * 128 + e * 128, &P.wg, w_full, h0 + half * 64,
+                              plan.packed ? 0 : e);
+          w_phase ^= 1u;
+          w_loaded = true;
+        }
+        chunk = c;
+        if (!dwg) continue;
+        ok = tc::mbar_wait(x_empty(r.at), r.phase ^ 1u, &s_abort, kWaitNs);
+        if (!ok) break;
+        tc::mbar_arrive_expect_tx(x_full(r.at), kXBytes);
+        tc::tma_load_2d(sX + r.at * kXBytes, &P.x, x_full(r.at), h0, t0);
+        tc::tma_load_2d(sX + r.at * kXBytes + kHalf, &P.x, x_full(r.at), h0 + 64, t0);
+        filled |= 1u << r.at;
+        fill_par = (fill_par & ~(1u << r.at)) | (r.phase << r.at);
+        r.next();
+      }
+      if (!ok) give_up(P.err, &s_abort);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ panels
+    if (lane == 0) {
+      Ring r(plan.np);
+      bool ok = true;
+      for (int64_t i = first; i < last && ok; ++i) {
+        const int t0 = (int)(i % P.tiles) * kTok;
+        for (int p = 0; p < plan.panels; ++p) {
+          ok = tc::mbar_wait(p_empty(r.at), r.phase ^ 1u, &s_abort, kWaitNs);
+          if (!ok) break;
+          tc::mbar_arrive_expect_tx(p_full(r.at), kHalf);
+          // the low parts first
+          tc::tma_load_2d(sP + r.at * kHalf, &P.panel, p_full(r.at),
+                          (plan.packed ? 1 - p : (2 - p / kGroups) * kGroups + p % kGroups) * 64, t0);
+          filled |= 1u << r.at;
+          fill_par = (fill_par & ~(1u << r.at)) | (r.phase << r.at);
+          r.next();
+        }
+      }
+      if (!ok) give_up(P.err, &s_abort);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      Ring x(plan.nx), p(plan.np), d1(plan.bufs), d2(2);
+      int chunk = -1;
+      bool ok = true;
+      constexpr uint32_t id1 = tc::idesc_bf16_f32(kCols, 64) | kMajorA | kMajorB;
+      constexpr uint32_t id2 = tc::idesc_bf16_f32(kTok, kCols) | kMajorB;
+      for (int64_t i = first; i < last && ok; ++i) {
+        const int c = (int)(i / P.tiles);
+        const bool fresh = dwg && starts(i);
+        if (c != chunk && P.dx_on) {
+          ok = tc::mbar_wait(w_full, w_phase, &s_abort, kWaitNs);
+          w_phase ^= 1u;
+        }
+        chunk = c;
+        if (ok && fresh) ok = tc::mbar_wait(d1_empty(d1.at), d1.phase ^ 1u, &s_abort, kWaitNs);
+        if (ok && dwg) ok = tc::mbar_wait(P.mask ? x_clean(x.at) : x_full(x.at), x.phase, &s_abort, kWaitNs);
+        if (ok && P.dx_on) ok = tc::mbar_wait(d2_empty(d2.at), d2.phase ^ 1u, &s_abort, kWaitNs);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t a1 = sdesc_mn(sX + x.at * kXBytes, kHalf);
+        const uint32_t to1 = tmem + d1.at * 128, to2 = tmem + kD2 + d2.at * kCols;
+        uint32_t seen = fresh ? 0u : ~0u;   // groups of D1 that hold sums
+        bool d2_on = false;
+        for (int n = 0; n < plan.panels; ++n) {
+          ok = tc::mbar_wait(p_full(p.at), p.phase, &s_abort, kWaitNs);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t at = sP + p.at * kHalf;
+          const bool low = n < (plan.packed ? 1 : kGroups);   // the low parts come first
+          const int g = n % kGroups;
+          if (dwg) {
+            const uint64_t b1 = sdesc_mn(at, kHalf);
+            const uint32_t on = (seen >> g) & 1u;
+#pragma unroll
+            for (int k = 0; k < kTok / 16; ++k)
+              tc::mma_bf16(to1 + g * 64, a1 + k * (2048 >> 4), b1 + k * (2048 >> 4), id1, k ? 1u : on);
+            seen |= 1u << g;
+          }
+          if (P.dx_on && !low) {
+            const uint64_t a2 = tc::sdesc_k128(at), b2 = sdesc_mn(sW + g * 64 * 128, kGroups * 64 * 128);
+            const int steps = plan.packed ? 4 : min(4, (P.E - g * 64 + 15) / 16);
+            for (int k = 0; k < steps; ++k) {
+              tc::mma_bf16(to2, a2 + k * (32 >> 4), b2 + k * (2048 >> 4), id2, d2_on);
+              d2_on = true;
+            }
+          }
+          tc::tc_commit(p_empty(p.at));
+          p.next();
+        }
+        if (!ok) break;
+        if (dwg) {
+          tc::tc_commit(x_empty(x.at));
+          x.next();
+          if (ends(i)) {
+            tc::tc_commit(d1_full(d1.at));
+            d1.next();
+          }
+        }
+        if (P.dx_on) {
+          tc::tc_commit(d2_full(d2.at));
+          d2.next();
+          if (i + 1 == last || (int)((i + 1) / P.tiles) != c) tc::tc_commit(w_empty);
+        }
+      }
+      if (!ok) give_up(P.err, &s_abort);
+      tc::tc_commit(done);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ masked rows of x
+    if (dwg && P.mask) {
+      Ring x(plan.nx);
+      for (int64_t i = first; i < last; ++i) {
+        const int64_t t0 = (int64_t)(i % P.tiles) * kTok;
+        uint32_t out[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t t = t0 + k * 32 + lane;
+          out[k] = __ballot_sync(0xffffffffu, t < P.T && !P.mask[t]);
+        }
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(x_full(x.at), x.phase, &s_abort, kWaitNs))) {
+          if (lane == 0) give_up(P.err, &s_abort);
+          break;
+        }
+        if (out[0] | out[1] | out[2] | out[3]) {
+          uint8_t* tile = smem_raw + (sX + x.at * kXBytes - tc::smem_u32(smem_raw));
+          // 16 bytes a lane: a row of both halves at a time
+          uint8_t* mine = tile + (lane >> 4 & 1) * kHalf + (lane & 7) * 16;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            // the lanes' bit 3 takes every other one of the rows
+            for (uint32_t rest = out[k]; rest;) {
+              const int r0 = __ffs(rest) - 1;
+              rest &= rest - 1;
+              const int r1 = rest ? __ffs(rest) - 1 : r0;
+              rest &= rest - 1;
+              *reinterpret_cast<uint4*>(mine + (k * 32 + (lane & 8 ? r1 : r0)) * 128) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          tc::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(x_clean(x.at));
+        x.next();
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, half = (warp - 4) >> 2;   // TMEM lanes 32 q .. 32 q + 31, columns
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t buf = sOut + (warp - 4) * kStoreBytes;
+    uint8_t* row = smem_raw + (buf - tc::smem_u32(smem_raw)) + lane * 128;
+    Ring d1(plan.bufs), d2(2);
+    float sum[kGroups * 32] = {};   // of column half * 32 + j of each group: this thread's column of x
+    bool ok = true;
+    for (int64_t i = first; i < last && ok; ++i) {
+      const int c = (int)(i / P.tiles);
+      if (P.dx_on) {
+        const int64_t t0 = (i - (int64_t)c * P.tiles) * kTok + q * 32;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(d2_full(d2.at), d2.phase, &s_abort, kWaitNs));
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (lane == 0) tc::bulk_wait_read();   // the last tile's store has read the buffer
+        __syncwarp();
+        const uint32_t at = lanes + kD2 + d2.at * kCols + half * 64;
+        uint32_t r[2][32];
+        tc::tmem_ld_32x32b_x32(at, r[0]);
+        tc::tmem_ld_32x32b_x32(at + 32, r[1]);
+        tc::tmem_wait_ld();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(d2_empty(d2.at));   // tensor memory has been read
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[k][j]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)   // 16 bytes at the place that the 128-byte swizzle gives them
+            *reinterpret_cast<uint4*>(row + (((k * 4 + j) ^ (lane & 7)) << 4)) = Vec<bf16>::pack(v + j * 8);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && t0 < P.T && c * kCols + half * 64 < P.H)
+          tc::tma_store_2d(&P.dx, buf, c * kCols + half * 64, (int)t0);
+        d2.next();
+      }
+      if (dwg && ends(i)) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(d1_full(d1.at), d1.phase, &s_abort, kWaitNs));
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          uint32_t r[32];
+          tc::tmem_ld_32x32b_x32(lanes + d1.at * 128 + g * 64 + half * 32, r);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[g * 32 + j] += __uint_as_float(r[j]);
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(d1_empty(d1.at));
+        d1.next();
+      }
+      if (dwg && (i + 1 == last || (int)((i + 1) / P.tiles) != c)) {
+        // up to 32 experts both halves have sums of the same experts: a row each
+        const int64_t slot = ((int64_t)blockIdx.x + c) * (plan.packed ? 2 : 1) + (plan.packed ? half : 0);
+        float* out = P.part + slot * P.E * kCols + q * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < kGroups * 32; ++j) {
+          const int e = plan.packed ? j : j / 32 * 64 + half * 32 + j % 32;
+          if (e < P.E) out[(int64_t)e * kCols] = sum[j];
+          sum[j] = 0.f;
+        }
+      }
+    }
+    if (!ok && lane == 0) give_up(P.err, &s_abort);
+    if (lane == 0) tc::bulk_wait_all();
+  }
+  __syncwarp();
+  tc::tc_fence_before();
+  __syncthreads();
+  if (s_abort && lane == 0) {   // every copy lands before the CTA leaves
+    if (w_loaded) tc::mbar_wait(w_full, w_phase ^ 1u, nullptr, kWaitNs);
+    for (int s = 0; s < (warp == 0 ? plan.nx : plan.np); ++s)
+      if ((filled >> s) & 1u) tc::mbar_wait(warp == 0 ? x_full(s) : p_full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
+  }
+  if (warp == 1) {
+    // and every MMA has finished before its memory is freed
+    if (lane == 0 && !tc::mbar_wait(done, 0, nullptr, kWaitNs)) set_error(P.err, kDevTimeout);
+    __syncwarp();
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// dWg: the partial sums of a chunk's CTAs in their order; the last blocks: the
+// bias' gradient, the rows of partial sums in order.
+__global__ void __launch_bounds__(256)
+gate_sums_kernel(const float* __restrict__ part, int tiles, int chunks, int ctas, int E, int H,
+                 float* __restrict__ dWg, const float* __restrict__ part_b, int rows_b, float* __restrict__ dbias) {
+  pdl_enter();
+  const int c = blockIdx.x;
+  if (c < chunks) {
+    const int64_t items = (int64_t)tiles * chunks, a = (int64_t)c * tiles, z = a + tiles;
+    int64_t i0 = a * ctas / items;   // the CTA that has item a, or one beside it
+    while (i0 > 0 && item_begin(i0, items, ctas) > a) --i0;
+    while (item_begin(i0 + 1, items, ctas) <= a) ++i0;
+    const int e = blockIdx.y * 8 + threadIdx.x / 32, h = c * kCols + threadIdx.x % 32 * 4;
+    if (e >= E || h >= H) return;   // H is a multiple of 8
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int64_t i = i0; i < ctas && item_begin(i, items, ctas) < z; ++i) {
+      const int n = Plan(E).packed ? 2 : 1;
+      for (int k = 0; k < n; ++k) {
+        const float4 v =
+            *reinterpret_cast<const float4*>(part + (((i + c) * n + k) * E + e) * kCols + threadIdx.x % 32 * 4);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+    }
+    *reinterpret_cast<float4*>(dWg + (int64_t)e * H + h) = s;
+  } else {
+    __shared__ float s_b[8][32];
+    const int e = blockIdx.y * 32 + threadIdx.x % 32, g = threadIdx.x / 32;
+    float v = 0.f;
+    if (e < E && blockIdx.y * 32 < E)
+      for (int r = g; r < rows_b; r += 8) v += part_b[(int64_t)r * E + e];
+    s_b[g][threadIdx.x % 32] = v;
+    __syncthreads();
+    if (g == 0 && e < E) {
+      for (int k = 1; k < 8; ++k) v += s_b[k][threadIdx.x];
+      dbias[e] = v;
+    }
+  }
+}
+
+}  // namespace
+
+int64_t gate_part_floats(const Shape& s) {
+  const int64_t chunks = (s.H + kCols - 1) / kCols;
+  return ((int64_t)sm_count() + chunks) * (Plan(s.E).packed ? 2 : 1) * s.E * kCols;
+}
+int gate_panel_cols(int E) { return Plan(E).panels * 64; }
+
+cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* panels, float* part,
+                           const float* part_b, int rows_b, int* err, cudaStream_t st) {
+  const Plan plan(s.E);
+  const int64_t tiles = (s.T + kTok - 1) / kTok, chunks = (s.H + kCols - 1) / kCols;
+  const int sms = sm_count();
+  const int ctas = (int)(tiles * chunks < sms ? tiles * chunks : sms);
+  cudaError_t e = cudaSuccess;
+  if (b.dx || b.dWg) {
+    Params P = {};
+    const uint64_t T = (uint64_t)s.T, H = (uint64_t)s.H;
+    if ((b.dWg && !tma_map_bf16(&P.x, b.x, T, H, kTok)) ||
+        (b.dx && (!tma_map_bf16(&P.wg, b.Wg, (uint64_t)s.E, H, 32) || !tma_map_bf16(&P.dx, b.dx, T, H, 32))) ||
+        !tma_map_bf16(&P.panel, panels, T, (uint64_t)plan.panels * 64, kTok))
+      return cudaErrorNotSupported;
+    P.mask = b.mask;
+    P.T = s.T;
+    P.tiles = (int)tiles;
+    P.chunks = (int)chunks;
+    P.E = s.E;
+    P.H = s.H;
+    P.part = b.dWg ? part : nullptr;
+    P.dx_on = b.dx != nullptr;
+    P.err = err;
+    auto kern = plan.groups == 1 ? gate_kernel<1> : plan.groups == 2 ? gate_kernel<2> : plan.groups == 3 ? gate_kernel<3> : gate_kernel<4>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem());
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(kern, dim3((unsigned)ctas), dim3(kThreads), plan.smem(), st, 1, P);
+  }
+  if (e == cudaSuccess && (b.dWg || b.dbias)) {
+    const int cols = b.dWg ? (int)chunks : 0;
+    e = launch_kernel(gate_sums_kernel, dim3((unsigned)(cols + (b.dbias ? 1 : 0)), (unsigned)((s.E + 7) / 8)), dim3(256),
+                      0, st, 1, part, (int)tiles, cols, ctas, s.E, s.H, b.dWg, part_b, rows_b, b.dbias);
+  }
+  return e;
+}
+
+}  // namespace moe
