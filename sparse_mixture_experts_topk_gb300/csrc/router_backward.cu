@@ -405,10 +405,10 @@ cudaError_t by_experts(int E, F f) {
 
 }  // namespace
 
-// Two blocks an SM at most while a block has no more than 2^13 tokens, and four rounds of tokens a block at least.
+// Two blocks an SM at most while a block has no more than 2^13 tokens.
 int64_t balance_partials(const Shape& s) {
   const int64_t tokens = kThreads / (s.E <= 32 ? 8 : s.E <= 64 ? 16 : 32);
-  const int64_t want = (s.T + 4 * tokens - 1) / (4 * tokens), cap = 2 * (int64_t)sm_count();
+  const int64_t want = (s.T + tokens - 1) / tokens, cap = 2 * (int64_t)sm_count();
   const int64_t least = (s.T + 8191) / 8192;
   int64_t n = want < cap ? want : cap;
   if (n < least) n = least;

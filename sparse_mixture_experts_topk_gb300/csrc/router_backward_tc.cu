@@ -54,11 +54,11 @@ struct Plan {
   int E, groups, panels;
   bool packed;      // up to 32 experts: panels [high | middle] and [low | 0]
   int nx, np;       // ring sizes
-  int bufs, run;    // buffers of D1, and tiles that it sums
+  int bufs;         // buffers of D1
   __host__ __device__ explicit Plan(int e)
       : E(e), groups((e + 63) / 64), panels(e <= 32 ? 2 : 3 * ((e + 63) / 64)), packed(e <= 32),
         nx(e <= 128 ? 3 : 2), np(e <= 64 || (e > 128 && e <= 192) ? 5 : 4),
-        bufs(e <= 128 ? 2 : 1), run(e <= 128 ? 1 : 4) {}
+        bufs(e <= 128 ? 2 : 1) {}
   __host__ __device__ int wg_bytes() const { return groups * 2 * 64 * 128; }
   size_t smem() const { return 1024 + (size_t)wg_bytes() + nx * kXBytes + np * kHalf + kOut; }
 };
@@ -76,6 +76,24 @@ struct Params {
 
 // First item of CTA i of n items dealt to g CTAs.
 __host__ __device__ inline int64_t item_begin(int64_t i, int64_t n, int64_t g) { return i * n / g; }
+
+// A CTA's (chunk, tile) pairs in order; 64-bit divisions once, not at each.
+struct Walk {
+  int64_t left;
+  int chunk, tile, tiles;
+  __device__ Walk(int64_t first, int64_t last, int n)
+      : left(last - first), chunk((int)(first / n)), tile((int)(first % n)), tiles(n) {}
+  __device__ void next() {
+    --left;
+    if (++tile == tiles) {
+      tile = 0;
+      ++chunk;
+    }
+  }
+  // whether the CTA leaves the chunk, and with it the tokens of a run of tiles, after this pair
+  __device__ bool leaves() const { return left == 1 || tile + 1 == tiles; }
+  __device__ bool ends(int run) const { return leaves() || (tile + 1) % run == 0; }
+};
 
 struct Ring {
   int n, at;
@@ -100,8 +118,8 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t group) {
 }
 constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;
 
-// kGroups: of 64 experts.
-template <int kGroups>
+// kGroups: of 64 experts; kPacked: up to 32.
+template <int kGroups, bool kPacked>
 __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant__ Params P) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -159,29 +177,27 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   const int64_t items = (int64_t)P.tiles * P.chunks;
   const int64_t first = item_begin(blockIdx.x, items, gridDim.x), last = item_begin(blockIdx.x + 1, items, gridDim.x);
   const bool dwg = P.part != nullptr;
-  // whether D1 starts with item i, and whether it is complete after it
-  auto starts = [&](int64_t i) { return i == first || i % P.tiles == 0 || (i % P.tiles) % plan.run == 0; };
-  auto ends = [&](int64_t i) { return i + 1 == last || starts(i + 1); };
+  constexpr int kRun = kGroups <= 2 ? 1 : 4;   // tiles that D1 sums
   // the producers' copies: stages filled and the parity of each one's latest
   uint32_t filled = 0, fill_par = 0, w_phase = 0;
   bool w_loaded = false;
 
   if (warp == 0) {
     // ------------------------------------------------------------ x and Wg
-    if (lane == 0) {
+    if (tc::elect_one()) {
       Ring r(plan.nx);
       bool ok = true;
       int chunk = -1;
-      for (int64_t i = first; i < last && ok; ++i) {
-        const int c = (int)(i / P.tiles), t0 = (int)(i - (int64_t)c * P.tiles) * kTok, h0 = c * kCols;
+      for (Walk w(first, last, P.tiles); w.left > 0 && ok; w.next()) {
+        const int c = w.chunk, t0 = w.tile * kTok, h0 = c * kCols;
         if (P.dx_on && c != chunk) {
           ok = tc::mbar_wait(w_empty, w_phase ^ 1u, &s_abort, kWaitNs);
           if (!ok) break;
           tc::mbar_arrive_expect_tx(w_full, (uint32_t)plan.wg_bytes());
           for (int half = 0; half < 2; ++half)
-            for (int e = 0; e < plan.groups * 64; e += 32)
-              tc::tma_load_2d(sW + half * plan.groups * 64 * 128 + e * 128, &P.wg, w_full, h0 + half * 64,
-                              plan.packed ? 0 : e);
+            for (int e = 0; e < kGroups * 64; e += 32)
+              tc::tma_load_2d(sW + half * kGroups * 64 * 128 + e * 128, &P.wg, w_full, h0 + half * 64,
+                              kPacked ? 0 : e);
           w_phase ^= 1u;
           w_loaded = true;
         }
@@ -200,18 +216,18 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ panels
-    if (lane == 0) {
+    if (tc::elect_one()) {
       Ring r(plan.np);
       bool ok = true;
-      for (int64_t i = first; i < last && ok; ++i) {
-        const int t0 = (int)(i % P.tiles) * kTok;
+      for (Walk w(first, last, P.tiles); w.left > 0 && ok; w.next()) {
+        const int t0 = w.tile * kTok;
         for (int p = 0; p < plan.panels; ++p) {
           ok = tc::mbar_wait(p_empty(r.at), r.phase ^ 1u, &s_abort, kWaitNs);
           if (!ok) break;
           tc::mbar_arrive_expect_tx(p_full(r.at), kHalf);
           // the low parts first
           tc::tma_load_2d(sP + r.at * kHalf, &P.panel, p_full(r.at),
-                          (plan.packed ? 1 - p : (2 - p / kGroups) * kGroups + p % kGroups) * 64, t0);
+                          (kPacked ? 1 - p : (2 - p / kGroups) * kGroups + p % kGroups) * 64, t0);
           filled |= 1u << r.at;
           fill_par = (fill_par & ~(1u << r.at)) | (r.phase << r.at);
           r.next();
@@ -221,68 +237,85 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      Ring x(plan.nx), p(plan.np), d1(plan.bufs), d2(2);
-      int chunk = -1;
-      bool ok = true;
+    // This thread's own latency counts: a wait takes 200 cycles even on a
+    // barrier that is complete, so the next ones are looked at before MMAs are
+    // issued, and the loops are unrolled (rolled ones took 6600 cycles a tile of
+    // 64 experts where the MMAs take 1700).
+    if (tc::elect_one()) {
+      constexpr int kPanels = kPacked ? 2 : 3 * kGroups, kLow = kPacked ? 1 : kGroups;
       constexpr uint32_t id1 = tc::idesc_bf16_f32(kCols, 64) | kMajorA | kMajorB;
       constexpr uint32_t id2 = tc::idesc_bf16_f32(kTok, kCols) | kMajorB;
-      for (int64_t i = first; i < last && ok; ++i) {
-        const int c = (int)(i / P.tiles);
-        const bool fresh = dwg && starts(i);
-        if (c != chunk && P.dx_on) {
+      Ring x(plan.nx), p(plan.np), d1(plan.bufs), d2(2);
+      const uint64_t x0 = sdesc_mn(sX, kHalf), p_mn = sdesc_mn(sP, kHalf), p_k = tc::sdesc_k128(sP);
+      const uint64_t w0 = sdesc_mn(sW, kGroups * 64 * 128);
+      const bool dx_on = P.dx_on, clean = P.mask != nullptr;
+      auto x_bar = [&](int at) { return clean ? x_clean(at) : x_full(at); };
+      int chunk = -1;
+      bool ok = true, begins = true;   // begins: D1 with this pair
+      bool x_ready = false, p_ready = false, d1_ready = false, d2_ready = false;
+#pragma unroll 1
+      for (Walk w(first, last, P.tiles); w.left > 0 && ok; w.next()) {
+        const bool fresh = begins;
+        begins = w.ends(kRun);
+        if (dx_on && w.chunk != chunk) {
           ok = tc::mbar_wait(w_full, w_phase, &s_abort, kWaitNs);
           w_phase ^= 1u;
         }
-        chunk = c;
-        if (ok && fresh) ok = tc::mbar_wait(d1_empty(d1.at), d1.phase ^ 1u, &s_abort, kWaitNs);
-        if (ok && dwg) ok = tc::mbar_wait(P.mask ? x_clean(x.at) : x_full(x.at), x.phase, &s_abort, kWaitNs);
-        if (ok && P.dx_on) ok = tc::mbar_wait(d2_empty(d2.at), d2.phase ^ 1u, &s_abort, kWaitNs);
+        chunk = w.chunk;
+        if (dwg) {
+          if (ok && fresh && !d1_ready) ok = tc::mbar_wait(d1_empty(d1.at), d1.phase ^ 1u, &s_abort, kWaitNs);
+          if (ok && !x_ready) ok = tc::mbar_wait(x_bar(x.at), x.phase, &s_abort, kWaitNs);
+        }
+        if (ok && dx_on && !d2_ready) ok = tc::mbar_wait(d2_empty(d2.at), d2.phase ^ 1u, &s_abort, kWaitNs);
         if (!ok) break;
         tc::tc_fence_after();
-        const uint64_t a1 = sdesc_mn(sX + x.at * kXBytes, kHalf);
+        const uint64_t a1 = x0 + (uint32_t)(x.at * (kXBytes >> 4));
         const uint32_t to1 = tmem + d1.at * 128, to2 = tmem + kD2 + d2.at * kCols;
-        uint32_t seen = fresh ? 0u : ~0u;   // groups of D1 that hold sums
-        bool d2_on = false;
-        for (int n = 0; n < plan.panels; ++n) {
-          ok = tc::mbar_wait(p_full(p.at), p.phase, &s_abort, kWaitNs);
-          if (!ok) break;
-          tc::tc_fence_after();
-          const uint32_t at = sP + p.at * kHalf;
-          const bool low = n < (plan.packed ? 1 : kGroups);   // the low parts come first
-          const int g = n % kGroups;
+        const int x_at = x.at, d1_at = d1.at, d2_at = d2.at;
+        if (dwg) {
+          x.next();
+          if (begins) d1.next();
+        }
+        if (dx_on) d2.next();
+#pragma unroll
+        for (int n = 0; n < kPanels; ++n) {
+          if (!p_ready && !tc::mbar_wait(p_full(p.at), p.phase, &s_abort, kWaitNs)) {
+            ok = false;
+            break;
+          }
+          const int here = p.at, g = n % kGroups;
+          p.next();
+          p_ready = tc::mbar_test_wait(p_full(p.at), p.phase);
+          if (n == kPanels - 1) {
+            x_ready = dwg && tc::mbar_test_wait(x_bar(x.at), x.phase);
+            d1_ready = dwg && begins && tc::mbar_test_wait(d1_empty(d1.at), d1.phase ^ 1u);
+            d2_ready = dx_on && tc::mbar_test_wait(d2_empty(d2.at), d2.phase ^ 1u);
+          }
+          const uint32_t off = (uint32_t)(here * (kHalf >> 4));
           if (dwg) {
-            const uint64_t b1 = sdesc_mn(at, kHalf);
-            const uint32_t on = (seen >> g) & 1u;
+            const uint64_t b1 = p_mn + off;
+            // the first panel of a group starts its sums (packed: one group)
+            const uint32_t on = n < (kPacked ? 1 : kGroups) && fresh ? 0u : 1u;
 #pragma unroll
             for (int k = 0; k < kTok / 16; ++k)
               tc::mma_bf16(to1 + g * 64, a1 + k * (2048 >> 4), b1 + k * (2048 >> 4), id1, k ? 1u : on);
-            seen |= 1u << g;
           }
-          if (P.dx_on && !low) {
-            const uint64_t a2 = tc::sdesc_k128(at), b2 = sdesc_mn(sW + g * 64 * 128, kGroups * 64 * 128);
-            const int steps = plan.packed ? 4 : min(4, (P.E - g * 64 + 15) / 16);
-            for (int k = 0; k < steps; ++k) {
-              tc::mma_bf16(to2, a2 + k * (32 >> 4), b2 + k * (2048 >> 4), id2, d2_on);
-              d2_on = true;
-            }
+          if (n >= kLow && dx_on) {   // the low parts come first
+            const uint64_t a2 = p_k + off, b2 = w0 + (uint32_t)(g * (64 * 128 >> 4));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::mma_bf16(to2, a2 + k * (32 >> 4), b2 + k * (2048 >> 4), id2, n > kLow || k ? 1u : 0u);
           }
-          tc::tc_commit(p_empty(p.at));
-          p.next();
+          tc::tc_commit(p_empty(here));
         }
         if (!ok) break;
         if (dwg) {
-          tc::tc_commit(x_empty(x.at));
-          x.next();
-          if (ends(i)) {
-            tc::tc_commit(d1_full(d1.at));
-            d1.next();
-          }
+          tc::tc_commit(x_empty(x_at));
+          if (begins) tc::tc_commit(d1_full(d1_at));
         }
-        if (P.dx_on) {
-          tc::tc_commit(d2_full(d2.at));
-          d2.next();
-          if (i + 1 == last || (int)((i + 1) / P.tiles) != c) tc::tc_commit(w_empty);
+        if (dx_on) {
+          tc::tc_commit(d2_full(d2_at));
+          if (w.leaves()) tc::tc_commit(w_empty);
         }
       }
       if (!ok) give_up(P.err, &s_abort);
@@ -292,8 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     // ------------------------------------------------------------ masked rows of x
     if (dwg && P.mask) {
       Ring x(plan.nx);
-      for (int64_t i = first; i < last; ++i) {
-        const int64_t t0 = (int64_t)(i % P.tiles) * kTok;
+      for (Walk w(first, last, P.tiles); w.left > 0; w.next()) {
+        const int64_t t0 = (int64_t)w.tile * kTok;
         uint32_t out[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -335,10 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     Ring d1(plan.bufs), d2(2);
     float sum[kGroups * 32] = {};   // of column half * 32 + j of each group: this thread's column of x
     bool ok = true;
-    for (int64_t i = first; i < last && ok; ++i) {
-      const int c = (int)(i / P.tiles);
+    for (Walk w(first, last, P.tiles); w.left > 0 && ok; w.next()) {
+      const int c = w.chunk;
       if (P.dx_on) {
-        const int64_t t0 = (i - (int64_t)c * P.tiles) * kTok + q * 32;
+        const int64_t t0 = (int64_t)w.tile * kTok + q * 32;
         ok = __all_sync(0xffffffffu, tc::mbar_wait(d2_full(d2.at), d2.phase, &s_abort, kWaitNs));
         if (!ok) break;
         tc::tc_fence_after();
@@ -367,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
           tc::tma_store_2d(&P.dx, buf, c * kCols + half * 64, (int)t0);
         d2.next();
       }
-      if (dwg && ends(i)) {
+      if (dwg && w.ends(kRun)) {
         ok = __all_sync(0xffffffffu, tc::mbar_wait(d1_full(d1.at), d1.phase, &s_abort, kWaitNs));
         if (!ok) break;
         tc::tc_fence_after();
@@ -384,13 +417,13 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
         if (lane == 0) tc::mbar_arrive(d1_empty(d1.at));
         d1.next();
       }
-      if (dwg && (i + 1 == last || (int)((i + 1) / P.tiles) != c)) {
+      if (dwg && w.leaves()) {
         // up to 32 experts both halves have sums of the same experts: a row each
-        const int64_t slot = ((int64_t)blockIdx.x + c) * (plan.packed ? 2 : 1) + (plan.packed ? half : 0);
+        const int64_t slot = ((int64_t)blockIdx.x + c) * (kPacked ? 2 : 1) + (kPacked ? half : 0);
         float* out = P.part + slot * P.E * kCols + q * 32 + lane;
 #pragma unroll
         for (int j = 0; j < kGroups * 32; ++j) {
-          const int e = plan.packed ? j : j / 32 * 64 + half * 32 + j % 32;
+          const int e = kPacked ? j : j / 32 * 64 + half * 32 + j % 32;
           if (e < P.E) out[(int64_t)e * kCols] = sum[j];
           sum[j] = 0.f;
         }
@@ -402,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
-  if (s_abort && lane == 0) {   // every copy lands before the CTA leaves
+  if (s_abort && (filled || w_loaded)) {   // the producing threads: every copy lands before the CTA leaves
     if (w_loaded) tc::mbar_wait(w_full, w_phase ^ 1u, nullptr, kWaitNs);
     for (int s = 0; s < (warp == 0 ? plan.nx : plan.np); ++s)
       if ((filled >> s) & 1u) tc::mbar_wait(warp == 0 ? x_full(s) : p_full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
@@ -490,7 +523,11 @@ cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* 
     P.part = b.dWg ? part : nullptr;
     P.dx_on = b.dx != nullptr;
     P.err = err;
-    auto kern = plan.groups == 1 ? gate_kernel<1> : plan.groups == 2 ? gate_kernel<2> : plan.groups == 3 ? gate_kernel<3> : gate_kernel<4>;
+    auto kern = plan.packed        ? gate_kernel<1, true>
+                : plan.groups == 1 ? gate_kernel<1, false>
+                : plan.groups == 2 ? gate_kernel<2, false>
+                : plan.groups == 3 ? gate_kernel<3, false>
+                                   : gate_kernel<4, false>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem());
     if (e != cudaSuccess) return e;
     e = launch_kernel(kern, dim3((unsigned)ctas), dim3(kThreads), plan.smem(), st, 1, P);
