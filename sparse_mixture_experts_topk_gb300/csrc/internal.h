@@ -238,6 +238,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int count, int grad_dt
 // The load-balancing loss and the router's gradient.  blocks: partial sums of
 // the tokens' kernels; the products' scratch follows from the shape.
 int64_t balance_partials(const Shape& s);
+int64_t dlogits_partials(const Shape& s);
 struct BalanceOut {
   float* psum;
   int32_t* count;
@@ -263,7 +264,7 @@ struct RouterBackward {
   void* dx;
 };
 // dl: router_scratch_bytes: the scores' gradient, [T, E] fp32, or in bf16
-// parts; part_b: [balance_partials, E] floats, part_w: router_weight_partials
+// parts; part_b: [dlogits_partials, E] floats, part_w: router_weight_partials
 // floats
 bool router_gate_on_tensor_cores(const Shape& s);
 size_t router_scratch_bytes(const Shape& s);

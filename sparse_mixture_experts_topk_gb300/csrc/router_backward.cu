@@ -23,6 +23,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 4;
 
 // Lanes for a token and experts for a lane, by the number of experts.
 template <int kLanes, int kVecs>
@@ -107,20 +108,28 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids
   const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   float acc[G::kN] = {};
   int n = 0;
-  for (int64_t t0 = (int64_t)blockIdx.x * G::kTokens; t0 < T; t0 += (int64_t)gridDim.x * G::kTokens) {
-    const int64_t t = t0 + group;
-    const bool live = t < T && (!mask || mask[t]);
-    float l[G::kN];
-    G::load(logits + t * E, lane, E, inv_tau, live, l);
-    G::softmax(l);
-    if (live) {
+  // kAhead tokens of a group at a time: their loads are in flight together
+  const int64_t stride = (int64_t)gridDim.x * G::kTokens;
+  for (int64_t t0 = (int64_t)blockIdx.x * G::kTokens; t0 < T; t0 += kAhead * stride) {
+    float l[kAhead][G::kN];
+    bool live[kAhead];
+    int id[kAhead];
 #pragma unroll
-      for (int i = 0; i < G::kN; ++i) acc[i] += l[i];
-      ++n;
-      if (lane < K) {
-        const int e = ids[t * K + lane];
-        if (e >= 0 && e < E) atomicAdd(&s_count[e], 1);
-        else if (e != -1) set_error(err, kDevBadIndex);
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t t = t0 + u * stride + group;
+      live[u] = t < T && (!mask || mask[t]);
+      id[u] = t < T && lane < K ? ids[t * K + lane] : -1;
+      G::load(logits + t * E, lane, E, inv_tau, t < T, l[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      G::softmax(l[u]);
+      if (live[u]) {
+#pragma unroll
+        for (int i = 0; i < G::kN; ++i) acc[i] += l[u][i];
+        ++n;
+        if (id[u] >= 0 && id[u] < E) atomicAdd(&s_count[id[u]], 1);
+        else if (id[u] != -1) set_error(err, kDevBadIndex);
       }
     }
   }
@@ -129,24 +138,37 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids
   for (int i = threadIdx.x; i <= E; i += kThreads) part_c[(int64_t)blockIdx.x * (E + 1) + i] = s_count[i];
 }
 
-// One block: the partial rows added up, four threads to an expert, and the loss.
+// a + b, and what its rounding lost added to `low` (exact: Knuth's two-sum).
+// The sums below are held as such pairs: GB300 does few fp64 operations a
+// cycle, and one block of them took 10 us for 256 experts.
+__device__ __forceinline__ float two_sum(float a, float b, float* low) {
+  const float s = a + b, t = s - a;
+  *low += (a - (s - t)) + (b - t);
+  return s;
+}
+
+// One block: the partial rows added up, 1024 / width threads to an expert
+// (width: E rounded up to 32, 64, 128 or 256), and the loss.
 __global__ void __launch_bounds__(1024)
 balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_c, int rows, int E, int K,
-                      BalanceOut o) {
-  __shared__ double s_p[4][256], s_term[256];
-  __shared__ int s_c[4][256];
+                      int width, BalanceOut o) {
+  __shared__ float s_hi[1024], s_lo[1024];
+  __shared__ int s_c[1024];
   __shared__ int s_n;
   pdl_enter();
-  const int e = threadIdx.x % 256, q = threadIdx.x / 256;
-  double p = 0.0;
+  const int e = threadIdx.x % width, q = threadIdx.x / width, threads = 1024 / width;
+  float hi = 0.f, lo = 0.f;
   int c = 0;
-  if (e < E)
-    for (int r = q; r < rows; r += 4) {
-      p += part_p[(int64_t)r * E + e];
+  if (e < E) {
+#pragma unroll 8
+    for (int r = q; r < rows; r += threads) {
+      hi = two_sum(hi, part_p[(int64_t)r * E + e], &lo);
       c += part_c[(int64_t)r * (E + 1) + e];
     }
-  s_p[q][e] = p;
-  s_c[q][e] = c;
+  }
+  s_hi[threadIdx.x] = hi;
+  s_lo[threadIdx.x] = lo;
+  s_c[threadIdx.x] = c;
   if (threadIdx.x < 32) {
     int n = 0;
     for (int r = threadIdx.x; r < rows; r += 32) n += part_c[(int64_t)r * (E + 1) + E];
@@ -154,26 +176,39 @@ balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restric
     for (int w = 16; w > 0; w >>= 1) n += __shfl_xor_sync(0xffffffffu, n, w);
     if (threadIdx.x == 0) s_n = n;
   }
-  __syncthreads();
-  if (q == 0) {
-    const double ps = (s_p[0][e] + s_p[1][e]) + (s_p[2][e] + s_p[3][e]);
-    const int ct = s_c[0][e] + s_c[1][e] + s_c[2][e] + s_c[3][e];
-    if (e < E) {
-      if (o.psum) o.psum[e] = (float)ps;
-      if (o.count) o.count[e] = ct;
+  for (int half = threads / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (q < half) {
+      const int other = threadIdx.x + half * width;
+      lo += s_lo[other];
+      hi = two_sum(hi, s_hi[other], &lo);
+      c += s_c[other];
+      s_hi[threadIdx.x] = hi;
+      s_lo[threadIdx.x] = lo;
+      s_c[threadIdx.x] = c;
     }
-    s_term[e] = e < E ? ps * ct : 0.0;
   }
   __syncthreads();
+  const float sum = hi + lo;
+  if (q == 0 && e < E) {
+    if (o.psum) o.psum[e] = sum;
+    if (o.count) o.count[e] = c;
+  }
+  const float n = (float)s_n;
+  // f_e P_e, each a share, in fp32
+  if (q == 0) s_hi[threadIdx.x] = e < E && s_n ? (float)c / (n * (float)K) * (sum / n) : 0.f;
+  __syncthreads();
   if (threadIdx.x < 32) {
-    double v = 0.0;
-    for (int i = threadIdx.x; i < 256; i += 32) v += s_term[i];
+    float v = 0.f, low = 0.f;
+    for (int i = threadIdx.x; i < width; i += 32) v = two_sum(v, s_hi[i], &low);
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
+    for (int w = 16; w > 0; w >>= 1) {
+      low += __shfl_xor_sync(0xffffffffu, low, w);
+      v = two_sum(v, __shfl_xor_sync(0xffffffffu, v, w), &low);
+    }
     if (threadIdx.x == 0) {
-      const double n = s_n;
       if (o.tokens) *o.tokens = s_n;
-      if (o.loss) *o.loss = s_n ? (float)(E * v / (n * K * n)) : 0.f;
+      if (o.loss) *o.loss = (float)E * (v + low);
     }
   }
 }
@@ -209,21 +244,24 @@ dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* 
   const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   float c[G::kN], acc[G::kN] = {};
   if (b.dloss) {
-    const int n = *b.tokens;
-    const double f = n > 0 ? (double)*b.dloss * E / ((double)n * n * K) : 0.0;
+    const float n = (float)*b.tokens, f = n > 0.f ? *b.dloss / n * ((float)E / (n * (float)K)) : 0.f;
 #pragma unroll
     for (int i = 0; i < G::kN; ++i) {
       const int e = G::expert(lane, i);
-      c[i] = e < E ? (float)(f * b.count[e]) : 0.f;
+      c[i] = e < E ? f * (float)b.count[e] : 0.f;
     }
   }
   for (int64_t t0 = (int64_t)blockIdx.x * G::kTokens; t0 < T; t0 += (int64_t)gridDim.x * G::kTokens) {
     const int64_t t = t0 + group;
     const bool live = t < T && (!b.mask || b.mask[t]);
+    // lane j has choice j; what is loaded for a token that does not count is not used
+    const bool mine = b.dw && t < T && lane < K;
+    int id = mine ? b.ids[t * K + lane] : -1;
+    float g = mine ? b.dw[t * K + lane] : 0.f;
     float d[G::kN] = {};
     if (b.dloss) {
       float p[G::kN], dot = 0.f;
-      G::load(b.logits + t * E, lane, E, inv_tau, live, p);
+      G::load(b.logits + t * E, lane, E, inv_tau, t < T, p);
       G::softmax(p);
 #pragma unroll
       for (int i = 0; i < G::kN; ++i) dot = fmaf(p[i], c[i], dot);
@@ -232,18 +270,13 @@ dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* 
       for (int i = 0; i < G::kN; ++i) d[i] = p[i] * (c[i] - dot);
     }
     if (b.dw) {
-      // lane j has choice j
-      int id = -1;
-      float z = -INFINITY, g = 0.f;
-      if (live && lane < K) {
-        id = b.ids[t * K + lane];
-        if (id >= 0 && id < E) {
-          z = b.logits[t * E + id] * inv_tau;
-          g = b.dw[t * K + lane];
-        } else {
-          if (id != -1) set_error(err, kDevBadIndex);
-          id = -1;
-        }
+      float z = -INFINITY;
+      if (live && id >= 0 && id < E) {
+        z = b.logits[t * E + id] * inv_tau;
+      } else {
+        if (live && id != -1) set_error(err, kDevBadIndex);
+        id = -1;
+        g = 0.f;
       }
       const float top = G::max(z), x = id >= 0 ? expf(z - top) : 0.f, s = G::sum(x);
       const float w = s != 0.f ? x / s : 0.f, dot = G::sum(w * g), v = w * (g - dot);
@@ -405,15 +438,19 @@ cudaError_t by_experts(int E, F f) {
 
 }  // namespace
 
-// Two blocks an SM at most while a block has no more than 2^13 tokens.
-int64_t balance_partials(const Shape& s) {
+// Two blocks an SM at most while a block has no more than 2^13 tokens.  (The
+// loss' tokens are in flight four at a time for each group of lanes.)
+static int64_t token_blocks(const Shape& s, int per_sm, int rounds) {
   const int64_t tokens = kThreads / (s.E <= 32 ? 8 : s.E <= 64 ? 16 : 32);
-  const int64_t want = (s.T + tokens - 1) / tokens, cap = 2 * (int64_t)sm_count();
+  const int64_t want = (s.T + rounds * tokens - 1) / (rounds * tokens), cap = per_sm * (int64_t)sm_count();
   const int64_t least = (s.T + 8191) / 8192;
   int64_t n = want < cap ? want : cap;
   if (n < least) n = least;
   return n < 1 ? 1 : n;
 }
+int64_t balance_partials(const Shape& s) { return token_blocks(s, 2, kAhead); }
+// The scores' gradient: five blocks of 256 threads fit an SM.
+int64_t dlogits_partials(const Shape& s) { return token_blocks(s, 5, 1); }
 
 bool router_gate_on_tensor_cores(const Shape& s) {
   return s.dtype == MOE_BF16 && !(s.flags & MOE_FLAG_SIMT_ROUTER);
@@ -433,7 +470,8 @@ cudaError_t launch_balance(const Shape& s, const float* logits, const int32_t* i
                          dim3(kThreads), 0, st, 1, logits, ids, mask, s.T, s.E, s.K, s.inv_tau, part_p, part_c, err);
   });
   if (e != cudaSuccess) return e;
-  return launch_kernel(balance_finish_kernel, dim3(1), dim3(1024), 0, st, 1, part_p, part_c, rows, s.E, s.K, o);
+  return launch_kernel(balance_finish_kernel, dim3(1), dim3(1024), 0, st, 1, part_p, part_c, rows, s.E, s.K,
+                       s.E <= 32 ? 32 : s.E <= 64 ? 64 : s.E <= 128 ? 128 : 256, o);
 }
 
 cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, void* dl, float* part_b, float* part_w,
@@ -447,7 +485,7 @@ cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, void
   const bool tc = router_gate_on_tensor_cores(s), products = b.dx || b.dWg;
   float* out = b.dlogits || tc || !products ? b.dlogits : (float*)dl;
   bf16* panels = tc && products ? (bf16*)dl : nullptr;
-  const int64_t rows = balance_partials(s);
+  const int64_t rows = dlogits_partials(s);
   e = by_experts(s.E, [&](auto lanes, auto vecs) {
     return launch_kernel(dlogits_kernel<decltype(lanes)::value, decltype(vecs)::value>, dim3((unsigned)rows),
                          dim3(kThreads), 0, st, 1, b, s.T, s.E, s.K, s.inv_tau, out, panels, gate_panel_cols(s.E),

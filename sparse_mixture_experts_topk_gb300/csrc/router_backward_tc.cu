@@ -325,14 +325,23 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     // ------------------------------------------------------------ masked rows of x
     if (dwg && P.mask) {
       Ring x(plan.nx);
-      for (Walk w(first, last, P.tiles); w.left > 0; w.next()) {
-        const int64_t t0 = (int64_t)w.tile * kTok;
-        uint32_t out[4];
+      // the mask's bytes of the next tile are on their way while this one's rows are zeroed
+      uint8_t on[4];
+      auto fetch = [&](int tile) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int64_t t = t0 + k * 32 + lane;
-          out[k] = __ballot_sync(0xffffffffu, t < P.T && !P.mask[t]);
+          const int64_t t = (int64_t)tile * kTok + k * 32 + lane;
+          on[k] = t < P.T ? P.mask[t] : 1;
         }
+      };
+      Walk w(first, last, P.tiles);
+      fetch(w.tile);
+      while (w.left > 0) {
+        uint32_t out[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[k] = __ballot_sync(0xffffffffu, !on[k]);
+        w.next();
+        if (w.left > 0) fetch(w.tile);
         if (!__all_sync(0xffffffffu, tc::mbar_wait(x_full(x.at), x.phase, &s_abort, kWaitNs))) {
           if (lane == 0) give_up(P.err, &s_abort);
           break;
@@ -457,24 +466,27 @@ gate_sums_kernel(const float* __restrict__ part, int tiles, int chunks, int ctas
   pdl_enter();
   const int c = blockIdx.x;
   if (c < chunks) {
-    const int64_t items = (int64_t)tiles * chunks, a = (int64_t)c * tiles, z = a + tiles;
-    int64_t i0 = a * ctas / items;   // the CTA that has item a, or one beside it
-    while (i0 > 0 && item_begin(i0, items, ctas) > a) --i0;
-    while (item_begin(i0 + 1, items, ctas) <= a) ++i0;
+    const int64_t items = (int64_t)tiles * chunks;
+    // the first CTA whose pairs end after pair a
+    auto first_after = [&](int64_t a) {
+      int64_t i = a * ctas / items;
+      while (i > 0 && item_begin(i, items, ctas) > a) --i;
+      while (item_begin(i + 1, items, ctas) <= a) ++i;
+      return (int)i;
+    };
+    const int n = Plan(E).packed ? 2 : 1;
+    const int i0 = first_after((int64_t)c * tiles), i1 = first_after((int64_t)c * tiles + tiles - 1);
     const int e = blockIdx.y * 8 + threadIdx.x / 32, h = c * kCols + threadIdx.x % 32 * 4;
     if (e >= E || h >= H) return;   // H is a multiple of 8
+    const float* p = part + ((int64_t)(i0 + c) * n * E + e) * kCols + threadIdx.x % 32 * 4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int64_t i = i0; i < ctas && item_begin(i, items, ctas) < z; ++i) {
-      const int n = Plan(E).packed ? 2 : 1;
-      for (int k = 0; k < n; ++k) {
-        const float4 v =
-            *reinterpret_cast<const float4*>(part + (((i + c) * n + k) * E + e) * kCols + threadIdx.x % 32 * 4);
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
-      }
+#pragma unroll 8
+    for (int k = (i1 - i0 + 1) * n; k > 0; --k, p += (int64_t)E * kCols) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
     }
     *reinterpret_cast<float4*>(dWg + (int64_t)e * H + h) = s;
   } else {
@@ -482,6 +494,7 @@ gate_sums_kernel(const float* __restrict__ part, int tiles, int chunks, int ctas
     const int e = blockIdx.y * 32 + threadIdx.x % 32, g = threadIdx.x / 32;
     float v = 0.f;
     if (e < E && blockIdx.y * 32 < E)
+#pragma unroll 8
       for (int r = g; r < rows_b; r += 8) v += part_b[(int64_t)r * E + e];
     s_b[g][threadIdx.x % 32] = v;
     __syncthreads();
