@@ -238,6 +238,7 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int count, int grad_dt
 // The load-balancing loss and the router's gradient.  blocks: partial sums of
 // the tokens' kernels; the products' scratch follows from the shape.
 int64_t balance_partials(const Shape& s);
+int64_t balance_rows(const Shape& s);   // of partial sums and of their bundles'
 int64_t dlogits_partials(const Shape& s);
 struct BalanceOut {
   float* psum;
@@ -245,7 +246,8 @@ struct BalanceOut {
   int32_t* tokens;
   float* loss;
 };
-// part_p: [balance_partials, E] floats, part_c: [balance_partials, E + 1] ints
+// part_p: [balance_rows, E] floats, part_c: [balance_rows, E + 1] ints; err: the
+// workspace's first 256 bytes
 cudaError_t launch_balance(const Shape& s, const float* logits, const int32_t* ids, const uint8_t* mask,
                            const BalanceOut& o, float* part_p, int32_t* part_c, int* err, cudaStream_t st);
 struct RouterBackward {
@@ -270,11 +272,12 @@ bool router_gate_on_tensor_cores(const Shape& s);
 size_t router_scratch_bytes(const Shape& s);
 int64_t router_weight_partials(const Shape& s);
 // The gate's products on the tensor cores, and the sum of part_b's rows_b rows
-// into dbias.  panels: [T, gate_panel_cols] bf16 as dlogits_kernel writes them.
+// into dbias.  panels: [T, gate_panel_cols] bf16 and alive as
+// dlogits_kernel writes them.
 int gate_panel_cols(int E);
 int64_t gate_part_floats(const Shape& s);
-cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* panels, float* part,
-                           const float* part_b, int rows_b, int* err, cudaStream_t st);
+cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* panels, const uint8_t* alive,
+                           float* part, const float* part_b, int rows_b, int* err, cudaStream_t st);
 cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, void* dl, float* part_b, float* part_w,
                                    int* err, cudaStream_t st);
 

@@ -23,7 +23,18 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;
+constexpr int kAhead = 2;      // tokens of a group in flight together
+constexpr int kBundles = 32;   // of partial rows
+constexpr int kCounters = 16;  // their counters' place behind the error word, in ints
+
+constexpr float kLog2E = 1.44269504088896341f;
+
+// 2^x, within 2^-22 relative; zero for -infinity and where it would be subnormal.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // Lanes for a token and experts for a lane, by the number of experts.
 template <int kLanes, int kVecs>
@@ -42,8 +53,8 @@ struct Group {
     for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
   }
-  // This lane's scores of a token times 1 / tau, -infinity past the last expert.
-  __device__ static void load(const float* __restrict__ row, int lane, int E, float inv_tau, bool live, float* l) {
+  // This lane's scores of a token, -infinity past the last expert.
+  __device__ static void load(const float* __restrict__ row, int lane, int E, bool live, float* l) {
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const int e = expert(lane, 4 * v);
@@ -57,12 +68,16 @@ struct Group {
 #pragma unroll
         for (int i = 0; i < 4; ++i) l[4 * v + i] = live && e + i < E ? row[e + i] : 0.f;
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) l[4 * v + i] = e + i < E ? l[4 * v + i] * inv_tau : -INFINITY;
     }
+    if (E == kLanes * kN) return;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (expert(lane, i) >= E) l[i] = -INFINITY;
   }
-  // Softmax in place over the group's scores.  A NaN among them makes all NaN.
-  __device__ static void softmax(float* l) {
+  // The group's exponentials of scores / tau, less the largest, in place;
+  // returns 1 / their sum.  scale: log2(e) / tau.  A NaN among the scores makes
+  // all of it NaN.
+  __device__ static float exponentials(float* l, float scale) {
     float top = l[0];
 #pragma unroll
     for (int i = 1; i < kN; ++i) top = fmaxf(top, l[i]);
@@ -70,12 +85,10 @@ struct Group {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      l[i] = expf(l[i] - top);
+      l[i] = exp2_fast((l[i] - top) * scale);
       s += l[i];
     }
-    const float inv = 1.f / sum(s);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) l[i] *= inv;
+    return __fdividef(1.f, sum(s));
   }
 };
 
@@ -94,11 +107,39 @@ __device__ __forceinline__ void block_sums(const float* acc, float* s, int lane,
   }
 }
 
+// a + b, and what its rounding lost added to `low` (exact: Knuth's two-sum).
+// The loss' sums are held as such pairs: GB300 does few fp64 operations a
+// cycle, and one block of them took 10 us for 256 experts.
+__device__ __forceinline__ float two_sum(float a, float b, float* low) {
+  const float s = a + b, t = s - a;
+  *low += (a - (s - t)) + (b - t);
+  return s;
+}
+
+// Whether this block is the last of n to arrive here; the counter is zero
+// before the first and after the last.  What the blocks wrote before is then
+// visible (to loads that bypass L1).
+__device__ __forceinline__ bool last_of(int* counter, int n) {
+  __shared__ int s_last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s_last = atomicAdd(counter, 1) == n - 1;
+    if (s_last) *counter = 0;
+  }
+  __syncthreads();
+  const bool last = s_last;
+  __syncthreads();
+  if (last) __threadfence();
+  return last;
+}
+
+// The whole loss in one launch.  counters: kBundles + 1 zeroed words.
 template <int kLanes, int kVecs>
 __global__ void __launch_bounds__(kThreads)
 balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
-               int64_t T, int E, int K, float inv_tau, float* __restrict__ part_p, int32_t* __restrict__ part_c,
-               int* err) {
+               int64_t T, int E, int K, float inv_tau, float* part_p, int32_t* part_c, int per, int* counters,
+               BalanceOut o, int* err) {
   using G = Group<kLanes, kVecs>;
   __shared__ float s_p[kThreads * 4 * kVecs];
   __shared__ int s_count[257];
@@ -119,14 +160,14 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids
       const int64_t t = t0 + u * stride + group;
       live[u] = t < T && (!mask || mask[t]);
       id[u] = t < T && lane < K ? ids[t * K + lane] : -1;
-      G::load(logits + t * E, lane, E, inv_tau, t < T, l[u]);
+      G::load(logits + t * E, lane, E, t < T, l[u]);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      G::softmax(l[u]);
+      const float inv = G::exponentials(l[u], inv_tau * kLog2E);
       if (live[u]) {
 #pragma unroll
-        for (int i = 0; i < G::kN; ++i) acc[i] += l[u][i];
+        for (int i = 0; i < G::kN; ++i) acc[i] = fmaf(l[u][i], inv, acc[i]);
         ++n;
         if (id[u] >= 0 && id[u] < E) atomicAdd(&s_count[id[u]], 1);
         else if (id[u] != -1) set_error(err, kDevBadIndex);
@@ -136,78 +177,57 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids
   if (lane == 0 && n) atomicAdd(&s_count[E], n);
   block_sums<G>(acc, s_p, lane, group, E, part_p + (int64_t)blockIdx.x * E);   // its barrier ends the counting too
   for (int i = threadIdx.x; i <= E; i += kThreads) part_c[(int64_t)blockIdx.x * (E + 1) + i] = s_count[i];
-}
-
-// a + b, and what its rounding lost added to `low` (exact: Knuth's two-sum).
-// The sums below are held as such pairs: GB300 does few fp64 operations a
-// cycle, and one block of them took 10 us for 256 experts.
-__device__ __forceinline__ float two_sum(float a, float b, float* low) {
-  const float s = a + b, t = s - a;
-  *low += (a - (s - t)) + (b - t);
-  return s;
-}
-
-// One block: the partial rows added up, 1024 / width threads to an expert
-// (width: E rounded up to 32, 64, 128 or 256), and the loss.
-__global__ void __launch_bounds__(1024)
-balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_c, int rows, int E, int K,
-                      int width, BalanceOut o) {
-  __shared__ float s_hi[1024], s_lo[1024];
-  __shared__ int s_c[1024];
-  __shared__ int s_n;
-  pdl_enter();
-  const int e = threadIdx.x % width, q = threadIdx.x / width, threads = 1024 / width;
-  float hi = 0.f, lo = 0.f;
-  int c = 0;
-  if (e < E) {
+  // The last block of a bundle of `per` to arrive adds up the bundle's rows,
+  // the last of those the bundles' rows: always in the rows' order.
+  const int bundle = blockIdx.x / per, bundles = (gridDim.x + per - 1) / per, row0 = bundle * per;
+  const int rows = min(per, (int)gridDim.x - row0);
+  float* sums = part_p + (int64_t)gridDim.x * E;              // [bundles, 2, E]: high and low
+  int32_t* counts = part_c + (int64_t)gridDim.x * (E + 1);    // [bundles, E + 1]
+  if (!last_of(counters + 1 + bundle, rows)) return;
+  for (int e = threadIdx.x; e <= E; e += kThreads) {
+    int c = 0;
+    for (int r = 0; r < rows; ++r) c += __ldcg(part_c + (int64_t)(row0 + r) * (E + 1) + e);
+    counts[(int64_t)bundle * (E + 1) + e] = c;
+    if (e == E) break;
+    float hi = 0.f, lo = 0.f;
 #pragma unroll 8
-    for (int r = q; r < rows; r += threads) {
-      hi = two_sum(hi, part_p[(int64_t)r * E + e], &lo);
-      c += part_c[(int64_t)r * (E + 1) + e];
+    for (int r = 0; r < rows; ++r) hi = two_sum(hi, __ldcg(part_p + (int64_t)(row0 + r) * E + e), &lo);
+    sums[(int64_t)bundle * 2 * E + e] = hi;
+    sums[((int64_t)bundle * 2 + 1) * E + e] = lo;
+  }
+  if (!last_of(counters, bundles)) return;
+  int tokens = 0;
+  for (int r = 0; r < bundles; ++r) tokens += __ldcg(counts + (int64_t)r * (E + 1) + E);
+  const int e = threadIdx.x;   // E <= kThreads
+  float term = 0.f;
+  if (e < E) {
+    float hi = 0.f, lo = 0.f;
+    int c = 0;
+#pragma unroll 8
+    for (int r = 0; r < bundles; ++r) {
+      hi = two_sum(hi, __ldcg(sums + (int64_t)r * 2 * E + e), &lo);
+      lo += __ldcg(sums + ((int64_t)r * 2 + 1) * E + e);
+      c += __ldcg(counts + (int64_t)r * (E + 1) + e);
     }
-  }
-  s_hi[threadIdx.x] = hi;
-  s_lo[threadIdx.x] = lo;
-  s_c[threadIdx.x] = c;
-  if (threadIdx.x < 32) {
-    int n = 0;
-    for (int r = threadIdx.x; r < rows; r += 32) n += part_c[(int64_t)r * (E + 1) + E];
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) n += __shfl_xor_sync(0xffffffffu, n, w);
-    if (threadIdx.x == 0) s_n = n;
-  }
-  for (int half = threads / 2; half > 0; half /= 2) {
-    __syncthreads();
-    if (q < half) {
-      const int other = threadIdx.x + half * width;
-      lo += s_lo[other];
-      hi = two_sum(hi, s_hi[other], &lo);
-      c += s_c[other];
-      s_hi[threadIdx.x] = hi;
-      s_lo[threadIdx.x] = lo;
-      s_c[threadIdx.x] = c;
-    }
-  }
-  __syncthreads();
-  const float sum = hi + lo;
-  if (q == 0 && e < E) {
-    if (o.psum) o.psum[e] = sum;
+    if (o.psum) o.psum[e] = hi + lo;
     if (o.count) o.count[e] = c;
+    // f_e P_e, each a share, in fp32
+    const float n = (float)tokens;
+    if (tokens) term = (float)c / (n * (float)K) * ((hi + lo) / n);
   }
-  const float n = (float)s_n;
-  // f_e P_e, each a share, in fp32
-  if (q == 0) s_hi[threadIdx.x] = e < E && s_n ? (float)c / (n * (float)K) * (sum / n) : 0.f;
+  s_p[e] = term;
   __syncthreads();
   if (threadIdx.x < 32) {
     float v = 0.f, low = 0.f;
-    for (int i = threadIdx.x; i < width; i += 32) v = two_sum(v, s_hi[i], &low);
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) v = two_sum(v, s_p[i * 32 + threadIdx.x], &low);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) {
       low += __shfl_xor_sync(0xffffffffu, low, w);
       v = two_sum(v, __shfl_xor_sync(0xffffffffu, v, w), &low);
     }
     if (threadIdx.x == 0) {
-      if (o.tokens) *o.tokens = s_n;
+      if (o.tokens) *o.tokens = tokens;
       if (o.loss) *o.loss = (float)E * (v + low);
     }
   }
@@ -233,11 +253,13 @@ __device__ __forceinline__ void split4(const float* v, uint2* parts) {
 // as [T, E] fp32 (dl) and as bf16 parts (panels), where these are not null.
 // Panels are 64 columns wide and zero past the last expert: the high parts of
 // all experts, the middle ones, the low ones; up to 32 experts: [high | middle],
-// [low | 0].
+// [low | 0].  alive (or null): for the tokens of each step of a block, whether
+// one counts, up to a multiple of 128 tokens.
 template <int kLanes, int kVecs>
 __global__ void __launch_bounds__(kThreads)
 dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* __restrict__ dl,
-               bf16* __restrict__ panels, int panel_cols, float* __restrict__ part_b, int* err) {
+               bf16* __restrict__ panels, int panel_cols, uint8_t* __restrict__ alive,
+               float* __restrict__ part_b, int* err) {
   using G = Group<kLanes, kVecs>;
   __shared__ float s_b[kThreads * 4 * kVecs];
   pdl_enter();
@@ -251,9 +273,14 @@ dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* 
       c[i] = e < E ? f * (float)b.count[e] : 0.f;
     }
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * G::kTokens; t0 < T; t0 += (int64_t)gridDim.x * G::kTokens) {
+  const int64_t end = alive ? (T + 127) / 128 * 128 : T;
+  for (int64_t t0 = (int64_t)blockIdx.x * G::kTokens; t0 < end; t0 += (int64_t)gridDim.x * G::kTokens) {
     const int64_t t = t0 + group;
     const bool live = t < T && (!b.mask || b.mask[t]);
+    if (alive) {
+      const int any = __syncthreads_or(live);
+      if (threadIdx.x == 0) alive[t0 / G::kTokens] = any != 0;
+    }
     // lane j has choice j; what is loaded for a token that does not count is not used
     const bool mine = b.dw && t < T && lane < K;
     int id = mine ? b.ids[t * K + lane] : -1;
@@ -261,24 +288,24 @@ dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* 
     float d[G::kN] = {};
     if (b.dloss) {
       float p[G::kN], dot = 0.f;
-      G::load(b.logits + t * E, lane, E, inv_tau, t < T, p);
-      G::softmax(p);
+      G::load(b.logits + t * E, lane, E, t < T, p);
+      const float inv = G::exponentials(p, inv_tau * kLog2E);
 #pragma unroll
       for (int i = 0; i < G::kN; ++i) dot = fmaf(p[i], c[i], dot);
-      dot = G::sum(dot);
+      dot = G::sum(dot) * inv;
 #pragma unroll
-      for (int i = 0; i < G::kN; ++i) d[i] = p[i] * (c[i] - dot);
+      for (int i = 0; i < G::kN; ++i) d[i] = p[i] * inv * (c[i] - dot);
     }
     if (b.dw) {
       float z = -INFINITY;
       if (live && id >= 0 && id < E) {
-        z = b.logits[t * E + id] * inv_tau;
+        z = b.logits[t * E + id];
       } else {
         if (live && id != -1) set_error(err, kDevBadIndex);
         id = -1;
         g = 0.f;
       }
-      const float top = G::max(z), x = id >= 0 ? expf(z - top) : 0.f, s = G::sum(x);
+      const float top = G::max(z), x = id >= 0 ? exp2_fast((z - top) * (inv_tau * kLog2E)) : 0.f, s = G::sum(x);
       const float w = s != 0.f ? x / s : 0.f, dot = G::sum(w * g), v = w * (g - dot);
       for (int j = 0; j < K; ++j) {
         const int e = __shfl_sync(0xffffffffu, id, j, kLanes);
@@ -438,8 +465,8 @@ cudaError_t by_experts(int E, F f) {
 
 }  // namespace
 
-// Two blocks an SM at most while a block has no more than 2^13 tokens.  (The
-// loss' tokens are in flight four at a time for each group of lanes.)
+// Blocks that walk over the tokens: `per_sm` an SM at most while a block has no
+// more than 2^13 tokens, and no more than have `rounds` tokens for each group.
 static int64_t token_blocks(const Shape& s, int per_sm, int rounds) {
   const int64_t tokens = kThreads / (s.E <= 32 ? 8 : s.E <= 64 ? 16 : 32);
   const int64_t want = (s.T + rounds * tokens - 1) / (rounds * tokens), cap = per_sm * (int64_t)sm_count();
@@ -448,7 +475,8 @@ static int64_t token_blocks(const Shape& s, int per_sm, int rounds) {
   if (n < least) n = least;
   return n < 1 ? 1 : n;
 }
-int64_t balance_partials(const Shape& s) { return token_blocks(s, 2, kAhead); }
+int64_t balance_partials(const Shape& s) { return token_blocks(s, 4, kAhead); }
+int64_t balance_rows(const Shape& s) { return balance_partials(s) + 2 * kBundles; }
 // The scores' gradient: five blocks of 256 threads fit an SM.
 int64_t dlogits_partials(const Shape& s) { return token_blocks(s, 5, 1); }
 
@@ -456,7 +484,8 @@ bool router_gate_on_tensor_cores(const Shape& s) {
   return s.dtype == MOE_BF16 && !(s.flags & MOE_FLAG_SIMT_ROUTER);
 }
 size_t router_scratch_bytes(const Shape& s) {
-  return (size_t)s.T * (router_gate_on_tensor_cores(s) ? (size_t)gate_panel_cols(s.E) * 2 : (size_t)s.E * 4);
+  if (!router_gate_on_tensor_cores(s)) return (size_t)s.T * s.E * 4;
+  return (size_t)s.T * gate_panel_cols(s.E) * 2 + (size_t)(s.T + 127) / 128 * 16;   // and a tile's flags
 }
 int64_t router_weight_partials(const Shape& s) {
   return router_gate_on_tensor_cores(s) ? gate_part_floats(s) : (int64_t)simt_splits(s) * s.E * s.H;
@@ -464,14 +493,12 @@ int64_t router_weight_partials(const Shape& s) {
 
 cudaError_t launch_balance(const Shape& s, const float* logits, const int32_t* ids, const uint8_t* mask,
                            const BalanceOut& o, float* part_p, int32_t* part_c, int* err, cudaStream_t st) {
-  const int rows = (int)balance_partials(s);
-  cudaError_t e = by_experts(s.E, [&](auto lanes, auto vecs) {
+  const int rows = (int)balance_partials(s), per = (rows + kBundles - 1) / kBundles;
+  return by_experts(s.E, [&](auto lanes, auto vecs) {
     return launch_kernel(balance_kernel<decltype(lanes)::value, decltype(vecs)::value>, dim3((unsigned)rows),
-                         dim3(kThreads), 0, st, 1, logits, ids, mask, s.T, s.E, s.K, s.inv_tau, part_p, part_c, err);
+                         dim3(kThreads), 0, st, 1, logits, ids, mask, s.T, s.E, s.K, s.inv_tau, part_p, part_c, per,
+                         err + kCounters, o, err);
   });
-  if (e != cudaSuccess) return e;
-  return launch_kernel(balance_finish_kernel, dim3(1), dim3(1024), 0, st, 1, part_p, part_c, rows, s.E, s.K,
-                       s.E <= 32 ? 32 : s.E <= 64 ? 64 : s.E <= 128 ? 128 : 256, o);
 }
 
 cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, void* dl, float* part_b, float* part_w,
@@ -485,14 +512,15 @@ cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, void
   const bool tc = router_gate_on_tensor_cores(s), products = b.dx || b.dWg;
   float* out = b.dlogits || tc || !products ? b.dlogits : (float*)dl;
   bf16* panels = tc && products ? (bf16*)dl : nullptr;
+  uint8_t* alive = panels && b.mask ? (uint8_t*)(panels + s.T * gate_panel_cols(s.E)) : nullptr;
   const int64_t rows = dlogits_partials(s);
   e = by_experts(s.E, [&](auto lanes, auto vecs) {
     return launch_kernel(dlogits_kernel<decltype(lanes)::value, decltype(vecs)::value>, dim3((unsigned)rows),
                          dim3(kThreads), 0, st, 1, b, s.T, s.E, s.K, s.inv_tau, out, panels, gate_panel_cols(s.E),
-                         part_b, err);
+                         alive, part_b, err);
   });
   if (e != cudaSuccess) return e;
-  if (tc) return launch_gate_tc(s, b, panels, part_w, part_b, (int)rows, err, st);
+  if (tc) return launch_gate_tc(s, b, panels, alive, part_w, part_b, (int)rows, err, st);
   if (b.dbias)
     e = launch_kernel(row_sums_kernel, dim3(1), dim3(256), 0, st, 1, part_b, rows, (int64_t)s.E, b.dbias);
   if (e != cudaSuccess || !(b.dx || b.dWg)) return e;

@@ -66,6 +66,7 @@ struct Plan {
 struct Params {
   CUtensorMap x, wg, panel, dx;   // boxes of 128, 32, 128 and 32 rows
   const uint8_t* mask;
+  const uint8_t* alive;   // with a mask: whether tokens of a tile count
   int64_t T;
   int tiles, chunks;
   int E, H;
@@ -78,17 +79,38 @@ struct Params {
 __host__ __device__ inline int64_t item_begin(int64_t i, int64_t n, int64_t g) { return i * n / g; }
 
 // A CTA's (chunk, tile) pairs in order; 64-bit divisions once, not at each.
+// kFlags: bytes for a tile that say whether a token of it counts (0: all do).
+// Those of the next tile are on their way while one is worked on.
+template <int kFlags>
 struct Walk {
   int64_t left;
   int chunk, tile, tiles;
-  __device__ Walk(int64_t first, int64_t last, int n)
-      : left(last - first), chunk((int)(first / n)), tile((int)(first % n)), tiles(n) {}
+  const uint8_t* alive;
+  bool live, ahead;
+  __device__ Walk(int64_t first, int64_t last, int n, const uint8_t* flags)
+      : left(last - first), chunk((int)(first / n)), tile((int)(first % n)), tiles(n), alive(flags) {
+    live = read(tile);
+    ahead = read(tile + 1 == tiles ? 0 : tile + 1);
+  }
+  __device__ bool read(int t) const {
+    if (kFlags == 0 || !alive) return true;
+    const uint8_t* p = alive + (int64_t)t * kFlags;
+    if (kFlags == 4) return __ldcg(reinterpret_cast<const unsigned*>(p)) != 0;
+    if (kFlags == 8) {
+      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
+      return (v.x | v.y) != 0;
+    }
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
+    return (v.x | v.y | v.z | v.w) != 0;
+  }
   __device__ void next() {
     --left;
     if (++tile == tiles) {
       tile = 0;
       ++chunk;
     }
+    live = ahead;
+    if (left > 1) ahead = read(tile + 1 == tiles ? 0 : tile + 1);
   }
   // whether the CTA leaves the chunk, and with it the tokens of a run of tiles, after this pair
   __device__ bool leaves() const { return left == 1 || tile + 1 == tiles; }
@@ -178,6 +200,9 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   const int64_t first = item_begin(blockIdx.x, items, gridDim.x), last = item_begin(blockIdx.x + 1, items, gridDim.x);
   const bool dwg = P.part != nullptr;
   constexpr int kRun = kGroups <= 2 ? 1 : 4;   // tiles that D1 sums
+  // a tile none of whose tokens counts is not loaded; sums of several tiles take each
+  constexpr int kFlags = kRun > 1 ? 0 : kGroups == 2 ? 16 : kPacked ? 4 : 8;
+  const uint8_t* alive = kFlags ? P.alive : nullptr;
   // the producers' copies: stages filled and the parity of each one's latest
   uint32_t filled = 0, fill_par = 0, w_phase = 0;
   bool w_loaded = false;
@@ -188,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
       Ring r(plan.nx);
       bool ok = true;
       int chunk = -1;
-      for (Walk w(first, last, P.tiles); w.left > 0 && ok; w.next()) {
+      for (Walk<kFlags> w(first, last, P.tiles, alive); w.left > 0 && ok; w.next()) {
         const int c = w.chunk, t0 = w.tile * kTok, h0 = c * kCols;
         if (P.dx_on && c != chunk) {
           ok = tc::mbar_wait(w_empty, w_phase ^ 1u, &s_abort, kWaitNs);
@@ -202,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
           w_loaded = true;
         }
         chunk = c;
-        if (!dwg) continue;
+        if (!dwg || !w.live) continue;
         ok = tc::mbar_wait(x_empty(r.at), r.phase ^ 1u, &s_abort, kWaitNs);
         if (!ok) break;
         tc::mbar_arrive_expect_tx(x_full(r.at), kXBytes);
@@ -219,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     if (tc::elect_one()) {
       Ring r(plan.np);
       bool ok = true;
-      for (Walk w(first, last, P.tiles); w.left > 0 && ok; w.next()) {
+      for (Walk<kFlags> w(first, last, P.tiles, alive); w.left > 0 && ok; w.next()) {
         const int t0 = w.tile * kTok;
-        for (int p = 0; p < plan.panels; ++p) {
+        for (int p = 0; p < plan.panels && w.live; ++p) {
           ok = tc::mbar_wait(p_empty(r.at), r.phase ^ 1u, &s_abort, kWaitNs);
           if (!ok) break;
           tc::mbar_arrive_expect_tx(p_full(r.at), kHalf);
@@ -254,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
       bool ok = true, begins = true;   // begins: D1 with this pair
       bool x_ready = false, p_ready = false, d1_ready = false, d2_ready = false;
 #pragma unroll 1
-      for (Walk w(first, last, P.tiles); w.left > 0 && ok; w.next()) {
+      for (Walk<kFlags> w(first, last, P.tiles, alive); w.left > 0 && ok; w.next()) {
         const bool fresh = begins;
         begins = w.ends(kRun);
         if (dx_on && w.chunk != chunk) {
@@ -262,6 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
           w_phase ^= 1u;
         }
         chunk = w.chunk;
+        if (!w.live) {
+          if (dx_on && w.leaves()) tc::tc_commit(w_empty);
+          continue;
+        }
         if (dwg) {
           if (ok && fresh && !d1_ready) ok = tc::mbar_wait(d1_empty(d1.at), d1.phase ^ 1u, &s_abort, kWaitNs);
           if (ok && !x_ready) ok = tc::mbar_wait(x_bar(x.at), x.phase, &s_abort, kWaitNs);
@@ -334,14 +363,16 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
           on[k] = t < P.T ? P.mask[t] : 1;
         }
       };
-      Walk w(first, last, P.tiles);
+      Walk<kFlags> w(first, last, P.tiles, alive);
       fetch(w.tile);
       while (w.left > 0) {
         uint32_t out[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) out[k] = __ballot_sync(0xffffffffu, !on[k]);
+        const bool live = w.live;
         w.next();
         if (w.left > 0) fetch(w.tile);
+        if (!live) continue;
         if (!__all_sync(0xffffffffu, tc::mbar_wait(x_full(x.at), x.phase, &s_abort, kWaitNs))) {
           if (lane == 0) give_up(P.err, &s_abort);
           break;
@@ -377,23 +408,26 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     Ring d1(plan.bufs), d2(2);
     float sum[kGroups * 32] = {};   // of column half * 32 + j of each group: this thread's column of x
     bool ok = true;
-    for (Walk w(first, last, P.tiles); w.left > 0 && ok; w.next()) {
+    for (Walk<kFlags> w(first, last, P.tiles, alive); w.left > 0 && ok; w.next()) {
       const int c = w.chunk;
       if (P.dx_on) {
         const int64_t t0 = (int64_t)w.tile * kTok + q * 32;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(d2_full(d2.at), d2.phase, &s_abort, kWaitNs));
-        if (!ok) break;
-        tc::tc_fence_after();
+        uint32_t r[2][32] = {};
+        if (w.live) {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(d2_full(d2.at), d2.phase, &s_abort, kWaitNs));
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t at = lanes + kD2 + d2.at * kCols + half * 64;
+          tc::tmem_ld_32x32b_x32(at, r[0]);
+          tc::tmem_ld_32x32b_x32(at + 32, r[1]);
+          tc::tmem_wait_ld();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(d2_empty(d2.at));   // tensor memory has been read
+          d2.next();
+        }
         if (lane == 0) tc::bulk_wait_read();   // the last tile's store has read the buffer
         __syncwarp();
-        const uint32_t at = lanes + kD2 + d2.at * kCols + half * 64;
-        uint32_t r[2][32];
-        tc::tmem_ld_32x32b_x32(at, r[0]);
-        tc::tmem_ld_32x32b_x32(at + 32, r[1]);
-        tc::tmem_wait_ld();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(d2_empty(d2.at));   // tensor memory has been read
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float v[32];
@@ -407,9 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
         __syncwarp();
         if (lane == 0 && t0 < P.T && c * kCols + half * 64 < P.H)
           tc::tma_store_2d(&P.dx, buf, c * kCols + half * 64, (int)t0);
-        d2.next();
       }
-      if (dwg && w.ends(kRun)) {
+      if (dwg && w.live && w.ends(kRun)) {
         ok = __all_sync(0xffffffffu, tc::mbar_wait(d1_full(d1.at), d1.phase, &s_abort, kWaitNs));
         if (!ok) break;
         tc::tc_fence_after();
@@ -513,7 +546,7 @@ int64_t gate_part_floats(const Shape& s) {
 }
 int gate_panel_cols(int E) { return Plan(E).panels * 64; }
 
-cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* panels, float* part,
+cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* panels, const uint8_t* alive, float* part,
                            const float* part_b, int rows_b, int* err, cudaStream_t st) {
   const Plan plan(s.E);
   const int64_t tiles = (s.T + kTok - 1) / kTok, chunks = (s.H + kCols - 1) / kCols;
@@ -528,6 +561,7 @@ cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* 
         !tma_map_bf16(&P.panel, panels, T, (uint64_t)plan.panels * 64, kTok))
       return cudaErrorNotSupported;
     P.mask = b.mask;
+    P.alive = b.mask ? alive : nullptr;
     P.T = s.T;
     P.tiles = (int)tiles;
     P.chunks = (int)chunks;
