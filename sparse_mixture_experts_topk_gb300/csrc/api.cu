@@ -910,7 +910,7 @@ RouterLayout router_layout(const moe_desc& d) {
     off += (bytes + 255) / 256 * 256;
     return o;
   };
-  const size_t rows = (size_t)balance_rows(s), rows_b = (size_t)dlogits_partials(s);
+  const size_t rows = (size_t)balance_partials(s), rows_b = (size_t)dlogits_partials(s);
   L.err = take(256);
   L.dl = take(router_scratch_bytes(s));
   L.part = take((rows > rows_b ? rows : rows_b) * s.E * 4);

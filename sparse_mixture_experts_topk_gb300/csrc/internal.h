@@ -238,7 +238,6 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int count, int grad_dt
 // The load-balancing loss and the router's gradient.  blocks: partial sums of
 // the tokens' kernels; the products' scratch follows from the shape.
 int64_t balance_partials(const Shape& s);
-int64_t balance_rows(const Shape& s);   // of partial sums and of their bundles'
 int64_t dlogits_partials(const Shape& s);
 struct BalanceOut {
   float* psum;
@@ -246,8 +245,7 @@ struct BalanceOut {
   int32_t* tokens;
   float* loss;
 };
-// part_p: [balance_rows, E] floats, part_c: [balance_rows, E + 1] ints; err: the
-// workspace's first 256 bytes
+// part_p: [balance_partials, E] floats, part_c: [balance_partials, E + 1] ints
 cudaError_t launch_balance(const Shape& s, const float* logits, const int32_t* ids, const uint8_t* mask,
                            const BalanceOut& o, float* part_p, int32_t* part_c, int* err, cudaStream_t st);
 struct RouterBackward {
