@@ -72,9 +72,10 @@ bool tma_map_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols,
 bool tma_map_bf16_3d(CUtensorMap* m, const void* ptr, uint64_t d2, uint64_t rows, uint64_t cols, uint32_t box_rows);
 
 // The same for 16-bit elements whose rows are `pitch` and matrices `plane`
-// elements apart (multiples of 8).
+// elements apart (multiples of 8); boxes of other than 64 columns are not
+// swizzled.
 bool tma_map_16bit_3d(CUtensorMap* m, const void* ptr, uint64_t d2, uint64_t rows, uint64_t cols, uint64_t pitch,
-                      uint64_t plane, uint32_t box_rows);
+                      uint64_t plane, uint32_t box_rows, uint32_t box_cols = 64);
 
 // ---------------------------------------------------------------- router
 // Upper bound of the rows of per-block probability partial sums the router

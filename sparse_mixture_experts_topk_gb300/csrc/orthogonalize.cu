@@ -13,13 +13,20 @@
 // instead, the result is 1.1 % off (in the 2-norm, for a gradient of four
 // strong directions over noise), with fp16 0.13 %.
 //
-// The products run on SM pairs (tcgen05 .cta_group::2, tiles of 256 x 256, fp32
-// accumulators in TMEM, operands staged by TMA), all matrices of one size
-// together.  A and the short products read both operands along their rows; X
-// as the second operand of B X is read as it lies ("MN-major").
+// All products of a call are one launch: tiles go round the CTAs by number,
+// step after step, and a tile starts once every tile of its matrix' step before
+// is written (a counter for each step and matrix; one CTA an SM, all resident,
+// and no tile waits for a later one).  Launched one by one, the steps of a few
+// small matrices took twice as long, and those of many large ones lost their
+// tails.
+//
+// Tiles are 256 x 256 on SM pairs (tcgen05 .cta_group::2), or 128 x 128 on
+// single SMs where those would leave SMs idle; fp32 accumulators in TMEM,
+// operands staged by TMA.  A and the short products read both operands along
+// their rows; X as the second operand of B X is read as it lies ("MN-major").
 //
 // Roles per CTA: warps 0 and 10 TMA producers, one for each operand, warp 1
-// MMA issuer (leader CTA of the pair), warps 2-9 epilogue.  Every wait is
+// MMA issuer (leader CTA of a pair), warps 2-9 epilogue.  Every wait is
 // bounded: on expiry the kernel records a timeout in the workspace's error
 // word, drains what it has in flight, frees its tensor memory and returns.
 #include <cuda_fp16.h>
@@ -38,43 +45,103 @@ constexpr float kHeld = 4096.f;                              // factor of every 
 
 // ---------------------------------------------------------------- products
 
-constexpr int kBM = 128;                  // operand rows (or columns) per CTA: the pair covers 256
-constexpr int kTile = 2 * kBM;
+constexpr int kBM = 128;                  // operand rows (or columns) per CTA
 constexpr int kBK = 64;                   // reduction elements per stage
 constexpr int kGroup = 16;                // reduction elements per MMA
 constexpr int kOperand = kBM * kBK * 2;   // bytes of one operand in a stage
 constexpr int kHalf = kOperand / 2;       // an MN-major operand is two boxes of 64 columns x 64 rows
-constexpr int kStages = 7;
-constexpr int kTmemCols = 512;            // two accumulators of 256 columns
+constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;              // per CTA: two for each quarter of the TMEM lanes
 constexpr int kThreads = 64 + 32 * kEpiWarps + 32, kSecondProducer = 2 + kEpiWarps;
-constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kOperand;
-// The limit of a wait, and what the epilogue's wait for a tile has on top for each stage of its reduction.
+constexpr int kStoreBytes = 32 * 128;     // an epilogue warp's 32 rows of 64 columns on their way to TMA, or their transpose
+constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kOperand + kEpiWarps * kStoreBytes;
+// The limit of a wait, and what it has on top for each stage of the tiles that a CTA has of a step: those may
+// have to be written first.
 constexpr uint64_t kWaitNs = 2000000000ull, kStageNs = 2000;
 
 // MN-major operand of 128 x 64: two boxes (64 columns of 128 bytes, 64 rows, 128-byte swizzle) one after the other.
 __device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr) {
   return tc::sdesc_k128(saddr) | ((uint64_t)(kHalf >> 4) << 16);
 }
-constexpr uint32_t kMajorB = 1u << 16;    // instruction descriptor: B is MN-major
+constexpr uint32_t kMajorB = 1u << 16;       // instruction descriptor: B is MN-major
 constexpr int kStepK = 32, kStepMN = 2048;   // bytes from one group of 16 to the next
 // Instruction descriptor of kind::f16: D fp32, A and B fp16 (formats 0), K-major.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// out = alpha A B^T (kMN: A B) + beta add + diag I, for `batch` matrices.
-struct Product {
-  CUtensorMap a, b;
-  __half* out;
-  const __half* add;     // as out, or null
-  int rows, cols, k;     // of out, and the reduction
-  int64_t pitch, plane;  // of out, in elements
-  int batch;
-  bool symmetric;        // out is: tiles on and above the diagonal
+// The buffers: X and its successor [s, L], three symmetric matrices [s, s].
+enum Buffer : int8_t { kX = 0, kY, kG, kP, kQ, kBuffers, kNone = -1 };
+
+// out = alpha a b^T + beta add + diag I, or, where b is X (read as it lies), alpha a b.
+struct Step {
+  Buffer a, b, out, add;
+  bool gram;         // a = b = X: the reduction is over L
   float alpha, beta, diag;
+  __host__ __device__ bool wide() const { return out <= kY; }   // else out is symmetric: tiles from the diagonal on
+  __host__ __device__ bool mn() const { return out <= kY; }
+};
+constexpr int kMaxSteps = 7 * MOE_ORTHOGONALIZE_MAX_ITERATIONS / 2;
+
+struct Chain {
+  CUtensorMap along[kBuffers];   // boxes of 128 rows of 64 elements
+  CUtensorMap across[2];         // X and Y: 64 rows of 64 elements
+  CUtensorMap store[kBuffers];   // 32 rows of 64 elements
+  CUtensorMap mirror[kBuffers];  // the symmetric ones: 64 rows of 32 elements, not swizzled
+  __half* buf[kBuffers];
+  int s, L, batch, steps;
+  int64_t pitch, plane, square, square_plane;   // elements of a row and of a matrix
+  Step step[kMaxSteps];
+  int* written;                  // [steps, batch] zeros: warps that have written their share of a tile
+  uint64_t limit;
   const int32_t* skip;
   int* err;
+};
+
+// The tiles of a chain in the order in which they are dealt out.
+template <int kTile>
+struct Tiles {
+  const Chain& C;
+  int mt, nt;
+  int p, per;          // the step at hand, and its tiles of a matrix
+  int64_t base;        // the first of its tiles
+  int matrix, m0, n0;
+  __device__ explicit Tiles(const Chain& c)
+      : C(c), mt((c.s + kTile - 1) / kTile), nt((c.L + kTile - 1) / kTile), p(0), base(0) {
+    per = tiles(0);
+  }
+  __device__ int tiles(int step) const { return C.step[step].wide() ? mt * nt : mt * (mt + 1) / 2; }
+  // Tile t, not before the last one asked for; false behind the last.
+  __device__ bool seek(int64_t t) {
+    while (t >= base + (int64_t)per * C.batch) {
+      base += (int64_t)per * C.batch;
+      if (++p == C.steps) return false;
+      per = tiles(p);
+    }
+    const uint32_t local = (uint32_t)(t - base);   // below 2^31: see Sizes::most
+    matrix = (int)(local / (uint32_t)per);
+    int i = 0, j = (int)(local % (uint32_t)per);
+    if (C.step[p].wide()) {
+      i = j % mt;
+      j /= mt;
+    } else {
+      while (j >= mt - i) {   // row i has mt - i tiles
+        j -= mt - i;
+        ++i;
+      }
+      j += i;
+    }
+    m0 = i * kTile;
+    n0 = j * kTile;
+    return true;
+  }
+  __device__ int k() const { return C.step[p].gram ? C.L : C.s; }
+  __device__ int cols() const { return C.step[p].wide() ? C.L : C.s; }
+  // Columns of an MMA: those that the tile has, to 16; to whole groups of 64 for each CTA where b is read across
+  __device__ int mma_n() const {
+    const int to = !C.step[p].mn() ? 16 : kTile / 2;
+    return min(kTile, (cols() - n0 + to - 1) / to * to);
+  }
 };
 
 __device__ __forceinline__ void advance(int& stage, uint32_t& phase) {
@@ -89,17 +156,33 @@ __device__ __forceinline__ void give_up(int* err, volatile int* abort) {
   *abort = 1;
 }
 
-struct Tile {
-  int matrix, m0, n0;
-};
+// Wait (bounded) until the counter reaches `need`; what was written before is
+// then visible to this thread's loads and to the tensor copies it issues.
+__device__ __forceinline__ bool wait_written(const int* counter, int need, volatile int* abort, uint64_t limit) {
+  const uint64_t t0 = tc::globaltimer();
+  while (true) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+    if (v >= need) {
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      return true;
+    }
+    if (*abort || tc::globaltimer() - t0 > limit) return false;
+  }
+}
 
-template <bool kMN>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product P) {
+// kPair: tiles of 256 x 256 on the two CTAs of a cluster, else of 128 x 128.
+template <bool kPair>
+__global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constant__ Chain C) {
+  constexpr int kTile = kPair ? 256 : 128, kCtas = kPair ? 2 : 1;
+  constexpr int kChunks = kTile / 128;   // of 64 columns, for each of a lane quarter's two epilogue warps
+  constexpr uint32_t kTmemCols = 2 * kTile;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u, sB = sA + kStages * kOperand;
+  const uint32_t sOut = sB + kStages * kOperand;
   const uint32_t bars = tc::smem_u32(s_bar);
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kStages + s); };
@@ -107,10 +190,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   auto tempty = [&](int a) { return bars + 8 * (2 * kStages + 2 + a); };
   const uint32_t done = bars + 8 * (2 * kStages + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)tc::cluster_ctarank();
+  const int rank = kPair ? (int)tc::cluster_ctarank() : 0;
+  auto commit = [&](uint32_t bar) {
+    if (kPair) tc::tc_commit_pair_mc(bar, 0x3);
+    else tc::tc_commit(bar);
+  };
 
   pdl_enter();
-  if (P.skip && *P.skip) return;   // every thread of both CTAs
+  if (C.skip && *C.skip) return;   // every thread of both CTAs
   if (warp == 0) {
     if (lane == 0) {
       for (int s = 0; s < kStages; ++s) {
@@ -119,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       }
       for (int a = 0; a < 2; ++a) {
         tc::mbar_init(tfull(a), 1);
-        tc::mbar_init(tempty(a), 2 * kEpiWarps);   // one arrival for each epilogue warp of the pair
+        tc::mbar_init(tempty(a), kCtas * kEpiWarps);   // one arrival for each epilogue warp
       }
       tc::mbar_init(done, 1);
       s_abort = 0;
@@ -127,40 +214,24 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       tc::fence_proxy_async_smem();
     }
   } else if (warp == 1) {
-    tc::tmem_alloc_pair(tc::smem_u32(&s_tmem), kTmemCols);
-    tc::tmem_relinquish_pair();
+    if (kPair) {
+      tc::tmem_alloc_pair(tc::smem_u32(&s_tmem), kTmemCols);
+      tc::tmem_relinquish_pair();
+    } else {
+      tc::tmem_alloc(tc::smem_u32(&s_tmem), kTmemCols);
+      tc::tmem_relinquish();
+    }
   }
   tc::tc_fence_before();
   __syncthreads();
-  tc::cluster_sync();
+  if (kPair) tc::cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
-
-  const int mt = (P.rows + kTile - 1) / kTile, nt = (P.cols + kTile - 1) / kTile;
-  const int per = P.symmetric ? mt * (mt + 1) / 2 : mt * nt;
-  const int64_t total = (int64_t)per * P.batch;
-  const int nk = (P.k + kBK - 1) / kBK;
-  const int first = blockIdx.x / 2, step = gridDim.x / 2;
-  // Columns of an MMA: those that the tile has, to 16, or to 128 where each CTA reads its half along the rows.
-  auto mma_n = [&](const Tile& d) {
-    constexpr int to = kMN ? 128 : 16;
-    return min(kTile, (P.cols - d.n0 + to - 1) / to * to);
-  };
-  auto decode = [&](int64_t t) {
-    Tile d;
-    d.matrix = (int)(t / per);
-    int i = 0, j = (int)(t - (int64_t)d.matrix * per);
-    if (P.symmetric) {
-      while (j >= mt - i) j -= mt - i++;   // row i has mt - i tiles
-      j += i;
-    } else {
-      i = j % mt;
-      j /= mt;
-    }
-    d.m0 = i * kTile;
-    d.n0 = j * kTile;
-    return d;
-  };
+  const int first = blockIdx.x / kCtas, stride = gridDim.x / kCtas;
+  Tiles<kTile> T(C);
+  // the counter of the step before a tile's, and what it has to reach
+  auto before = [&]() { return C.written + (int64_t)(T.p - 1) * C.batch + T.matrix; };
+  auto need = [&]() { return T.tiles(T.p - 1) * kCtas * kEpiWarps; };
 
   uint32_t filled = 0, fill_par = 0;
   bool producer = false;
@@ -169,33 +240,46 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const bool second = warp == kSecondProducer;
     if (tc::elect_one()) {
       producer = !second;
-      int stage = 0;
+      int stage = 0, seen_p = 0, seen_m = -1;   // a step and matrix whose operands are known to be written
       uint32_t phase = 0;
       bool ok = true;
       const uint32_t to = second ? sB : sA;
-      const CUtensorMap* map = second ? &P.b : &P.a;
-      for (int64_t t = first; t < total && ok; t += step) {
-        const Tile d = decode(t);
-        const int r = second ? d.n0 + rank * (mma_n(d) / 2) : d.m0 + rank * kBM;   // B's columns are split evenly
+      for (int64_t t = first; ok && T.seek(t); t += stride) {
+        if (T.p > 0 && (T.p != seen_p || T.matrix != seen_m)) {
+          ok = wait_written(before(), need(), &s_abort, C.limit);
+          if (!ok) break;
+          seen_p = T.p;
+          seen_m = T.matrix;
+        }
+        const Step& S = C.step[T.p];
+        const bool mn = second && S.mn();
+        const CUtensorMap* map = mn ? &C.across[S.b] : &C.along[second ? S.b : S.a];
+        // b's columns are split evenly between the CTAs
+        const int r = second ? T.n0 + rank * (T.mma_n() / 2) : T.m0 + rank * kBM;
+        const int nk = (T.k() + kBK - 1) / kBK;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!tc::mbar_wait(empty(stage), phase ^ 1u, &s_abort, kWaitNs)) {
+          if (!tc::mbar_wait(empty(stage), phase ^ 1u, &s_abort, C.limit)) {
             ok = false;
             break;
           }
-          if (rank == 0 && !second) tc::mbar_arrive_expect_tx(full(stage), 4 * kOperand);
-          const uint32_t at = to + stage * kOperand, fbar = tc::map_peer(full(stage), 0);
-          if (kMN && second) {
-            tc::tma_load_3d_pair(at, map, fbar, r, kb * kBK, d.matrix);
-            tc::tma_load_3d_pair(at + kHalf, map, fbar, r + 64, kb * kBK, d.matrix);
+          if (rank == 0 && !second) tc::mbar_arrive_expect_tx(full(stage), 2 * kCtas * kOperand);
+          const uint32_t at = to + stage * kOperand;
+          auto load = [&](uint32_t dst, int c0, int c1) {
+            if (kPair) tc::tma_load_3d_pair(dst, map, tc::map_peer(full(stage), 0), c0, c1, T.matrix);
+            else tc::tma_load_3d(dst, map, full(stage), c0, c1, T.matrix);
+          };
+          if (mn) {
+            load(at, r, kb * kBK);
+            load(at + kHalf, r + 64, kb * kBK);
           } else {
-            tc::tma_load_3d_pair(at, map, fbar, kb * kBK, r, d.matrix);
+            load(at, kb * kBK, r);
           }
           filled |= 1u << stage;
           fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
           advance(stage, phase);
         }
       }
-      if (!ok) give_up(P.err, &s_abort);
+      if (!ok) give_up(C.err, &s_abort);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -204,12 +288,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, ready = false;   // ready: the stage at hand was seen full
-      const uint64_t a0 = tc::sdesc_k128(sA), b0 = kMN ? sdesc_mn128(sB) : tc::sdesc_k128(sB);
-      constexpr uint32_t as = kStepK >> 4, bs = (kMN ? kStepMN : kStepK) >> 4;
-      for (int64_t t = first; t < total && ok; t += step) {
-        const Tile d = decode(t);
-        const uint32_t idesc = idesc_f16_f32(kTile, mma_n(d)) | (kMN ? kMajorB : 0u);
-        if (!tc::mbar_wait(tempty(acc), acc_phase ^ 1u, &s_abort, kWaitNs)) {
+      const uint64_t a0 = tc::sdesc_k128(sA);
+      for (int64_t t = first; ok && T.seek(t); t += stride) {
+        const bool mn = C.step[T.p].mn();
+        const uint64_t b0 = mn ? sdesc_mn128(sB) : tc::sdesc_k128(sB);
+        const uint32_t as = kStepK >> 4, bs = (mn ? kStepMN : kStepK) >> 4;
+        const uint32_t idesc = idesc_f16_f32(kTile, T.mma_n()) | (mn ? kMajorB : 0u);
+        const int k = T.k(), nk = (k + kBK - 1) / kBK;
+        if (!tc::mbar_wait(tempty(acc), acc_phase ^ 1u, &s_abort, C.limit)) {
           ok = false;
           break;
         }
@@ -217,105 +303,145 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const uint32_t dst = tmem + (uint32_t)(acc * kTile);
 #pragma unroll 1
         for (int kb = 0; kb < nk; ++kb) {
-          if (!ready && !tc::mbar_wait(full(stage), phase, &s_abort, kWaitNs)) {
+          if (!ready && !tc::mbar_wait(full(stage), phase, &s_abort, C.limit)) {
             ok = false;
             break;
           }
-          const int here = stage, ng = min(kBK / kGroup, (P.k - kb * kBK + kGroup - 1) / kGroup);
+          const int here = stage, ng = min(kBK / kGroup, (k - kb * kBK + kGroup - 1) / kGroup);
           advance(stage, phase);
           // looked at under the MMAs still running (the wait itself costs 200 cycles)
-          ready = tc::mbar_try_wait(full(stage), phase);
+          ready = tc::mbar_test_wait(full(stage), phase);
           const uint64_t a = a0 + (uint32_t)(here * (kOperand >> 4)), b = b0 + (uint32_t)(here * (kOperand >> 4));
-          tc::mma_bf16_pair(dst, a, b, idesc, kb != 0);
 #pragma unroll
-          for (int g = 1; g < kBK / kGroup; ++g)
-            if (g < ng) tc::mma_bf16_pair(dst, a + g * as, b + g * bs, idesc, 1);
-          tc::tc_commit_pair_mc(empty(here), 0x3);
+          for (int g = 0; g < kBK / kGroup; ++g) {
+            if (g < ng) {
+              if (kPair) tc::mma_bf16_pair(dst, a + g * as, b + g * bs, idesc, g || kb);
+              else tc::mma_bf16(dst, a + g * as, b + g * bs, idesc, g || kb);
+            }
+          }
+          commit(empty(here));
         }
         if (!ok) break;
-        tc::tc_commit_pair_mc(tfull(acc), 0x3);
+        commit(tfull(acc));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      if (!ok) give_up(P.err, &s_abort);
-      tc::tc_commit_pair_mc(done, 0x3);   // both CTAs learn when every MMA has finished
+      if (!ok) give_up(C.err, &s_abort);
+      commit(done);   // both CTAs learn when every MMA has finished
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, half = (warp - 2) >> 2;   // TMEM lanes 32 q .. 32 q + 31 belong to this warp
+    const uint32_t buf = sOut + (warp - 2) * kStoreBytes;
+    uint8_t* mine = smem_raw + (buf - tc::smem_u32(smem_raw));
     int acc = 0;
     uint32_t acc_phase = 0;
-    const uint64_t limit = kWaitNs + (uint64_t)nk * kStageNs;
-    for (int64_t t = first; t < total; t += step) {
-      const Tile d = decode(t);
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(tfull(acc), acc_phase, &s_abort, limit))) {
-        give_up(P.err, &s_abort);
+    for (int64_t t = first; T.seek(t); t += stride) {
+      const Step& S = C.step[T.p];
+      const int cols = T.cols(), row0 = T.m0 + rank * kBM + q * 32, row = row0 + lane;
+      const bool mirror = !S.wide() && T.m0 != T.n0;
+      const __half* add = S.add >= 0 && row < C.s
+                              ? C.buf[S.add] + T.matrix * C.square_plane + row * C.square : nullptr;
+      // 32 elements of the addend; rows are padded to 8: a vector that starts inside the row lies inside it
+      auto fetch = [&](int col, uint4* v) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          v[g] = add && col + g * 8 < cols ? __ldcg(reinterpret_cast<const uint4*>(add + col + g * 8))
+                                           : make_uint4(0u, 0u, 0u, 0u);
+      };
+      uint4 ahead[4];
+      const int first_col = T.n0 + half * kChunks * 64;
+      bool ok = true;
+      if (S.add >= 0) {
+        ok = wait_written(before(), need(), &s_abort, C.limit);   // long since: the operands are
+        fetch(first_col, ahead);
+      }
+      ok = ok && tc::mbar_wait(tfull(acc), acc_phase, &s_abort, C.limit);
+      if (!__all_sync(0xffffffffu, ok)) {
+        give_up(C.err, &s_abort);
         break;
       }
       tc::tc_fence_after();
-      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile);
-      const int row = d.m0 + rank * kBM + q * 32 + lane;
-      __half* out = P.out + (int64_t)d.matrix * P.plane;
-      const __half* add = P.add ? P.add + (int64_t)d.matrix * P.plane : nullptr;
-      const bool mirror = P.symmetric && d.m0 != d.n0;
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile + half * kChunks * 64);
 #pragma unroll 1
-      for (int c = half * 4; c < half * 4 + 4; ++c) {
-        const int col = d.n0 + c * 32;
-        if (col >= P.cols) break;
-        uint32_t r[32];
-        tc::tmem_ld_32x32b_x32(tbase + c * 32, r);
-        uint4 more[4] = {};
-        // rows are padded to 8 elements: a vector that starts inside the row lies inside it
-        if (add && row < P.rows)
+      for (int c = 0; c < kChunks; ++c) {
+        const int col = first_col + c * 64;
+        uint32_t packed[2][16];
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if (col + g * 8 < P.cols) more[g] = *reinterpret_cast<const uint4*>(add + row * P.pitch + col + g * 8);
-        tc::tmem_wait_ld();
-        uint32_t packed[16];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
+          tc::tmem_ld_32x32b_x32(tbase + c * 64 + h * 32, r);
+          uint4 more[4] = {};
+          if (S.add >= 0) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float v[2];
-          const float2 m = __half22float2(reinterpret_cast<const __half2*>(more)[j]);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            v[x] = P.alpha * __uint_as_float(r[2 * j + x]);
-            v[x] = fmaf(P.beta, x ? m.y : m.x, v[x]);
-            if (row == col + 2 * j + x) v[x] += P.diag;
+            for (int g = 0; g < 4; ++g) more[g] = ahead[g];
+            if (h == 0 || c + 1 < kChunks) fetch(col + (h + 1) * 32, ahead);
           }
-          const __half2 h = __floats2half2_rn(v[0], v[1]);
-          packed[j] = *reinterpret_cast<const uint32_t*>(&h);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float v[2];
+            const float2 m = __half22float2(reinterpret_cast<const __half2*>(more)[j]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              v[x] = S.alpha * __uint_as_float(r[2 * j + x]);
+              v[x] = fmaf(S.beta, x ? m.y : m.x, v[x]);
+              if (row == col + h * 32 + 2 * j + x) v[x] += S.diag;
+            }
+            const __half2 f = __floats2half2_rn(v[0], v[1]);
+            packed[h][j] = *reinterpret_cast<const uint32_t*>(&f);
+          }
         }
-        if (row < P.rows) {
-          uint4* to = reinterpret_cast<uint4*>(out + row * P.pitch + col);
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if (col + g * 8 < P.cols)
-              to[g] = make_uint4(packed[4 * g], packed[4 * g + 1], packed[4 * g + 2], packed[4 * g + 3]);
-          if (mirror) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col + j < P.cols)
-                reinterpret_cast<uint16_t*>(out)[(int64_t)(col + j) * P.pitch + row] =
-                    (uint16_t)(packed[j >> 1] >> (16 * (j & 1)));
+        if (c == kChunks - 1) {   // tensor memory has been read
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (rank == 0) tc::mbar_arrive(tempty(acc));
+            else tc::mbar_arrive_remote_relaxed(tc::map_peer(tempty(acc), 0));
           }
+        }
+        if (row0 >= C.s || col >= cols) continue;
+        // The tile leaves through shared memory by TMA, which writes what lies
+        // inside the matrix; stored by its threads, a row each and the mirrored
+        // elements one by one, a short product's tile took longer than its MMAs.
+        if (lane == 0) tc::bulk_wait_read();   // the buffer's previous store has been read
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)   // 16 bytes at the place that the 128-byte swizzle gives them
+          *reinterpret_cast<uint4*>(mine + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+              make_uint4(packed[j >> 2][j % 4 * 4], packed[j >> 2][j % 4 * 4 + 1], packed[j >> 2][j % 4 * 4 + 2],
+                         packed[j >> 2][j % 4 * 4 + 3]);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::tma_store_3d(&C.store[S.out], buf, col, row0, T.matrix);
+        if (mirror) {
+          if (lane == 0) tc::bulk_wait_read();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            reinterpret_cast<uint16_t*>(mine)[j * 32 + lane] = (uint16_t)(packed[j >> 5][(j & 31) >> 1] >> (16 * (j & 1)));
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::tma_store_3d(&C.mirror[S.out], buf, row0, col, T.matrix);
         }
       }
-      tc::tc_fence_before();
-      __syncwarp();
       if (lane == 0) {
-        if (rank == 0) tc::mbar_arrive(tempty(acc));
-        else tc::mbar_arrive_remote_relaxed(tc::map_peer(tempty(acc), 0));
+        tc::bulk_wait_all();   // written, and ...
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        __threadfence();       // ... before the count
+        atomicAdd(C.written + (int64_t)T.p * C.batch + T.matrix, 1);
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
+    if (lane == 0) tc::bulk_wait_all();
   }
   tc::tc_fence_before();
   __syncthreads();
   // every MMA has finished before the CTAs part
   if (warp == 1) {
-    if (lane == 0 && !tc::mbar_wait(done, 0, nullptr, kWaitNs)) set_error(P.err, kDevTimeout);
+    if (lane == 0 && !tc::mbar_wait(done, 0, nullptr, kWaitNs)) set_error(C.err, kDevTimeout);
     __syncwarp();
   }
   // after an abort the leader drains its stage barriers, on which both CTAs'
@@ -329,55 +455,64 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     while (tc::globaltimer() - t0 < 1000000ull) {
     }
   }
-  __syncwarp();         // the cluster's barrier takes whole warps
-  tc::cluster_sync();   // neither CTA leaves while the other may still signal it
+  __syncwarp();                     // the cluster's barrier takes whole warps
+  if (kPair) tc::cluster_sync();    // neither CTA leaves while the other may still signal it
   if (warp == 1) {
     tc::tc_fence_after();
-    tc::tmem_dealloc_pair(tmem, kTmemCols);
+    if (kPair) tc::tmem_dealloc_pair(tmem, kTmemCols);
+    else tc::tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-// Matrices [rows, cols], `pitch` elements a row, one after the other.
-struct Held {
-  __half* p;
-  int rows, cols;
-  int64_t pitch;
-  int64_t plane() const { return (int64_t)rows * pitch; }
-};
+// The steps of `iterations`; X ends in kX or kY, which is returned.  In pairs:
+// with B1 and A1 = (B1 A) B1 the next A without X, and X <- (B2 B1) X once for
+// two iterations, three more products of s x s for one X X^T and one B X less.
+Buffer plan_steps(Chain& C, int iterations, bool pairs) {
+  const float back = 1.f / kHeld;   // what is held is 2^12 times the value: a product of two comes out 2^24 times
+  Buffer X = kX, Y = kY;
+  int n = 0;
+  auto put = [&](Buffer a, Buffer b, Buffer out) {
+    C.step[n++] = Step{a, b, out, kNone, a == b && a <= kY, back, 0.f, 0.f};
+  };
+  auto polynomial = [&](Buffer out) { C.step[n++] = Step{kG, kG, out, kG, false, kC * back, kB, kA * kHeld}; };
+  for (int i = 0; i < iterations;) {
+    put(X, X, kG);
+    polynomial(kP);
+    Buffer apply = kP;
+    if (pairs && i + 2 <= iterations) {
+      put(kP, kG, kQ);
+      put(kQ, kP, kG);
+      polynomial(kQ);
+      put(kQ, kP, kG);
+      apply = kG;
+      ++i;
+    }
+    put(apply, X, Y);
+    const Buffer t = X;
+    X = Y;
+    Y = t;
+    ++i;
+  }
+  C.steps = n;
+  return X;
+}
 
-template <bool kMN>
-cudaError_t product(const Held& a, const Held& b, const Held& out, int batch, bool symmetric, float alpha,
-                    const Held* add, float beta, float diag, const int32_t* skip, int* err, cudaStream_t st) {
-  Product P = {};
-  if (!tma_map_16bit_3d(&P.a, a.p, batch, a.rows, a.cols, a.pitch, a.plane(), kBM) ||
-      !tma_map_16bit_3d(&P.b, b.p, batch, b.rows, b.cols, b.pitch, b.plane(), kMN ? kBK : kBM))
-    return cudaErrorNotSupported;
-  P.out = out.p;
-  P.add = add ? add->p : nullptr;
-  P.rows = out.rows;
-  P.cols = out.cols;
-  P.k = a.cols;
-  P.pitch = out.pitch;
-  P.plane = out.plane();
-  P.batch = batch;
-  P.symmetric = symmetric;
-  P.alpha = alpha;
-  P.beta = beta;
-  P.diag = diag;
-  P.skip = skip;
-  P.err = err;
-  const int64_t mt = (out.rows + kTile - 1) / kTile, nt = (out.cols + kTile - 1) / kTile;
-  const int64_t tiles = batch * (symmetric ? mt * (mt + 1) / 2 : mt * nt), pairs = sm_count() / 2;
-  auto kern = product_kernel<kMN>;
+template <bool kPair>
+cudaError_t launch_chain(Chain& C, int64_t tiles, cudaStream_t st) {
+  constexpr int kCtas = kPair ? 2 : 1;
+  const int64_t most = sm_count() / kCtas, ctas = tiles < most ? tiles : most;
+  const int64_t stages = (C.L + kBK - 1) / kBK;
+  C.limit = kWaitNs + (uint64_t)((tiles / ctas + 2) * stages) * kStageNs;
+  auto kern = chain_kernel<kPair>;
   const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (r != cudaSuccess) return r;
-  return launch_kernel(kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kThreads), kSmem, st, 2, P);
+  return launch_kernel(kern, dim3((unsigned)(kCtas * ctas)), dim3(kThreads), kSmem, st, kCtas, C);
 }
 
 // ---------------------------------------------------------------- what surrounds them
 
-// A part of a tensor: `count` of its matrices, which are matrices `first` and
-// on of the ones at hand.
+// A part of a tensor: matrices of it, which are matrices `first` and on of the
+// ones at hand, up to the next segment's.
 struct Segment {
   float* p;
   bf16* p16;
@@ -385,7 +520,7 @@ struct Segment {
   float* m;
   void* out;             // raw: receives the result
   int rows, cols;
-  int first, count;
+  int first;
   float keep, step;      // p = p keep - step O
 };
 constexpr int kSegments = 24;
@@ -470,6 +605,35 @@ __device__ __forceinline__ Squares warp_sum(Squares v) {
 constexpr int kPart = 8192;   // elements of a partial sum
 constexpr float kUp = 1.2379400392853803e27f, kDown = 8.077935669463161e-28f;   // 2^90, 2^-90
 
+__device__ __forceinline__ void add_square(Squares& q, float u) {
+  const float b = u * kDown, s = u * kUp;
+  q.mid = fmaf(u, u, q.mid);
+  q.big = fmaf(b, b, q.big);
+  q.small = fmaf(s, s, q.small);
+}
+
+// The two factors that take u to X as it is held: a power of two first, so that
+// no product overflows or vanishes on the way.
+__device__ __forceinline__ float2 factors_of(const Squares& q) {
+  if (isinf(q.mid)) return isinf(q.big) ? make_float2(NAN, NAN) : make_float2(kDown, kHeld / sqrtf(q.big));
+  // a sum above 1e-20 has no share worth mentioning of squares that vanished
+  if (!(q.mid <= 1e-20f)) return make_float2(1.f, kHeld / sqrtf(q.mid));   // a NaN too
+  return q.small > 0.f ? make_float2(kUp, kHeld / sqrtf(q.small)) : make_float2(0.f, 0.f);
+}
+// The sum over a block's warps (at most 8), for thread 0.
+__device__ __forceinline__ Squares block_sum(Squares q, Squares* s_w) {
+  q = warp_sum(q);
+  if (threadIdx.x % 32 == 0) s_w[threadIdx.x / 32] = q;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int w = 1; w < (int)blockDim.x / 32; ++w) {
+      q.mid += s_w[w].mid;
+      q.big += s_w[w].big;
+      q.small += s_w[w].small;
+    }
+  return q;
+}
+
 // The momentum's step, and the sums of squares of each matrix' update.
 template <typename T>
 __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ Matrices M, Squares* __restrict__ part) {
@@ -503,70 +667,30 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ M
       store4(m + i, vm, left, mm);
     }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (x >= left) continue;
-      const float b = u[x] * kDown, s = u[x] * kUp;
-      q.mid = fmaf(u[x], u[x], q.mid);
-      q.big = fmaf(b, b, q.big);
-      q.small = fmaf(s, s, q.small);
-    }
+    for (int x = 0; x < 4; ++x)
+      if (x < left) add_square(q, u[x]);
   }
-  q = warp_sum(q);
-  if (threadIdx.x % 32 == 0) s_w[threadIdx.x / 32] = q;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 8; ++w) {
-      q.mid += s_w[w].mid;
-      q.big += s_w[w].big;
-      q.small += s_w[w].small;
-    }
-    part[blockIdx.x] = q;
-  }
+  q = block_sum(q, s_w);
+  if (threadIdx.x == 0) part[blockIdx.x] = q;
 }
 
-// One block for each matrix: the two factors that take u to X as it is held,
-// 2^-e first, so that no product overflows or vanishes on the way.
+// One block for each matrix: its counters to zero, and X's factors.
 __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ Matrices M, const Squares* __restrict__ part,
-                                                   float2* __restrict__ factor) {
-  __shared__ double s_w[3][8];
+                                                   float2* __restrict__ factor, int* __restrict__ written, int steps) {
+  __shared__ Squares s_w[8];
   pdl_enter();
   if (M.skip && *M.skip) return;
-  double v[3] = {};
+  for (int i = threadIdx.x; i < steps; i += 256) written[(int64_t)i * gridDim.x + blockIdx.x] = 0;
+  Squares q = {0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int i = threadIdx.x; i < M.parts; i += 256) {
-    const Squares q = part[(int64_t)blockIdx.x * M.parts + i];
-    v[0] += q.mid;
-    v[1] += q.big;
-    v[2] += q.small;
+    const Squares p = part[(int64_t)blockIdx.x * M.parts + i];
+    q.mid += p.mid;
+    q.big += p.big;
+    q.small += p.small;
   }
-#pragma unroll
-  for (int c = 0; c < 3; ++c) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[c] += __shfl_xor_sync(0xffffffffu, v[c], o);
-    if (threadIdx.x % 32 == 0) s_w[c][threadIdx.x / 32] = v[c];
-  }
-  __syncthreads();
-  if (threadIdx.x) return;
-  for (int c = 0; c < 3; ++c) {
-    v[c] = s_w[c][0];
-    for (int w = 1; w < 8; ++w) v[c] += s_w[c][w];
-  }
-  // a sum above 1e-20 has no share worth mentioning of squares that vanished
-  double norm;
-  if (v[0] != v[0]) norm = v[0];
-  else if (isinf(v[0])) norm = sqrt(v[1]) * (double)kUp;
-  else if (v[0] > 1e-20) norm = sqrt(v[0]);
-  else norm = sqrt(v[2]) * (double)kDown;
-  float2 f = make_float2(0.f, 0.f);
-  if (norm > 0 && !isinf(norm)) {
-    int e;
-    frexp(norm, &e);
-    e = e > 126 ? 126 : e < -126 ? -126 : e;
-    f.x = (float)ldexp(1.0, -e);
-    f.y = (float)((double)kHeld / ldexp(norm, -e));
-  } else if (!(norm == 0)) {
-    f.x = f.y = NAN;   // a NaN or an infinity in u
-  }
-  factor[blockIdx.x] = f;
+  q = block_sum(q, s_w);
+  if (threadIdx.x == 0) factor[blockIdx.x] = factors_of(q);
 }
 
 // A block's tile of 64 x 64 elements of a matrix: rows r0.., columns c0.. as it
@@ -648,7 +772,29 @@ build_kernel(const __grid_constant__ Matrices M, const float2* __restrict__ fact
   }
 }
 
-// p = p keep - step O, and its bf16 copy; raw: out = O.
+// Four elements, of which `left` exist, from e on: p = p keep - step O, and its bf16 copy; raw: out = O.
+__device__ __forceinline__ void put4(const Matrices& M, const Segment& S, int64_t e, bool even, int left, const float* o) {
+  if (M.raw) {
+    if (M.out_dtype == MOE_BF16) {
+      bf16* to = reinterpret_cast<bf16*>(S.out) + e;
+      store4(to, even && aligned_to(to, 8), left, o);
+    } else {
+      float* to = reinterpret_cast<float*>(S.out) + e;
+      store4(to, even && aligned_to(to, 16), left, o);
+    }
+    return;
+  }
+  float* p = S.p + e;
+  const bool vp = even && aligned_to(p, 16);
+  float v[4];
+  load4(p, vp, left, v);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) v[x] = v[x] * S.keep - S.step * o[x];
+  store4(p, vp, left, v);
+  if (S.p16) store4(S.p16 + e, even && aligned_to(S.p16 + e, 8), left, v);
+}
+
+// The result from X.
 __global__ void __launch_bounds__(256)
 apply_kernel(const __grid_constant__ Matrices M, const __half* __restrict__ X) {
   __shared__ float tile[64][65];
@@ -692,25 +838,332 @@ apply_kernel(const __grid_constant__ Matrices M, const __half* __restrict__ X) {
     } else {
       held4(r, c, o);
     }
-    const int64_t e = base + (int64_t)r * S.cols + c;
-    if (M.raw) {
-      if (M.out_dtype == MOE_BF16) {
-        bf16* to = reinterpret_cast<bf16*>(S.out) + e;
-        store4(to, even && aligned_to(to, 8), left, o);
-      } else {
-        float* to = reinterpret_cast<float*>(S.out) + e;
-        store4(to, even && aligned_to(to, 16), left, o);
-      }
-      continue;
+    put4(M, S, base + (int64_t)r * S.cols + c, even, left, o);
+  }
+}
+
+// ---------------------------------------------------------------- small matrices
+
+// Matrices with a short side of at most 128 and a long one of at most 4096 stay
+// on chip: a cluster takes a matrix, each of its CTAs up to 512 columns of X,
+// and the whole step is one launch.  X, A and B lie in shared memory as panels
+// of 64 columns (128 rows of 128 bytes, 128-byte swizzle), which the MMAs read
+// along the rows (X X^T, A A, and B) or across them (X in B X).  With several
+// CTAs the partial sums of X X^T are added up in the CTAs' order through the
+// cluster's shared memory, each CTA taking a share of the rows.
+//
+// What bounds it is the chain of products, each of which waits for the one
+// before: a phase takes about a microsecond.
+constexpr int kSide = 128, kPanel = kSide * 128, kSlice = 512, kMostCtas = 8;
+constexpr size_t kSmallSmem = 1024 + (size_t)(kSlice / 64 + 4) * kPanel;
+
+// Byte offset of elements (row, col) .. (col a multiple of 4) in panels.
+__device__ __forceinline__ uint32_t panel_at(int row, int col) {
+  const int b = col % 64 * 2;
+  return (uint32_t)(col / 64 * kPanel + row * 128 + ((((b >> 4) ^ (row & 7)) << 4) | (b & 15)));
+}
+
+__device__ __forceinline__ float4 ld_peer_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256, 1)
+small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ __align__(8) uint64_t s_bar;
+  __shared__ Squares s_w[8], s_part[kMostCtas];
+  const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const X = smem_raw + (base - tc::smem_u32(smem_raw));   // panels of X, then two of A and two of B
+  uint8_t* const A = X + kSlice / 64 * kPanel;
+  uint8_t* const B = A + 2 * kPanel;
+  const uint32_t sX = base, sA = sX + kSlice / 64 * kPanel, sB = sA + 2 * kPanel, bar = tc::smem_u32(&s_bar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, half = warp >> 2;
+  const int rank = (int)tc::cluster_ctarank();
+  uint32_t ctas;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  if (warp == 0) {
+    if (lane == 0) {
+      tc::mbar_init(bar, 1);
+      tc::fence_barrier_init();
     }
-    float* p = S.p + e;
-    const bool vp = even && aligned_to(p, 16);
-    float v[4];
-    load4(p, vp, left, v);
+    __syncwarp();
+    tc::tmem_alloc(tc::smem_u32(&s_tmem), 512);
+    tc::tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < kSlice / 64 * kPanel / 16; i += 256)
+    reinterpret_cast<uint4*>(X)[i] = make_uint4(0u, 0u, 0u, 0u);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  pdl_enter();
+  const uint32_t tmem = s_tmem;
+  const bool skip = M.skip && *M.skip;   // the same for every thread of the cluster
+
+  const int matrix = blockIdx.x / ctas;
+  const Segment& S = segment_of(M, matrix);
+  const bool flip = S.rows > S.cols;
+  const int s = flip ? S.cols : S.rows, L = flip ? S.rows : S.cols;
+  const int c0 = rank * kSlice, w = max(0, min(kSlice, L - c0)), panels = (w + 63) / 64;
+  const int64_t first = (int64_t)(matrix - S.first) * S.rows * S.cols;
+  const T* g = reinterpret_cast<const T*>(S.g) + first;
+  float* m = M.raw ? nullptr : S.m + first;
+  const float scale = M.grad_scale ? *M.grad_scale : 1.f;
+  // this CTA's part of the tensor, four elements of a row at a time
+  const int r0 = flip ? c0 : 0, nr = flip ? w : s, t0 = flip ? 0 : c0, nc = flip ? s : w, vecs = (nc + 3) / 4;
+  const bool even = S.cols % 4 == 0;
+  auto each = [&](auto f) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nr * vecs; i += 256) {
+      const int r = i / vecs, c = (i - r * vecs) * 4;
+      f((int64_t)(r0 + r) * S.cols + t0 + c, r, c, min(4, nc - c));
+    }
+  };
+
+  if (!skip) {
+    // the momentum's step and the update's norm
+    const bool vg = even && aligned_to(g, 4 * sizeof(T)), vm = even && aligned_to(m, 16);
+    Squares sq = {0.f, 0.f, 0.f};
+    auto update = [&](int64_t o, int left, float* u, bool write) {
+      load4(g + o, vg, left, u);
+      if (M.raw) return;
+      float mm[4];
+      load4(m + o, vm, left, mm);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) v[x] = v[x] * S.keep - S.step * o[x];
-    store4(p, vp, left, v);
-    if (S.p16) store4(S.p16 + e, even && aligned_to(S.p16 + e, 8), left, v);
+      for (int x = 0; x < 4; ++x) {
+        const float gx = u[x] * scale;
+        if (write) mm[x] = fmaf(M.mu, mm[x], gx);
+        u[x] = M.nesterov ? fmaf(M.mu, mm[x], gx) : mm[x];
+      }
+      if (write) store4(m + o, vm, left, mm);
+    };
+    each([&](int64_t o, int, int, int left) {
+      float u[4];
+      update(o, left, u, true);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (x < left) add_square(sq, u[x]);
+    });
+    sq = block_sum(sq, s_w);
+    if (threadIdx.x == 0) {
+      for (uint32_t i = 0; i < ctas; ++i) {   // to every CTA of the cluster
+        const uint32_t to = tc::map_peer(tc::smem_u32(&s_part[rank]), i);
+        tc::st_peer_f32(to, sq.mid);
+        tc::st_peer_f32(to + 4, sq.big);
+        tc::st_peer_f32(to + 8, sq.small);
+      }
+    }
+    __syncwarp();
+    tc::cluster_sync();
+    Squares all = s_part[0];
+    for (uint32_t i = 1; i < ctas; ++i) {
+      all.mid += s_part[i].mid;
+      all.big += s_part[i].big;
+      all.small += s_part[i].small;
+    }
+    const float2 f = factors_of(all);
+    each([&](int64_t o, int r, int c, int left) {
+      float u[4];
+      update(o, left, u, false);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) u[x] = x < left ? u[x] * f.x * f.y : 0.f;
+      const __half2 h[2] = {__floats2half2_rn(u[0], u[1]), __floats2half2_rn(u[2], u[3])};
+      if (flip) {
+        const __half* e = reinterpret_cast<const __half*>(h);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (x < left) {
+            const uint32_t at = panel_at(c + x, r & ~3) + (r & 3) * 2;
+            *reinterpret_cast<__half*>(X + at) = e[x];
+          }
+      } else {
+        *reinterpret_cast<uint2*>(X + panel_at(r, c)) = *reinterpret_cast<const uint2*>(h);
+      }
+    });
+
+    uint32_t phase = 0;
+    // What the threads wrote to shared memory is there for the MMAs that `issue` starts; returns when they are done.
+    auto products = [&](auto issue) {
+      tc::fence_proxy_async_smem();
+      tc::tc_fence_before();
+      __syncthreads();
+      if (warp == 0 && tc::elect_one()) {
+        tc::tc_fence_after();
+        issue();
+        tc::tc_commit(bar);
+      }
+      __syncwarp();
+      if (!tc::mbar_wait(bar, phase, nullptr, kWaitNs)) set_error(err, kDevTimeout);
+      phase ^= 1u;
+      __syncwarp();
+      tc::tc_fence_after();
+    };
+    const int row = q * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    // 32 values of this thread's row to columns col .. of panels
+    auto keep32 = [&](uint8_t* to, int col, const float* v) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4 u;
+        __half2* h = reinterpret_cast<__half2*>(&u);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) h[x] = __floats2half2_rn(v[j * 8 + 2 * x], v[j * 8 + 2 * x + 1]);
+        *reinterpret_cast<uint4*>(to + panel_at(row, col + j * 8)) = u;
+      }
+    };
+    constexpr float back = 1.f / kHeld;
+#pragma unroll 1
+    for (int it = 0; it < iterations; ++it) {
+      // A = X X^T
+      products([&]() {
+        const int steps = (w + 15) / 16;
+        for (int k = 0; k < steps; ++k) {
+          const uint64_t d = tc::sdesc_k128(sX + k / 4 * kPanel) + (uint32_t)(k % 4 * 2);
+          tc::mma_bf16(tmem, d, d, idesc_f16_f32(kSide, kSide), k > 0);
+        }
+      });
+      if (ctas == 1) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
+          tc::tmem_ld_32x32b_x32(lanes + half * 64 + h * 32, r);
+          tc::tmem_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = back * __uint_as_float(r[j]);
+          keep32(A, half * 64 + h * 32, v);
+        }
+      } else {
+        // partial sums: 128 rows of 128 fp32 over A's and B's panels, 16 bytes of a row exchanged by the row's number
+        float4* part = reinterpret_cast<float4*>(A);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
+          tc::tmem_ld_32x32b_x32(lanes + half * 64 + h * 32, r);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                         __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+            part[row * 32 + ((half * 16 + h * 8 + j) ^ (row & 31))] = w > 0 ? v : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+        tc::tc_fence_before();
+        __syncthreads();
+        tc::cluster_sync();
+        // rows rank * share ..: every fourth of a row's 32 groups of four to a thread at a time
+        const int share = kSide / (int)ctas, groups = share * 32 / 256;
+        uint2 mine[16];
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          if (n >= groups) break;
+          const int i = n * 256 + threadIdx.x, r = rank * share + i / 32, j = i % 32;
+          const uint32_t at = sA + (uint32_t)(r * 32 + (j ^ (r & 31))) * 16;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (uint32_t k = 0; k < ctas; ++k) {
+            const float4 x = ld_peer_f32x4(tc::map_peer(at, k));
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
+          }
+          const float e[4] = {v.x * back, v.y * back, v.z * back, v.w * back};
+          mine[n] = pack_half4(e);
+        }
+        tc::cluster_sync();   // every partial sum has been read
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          if (n >= groups) break;
+          const int i = n * 256 + threadIdx.x, r = rank * share + i / 32, j = i % 32;
+          const uint32_t at = sA + panel_at(r, j * 4);
+          const unsigned long long u = (unsigned long long)mine[n].y << 32 | mine[n].x;
+          for (uint32_t k = 0; k < ctas; ++k) tc::st_peer_u64(tc::map_peer(at, k), u);
+        }
+        asm volatile("fence.proxy.async;" ::: "memory");
+        tc::cluster_sync();
+      }
+      // B = a I + b A + c A A
+      products([&]() {
+        for (int k = 0; k < kSide / 16; ++k) {
+          const uint64_t d = tc::sdesc_k128(sA + k / 4 * kPanel) + (uint32_t)(k % 4 * 2);
+          tc::mma_bf16(tmem, d, d, idesc_f16_f32(kSide, kSide), k > 0);
+        }
+      });
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const int col = half * 64 + h * 32;
+        uint32_t r[32];
+        tc::tmem_ld_32x32b_x32(lanes + col, r);
+        tc::tmem_wait_ld();
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 u = *reinterpret_cast<const uint4*>(A + panel_at(row, col + j * 8));
+          const __half2* e = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 a = __half22float2(e[x]);
+            const int i = j * 8 + 2 * x;
+            v[i] = fmaf(kB, a.x, kC * back * __uint_as_float(r[i])) + (row == col + i ? kA * kHeld : 0.f);
+            v[i + 1] = fmaf(kB, a.y, kC * back * __uint_as_float(r[i + 1])) + (row == col + i + 1 ? kA * kHeld : 0.f);
+          }
+        }
+        keep32(B, col, v);
+      }
+      // X = B X
+      products([&]() {
+        for (int n = 0; n < panels; n += 4) {
+          const uint32_t idesc = idesc_f16_f32(kSide, min(4, panels - n) * 64) | kMajorB;
+          for (int k = 0; k < kSide / 16; ++k) {
+            const uint64_t a = tc::sdesc_k128(sB + k / 4 * kPanel) + (uint32_t)(k % 4 * 2);
+            const uint64_t b = (tc::sdesc_k128(sX + n * kPanel) | ((uint64_t)(kPanel >> 4) << 16)) + (uint32_t)(k * (2048 >> 4));
+            tc::mma_bf16(tmem + n * 64, a, b, idesc, k > 0);
+          }
+        }
+      });
+#pragma unroll 1
+      for (int c = half; c < panels * 2; c += 2) {
+        uint32_t r[32];
+        tc::tmem_ld_32x32b_x32(lanes + c * 32, r);
+        tc::tmem_wait_ld();
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = back * __uint_as_float(r[j]);
+        keep32(X, c * 32, v);
+      }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    // p = p keep - step O, and its bf16 copy; raw: out = O
+    each([&](int64_t o, int r, int c, int left) {
+      float v[4];
+      if (flip) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          v[x] = x < left ? __half2float(*reinterpret_cast<const __half*>(X + panel_at(c + x, r & ~3) + (r & 3) * 2)) * back
+                          : 0.f;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(X + panel_at(r, c));
+        const __half2* h = reinterpret_cast<const __half2*>(&u);
+        const float2 x = __half22float2(h[0]), y = __half22float2(h[1]);
+        v[0] = x.x * back;
+        v[1] = x.y * back;
+        v[2] = y.x * back;
+        v[3] = y.y * back;
+      }
+      put4(M, S, first + o, even, left, v);
+    });
+  }
+  if (ctas > 1) tc::cluster_sync();   // no CTA leaves while another may still read its shared memory
+  if (warp == 0) {
+    __syncwarp();
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
   }
 }
 
@@ -733,27 +1186,37 @@ struct Sizes {
   }
   size_t x() const { return (size_t)s * pitch * 2; }
   size_t a() const { return (size_t)s * square * 2; }
-  size_t bytes(int64_t n) const {   // X and its successor, A, B, sums, factors
-    return 2 * round256(n * x()) + 2 * round256(n * a()) + round256(n * parts * sizeof(Squares)) +
-           round256(n * sizeof(float2));
+  size_t bytes(int64_t n) const {   // X and its successor, three short matrices, counters, sums, factors
+    return 2 * round256(n * x()) + 3 * round256(n * a()) + round256(n * kMaxSteps * sizeof(int)) +
+           round256(n * parts * sizeof(Squares)) + round256(n * sizeof(float2));
   }
   int64_t most() const {
-    int64_t n = (int64_t)(kMostBytes / (2 * x() + 2 * a() + parts * sizeof(Squares) + sizeof(float2)));
-    const int64_t grid = ((int64_t)1 << 30) / ((int64_t)((s + 63) / 64) * ((L + 63) / 64));   // blocks of a launch
+    int64_t n = (int64_t)(kMostBytes /
+                          (2 * x() + 3 * a() + kMaxSteps * sizeof(int) + parts * sizeof(Squares) + sizeof(float2)));
+    const int64_t grid = ((int64_t)1 << 30) / ((int64_t)((s + 63) / 64) * ((L + 63) / 64));   // blocks and tiles of a launch
     if (n > grid) n = grid;
     return n < 1 ? 1 : n;
   }
 };
 
 bool empty(const moe_muon_tensor& t) { return t.batch == 0 || t.rows == 0 || t.cols == 0; }
+// CTAs of the cluster that a small matrix takes, 0 for another.
+int small_ctas(const moe_muon_tensor& t) {
+  const int s = t.rows < t.cols ? t.rows : t.cols, L = t.rows < t.cols ? t.cols : t.rows;
+  if (s > kSide || L > kMostCtas * kSlice) return 0;
+  int n = 1;
+  while (n * kSlice < L) n *= 2;
+  return n;
+}
+bool large(const moe_muon_tensor& t) { return !empty(t) && !small_ctas(t); }
 bool alike(const moe_muon_tensor& a, const moe_muon_tensor& b) {
   return (a.rows == b.rows && a.cols == b.cols) || (a.rows == b.cols && a.cols == b.rows);
 }
-// Whether tensor i is the first of its size.
+// Whether tensor i is the first large one of its size.
 bool leads(const moe_muon_tensor* t, int i) {
-  if (empty(t[i])) return false;
+  if (!large(t[i])) return false;
   for (int j = 0; j < i; ++j)
-    if (!empty(t[j]) && alike(t[i], t[j])) return false;
+    if (large(t[j]) && alike(t[i], t[j])) return false;
   return true;
 }
 
@@ -766,28 +1229,60 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
     at += round256(bytes);
     return p;
   };
-  Held X{(__half*)take(n * z.x()), z.s, z.L, z.pitch}, Y{(__half*)take(n * z.x()), z.s, z.L, z.pitch};
-  Held A{(__half*)take(n * z.a()), z.s, z.s, z.square}, B{(__half*)take(n * z.a()), z.s, z.s, z.square};
+  Chain C = {};
+  for (int i = 0; i < kBuffers; ++i) C.buf[i] = (__half*)take(n * (i <= kY ? z.x() : z.a()));
+  C.written = (int*)take((size_t)n * kMaxSteps * sizeof(int));
   Squares* part = (Squares*)take((size_t)n * z.parts * sizeof(Squares));
   float2* factor = (float2*)take((size_t)n * sizeof(float2));
+  C.s = z.s;
+  C.L = z.L;
+  C.batch = n;
+  C.pitch = z.pitch;
+  C.plane = z.s * z.pitch;
+  C.square = z.square;
+  C.square_plane = z.s * z.square;
+  C.skip = M.skip;
+  C.err = err;
+  for (int i = 0; i < kBuffers; ++i) {
+    const bool x = i <= kY;
+    if (!tma_map_16bit_3d(&C.along[i], C.buf[i], n, z.s, x ? z.L : z.s, x ? z.pitch : z.square,
+                          x ? C.plane : C.square_plane, kBM) ||
+        !tma_map_16bit_3d(&C.store[i], C.buf[i], n, z.s, x ? z.L : z.s, x ? z.pitch : z.square,
+                          x ? C.plane : C.square_plane, 32) ||
+        (x && !tma_map_16bit_3d(&C.across[i], C.buf[i], n, z.s, z.L, z.pitch, C.plane, kBK)) ||
+        (!x && !tma_map_16bit_3d(&C.mirror[i], C.buf[i], n, z.s, z.s, z.square, C.square_plane, 64, 32)))
+      return cudaErrorNotSupported;
+  }
+  // Which of the two tiles takes less time by their number: a stage of a pair's
+  // tile takes 600 cycles, of a single one's 540 (a quarter of the work, but
+  // both load 32 KB for each SM, which is what L2 gives in that time), and a
+  // step's start and the epilogue of its last tile 12000 and 6500.
+  // Single tiles win where the pairs' would leave most SMs idle.
+  auto tiles_of = [&](int tile, bool wide) {
+    const int64_t mt = (z.s + tile - 1) / tile, nt = (z.L + tile - 1) / tile;
+    return n * (wide ? mt * nt : mt * (mt + 1) / 2);
+  };
+  const int64_t pair_tiles = tiles_of(256, true), single_tiles = tiles_of(128, true), sms = sm_count();
+  auto cost = [&](int64_t wide, int64_t shorts, int64_t ctas, int64_t stage, int64_t start) {
+    const int64_t a = (z.L + kBK - 1) / kBK, b = (z.s + kBK - 1) / kBK;
+    return ((shorts + ctas - 1) / ctas * (a + b) + (wide + ctas - 1) / ctas * b) * stage + 3 * start;
+  };
+  const bool pair = cost(pair_tiles, tiles_of(256, false), sms / 2, 600, 12000) <=
+                    cost(single_tiles, tiles_of(128, false), sms, 540, 6500);
+  // Two iterations at a time where the products with X are longer by enough and
+  // the short ones fill the SMs.
+  const bool pairs = 4 * (int64_t)z.L >= 5 * (int64_t)z.s && pair && tiles_of(256, false) >= sms / 2;
+  const Buffer result = plan_steps(C, iterations, pairs);
   const dim3 sums((unsigned)(n * z.parts)), tiles((unsigned)((int64_t)n * M.tiles_s * M.tiles_L)), threads(256);
   cudaError_t e = grad_bf16 ? launch_kernel(momentum_kernel<bf16>, sums, threads, 0, st, 1, M, part)
                             : launch_kernel(momentum_kernel<float>, sums, threads, 0, st, 1, M, part);
-  if (e == cudaSuccess) e = launch_kernel(norm_kernel, dim3((unsigned)n), threads, 0, st, 1, M, part, factor);
+  if (e == cudaSuccess) e = launch_kernel(norm_kernel, dim3((unsigned)n), threads, 0, st, 1, M, part, factor, C.written, C.steps);
   if (e == cudaSuccess)
-    e = grad_bf16 ? launch_kernel(build_kernel<bf16>, tiles, threads, 0, st, 1, M, factor, X.p)
-                  : launch_kernel(build_kernel<float>, tiles, threads, 0, st, 1, M, factor, X.p);
-  // what is held is 2^12 times the value: a product of two comes out 2^24 times
-  const float back = 1.f / kHeld;
-  for (int i = 0; i < iterations && e == cudaSuccess; ++i) {
-    e = product<false>(X, X, A, n, true, back, nullptr, 0.f, 0.f, M.skip, err, st);
-    if (e == cudaSuccess) e = product<false>(A, A, B, n, true, kC * back, &A, kB, kA * kHeld, M.skip, err, st);
-    if (e == cudaSuccess) e = product<true>(B, X, Y, n, false, back, nullptr, 0.f, 0.f, M.skip, err, st);
-    const Held t = X;
-    X = Y;
-    Y = t;
-  }
-  if (e == cudaSuccess) e = launch_kernel(apply_kernel, tiles, threads, 0, st, 1, M, X.p);
+    e = grad_bf16 ? launch_kernel(build_kernel<bf16>, tiles, threads, 0, st, 1, M, factor, C.buf[kX])
+                  : launch_kernel(build_kernel<float>, tiles, threads, 0, st, 1, M, factor, C.buf[kX]);
+  if (e != cudaSuccess) return e;
+  e = pair ? launch_chain<true>(C, pair_tiles, st) : launch_chain<false>(C, single_tiles, st);
+  if (e == cudaSuccess) e = launch_kernel(apply_kernel, tiles, threads, 0, st, 1, M, C.buf[result]);
   return e;
 }
 
@@ -800,7 +1295,7 @@ size_t orthogonal_workspace(const moe_muon_tensor* tensors, int count) {
     const Sizes z(tensors[i].rows, tensors[i].cols);
     int64_t n = 0;
     for (int j = i; j < count; ++j)
-      if (!empty(tensors[j]) && alike(tensors[i], tensors[j])) n += tensors[j].batch;
+      if (large(tensors[j]) && alike(tensors[i], tensors[j])) n += tensors[j].batch;
     const int64_t cap = z.most();
     const size_t bytes = z.bytes(n < cap ? n : cap);
     if (bytes > most) most = bytes;
@@ -808,14 +1303,75 @@ size_t orthogonal_workspace(const moe_muon_tensor* tensors, int count) {
   return 256 + most;
 }
 
+// What the kernels are told of matrices b .. b + n of a tensor.
+static Segment segment(const moe_muon_tensor& t, int64_t b, int64_t n, int held, int grad_dtype,
+                       const moe_muon_params& h, const OrthogonalRaw* raw) {
+  const int64_t at = b * t.rows * t.cols;
+  Segment S = {};
+  S.rows = t.rows;
+  S.cols = t.cols;
+  S.first = held;
+  if (raw) {
+    S.g = (const char*)raw->x + at * (raw->x_dtype == MOE_BF16 ? 2 : 4);
+    S.out = (char*)raw->out + at * (raw->out_dtype == MOE_BF16 ? 2 : 4);
+  } else {
+    S.p = t.p + at;
+    S.p16 = t.p_bf16 ? (bf16*)t.p_bf16 + at : nullptr;
+    S.g = (const char*)t.grad + at * (grad_dtype == MOE_BF16 ? 2 : 4);
+    S.m = t.m + at;
+    S.keep = (float)(1.0 - h.lr * t.weight_decay);
+    S.step = (float)(h.lr * t.scale);
+  }
+  return S;
+}
+
 cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int grad_dtype, const moe_muon_params& h,
                               const OrthogonalRaw* raw, const float* grad_scale, const int32_t* skip, void* ws,
                               cudaStream_t st) {
+  Matrices M = {};
+  M.mu = (float)h.momentum;
+  M.nesterov = h.nesterov != 0;
+  M.raw = raw != nullptr;
+  M.out_dtype = raw ? raw->out_dtype : MOE_F32;
+  M.grad_scale = grad_scale;
+  M.skip = skip;
+  int held = 0;   // matrices in M
+  // Collects the matrices of the tensors that `which` names, from tensor i on,
+  // and has `run` run `most` of them at a time.
+  auto collect = [&](int i, int64_t most, auto which, auto run) {
+    M.n = held = 0;
+    for (int j = i; j < count; ++j) {
+      const moe_muon_tensor& t = tensors[j];
+      if (!which(t)) continue;
+      for (int64_t b = 0; b < t.batch;) {
+        if (held == most || M.n == kSegments) {
+          const cudaError_t e = run();
+          if (e != cudaSuccess) return e;
+          M.n = held = 0;
+        }
+        const int64_t n = t.batch - b < most - held ? t.batch - b : most - held;
+        M.seg[M.n++] = segment(t, b, n, held, grad_dtype, h, raw);
+        held += (int)n;
+        b += n;
+      }
+    }
+    return held ? run() : cudaSuccess;
+  };
+  for (int ctas = 1; ctas <= kMostCtas; ctas *= 2) {
+    const cudaError_t e = collect(
+        0, 1 << 24, [&](const moe_muon_tensor& t) { return !empty(t) && small_ctas(t) == ctas; },
+        [&]() {
+          auto kern = grad_dtype == MOE_BF16 ? small_kernel<bf16> : small_kernel<float>;
+          const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
+          if (r != cudaSuccess) return r;
+          return launch_kernel(kern, dim3((unsigned)(held * ctas)), dim3(256), kSmallSmem, st, (unsigned)ctas, M,
+                               (int)h.iterations, (int*)ws);
+        });
+    if (e != cudaSuccess) return e;
+  }
   for (int i = 0; i < count; ++i) {
     if (!leads(tensors, i)) continue;
     const Sizes z(tensors[i].rows, tensors[i].cols);
-    const int64_t cap = z.most();
-    Matrices M = {};
     M.s = z.s;
     M.L = z.L;
     M.pitch = z.pitch;
@@ -823,51 +1379,9 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
     M.parts = z.parts;
     M.tiles_s = (z.s + 63) / 64;
     M.tiles_L = (z.L + 63) / 64;
-    M.mu = (float)h.momentum;
-    M.nesterov = h.nesterov != 0;
-    M.raw = raw != nullptr;
-    M.out_dtype = raw ? raw->out_dtype : MOE_F32;
-    M.grad_scale = grad_scale;
-    M.skip = skip;
-    int held = 0;   // matrices in M
-    auto flush = [&]() {
-      if (held == 0) return cudaSuccess;
-      const cudaError_t e = run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, (char*)ws, st);
-      M.n = held = 0;
-      return e;
-    };
-    for (int j = i; j < count; ++j) {
-      const moe_muon_tensor& t = tensors[j];
-      if (empty(t) || !alike(tensors[i], t)) continue;
-      const int64_t size = (int64_t)t.rows * t.cols;
-      for (int64_t b = 0; b < t.batch;) {
-        if (held == cap || M.n == kSegments) {
-          const cudaError_t e = flush();
-          if (e != cudaSuccess) return e;
-        }
-        const int64_t n = t.batch - b < cap - held ? t.batch - b : cap - held;
-        Segment& S = M.seg[M.n++];
-        S = {};
-        S.rows = t.rows;
-        S.cols = t.cols;
-        S.first = held;
-        S.count = (int)n;
-        if (raw) {
-          S.g = (const char*)raw->x + b * size * (raw->x_dtype == MOE_BF16 ? 2 : 4);
-          S.out = (char*)raw->out + b * size * (raw->out_dtype == MOE_BF16 ? 2 : 4);
-        } else {
-          S.p = t.p + b * size;
-          S.p16 = t.p_bf16 ? (bf16*)t.p_bf16 + b * size : nullptr;
-          S.g = (const char*)t.grad + b * size * (grad_dtype == MOE_BF16 ? 2 : 4);
-          S.m = t.m + b * size;
-          S.keep = (float)(1.0 - h.lr * t.weight_decay);
-          S.step = (float)(h.lr * t.scale);
-        }
-        held += (int)n;
-        b += n;
-      }
-    }
-    const cudaError_t e = flush();
+    const cudaError_t e = collect(
+        i, z.most(), [&](const moe_muon_tensor& t) { return large(t) && alike(tensors[i], t); },
+        [&]() { return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, (char*)ws, st); });
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

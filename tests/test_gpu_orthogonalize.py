@@ -73,7 +73,10 @@ def run(x, out_dtype, iterations=5):
 
 
 SHAPES = [(1, 1, 1), (2, 1, 7), (1, 5, 1), (3, 2, 2), (1, 64, 96), (2, 96, 64), (1, 17, 1000), (2, 257, 300),
-          (1, 255, 256), (1, 1001, 130), (2, 520, 520), (1, 384, 1537), (1, 640, 768), (5, 129, 511)]
+          (1, 255, 256), (1, 1001, 130), (2, 520, 520), (1, 384, 1537), (1, 640, 768), (5, 129, 511),
+          # on chip, by one, two, four and eight CTAs, and just past that
+          (3, 128, 512), (2, 128, 513), (1, 600, 100), (2, 100, 2000), (1, 3000, 33), (2, 128, 4096), (1, 4096, 127),
+          (1, 3, 4090), (1, 129, 512), (1, 128, 4100)]
 
 
 @pytest.mark.parametrize("out_dtype", ["bf16", "f32"])

@@ -82,7 +82,7 @@ def test_orthogonalize_refuses():
                dict(it=0), dict(it=17), dict(x=A + 2), dict(out=A + 2), dict(xd=moe.MOE_BF16),
                dict(out=A + 1, od=moe.MOE_BF16)):
         assert call(**kw) == moe.MOE_ERR_INVALID, kw
-    for kw in (dict(ws=None), dict(ws=A + 8), dict(nbytes=n - 1), dict(rows=300, nbytes=n)):
+    for kw in (dict(ws=None), dict(ws=A + 8), dict(nbytes=n - 1), dict(rows=300, cols=300, nbytes=n)):
         assert call(**kw) == moe.MOE_ERR_WORKSPACE, kw
     for kw in (dict(rows=32769), dict(cols=1 << 20), dict(batch=1 << 24)):
         assert call(**kw) == moe.MOE_ERR_UNSUPPORTED, kw
