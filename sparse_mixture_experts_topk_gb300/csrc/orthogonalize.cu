@@ -43,6 +43,109 @@ namespace {
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;   // the quintic's coefficients
 constexpr float kHeld = 4096.f;                              // factor of every value held in fp16
 
+// ---------------------------------------------------------------- the tensors
+
+// A part of a tensor: matrices of it, which are matrices `first` and on of the
+// ones at hand, up to the next segment's.
+struct Segment {
+  float* p;
+  bf16* p16;
+  const void* g;
+  float* m;
+  void* out;             // raw: receives the result
+  int rows, cols;
+  int first;
+  float keep, step;      // p = p keep - step O
+};
+constexpr int kSegments = 24;
+struct Matrices {
+  Segment seg[kSegments];
+  int n;                 // segments
+  int s, L;              // of X
+  int64_t pitch, plane;  // of X
+  int parts;             // partial sums of a matrix
+  int tiles_s, tiles_L;  // tiles of 64 x 64
+  float mu;              // m = mu m + g, u = g + mu m (nesterov) or m
+  bool nesterov, raw;
+  int out_dtype;
+  const float* grad_scale;
+  const int32_t* skip;
+};
+
+__device__ __forceinline__ const Segment& segment_of(const Matrices& M, int matrix) {
+  int i = 0;
+  while (i + 1 < M.n && M.seg[i + 1].first <= matrix) ++i;
+  return M.seg[i];
+}
+
+// Four elements of fp32 or bf16, of which the first n exist.
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, bool vec, int n, float* v) {
+  if (vec && n == 4) {
+    if (sizeof(T) == 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p);
+      v[0] = q.x;
+      v[1] = q.y;
+      v[2] = q.z;
+      v[3] = q.w;
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
+      const float2 a = __bfloat1622float2(h[0]), b = __bfloat1622float2(h[1]);
+      v[0] = a.x;
+      v[1] = a.y;
+      v[2] = b.x;
+      v[3] = b.y;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, bool vec, int n, const float* v) {
+  if (vec && n == 4) {
+    if (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint2 q;
+      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
+      h[0] = __floats2bfloat162_rn(v[0], v[1]);
+      h[1] = __floats2bfloat162_rn(v[2], v[3]);
+      *reinterpret_cast<uint2*>(p) = q;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) p[i] = from_f32<T>(v[i]);
+}
+__device__ __forceinline__ bool aligned_to(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+// Four elements of p, of which `left` exist, from e on, to go with put4; nothing for raw.
+__device__ __forceinline__ void get4(const Matrices& M, const Segment& S, int64_t e, bool even, int left, float* p) {
+  if (!M.raw) load4(S.p + e, even && aligned_to(S.p + e, 16), left, p);
+}
+// p = p keep - step o there, and its bf16 copy; raw: out = o.
+__device__ __forceinline__ void put4(const Matrices& M, const Segment& S, int64_t e, bool even, int left, const float* p,
+                                     const float* o) {
+  if (M.raw) {
+    if (M.out_dtype == MOE_BF16) {
+      bf16* to = reinterpret_cast<bf16*>(S.out) + e;
+      store4(to, even && aligned_to(to, 8), left, o);
+    } else {
+      float* to = reinterpret_cast<float*>(S.out) + e;
+      store4(to, even && aligned_to(to, 16), left, o);
+    }
+    return;
+  }
+  float v[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) v[x] = p[x] * S.keep - S.step * o[x];
+  store4(S.p + e, even && aligned_to(S.p + e, 16), left, v);
+  if (S.p16) store4(S.p16 + e, even && aligned_to(S.p16 + e, 8), left, v);
+}
+
 // ---------------------------------------------------------------- products
 
 constexpr int kBM = 128;                  // operand rows (or columns) per CTA
@@ -171,9 +274,60 @@ __device__ __forceinline__ bool wait_written(const int* counter, int need, volat
   }
 }
 
+// 32 rows and 64 columns of the result, from (row0, col) of X on, to the
+// tensor, by one warp: turned through its buffer so that the lanes' accesses lie
+// along the tensor's rows.  packed: this lane's row, as held.
+__device__ __forceinline__ void finish(const Matrices& M, const Segment& S, int64_t base, uint8_t* buf,
+                                       const uint32_t (&packed)[2][16], int row0, int col, int lane) {
+  const bool flip = S.rows > S.cols, even = S.cols % 4 == 0;
+  __half* tile = reinterpret_cast<__half*>(buf);
+  __syncwarp();   // the lanes have read the tile before
+  if (flip) {
+    // 64 rows of 32 of the tensor; 8 bytes of a row exchanged by its number
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+      reinterpret_cast<uint16_t*>(tile)[j * 32 + ((((lane >> 2) ^ (j & 7)) << 2) | (lane & 3))] =
+          (uint16_t)(packed[j >> 5][(j & 31) >> 1] >> (16 * (j & 1)));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)   // 32 rows of 64; 16 bytes of a row exchanged by its number
+      *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+          make_uint4(packed[j >> 2][j % 4 * 4], packed[j >> 2][j % 4 * 4 + 1], packed[j >> 2][j % 4 * 4 + 2],
+                     packed[j >> 2][j % 4 * 4 + 3]);
+  }
+  __syncwarp();
+  // four elements of a row to a lane, 16 or 8 lanes to a row; eight loads in flight
+#pragma unroll 1
+  for (int i0 = 0; i0 < 16; i0 += 8) {
+    float p[8][4];
+    int64_t e[8];
+    int left[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = (i0 + i) * 32 + lane, r = flip ? at / 8 : at / 16, x = flip ? at % 8 : at % 16;
+      const int tr = (flip ? col : row0) + r, tc = (flip ? row0 : col) + x * 4;
+      left[i] = tr < S.rows ? min(4, S.cols - tc) : 0;
+      e[i] = base + (int64_t)tr * S.cols + tc;
+      if (left[i] > 0) get4(M, S, e[i], even, left[i], p[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (left[i] <= 0) continue;
+      const int at = (i0 + i) * 32 + lane, r = flip ? at / 8 : at / 16, x = flip ? at % 8 : at % 16;
+      const uint2 u = *reinterpret_cast<const uint2*>(
+          buf + (flip ? r * 64 + ((x ^ (r & 7)) << 3) : r * 128 + (((x >> 1) ^ (r & 7)) << 4) + (x & 1) * 8));
+      const __half2* h = reinterpret_cast<const __half2*>(&u);
+      const float2 a = __half22float2(h[0]), b = __half22float2(h[1]);
+      const float o[4] = {a.x * (1.f / kHeld), a.y * (1.f / kHeld), b.x * (1.f / kHeld), b.y * (1.f / kHeld)};
+      put4(M, S, e[i], even, left[i], p[i], o);
+    }
+  }
+}
+
 // kPair: tiles of 256 x 256 on the two CTAs of a cluster, else of 128 x 128.
 template <bool kPair>
-__global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constant__ Chain C) {
+__global__ void __launch_bounds__(kThreads, 1)
+chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M) {
   constexpr int kTile = kPair ? 256 : 128, kCtas = kPair ? 2 : 1;
   constexpr int kChunks = kTile / 128;   // of 64 columns, for each of a lane quarter's two epilogue warps
   constexpr uint32_t kTmemCols = 2 * kTile;
@@ -405,6 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         // The tile leaves through shared memory by TMA, which writes what lies
         // inside the matrix; stored by its threads, a row each and the mirrored
         // elements one by one, a short product's tile took longer than its MMAs.
+        if (T.p == C.steps - 1) {
+          // the result goes straight to the tensor
+          const Segment& D = segment_of(M, T.matrix);
+          finish(M, D, (int64_t)(T.matrix - D.first) * D.rows * D.cols, mine, packed, row0, col, lane);
+          continue;
+        }
         if (lane == 0) tc::bulk_wait_read();   // the buffer's previous store has been read
         __syncwarp();
 #pragma unroll
@@ -426,11 +586,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
           if (lane == 0) tc::tma_store_3d(&C.mirror[S.out], buf, row0, col, T.matrix);
         }
       }
-      if (lane == 0) {
+      if (lane == 0 && T.p < C.steps - 1) {
         tc::bulk_wait_all();   // written, and ...
         asm volatile("fence.proxy.async.global;" ::: "memory");
-        __threadfence();       // ... before the count
-        atomicAdd(C.written + (int64_t)T.p * C.batch + T.matrix, 1);
+        // ... before the count
+        asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(C.written + (int64_t)T.p * C.batch + T.matrix)
+                     : "memory");
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
@@ -464,10 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   }
 }
 
-// The steps of `iterations`; X ends in kX or kY, which is returned.  In pairs:
+// The steps of `iterations`; the last one's result goes to the tensor.  In pairs:
 // with B1 and A1 = (B1 A) B1 the next A without X, and X <- (B2 B1) X once for
 // two iterations, three more products of s x s for one X X^T and one B X less.
-Buffer plan_steps(Chain& C, int iterations, bool pairs) {
+void plan_steps(Chain& C, int iterations, bool pairs) {
   const float back = 1.f / kHeld;   // what is held is 2^12 times the value: a product of two comes out 2^24 times
   Buffer X = kX, Y = kY;
   int n = 0;
@@ -494,11 +655,10 @@ Buffer plan_steps(Chain& C, int iterations, bool pairs) {
     ++i;
   }
   C.steps = n;
-  return X;
 }
 
 template <bool kPair>
-cudaError_t launch_chain(Chain& C, int64_t tiles, cudaStream_t st) {
+cudaError_t launch_chain(Chain& C, const Matrices& M, int64_t tiles, cudaStream_t st) {
   constexpr int kCtas = kPair ? 2 : 1;
   const int64_t most = sm_count() / kCtas, ctas = tiles < most ? tiles : most;
   const int64_t stages = (C.L + kBK - 1) / kBK;
@@ -506,87 +666,10 @@ cudaError_t launch_chain(Chain& C, int64_t tiles, cudaStream_t st) {
   auto kern = chain_kernel<kPair>;
   const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (r != cudaSuccess) return r;
-  return launch_kernel(kern, dim3((unsigned)(kCtas * ctas)), dim3(kThreads), kSmem, st, kCtas, C);
+  return launch_kernel(kern, dim3((unsigned)(kCtas * ctas)), dim3(kThreads), kSmem, st, kCtas, C, M);
 }
 
-// ---------------------------------------------------------------- what surrounds them
-
-// A part of a tensor: matrices of it, which are matrices `first` and on of the
-// ones at hand, up to the next segment's.
-struct Segment {
-  float* p;
-  bf16* p16;
-  const void* g;
-  float* m;
-  void* out;             // raw: receives the result
-  int rows, cols;
-  int first;
-  float keep, step;      // p = p keep - step O
-};
-constexpr int kSegments = 24;
-struct Matrices {
-  Segment seg[kSegments];
-  int n;                 // segments
-  int s, L;              // of X
-  int64_t pitch, plane;  // of X
-  int parts;             // partial sums of a matrix
-  int tiles_s, tiles_L;  // tiles of 64 x 64
-  float mu;              // m = mu m + g, u = g + mu m (nesterov) or m
-  bool nesterov, raw;
-  int out_dtype;
-  const float* grad_scale;
-  const int32_t* skip;
-};
-
-__device__ __forceinline__ const Segment& segment_of(const Matrices& M, int matrix) {
-  int i = 0;
-  while (i + 1 < M.n && M.seg[i + 1].first <= matrix) ++i;
-  return M.seg[i];
-}
-
-// Four elements of fp32 or bf16, of which the first n exist.
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, bool vec, int n, float* v) {
-  if (vec && n == 4) {
-    if (sizeof(T) == 4) {
-      const float4 q = *reinterpret_cast<const float4*>(p);
-      v[0] = q.x;
-      v[1] = q.y;
-      v[2] = q.z;
-      v[3] = q.w;
-    } else {
-      const uint2 q = *reinterpret_cast<const uint2*>(p);
-      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
-      const float2 a = __bfloat1622float2(h[0]), b = __bfloat1622float2(h[1]);
-      v[0] = a.x;
-      v[1] = a.y;
-      v[2] = b.x;
-      v[3] = b.y;
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
-}
-template <typename T>
-__device__ __forceinline__ void store4(T* p, bool vec, int n, const float* v) {
-  if (vec && n == 4) {
-    if (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-      uint2 q;
-      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
-      h[0] = __floats2bfloat162_rn(v[0], v[1]);
-      h[1] = __floats2bfloat162_rn(v[2], v[3]);
-      *reinterpret_cast<uint2*>(p) = q;
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < n) p[i] = from_f32<T>(v[i]);
-}
-__device__ __forceinline__ bool aligned_to(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) == 0; }
+// ---------------------------------------------------------------- before the products
 
 // Sums of squares that neither overflow nor vanish: of u, and of u 2^-90 and u 2^90.
 struct Squares {
@@ -769,76 +852,6 @@ build_kernel(const __grid_constant__ Matrices M, const float2* __restrict__ fact
 #pragma unroll
     for (int x = 0; x < 4; ++x) v[x] = tile[x4 + x][y + 16 * i];
     *reinterpret_cast<uint2*>(out + (int64_t)r * M.pitch + c) = pack_half4(v);
-  }
-}
-
-// Four elements, of which `left` exist, from e on: p = p keep - step O, and its bf16 copy; raw: out = O.
-__device__ __forceinline__ void put4(const Matrices& M, const Segment& S, int64_t e, bool even, int left, const float* o) {
-  if (M.raw) {
-    if (M.out_dtype == MOE_BF16) {
-      bf16* to = reinterpret_cast<bf16*>(S.out) + e;
-      store4(to, even && aligned_to(to, 8), left, o);
-    } else {
-      float* to = reinterpret_cast<float*>(S.out) + e;
-      store4(to, even && aligned_to(to, 16), left, o);
-    }
-    return;
-  }
-  float* p = S.p + e;
-  const bool vp = even && aligned_to(p, 16);
-  float v[4];
-  load4(p, vp, left, v);
-#pragma unroll
-  for (int x = 0; x < 4; ++x) v[x] = v[x] * S.keep - S.step * o[x];
-  store4(p, vp, left, v);
-  if (S.p16) store4(S.p16 + e, even && aligned_to(S.p16 + e, 8), left, v);
-}
-
-// The result from X.
-__global__ void __launch_bounds__(256)
-apply_kernel(const __grid_constant__ Matrices M, const __half* __restrict__ X) {
-  __shared__ float tile[64][65];
-  pdl_enter();
-  if (M.skip && *M.skip) return;
-  const Place at = place_of(M);
-  const Segment& S = *at.S;
-  const int64_t base = (int64_t)(at.matrix - S.first) * S.rows * S.cols;
-  const __half* in = X + (int64_t)at.matrix * M.plane;
-  const int x4 = threadIdx.x % 16 * 4, y = threadIdx.x / 16;
-  auto held4 = [&](int r, int c, float* v) {   // 4 elements of X; the pitch is a multiple of 8
-    const uint2 q = r < M.s && c < M.L ? *reinterpret_cast<const uint2*>(in + (int64_t)r * M.pitch + c)
-                                       : make_uint2(0u, 0u);
-    const __half2* h = reinterpret_cast<const __half2*>(&q);
-    const float2 a = __half22float2(h[0]), b = __half22float2(h[1]);
-    v[0] = a.x * (1.f / kHeld);
-    v[1] = a.y * (1.f / kHeld);
-    v[2] = b.x * (1.f / kHeld);
-    v[3] = b.y * (1.f / kHeld);
-  };
-  if (at.flip) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[4];
-      held4(at.c0 + y + 16 * i, at.r0 + x4, v);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) tile[x4 + x][y + 16 * i] = v[x];
-    }
-    __syncthreads();
-  }
-  const bool even = S.cols % 4 == 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = at.r0 + y + 16 * i, c = at.c0 + x4;
-    const int left = r < S.rows && c < S.cols ? min(4, S.cols - c) : 0;
-    if (left <= 0) continue;
-    float o[4];
-    if (at.flip) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] = tile[y + 16 * i][x4 + x];
-    } else {
-      held4(r, c, o);
-    }
-    put4(M, S, base + (int64_t)r * S.cols + c, even, left, o);
   }
 }
 
@@ -1156,7 +1169,9 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
         v[2] = y.x * back;
         v[3] = y.y * back;
       }
-      put4(M, S, first + o, even, left, v);
+      float p[4];
+      get4(M, S, first + o, even, left, p);
+      put4(M, S, first + o, even, left, p, v);
     });
   }
   if (ctas > 1) tc::cluster_sync();   // no CTA leaves while another may still read its shared memory
@@ -1272,7 +1287,7 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
   // Two iterations at a time where the products with X are longer by enough and
   // the short ones fill the SMs.
   const bool pairs = 4 * (int64_t)z.L >= 5 * (int64_t)z.s && pair && tiles_of(256, false) >= sms / 2;
-  const Buffer result = plan_steps(C, iterations, pairs);
+  plan_steps(C, iterations, pairs);
   const dim3 sums((unsigned)(n * z.parts)), tiles((unsigned)((int64_t)n * M.tiles_s * M.tiles_L)), threads(256);
   cudaError_t e = grad_bf16 ? launch_kernel(momentum_kernel<bf16>, sums, threads, 0, st, 1, M, part)
                             : launch_kernel(momentum_kernel<float>, sums, threads, 0, st, 1, M, part);
@@ -1281,9 +1296,7 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
     e = grad_bf16 ? launch_kernel(build_kernel<bf16>, tiles, threads, 0, st, 1, M, factor, C.buf[kX])
                   : launch_kernel(build_kernel<float>, tiles, threads, 0, st, 1, M, factor, C.buf[kX]);
   if (e != cudaSuccess) return e;
-  e = pair ? launch_chain<true>(C, pair_tiles, st) : launch_chain<false>(C, single_tiles, st);
-  if (e == cudaSuccess) e = launch_kernel(apply_kernel, tiles, threads, 0, st, 1, M, C.buf[result]);
-  return e;
+  return pair ? launch_chain<true>(C, M, pair_tiles, st) : launch_chain<false>(C, M, single_tiles, st);
 }
 
 }  // namespace
