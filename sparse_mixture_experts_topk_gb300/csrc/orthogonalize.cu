@@ -149,11 +149,14 @@ __device__ __forceinline__ void put4(const Matrices& M, const Segment& S, int64_
 // ---------------------------------------------------------------- products
 
 constexpr int kBM = 128;                  // operand rows (or columns) per CTA
-constexpr int kBK = 64;                   // reduction elements per stage
+constexpr int kBox = 64;                  // reduction elements of a box
+constexpr int kSub = 2;                   // boxes of an operand in a stage
+constexpr int kBK = kSub * kBox;          // reduction elements per stage
 constexpr int kGroup = 16;                // reduction elements per MMA
-constexpr int kOperand = kBM * kBK * 2;   // bytes of one operand in a stage
-constexpr int kHalf = kOperand / 2;       // an MN-major operand is two boxes of 64 columns x 64 rows
-constexpr int kStages = 6;
+constexpr int kBlock = kBM * kBox * 2;    // bytes of one operand's box
+constexpr int kOperand = kSub * kBlock;   // and of a stage's
+constexpr int kHalf = kBlock / 2;       // an MN-major operand is two boxes of 64 columns x 64 rows
+constexpr int kStages = 6 / kSub;
 constexpr int kEpiWarps = 8;              // per CTA: two for each quarter of the TMEM lanes
 constexpr int kThreads = 64 + 32 * kEpiWarps + 32, kSecondProducer = 2 + kEpiWarps;
 constexpr int kStoreBytes = 32 * 128;     // an epilogue warp's 32 rows of 64 columns on their way to TMA, or their transpose
@@ -422,11 +425,15 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
             if (kPair) tc::tma_load_3d_pair(dst, map, tc::map_peer(full(stage), 0), c0, c1, T.matrix);
             else tc::tma_load_3d(dst, map, full(stage), c0, c1, T.matrix);
           };
-          if (mn) {
-            load(at, r, kb * kBK);
-            load(at + kHalf, r + 64, kb * kBK);
-          } else {
-            load(at, kb * kBK, r);
+#pragma unroll
+          for (int u = 0; u < kSub; ++u) {
+            const int k = kb * kBK + u * kBox;
+            if (mn) {
+              load(at + u * kBlock, r, k);
+              load(at + u * kBlock + kHalf, r + 64, k);
+            } else {
+              load(at + u * kBlock, k, r);
+            }
           }
           filled |= 1u << stage;
           fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
@@ -469,8 +476,9 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
 #pragma unroll
           for (int g = 0; g < kBK / kGroup; ++g) {
             if (g < ng) {
-              if (kPair) tc::mma_bf16_pair(dst, a + g * as, b + g * bs, idesc, g || kb);
-              else tc::mma_bf16(dst, a + g * as, b + g * bs, idesc, g || kb);
+              const uint32_t sub = g / (kBox / kGroup) * (kBlock >> 4), in = g % (kBox / kGroup);
+              if (kPair) tc::mma_bf16_pair(dst, a + sub + in * as, b + sub + in * bs, idesc, g || kb);
+              else tc::mma_bf16(dst, a + sub + in * as, b + sub + in * bs, idesc, g || kb);
             }
           }
           commit(empty(here));
@@ -1264,7 +1272,7 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
                           x ? C.plane : C.square_plane, kBM) ||
         !tma_map_16bit_3d(&C.store[i], C.buf[i], n, z.s, x ? z.L : z.s, x ? z.pitch : z.square,
                           x ? C.plane : C.square_plane, 32) ||
-        (x && !tma_map_16bit_3d(&C.across[i], C.buf[i], n, z.s, z.L, z.pitch, C.plane, kBK)) ||
+        (x && !tma_map_16bit_3d(&C.across[i], C.buf[i], n, z.s, z.L, z.pitch, C.plane, kBox)) ||
         (!x && !tma_map_16bit_3d(&C.mirror[i], C.buf[i], n, z.s, z.s, z.square, C.square_plane, 64, 32)))
       return cudaErrorNotSupported;
   }
