@@ -18,8 +18,13 @@
 // tile (every four above 128 experts), small parts first, and the epilogue adds
 // it to sums in registers, which leave as partial ones when the chunk ends for
 // this CTA; a last kernel adds those of a chunk in order.  D2 is double-buffered
-// and leaves through shared memory by TMA.  The (chunk, tile) pairs are dealt
-// out evenly, chunk by chunk, in one stretch for each CTA.
+// and leaves through shared memory by TMA.
+//
+// CTA b has chunk b mod chunks and every splits-th tile, so that the CTAs
+// running at one time read whole rows of the same few tiles, and padding at
+// the sequences' ends is shared out.  (Dealt out chunk by chunk, evenly over
+// all SMs, the prefill layer's products took 6 us more: pieces of 256 bytes of
+// rows far apart.)
 //
 // Roles: warp 0 producer of x and Wg, warp 1 of the panels, warp 2 MMA issuer,
 // warp 3 zeroes the rows of tokens that the mask leaves out (0 x NaN is NaN),
@@ -70,30 +75,26 @@ struct Params {
   int64_t T;
   int tiles, chunks;
   int E, H;
-  float* part;     // [CTAs + chunks (packed: twice), E, 128] or null: no dWg
+  float* part;     // [CTAs (packed: twice), E, 128] or null: no dWg
   bool dx_on;
   int* err;
 };
 
-// First item of CTA i of n items dealt to g CTAs.
-__host__ __device__ inline int64_t item_begin(int64_t i, int64_t n, int64_t g) { return i * n / g; }
-
-// A CTA's (chunk, tile) pairs in order; 64-bit divisions once, not at each.
-// kFlags: bytes for a tile that say whether a token of it counts (0: all do).
-// Those of the next tile are on their way while one is worked on.
+// A CTA's tiles: `first` and every step-th after it.  kFlags: bytes for a tile
+// that say whether a token of it counts (0: all do); those of the next tile are
+// on their way while one is worked on.
 template <int kFlags>
 struct Walk {
-  int64_t left;
-  int chunk, tile, tiles;
+  int tile, step, tiles, n;   // n: tiles before this one
   const uint8_t* alive;
   bool live, ahead;
-  __device__ Walk(int64_t first, int64_t last, int n, const uint8_t* flags)
-      : left(last - first), chunk((int)(first / n)), tile((int)(first % n)), tiles(n), alive(flags) {
+  __device__ Walk(int first, int every, int count, const uint8_t* flags)
+      : tile(first), step(every), tiles(count), n(0), alive(flags) {
     live = read(tile);
-    ahead = read(tile + 1 == tiles ? 0 : tile + 1);
+    ahead = read(tile + step);
   }
   __device__ bool read(int t) const {
-    if (kFlags == 0 || !alive) return true;
+    if (kFlags == 0 || !alive || t >= tiles) return true;
     const uint8_t* p = alive + (int64_t)t * kFlags;
     if (kFlags == 4) return __ldcg(reinterpret_cast<const unsigned*>(p)) != 0;
     if (kFlags == 8) {
@@ -103,18 +104,16 @@ struct Walk {
     const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
     return (v.x | v.y | v.z | v.w) != 0;
   }
+  __device__ bool more() const { return tile < tiles; }
   __device__ void next() {
-    --left;
-    if (++tile == tiles) {
-      tile = 0;
-      ++chunk;
-    }
+    tile += step;
+    ++n;
     live = ahead;
-    if (left > 1) ahead = read(tile + 1 == tiles ? 0 : tile + 1);
+    ahead = read(tile + step);
   }
-  // whether the CTA leaves the chunk, and with it the tokens of a run of tiles, after this pair
-  __device__ bool leaves() const { return left == 1 || tile + 1 == tiles; }
-  __device__ bool ends(int run) const { return leaves() || (tile + 1) % run == 0; }
+  __device__ bool last() const { return tile + step >= tiles; }
+  // whether a run of tiles is complete after this one
+  __device__ bool ends(int run) const { return last() || (n + 1) % run == 0; }
 };
 
 struct Ring {
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   auto p_full = [&](int s) { return bars + 8 * (3 * kMaxX + s); };
   auto p_empty = [&](int s) { return bars + 8 * (3 * kMaxX + kMaxPanels + s); };
   const uint32_t more = bars + 8 * (3 * kMaxX + 2 * kMaxPanels);
-  const uint32_t w_full = more, w_empty = more + 8, done = more + 16;
+  const uint32_t w_full = more, done = more + 16;
   auto d1_full = [&](int a) { return more + 24 + 8 * a; };
   auto d1_empty = [&](int a) { return more + 40 + 8 * a; };
   auto d2_full = [&](int a) { return more + 56 + 8 * a; };
@@ -175,7 +174,6 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
         tc::mbar_init(p_empty(s), 1);
       }
       tc::mbar_init(w_full, 1);
-      tc::mbar_init(w_empty, 1);
       for (int a = 0; a < 2; ++a) {
         tc::mbar_init(d1_full(a), 1);
         tc::mbar_init(d1_empty(a), kEpiWarps);
@@ -194,17 +192,21 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  pdl_enter();
+  // What was on the stream before the call is complete: the kernel before
+  // lets this one start only then.  x and Wg need no more, the rest waits for
+  // that kernel.
+  if (warp != 0 || P.alive) pdl_wait();
+  pdl_trigger();
   const uint32_t tmem = s_tmem;
-  const int64_t items = (int64_t)P.tiles * P.chunks;
-  const int64_t first = item_begin(blockIdx.x, items, gridDim.x), last = item_begin(blockIdx.x + 1, items, gridDim.x);
+  const int chunk = blockIdx.x % P.chunks, h0 = chunk * kCols;
+  const int first = blockIdx.x / P.chunks, splits = gridDim.x / P.chunks;
   const bool dwg = P.part != nullptr;
   constexpr int kRun = kGroups <= 2 ? 1 : 4;   // tiles that D1 sums
   // a tile none of whose tokens counts is not loaded; sums of several tiles take each
   constexpr int kFlags = kRun > 1 ? 0 : kGroups == 2 ? 16 : kPacked ? 4 : 8;
   const uint8_t* alive = kFlags ? P.alive : nullptr;
   // the producers' copies: stages filled and the parity of each one's latest
-  uint32_t filled = 0, fill_par = 0, w_phase = 0;
+  uint32_t filled = 0, fill_par = 0;
   bool w_loaded = false;
 
   if (warp == 0) {
@@ -212,21 +214,15 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     if (tc::elect_one()) {
       Ring r(plan.nx);
       bool ok = true;
-      int chunk = -1;
-      for (Walk<kFlags> w(first, last, P.tiles, alive); w.left > 0 && ok; w.next()) {
-        const int c = w.chunk, t0 = w.tile * kTok, h0 = c * kCols;
-        if (P.dx_on && c != chunk) {
-          ok = tc::mbar_wait(w_empty, w_phase ^ 1u, &s_abort, kWaitNs);
-          if (!ok) break;
-          tc::mbar_arrive_expect_tx(w_full, (uint32_t)plan.wg_bytes());
-          for (int half = 0; half < 2; ++half)
-            for (int e = 0; e < kGroups * 64; e += 32)
-              tc::tma_load_2d(sW + half * kGroups * 64 * 128 + e * 128, &P.wg, w_full, h0 + half * 64,
-                              kPacked ? 0 : e);
-          w_phase ^= 1u;
-          w_loaded = true;
-        }
-        chunk = c;
+      if (P.dx_on) {
+        tc::mbar_arrive_expect_tx(w_full, (uint32_t)plan.wg_bytes());
+        for (int half = 0; half < 2; ++half)
+          for (int e = 0; e < kGroups * 64; e += 32)
+            tc::tma_load_2d(sW + half * kGroups * 64 * 128 + e * 128, &P.wg, w_full, h0 + half * 64, kPacked ? 0 : e);
+        w_loaded = true;
+      }
+      for (Walk<kFlags> w(first, splits, P.tiles, alive); w.more() && ok; w.next()) {
+        const int t0 = w.tile * kTok;
         if (!dwg || !w.live) continue;
         ok = tc::mbar_wait(x_empty(r.at), r.phase ^ 1u, &s_abort, kWaitNs);
         if (!ok) break;
@@ -244,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     if (tc::elect_one()) {
       Ring r(plan.np);
       bool ok = true;
-      for (Walk<kFlags> w(first, last, P.tiles, alive); w.left > 0 && ok; w.next()) {
+      for (Walk<kFlags> w(first, splits, P.tiles, alive); w.more() && ok; w.next()) {
         const int t0 = w.tile * kTok;
         for (int p = 0; p < plan.panels && w.live; ++p) {
           ok = tc::mbar_wait(p_empty(r.at), r.phase ^ 1u, &s_abort, kWaitNs);
@@ -275,22 +271,14 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
       const uint64_t w0 = sdesc_mn(sW, kGroups * 64 * 128);
       const bool dx_on = P.dx_on, clean = P.mask != nullptr;
       auto x_bar = [&](int at) { return clean ? x_clean(at) : x_full(at); };
-      int chunk = -1;
-      bool ok = true, begins = true;   // begins: D1 with this pair
+      bool begins = true;   // D1 with this tile
+      bool ok = !dx_on || tc::mbar_wait(w_full, 0, &s_abort, kWaitNs);
       bool x_ready = false, p_ready = false, d1_ready = false, d2_ready = false;
 #pragma unroll 1
-      for (Walk<kFlags> w(first, last, P.tiles, alive); w.left > 0 && ok; w.next()) {
+      for (Walk<kFlags> w(first, splits, P.tiles, alive); w.more() && ok; w.next()) {
         const bool fresh = begins;
         begins = w.ends(kRun);
-        if (dx_on && w.chunk != chunk) {
-          ok = tc::mbar_wait(w_full, w_phase, &s_abort, kWaitNs);
-          w_phase ^= 1u;
-        }
-        chunk = w.chunk;
-        if (!w.live) {
-          if (dx_on && w.leaves()) tc::tc_commit(w_empty);
-          continue;
-        }
+        if (!w.live) continue;
         if (dwg) {
           if (ok && fresh && !d1_ready) ok = tc::mbar_wait(d1_empty(d1.at), d1.phase ^ 1u, &s_abort, kWaitNs);
           if (ok && !x_ready) ok = tc::mbar_wait(x_bar(x.at), x.phase, &s_abort, kWaitNs);
@@ -344,7 +332,6 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
         }
         if (dx_on) {
           tc::tc_commit(d2_full(d2_at));
-          if (w.leaves()) tc::tc_commit(w_empty);
         }
       }
       if (!ok) give_up(P.err, &s_abort);
@@ -363,15 +350,15 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
           on[k] = t < P.T ? P.mask[t] : 1;
         }
       };
-      Walk<kFlags> w(first, last, P.tiles, alive);
+      Walk<kFlags> w(first, splits, P.tiles, alive);
       fetch(w.tile);
-      while (w.left > 0) {
+      while (w.more()) {
         uint32_t out[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) out[k] = __ballot_sync(0xffffffffu, !on[k]);
         const bool live = w.live;
         w.next();
-        if (w.left > 0) fetch(w.tile);
+        if (w.more()) fetch(w.tile);
         if (!live) continue;
         if (!__all_sync(0xffffffffu, tc::mbar_wait(x_full(x.at), x.phase, &s_abort, kWaitNs))) {
           if (lane == 0) give_up(P.err, &s_abort);
@@ -408,8 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     Ring d1(plan.bufs), d2(2);
     float sum[kGroups * 32] = {};   // of column half * 32 + j of each group: this thread's column of x
     bool ok = true;
-    for (Walk<kFlags> w(first, last, P.tiles, alive); w.left > 0 && ok; w.next()) {
-      const int c = w.chunk;
+    for (Walk<kFlags> w(first, splits, P.tiles, alive); w.more() && ok; w.next()) {
       if (P.dx_on) {
         const int64_t t0 = (int64_t)w.tile * kTok + q * 32;
         uint32_t r[2][32] = {};
@@ -439,8 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && t0 < P.T && c * kCols + half * 64 < P.H)
-          tc::tma_store_2d(&P.dx, buf, c * kCols + half * 64, (int)t0);
+        if (lane == 0 && t0 < P.T && h0 + half * 64 < P.H)
+          tc::tma_store_2d(&P.dx, buf, h0 + half * 64, (int)t0);
       }
       if (dwg && w.live && w.ends(kRun)) {
         ok = __all_sync(0xffffffffu, tc::mbar_wait(d1_full(d1.at), d1.phase, &s_abort, kWaitNs));
@@ -459,16 +445,15 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
         if (lane == 0) tc::mbar_arrive(d1_empty(d1.at));
         d1.next();
       }
-      if (dwg && w.leaves()) {
-        // up to 32 experts both halves have sums of the same experts: a row each
-        const int64_t slot = ((int64_t)blockIdx.x + c) * (kPacked ? 2 : 1) + (kPacked ? half : 0);
-        float* out = P.part + slot * P.E * kCols + q * 32 + lane;
+    }
+    if (ok && dwg) {
+      // up to 32 experts both halves have sums of the same experts: a row each
+      const int64_t slot = ((int64_t)chunk * splits + first) * (kPacked ? 2 : 1) + (kPacked ? half : 0);
+      float* out = P.part + slot * P.E * kCols + q * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < kGroups * 32; ++j) {
-          const int e = kPacked ? j : j / 32 * 64 + half * 32 + j % 32;
-          if (e < P.E) out[(int64_t)e * kCols] = sum[j];
-          sum[j] = 0.f;
-        }
+      for (int j = 0; j < kGroups * 32; ++j) {
+        const int e = kPacked ? j : j / 32 * 64 + half * 32 + j % 32;
+        if (e < P.E) out[(int64_t)e * kCols] = sum[j];
       }
     }
     if (!ok && lane == 0) give_up(P.err, &s_abort);
@@ -478,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   tc::tc_fence_before();
   __syncthreads();
   if (s_abort && (filled || w_loaded)) {   // the producing threads: every copy lands before the CTA leaves
-    if (w_loaded) tc::mbar_wait(w_full, w_phase ^ 1u, nullptr, kWaitNs);
+    if (w_loaded) tc::mbar_wait(w_full, 0, nullptr, kWaitNs);
     for (int s = 0; s < (warp == 0 ? plan.nx : plan.np); ++s)
       if ((filled >> s) & 1u) tc::mbar_wait(warp == 0 ? x_full(s) : p_full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
   }
@@ -491,30 +476,20 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   }
 }
 
-// dWg: the partial sums of a chunk's CTAs in their order; the last blocks: the
+// dWg: a chunk's rows of partial sums in their order; the last blocks: the
 // bias' gradient, the rows of partial sums in order.
 __global__ void __launch_bounds__(256)
-gate_sums_kernel(const float* __restrict__ part, int tiles, int chunks, int ctas, int E, int H,
+gate_sums_kernel(const float* __restrict__ part, int rows, int chunks, int E, int H,
                  float* __restrict__ dWg, const float* __restrict__ part_b, int rows_b, float* __restrict__ dbias) {
   pdl_enter();
   const int c = blockIdx.x;
   if (c < chunks) {
-    const int64_t items = (int64_t)tiles * chunks;
-    // the first CTA whose pairs end after pair a
-    auto first_after = [&](int64_t a) {
-      int64_t i = a * ctas / items;
-      while (i > 0 && item_begin(i, items, ctas) > a) --i;
-      while (item_begin(i + 1, items, ctas) <= a) ++i;
-      return (int)i;
-    };
-    const int n = Plan(E).packed ? 2 : 1;
-    const int i0 = first_after((int64_t)c * tiles), i1 = first_after((int64_t)c * tiles + tiles - 1);
     const int e = blockIdx.y * 8 + threadIdx.x / 32, h = c * kCols + threadIdx.x % 32 * 4;
     if (e >= E || h >= H) return;   // H is a multiple of 8
-    const float* p = part + ((int64_t)(i0 + c) * n * E + e) * kCols + threadIdx.x % 32 * 4;
+    const float* p = part + ((int64_t)c * rows * E + e) * kCols + threadIdx.x % 32 * 4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int k = (i1 - i0 + 1) * n; k > 0; --k, p += (int64_t)E * kCols) {
+    for (int k = rows; k > 0; --k, p += (int64_t)E * kCols) {
       const float4 v = *reinterpret_cast<const float4*>(p);
       s.x += v.x;
       s.y += v.y;
@@ -540,9 +515,14 @@ gate_sums_kernel(const float* __restrict__ part, int tiles, int chunks, int ctas
 
 }  // namespace
 
+// CTAs of a chunk.
+static int64_t gate_splits(const Shape& s) {
+  const int64_t n = sm_count() / ((s.H + kCols - 1) / kCols), tiles = (s.T + kTok - 1) / kTok, most = n < 1 ? 1 : n;
+  return tiles < most ? (tiles < 1 ? 1 : tiles) : most;
+}
 int64_t gate_part_floats(const Shape& s) {
   const int64_t chunks = (s.H + kCols - 1) / kCols;
-  return ((int64_t)sm_count() + chunks) * (Plan(s.E).packed ? 2 : 1) * s.E * kCols;
+  return chunks * gate_splits(s) * (Plan(s.E).packed ? 2 : 1) * s.E * kCols;
 }
 int gate_panel_cols(int E) { return Plan(E).panels * 64; }
 
@@ -550,8 +530,7 @@ cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* 
                            const float* part_b, int rows_b, int* err, cudaStream_t st) {
   const Plan plan(s.E);
   const int64_t tiles = (s.T + kTok - 1) / kTok, chunks = (s.H + kCols - 1) / kCols;
-  const int sms = sm_count();
-  const int ctas = (int)(tiles * chunks < sms ? tiles * chunks : sms);
+  const int splits = (int)gate_splits(s);
   cudaError_t e = cudaSuccess;
   if (b.dx || b.dWg) {
     Params P = {};
@@ -577,12 +556,12 @@ cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* 
                                    : gate_kernel<4, false>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem());
     if (e != cudaSuccess) return e;
-    e = launch_kernel(kern, dim3((unsigned)ctas), dim3(kThreads), plan.smem(), st, 1, P);
+    e = launch_kernel(kern, dim3((unsigned)(splits * chunks)), dim3(kThreads), plan.smem(), st, 1, P);
   }
   if (e == cudaSuccess && (b.dWg || b.dbias)) {
     const int cols = b.dWg ? (int)chunks : 0;
     e = launch_kernel(gate_sums_kernel, dim3((unsigned)(cols + (b.dbias ? 1 : 0)), (unsigned)((s.E + 7) / 8)), dim3(256),
-                      0, st, 1, part, (int)tiles, cols, ctas, s.E, s.H, b.dWg, part_b, rows_b, b.dbias);
+                      0, st, 1, part, splits * (plan.packed ? 2 : 1), cols, s.E, s.H, b.dWg, part_b, rows_b, b.dbias);
   }
   return e;
 }

@@ -210,7 +210,7 @@ def test_router_gradient_is_deterministic_and_each_result_alone_is_the_same(kind
     c = case(700, 392, 40, 3, kind[:4].rstrip("_"), mask=True, seed=6)
     flags = moe.MOE_FLAG_SIMT_ROUTER if kind == "bf16_simt" else 0
     first = run_backward(c, flags=flags)
-    ws = moe.router_backward_workspace(c["desc"])
+    ws = moe.router_backward_workspace(moe.make_desc(700, 392, 40, 3, 8, dtype=c["desc"].dtype, flags=flags))
     for _ in range(2):
         again = run_backward(c, flags=flags, ws=ws)
         for k in first:
