@@ -15,7 +15,7 @@
 // so the same panel in shared memory serves both.  The tensor cores' fp32 sums
 // round towards zero, half a last place low each on average: over all of a
 // CTA's tokens dWg would be 1e-4 small (32768 tokens).  So D1 starts anew every
-// tile (every four above 128 experts), small parts first, and the epilogue adds
+// tile (every four above 128 experts), the small parts apart or first, and the epilogue adds
 // it to sums in registers, which leave as partial ones when the chunk ends for
 // this CTA; a last kernel adds those of a chunk in order.  D2 is double-buffered
 // and leaves through shared memory by TMA.
@@ -50,22 +50,26 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kStoreBytes = 32 * 128;         // an epilogue warp's 32 rows of 64 columns
 constexpr int kOut = kEpiWarps * kStoreBytes;
 constexpr int kMaxX = 3, kMaxPanels = 5;
-constexpr uint32_t kD2 = 256;                 // TMEM columns: D1 at 0 (and 128), D2 twice 128
 constexpr int kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// How E experts are held: `groups` of 64 columns of D1; panels of a tile.
+// How E experts are held: `groups` of 64 columns of D1; panels of a tile, `per`
+// of them in a slot of the ring.  Up to 32 experts a slot holds a tile's two
+// panels and one MMA takes both: its operand x is read from shared memory once
+// for 128 columns instead of for 64 (prefill layer 30.9 -> 28.9 us).  For 64
+// experts the three panels in a slot leave room for two tiles of x only (104.7
+// instead of 102.7 us for 32768 padded tokens), so slots hold one.
 struct Plan {
   int E, groups, panels;
   bool packed;      // up to 32 experts: panels [high | middle] and [low | 0]
-  int nx, np;       // ring sizes
+  int per, nx, np;  // ring sizes: tiles of x, slots of panels
   int bufs;         // buffers of D1
   __host__ __device__ explicit Plan(int e)
       : E(e), groups((e + 63) / 64), panels(e <= 32 ? 2 : 3 * ((e + 63) / 64)), packed(e <= 32),
-        nx(e <= 128 ? 3 : 2), np(e <= 64 || (e > 128 && e <= 192) ? 5 : 4),
-        bufs(e <= 128 ? 2 : 1) {}
+        per(e <= 32 ? 2 : 1), nx(e <= 128 ? 3 : 2),
+        np(e <= 32 ? 2 : e <= 64 || (e > 128 && e <= 192) ? 5 : 4), bufs(e <= 128 ? 2 : 1) {}
   __host__ __device__ int wg_bytes() const { return groups * 2 * 64 * 128; }
-  size_t smem() const { return 1024 + (size_t)wg_bytes() + nx * kXBytes + np * kHalf + kOut; }
+  size_t smem() const { return 1024 + (size_t)wg_bytes() + nx * kXBytes + np * per * kHalf + kOut; }
 };
 
 struct Params {
@@ -148,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   __shared__ __align__(8) uint64_t s_bar[3 * kMaxX + 2 * kMaxPanels + 11];
   const Plan plan(P.E);
   const uint32_t sW = (tc::smem_u32(smem_raw) + 1023u) & ~1023u, sX = sW + plan.wg_bytes();
-  const uint32_t sP = sX + plan.nx * kXBytes, sOut = sP + plan.np * kHalf;
+  const uint32_t sP = sX + plan.nx * kXBytes, sOut = sP + plan.np * plan.per * kHalf;
   const uint32_t bars = tc::smem_u32(s_bar);
   auto x_full = [&](int s) { return bars + 8 * s; };
   auto x_clean = [&](int s) { return bars + 8 * (kMaxX + s); };      // masked rows zeroed
@@ -203,6 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   const bool dwg = P.part != nullptr;
   constexpr int kRun = kGroups <= 2 ? 1 : 4;   // tiles that D1 sums
   // a tile none of whose tokens counts is not loaded; sums of several tiles take each
+  constexpr int kPer = kPacked ? 2 : 1, kSlot = kPer * kHalf;
+  constexpr int kD2 = 256;   // TMEM columns: D1 at 0 (and 128), D2 twice 128
   constexpr int kFlags = kRun > 1 ? 0 : kGroups == 2 ? 16 : kPacked ? 4 : 8;
   const uint8_t* alive = kFlags ? P.alive : nullptr;
   // the producers' copies: stages filled and the parity of each one's latest
@@ -242,13 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
       bool ok = true;
       for (Walk<kFlags> w(first, splits, P.tiles, alive); w.more() && ok; w.next()) {
         const int t0 = w.tile * kTok;
-        for (int p = 0; p < plan.panels && w.live; ++p) {
+        for (int p = 0; p < plan.panels && w.live; p += kPer) {
           ok = tc::mbar_wait(p_empty(r.at), r.phase ^ 1u, &s_abort, kWaitNs);
           if (!ok) break;
-          tc::mbar_arrive_expect_tx(p_full(r.at), kHalf);
-          // the low parts first
-          tc::tma_load_2d(sP + r.at * kHalf, &P.panel, p_full(r.at),
-                          (kPacked ? 1 - p : (2 - p / kGroups) * kGroups + p % kGroups) * 64, t0);
+          tc::mbar_arrive_expect_tx(p_full(r.at), kSlot);
+          // one by one, the low parts come first
+          const int at = kPacked ? p : (2 - p / kGroups) * kGroups + p % kGroups;
+          for (int u = 0; u < kPer; ++u)
+            tc::tma_load_2d(sP + r.at * kSlot + u * kHalf, &P.panel, p_full(r.at), (at + u) * 64, t0);
           filled |= 1u << r.at;
           fill_par = (fill_par & ~(1u << r.at)) | (r.phase << r.at);
           r.next();
@@ -263,8 +270,8 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
     // issued, and the loops are unrolled (rolled ones took 6600 cycles a tile of
     // 64 experts where the MMAs take 1700).
     if (tc::elect_one()) {
-      constexpr int kPanels = kPacked ? 2 : 3 * kGroups, kLow = kPacked ? 1 : kGroups;
-      constexpr uint32_t id1 = tc::idesc_bf16_f32(kCols, 64) | kMajorA | kMajorB;
+      constexpr int kSlots = kPacked ? 1 : 3 * kGroups;   // of a tile
+      constexpr uint32_t id1 = tc::idesc_bf16_f32(kCols, kPer * 64) | kMajorA | kMajorB;
       constexpr uint32_t id2 = tc::idesc_bf16_f32(kTok, kCols) | kMajorB;
       Ring x(plan.nx), p(plan.np), d1(plan.bufs), d2(2);
       const uint64_t x0 = sdesc_mn(sX, kHalf), p_mn = sdesc_mn(sP, kHalf), p_k = tc::sdesc_k128(sP);
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
       auto x_bar = [&](int at) { return clean ? x_clean(at) : x_full(at); };
       bool begins = true;   // D1 with this tile
       bool ok = !dx_on || tc::mbar_wait(w_full, 0, &s_abort, kWaitNs);
-      bool x_ready = false, p_ready = false, d1_ready = false, d2_ready = false;
+      bool x_ready = false, p_ready = false, d1_ready = false;
 #pragma unroll 1
       for (Walk<kFlags> w(first, splits, P.tiles, alive); w.more() && ok; w.next()) {
         const bool fresh = begins;
@@ -283,19 +290,19 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
           if (ok && fresh && !d1_ready) ok = tc::mbar_wait(d1_empty(d1.at), d1.phase ^ 1u, &s_abort, kWaitNs);
           if (ok && !x_ready) ok = tc::mbar_wait(x_bar(x.at), x.phase, &s_abort, kWaitNs);
         }
-        if (ok && dx_on && !d2_ready) ok = tc::mbar_wait(d2_empty(d2.at), d2.phase ^ 1u, &s_abort, kWaitNs);
         if (!ok) break;
         tc::tc_fence_after();
         const uint64_t a1 = x0 + (uint32_t)(x.at * (kXBytes >> 4));
         const uint32_t to1 = tmem + d1.at * 128, to2 = tmem + kD2 + d2.at * kCols;
         const int x_at = x.at, d1_at = d1.at, d2_at = d2.at;
+        const uint32_t d2_phase = d2.phase;
         if (dwg) {
           x.next();
           if (begins) d1.next();
         }
         if (dx_on) d2.next();
 #pragma unroll
-        for (int n = 0; n < kPanels; ++n) {
+        for (int n = 0; n < kSlots; ++n) {
           if (!p_ready && !tc::mbar_wait(p_full(p.at), p.phase, &s_abort, kWaitNs)) {
             ok = false;
             break;
@@ -303,25 +310,31 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
           const int here = p.at, g = n % kGroups;
           p.next();
           p_ready = tc::mbar_test_wait(p_full(p.at), p.phase);
-          if (n == kPanels - 1) {
+          if (n == kSlots - 1) {
             x_ready = dwg && tc::mbar_test_wait(x_bar(x.at), x.phase);
             d1_ready = dwg && begins && tc::mbar_test_wait(d1_empty(d1.at), d1.phase ^ 1u);
-            d2_ready = dx_on && tc::mbar_test_wait(d2_empty(d2.at), d2.phase ^ 1u);
           }
-          const uint32_t off = (uint32_t)(here * (kHalf >> 4));
+          const uint32_t off = (uint32_t)(here * (kSlot >> 4));
           if (dwg) {
             const uint64_t b1 = p_mn + off;
-            // the first panel of a group starts its sums (packed: one group)
-            const uint32_t on = n < (kPacked ? 1 : kGroups) && fresh ? 0u : 1u;
+            // the first panel of a group starts its sums
+            const uint32_t on = n < kGroups && fresh ? 0u : 1u;
 #pragma unroll
             for (int k = 0; k < kTok / 16; ++k)
               tc::mma_bf16(to1 + g * 64, a1 + k * (2048 >> 4), b1 + k * (2048 >> 4), id1, k ? 1u : on);
           }
-          if (n >= kLow && dx_on) {   // the low parts come first
+          if (dx_on && n == 0) {   // D1's MMAs run while the epilogue empties D2
+            if (!tc::mbar_wait(d2_empty(d2_at), d2_phase ^ 1u, &s_abort, kWaitNs)) {
+              ok = false;
+              break;
+            }
+            tc::tc_fence_after();
+          }
+          if (dx_on && (kPacked || n >= kGroups)) {   // high and middle parts
             const uint64_t a2 = p_k + off, b2 = w0 + (uint32_t)(g * (64 * 128 >> 4));
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc::mma_bf16(to2, a2 + k * (32 >> 4), b2 + k * (2048 >> 4), id2, n > kLow || k ? 1u : 0u);
+              tc::mma_bf16(to2, a2 + k * (32 >> 4), b2 + k * (2048 >> 4), id2, n > kGroups || k ? 1u : 0u);
           }
           tc::tc_commit(p_empty(here));
         }
@@ -437,6 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
           uint32_t r[32];
           tc::tmem_ld_32x32b_x32(lanes + d1.at * 128 + g * 64 + half * 32, r);
           tc::tmem_wait_ld();
+          if (kPacked && half) {   // to the middle parts' sums the low ones'
+            uint32_t m[32];
+            tc::tmem_ld_32x32b_x32(lanes + d1.at * 128 + 64, m);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(m[j]));
+          }
 #pragma unroll
           for (int j = 0; j < 32; ++j) sum[g * 32 + j] += __uint_as_float(r[j]);
         }
