@@ -347,66 +347,81 @@ dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* 
   if (b.dbias) block_sums<G>(acc, s_b, lane, group, E, part_b + (int64_t)blockIdx.x * E);
 }
 
-// dx[t, h] = sum_e dl[t, e] Wg[e, h] on CUDA cores: 16 tokens, a thread a column.
-constexpr int kTokTile = 16;
-template <typename T>
-__global__ void __launch_bounds__(128)
-dx_simt_kernel(const float* __restrict__ dl, const T* __restrict__ Wg, int64_t Tn, int E, int H, T* __restrict__ dx) {
-  __shared__ float s_dl[256][kTokTile];
-  pdl_enter();
-  const int64_t t0 = (int64_t)blockIdx.x * kTokTile;
-  for (int i = threadIdx.x; i < E * kTokTile; i += 128) {
-    const int tt = i / E, e = i % E;
-    s_dl[e][tt] = t0 + tt < Tn ? dl[(t0 + tt) * E + e] : 0.f;
-  }
-  __syncthreads();
-  const int h = blockIdx.y * 128 + threadIdx.x;
-  if (h >= H) return;
-  float acc[kTokTile] = {};
-  for (int e = 0; e < E; ++e) {
-    const float w = to_f32(Wg[(int64_t)e * H + h]);
-#pragma unroll
-    for (int i = 0; i < kTokTile; ++i) acc[i] = fmaf(s_dl[e][i], w, acc[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < kTokTile; ++i)
-    if (t0 + i < Tn) dx[(t0 + i) * H + h] = from_f32<T>(acc[i]);
-}
+// The gate's products on CUDA cores, each of a launch's blocks for one of them:
+//   dx: 16 tokens, a thread a column
+//   dWg: partial sums over a share of the tokens, 16 experts, a thread a column
+//   (a masked token's x is not read: it may hold anything)
+//   dbias: the last block, the rows of partial sums in order
+constexpr int kTokTile = 16, kExpTile = 16, kTokStep = 32;
+struct SimtBlocks {
+  int cols;             // blocks of 128 columns
+  int64_t dx;           // blocks of dx
+  int groups, splits;   // of dWg: of experts and of tokens
+  int64_t dwg;
+};
 
-// dWg on CUDA cores: partial sums over a share of the tokens, 16 experts, a
-// thread a column.  A masked token's x is not read: it may hold anything.
-constexpr int kExpTile = 16, kTokStep = 32;
 template <typename T>
 __global__ void __launch_bounds__(128)
-dwg_simt_kernel(const float* __restrict__ dl, const T* __restrict__ x, const uint8_t* __restrict__ mask, int64_t Tn,
-                int E, int H, float* __restrict__ part) {
-  __shared__ float s_dl[kTokStep][kExpTile];
+products_simt_kernel(RouterBackward b, SimtBlocks n, const float* __restrict__ dl, int64_t Tn, int E, int H,
+                     float* __restrict__ part_w, const float* __restrict__ part_b, int rows_b) {
+  __shared__ float s_dl[256 * kTokTile];
   pdl_enter();
-  const int h = blockIdx.x * 128 + threadIdx.x, e0 = blockIdx.y * kExpTile;
-  const int64_t a = Tn * blockIdx.z / gridDim.z, z = Tn * (blockIdx.z + 1) / gridDim.z;
-  float acc[kExpTile] = {};
-  for (int64_t t0 = a; t0 < z; t0 += kTokStep) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTokStep * kExpTile; i += 128) {
-      const int tt = i / kExpTile, e = e0 + i % kExpTile;
-      s_dl[tt][i % kExpTile] = t0 + tt < z && e < E ? dl[(t0 + tt) * E + e] : 0.f;
+  int64_t i = blockIdx.x;
+  if (i < n.dx) {
+    const T* Wg = reinterpret_cast<const T*>(b.Wg);
+    T* dx = reinterpret_cast<T*>(b.dx);
+    const int64_t t0 = i / n.cols * kTokTile;
+    for (int k = threadIdx.x; k < E * kTokTile; k += 128) {
+      const int tt = k / E, e = k % E;
+      s_dl[e * kTokTile + tt] = t0 + tt < Tn ? dl[(t0 + tt) * E + e] : 0.f;
     }
     __syncthreads();
-    if (h < H) {
-      const int n = (int)(z - t0 < kTokStep ? z - t0 : kTokStep);
+    const int h = (int)(i % n.cols) * 128 + threadIdx.x;
+    if (h >= H) return;
+    float acc[kTokTile] = {};
 #pragma unroll 4
-      for (int tt = 0; tt < n; ++tt) {
-        if (mask && !mask[t0 + tt]) continue;
-        const float v = to_f32(x[(t0 + tt) * H + h]);
+    for (int e = 0; e < E; ++e) {
+      const float w = to_f32(Wg[(int64_t)e * H + h]);
 #pragma unroll
-        for (int i = 0; i < kExpTile; ++i) acc[i] = fmaf(s_dl[tt][i], v, acc[i]);
+      for (int k = 0; k < kTokTile; ++k) acc[k] = fmaf(s_dl[e * kTokTile + k], w, acc[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kTokTile; ++k)
+      if (t0 + k < Tn) dx[(t0 + k) * H + h] = from_f32<T>(acc[k]);
+  } else if ((i -= n.dx) < n.dwg) {
+    const T* x = reinterpret_cast<const T*>(b.x);
+    const int h = (int)(i % n.cols) * 128 + threadIdx.x, e0 = (int)(i / n.cols % n.groups) * kExpTile;
+    const int64_t split = i / n.cols / n.groups, a = Tn * split / n.splits, z = Tn * (split + 1) / n.splits;
+    float acc[kExpTile] = {};
+    for (int64_t t0 = a; t0 < z; t0 += kTokStep) {
+      __syncthreads();
+      for (int k = threadIdx.x; k < kTokStep * kExpTile; k += 128) {
+        const int tt = k / kExpTile, e = e0 + k % kExpTile;
+        s_dl[k] = t0 + tt < z && e < E ? dl[(t0 + tt) * E + e] : 0.f;
+      }
+      __syncthreads();
+      if (h < H) {
+        const int left = (int)(z - t0 < kTokStep ? z - t0 : kTokStep);
+#pragma unroll 8
+        for (int tt = 0; tt < left; ++tt) {
+          const float v = !b.mask || b.mask[t0 + tt] ? to_f32(x[(t0 + tt) * H + h]) : 0.f;
+#pragma unroll
+          for (int k = 0; k < kExpTile; ++k) acc[k] = fmaf(s_dl[tt * kExpTile + k], v, acc[k]);
+        }
       }
     }
-  }
-  if (h < H)
+    if (h < H)
 #pragma unroll
-    for (int i = 0; i < kExpTile; ++i)
-      if (e0 + i < E) part[((int64_t)blockIdx.z * E + e0 + i) * H + h] = acc[i];
+      for (int k = 0; k < kExpTile; ++k)
+        if (e0 + k < E) part_w[(split * E + e0 + k) * H + h] = acc[k];
+  } else {
+    for (int e = threadIdx.x; e < E; e += 128) {
+      float v = 0.f;
+#pragma unroll 8
+      for (int r = 0; r < rows_b; ++r) v += part_b[(int64_t)r * E + e];
+      b.dbias[e] = v;
+    }
+  }
 }
 
 // out[i] = the sum of `rows` rows of n, in order.
@@ -429,21 +444,22 @@ int simt_splits(const Shape& s) {
 }
 
 template <typename T>
-cudaError_t products_simt(const Shape& s, const RouterBackward& b, const float* dl, float* part_w, cudaStream_t st) {
-  cudaError_t e = cudaSuccess;
-  const unsigned cols = (unsigned)((s.H + 127) / 128);
-  if (b.dx)
-    e = launch_kernel(dx_simt_kernel<T>, dim3((unsigned)((s.T + kTokTile - 1) / kTokTile), cols), dim3(128), 0, st, 1,
-                      dl, (const T*)b.Wg, s.T, s.E, s.H, (T*)b.dx);
-  if (e == cudaSuccess && b.dWg) {
-    const int splits = simt_splits(s);
-    e = launch_kernel(dwg_simt_kernel<T>, dim3(cols, (unsigned)((s.E + kExpTile - 1) / kExpTile), (unsigned)splits),
-                      dim3(128), 0, st, 1, dl, (const T*)b.x, b.mask, s.T, s.E, s.H, part_w);
-    const int64_t n = (int64_t)s.E * s.H;
-    if (e == cudaSuccess)
-      e = launch_kernel(row_sums_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, 1, part_w,
-                        (int64_t)splits, n, b.dWg);
-  }
+cudaError_t products_simt(const Shape& s, const RouterBackward& b, const float* dl, float* part_w, const float* part_b,
+                          int rows_b, cudaStream_t st) {
+  SimtBlocks n = {};
+  n.cols = (s.H + 127) / 128;
+  n.dx = b.dx ? (s.T + kTokTile - 1) / kTokTile * n.cols : 0;
+  n.groups = (s.E + kExpTile - 1) / kExpTile;
+  n.splits = simt_splits(s);
+  n.dwg = b.dWg ? (int64_t)n.cols * n.groups * n.splits : 0;
+  const int64_t blocks = n.dx + n.dwg + (b.dbias ? 1 : 0), size = (int64_t)s.E * s.H;
+  if (blocks == 0) return cudaSuccess;
+  if (blocks >= (int64_t)1 << 31) return cudaErrorNotSupported;
+  cudaError_t e = launch_kernel(products_simt_kernel<T>, dim3((unsigned)blocks), dim3(128), 0, st, 1, b, n, dl, s.T, s.E,
+                                s.H, n.splits > 1 ? part_w : b.dWg, part_b, rows_b);
+  if (e == cudaSuccess && b.dWg && n.splits > 1)
+    e = launch_kernel(row_sums_kernel, dim3((unsigned)((size + 255) / 256)), dim3(256), 0, st, 1, part_w,
+                      (int64_t)n.splits, size, b.dWg);
   return e;
 }
 
@@ -516,10 +532,8 @@ cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, void
   });
   if (e != cudaSuccess) return e;
   if (tc) return launch_gate_tc(s, b, panels, alive, part_w, part_b, (int)rows, err, st);
-  if (b.dbias)
-    e = launch_kernel(row_sums_kernel, dim3(1), dim3(256), 0, st, 1, part_b, rows, (int64_t)s.E, b.dbias);
-  if (e != cudaSuccess || !(b.dx || b.dWg)) return e;
-  return s.dtype == MOE_BF16 ? products_simt<bf16>(s, b, out, part_w, st) : products_simt<float>(s, b, out, part_w, st);
+  return s.dtype == MOE_BF16 ? products_simt<bf16>(s, b, out, part_w, part_b, (int)rows, st)
+                             : products_simt<float>(s, b, out, part_w, part_b, (int)rows, st);
 }
 
 }  // namespace moe
