@@ -534,24 +534,28 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
         for (int h = 0; h < 2; ++h) {
           uint32_t r[32];
           tc::tmem_ld_32x32b_x32(tbase + c * 64 + h * 32, r);
-          uint4 more[4] = {};
-          if (S.add >= 0) {
+          if (S.add < 0) {
+            tc::tmem_wait_ld();
 #pragma unroll
-            for (int g = 0; g < 4; ++g) more[g] = ahead[g];
-            if (h == 0 || c + 1 < kChunks) fetch(col + (h + 1) * 32, ahead);
+            for (int j = 0; j < 16; ++j) {
+              const __half2 f = __floats2half2_rn(S.alpha * __uint_as_float(r[2 * j]), S.alpha * __uint_as_float(r[2 * j + 1]));
+              packed[h][j] = *reinterpret_cast<const uint32_t*>(&f);
+            }
+            continue;
           }
+          uint4 more[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) more[g] = ahead[g];
+          if (h == 0 || c + 1 < kChunks) fetch(col + (h + 1) * 32, ahead);
           tc::tmem_wait_ld();
+          const int diagonal = row - col - h * 32;   // the column of diag I, if it is one of these
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float v[2];
             const float2 m = __half22float2(reinterpret_cast<const __half2*>(more)[j]);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              v[x] = S.alpha * __uint_as_float(r[2 * j + x]);
-              v[x] = fmaf(S.beta, x ? m.y : m.x, v[x]);
-              if (row == col + h * 32 + 2 * j + x) v[x] += S.diag;
-            }
-            const __half2 f = __floats2half2_rn(v[0], v[1]);
+            const float x = fmaf(S.beta, m.x, S.alpha * __uint_as_float(r[2 * j])) + (diagonal == 2 * j ? S.diag : 0.f);
+            const float y =
+                fmaf(S.beta, m.y, S.alpha * __uint_as_float(r[2 * j + 1])) + (diagonal == 2 * j + 1 ? S.diag : 0.f);
+            const __half2 f = __floats2half2_rn(x, y);
             packed[h][j] = *reinterpret_cast<const uint32_t*>(&f);
           }
         }
