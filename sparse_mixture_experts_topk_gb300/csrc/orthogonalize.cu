@@ -1280,18 +1280,18 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
         (!x && !tma_map_16bit_3d(&C.mirror[i], C.buf[i], n, z.s, z.s, z.square, C.square_plane, 64, 32)))
       return cudaErrorNotSupported;
   }
-  // Which of the two tiles takes less time by their number: a stage of a pair's
-  // tile takes 600 cycles, of a single one's 540 (a quarter of the work, but
-  // both load 32 KB for each SM, which is what L2 gives in that time), and a
-  // step's start and the epilogue of its last tile 12000 and 6500.
-  // Single tiles win where the pairs' would leave most SMs idle.
+  // Which of the two tiles takes less time by their number: 64 elements of the
+  // reduction of a pair's tile take 600 cycles, of a single one's 540 (a quarter
+  // of the work, but both load 32 KB for each SM, and L2 gives an SM 64 bytes a
+  // cycle), and a step's start with the epilogue of its last tile 12000 and
+  // 6500.  Single tiles win where the pairs' would leave most SMs idle.
   auto tiles_of = [&](int tile, bool wide) {
     const int64_t mt = (z.s + tile - 1) / tile, nt = (z.L + tile - 1) / tile;
     return n * (wide ? mt * nt : mt * (mt + 1) / 2);
   };
   const int64_t pair_tiles = tiles_of(256, true), single_tiles = tiles_of(128, true), sms = sm_count();
   auto cost = [&](int64_t wide, int64_t shorts, int64_t ctas, int64_t stage, int64_t start) {
-    const int64_t a = (z.L + kBK - 1) / kBK, b = (z.s + kBK - 1) / kBK;
+    const int64_t a = (z.L + kBox - 1) / kBox, b = (z.s + kBox - 1) / kBox;
     return ((shorts + ctas - 1) / ctas * (a + b) + (wide + ctas - 1) / ctas * b) * stage + 3 * start;
   };
   const bool pair = cost(pair_tiles, tiles_of(256, false), sms / 2, 600, 12000) <=
