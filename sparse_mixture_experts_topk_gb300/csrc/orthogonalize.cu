@@ -13,12 +13,12 @@
 // instead, the result is 1.1 % off (in the 2-norm, for a gradient of four
 // strong directions over noise), with fp16 0.13 %.
 //
-// All products of a call are one launch: tiles go round the CTAs by number,
-// step after step, and a tile starts once every tile of its matrix' step before
-// is written (a counter for each step and matrix; one CTA an SM, all resident,
-// and no tile waits for a later one).  Launched one by one, the steps of a few
-// small matrices took twice as long, and those of many large ones lost their
-// tails.
+// All products of a call are one launch: running CTAs take tiles by number from
+// a counter, step after step, and a tile starts once every tile of its matrix'
+// step before is written (a counter for each step and matrix).  A tile waits for
+// lower numbers only, and those are taken by CTAs that run: no CTA needs
+// another one to be resident.  Launched one by one, the steps of a few small
+// matrices took twice as long, and those of many large ones lost their tails.
 //
 // Tiles are 256 x 256 on SM pairs (tcgen05 .cta_group::2), or 128 x 128 on
 // single SMs where those would leave SMs idle; fp32 accumulators in TMEM,
@@ -164,6 +164,7 @@ constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kOperand + kEpiWarps * kSt
 // The limit of a wait, and what it has on top for each stage of the tiles that a CTA has of a step: those may
 // have to be written first.
 constexpr uint64_t kWaitNs = 2000000000ull, kStageNs = 2000;
+constexpr int kQueue = 16, kNoTile = -1, kAborted = -2;
 
 // MN-major operand of 128 x 64: two boxes (64 columns of 128 bytes, 64 rows, 128-byte swizzle) one after the other.
 __device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr) {
@@ -199,18 +200,19 @@ struct Chain {
   int64_t pitch, plane, square, square_plane;   // elements of a row and of a matrix
   Step step[kMaxSteps];
   int* written;                  // [steps, batch] zeros: warps that have written their share of a tile
+  int* next;                     // zero: the first tile that nobody has taken
   uint64_t limit;
   const int32_t* skip;
   int* err;
 };
 
-// The tiles of a chain in the order in which they are dealt out.
+// The tiles of a chain in the order in which they are taken.
 template <int kTile>
 struct Tiles {
   const Chain& C;
   int mt, nt;
   int p, per;          // the step at hand, and its tiles of a matrix
-  int64_t base;        // the first of its tiles
+  int64_t base;        // the first of its tiles (all are below 2^31: see Sizes::most)
   int matrix, m0, n0;
   __device__ explicit Tiles(const Chain& c)
       : C(c), mt((c.s + kTile - 1) / kTile), nt((c.L + kTile - 1) / kTile), p(0), base(0) {
@@ -224,7 +226,7 @@ struct Tiles {
       if (++p == C.steps) return false;
       per = tiles(p);
     }
-    const uint32_t local = (uint32_t)(t - base);   // below 2^31: see Sizes::most
+    const uint32_t local = (uint32_t)(t - base);
     matrix = (int)(local / (uint32_t)per);
     int i = 0, j = (int)(local % (uint32_t)per);
     if (C.step[p].wide()) {
@@ -337,6 +339,7 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ unsigned long long s_queue[kQueue];
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u, sB = sA + kStages * kOperand;
   const uint32_t sOut = sB + kStages * kOperand;
@@ -366,6 +369,7 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
         tc::mbar_init(tempty(a), kCtas * kEpiWarps);   // one arrival for each epilogue warp
       }
       tc::mbar_init(done, 1);
+      for (int i = 0; i < kQueue; ++i) s_queue[i] = 0;
       s_abort = 0;
       tc::fence_barrier_init();
       tc::fence_proxy_async_smem();
@@ -384,8 +388,24 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
   if (kPair) tc::cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const int first = blockIdx.x / kCtas, stride = gridDim.x / kCtas;
   Tiles<kTile> T(C);
+  // The leader's first producer takes tiles and publishes each, or kNoTile at
+  // the end, as an entry of a queue in both CTAs; the other roles read it there.
+  // No role is kQueue tiles behind: two accumulators and kStages stages at most.
+  auto publish = [&](int seq, int t) {
+    const unsigned long long v = (unsigned long long)(unsigned)(seq + 1) << 32 | (unsigned)t;
+    *(volatile unsigned long long*)&s_queue[seq % kQueue] = v;
+    if (kPair) tc::st_peer_u64(tc::map_peer(tc::smem_u32(&s_queue[seq % kQueue]), 1), v);
+  };
+  auto read = [&](int seq) {   // kAborted if it does not come
+    volatile unsigned long long* slot = &s_queue[seq % kQueue];
+    const uint64_t t0 = tc::globaltimer();
+    while (true) {
+      const unsigned long long v = *slot;
+      if ((v >> 32) == (unsigned)(seq + 1)) return (int)(unsigned)v;
+      if (s_abort || tc::globaltimer() - t0 > C.limit) return (int)kAborted;
+    }
+  };
   // the counter of the step before a tile's, and what it has to reach
   auto before = [&]() { return C.written + (int64_t)(T.p - 1) * C.batch + T.matrix; };
   auto need = [&]() { return T.tiles(T.p - 1) * kCtas * kEpiWarps; };
@@ -401,7 +421,20 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
       uint32_t phase = 0;
       bool ok = true;
       const uint32_t to = second ? sB : sA;
-      for (int64_t t = first; ok && T.seek(t); t += stride) {
+      const bool takes = rank == 0 && !second;
+      int ahead = takes ? atomicAdd(C.next, 1) : 0;   // the following tile, taken while this one loads
+      for (int seq = 0; ok; ++seq) {
+        int t = ahead;
+        if (takes) {
+          if (!T.seek(t)) t = kNoTile;
+          publish(seq, t);
+          if (t >= 0) ahead = atomicAdd(C.next, 1);
+        } else {
+          t = read(seq);
+          if (t >= 0) T.seek(t);
+        }
+        ok = t != kAborted;
+        if (t < 0) break;
         if (T.p > 0 && (T.p != seen_p || T.matrix != seen_m)) {
           ok = wait_written(before(), need(), &s_abort, C.limit);
           if (!ok) break;
@@ -450,7 +483,11 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, ready = false;   // ready: the stage at hand was seen full
       const uint64_t a0 = tc::sdesc_k128(sA);
-      for (int64_t t = first; ok && T.seek(t); t += stride) {
+      for (int seq = 0; ok; ++seq) {
+        const int t = read(seq);
+        ok = t != kAborted;
+        if (t < 0) break;
+        T.seek(t);
         const bool mn = C.step[T.p].mn();
         const uint64_t b0 = mn ? sdesc_mn128(sB) : tc::sdesc_k128(sB);
         const uint32_t as = kStepK >> 4, bs = (mn ? kStepMN : kStepK) >> 4;
@@ -499,7 +536,11 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
     uint8_t* mine = smem_raw + (buf - tc::smem_u32(smem_raw));
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int64_t t = first; T.seek(t); t += stride) {
+    for (int seq = 0;; ++seq) {
+      const int t = __shfl_sync(0xffffffffu, lane == 0 ? read(seq) : 0, 0);
+      if (t == kAborted) give_up(C.err, &s_abort);
+      if (t < 0) break;
+      T.seek(t);
       const Step& S = C.step[T.p];
       const int cols = T.cols(), row0 = T.m0 + rank * kBM + q * 32, row = row0 + lane;
       const bool mirror = !S.wide() && T.m0 != T.n0;
@@ -771,11 +812,13 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ M
 
 // One block for each matrix: its counters to zero, and X's factors.
 __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ Matrices M, const Squares* __restrict__ part,
-                                                   float2* __restrict__ factor, int* __restrict__ written, int steps) {
+                                                   float2* __restrict__ factor, int* __restrict__ written, int steps,
+                                                   int* __restrict__ next) {
   __shared__ Squares s_w[8];
   pdl_enter();
   if (M.skip && *M.skip) return;
   for (int i = threadIdx.x; i < steps; i += 256) written[(int64_t)i * gridDim.x + blockIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *next = 0;
   Squares q = {0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int i = threadIdx.x; i < M.parts; i += 256) {
@@ -1214,14 +1257,17 @@ struct Sizes {
   size_t x() const { return (size_t)s * pitch * 2; }
   size_t a() const { return (size_t)s * square * 2; }
   size_t bytes(int64_t n) const {   // X and its successor, three short matrices, counters, sums, factors
-    return 2 * round256(n * x()) + 3 * round256(n * a()) + round256(n * kMaxSteps * sizeof(int)) +
+    return 2 * round256(n * x()) + 3 * round256(n * a()) + 256 + round256(n * kMaxSteps * sizeof(int)) +
            round256(n * parts * sizeof(Squares)) + round256(n * sizeof(float2));
   }
   int64_t most() const {
     int64_t n = (int64_t)(kMostBytes /
                           (2 * x() + 3 * a() + kMaxSteps * sizeof(int) + parts * sizeof(Squares) + sizeof(float2)));
-    const int64_t grid = ((int64_t)1 << 30) / ((int64_t)((s + 63) / 64) * ((L + 63) / 64));   // blocks and tiles of a launch
+    const int64_t blocks = (int64_t)((s + 63) / 64) * ((L + 63) / 64);    // of X's kernels, for a matrix
+    const int64_t tiles = (int64_t)((s + 127) / 128) * ((L + 127) / 128);   // of a step, at most
+    const int64_t grid = ((int64_t)1 << 30) / blocks, numbers = ((int64_t)1 << 30) / (tiles * kMaxSteps);
     if (n > grid) n = grid;
+    if (n > numbers) n = numbers;
     return n < 1 ? 1 : n;
   }
 };
@@ -1258,6 +1304,7 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
   };
   Chain C = {};
   for (int i = 0; i < kBuffers; ++i) C.buf[i] = (__half*)take(n * (i <= kY ? z.x() : z.a()));
+  C.next = (int*)take(256);
   C.written = (int*)take((size_t)n * kMaxSteps * sizeof(int));
   Squares* part = (Squares*)take((size_t)n * z.parts * sizeof(Squares));
   float2* factor = (float2*)take((size_t)n * sizeof(float2));
@@ -1303,7 +1350,7 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
   const dim3 sums((unsigned)(n * z.parts)), tiles((unsigned)((int64_t)n * M.tiles_s * M.tiles_L)), threads(256);
   cudaError_t e = grad_bf16 ? launch_kernel(momentum_kernel<bf16>, sums, threads, 0, st, 1, M, part)
                             : launch_kernel(momentum_kernel<float>, sums, threads, 0, st, 1, M, part);
-  if (e == cudaSuccess) e = launch_kernel(norm_kernel, dim3((unsigned)n), threads, 0, st, 1, M, part, factor, C.written, C.steps);
+  if (e == cudaSuccess) e = launch_kernel(norm_kernel, dim3((unsigned)n), threads, 0, st, 1, M, part, factor, C.written, C.steps, C.next);
   if (e == cudaSuccess)
     e = grad_bf16 ? launch_kernel(build_kernel<bf16>, tiles, threads, 0, st, 1, M, factor, C.buf[kX])
                   : launch_kernel(build_kernel<float>, tiles, threads, 0, st, 1, M, factor, C.buf[kX]);

@@ -125,6 +125,42 @@ def test_a_stream_given_and_two_streams_at_once():
         assert same(s.results(), w)
 
 
+def test_two_steps_that_fill_the_gpu_at_once():
+    """Either call has tiles for more CTAs than the GPU holds, beside the other's: none may wait for a CTA that
+    finds no room."""
+    t = t_()
+
+    def tensors(seed):
+        g = t.Generator(device="cuda").manual_seed(seed)
+        p = [t.randn(s, generator=g, device="cuda") * 0.02 for s in ((24, 520, 776), (24, 776, 520))]
+        return [{"p": q, "g": t.randn(q.shape, generator=g, device="cuda"), "m": t.zeros_like(q)} for q in p]
+
+    def results(ts):
+        t.cuda.synchronize()
+        return [v.clone() for d in ts for v in (d["p"], d["m"])]
+
+    def plan(ts):
+        p = moe.muon_tensors(ts)
+        return p, moe.muon_workspace(p)
+
+    params, want = moe.make_muon(0.01), []
+    for seed in (1, 2):
+        ts = tensors(seed)
+        p, ws = plan(ts)
+        for _ in range(10):
+            moe.moe_muon_step(p, params, None, None, ws)
+        want.append(results(ts))
+    both = [tensors(1), tensors(2)]
+    plans, streams = [plan(ts) for ts in both], [t.cuda.Stream() for _ in both]
+    t.cuda.synchronize()
+    for _ in range(10):
+        for (p, ws), st in zip(plans, streams):
+            moe.moe_muon_step(p, params, None, None, ws, st)
+    for ts, w in zip(both, want):
+        assert same(results(ts), w)
+    assert all(moe.moe_get_device_error(ws) == 0 for _, ws in plans)
+
+
 def test_a_workspace_serves_calls_of_all_sizes_in_turn():
     """One workspace as large as the largest call's: what one call leaves in it does not reach the next."""
     big, small = Step(6, T=2000, H=520, E=64, F=320), Step(7, T=17, H=72, E=5, F=40)
