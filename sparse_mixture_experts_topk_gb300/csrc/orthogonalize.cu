@@ -422,13 +422,13 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
       bool ok = true;
       const uint32_t to = second ? sB : sA;
       const bool takes = rank == 0 && !second;
-      int ahead = takes ? atomicAdd(C.next, 1) : 0;   // the following tile, taken while this one loads
       for (int seq = 0; ok; ++seq) {
-        int t = ahead;
+        int t;
         if (takes) {
+          // not ahead of time: while it waited here another CTA could have started it
+          t = atomicAdd(C.next, 1);
           if (!T.seek(t)) t = kNoTile;
           publish(seq, t);
-          if (t >= 0) ahead = atomicAdd(C.next, 1);
         } else {
           t = read(seq);
           if (t >= 0) T.seek(t);
