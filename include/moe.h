@@ -69,9 +69,9 @@ typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
  * out (about 2 s): the kernel records MOE_ERR_TIMEOUT in the workspace error
  * word, drains the loads it issued, frees its tensor memory and returns;
  * outputs are undefined.  It exercises the timeout path without a fault.
- * moe_expert_ffn_backward on the tensor cores does the same: the barrier of
- * each kernel's first stage waits for an arrival that nobody makes (about 4 s
- * a kernel, the drain's own wait running out too). */
+ * moe_expert_ffn_backward and moe_router_backward on the tensor cores do the
+ * same: the barrier of each kernel's first stage waits for an arrival that
+ * nobody makes (about 4 s a kernel, the drain's own wait running out too). */
 #define MOE_FLAG_TEST_WAIT_TIMEOUT (1u << 7)
 /* bf16 with SM pairs: every block of an expert's token rows runs with the
  * rows on the MMA's M side (padded to 256), instead of the default where an
@@ -478,8 +478,8 @@ int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, int32_t grad_
  *   out, or NULL each.  Ranks of a data-parallel batch add up the first three
  *   before they take the loss (moe_aux_loss) or its gradient.
  *   ws: of moe_router_backward_workspace_size() bytes
- * psum is summed in a fixed order, in fp32 over at most 2^13 tokens and in fp64
- * beyond.  An id outside [-1, E) of a token that counts sets MOE_ERR_DEVICE in
+ * psum is summed in a fixed order, in fp32 over at most 2^13 tokens and with
+ * twice its bits beyond.  An id outside [-1, E) of a token that counts sets MOE_ERR_DEVICE in
  * the workspace error word and counts for no expert.  Deterministic.
  */
 int moe_balance_loss(const moe_desc* desc, const float* logits, const int32_t* ids, const uint8_t* mask,
@@ -530,15 +530,21 @@ int moe_router_backward(const moe_desc* desc, const void* x, const void* Wg, con
  *   (a, b, c) = (3.4445, -4.7750, 2.0315)
  * which takes every singular value that is not tiny into about [0.7, 1.2] (five
  * iterations: those above 1/500 of |u|).  X and the products are held in fp16
- * times 2^12, their sums in fp32: the result is within about 2e-3 of the exact
- * iteration's, relative, in the 2-norm of the elements.  A matrix with a NaN or
- * an infinity becomes NaN throughout; the others of its batch do not.
+ * times 2^12, their sums in fp32.  That is as if each element of u were off by
+ * up to 2^-12 of itself (a bf16 gradient is off by 2^-8): 1e-3 to 3e-3 of the
+ * result in the 2-norm for gradients with strong directions over noise; what
+ * lies far below the elements it is part of is off by more (2e-2 for a matrix
+ * of rank one over noise 100 times smaller).  For large batches of longer
+ * matrices (more columns than 5/4 of the rows) two iterations are taken at a
+ * time, (B2 B1) X; bits then depend on the batch.  A matrix with a NaN or an
+ * infinity becomes NaN throughout; the others of its batch do not.
  */
 #define MOE_ORTHOGONALIZE_MAX_SIDE 32768       /* rows, cols <= this */
 #define MOE_ORTHOGONALIZE_MAX_ITERATIONS 16
 
 /* Bytes of device workspace moe_orthogonalize needs for `batch` matrices (a
- * large batch runs in parts); its first 256 bytes have to be zeros before the
+ * large batch runs in parts of 4 GiB; matrices of up to 128 x 4096 stay on
+ * chip and need 256 bytes); its first 256 bytes have to be zeros before the
  * first call. */
 int moe_orthogonalize_workspace_size(int64_t batch, int32_t rows, int32_t cols, size_t* bytes);
 

@@ -82,6 +82,7 @@ struct Params {
   float* part;     // [CTAs (packed: twice), E, 128] or null: no dWg
   bool dx_on;
   int* err;
+  int stall;       // testing: 1 = the first panels' barrier waits for an arrival that nobody makes
 };
 
 // A CTA's tiles: `first` and every step-th after it.  kFlags: bytes for a tile
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
         tc::mbar_init(x_empty(s), 1);
       }
       for (int s = 0; s < kMaxPanels; ++s) {
-        tc::mbar_init(p_full(s), 1);
+        tc::mbar_init(p_full(s), s == 0 ? 1 + P.stall : 1);
         tc::mbar_init(p_empty(s), 1);
       }
       tc::mbar_init(w_full, 1);
@@ -569,6 +570,7 @@ cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* 
     P.part = b.dWg ? part : nullptr;
     P.dx_on = b.dx != nullptr;
     P.err = err;
+    P.stall = (s.flags & MOE_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
     auto kern = plan.packed        ? gate_kernel<1, true>
                 : plan.groups == 1 ? gate_kernel<1, false>
                 : plan.groups == 2 ? gate_kernel<2, false>

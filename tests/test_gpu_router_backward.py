@@ -276,3 +276,25 @@ def test_scores_of_minus_infinity():
     assert (out["dlogits"].cpu().numpy()[off] == 0).all()
     c["n"]["logits"] = np.where(off, 0, c["n"]["logits"])      # for the bound alone
     check_backward(c, out, ref)
+
+
+@pytest.mark.parametrize("E,want", [(12, ("dWg", "dx", "dbias")), (100, ("dx",)), (200, ("dWg",))])
+def test_expired_wait_reports_timeout_and_context_survives(E, want):
+    """The first panels' barrier waits for an arrival that nobody makes: every role gives up, what is in flight
+    lands, tensor memory is freed and the error word says so.  The next call, in the same workspace, is right."""
+    t = t_()
+    c = case(1500, 520, E, 2, mask=True, seed=11)
+    ws = moe.router_backward_workspace(c["desc"])
+    start, end = (t.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    d = moe.make_desc(1500, 520, E, 2, 8, flags=moe.MOE_FLAG_TEST_WAIT_TIMEOUT)
+    q = c["t"]
+    out = dict(dWg=t.empty(E, 520, device="cuda"), dx=t.empty_like(q["x"]), dbias=t.empty(E, device="cuda"))
+    out = {k: v if k in want else None for k, v in out.items()}
+    moe.moe_router_backward(d, q["x"], q["Wg"], q["logits"], q["ids"], q["dw"], q["dloss"], q["count"], q["tokens"],
+                            q["mask"], None, out["dWg"], out["dbias"], out["dx"], ws)
+    end.record()
+    t.cuda.synchronize()
+    assert moe.moe_get_device_error(ws) == moe.MOE_ERR_TIMEOUT
+    assert start.elapsed_time(end) < 30e3
+    check_backward(c, run_backward(c, ws=ws), oracle(c))      # the read cleared the error word
