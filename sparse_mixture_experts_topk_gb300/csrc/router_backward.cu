@@ -91,19 +91,17 @@ struct Group {
   }
 };
 
-// The groups' sums of each expert over a block's tokens, added in order and
-// written as the block's row of partial sums.
+// The groups' sums over a block's tokens, added in order: thread e has expert e's.
 template <typename G>
-__device__ __forceinline__ void block_sums(const float* acc, float* s, int lane, int group, int E, float* row) {
+__device__ __forceinline__ float block_sums(const float* acc, float* s, int lane, int group, int E) {
   constexpr int kWidth = G::kN * (kThreads / G::kTokens);
 #pragma unroll
   for (int i = 0; i < G::kN; ++i) s[group * kWidth + G::expert(lane, i)] = acc[i];
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    float v = 0.f;
-    for (int g = 0; g < G::kTokens; ++g) v += s[g * kWidth + e];
-    row[e] = v;
-  }
+  float v = 0.f;
+  if ((int)threadIdx.x < E)
+    for (int g = 0; g < G::kTokens; ++g) v += s[g * kWidth + threadIdx.x];
+  return v;
 }
 
 // a + b, and what its rounding lost added to `low` (exact: Knuth's two-sum).
@@ -115,12 +113,12 @@ __device__ __forceinline__ float two_sum(float a, float b, float* low) {
   return s;
 }
 
-// A block's row of partial sums and counts.
-template <int kLanes, int kVecs>
+// A block's row of partial sums and counts; kOne: of the only block, the loss.
+template <int kLanes, int kVecs, bool kOne>
 __global__ void __launch_bounds__(kThreads)
 balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
                int64_t T, int E, int K, float inv_tau, float* __restrict__ part_p, int32_t* __restrict__ part_c,
-               int* err) {
+               BalanceOut o, int* err) {
   using G = Group<kLanes, kVecs>;
   __shared__ float s_p[kThreads * 4 * kVecs];
   __shared__ int s_count[257];
@@ -156,8 +154,31 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids
     }
   }
   if (lane == 0 && n) atomicAdd(&s_count[E], n);
-  block_sums<G>(acc, s_p, lane, group, E, part_p + (int64_t)blockIdx.x * E);   // its barrier ends the counting too
-  for (int i = threadIdx.x; i <= E; i += kThreads) part_c[(int64_t)blockIdx.x * (E + 1) + i] = s_count[i];
+  const int e = threadIdx.x;
+  const float sum = block_sums<G>(acc, s_p, lane, group, E);   // its barrier ends the counting too
+  if (!kOne) {
+    if (e < E) part_p[(int64_t)blockIdx.x * E + e] = sum;
+    for (int i = e; i <= E; i += kThreads) part_c[(int64_t)blockIdx.x * (E + 1) + i] = s_count[i];
+    return;
+  }
+  // the results as balance_finish_kernel has them
+  const int tokens = s_count[E];
+  const float total = (float)tokens;
+  if (e < E) {
+    if (o.psum) o.psum[e] = sum;
+    if (o.count) o.count[e] = s_count[e];
+  }
+  float v = e < E && tokens ? (float)s_count[e] / (total * (float)K) * (sum / total) : 0.f;
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
+  __syncthreads();   // s_p has been read
+  if (e % 32 == 0) s_p[e / 32] = v;
+  __syncthreads();
+  if (e == 0) {
+    for (int i = 1; i < kThreads / 32; ++i) v += s_p[i];
+    if (o.tokens) *o.tokens = tokens;
+    if (o.loss) *o.loss = (float)E * v;
+  }
 }
 
 // The partial rows added up, 32 experts to a block, and the loss from the
@@ -344,7 +365,10 @@ dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* 
       }
     }
   }
-  if (b.dbias) block_sums<G>(acc, s_b, lane, group, E, part_b + (int64_t)blockIdx.x * E);
+  if (b.dbias) {
+    const float sum = block_sums<G>(acc, s_b, lane, group, E);
+    if ((int)threadIdx.x < E) part_b[(int64_t)blockIdx.x * E + threadIdx.x] = sum;
+  }
 }
 
 // The gate's products on CUDA cores, each of a launch's blocks for one of them:
@@ -503,10 +527,12 @@ cudaError_t launch_balance(const Shape& s, const float* logits, const int32_t* i
                            const BalanceOut& o, float* part_p, int32_t* part_c, int* err, cudaStream_t st) {
   const int rows = (int)balance_partials(s);
   const cudaError_t e = by_experts(s.E, [&](auto lanes, auto vecs) {
-    return launch_kernel(balance_kernel<decltype(lanes)::value, decltype(vecs)::value>, dim3((unsigned)rows),
-                         dim3(kThreads), 0, st, 1, logits, ids, mask, s.T, s.E, s.K, s.inv_tau, part_p, part_c, err);
+    constexpr int kLanes = decltype(lanes)::value, kVecs = decltype(vecs)::value;
+    return launch_kernel(rows == 1 ? balance_kernel<kLanes, kVecs, true> : balance_kernel<kLanes, kVecs, false>,
+                         dim3((unsigned)rows), dim3(kThreads), 0, st, 1, logits, ids, mask, s.T, s.E, s.K, s.inv_tau,
+                         part_p, part_c, o, err);
   });
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || rows == 1) return e;
   const unsigned blocks = s.E <= 32 ? 1 : s.E <= 64 ? 2 : s.E <= 128 ? 4 : 8;
   return launch_kernel(balance_finish_kernel, dim3(blocks), dim3(1024), 0, st, blocks, part_p, part_c, rows, s.E, s.K,
                        o);
