@@ -8,7 +8,7 @@
 //   dl[t, e] = 1/tau ( sum_{ids_j = e} w_j (dw_j - <w, dw>) + p_e (c_e - <p, c>) )
 //   dWg = dl^T x,  dbias = sum_t dl,  dx = dl Wg
 //
-// A group of 8, 16 or 32 lanes takes a token, each lane 4 experts at a time,
+// A group of 8 or 16 lanes takes a token, each lane 4 experts at a time,
 // so that a token's scores are one vector load a lane and every sum over them
 // stays in the group.  What is summed over tokens leaves a block as one row of
 // partial sums; the rows are added in their order, so results are
@@ -24,7 +24,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;      // tokens of a group in flight together
 
 constexpr float kLog2E = 1.44269504088896341f;
 
@@ -35,11 +34,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Lanes for a token and experts for a lane, by the number of experts.
+// Lanes for a token and experts for a lane, by the number of experts: few lanes
+// with many experts, since a sum over a group's lanes costs the same for any
+// number of groups in a warp (131072 tokens of 256 experts: 32 lanes 34 us, 16
+// lanes 31).
 template <int kLanes, int kVecs>
 struct Group {
   static constexpr int kTokens = kThreads / kLanes;   // at a time in a block
   static constexpr int kN = 4 * kVecs;
+  static constexpr int kAhead = kN > 8 ? 1 : 2;   // tokens of a group in flight together
   // expert i of this lane
   __device__ static int expert(int lane, int i) { return (i / 4) * kLanes * 4 + lane * 4 + i % 4; }
   __device__ static float sum(float v) {
@@ -128,7 +131,7 @@ balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids
   const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   float acc[G::kN] = {};
   int n = 0;
-  // kAhead tokens of a group at a time: their loads are in flight together
+  constexpr int kAhead = G::kAhead;
   const int64_t stride = (int64_t)gridDim.x * G::kTokens;
   for (int64_t t0 = (int64_t)blockIdx.x * G::kTokens; t0 < T; t0 += kAhead * stride) {
     float l[kAhead][G::kN];
@@ -336,7 +339,7 @@ dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* 
     }
     if (t < T && panels) {
       bf16* row = panels + t * panel_cols;
-      const bool packed = kLanes == 8;
+      const bool packed = E <= 32;
       const int width = packed ? 32 : panel_cols / 3;
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
@@ -491,9 +494,9 @@ cudaError_t products_simt(const Shape& s, const RouterBackward& b, const float* 
 template <typename F>
 cudaError_t by_experts(int E, F f) {
   if (E <= 32) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
-  if (E <= 64) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
-  if (E <= 128) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
-  return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
+  if (E <= 64) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
+  if (E <= 128) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 2>());
+  return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
 }
 
 }  // namespace
@@ -501,14 +504,14 @@ cudaError_t by_experts(int E, F f) {
 // Blocks that walk over the tokens: `per_sm` an SM at most while a block has no
 // more than 2^13 tokens, and no more than have `rounds` tokens for each group.
 static int64_t token_blocks(const Shape& s, int per_sm, int rounds) {
-  const int64_t tokens = kThreads / (s.E <= 32 ? 8 : s.E <= 64 ? 16 : 32);
+  const int64_t tokens = kThreads / (s.E <= 64 ? 8 : 16);
   const int64_t want = (s.T + rounds * tokens - 1) / (rounds * tokens), cap = per_sm * (int64_t)sm_count();
   const int64_t least = (s.T + 8191) / 8192;
   int64_t n = want < cap ? want : cap;
   if (n < least) n = least;
   return n < 1 ? 1 : n;
 }
-int64_t balance_partials(const Shape& s) { return token_blocks(s, 4, kAhead); }
+int64_t balance_partials(const Shape& s) { return token_blocks(s, 4, s.E <= 128 ? 2 : 1); }
 // The scores' gradient: five blocks of 256 threads fit an SM.
 int64_t dlogits_partials(const Shape& s) { return token_blocks(s, 5, 1); }
 

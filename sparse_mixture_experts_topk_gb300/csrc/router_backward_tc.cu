@@ -102,12 +102,8 @@ struct Walk {
     if (kFlags == 0 || !alive || t >= tiles) return true;
     const uint8_t* p = alive + (int64_t)t * kFlags;
     if (kFlags == 4) return __ldcg(reinterpret_cast<const unsigned*>(p)) != 0;
-    if (kFlags == 8) {
-      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
-      return (v.x | v.y) != 0;
-    }
-    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
-    return (v.x | v.y | v.z | v.w) != 0;
+    const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
+    return (v.x | v.y) != 0;
   }
   __device__ bool more() const { return tile < tiles; }
   __device__ void next() {
@@ -210,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   // a tile none of whose tokens counts is not loaded; sums of several tiles take each
   constexpr int kPer = kPacked ? 2 : 1, kSlot = kPer * kHalf;
   constexpr int kD2 = 256;   // TMEM columns: D1 at 0 (and 128), D2 twice 128
-  constexpr int kFlags = kRun > 1 ? 0 : kGroups == 2 ? 16 : kPacked ? 4 : 8;
+  constexpr int kFlags = kRun > 1 ? 0 : kGroups == 2 ? 8 : 4;
   const uint8_t* alive = kFlags ? P.alive : nullptr;
   // the producers' copies: stages filled and the parity of each one's latest
   uint32_t filled = 0, fill_par = 0;
