@@ -756,7 +756,7 @@ __device__ __forceinline__ float2 factors_of(const Squares& q) {
   if (!(q.mid <= 1e-20f)) return make_float2(1.f, kHeld / sqrtf(q.mid));   // a NaN too
   return q.small > 0.f ? make_float2(kUp, kHeld / sqrtf(q.small)) : make_float2(0.f, 0.f);
 }
-// The sum over a block's warps (at most 8), for thread 0.
+// The sum over a block's warps, for thread 0.
 __device__ __forceinline__ Squares block_sum(Squares q, Squares* s_w) {
   q = warp_sum(q);
   if (threadIdx.x % 32 == 0) s_w[threadIdx.x / 32] = q;
@@ -922,7 +922,7 @@ build_kernel(const __grid_constant__ Matrices M, const float2* __restrict__ fact
 //
 // What bounds it is the chain of products, each of which waits for the one
 // before: a phase takes about a microsecond.
-constexpr int kSide = 128, kPanel = kSide * 128, kSlice = 512, kMostCtas = 8;
+constexpr int kSide = 128, kPanel = kSide * 128, kSlice = 512, kMostCtas = 8, kSmallThreads = 512;
 constexpr size_t kSmallSmem = 1024 + (size_t)(kSlice / 64 + 4) * kPanel;
 
 // Byte offset of elements (row, col) .. (col a multiple of 4) in panels.
@@ -940,18 +940,18 @@ __device__ __forceinline__ float4 ld_peer_f32x4(uint32_t addr) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(kSmallThreads, 1)
 small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ __align__(8) uint64_t s_bar;
-  __shared__ Squares s_w[8], s_part[kMostCtas];
+  __shared__ Squares s_w[kSmallThreads / 32], s_part[kMostCtas];
   const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const X = smem_raw + (base - tc::smem_u32(smem_raw));   // panels of X, then two of A and two of B
   uint8_t* const A = X + kSlice / 64 * kPanel;
   uint8_t* const B = A + 2 * kPanel;
   const uint32_t sX = base, sA = sX + kSlice / 64 * kPanel, sB = sA + 2 * kPanel, bar = tc::smem_u32(&s_bar);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, half = warp >> 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, part = warp >> 2;   // TMEM lanes, and columns
   const int rank = (int)tc::cluster_ctarank();
   uint32_t ctas;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
@@ -964,7 +964,7 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
     tc::tmem_alloc(tc::smem_u32(&s_tmem), 512);
     tc::tmem_relinquish();
   }
-  for (int i = threadIdx.x; i < kSlice / 64 * kPanel / 16; i += 256)
+  for (int i = threadIdx.x; i < kSlice / 64 * kPanel / 16; i += kSmallThreads)
     reinterpret_cast<uint4*>(X)[i] = make_uint4(0u, 0u, 0u, 0u);
   tc::tc_fence_before();
   __syncthreads();
@@ -985,11 +985,25 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
   // this CTA's part of the tensor, four elements of a row at a time
   const int r0 = flip ? c0 : 0, nr = flip ? w : s, t0 = flip ? 0 : c0, nc = flip ? s : w, vecs = (nc + 3) / 4;
   const bool even = S.cols % 4 == 0;
-  auto each = [&](auto f) {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < nr * vecs; i += 256) {
+  // Four of a thread's groups of four at a time: `load` starts their loads, `use` has them.
+  struct At {
+    int64_t o;      // in the matrix
+    int r, c, left;
+  };
+  auto each = [&](auto load, auto use) {
+    auto at = [&](int i) {
       const int r = i / vecs, c = (i - r * vecs) * 4;
-      f((int64_t)(r0 + r) * S.cols + t0 + c, r, c, min(4, nc - c));
+      return At{(int64_t)(r0 + r) * S.cols + t0 + c, r, c, min(4, nc - c)};
+    };
+    const int n = nr * vecs;
+    for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kSmallThreads) {
+      float a[4][4], b[4][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kSmallThreads < n) load(at(i0 + u * kSmallThreads), a[u], b[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kSmallThreads < n) use(at(i0 + u * kSmallThreads), a[u], b[u]);
     }
   };
 
@@ -997,25 +1011,23 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
     // the momentum's step and the update's norm
     const bool vg = even && aligned_to(g, 4 * sizeof(T)), vm = even && aligned_to(m, 16);
     Squares sq = {0.f, 0.f, 0.f};
-    auto update = [&](int64_t o, int left, float* u, bool write) {
-      load4(g + o, vg, left, u);
-      if (M.raw) return;
-      float mm[4];
-      load4(m + o, vm, left, mm);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float gx = u[x] * scale;
-        if (write) mm[x] = fmaf(M.mu, mm[x], gx);
-        u[x] = M.nesterov ? fmaf(M.mu, mm[x], gx) : mm[x];
-      }
-      if (write) store4(m + o, vm, left, mm);
+    auto load_u = [&](const At& p, float* u, float* mm) {
+      load4(g + p.o, vg, p.left, u);
+      if (!M.raw) load4(m + p.o, vm, p.left, mm);
     };
-    each([&](int64_t o, int, int, int left) {
-      float u[4];
-      update(o, left, u, true);
+    each(load_u, [&](const At& p, float* u, float* mm) {
+      if (!M.raw) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float gx = u[x] * scale;
+          mm[x] = fmaf(M.mu, mm[x], gx);
+          u[x] = M.nesterov ? fmaf(M.mu, mm[x], gx) : mm[x];
+        }
+        store4(m + p.o, vm, p.left, mm);
+      }
 #pragma unroll
       for (int x = 0; x < 4; ++x)
-        if (x < left) add_square(sq, u[x]);
+        if (x < p.left) add_square(sq, u[x]);
     });
     sq = block_sum(sq, s_w);
     if (threadIdx.x == 0) {
@@ -1035,22 +1047,20 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
       all.small += s_part[i].small;
     }
     const float2 f = factors_of(all);
-    each([&](int64_t o, int r, int c, int left) {
-      float u[4];
-      update(o, left, u, false);
+    each(load_u, [&](const At& p, float* u, const float* mm) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) u[x] = x < left ? u[x] * f.x * f.y : 0.f;
-      const __half2 h[2] = {__floats2half2_rn(u[0], u[1]), __floats2half2_rn(u[2], u[3])};
+      for (int x = 0; x < 4; ++x) {
+        if (!M.raw) u[x] = M.nesterov ? fmaf(M.mu, mm[x], u[x] * scale) : mm[x];
+        u[x] = x < p.left ? u[x] * f.x * f.y : 0.f;
+      }
+      const uint2 h = pack_half4(u);
       if (flip) {
-        const __half* e = reinterpret_cast<const __half*>(h);
+        const __half* e = reinterpret_cast<const __half*>(&h);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          if (x < left) {
-            const uint32_t at = panel_at(c + x, r & ~3) + (r & 3) * 2;
-            *reinterpret_cast<__half*>(X + at) = e[x];
-          }
+          if (x < p.left) *reinterpret_cast<__half*>(X + panel_at(p.c + x, p.r & ~3) + (p.r & 3) * 2) = e[x];
       } else {
-        *reinterpret_cast<uint2*>(X + panel_at(r, c)) = *reinterpret_cast<const uint2*>(h);
+        *reinterpret_cast<uint2*>(X + panel_at(p.r, p.c)) = h;
       }
     });
 
@@ -1095,42 +1105,33 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
           tc::mma_bf16(tmem, d, d, idesc_f16_f32(kSide, kSide), k > 0);
         }
       });
+      uint32_t r[32];
+      tc::tmem_ld_32x32b_x32(lanes + part * 32, r);
+      tc::tmem_wait_ld();
       if (ctas == 1) {
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[32];
-          tc::tmem_ld_32x32b_x32(lanes + half * 64 + h * 32, r);
-          tc::tmem_wait_ld();
-          float v[32];
+        float v[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = back * __uint_as_float(r[j]);
-          keep32(A, half * 64 + h * 32, v);
-        }
+        for (int j = 0; j < 32; ++j) v[j] = back * __uint_as_float(r[j]);
+        keep32(A, part * 32, v);
       } else {
         // partial sums: 128 rows of 128 fp32 over A's and B's panels, 16 bytes of a row exchanged by the row's number
-        float4* part = reinterpret_cast<float4*>(A);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[32];
-          tc::tmem_ld_32x32b_x32(lanes + half * 64 + h * 32, r);
-          tc::tmem_wait_ld();
+        float4* sums = reinterpret_cast<float4*>(A);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                                         __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-            part[row * 32 + ((half * 16 + h * 8 + j) ^ (row & 31))] = w > 0 ? v : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
+        for (int j = 0; j < 8; ++j) {
+          const float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                       __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+          sums[row * 32 + ((part * 8 + j) ^ (row & 31))] = w > 0 ? v : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         tc::tc_fence_before();
         __syncthreads();
         tc::cluster_sync();
         // rows rank * share ..: every fourth of a row's 32 groups of four to a thread at a time
-        const int share = kSide / (int)ctas, groups = share * 32 / 256;
-        uint2 mine[16];
+        const int share = kSide / (int)ctas, groups = share * 32 / kSmallThreads;
+        uint2 mine[4];
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
+        for (int n = 0; n < 4; ++n) {
           if (n >= groups) break;
-          const int i = n * 256 + threadIdx.x, r = rank * share + i / 32, j = i % 32;
+          const int i = n * kSmallThreads + threadIdx.x, r = rank * share + i / 32, j = i % 32;
           const uint32_t at = sA + (uint32_t)(r * 32 + (j ^ (r & 31))) * 16;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           for (uint32_t k = 0; k < ctas; ++k) {
@@ -1145,9 +1146,9 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
         }
         tc::cluster_sync();   // every partial sum has been read
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
+        for (int n = 0; n < 4; ++n) {
           if (n >= groups) break;
-          const int i = n * 256 + threadIdx.x, r = rank * share + i / 32, j = i % 32;
+          const int i = n * kSmallThreads + threadIdx.x, r = rank * share + i / 32, j = i % 32;
           const uint32_t at = sA + panel_at(r, j * 4);
           const unsigned long long u = (unsigned long long)mine[n].y << 32 | mine[n].x;
           for (uint32_t k = 0; k < ctas; ++k) tc::st_peer_u64(tc::map_peer(at, k), u);
@@ -1162,10 +1163,8 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
           tc::mma_bf16(tmem, d, d, idesc_f16_f32(kSide, kSide), k > 0);
         }
       });
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        const int col = half * 64 + h * 32;
-        uint32_t r[32];
+      {
+        const int col = part * 32;
         tc::tmem_ld_32x32b_x32(lanes + col, r);
         tc::tmem_wait_ld();
         float v[32];
@@ -1195,8 +1194,7 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
         }
       });
 #pragma unroll 1
-      for (int c = half; c < panels * 2; c += 2) {
-        uint32_t r[32];
+      for (int c = part; c < panels * 2; c += 4) {
         tc::tmem_ld_32x32b_x32(lanes + c * 32, r);
         tc::tmem_wait_ld();
         float v[32];
@@ -1208,26 +1206,25 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
     tc::tc_fence_before();
     __syncthreads();
     // p = p keep - step O, and its bf16 copy; raw: out = O
-    each([&](int64_t o, int r, int c, int left) {
-      float v[4];
-      if (flip) {
+    each([&](const At& a, float* p, float*) { get4(M, S, first + a.o, even, a.left, p); },
+         [&](const At& a, const float* p, float* v) {
+           if (flip) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          v[x] = x < left ? __half2float(*reinterpret_cast<const __half*>(X + panel_at(c + x, r & ~3) + (r & 3) * 2)) * back
+             for (int x = 0; x < 4; ++x)
+               v[x] = x < a.left
+                          ? __half2float(*reinterpret_cast<const __half*>(X + panel_at(a.c + x, a.r & ~3) + (a.r & 3) * 2)) * back
                           : 0.f;
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(X + panel_at(r, c));
-        const __half2* h = reinterpret_cast<const __half2*>(&u);
-        const float2 x = __half22float2(h[0]), y = __half22float2(h[1]);
-        v[0] = x.x * back;
-        v[1] = x.y * back;
-        v[2] = y.x * back;
-        v[3] = y.y * back;
-      }
-      float p[4];
-      get4(M, S, first + o, even, left, p);
-      put4(M, S, first + o, even, left, p, v);
-    });
+           } else {
+             const uint2 u = *reinterpret_cast<const uint2*>(X + panel_at(a.r, a.c));
+             const __half2* h = reinterpret_cast<const __half2*>(&u);
+             const float2 x = __half22float2(h[0]), y = __half22float2(h[1]);
+             v[0] = x.x * back;
+             v[1] = x.y * back;
+             v[2] = y.x * back;
+             v[3] = y.y * back;
+           }
+           put4(M, S, first + a.o, even, a.left, p, v);
+         });
   }
   if (ctas > 1) tc::cluster_sync();   // no CTA leaves while another may still read its shared memory
   if (warp == 0) {
@@ -1436,7 +1433,7 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
           auto kern = grad_dtype == MOE_BF16 ? small_kernel<bf16> : small_kernel<float>;
           const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
           if (r != cudaSuccess) return r;
-          return launch_kernel(kern, dim3((unsigned)(held * ctas)), dim3(256), kSmallSmem, st, (unsigned)ctas, M,
+          return launch_kernel(kern, dim3((unsigned)(held * ctas)), dim3(kSmallThreads), kSmallSmem, st, (unsigned)ctas, M,
                                (int)h.iterations, (int*)ws);
         });
     if (e != cudaSuccess) return e;
