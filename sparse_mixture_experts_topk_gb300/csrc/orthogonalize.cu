@@ -923,7 +923,7 @@ build_kernel(const __grid_constant__ Matrices M, const float2* __restrict__ fact
 // What bounds it is the chain of products, each of which waits for the one
 // before: a phase takes about a microsecond.
 constexpr int kSide = 128, kPanel = kSide * 128, kSlice = 512, kMostCtas = 8, kSmallThreads = 512;
-constexpr size_t kSmallSmem = 1024 + (size_t)(kSlice / 64 + 4) * kPanel;
+constexpr size_t kSmallSmem = 1024 + (size_t)(kSlice / 64 + 6) * kPanel;
 
 // Byte offset of elements (row, col) .. (col a multiple of 4) in panels.
 __device__ __forceinline__ uint32_t panel_at(int row, int col) {
@@ -947,7 +947,7 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
   __shared__ __align__(8) uint64_t s_bar;
   __shared__ Squares s_w[kSmallThreads / 32], s_part[kMostCtas];
   const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* const X = smem_raw + (base - tc::smem_u32(smem_raw));   // panels of X, then two of A and two of B
+  uint8_t* const X = smem_raw + (base - tc::smem_u32(smem_raw));   // panels of X, two of A, four of partial sums (two of B)
   uint8_t* const A = X + kSlice / 64 * kPanel;
   uint8_t* const B = A + 2 * kPanel;
   const uint32_t sX = base, sA = sX + kSlice / 64 * kPanel, sB = sA + 2 * kPanel, bar = tc::smem_u32(&s_bar);
@@ -985,25 +985,35 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
   // this CTA's part of the tensor, four elements of a row at a time
   const int r0 = flip ? c0 : 0, nr = flip ? w : s, t0 = flip ? 0 : c0, nc = flip ? s : w, vecs = (nc + 3) / 4;
   const bool even = S.cols % 4 == 0;
-  // Four of a thread's groups of four at a time: `load` starts their loads, `use` has them.
+  // Lanes go along a row, `along` (a power of two) to a row; four rows of a
+  // thread at a time: `load` starts their loads, `use` has them.  (What bounds
+  // these passes is their instructions: with a division for each group of four a
+  // matrix of 128 x 512 took 39 us for one iteration.)
   struct At {
     int64_t o;      // in the matrix
     int r, c, left;
   };
+  // a transposed matrix: 8 lanes at most, since a row's elements are one column of X in shared memory, whose
+  // rows share their banks
+  const int most = flip ? 8 : 32, along = min(most, vecs > 16 ? 32 : vecs > 8 ? 16 : vecs > 4 ? 8 : vecs > 2 ? 4 : 2);
+  const int rows = kSmallThreads / along;
   auto each = [&](auto load, auto use) {
-    auto at = [&](int i) {
-      const int r = i / vecs, c = (i - r * vecs) * 4;
-      return At{(int64_t)(r0 + r) * S.cols + t0 + c, r, c, min(4, nc - c)};
-    };
-    const int n = nr * vecs;
-    for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kSmallThreads) {
-      float a[4][4], b[4][4];
+    for (int v = threadIdx.x % along; v < vecs; v += along) {
+      const int c = v * 4, left = min(4, nc - c);
+      const int64_t o = (int64_t)r0 * S.cols + t0 + c;
+      for (int i = threadIdx.x / along; i < nr; i += 4 * rows) {
+        float a[4][4], b[4][4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i0 + u * kSmallThreads < n) load(at(i0 + u * kSmallThreads), a[u], b[u]);
+        for (int u = 0; u < 4; ++u) {
+          const int r = i + u * rows;
+          if (r < nr) load(At{o + (int64_t)r * S.cols, r, c, left}, a[u], b[u]);
+        }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i0 + u * kSmallThreads < n) use(at(i0 + u * kSmallThreads), a[u], b[u]);
+        for (int u = 0; u < 4; ++u) {
+          const int r = i + u * rows;
+          if (r < nr) use(At{o + (int64_t)r * S.cols, r, c, left}, a[u], b[u]);
+        }
+      }
     }
   };
 
@@ -1114,8 +1124,8 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
         for (int j = 0; j < 32; ++j) v[j] = back * __uint_as_float(r[j]);
         keep32(A, part * 32, v);
       } else {
-        // partial sums: 128 rows of 128 fp32 over A's and B's panels, 16 bytes of a row exchanged by the row's number
-        float4* sums = reinterpret_cast<float4*>(A);
+        // partial sums: 128 rows of 128 fp32, 16 bytes of a row exchanged by the row's number
+        float4* sums = reinterpret_cast<float4*>(B);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
@@ -1125,33 +1135,24 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
         tc::tc_fence_before();
         __syncthreads();
         tc::cluster_sync();
-        // rows rank * share ..: every fourth of a row's 32 groups of four to a thread at a time
-        const int share = kSide / (int)ctas, groups = share * 32 / kSmallThreads;
-        uint2 mine[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          if (n >= groups) break;
-          const int i = n * kSmallThreads + threadIdx.x, r = rank * share + i / 32, j = i % 32;
-          const uint32_t at = sA + (uint32_t)(r * 32 + (j ^ (r & 31))) * 16;
+        // rows rank * share ..: every CTA's sums of four elements added up, for every CTA
+        const int share = kSide / (int)ctas;
+        for (int i = threadIdx.x; i < share * 32; i += kSmallThreads) {
+          const int rr = rank * share + i / 32, j = i % 32;
+          const uint32_t from = sB + (uint32_t)(rr * 32 + (j ^ (rr & 31))) * 16, to = sA + panel_at(rr, j * 4);
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
           for (uint32_t k = 0; k < ctas; ++k) {
-            const float4 x = ld_peer_f32x4(tc::map_peer(at, k));
+            const float4 x = ld_peer_f32x4(tc::map_peer(from, k));
             v.x += x.x;
             v.y += x.y;
             v.z += x.z;
             v.w += x.w;
           }
           const float e[4] = {v.x * back, v.y * back, v.z * back, v.w * back};
-          mine[n] = pack_half4(e);
-        }
-        tc::cluster_sync();   // every partial sum has been read
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          if (n >= groups) break;
-          const int i = n * kSmallThreads + threadIdx.x, r = rank * share + i / 32, j = i % 32;
-          const uint32_t at = sA + panel_at(r, j * 4);
-          const unsigned long long u = (unsigned long long)mine[n].y << 32 | mine[n].x;
-          for (uint32_t k = 0; k < ctas; ++k) tc::st_peer_u64(tc::map_peer(at, k), u);
+          const uint2 h = pack_half4(e);
+          for (uint32_t k = 0; k < ctas; ++k)
+            tc::st_peer_u64(tc::map_peer(to, k), (unsigned long long)h.y << 32 | h.x);
         }
         asm volatile("fence.proxy.async;" ::: "memory");
         tc::cluster_sync();
