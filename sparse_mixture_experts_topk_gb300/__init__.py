@@ -435,12 +435,19 @@ def moe_adamw_step(tensors: AdamwTensors, params: MoeAdamwParams, grad_scale=Non
         _ptr(grad_scale), _ptr(skip), _stream(stream)))
 
 
+def _mask(fn, desc, mask):
+    # an address is taken as it is
+    if mask is not None and not isinstance(mask, int) and (mask.element_size() != 1 or mask.numel() != desc.T):
+        raise ValueError(f"{fn}: mask is not a byte for each of {desc.T} tokens")
+    return _ptr(mask)
+
+
 def moe_balance_loss(desc, logits, ids, mask, psum, count, tokens, loss, ws, stream=None):
     """The load-balancing loss over the tokens that ``mask`` ([T] ``bool`` or
     ``uint8``, or ``None``) keeps, with its counts and probability sums."""
     _check("moe_balance_loss", lib().moe_balance_loss(
-        ctypes.byref(desc), _ptr(logits), _ptr(ids), _ptr(mask), _ptr(psum), _ptr(count), _ptr(tokens), _ptr(loss),
-        _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+        ctypes.byref(desc), _ptr(logits), _ptr(ids), _mask("moe_balance_loss", desc, mask), _ptr(psum), _ptr(count),
+        _ptr(tokens), _ptr(loss), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
 
 
 def moe_router_backward_workspace_size(desc: MoeDesc) -> int:
@@ -466,7 +473,7 @@ def moe_router_backward(desc, x, Wg, logits, ids, dw, dloss, count, tokens, mask
                         stream=None):
     _check("moe_router_backward", lib().moe_router_backward(
         ctypes.byref(desc), _ptr(x), _ptr(Wg), _ptr(logits), _ptr(ids), _ptr(dw), _ptr(dloss), _ptr(count),
-        _ptr(tokens), _ptr(mask), _ptr(dlogits), _ptr(dWg), _ptr(dgate_bias), _ptr(dx), _ptr(ws),
+        _ptr(tokens), _mask("moe_router_backward", desc, mask), _ptr(dlogits), _ptr(dWg), _ptr(dgate_bias), _ptr(dx), _ptr(ws),
         ws.numel() if ws is not None else 0, _stream(stream)))
 
 

@@ -13,6 +13,11 @@
 // stays in the group.  What is summed over tokens leaves a block as one row of
 // partial sums; the rows are added in their order, so results are
 // deterministic.
+//
+// Long batches of many experts are bound by HBM and by the issue slots, half of
+// which are taken (131072 tokens of 256 experts, 138 MB: 26 us, with the sums
+// 31), short ones by the launches (8192 padded tokens of 32 experts: 6.7 us;
+// 64 tokens, which one block has: 4.8).
 #include <type_traits>
 
 #include "common.cuh"

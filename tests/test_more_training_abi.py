@@ -71,6 +71,17 @@ def test_router_backward_refuses():
         moe.moe_router_backward_workspace_size(desc(K=9, E=16))
 
 
+def test_a_mask_is_a_byte_for_each_token():
+    import torch
+    d = desc(T=4)
+    ws = Ws(A, moe.moe_router_backward_workspace_size(d))
+    for bad in (torch.ones(4), torch.ones(4, dtype=torch.int32), torch.ones(5, dtype=torch.bool)):
+        with pytest.raises(ValueError):
+            moe.moe_balance_loss(d, A, A, bad, A, A, A, A, ws, 0)
+        with pytest.raises(ValueError):
+            moe.moe_router_backward(d, A, A, A, A, A, A, A, A, bad, A, A, A, A, ws, 0)
+
+
 def test_orthogonalize_refuses():
     f = moe.lib().moe_orthogonalize
     n = moe.moe_orthogonalize_workspace_size(2, 30, 40)
