@@ -20,18 +20,16 @@
 // another one to be resident.  Launched one by one, the steps of a few small
 // matrices took twice as long, and those of many large ones lost their tails.
 //
-// Tiles are 256 x 256 on SM pairs (tcgen05 .cta_group::2), or 128 x 128 on
-// single SMs where those would leave SMs idle; fp32 accumulators in TMEM,
-// operands staged by TMA.  A and the short products read both operands along
+// Tiles are 256 x 256 on SM pairs (tcgen05 .cta_group::2), or 256 x 128 where
+// those would leave SMs idle; fp32 accumulators in TMEM, operands staged by TMA.  A and the short products read both operands along
 // their rows; X as the second operand of B X is read as it lies ("MN-major").
 //
 // What bounds it: 64 elements of a reduction take a tile's MMAs 512 cycles on a
 // pair, and the 32 KB for each SM that go with them as long at the 64 bytes a
-// cycle that L2 gives an SM (a tile of 128 x 128 loads as much for a quarter of
-// the work); with few matrices the latency of a step, 7 us beside its MMAs.
+// cycle that L2 gives an SM (half a tile loads 24 KB); with few matrices the latency of a step, 7 us beside its MMAs.
 // Measured: 16 matrices of 2560 x 3584 (6.3 TFLOP in the order below) 4.3 ms of
 // a Muon step's 4.9 to 5.1, 48 of 1408 x 4096 4.0 of 5.2 to 5.3; 3 matrices of
-// 1416 x 1001 222 us, 16 of 256 x 512 114 us, one of 64 x 96 18 us.
+// 1416 x 1001 201 us, 16 of 256 x 512 110 us, one of 64 x 96 18 us.
 //
 // Roles per CTA: warps 0 and 10 TMA producers, one for each operand, warp 1
 // MMA issuer (leader CTA of a pair), warps 2-9 epilogue.  Every wait is
@@ -156,25 +154,26 @@ __device__ __forceinline__ void put4(const Matrices& M, const Segment& S, int64_
 
 // ---------------------------------------------------------------- products
 
-constexpr int kBM = 128;                  // operand rows (or columns) per CTA
+constexpr int kRows = 256;                // of a tile
+constexpr int kBM = 128;                  // of them in a CTA
 constexpr int kBox = 64;                  // reduction elements of a box
 constexpr int kSub = 2;                   // boxes of an operand in a stage
 constexpr int kBK = kSub * kBox;          // reduction elements per stage
 constexpr int kGroup = 16;                // reduction elements per MMA
-constexpr int kBlock = kBM * kBox * 2;    // bytes of one operand's box
-constexpr int kOperand = kSub * kBlock;   // and of a stage's
-constexpr int kHalf = kBlock / 2;       // an MN-major operand is two boxes of 64 columns x 64 rows
-constexpr int kStages = 6 / kSub;
+constexpr int kBlock = kBM * kBox * 2;    // bytes of 128 rows of a box
+constexpr int kOperand = kSub * kBlock;   // and of a's in a stage
+constexpr int kHalf = kBlock / 2;         // a box of 64 columns x 64 rows: b read across is made of those
+constexpr int kRing = 6 * 2 * kBlock;     // bytes of all stages
 constexpr int kEpiWarps = 8;              // per CTA: two for each quarter of the TMEM lanes
 constexpr int kThreads = 64 + 32 * kEpiWarps + 32, kSecondProducer = 2 + kEpiWarps;
 constexpr int kStoreBytes = 32 * 128;     // an epilogue warp's 32 rows of 64 columns on their way to TMA, or their transpose
-constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kOperand + kEpiWarps * kStoreBytes;
+constexpr size_t kSmem = 1024 + (size_t)kRing + kEpiWarps * kStoreBytes;
 // The limit of a wait, and what it has on top for each stage of the tiles that a CTA has of a step: those may
 // have to be written first.
 constexpr uint64_t kWaitNs = 2000000000ull, kStageNs = 2000;
 constexpr int kQueue = 16, kNoTile = -1, kAborted = -2;
 
-// MN-major operand of 128 x 64: two boxes (64 columns of 128 bytes, 64 rows, 128-byte swizzle) one after the other.
+// MN-major operand: boxes of 64 columns (128 bytes, 128-byte swizzle) and 64 rows one after the other.
 __device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr) {
   return tc::sdesc_k128(saddr) | ((uint64_t)(kHalf >> 4) << 16);
 }
@@ -200,7 +199,7 @@ constexpr int kMaxSteps = 7 * MOE_ORTHOGONALIZE_MAX_ITERATIONS / 2;
 
 struct Chain {
   CUtensorMap along[kBuffers];   // boxes of 128 rows of 64 elements
-  CUtensorMap across[2];         // X and Y: 64 rows of 64 elements
+  CUtensorMap across[kBuffers];  // 64 rows of 64 elements
   CUtensorMap store[kBuffers];   // 32 rows of 64 elements
   CUtensorMap mirror[kBuffers];  // the symmetric ones: 64 rows of 32 elements, not swizzled
   __half* buf[kBuffers];
@@ -215,18 +214,22 @@ struct Chain {
 };
 
 // The tiles of a chain in the order in which they are taken.
-template <int kTile>
+// kN: columns of a tile.
+template <int kN>
 struct Tiles {
+  static constexpr int kSteps = kRows / kN;   // tiles beside the diagonal in a row of them
   const Chain& C;
-  int mt, nt;
+  int mt, nt, nL;      // rows of tiles, and columns over s and L
   int p, per;          // the step at hand, and its tiles of a matrix
   int64_t base;        // the first of its tiles (all are below 2^31: see Sizes::most)
   int matrix, m0, n0;
   __device__ explicit Tiles(const Chain& c)
-      : C(c), mt((c.s + kTile - 1) / kTile), nt((c.L + kTile - 1) / kTile), p(0), base(0) {
+      : C(c), mt((c.s + kRows - 1) / kRows), nt((c.s + kN - 1) / kN), nL((c.L + kN - 1) / kN), p(0), base(0) {
     per = tiles(0);
   }
-  __device__ int tiles(int step) const { return C.step[step].wide() ? mt * nt : mt * (mt + 1) / 2; }
+  __device__ int tiles(int step) const {
+    return C.step[step].wide() ? mt * nL : mt * nt - kSteps * (mt * (mt - 1) / 2);
+  }
   // Tile t, not before the last one asked for; false behind the last.
   __device__ bool seek(int64_t t) {
     while (t >= base + (int64_t)per * C.batch) {
@@ -241,25 +244,26 @@ struct Tiles {
       i = j % mt;
       j /= mt;
     } else {
-      while (j >= mt - i) {   // row i has mt - i tiles
-        j -= mt - i;
+      while (j >= nt - kSteps * i) {   // those of row i from the diagonal on
+        j -= nt - kSteps * i;
         ++i;
       }
-      j += i;
+      j += kSteps * i;
     }
-    m0 = i * kTile;
-    n0 = j * kTile;
+    m0 = i * kRows;
+    n0 = j * kN;
     return true;
   }
   __device__ int k() const { return C.step[p].gram ? C.L : C.s; }
   __device__ int cols() const { return C.step[p].wide() ? C.L : C.s; }
   // Columns of an MMA: those that the tile has, to 16; to whole groups of 64 for each CTA where b is read across
   __device__ int mma_n() const {
-    const int to = !C.step[p].mn() ? 16 : kTile / 2;
-    return min(kTile, (cols() - n0 + to - 1) / to * to);
+    const int to = C.step[p].mn() ? 128 : 16;
+    return min(kN, (cols() - n0 + to - 1) / to * to);
   }
 };
 
+template <int kStages>
 __device__ __forceinline__ void advance(int& stage, uint32_t& phase) {
   if (++stage == kStages) {
     stage = 0;
@@ -337,20 +341,21 @@ __device__ __forceinline__ void finish(const Matrices& M, const Segment& S, int6
   }
 }
 
-// kPair: tiles of 256 x 256 on the two CTAs of a cluster, else of 128 x 128.
-template <bool kPair>
+// Tiles of 256 x kN on the two CTAs of a cluster.
+template <int kN>
 __global__ void __launch_bounds__(kThreads, 1)
 chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M) {
-  constexpr int kTile = kPair ? 256 : 128, kCtas = kPair ? 2 : 1;
-  constexpr int kChunks = kTile / 128;   // of 64 columns, for each of a lane quarter's two epilogue warps
-  constexpr uint32_t kTmemCols = 2 * kTile;
+  constexpr int kChunks = kN / 128;   // of 64 columns, for each of a lane quarter's two epilogue warps
+  constexpr int kBlockB = kN / 2 * kBox * 2, kOperandB = kSub * kBlockB;   // b's part in a CTA, as kBlock and kOperand
+  constexpr int kStages = kRing / (kOperand + kOperandB);
+  constexpr uint32_t kTmemCols = 2 * kN;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ unsigned long long s_queue[kQueue];
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u, sB = sA + kStages * kOperand;
-  const uint32_t sOut = sB + kStages * kOperand;
+  const uint32_t sOut = sB + kStages * kOperandB;
   const uint32_t bars = tc::smem_u32(s_bar);
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kStages + s); };
@@ -358,10 +363,9 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
   auto tempty = [&](int a) { return bars + 8 * (2 * kStages + 2 + a); };
   const uint32_t done = bars + 8 * (2 * kStages + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = kPair ? (int)tc::cluster_ctarank() : 0;
+  const int rank = (int)tc::cluster_ctarank();
   auto commit = [&](uint32_t bar) {
-    if (kPair) tc::tc_commit_pair_mc(bar, 0x3);
-    else tc::tc_commit(bar);
+    tc::tc_commit_pair_mc(bar, 0x3);
   };
 
   pdl_enter();
@@ -374,7 +378,7 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
       }
       for (int a = 0; a < 2; ++a) {
         tc::mbar_init(tfull(a), 1);
-        tc::mbar_init(tempty(a), kCtas * kEpiWarps);   // one arrival for each epilogue warp
+        tc::mbar_init(tempty(a), 2 * kEpiWarps);   // one arrival for each epilogue warp of the pair
       }
       tc::mbar_init(done, 1);
       for (int i = 0; i < kQueue; ++i) s_queue[i] = 0;
@@ -383,27 +387,22 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
       tc::fence_proxy_async_smem();
     }
   } else if (warp == 1) {
-    if (kPair) {
-      tc::tmem_alloc_pair(tc::smem_u32(&s_tmem), kTmemCols);
-      tc::tmem_relinquish_pair();
-    } else {
-      tc::tmem_alloc(tc::smem_u32(&s_tmem), kTmemCols);
-      tc::tmem_relinquish();
-    }
+    tc::tmem_alloc_pair(tc::smem_u32(&s_tmem), kTmemCols);
+    tc::tmem_relinquish_pair();
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (kPair) tc::cluster_sync();
+  tc::cluster_sync();
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
-  Tiles<kTile> T(C);
+  Tiles<kN> T(C);
   // The leader's first producer takes tiles and publishes each, or kNoTile at
   // the end, as an entry of a queue in both CTAs; the other roles read it there.
   // No role is kQueue tiles behind: two accumulators and kStages stages at most.
   auto publish = [&](int seq, int t) {
     const unsigned long long v = (unsigned long long)(unsigned)(seq + 1) << 32 | (unsigned)t;
     *(volatile unsigned long long*)&s_queue[seq % kQueue] = v;
-    if (kPair) tc::st_peer_u64(tc::map_peer(tc::smem_u32(&s_queue[seq % kQueue]), 1), v);
+    tc::st_peer_u64(tc::map_peer(tc::smem_u32(&s_queue[seq % kQueue]), 1), v);
   };
   auto read = [&](int seq) {   // kAborted if it does not come
     volatile unsigned long long* slot = &s_queue[seq % kQueue];
@@ -416,7 +415,7 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
   };
   // the counter of the step before a tile's, and what it has to reach
   auto before = [&]() { return C.written + (int64_t)(T.p - 1) * C.batch + T.matrix; };
-  auto need = [&]() { return T.tiles(T.p - 1) * kCtas * kEpiWarps; };
+  auto need = [&]() { return T.tiles(T.p - 1) * 2 * kEpiWarps; };
 
   uint32_t filled = 0, fill_par = 0;
   bool producer = false;
@@ -451,7 +450,8 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
         }
         const Step& S = C.step[T.p];
         const bool mn = second && S.mn();
-        const CUtensorMap* map = mn ? &C.across[S.b] : &C.along[second ? S.b : S.a];
+        // b's part of a tile of 128 columns is 64 rows, too
+        const CUtensorMap* map = mn || (second && kN == 128) ? &C.across[S.b] : &C.along[second ? S.b : S.a];
         // b's columns are split evenly between the CTAs
         const int r = second ? T.n0 + rank * (T.mma_n() / 2) : T.m0 + rank * kBM;
         const int nk = (T.k() + kBK - 1) / kBK;
@@ -460,25 +460,24 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
             ok = false;
             break;
           }
-          if (rank == 0 && !second) tc::mbar_arrive_expect_tx(full(stage), 2 * kCtas * kOperand);
-          const uint32_t at = to + stage * kOperand;
+          if (rank == 0 && !second) tc::mbar_arrive_expect_tx(full(stage), 2 * (kOperand + kOperandB));
+          const uint32_t at = to + stage * (second ? kOperandB : kOperand);
           auto load = [&](uint32_t dst, int c0, int c1) {
-            if (kPair) tc::tma_load_3d_pair(dst, map, tc::map_peer(full(stage), 0), c0, c1, T.matrix);
-            else tc::tma_load_3d(dst, map, full(stage), c0, c1, T.matrix);
+            tc::tma_load_3d_pair(dst, map, tc::map_peer(full(stage), 0), c0, c1, T.matrix);
           };
 #pragma unroll
           for (int u = 0; u < kSub; ++u) {
             const int k = kb * kBK + u * kBox;
             if (mn) {
-              load(at + u * kBlock, r, k);
-              load(at + u * kBlock + kHalf, r + 64, k);
+              load(at + u * kBlockB, r, k);
+              if (kN == 256) load(at + u * kBlockB + kHalf, r + 64, k);
             } else {
-              load(at + u * kBlock, k, r);
+              load(at + u * (second ? kBlockB : kBlock), k, r);
             }
           }
           filled |= 1u << stage;
           fill_par = (fill_par & ~(1u << stage)) | (phase << stage);
-          advance(stage, phase);
+          advance<kStages>(stage, phase);
         }
       }
       if (!ok) give_up(C.err, &s_abort);
@@ -499,14 +498,14 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
         const bool mn = C.step[T.p].mn();
         const uint64_t b0 = mn ? sdesc_mn128(sB) : tc::sdesc_k128(sB);
         const uint32_t as = kStepK >> 4, bs = (mn ? kStepMN : kStepK) >> 4;
-        const uint32_t idesc = idesc_f16_f32(kTile, T.mma_n()) | (mn ? kMajorB : 0u);
+        const uint32_t idesc = idesc_f16_f32(kRows, T.mma_n()) | (mn ? kMajorB : 0u);
         const int k = T.k(), nk = (k + kBK - 1) / kBK;
         if (!tc::mbar_wait(tempty(acc), acc_phase ^ 1u, &s_abort, C.limit)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
-        const uint32_t dst = tmem + (uint32_t)(acc * kTile);
+        const uint32_t dst = tmem + (uint32_t)(acc * kN);
 #pragma unroll 1
         for (int kb = 0; kb < nk; ++kb) {
           if (!ready && !tc::mbar_wait(full(stage), phase, &s_abort, C.limit)) {
@@ -514,16 +513,15 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
             break;
           }
           const int here = stage, ng = min(kBK / kGroup, (k - kb * kBK + kGroup - 1) / kGroup);
-          advance(stage, phase);
+          advance<kStages>(stage, phase);
           // looked at under the MMAs still running (the wait itself costs 200 cycles)
           ready = tc::mbar_test_wait(full(stage), phase);
-          const uint64_t a = a0 + (uint32_t)(here * (kOperand >> 4)), b = b0 + (uint32_t)(here * (kOperand >> 4));
+          const uint64_t a = a0 + (uint32_t)(here * (kOperand >> 4)), b = b0 + (uint32_t)(here * (kOperandB >> 4));
 #pragma unroll
           for (int g = 0; g < kBK / kGroup; ++g) {
             if (g < ng) {
-              const uint32_t sub = g / (kBox / kGroup) * (kBlock >> 4), in = g % (kBox / kGroup);
-              if (kPair) tc::mma_bf16_pair(dst, a + sub + in * as, b + sub + in * bs, idesc, g || kb);
-              else tc::mma_bf16(dst, a + sub + in * as, b + sub + in * bs, idesc, g || kb);
+              const uint32_t sub = g / (kBox / kGroup), in = g % (kBox / kGroup);
+              tc::mma_bf16_pair(dst, a + sub * (kBlock >> 4) + in * as, b + sub * (kBlockB >> 4) + in * bs, idesc, g || kb);
             }
           }
           commit(empty(here));
@@ -551,7 +549,7 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
       T.seek(t);
       const Step& S = C.step[T.p];
       const int cols = T.cols(), row0 = T.m0 + rank * kBM + q * 32, row = row0 + lane;
-      const bool mirror = !S.wide() && T.m0 != T.n0;
+      const bool mirror = !S.wide() && T.n0 >= T.m0 + kRows;
       const __half* add = S.add >= 0 && row < C.s
                               ? C.buf[S.add] + T.matrix * C.square_plane + row * C.square : nullptr;
       // 32 elements of the addend; rows are padded to 8: a vector that starts inside the row lies inside it
@@ -574,7 +572,7 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
         break;
       }
       tc::tc_fence_after();
-      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTile + half * kChunks * 64);
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kN + half * kChunks * 64);
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
         const int col = first_col + c * 64;
@@ -678,11 +676,10 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
     }
   }
   __syncwarp();                     // the cluster's barrier takes whole warps
-  if (kPair) tc::cluster_sync();    // neither CTA leaves while the other may still signal it
+  tc::cluster_sync();               // neither CTA leaves while the other may still signal it
   if (warp == 1) {
     tc::tc_fence_after();
-    if (kPair) tc::tmem_dealloc_pair(tmem, kTmemCols);
-    else tc::tmem_dealloc(tmem, kTmemCols);
+    tc::tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
@@ -718,16 +715,15 @@ void plan_steps(Chain& C, int iterations, bool pairs) {
   C.steps = n;
 }
 
-template <bool kPair>
+template <int kN>
 cudaError_t launch_chain(Chain& C, const Matrices& M, int64_t tiles, cudaStream_t st) {
-  constexpr int kCtas = kPair ? 2 : 1;
-  const int64_t most = sm_count() / kCtas, ctas = tiles < most ? tiles : most;
+  const int64_t most = sm_count() / 2, pairs = tiles < most ? tiles : most;
   const int64_t stages = (C.L + kBK - 1) / kBK;
-  C.limit = kWaitNs + (uint64_t)((tiles / ctas + 2) * stages) * kStageNs;
-  auto kern = chain_kernel<kPair>;
+  C.limit = kWaitNs + (uint64_t)((tiles / pairs + 2) * stages) * kStageNs;
+  auto kern = chain_kernel<kN>;
   const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (r != cudaSuccess) return r;
-  return launch_kernel(kern, dim3((unsigned)(kCtas * ctas)), dim3(kThreads), kSmem, st, kCtas, C, M);
+  return launch_kernel(kern, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem, st, 2, C, M);
 }
 
 // ---------------------------------------------------------------- before the products
@@ -1330,29 +1326,30 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
                           x ? C.plane : C.square_plane, kBM) ||
         !tma_map_16bit_3d(&C.store[i], C.buf[i], n, z.s, x ? z.L : z.s, x ? z.pitch : z.square,
                           x ? C.plane : C.square_plane, 32) ||
-        (x && !tma_map_16bit_3d(&C.across[i], C.buf[i], n, z.s, z.L, z.pitch, C.plane, kBox)) ||
+        !tma_map_16bit_3d(&C.across[i], C.buf[i], n, z.s, x ? z.L : z.s, x ? z.pitch : z.square,
+                          x ? C.plane : C.square_plane, kBox) ||
         (!x && !tma_map_16bit_3d(&C.mirror[i], C.buf[i], n, z.s, z.s, z.square, C.square_plane, 64, 32)))
       return cudaErrorNotSupported;
   }
-  // Which of the two tiles takes less time by their number: 64 elements of the
-  // reduction of a pair's tile take 600 cycles, of a single one's 540 (a quarter
-  // of the work, but both load 32 KB for each SM, and L2 gives an SM 64 bytes a
-  // cycle), and a step's start with the epilogue of its last tile 12000 and
-  // 6500.  Single tiles win where the pairs' would leave most SMs idle.
-  auto tiles_of = [&](int tile, bool wide) {
-    const int64_t mt = (z.s + tile - 1) / tile, nt = (z.L + tile - 1) / tile;
-    return n * (wide ? mt * nt : mt * (mt + 1) / 2);
+  // Tiles of 256 or of 128 columns, whichever take less time by their number: 64
+  // elements of the reduction take 600 cycles with 256 columns and 420 with 128
+  // (half of the work, but 24 KB for each SM instead of 32, and L2 gives an SM 64
+  // bytes a cycle), and a step's start with the epilogue of its last tile 12000
+  // and 9000.
+  auto tiles_of = [&](int cols, bool wide) {
+    const int64_t mt = (z.s + kRows - 1) / kRows, nt = (z.s + cols - 1) / cols, nL = (z.L + cols - 1) / cols;
+    return n * (wide ? mt * nL : mt * nt - kRows / cols * (mt * (mt - 1) / 2));
   };
-  const int64_t pair_tiles = tiles_of(256, true), single_tiles = tiles_of(128, true), sms = sm_count();
-  auto cost = [&](int64_t wide, int64_t shorts, int64_t ctas, int64_t stage, int64_t start) {
+  const int64_t most = sm_count() / 2;
+  auto cost = [&](int cols, int64_t stage, int64_t start) {
     const int64_t a = (z.L + kBox - 1) / kBox, b = (z.s + kBox - 1) / kBox;
-    return ((shorts + ctas - 1) / ctas * (a + b) + (wide + ctas - 1) / ctas * b) * stage + 3 * start;
+    const int64_t wide = (tiles_of(cols, true) + most - 1) / most, shorts = (tiles_of(cols, false) + most - 1) / most;
+    return (shorts * (a + b) + wide * b) * stage + 3 * start;
   };
-  const bool pair = cost(pair_tiles, tiles_of(256, false), sms / 2, 600, 12000) <=
-                    cost(single_tiles, tiles_of(128, false), sms, 540, 6500);
+  const bool broad = cost(256, 600, 12000) <= cost(128, 420, 9000);
   // Two iterations at a time where the products with X are longer by enough and
   // the short ones fill the SMs.
-  const bool pairs = 4 * (int64_t)z.L >= 5 * (int64_t)z.s && pair && tiles_of(256, false) >= sms / 2;
+  const bool pairs = 4 * (int64_t)z.L >= 5 * (int64_t)z.s && tiles_of(256, false) >= most;
   plan_steps(C, iterations, pairs);
   const dim3 sums((unsigned)(n * z.parts)), tiles((unsigned)((int64_t)n * M.tiles_s * M.tiles_L)), threads(256);
   cudaError_t e = grad_bf16 ? launch_kernel(momentum_kernel<bf16>, sums, threads, 0, st, 1, M, part)
@@ -1362,7 +1359,7 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
     e = grad_bf16 ? launch_kernel(build_kernel<bf16>, tiles, threads, 0, st, 1, M, factor, C.buf[kX])
                   : launch_kernel(build_kernel<float>, tiles, threads, 0, st, 1, M, factor, C.buf[kX]);
   if (e != cudaSuccess) return e;
-  return pair ? launch_chain<true>(C, M, pair_tiles, st) : launch_chain<false>(C, M, single_tiles, st);
+  return broad ? launch_chain<256>(C, M, tiles_of(256, true), st) : launch_chain<128>(C, M, tiles_of(128, true), st);
 }
 
 }  // namespace
