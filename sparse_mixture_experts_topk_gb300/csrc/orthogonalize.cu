@@ -293,7 +293,10 @@ __device__ __forceinline__ bool wait_written(const int* counter, int need, volat
 
 // 32 rows and 64 columns of the result, from (row0, col) of X on, to the
 // tensor, by one warp: turned through its buffer so that the lanes' accesses lie
-// along the tensor's rows.  packed: this lane's row, as held.
+// along the tensor's rows.  packed: this lane's row, as held.  kWhole: with a
+// loop of its own for what lies inside the tensor (where the epilogue's
+// instructions count; cold code costs a few short products 2 %).
+template <bool kWhole>
 __device__ __forceinline__ void finish(const Matrices& M, const Segment& S, int64_t base, uint8_t* buf,
                                        const uint32_t (&packed)[2][16], int row0, int col, int lane) {
   const bool flip = S.rows > S.cols, even = S.cols % 4 == 0;
@@ -314,6 +317,40 @@ __device__ __forceinline__ void finish(const Matrices& M, const Segment& S, int6
   }
   __syncwarp();
   // four elements of a row to a lane, 16 or 8 lanes to a row; eight loads in flight
+  const int tr0 = flip ? col : row0, tc0 = flip ? row0 : col, along = flip ? 8 : 16;
+  if (kWhole && !M.raw && even && aligned_to(S.p, 16) && aligned_to(S.p16, 8) && tr0 + 512 / along <= S.rows &&
+      tc0 + 4 * along <= S.cols) {
+    // all of it lies inside: with the bounds and alignments of each group
+    // checked, the instructions of this took longer than a tile's MMAs
+    const int r = lane / along, x = lane % along;
+    const int64_t e = base + (int64_t)(tr0 + r) * S.cols + tc0 + x * 4, step = (int64_t)(32 / along) * S.cols;
+    float4* p = reinterpret_cast<float4*>(S.p + e);
+    uint2* p16 = S.p16 ? reinterpret_cast<uint2*>(S.p16 + e) : nullptr;
+    const float keep = S.keep, by = S.step * (1.f / kHeld);
+#pragma unroll 1
+    for (int i0 = 0; i0 < 16; i0 += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __ldcs(p + (i0 + i) * step / 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = (i0 + i) * (32 / along) + r;
+        const uint2 u = *reinterpret_cast<const uint2*>(
+            buf + (flip ? row * 64 + ((x ^ (row & 7)) << 3) : row * 128 + (((x >> 1) ^ (row & 7)) << 4) + (x & 1) * 8));
+        const __half2* h = reinterpret_cast<const __half2*>(&u);
+        const float2 a = __half22float2(h[0]), b = __half22float2(h[1]);
+        v[i] = make_float4(v[i].x * keep - by * a.x, v[i].y * keep - by * a.y, v[i].z * keep - by * b.x,
+                           v[i].w * keep - by * b.y);
+        __stcs(p + (i0 + i) * step / 4, v[i]);
+        if (p16) {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v[i].x, v[i].y), hi = __floats2bfloat162_rn(v[i].z, v[i].w);
+          __stcs(p16 + (i0 + i) * step / 4,
+                 make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)));
+        }
+      }
+    }
+    return;
+  }
 #pragma unroll 1
   for (int i0 = 0; i0 < 16; i0 += 8) {
     float p[8][4];
@@ -621,7 +658,7 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
         if (T.p == C.steps - 1) {
           // the result goes straight to the tensor
           const Segment& D = segment_of(M, T.matrix);
-          finish(M, D, (int64_t)(T.matrix - D.first) * D.rows * D.cols, mine, packed, row0, col, lane);
+          finish<kN == 256>(M, D, (int64_t)(T.matrix - D.first) * D.rows * D.cols, mine, packed, row0, col, lane);
           continue;
         }
         if (lane == 0) tc::bulk_wait_read();   // the buffer's previous store has been read
