@@ -983,7 +983,7 @@ __device__ __forceinline__ float4 ld_peer_f32x4(uint32_t addr) {
 
 template <typename T>
 __global__ void __launch_bounds__(kSmallThreads, 1)
-small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
+small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int* err) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ __align__(8) uint64_t s_bar;
@@ -1011,7 +1011,14 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  pdl_enter();
+  // A call's launches of this kernel have nothing to do with one another, nor
+  // with the products of larger matrices before them: but for one that opens the
+  // call they start beside what is before them, and end behind it.  (What was on
+  // the stream before the call is complete: the call's first kernel waits for
+  // that before it lets another start.  24 matrices of up to 2048 to a side:
+  // 253 us one after another, of which 120 are one larger matrix'.)
+  if (opens) pdl_wait();
+  pdl_trigger();
   const uint32_t tmem = s_tmem;
   const bool skip = M.skip && *M.skip;   // the same for every thread of the cluster
 
@@ -1269,6 +1276,8 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, int* err) {
            put4(M, S, first + a.o, even, a.left, p, v);
          });
   }
+  if (!opens) pdl_wait();
+  __syncwarp();
   if (ctas > 1) tc::cluster_sync();   // no CTA leaves while another may still read its shared memory
   if (warp == 0) {
     __syncwarp();
@@ -1470,18 +1479,7 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
     }
     return held ? run() : cudaSuccess;
   };
-  for (int ctas = 1; ctas <= kMostCtas; ctas *= 2) {
-    const cudaError_t e = collect(
-        0, 1 << 24, [&](const moe_muon_tensor& t) { return !empty(t) && small_ctas(t) == ctas; },
-        [&]() {
-          auto kern = grad_dtype == MOE_BF16 ? small_kernel<bf16> : small_kernel<float>;
-          const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
-          if (r != cudaSuccess) return r;
-          return launch_kernel(kern, dim3((unsigned)(held * ctas)), dim3(kSmallThreads), kSmallSmem, st, (unsigned)ctas, M,
-                               (int)h.iterations, (int*)ws);
-        });
-    if (e != cudaSuccess) return e;
-  }
+  bool opens = true;   // the call with its next launch
   for (int i = 0; i < count; ++i) {
     if (!leads(tensors, i)) continue;
     const Sizes z(tensors[i].rows, tensors[i].cols);
@@ -1492,9 +1490,24 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
     M.parts = z.parts;
     M.tiles_s = (z.s + 63) / 64;
     M.tiles_L = (z.L + 63) / 64;
+    opens = false;
     const cudaError_t e = collect(
         i, z.most(), [&](const moe_muon_tensor& t) { return large(t) && alike(tensors[i], t); },
         [&]() { return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, (char*)ws, st); });
+    if (e != cudaSuccess) return e;
+  }
+  for (int ctas = 1; ctas <= kMostCtas; ctas *= 2) {
+    const cudaError_t e = collect(
+        0, 1 << 24, [&](const moe_muon_tensor& t) { return !empty(t) && small_ctas(t) == ctas; },
+        [&]() {
+          auto kern = grad_dtype == MOE_BF16 ? small_kernel<bf16> : small_kernel<float>;
+          const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
+          if (r != cudaSuccess) return r;
+          const bool now = opens;
+          opens = false;
+          return launch_kernel(kern, dim3((unsigned)(held * ctas)), dim3(kSmallThreads), kSmallSmem, st, (unsigned)ctas, M,
+                               (int)h.iterations, now, (int*)ws);
+        });
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
