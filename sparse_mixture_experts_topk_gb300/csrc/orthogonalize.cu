@@ -6,7 +6,8 @@
 // B is a polynomial of the symmetric A, so A and B are symmetric: their tiles
 // below the diagonal are the mirrored ones above it and are not computed.
 //
-// X, A and B are held in fp16 times 2^12.  Their values are at most 1.21, 1.46
+// X, A and B are held in fp16 times 2^12 (but in fp32 on the CUDA cores for a
+// short side of up to 16, see small_kernel).  Their values are at most 1.21, 1.46
 // and 3.45 in magnitude (no singular value passes 1.21), those of a product of
 // two B at most 11.9 of the 15.9 that fit, and nothing above 2^-26 loses bits;
 // fp16 has three bits more than bf16 at the same rate of the tensor cores.
@@ -964,7 +965,19 @@ build_kernel(const __grid_constant__ Matrices M, const float2* __restrict__ fact
 // What bounds it is the chain of products, each of which waits for the one
 // before: 2.3 us an iteration for 64 x 96, 4.6 for 128 x 512 (of 18 and 44 us
 // with five), 7 to 9 with several CTAs (128 x 4096: 67 us).
+//
+// With a short side of at most 16 an MMA is mostly padding: X stays in fp32, and
+// the products are the CUDA cores', exact to fp32 (held in fp16 a vector is 1e-3
+// off, a matrix of two rows up to 4e-3).  X X^T by warps, in blocks of 4 x 4
+// elements whose sums over the lanes take 16 exchanges; B by a thread for each
+// element; B X by a thread for each column, which it keeps in registers.  One
+// iteration of 16 x 16 takes 1.8 us (MMAs 2.0), 16 x 512 3.5 (4.6), 16 x 4096
+// 4.7 (8.8); 64 matrices of 16 x 4096 96 us with five (276).
 constexpr int kSide = 128, kPanel = kSide * 128, kSlice = 512, kMostCtas = 8, kSmallThreads = 512;
+// Short sides of at most kThinSide are left to the CUDA cores, in fp32.
+constexpr int kThinSide = 16, kThinPitch = kSlice + 4, kThinSums = kSmallThreads / 2;
+constexpr size_t kThinSmem =
+    4 * (size_t)(kThinSide * kThinPitch + 2 * kMostCtas * kThinSums + kThinSide * (2 * kThinSide + 1));
 constexpr size_t kSmallSmem = 1024 + (size_t)(kSlice / 64 + 6) * kPanel;
 
 // Byte offset of elements (row, col) .. (col a multiple of 4) in panels.
@@ -981,8 +994,8 @@ __device__ __forceinline__ float4 ld_peer_f32x4(uint32_t addr) {
   return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kSmallThreads, 1)
+template <typename T, bool kThin>
+__global__ void __launch_bounds__(kSmallThreads, kThin ? 2 : 1)
 small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int* err) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -997,20 +1010,30 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
   const int rank = (int)tc::cluster_ctarank();
   uint32_t ctas;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
-  if (warp == 0) {
-    if (lane == 0) {
-      tc::mbar_init(bar, 1);
-      tc::fence_barrier_init();
+  // thin: X in fp32, two sets of every warp's sums of X X^T, B and A
+  float* const thin_x = reinterpret_cast<float*>(smem_raw);
+  float* const thin_sums = thin_x + kThinSide * kThinPitch;
+  float* const thin_b = thin_sums + 2 * kMostCtas * kThinSums;
+  float* const thin_a = thin_b + kThinSide * kThinSide;
+  if (kThin) {
+    for (int i = threadIdx.x; i < kThinSide * kThinPitch / 4; i += kSmallThreads)
+      reinterpret_cast<float4*>(thin_x)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  } else {
+    if (warp == 0) {
+      if (lane == 0) {
+        tc::mbar_init(bar, 1);
+        tc::fence_barrier_init();
+      }
+      __syncwarp();
+      tc::tmem_alloc(tc::smem_u32(&s_tmem), 512);
+      tc::tmem_relinquish();
     }
-    __syncwarp();
-    tc::tmem_alloc(tc::smem_u32(&s_tmem), 512);
-    tc::tmem_relinquish();
+    for (int i = threadIdx.x; i < kSlice / 64 * kPanel / 16; i += kSmallThreads)
+      reinterpret_cast<uint4*>(X)[i] = make_uint4(0u, 0u, 0u, 0u);
+    tc::tc_fence_before();
   }
-  for (int i = threadIdx.x; i < kSlice / 64 * kPanel / 16; i += kSmallThreads)
-    reinterpret_cast<uint4*>(X)[i] = make_uint4(0u, 0u, 0u, 0u);
-  tc::tc_fence_before();
   __syncthreads();
-  tc::tc_fence_after();
+  if (!kThin) tc::tc_fence_after();
   // A call's launches of this kernel have nothing to do with one another, nor
   // with the products of larger matrices before them: but for one that opens the
   // call they start beside what is before them, and end behind it.  (What was on
@@ -1019,7 +1042,7 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
   // 253 us one after another, of which 120 are one larger matrix'.)
   if (opens) pdl_wait();
   pdl_trigger();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = kThin ? 0 : s_tmem;
   const bool skip = M.skip && *M.skip;   // the same for every thread of the cluster
 
   const int matrix = blockIdx.x / ctas;
@@ -1112,6 +1135,18 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
         if (!M.raw) u[x] = M.nesterov ? fmaf(M.mu, mm[x], u[x] * scale) : mm[x];
         u[x] = x < p.left ? u[x] * f.x * f.y : 0.f;
       }
+      if (kThin) {   // as it is, not times 2^12
+#pragma unroll
+        for (int x = 0; x < 4; ++x) u[x] *= 1.f / kHeld;
+        if (flip) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (x < p.left) thin_x[(p.c + x) * kThinPitch + p.r] = u[x];
+        } else {
+          *reinterpret_cast<float4*>(thin_x + p.r * kThinPitch + p.c) = make_float4(u[0], u[1], u[2], u[3]);
+        }
+        return;
+      }
       const uint2 h = pack_half4(u);
       if (flip) {
         const __half* e = reinterpret_cast<const __half*>(&h);
@@ -1123,142 +1158,238 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
       }
     });
 
-    uint32_t phase = 0;
-    // What the threads wrote to shared memory is there for the MMAs that `issue` starts; returns when they are done.
-    auto products = [&](auto issue) {
-      tc::fence_proxy_async_smem();
-      tc::tc_fence_before();
+    if constexpr (kThin) {
+      // A = X X^T in blocks of 4 x 4 on and above the diagonal, each the work of `parts` warps, which share the
+      // columns: this warp has every parts-th 32 columns of block (bi, bj).
+      const int side = (s + 3) / 4, blocks = side * (side + 1) / 2, parts = kSmallThreads / 32 / blocks;
+      const int mine = warp / blocks;
+      int bi = 0, bj = warp % blocks;
+      while (bj >= side - bi) bj -= side - bi++;
+      bj += bi;
       __syncthreads();
-      if (warp == 0 && tc::elect_one()) {
-        tc::tc_fence_after();
-        issue();
-        tc::tc_commit(bar);
-      }
-      __syncwarp();
-      if (!tc::mbar_wait(bar, phase, nullptr, kWaitNs)) set_error(err, kDevTimeout);
-      phase ^= 1u;
-      __syncwarp();
-      tc::tc_fence_after();
-    };
-    const int row = q * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    // 32 values of this thread's row to columns col .. of panels
-    auto keep32 = [&](uint8_t* to, int col, const float* v) {
+      float x[kThinSide];   // this thread's column
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint4 u;
-        __half2* h = reinterpret_cast<__half2*>(&u);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) h[x] = __floats2half2_rn(v[j * 8 + 2 * x], v[j * 8 + 2 * x + 1]);
-        *reinterpret_cast<uint4*>(to + panel_at(row, col + j * 8)) = u;
-      }
-    };
-    constexpr float back = 1.f / kHeld;
+      for (int n = 0; n < kThinSide; ++n) x[n] = thin_x[n * kThinPitch + threadIdx.x];
 #pragma unroll 1
-    for (int it = 0; it < iterations; ++it) {
-      // A = X X^T
-      products([&]() {
-        const int steps = (w + 15) / 16;
-        for (int k = 0; k < steps; ++k) {
-          const uint64_t d = tc::sdesc_k128(sX + k / 4 * kPanel) + (uint32_t)(k % 4 * 2);
-          tc::mma_bf16(tmem, d, d, idesc_f16_f32(kSide, kSide), k > 0);
-        }
-      });
-      uint32_t r[32];
-      tc::tmem_ld_32x32b_x32(lanes + part * 32, r);
-      tc::tmem_wait_ld();
-      if (ctas == 1) {
-        float v[32];
+      for (int it = 0; it < iterations; ++it) {
+        float* sums = thin_sums + (it & 1) * kMostCtas * kThinSums;
+        if (mine < parts) {
+          float v[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = back * __uint_as_float(r[j]);
-        keep32(A, part * 32, v);
-      } else {
-        // partial sums: 128 rows of 128 fp32, 16 bytes of a row exchanged by the row's number
-        float4* sums = reinterpret_cast<float4*>(B);
+          for (int n = 0; n < 16; ++n) v[n] = 0.f;
+#pragma unroll 2
+          for (int c = mine * 32 + lane; c < w; c += parts * 32) {
+            float e[4], o[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                                       __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-          sums[row * 32 + ((part * 8 + j) ^ (row & 31))] = w > 0 ? v : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int n = 0; n < 4; ++n) {
+              e[n] = thin_x[(bi * 4 + n) * kThinPitch + c];
+              o[n] = thin_x[(bj * 4 + n) * kThinPitch + c];
+            }
+#pragma unroll
+            for (int n = 0; n < 16; ++n) v[n] = fmaf(e[n / 4], o[n % 4], v[n]);
+          }
+          // over the lanes: lanes 2 n and 2 n + 1 end with value n
+#pragma unroll
+          for (int half = 8; half > 0; half /= 2) {
+            const bool up = lane & (2 * half);
+#pragma unroll
+            for (int n = 0; n < half; ++n) {
+              const float give = up ? v[n] : v[n + half], keep = up ? v[n + half] : v[n];
+              v[n] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * half);
+            }
+          }
+          v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+          const uint32_t to = tc::smem_u32(sums + rank * kThinSums + warp * 16 + lane / 2);
+          for (uint32_t r = lane & 1; r < ctas; r += 2) tc::st_peer_f32(tc::map_peer(to, r), v[0]);
         }
+        __syncwarp();
+        if (ctas > 1) tc::cluster_sync();
+        else __syncthreads();
+        const int i = threadIdx.x / kThinSide, j = threadIdx.x % kThinSide;   // of A and B, 256 threads
+        if (i < kThinSide) {
+          float v = 0.f;
+          const int lo = min(i / 4, j / 4), hi = max(i / 4, j / 4);
+          if (hi < side) {
+            const int block = lo * side - lo * (lo - 1) / 2 + hi - lo;
+            const int at = block * 16 + (i / 4 <= j / 4 ? i % 4 * 4 + j % 4 : j % 4 * 4 + i % 4);
+            for (uint32_t r = 0; r < ctas; ++r)
+              for (int n = 0; n < parts; ++n) v += sums[r * kThinSums + n * blocks * 16 + at];
+          }
+          thin_a[i * (kThinSide + 1) + j] = v;
+        }
+        __syncthreads();
+        // B = a I + b A + c A A
+        if (i < kThinSide) {
+          float v[2] = {0.f, 0.f};
+#pragma unroll
+          for (int n = 0; n < kThinSide; ++n)
+            v[n & 1] = fmaf(thin_a[i * (kThinSide + 1) + n], thin_a[n * (kThinSide + 1) + j], v[n & 1]);
+          thin_b[i * kThinSide + j] =
+              kC * (v[0] + v[1]) + kB * thin_a[i * (kThinSide + 1) + j] + (i == j ? kA : 0.f);
+        }
+        __syncthreads();
+        // X = B X: a thread for a column
+        if ((int)threadIdx.x < w) {
+          float y[kThinSide];
+#pragma unroll
+          for (int r = 0; r < kThinSide; ++r) {
+            y[r] = 0.f;
+            if (r >= s) continue;
+#pragma unroll
+            for (int n = 0; n < kThinSide; n += 4) {
+              const float4 e = *reinterpret_cast<const float4*>(thin_b + r * kThinSide + n);
+              y[r] = fmaf(e.x, x[n], fmaf(e.y, x[n + 1], fmaf(e.z, x[n + 2], fmaf(e.w, x[n + 3], y[r]))));
+            }
+            thin_x[r * kThinPitch + threadIdx.x] = y[r];
+          }
+#pragma unroll
+          for (int r = 0; r < kThinSide; ++r) x[r] = y[r];
+        }
+        __syncthreads();
+      }
+    } else {
+      uint32_t phase = 0;
+      // What the threads wrote to shared memory is there for the MMAs that `issue` starts; returns when they are done.
+      auto products = [&](auto issue) {
+        tc::fence_proxy_async_smem();
         tc::tc_fence_before();
         __syncthreads();
-        tc::cluster_sync();
-        // rows rank * share ..: every CTA's sums of four elements added up, for every CTA
-        const int share = kSide / (int)ctas;
-        for (int i = threadIdx.x; i < share * 32; i += kSmallThreads) {
-          const int rr = rank * share + i / 32, j = i % 32;
-          const uint32_t from = sB + (uint32_t)(rr * 32 + (j ^ (rr & 31))) * 16, to = sA + panel_at(rr, j * 4);
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (uint32_t k = 0; k < ctas; ++k) {
-            const float4 x = ld_peer_f32x4(tc::map_peer(from, k));
-            v.x += x.x;
-            v.y += x.y;
-            v.z += x.z;
-            v.w += x.w;
-          }
-          const float e[4] = {v.x * back, v.y * back, v.z * back, v.w * back};
-          const uint2 h = pack_half4(e);
-          for (uint32_t k = 0; k < ctas; ++k)
-            tc::st_peer_u64(tc::map_peer(to, k), (unsigned long long)h.y << 32 | h.x);
+        if (warp == 0 && tc::elect_one()) {
+          tc::tc_fence_after();
+          issue();
+          tc::tc_commit(bar);
         }
-        asm volatile("fence.proxy.async;" ::: "memory");
-        tc::cluster_sync();
-      }
-      // B = a I + b A + c A A
-      products([&]() {
-        for (int k = 0; k < kSide / 16; ++k) {
-          const uint64_t d = tc::sdesc_k128(sA + k / 4 * kPanel) + (uint32_t)(k % 4 * 2);
-          tc::mma_bf16(tmem, d, d, idesc_f16_f32(kSide, kSide), k > 0);
-        }
-      });
-      {
-        const int col = part * 32;
-        tc::tmem_ld_32x32b_x32(lanes + col, r);
-        tc::tmem_wait_ld();
-        float v[32];
+        __syncwarp();
+        if (!tc::mbar_wait(bar, phase, nullptr, kWaitNs)) set_error(err, kDevTimeout);
+        phase ^= 1u;
+        __syncwarp();
+        tc::tc_fence_after();
+      };
+      const int row = q * 32 + lane;
+      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+      // 32 values of this thread's row to columns col .. of panels
+      auto keep32 = [&](uint8_t* to, int col, const float* v) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 u = *reinterpret_cast<const uint4*>(A + panel_at(row, col + j * 8));
-          const __half2* e = reinterpret_cast<const __half2*>(&u);
+          uint4 u;
+          __half2* h = reinterpret_cast<__half2*>(&u);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 a = __half22float2(e[x]);
-            const int i = j * 8 + 2 * x;
-            v[i] = fmaf(kB, a.x, kC * back * __uint_as_float(r[i])) + (row == col + i ? kA * kHeld : 0.f);
-            v[i + 1] = fmaf(kB, a.y, kC * back * __uint_as_float(r[i + 1])) + (row == col + i + 1 ? kA * kHeld : 0.f);
-          }
+          for (int x = 0; x < 4; ++x) h[x] = __floats2half2_rn(v[j * 8 + 2 * x], v[j * 8 + 2 * x + 1]);
+          *reinterpret_cast<uint4*>(to + panel_at(row, col + j * 8)) = u;
         }
-        keep32(B, col, v);
-      }
-      // X = B X
-      products([&]() {
-        for (int n = 0; n < panels; n += 4) {
-          const uint32_t idesc = idesc_f16_f32(kSide, min(4, panels - n) * 64) | kMajorB;
-          for (int k = 0; k < kSide / 16; ++k) {
-            const uint64_t a = tc::sdesc_k128(sB + k / 4 * kPanel) + (uint32_t)(k % 4 * 2);
-            const uint64_t b = (tc::sdesc_k128(sX + n * kPanel) | ((uint64_t)(kPanel >> 4) << 16)) + (uint32_t)(k * (2048 >> 4));
-            tc::mma_bf16(tmem + n * 64, a, b, idesc, k > 0);
-          }
-        }
-      });
+      };
+      constexpr float back = 1.f / kHeld;
 #pragma unroll 1
-      for (int c = part; c < panels * 2; c += 4) {
-        tc::tmem_ld_32x32b_x32(lanes + c * 32, r);
+      for (int it = 0; it < iterations; ++it) {
+        // A = X X^T
+        products([&]() {
+          const int steps = (w + 15) / 16;
+          for (int k = 0; k < steps; ++k) {
+            const uint64_t d = tc::sdesc_k128(sX + k / 4 * kPanel) + (uint32_t)(k % 4 * 2);
+            tc::mma_bf16(tmem, d, d, idesc_f16_f32(kSide, kSide), k > 0);
+          }
+        });
+        uint32_t r[32];
+        tc::tmem_ld_32x32b_x32(lanes + part * 32, r);
         tc::tmem_wait_ld();
-        float v[32];
+        if (ctas == 1) {
+          float v[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = back * __uint_as_float(r[j]);
-        keep32(X, c * 32, v);
+          for (int j = 0; j < 32; ++j) v[j] = back * __uint_as_float(r[j]);
+          keep32(A, part * 32, v);
+        } else {
+          // partial sums: 128 rows of 128 fp32, 16 bytes of a row exchanged by the row's number
+          float4* sums = reinterpret_cast<float4*>(B);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                         __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+            sums[row * 32 + ((part * 8 + j) ^ (row & 31))] = w > 0 ? v : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          tc::tc_fence_before();
+          __syncthreads();
+          tc::cluster_sync();
+          // rows rank * share ..: every CTA's sums of four elements added up, for every CTA
+          const int share = kSide / (int)ctas;
+          for (int i = threadIdx.x; i < share * 32; i += kSmallThreads) {
+            const int rr = rank * share + i / 32, j = i % 32;
+            const uint32_t from = sB + (uint32_t)(rr * 32 + (j ^ (rr & 31))) * 16, to = sA + panel_at(rr, j * 4);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (uint32_t k = 0; k < ctas; ++k) {
+              const float4 x = ld_peer_f32x4(tc::map_peer(from, k));
+              v.x += x.x;
+              v.y += x.y;
+              v.z += x.z;
+              v.w += x.w;
+            }
+            const float e[4] = {v.x * back, v.y * back, v.z * back, v.w * back};
+            const uint2 h = pack_half4(e);
+            for (uint32_t k = 0; k < ctas; ++k)
+              tc::st_peer_u64(tc::map_peer(to, k), (unsigned long long)h.y << 32 | h.x);
+          }
+          asm volatile("fence.proxy.async;" ::: "memory");
+          tc::cluster_sync();
+        }
+        // B = a I + b A + c A A
+        products([&]() {
+          for (int k = 0; k < kSide / 16; ++k) {
+            const uint64_t d = tc::sdesc_k128(sA + k / 4 * kPanel) + (uint32_t)(k % 4 * 2);
+            tc::mma_bf16(tmem, d, d, idesc_f16_f32(kSide, kSide), k > 0);
+          }
+        });
+        {
+          const int col = part * 32;
+          tc::tmem_ld_32x32b_x32(lanes + col, r);
+          tc::tmem_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 u = *reinterpret_cast<const uint4*>(A + panel_at(row, col + j * 8));
+            const __half2* e = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float2 a = __half22float2(e[x]);
+              const int i = j * 8 + 2 * x;
+              v[i] = fmaf(kB, a.x, kC * back * __uint_as_float(r[i])) + (row == col + i ? kA * kHeld : 0.f);
+              v[i + 1] = fmaf(kB, a.y, kC * back * __uint_as_float(r[i + 1])) + (row == col + i + 1 ? kA * kHeld : 0.f);
+            }
+          }
+          keep32(B, col, v);
+        }
+        // X = B X
+        products([&]() {
+          for (int n = 0; n < panels; n += 4) {
+            const uint32_t idesc = idesc_f16_f32(kSide, min(4, panels - n) * 64) | kMajorB;
+            for (int k = 0; k < kSide / 16; ++k) {
+              const uint64_t a = tc::sdesc_k128(sB + k / 4 * kPanel) + (uint32_t)(k % 4 * 2);
+              const uint64_t b = (tc::sdesc_k128(sX + n * kPanel) | ((uint64_t)(kPanel >> 4) << 16)) + (uint32_t)(k * (2048 >> 4));
+              tc::mma_bf16(tmem + n * 64, a, b, idesc, k > 0);
+            }
+          }
+        });
+#pragma unroll 1
+        for (int c = part; c < panels * 2; c += 4) {
+          tc::tmem_ld_32x32b_x32(lanes + c * 32, r);
+          tc::tmem_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = back * __uint_as_float(r[j]);
+          keep32(X, c * 32, v);
+        }
       }
+      tc::tc_fence_before();
+      __syncthreads();
     }
-    tc::tc_fence_before();
-    __syncthreads();
     // p = p keep - step O, and its bf16 copy; raw: out = O
     each([&](const At& a, float* p, float*) { get4(M, S, first + a.o, even, a.left, p); },
          [&](const At& a, const float* p, float* v) {
-           if (flip) {
+           constexpr float back = 1.f / kHeld;
+           if (kThin) {
+#pragma unroll
+             for (int x = 0; x < 4; ++x)
+               v[x] = x < a.left ? thin_x[flip ? (a.c + x) * kThinPitch + a.r : a.r * kThinPitch + a.c + x] : 0.f;
+           } else if (flip) {
 #pragma unroll
              for (int x = 0; x < 4; ++x)
                v[x] = x < a.left
@@ -1279,7 +1410,7 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
   if (!opens) pdl_wait();
   __syncwarp();
   if (ctas > 1) tc::cluster_sync();   // no CTA leaves while another may still read its shared memory
-  if (warp == 0) {
+  if (!kThin && warp == 0) {
     __syncwarp();
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
@@ -1496,20 +1627,28 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
         [&]() { return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, (char*)ws, st); });
     if (e != cudaSuccess) return e;
   }
-  for (int ctas = 1; ctas <= kMostCtas; ctas *= 2) {
+  for (int n = 0; n < 8; ++n) {   // the longest first
+    const int ctas = kMostCtas >> (n % 4);
+    const bool thin = n >= 4;
     const cudaError_t e = collect(
-        0, 1 << 24, [&](const moe_muon_tensor& t) { return !empty(t) && small_ctas(t) == ctas; },
+        0, 1 << 24,
+        [&](const moe_muon_tensor& t) {
+          return !empty(t) && small_ctas(t) == ctas && (t.rows <= kThinSide || t.cols <= kThinSide) == thin;
+        },
         [&]() {
-          auto kern = grad_dtype == MOE_BF16 ? small_kernel<bf16> : small_kernel<float>;
-          const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
+          auto kern = grad_dtype == MOE_BF16 ? thin ? small_kernel<bf16, true> : small_kernel<bf16, false>
+                                             : thin ? small_kernel<float, true> : small_kernel<float, false>;
+          const size_t smem = thin ? kThinSmem : kSmallSmem;
+          const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
           if (r != cudaSuccess) return r;
           const bool now = opens;
           opens = false;
-          return launch_kernel(kern, dim3((unsigned)(held * ctas)), dim3(kSmallThreads), kSmallSmem, st, (unsigned)ctas, M,
+          return launch_kernel(kern, dim3((unsigned)(held * ctas)), dim3(kSmallThreads), smem, st, (unsigned)ctas, M,
                                (int)h.iterations, now, (int*)ws);
         });
     if (e != cudaSuccess) return e;
   }
+  static_assert(kMostCtas == 8, "one, two, four or eight CTAs");
   return cudaSuccess;
 }
 

@@ -89,6 +89,23 @@ def test_orthogonalize(shape, dtype, out_dtype):
         check(out[i], x[i].double().cpu().numpy(), 5, U16 if out_dtype == "bf16" else U32)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(2, 1, 1), (3, 1, 6), (2, 9, 1), (2, 2, 2), (1, 13, 16), (2, 16, 16), (3, 16, 512),
+                                   (2, 513, 16), (1, 7, 1001), (2, 1030, 3), (1, 1, 2049), (2, 16, 4096), (1, 4095, 15)])
+def test_thin_matrices_are_iterated_in_fp32(shape, dtype):
+    """Short sides of up to 16 hold fp32.  The model rounds X, A and B once; the kernel's sums round at each of up to
+    30 partial sums (16 columns of a lane, 5 exchanges, 8 CTAs), which in a random walk is under 6 times as far.  A
+    matrix of one element has no averaging: the three terms of a step, of 14 together, rounded a few times each, are
+    64 half steps with what later steps make of them."""
+    x = dev(update_like(np.random.default_rng(shape), *shape), dtype)
+    out = run(x, "f32").double().cpu().numpy()
+    for i in range(shape[0]):
+        u = x[i].double().cpu().numpy()
+        want = newton_schulz(u, 5)
+        model = np.linalg.norm(newton_schulz(u, 5, lambda v: v.astype(np.float32).astype(np.float64)) - want)
+        assert np.linalg.norm(out[i] - want) <= 6 * model + 64 * U32 * np.linalg.norm(want)
+
+
 @pytest.mark.parametrize("iterations", [5, 4])
 @pytest.mark.parametrize("shape", [(12, 1300, 1701), (12, 1900, 1304), (12, 1304, 1304)])
 def test_batches_that_fill_the_gpu(shape, iterations):
