@@ -36,6 +36,8 @@
 // MMA issuer (leader CTA of a pair), warps 2-9 epilogue.  Every wait is
 // bounded: on expiry the kernel records a timeout in the workspace's error
 // word, drains what it has in flight, frees its tensor memory and returns.
+#include <algorithm>
+
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
@@ -192,11 +194,18 @@ enum Buffer : int8_t { kX = 0, kY, kG, kP, kQ, kBuffers, kNone = -1 };
 struct Step {
   Buffer a, b, out, add;
   bool gram;         // a = b = X: the reduction is over L
+  int8_t opens;      // operands that are the X before the first step, off by its correction
   float alpha, beta, diag;
   __host__ __device__ bool wide() const { return out <= kY; }   // else out is symmetric: tiles from the diagonal on
   __host__ __device__ bool mn() const { return out <= kY; }
 };
 constexpr int kMaxSteps = 7 * MOE_ORTHOGONALIZE_MAX_ITERATIONS / 2;
+
+// X as it is held before the first step: u times a times b, times which `correction` it is u / |u| 2^12.
+struct Scale {
+  float a, b, correction;
+  int build;   // not written yet
+};
 
 struct Chain {
   CUtensorMap along[kBuffers];   // boxes of 128 rows of 64 elements
@@ -209,6 +218,8 @@ struct Chain {
   Step step[kMaxSteps];
   int* written;                  // [steps, batch] zeros: warps that have written their share of a tile
   int* next;                     // zero: the first tile that nobody has taken
+  const Scale* scale;            // of each matrix
+  bool beside;                   // launches that run beside this one follow
   uint64_t limit;
   const int32_t* skip;
   int* err;
@@ -406,7 +417,11 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
     tc::tc_commit_pair_mc(bar, 0x3);
   };
 
-  pdl_enter();
+  // What comes after the call waits for the end of this kernel: a next call's few
+  // first blocks, started beside it, made it slower (steps on 8 matrices of 1024 x
+  // 1024 one after another 85 -> 121 us, 16 of 256 x 512 101 -> 110).
+  pdl_wait();
+  if (C.beside) pdl_trigger();
   if (C.skip && *C.skip) return;   // every thread of both CTAs
   if (warp == 0) {
     if (lane == 0) {
@@ -588,6 +603,11 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
       const Step& S = C.step[T.p];
       const int cols = T.cols(), row0 = T.m0 + rank * kBM + q * 32, row = row0 + lane;
       const bool mirror = !S.wide() && T.n0 >= T.m0 + kRows;
+      float alpha = S.alpha;
+      if (S.opens) {
+        const float by = C.scale[T.matrix].correction;
+        alpha *= S.opens == 2 ? by * by : by;
+      }
       const __half* add = S.add >= 0 && row < C.s
                               ? C.buf[S.add] + T.matrix * C.square_plane + row * C.square : nullptr;
       // 32 elements of the addend; rows are padded to 8: a vector that starts inside the row lies inside it
@@ -623,7 +643,7 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
             tc::tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const __half2 f = __floats2half2_rn(S.alpha * __uint_as_float(r[2 * j]), S.alpha * __uint_as_float(r[2 * j + 1]));
+              const __half2 f = __floats2half2_rn(alpha * __uint_as_float(r[2 * j]), alpha * __uint_as_float(r[2 * j + 1]));
               packed[h][j] = *reinterpret_cast<const uint32_t*>(&f);
             }
             continue;
@@ -727,11 +747,13 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
 void plan_steps(Chain& C, int iterations, bool pairs) {
   const float back = 1.f / kHeld;   // what is held is 2^12 times the value: a product of two comes out 2^24 times
   Buffer X = kX, Y = kY;
+  bool X0 = true;   // X is the first
   int n = 0;
   auto put = [&](Buffer a, Buffer b, Buffer out) {
-    C.step[n++] = Step{a, b, out, kNone, a == b && a <= kY, back, 0.f, 0.f};
+    const int8_t opens = (int8_t)((a == X && X0) + (b == X && X0));
+    C.step[n++] = Step{a, b, out, kNone, a == b && a <= kY, opens, back, 0.f, 0.f};
   };
-  auto polynomial = [&](Buffer out) { C.step[n++] = Step{kG, kG, out, kG, false, kC * back, kB, kA * kHeld}; };
+  auto polynomial = [&](Buffer out) { C.step[n++] = Step{kG, kG, out, kG, false, 0, kC * back, kB, kA * kHeld}; };
   for (int i = 0; i < iterations;) {
     put(X, X, kG);
     polynomial(kP);
@@ -748,6 +770,7 @@ void plan_steps(Chain& C, int iterations, bool pairs) {
     const Buffer t = X;
     X = Y;
     Y = t;
+    X0 = false;
     ++i;
   }
   C.steps = n;
@@ -852,10 +875,12 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ M
   if (threadIdx.x == 0) part[blockIdx.x] = q;
 }
 
-// One block for each matrix: its counters to zero, and X's factors.
+// One block for each matrix: its counters to zero, and X's factors.  guess: those
+// with which X has been written already; it stays if they are off by a factor
+// of 2 at most.
 __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ Matrices M, const Squares* __restrict__ part,
-                                                   float2* __restrict__ factor, int* __restrict__ written, int steps,
-                                                   int* __restrict__ next) {
+                                                   const float2* __restrict__ guess, Scale* __restrict__ scale,
+                                                   int* __restrict__ written, int steps, int* __restrict__ next) {
   __shared__ Squares s_w[8];
   pdl_enter();
   if (M.skip && *M.skip) return;
@@ -870,7 +895,16 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ Matri
     q.small += p.small;
   }
   q = block_sum(q, s_w);
-  if (threadIdx.x == 0) factor[blockIdx.x] = factors_of(q);
+  if (threadIdx.x == 0) {
+    const float2 f = factors_of(q);
+    Scale S = {f.x, f.y, 1.f, 1};
+    if (guess) {
+      const float2 g = guess[blockIdx.x];
+      const float by = f.y / g.y;
+      if (f.x == g.x && by >= 0.5f && by <= 2.f) S = {g.x, g.y, by, 0};
+    }
+    scale[blockIdx.x] = S;
+  }
 }
 
 // A block's tile of 64 x 64 elements of a matrix: rows r0.., columns c0.. as it
@@ -880,11 +914,9 @@ struct Place {
   int matrix, r0, c0;
   bool flip;
 };
-__device__ __forceinline__ Place place_of(const Matrices& M) {
-  const int per = M.tiles_s * M.tiles_L;
+__device__ __forceinline__ Place place_of(const Matrices& M, int matrix, int t) {
   Place p;
-  p.matrix = blockIdx.x / per;
-  const int t = blockIdx.x % per;
+  p.matrix = matrix;
   p.S = &segment_of(M, p.matrix);
   p.flip = p.S->rows > p.S->cols;
   const int a = t / M.tiles_L * 64, b = t % M.tiles_L * 64;   // in X
@@ -898,58 +930,244 @@ __device__ __forceinline__ uint2 pack_half4(const float* v) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// X = u / |u|, as it is held, its columns padded with zeros to the pitch.
+// X = u / |u|, as it is held, its columns padded with zeros to the pitch, for the
+// matrices whose X is not there yet; `blocks` blocks for each matrix.
 template <typename T>
 __global__ void __launch_bounds__(256)
-build_kernel(const __grid_constant__ Matrices M, const float2* __restrict__ factor, __half* __restrict__ X) {
+build_kernel(const __grid_constant__ Matrices M, const Scale* __restrict__ factors, int blocks, __half* __restrict__ X) {
   __shared__ float tile[64][65];
   pdl_enter();
   if (M.skip && *M.skip) return;
-  const Place at = place_of(M);
-  const Segment& S = *at.S;
-  const int64_t base = (int64_t)(at.matrix - S.first) * S.rows * S.cols;
+  const int matrix = blockIdx.x / blocks;
+  const Scale f = factors[matrix];
+  if (!f.build) return;
+  for (int t = blockIdx.x % blocks; t < M.tiles_s * M.tiles_L; t += blocks) {
+    const Place at = place_of(M, matrix, t);
+    const Segment& S = *at.S;
+    const int64_t base = (int64_t)(at.matrix - S.first) * S.rows * S.cols;
+    const T* g = reinterpret_cast<const T*>(S.g) + base;
+    const float* m = M.raw ? nullptr : S.m + base;
+    const float scale = M.grad_scale ? *M.grad_scale : 1.f;
+    const bool vg = aligned_to(g, 4 * sizeof(T)) && S.cols % 4 == 0, vm = aligned_to(m, 16) && S.cols % 4 == 0;
+    __half* out = X + (int64_t)at.matrix * M.plane;
+    const int x4 = threadIdx.x % 16 * 4, y = threadIdx.x / 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = at.r0 + y + 16 * i, c = at.c0 + x4;
+      const int left = r < S.rows && c < S.cols ? min(4, S.cols - c) : 0;
+      float u[4] = {0.f, 0.f, 0.f, 0.f};
+      if (left > 0) {
+        const int64_t o = (int64_t)r * S.cols + c;
+        load4(g + o, vg, left, u);
+        if (!M.raw) {
+          float mm[4];
+          load4(m + o, vm, left, mm);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) u[x] = M.nesterov ? fmaf(M.mu, mm[x], u[x] * scale) : mm[x];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) u[x] = u[x] * f.a * f.b;
+      if (at.flip) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tile[y + 16 * i][x4 + x] = u[x];
+      } else if (r < M.s && c < M.pitch) {
+        *reinterpret_cast<uint2*>(out + (int64_t)r * M.pitch + c) = pack_half4(u);
+      }
+    }
+    if (!at.flip) continue;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = at.c0 + y + 16 * i, c = at.r0 + x4;   // in X
+      if (r >= M.s || c >= M.pitch) continue;
+      float v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] = tile[x4 + x][y + 16 * i];
+      *reinterpret_cast<uint2*>(out + (int64_t)r * M.pitch + c) = pack_half4(v);
+    }  __syncthreads();
+  }
+}
+
+// The same in one pass, with X's factors guessed: the update's size from 4096 of
+// its elements, taken to a power of two.  The products with that X take the norm
+// itself into account (in fp32: X is rounded once, as it would be), and where the
+// guess is wrong by more than a factor of 2 X is built again.  With the factors
+// known beforehand g and m are read once: 12 bytes an element instead of 18,
+// where they are bf16 and fp32.  48 matrices of 1408 x 4096 0.47 ms (7.1 TB/s),
+// where the two kernels above took 0.9.
+constexpr int kSample = 4096;
+template <typename T>
+__global__ void __launch_bounds__(256) sample_kernel(const __grid_constant__ Matrices M, float2* __restrict__ guess) {
+  __shared__ Squares s_w[8];
+  pdl_enter();
+  if (M.skip && *M.skip) return;
+  const Segment& S = segment_of(M, blockIdx.x);
+  const int64_t n = (int64_t)S.rows * S.cols, base = (int64_t)(blockIdx.x - S.first) * n;
   const T* g = reinterpret_cast<const T*>(S.g) + base;
   const float* m = M.raw ? nullptr : S.m + base;
   const float scale = M.grad_scale ? *M.grad_scale : 1.f;
-  const float2 f = factor[at.matrix];
-  const bool vg = aligned_to(g, 4 * sizeof(T)) && S.cols % 4 == 0, vm = aligned_to(m, 16) && S.cols % 4 == 0;
-  __half* out = X + (int64_t)at.matrix * M.plane;
-  const int x4 = threadIdx.x % 16 * 4, y = threadIdx.x / 16;
+  const bool vg = aligned_to(g, 4 * sizeof(T)), vm = aligned_to(m, 16);
+  const uint32_t stride = (uint32_t)(n / kSample);   // groups of four between two that are read
+  Squares q = {0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = at.r0 + y + 16 * i, c = at.c0 + x4;
-    const int left = r < S.rows && c < S.cols ? min(4, S.cols - c) : 0;
-    float u[4] = {0.f, 0.f, 0.f, 0.f};
-    if (left > 0) {
-      const int64_t o = (int64_t)r * S.cols + c;
-      load4(g + o, vg, left, u);
+  for (int it = 0; it < kSample / 1024; ++it) {
+    // one of each `stride` groups, another one every time
+    const uint32_t j = it * 256 + threadIdx.x;
+    const int64_t i = ((int64_t)j * stride + (uint32_t)(((uint64_t)(j * 2654435769u) * stride) >> 32)) * 4;
+    float u[4], mm[4];
+    load4(g + i, vg, 4, u);
+    if (!M.raw) load4(m + i, vm, 4, mm);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
       if (!M.raw) {
-        float mm[4];
-        load4(m + o, vm, left, mm);
+        const float gx = u[x] * scale, mx = fmaf(M.mu, mm[x], gx);
+        u[x] = M.nesterov ? fmaf(M.mu, mx, gx) : mx;
+      }
+      add_square(q, u[x]);
+    }
+  }
+  q = block_sum(q, s_w);
+  if (threadIdx.x == 0) {
+    const float by = (float)n / kSample;
+    const float2 f = factors_of(Squares{q.mid * by, q.big * by, q.small * by});
+    guess[blockIdx.x] = make_float2(f.x, __int_as_float((__float_as_int(f.y) + 0x400000) & 0xff800000));
+  }
+}
+
+// A block has 64 rows of 128 columns of X; transposed through shared memory, a
+// row's groups of four columns exchanged by the row's number.  What bounds it is
+// HBM, with eight rows of a thread in flight, and the sums of squares that hardly
+// ever count left out (with four rows and all sums 0.66 ms instead of 0.47).
+template <typename T>
+__global__ void __launch_bounds__(256, 3)
+step_kernel(const __grid_constant__ Matrices M, const float2* __restrict__ guess, Squares* __restrict__ part,
+            __half* __restrict__ X) {
+  __shared__ Squares s_w[8];
+  __shared__ __align__(16) float tile[64][128];
+  pdl_enter();
+  if (M.skip && *M.skip) return;
+  const int matrix = blockIdx.x / M.parts, t = blockIdx.x % M.parts, across = (M.L + 127) / 128;
+  const Segment& S = segment_of(M, matrix);
+  const bool flip = S.rows > S.cols;
+  const int a = t / across * 64, b = t % across * 128;   // in X
+  const int64_t base = (int64_t)(matrix - S.first) * S.rows * S.cols;
+  const T* g = reinterpret_cast<const T*>(S.g) + base;
+  float* m = M.raw ? nullptr : S.m + base;
+  const float scale = M.grad_scale ? *M.grad_scale : 1.f;
+  const float2 f = guess[matrix];
+  const bool vg = aligned_to(g, 4 * sizeof(T)) && S.cols % 4 == 0, vm = aligned_to(m, 16) && S.cols % 4 == 0;
+  __half* out = X + (int64_t)matrix * M.plane;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // four columns of the tensor to a thread, every `by`-th row
+  const int x4 = flip ? threadIdx.x % 16 * 4 : lane * 4, y = flip ? threadIdx.x / 16 : warp, by = flip ? 16 : 8;
+  const int r0 = (flip ? b : a) + y, c = (flip ? a : b) + x4;
+  Squares q = {0.f, 0.f, 0.f};
+  const bool whole = vg && (M.raw || vm) && f.x == 1.f &&
+                     (flip ? b + 128 <= S.rows && a + 64 <= S.cols : a + 64 <= S.rows && b + 128 <= S.cols);
+  if (whole) {
+    // all of it lies inside, and X takes one factor: eight rows in flight, and one sum of squares
+    float u[8][4], mm[8][4];
+    const int64_t o = (int64_t)r0 * S.cols + c, step = (int64_t)by * S.cols;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) u[x] = M.nesterov ? fmaf(M.mu, mm[x], u[x] * scale) : mm[x];
+    for (int i = 0; i < 8; ++i) {
+      load4(g + o + i * step, true, 4, u[i]);
+      if (!M.raw) load4(m + o + i * step, true, 4, mm[i]);
+    }
+    float mid = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!M.raw) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float gx = u[i][x] * scale;
+          mm[i][x] = fmaf(M.mu, mm[i][x], gx);
+          u[i][x] = M.nesterov ? fmaf(M.mu, mm[i][x], gx) : mm[i][x];
+        }
+        store4(m + o + i * step, true, 4, mm[i]);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        mid = fmaf(u[i][x], u[i][x], mid);
+        u[i][x] *= f.y;
+      }
+      if (flip) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tile[x4 + x][(y + i * by) ^ (x4 & 28)] = u[i][x];
+      } else {
+        *reinterpret_cast<uint2*>(out + (int64_t)(r0 + i * by) * M.pitch + c) = pack_half4(u[i]);
+      }
+    }
+    // The other two sums are this one times 2^-180 and 2^180, unless squares overflowed, or vanished and count.
+    float sum = mid;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    q = Squares{mid, mid * kDown * kDown, mid * kUp * kUp};
+    if (!(sum > 1e-30f && sum <= 3e38f)) {
+      q = Squares{0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        float v[4], mv[4];
+        load4(g + o + i * step, true, 4, v);
+        if (!M.raw) load4(m + o + i * step, true, 4, mv);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (!M.raw) v[x] = M.nesterov ? fmaf(M.mu, mv[x], v[x] * scale) : mv[x];
+          add_square(q, v[x]);
+        }
+      }
+    }
+  }
+#pragma unroll 1
+  for (int i0 = 0; i0 < 8 && !whole; i0 += 4) {
+    float u[4][4], mm[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + (i0 + i) * by, left = r < S.rows ? min(4, S.cols - c) : 0;
+      const int64_t o = (int64_t)r * S.cols + c;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) u[i][x] = mm[i][x] = 0.f;
+      if (left > 0) {
+        load4(g + o, vg, left, u[i]);
+        if (!M.raw) load4(m + o, vm, left, mm[i]);
       }
     }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) u[x] = u[x] * f.x * f.y;
-    if (at.flip) {
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + (i0 + i) * by, left = r < S.rows ? min(4, S.cols - c) : 0;
+      if (!M.raw) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) tile[y + 16 * i][x4 + x] = u[x];
-    } else if (r < M.s && c < M.pitch) {
-      *reinterpret_cast<uint2*>(out + (int64_t)r * M.pitch + c) = pack_half4(u);
+        for (int x = 0; x < 4; ++x) {
+          const float gx = u[i][x] * scale;
+          mm[i][x] = fmaf(M.mu, mm[i][x], gx);
+          u[i][x] = M.nesterov ? fmaf(M.mu, mm[i][x], gx) : mm[i][x];
+        }
+        if (left > 0) store4(m + (int64_t)r * S.cols + c, vm, left, mm[i]);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {   // zeros behind the row
+        add_square(q, u[i][x]);
+        u[i][x] = u[i][x] * f.x * f.y;
+      }
+      if (flip) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tile[x4 + x][(y + (i0 + i) * by) ^ (x4 & 28)] = u[i][x];
+      } else if (r < M.s && c < M.pitch) {
+        *reinterpret_cast<uint2*>(out + (int64_t)r * M.pitch + c) = pack_half4(u[i]);
+      }
     }
   }
-  if (!at.flip) return;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = at.c0 + y + 16 * i, c = at.r0 + x4;   // in X
-    if (r >= M.s || c >= M.pitch) continue;
-    float v[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) v[x] = tile[x4 + x][y + 16 * i];
-    *reinterpret_cast<uint2*>(out + (int64_t)r * M.pitch + c) = pack_half4(v);
+  if (flip) {
+    __syncthreads();
+    const int to = b + lane * 4;
+#pragma unroll 4
+    for (int i = warp; i < 64; i += 8)
+      if (a + i < M.s && to < M.pitch)
+        *reinterpret_cast<uint2*>(out + (int64_t)(a + i) * M.pitch + to) =
+            pack_half4(reinterpret_cast<const float*>(&tile[i][(lane * 4) ^ (i & 28)]));
   }
+  q = block_sum(q, s_w);
+  if (threadIdx.x == 0) part[blockIdx.x] = q;
 }
 
 // ---------------------------------------------------------------- small matrices
@@ -1425,7 +1643,7 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // Matrices of s x L (s <= L) that run together, and their buffers.
 constexpr size_t kMostBytes = (size_t)4 << 30;   // a larger batch runs in parts of this size
 struct Sizes {
-  int s, L, parts;
+  int s, L, parts, tiles;   // partial sums of a matrix by the element, and by the tile
   int64_t pitch, square;   // of X, and of A and B
   Sizes(int rows, int cols) {
     s = rows < cols ? rows : cols;
@@ -1433,16 +1651,18 @@ struct Sizes {
     pitch = round8(L);
     square = round8(s);
     parts = (int)(((int64_t)s * L + kPart - 1) / kPart);
+    tiles = (s + 63) / 64 * ((L + 127) / 128);
   }
+
   size_t x() const { return (size_t)s * pitch * 2; }
   size_t a() const { return (size_t)s * square * 2; }
   size_t bytes(int64_t n) const {   // X and its successor, three short matrices, counters, sums, factors
     return 2 * round256(n * x()) + 3 * round256(n * a()) + 256 + round256(n * kMaxSteps * sizeof(int)) +
-           round256(n * parts * sizeof(Squares)) + round256(n * sizeof(float2));
+           round256(n * tiles * sizeof(Squares)) + round256(n * sizeof(Scale)) + round256(n * sizeof(float2));
   }
   int64_t most() const {
     int64_t n = (int64_t)(kMostBytes /
-                          (2 * x() + 3 * a() + kMaxSteps * sizeof(int) + parts * sizeof(Squares) + sizeof(float2)));
+                          (2 * x() + 3 * a() + kMaxSteps * sizeof(int) + tiles * sizeof(Squares) + sizeof(Scale) + sizeof(float2)));
     const int64_t blocks = (int64_t)((s + 63) / 64) * ((L + 63) / 64);    // of X's kernels, for a matrix
     const int64_t tiles = (int64_t)((s + 127) / 128) * ((L + 127) / 128);   // of a step, at most
     const int64_t grid = ((int64_t)1 << 30) / blocks, numbers = ((int64_t)1 << 30) / (tiles * kMaxSteps);
@@ -1473,7 +1693,7 @@ bool leads(const moe_muon_tensor* t, int i) {
   return true;
 }
 
-cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf16, int iterations, char* ws,
+cudaError_t run_matrices(Matrices& M, const Sizes& z, int n, bool grad_bf16, int iterations, bool beside, char* ws,
                          cudaStream_t st) {
   int* err = (int*)ws;
   char* at = ws + 256;
@@ -1486,8 +1706,10 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
   for (int i = 0; i < kBuffers; ++i) C.buf[i] = (__half*)take(n * (i <= kY ? z.x() : z.a()));
   C.next = (int*)take(256);
   C.written = (int*)take((size_t)n * kMaxSteps * sizeof(int));
-  Squares* part = (Squares*)take((size_t)n * z.parts * sizeof(Squares));
-  float2* factor = (float2*)take((size_t)n * sizeof(float2));
+  Squares* part = (Squares*)take((size_t)n * z.tiles * sizeof(Squares));
+  Scale* scale = (Scale*)take((size_t)n * sizeof(Scale));
+  float2* guess = (float2*)take((size_t)n * sizeof(float2));
+  C.scale = scale;
   C.s = z.s;
   C.L = z.L;
   C.batch = n;
@@ -1497,6 +1719,7 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
   C.square_plane = z.s * z.square;
   C.skip = M.skip;
   C.err = err;
+  C.beside = beside;
   for (int i = 0; i < kBuffers; ++i) {
     const bool x = i <= kY;
     if (!tma_map_16bit_3d(&C.along[i], C.buf[i], n, z.s, x ? z.L : z.s, x ? z.pitch : z.square,
@@ -1528,13 +1751,34 @@ cudaError_t run_matrices(const Matrices& M, const Sizes& z, int n, bool grad_bf1
   // the short ones fill the SMs.
   const bool pairs = 4 * (int64_t)z.L >= 5 * (int64_t)z.s && tiles_of(256, false) >= most;
   plan_steps(C, iterations, pairs);
-  const dim3 sums((unsigned)(n * z.parts)), tiles((unsigned)((int64_t)n * M.tiles_s * M.tiles_L)), threads(256);
-  cudaError_t e = grad_bf16 ? launch_kernel(momentum_kernel<bf16>, sums, threads, 0, st, 1, M, part)
-                            : launch_kernel(momentum_kernel<float>, sums, threads, 0, st, 1, M, part);
-  if (e == cudaSuccess) e = launch_kernel(norm_kernel, dim3((unsigned)n), threads, 0, st, 1, M, part, factor, C.written, C.steps, C.next);
+  // X with guessed factors where that saves more than its two launches cost (8
+  // matrices of 1024 x 1024 94 -> 87 us, 4 of them 60 -> 58, 6 of 1704 x 904 119
+  // -> 122) and rows start on four elements (6 of 1700 x 901: 131 -> 144).
+  bool guessed = (int64_t)n * z.s * z.L >= 1 << 23;
+  for (int i = 0; i < M.n; ++i) guessed = guessed && M.seg[i].cols % 4 == 0;
+  M.parts = guessed ? z.tiles : z.parts;
+  // blocks for a matrix' X: all it takes, or a few that find it written
+  const int per = M.tiles_s * M.tiles_L;
+  const int blocks = guessed ? std::max(1, std::min(per, 8 * sm_count() / n)) : per;
+  const dim3 sums((unsigned)((int64_t)n * M.parts)), one((unsigned)n), threads(256);
+  cudaError_t e = cudaSuccess;
+  if (guessed) {
+    e = grad_bf16 ? launch_kernel(sample_kernel<bf16>, one, threads, 0, st, 1, M, guess)
+                  : launch_kernel(sample_kernel<float>, one, threads, 0, st, 1, M, guess);
+    if (e == cudaSuccess)
+      e = grad_bf16 ? launch_kernel(step_kernel<bf16>, sums, threads, 0, st, 1, M, guess, part, C.buf[kX])
+                    : launch_kernel(step_kernel<float>, sums, threads, 0, st, 1, M, guess, part, C.buf[kX]);
+  } else {
+    e = grad_bf16 ? launch_kernel(momentum_kernel<bf16>, sums, threads, 0, st, 1, M, part)
+                  : launch_kernel(momentum_kernel<float>, sums, threads, 0, st, 1, M, part);
+  }
   if (e == cudaSuccess)
-    e = grad_bf16 ? launch_kernel(build_kernel<bf16>, tiles, threads, 0, st, 1, M, factor, C.buf[kX])
-                  : launch_kernel(build_kernel<float>, tiles, threads, 0, st, 1, M, factor, C.buf[kX]);
+    e = launch_kernel(norm_kernel, one, threads, 0, st, 1, M, part, guessed ? guess : nullptr, scale, C.written, C.steps,
+                      C.next);
+  const dim3 builds((unsigned)((int64_t)n * blocks));
+  if (e == cudaSuccess)
+    e = grad_bf16 ? launch_kernel(build_kernel<bf16>, builds, threads, 0, st, 1, M, scale, blocks, C.buf[kX])
+                  : launch_kernel(build_kernel<float>, builds, threads, 0, st, 1, M, scale, blocks, C.buf[kX]);
   if (e != cudaSuccess) return e;
   return broad ? launch_chain<256>(C, M, tiles_of(256, true), st) : launch_chain<128>(C, M, tiles_of(128, true), st);
 }
@@ -1611,6 +1855,8 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
     return held ? run() : cudaSuccess;
   };
   bool opens = true;   // the call with its next launch
+  const bool beside = std::any_of(tensors, tensors + count,
+                                  [](const moe_muon_tensor& t) { return !empty(t) && small_ctas(t); });
   for (int i = 0; i < count; ++i) {
     if (!leads(tensors, i)) continue;
     const Sizes z(tensors[i].rows, tensors[i].cols);
@@ -1618,13 +1864,12 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
     M.L = z.L;
     M.pitch = z.pitch;
     M.plane = z.s * z.pitch;
-    M.parts = z.parts;
     M.tiles_s = (z.s + 63) / 64;
     M.tiles_L = (z.L + 63) / 64;
     opens = false;
     const cudaError_t e = collect(
         i, z.most(), [&](const moe_muon_tensor& t) { return large(t) && alike(tensors[i], t); },
-        [&]() { return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, (char*)ws, st); });
+        [&]() { return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, beside, (char*)ws, st); });
     if (e != cudaSuccess) return e;
   }
   for (int n = 0; n < 8; ++n) {   // the longest first

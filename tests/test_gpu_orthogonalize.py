@@ -134,6 +134,81 @@ def test_batches_that_fill_the_gpu(shape, iterations):
         assert (out[i].double() - want).norm() <= 2 * model + (U32 + 16 * 2.0 ** -12) * want.norm()
 
 
+def on_gpu(u, iterations, held=lambda v: v):
+    """newton_schulz for a batch, in 64 bits on the GPU; zeros for a zero matrix."""
+    t = t_()
+    a, b, c = NS
+    flip = u.shape[-2] > u.shape[-1]
+    v = u.double().mT if flip else u.double()
+    norm = t.linalg.matrix_norm(v, keepdim=True)
+    v = held(t.where(norm > 0, v / norm, 0.0))
+    one = t.eye(v.shape[-2], dtype=t.float64, device="cuda")
+    for _ in range(iterations):
+        A = held(v @ v.mT)
+        v = held(held(a * one + b * A + c * (A @ A)) @ v)
+    return v.mT if flip else v
+
+
+def check_batch(got, u, iterations, noise=0.0):
+    """As check(), for each matrix."""
+    t = t_()
+    want = on_gpu(u, iterations)
+    model = t.linalg.matrix_norm(on_gpu(u, iterations, lambda v: (v * 4096).half().double() / 4096) - want)
+    off = t.linalg.matrix_norm(got.double() - want)
+    assert (off <= 2 * model + (U32 + 16 * 2.0 ** -12) * t.linalg.matrix_norm(want) + noise).all()
+
+
+def uneven(shape, dtype):
+    """Matrices whose size a few of their elements tell, and others where they do not."""
+    t = t_()
+    n, rows, cols = shape
+    gen = t.Generator(device="cuda").manual_seed(rows)
+    x = t.randn(shape, device="cuda", generator=gen)
+    for i in range(n):
+        kind = i % 8
+        if kind == 1:       # four strong directions
+            x[i] += t.randn(rows, 4, device="cuda", generator=gen) @ t.randn(4, cols, device="cuda", generator=gen)
+        elif kind == 2:
+            x[i] = 0
+        elif kind == 3:     # a single element
+            v = x[i, rows // 2, cols // 3].item()
+            x[i] = 0
+            x[i, rows // 2, cols // 3] = v
+        elif kind == 4:     # a few rows
+            x[i, 3:] = 0
+        elif kind == 5:     # columns of very different sizes
+            x[i] *= t.exp(3 * t.randn(cols, device="cuda", generator=gen))
+        elif kind == 6:
+            x[i] *= 1e-25
+        elif kind == 7:
+            x[i] *= 1e25
+    return x.to(t.bfloat16 if dtype == "bf16" else t.float32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(20, 601, 904), (24, 1000, 440), (10, 1024, 1024), (20, 601, 903)])
+def test_batches_whose_norms_are_guessed(shape, dtype):
+    x = uneven(shape, dtype)
+    out = run(x, "f32")
+    check_batch(out, x, 5)
+    assert (run(x, "f32") == out).all()
+    # off the 16-byte grid, and in place
+    t = t_()
+    y = t.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(shape)
+    y.copy_(x)
+    assert (run(y, "f32") == out).all()
+    if dtype == "f32":
+        ws = moe.orthogonalize_workspace(*shape)
+        moe.moe_orthogonalize(y, y, 5, ws)
+        assert (y == out).all()
+    # each keeps to itself: NaN, and another's size
+    y = x.clone()
+    y[0, 3, 4] = float("nan")
+    y[1] = y[2]
+    again = run(y, "f32")
+    assert again[0].isnan().all() and (again[1] == out[2]).all() and (again[2:] == out[2:]).all()
+
+
 @pytest.mark.parametrize("iterations", [1, 2, 3, 4, 6])
 @pytest.mark.parametrize("shape", [(200, 300), (300, 200), (264, 1100)])
 def test_number_of_iterations(shape, iterations):
@@ -250,6 +325,27 @@ def test_muon_step(grad, nesterov):
         moe.moe_muon_step(plan, params, factor, None, ws)
         check_step(before, numbers(tensors), 0.02, np.float64(np.float32(0.9)), nesterov, 5, 0.5)
     assert moe.moe_get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("nesterov", [True, False])
+def test_muon_step_of_batches_whose_norms_are_guessed(grad, nesterov):
+    t = t_()
+    mu, lr, f = float(np.float32(0.9)), 0.02, 0.5
+    tensors = [{"p": t.randn(s, device="cuda") * 0.02, "g": uneven(s, grad), "m": uneven(s, "f32").flip(0).contiguous() * 0.1,
+                "weight_decay": 0.1, "scale": 1.0} for s in [(16, 604, 900), (9, 900, 604)]]
+    plan, params = moe.muon_tensors(tensors), moe.make_muon(lr, 0.9, nesterov, 5)
+    ws = moe.muon_workspace(plan)
+    before = [{k: v.clone() if hasattr(v, "clone") else v for k, v in d.items()} for d in tensors]
+    moe.moe_muon_step(plan, params, t.full((1,), f, device="cuda"), None, ws)
+    assert moe.moe_get_device_error(ws) == 0
+    for b, a in zip(before, tensors):
+        g, p = b["g"].double() * f, b["p"].double()
+        m = mu * b["m"].double() + g
+        assert ((a["m"].double() - m).abs() <= 4 * U32 * ((mu * b["m"].double()).abs() + g.abs())).all()
+        u = g + mu * m if nesterov else m
+        moved = (p * (1 - lr * 0.1) - a["p"].double()) / lr
+        check_batch(moved, u, 5, t.linalg.matrix_norm(p) * 4 * U32 / lr)
 
 
 def test_muon_step_skips_and_takes_no_tensor():
