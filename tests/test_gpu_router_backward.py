@@ -260,6 +260,33 @@ def test_router_gradient_against_differences():
         assert abs(quotient - (got * d).sum()) <= 1e-5 * np.abs(got * d).sum()
 
 
+@pytest.mark.parametrize("off", [0, 1, 3])
+@pytest.mark.parametrize("T,E,K", [(2, 2, 1), (96, 12, 3), (4096, 16, 2), (65536, 128, 4)])
+def test_balance_gradient_of_nearly_equal_counts(T, E, K, off):
+    """As small as the counts' differences, and as exact: with p off by u as in check_backward, c - <p, c> (2 max|c - mean|
+    at most) brings 2 u p max|c - mean|, and the error of <p, c> and the roundings of c and the product under 2 u more;
+    nothing where all counts are equal."""
+    r = np.random.default_rng([T, E, off])
+    t = t_()
+    z = r.standard_normal((T, E)).astype(np.float32)
+    count = np.full(E, T * K // E)
+    count[0] += off
+    count[-1] -= off
+    if count.min() < 0:
+        pytest.skip("fewer choices than that")
+    f32, i32 = dict(device="cuda", dtype=t.float32), dict(device="cuda", dtype=t.int32)
+    d = moe.make_desc(T, 64, E, K, 8)
+    out = t.full((T, E), 7.0, **f32)
+    ws = moe.router_backward_workspace(d)
+    moe.moe_router_backward(d, None, None, t.tensor(z, **f32), t.zeros(T, K, **i32), None, t.full((1,), 0.7, **f32),
+                            t.tensor(count, **i32), t.tensor([T], **i32), None, out, None, None, None, ws)
+    p = np.exp(z.astype(np.float64) - z.max(axis=1, keepdims=True))
+    p /= p.sum(axis=1, keepdims=True)
+    c = float(np.float32(0.7)) / T * E * (count - count.mean()) / (T * K)
+    want = p * (c - p @ c[:, None])
+    assert (abs(out.double().cpu().numpy() - want) <= 4 * (64 + 4 * abs(z).max()) * U32 * p * abs(c).max()).all()
+
+
 def test_scores_of_minus_infinity():
     """Experts switched off by a score of -infinity have no probability and no gradient."""
     c = case(60, 64, 16, 2, "bf16", seed=10)
