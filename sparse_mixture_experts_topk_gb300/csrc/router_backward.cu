@@ -291,11 +291,11 @@ dlogits_kernel(RouterBackward b, int64_t T, int E, int K, float inv_tau, float* 
     const float n = (float)*b.tokens, f = n > 0.f ? *b.dloss / n * ((float)E / (n * (float)K)) : 0.f;
     // sum_e p_e = 1: any constant may be taken off the counts.  Their mean, to an
     // integer: what is left of nearly equal ones has all its bits.
-    const int mean = __float2int_rn(n * (float)K / (float)E);
+    const int mean = __float2int_rn(n * ((float)K / (float)E));
 #pragma unroll
     for (int i = 0; i < G::kN; ++i) {
       const int e = G::expert(lane, i);
-      c[i] = e < E ? f * (float)((int64_t)b.count[e] - mean) : 0.f;
+      c[i] = e < E ? f * (float)(b.count[e] - mean) : 0.f;
     }
   }
   const int64_t end = alive ? (T + 127) / 128 * 128 : T;
