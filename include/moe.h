@@ -535,10 +535,11 @@ int moe_router_backward(const moe_desc* desc, const void* x, const void* Wg, con
  * result in the 2-norm for gradients with strong directions over noise; what
  * lies far below the elements it is part of is off by more (2e-2 for a matrix
  * of rank one over noise 100 times smaller).  Matrices with a short side of up
- * to 16 and a long one of up to 4096 are held in fp32.  For large batches of longer
- * matrices (more columns than 5/4 of the rows) two iterations are taken at a
- * time, (B2 B1) X; bits then depend on the batch.  A matrix with a NaN or an
- * infinity becomes NaN throughout; the others of its batch do not.
+ * to 16 and a long one of up to 4096 are held in fp32.  For large batches of
+ * longer matrices (more columns than 5/4 of the rows) two iterations are taken
+ * at a time, (B2 B1) X, and for batches of 2^23 elements X is held times the
+ * norm over a power of two: bits then depend on the batch.  A matrix with a NaN
+ * or an infinity becomes NaN throughout; the others of its batch do not.
  */
 #define MOE_ORTHOGONALIZE_MAX_SIDE 32768       /* rows, cols <= this */
 #define MOE_ORTHOGONALIZE_MAX_ITERATIONS 16
