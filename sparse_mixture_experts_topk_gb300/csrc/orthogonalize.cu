@@ -986,7 +986,8 @@ build_kernel(const __grid_constant__ Matrices M, const Scale* __restrict__ facto
 #pragma unroll
       for (int x = 0; x < 4; ++x) v[x] = tile[x4 + x][y + 16 * i];
       *reinterpret_cast<uint2*>(out + (int64_t)r * M.pitch + c) = pack_half4(v);
-    }  __syncthreads();
+    }
+    __syncthreads();
   }
 }
 
@@ -1654,7 +1655,6 @@ struct Sizes {
     parts = (int)(((int64_t)s * L + kPart - 1) / kPart);
     tiles = (s + 63) / 64 * ((L + 127) / 128);
   }
-
   size_t x() const { return (size_t)s * pitch * 2; }
   size_t a() const { return (size_t)s * square * 2; }
   size_t bytes(int64_t n) const {   // X and its successor, three short matrices, counters, sums, factors
@@ -1856,8 +1856,11 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
     return held ? run() : cudaSuccess;
   };
   bool opens = true;   // the call with its next launch
-  const bool beside = std::any_of(tensors, tensors + count,
-                                  [](const moe_muon_tensor& t) { return !empty(t) && small_ctas(t); });
+  // the last size before the small matrices: those start beside its products
+  int last = -1;
+  if (std::any_of(tensors, tensors + count, [](const moe_muon_tensor& t) { return !empty(t) && small_ctas(t); }))
+    for (int i = 0; i < count; ++i)
+      if (leads(tensors, i)) last = i;
   for (int i = 0; i < count; ++i) {
     if (!leads(tensors, i)) continue;
     const Sizes z(tensors[i].rows, tensors[i].cols);
@@ -1870,7 +1873,7 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
     opens = false;
     const cudaError_t e = collect(
         i, z.most(), [&](const moe_muon_tensor& t) { return large(t) && alike(tensors[i], t); },
-        [&]() { return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, beside, (char*)ws, st); });
+        [&]() { return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, i == last, (char*)ws, st); });
     if (e != cudaSuccess) return e;
   }
   for (int n = 0; n < 8; ++n) {   // the longest first

@@ -272,6 +272,20 @@ def test_a_zero_matrix_and_a_matrix_with_nan_keep_to_themselves():
     assert (out[0] == clean[0]).all() and (out[4] == clean[4]).all()
 
 
+@pytest.mark.parametrize("rows,cols", [(9, 40), (700, 16), (64, 96)])
+def test_a_zero_matrix_and_a_matrix_with_nan_on_chip(rows, cols):
+    r = np.random.default_rng(4)
+    x = dev(update_like(r, 5, rows, cols))
+    clean = run(x, "f32")
+    x[1] = 0
+    x[2, 3, 4] = float("nan")
+    x[3, -1, -1] = float("inf")
+    out = run(x, "f32")
+    assert (out[1] == 0).all()
+    assert out[2].isnan().all() and out[3].isnan().all()
+    assert (out[0] == clean[0]).all() and (out[4] == clean[4]).all()
+
+
 # ------------------------------------------------------------------ the step
 
 def step_case(shapes, grad, seed, p16=True):
