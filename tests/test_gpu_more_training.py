@@ -161,6 +161,41 @@ def test_two_steps_that_fill_the_gpu_at_once():
     assert all(moe.moe_get_device_error(ws) == 0 for _, ws in plans)
 
 
+def test_captured_step_of_every_kind_of_matrix():
+    """Two sizes of tensor-core batches, one with guessed norms, small matrices by one and by several CTAs and thin
+    ones, which start beside those: replayed as in a loop of eager calls, alone and with another call behind it."""
+    t = t_()
+
+    def tensors():
+        g = t.Generator(device="cuda").manual_seed(5)
+        shapes = [(8, 200), (12, 1024, 800), (5, 64, 96), (2, 300, 500), (4096, 100), (3, 700, 16), (1, 1), (500, 300)]
+        p = [t.randn(s, generator=g, device="cuda") * 0.02 for s in shapes]
+        return [{"p": q, "g": t.randn(q.shape, generator=g, device="cuda"), "m": t.zeros_like(q)} for q in p]
+
+    def results(ts):
+        t.cuda.synchronize()
+        return [v.clone() for d in ts for v in (d["p"], d["m"])]
+
+    params = moe.make_muon(0.02)
+    eager_ts = tensors()
+    plan = moe.muon_tensors(eager_ts)
+    ws = moe.muon_workspace(plan)
+    for _ in range(6):
+        moe.moe_muon_step(plan, params, None, None, ws)
+    want = results(eager_ts)
+    ts = tensors()
+    plan2 = moe.muon_tensors(ts)
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        moe.moe_muon_step(plan2, params, None, None, ws)
+        moe.moe_muon_step(plan2, params, None, None, ws)
+    for _ in range(3):
+        graph.replay()
+    for got, w in zip(results(ts), want):
+        assert (got == w).all()
+    assert moe.moe_get_device_error(ws) == 0
+
+
 def test_a_workspace_serves_calls_of_all_sizes_in_turn():
     """One workspace as large as the largest call's: what one call leaves in it does not reach the next."""
     big, small = Step(6, T=2000, H=520, E=64, F=320), Step(7, T=17, H=72, E=5, F=40)
