@@ -29,8 +29,8 @@
 // pair, and the 32 KB for each SM that go with them as long at the 64 bytes a
 // cycle that L2 gives an SM (half a tile loads 24 KB); with few matrices the latency of a step, 7 us beside its MMAs.
 // Measured: a Muon step on 16 matrices of 2560 x 3584 (6.3 TFLOP in the order
-// below) 4.8 to 5.1 ms, 0.25 of them before the products, on 48 of 1408 x 4096
-// 4.9 to 5.0 and 0.47; 3 matrices of 1416 x 1001 201 us, 16 of 256 x 512 102 us,
+// below) 4.7 to 5.1 ms, 0.25 of them before the products, on 48 of 1408 x 4096
+// 4.7 to 5.0 and 0.47; 3 matrices of 1416 x 1001 201 us, 16 of 256 x 512 102 us,
 // one of 64 x 96 18 us.
 //
 // Roles per CTA: warps 0 and 10 TMA producers, one for each operand, warp 1
