@@ -22,12 +22,14 @@
 // matrices took twice as long, and those of many large ones lost their tails.
 //
 // Tiles are 256 x 256 on SM pairs (tcgen05 .cta_group::2), or 256 x 128 where
-// those would leave SMs idle; fp32 accumulators in TMEM, operands staged by TMA.  A and the short products read both operands along
-// their rows; X as the second operand of B X is read as it lies ("MN-major").
+// those would leave SMs idle; fp32 accumulators in TMEM, operands staged by TMA.
+// A and the short products read both operands along their rows; X as the second
+// operand of B X is read as it lies ("MN-major").
 //
 // What bounds it: 64 elements of a reduction take a tile's MMAs 512 cycles on a
 // pair, and the 32 KB for each SM that go with them as long at the 64 bytes a
-// cycle that L2 gives an SM (half a tile loads 24 KB); with few matrices the latency of a step, 7 us beside its MMAs.
+// cycle that L2 gives an SM (half a tile loads 24 KB); with few matrices the
+// latency of a step, 7 us beside its MMAs.
 // Measured: a Muon step on 16 matrices of 2560 x 3584 (6.3 TFLOP in the order
 // below) 4.7 to 5.1 ms, 0.25 of them before the products, on 48 of 1408 x 4096
 // 4.7 to 5.0 and 0.47; 3 matrices of 1416 x 1001 201 us, 16 of 256 x 512 102 us,
