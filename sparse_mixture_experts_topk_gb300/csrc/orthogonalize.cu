@@ -1256,6 +1256,7 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
   }
   __syncthreads();
   if (!kThin) tc::tc_fence_after();
+  if (ctas > 1) tc::cluster_arrive();   // awaited before the first store to another CTA, or where there is none
   // A call's launches of this kernel have nothing to do with one another, nor
   // with the products of larger matrices before them: but for one that opens the
   // call they start beside what is before them, and end behind it.  (What was on
@@ -1334,6 +1335,8 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
         if (x < p.left) add_square(sq, u[x]);
     });
     sq = block_sum(sq, s_w);
+    __syncwarp();
+    if (ctas > 1) tc::cluster_wait();
     if (threadIdx.x == 0) {
       for (uint32_t i = 0; i < ctas; ++i) {   // to every CTA of the cluster
         const uint32_t to = tc::map_peer(tc::smem_u32(&s_part[rank]), i);
@@ -1628,6 +1631,8 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
            }
            put4(M, S, first + a.o, even, a.left, p, v);
          });
+  } else if (ctas > 1) {
+    tc::cluster_wait();
   }
   if (!opens) pdl_wait();
   __syncwarp();
