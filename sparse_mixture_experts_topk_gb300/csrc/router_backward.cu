@@ -201,6 +201,7 @@ balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restric
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
   if (threadIdx.x == 0) s_n = 0;
   __syncthreads();
+  tc::cluster_arrive();   // awaited before the store to the first block
   pdl_enter();
   float hi = 0.f, lo = 0.f;
   int c = 0, n = 0;
@@ -236,6 +237,7 @@ balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restric
     s_term[warp] = mine < E && s_n ? (float)c / (total * (float)K) * (sum / total) : 0.f;
   }
   __syncthreads();
+  tc::cluster_wait();
   if (warp == 0) {
     float v = s_term[lane], low = 0.f;
 #pragma unroll
