@@ -141,6 +141,7 @@ router_small_kernel(const bf16* __restrict__ x, const bf16* __restrict__ Wg,
   const int G = (int)gridDim.x * kRouterWarps;
   const int units = E * nch;
   const int mine = g0 < units ? (units - 1 - g0) / G + 1 : 0;
+  tc::cluster_arrive();            // awaited before the first store to the leader
   for (int e = threadIdx.x; e < 256; e += kRouterThreads) s_hist[e] = 0;
   pdl_enter();
   uint4 gw[kSmallChunk];
@@ -159,6 +160,7 @@ router_small_kernel(const bf16* __restrict__ x, const bf16* __restrict__ Wg,
   const uint4* xv = reinterpret_cast<const uint4*>(x);
   for (int i = threadIdx.x; i < Tn * kv; i += kRouterThreads) s_x[i] = xv[i];
   __syncthreads();
+  tc::cluster_wait();
   const uint32_t lp_leader = tc::map_peer(tc::smem_u32(lp), 0);
 #pragma unroll 1
   for (int p = 0; p < mine; ++p) {

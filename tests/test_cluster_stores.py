@@ -13,7 +13,9 @@ CSRC = os.path.join(os.path.dirname(moe.__file__), "csrc")
 ACCESS = re.compile(r"\b(st_peer|ld_peer|red_peer)\w*\(")
 BARRIER = re.compile(r"\bcluster_(sync|wait)\(\)")
 
-KERNELS = [("orthogonalize.cu", "small_kernel"), ("router_backward.cu", "balance_finish_kernel")]
+KERNELS = [("orthogonalize.cu", "small_kernel"), ("router_backward.cu", "balance_finish_kernel"),
+           ("router.cu", "router_small_kernel"), ("router_tc.cu", "router_tc_kernel"),
+           ("orthogonalize.cu", "chain_kernel"), ("ffn_tc2.cu", "grouped_gemm_pair_kernel")]
 
 
 def kernel(name, function):
