@@ -543,6 +543,13 @@ int moe_router_backward(const moe_desc* desc, const void* x, const void* Wg, con
  */
 #define MOE_ORTHOGONALIZE_MAX_SIDE 32768       /* rows, cols <= this */
 #define MOE_ORTHOGONALIZE_MAX_ITERATIONS 16
+/* Testing, added to `iterations`: the first barrier of each kernel that waits
+ * for its tensor cores waits for an arrival that nobody makes (2 s); the call
+ * then ends as after any expired wait, with MOE_ERR_TIMEOUT in the workspace
+ * error word.  Each element of out, or of p and its bf16 copy, has its old value
+ * or its new one then, m the new one.  The next call in that workspace is not
+ * affected. */
+#define MOE_ORTHOGONALIZE_TEST_WAIT_TIMEOUT (1 << 30)
 
 /* Bytes of device workspace moe_orthogonalize needs for `batch` matrices (a
  * large batch runs in parts of 4 GiB; matrices of up to 128 x 4096 stay on

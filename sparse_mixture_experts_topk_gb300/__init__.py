@@ -31,7 +31,8 @@ __all__ = [
     "AdamwTensors", "adamw_tensors", "make_adamw",
     "moe_balance_loss", "moe_router_backward", "moe_router_backward_workspace_size", "router_backward_workspace",
     "moe_orthogonalize", "moe_orthogonalize_workspace_size", "orthogonalize_workspace",
-    "MOE_ORTHOGONALIZE_MAX_SIDE", "MOE_ORTHOGONALIZE_MAX_ITERATIONS", "moe_muon_step", "moe_muon_workspace_size",
+    "MOE_ORTHOGONALIZE_MAX_SIDE", "MOE_ORTHOGONALIZE_MAX_ITERATIONS", "MOE_ORTHOGONALIZE_TEST_WAIT_TIMEOUT",
+    "moe_muon_step", "moe_muon_workspace_size",
     "MoeMuonTensor", "MoeMuonParams", "MuonTensors", "muon_tensors", "make_muon", "muon_workspace",
 ]
 
@@ -57,6 +58,7 @@ MOE_ADAMW_BLOCK = 256   # elements that share a scale in 8-bit moments
 
 MOE_ORTHOGONALIZE_MAX_SIDE = 32768
 MOE_ORTHOGONALIZE_MAX_ITERATIONS = 16
+MOE_ORTHOGONALIZE_TEST_WAIT_TIMEOUT = 1 << 30   # added to the iterations: testing
 
 # status codes (MoeError.code)
 MOE_OK = 0

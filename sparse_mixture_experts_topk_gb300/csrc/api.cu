@@ -934,6 +934,9 @@ int check_matrices(const moe_muon_tensor* tensors, int32_t count) {
   return MOE_OK;
 }
 
+// Iterations without the testing flag.
+int iterations_of(int32_t v) { return v & ~(int32_t)MOE_ORTHOGONALIZE_TEST_WAIT_TIMEOUT; }
+
 bool off_by(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
 
 }  // namespace
@@ -1003,8 +1006,9 @@ int moe_orthogonalize(const void* x, int32_t x_dtype, int64_t batch, int32_t row
   t.cols = cols;
   const int rc = check_matrices(&t, 1);
   if (rc) return rc;
-  if ((x_dtype != MOE_F32 && x_dtype != MOE_BF16) || (out_dtype != MOE_F32 && out_dtype != MOE_BF16) ||
-      iterations < 1 || iterations > MOE_ORTHOGONALIZE_MAX_ITERATIONS)
+  const int n = iterations_of(iterations);
+  if ((x_dtype != MOE_F32 && x_dtype != MOE_BF16) || (out_dtype != MOE_F32 && out_dtype != MOE_BF16) || n < 1 ||
+      n > MOE_ORTHOGONALIZE_MAX_ITERATIONS)
     return MOE_ERR_INVALID;
   if (batch == 0 || rows == 0 || cols == 0) return MOE_OK;
   if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < orthogonal_workspace(&t, 1)) return MOE_ERR_WORKSPACE;
@@ -1012,8 +1016,9 @@ int moe_orthogonalize(const void* x, int32_t x_dtype, int64_t batch, int32_t row
       (x == out && x_dtype != out_dtype))
     return MOE_ERR_INVALID;
   const OrthogonalRaw raw{x, x_dtype, out, out_dtype};
-  const moe_muon_params h{0.0, 0.0, 0, iterations};
-  return cuda_status(launch_orthogonal(&t, 1, x_dtype, h, &raw, nullptr, nullptr, ws, (cudaStream_t)stream));
+  const moe_muon_params h{0.0, 0.0, 0, n};
+  return cuda_status(
+      launch_orthogonal(&t, 1, x_dtype, h, &raw, nullptr, nullptr, n != iterations, ws, (cudaStream_t)stream));
 }
 
 int moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count, size_t* bytes) {
@@ -1030,7 +1035,8 @@ int moe_muon_step(const moe_muon_tensor* tensors, int32_t count, int32_t grad_dt
   if (rc) return rc;
   if (!params || (grad_dtype != MOE_F32 && grad_dtype != MOE_BF16) || off_by(grad_scale, 4) || off_by(skip, 4))
     return MOE_ERR_INVALID;
-  const moe_muon_params& h = *params;
+  moe_muon_params h = *params;
+  h.iterations = iterations_of(h.iterations);
   // every comparison is false for a NaN
   if (!(h.lr >= 0 && h.lr < 1e30 && h.momentum >= 0 && h.momentum < 1) || (h.nesterov != 0 && h.nesterov != 1) ||
       h.iterations < 1 || h.iterations > MOE_ORTHOGONALIZE_MAX_ITERATIONS)
@@ -1047,8 +1053,8 @@ int moe_muon_step(const moe_muon_tensor* tensors, int32_t count, int32_t grad_dt
   }
   if (!any) return MOE_OK;
   if (!ws || ((uintptr_t)ws & 255u) || ws_bytes < orthogonal_workspace(tensors, count)) return MOE_ERR_WORKSPACE;
-  return cuda_status(launch_orthogonal(tensors, count, grad_dtype, h, nullptr, grad_scale, skip, ws,
-                                       (cudaStream_t)stream));
+  return cuda_status(launch_orthogonal(tensors, count, grad_dtype, h, nullptr, grad_scale, skip,
+                                       h.iterations != params->iterations, ws, (cudaStream_t)stream));
 }
 
 }  // extern "C"

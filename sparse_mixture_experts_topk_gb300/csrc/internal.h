@@ -281,7 +281,8 @@ cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, void
                                    int* err, cudaStream_t st);
 
 // Orthogonalised updates.  With `tensors` of one matrix each way round in
-// `raw`: moe_orthogonalize; else a Muon step.
+// `raw`: moe_orthogonalize; else a Muon step.  stall: testing, barriers wait for
+// an arrival that nobody makes.
 struct OrthogonalRaw {
   const void* x;
   int x_dtype;
@@ -290,8 +291,8 @@ struct OrthogonalRaw {
 };
 size_t orthogonal_workspace(const moe_muon_tensor* tensors, int count);
 cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int grad_dtype, const moe_muon_params& h,
-                              const OrthogonalRaw* raw, const float* grad_scale, const int32_t* skip, void* ws,
-                              cudaStream_t st);
+                              const OrthogonalRaw* raw, const float* grad_scale, const int32_t* skip, bool stall,
+                              void* ws, cudaStream_t st);
 
 // The statistics of a layer run in pieces of tokens: count[e] and psum[e]
 // summed over the n pieces in order, then the loss of the whole batch (s.T

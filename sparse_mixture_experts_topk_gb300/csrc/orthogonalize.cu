@@ -1218,16 +1218,17 @@ __device__ __forceinline__ float4 ld_peer_f32x4(uint32_t addr) {
 
 template <typename T, bool kThin>
 __global__ void __launch_bounds__(kSmallThreads, kThin ? 2 : 1)
-small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int* err) {
+small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int stall, int* err) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
-  __shared__ __align__(8) uint64_t s_bar;
+  __shared__ int s_abort;
+  __shared__ __align__(8) uint64_t s_bar[2];
   __shared__ Squares s_w[kSmallThreads / 32], s_part[kMostCtas];
   const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const X = smem_raw + (base - tc::smem_u32(smem_raw));   // panels of X, two of A, four of partial sums (two of B)
   uint8_t* const A = X + kSlice / 64 * kPanel;
   uint8_t* const B = A + 2 * kPanel;
-  const uint32_t sX = base, sA = sX + kSlice / 64 * kPanel, sB = sA + 2 * kPanel, bar = tc::smem_u32(&s_bar);
+  const uint32_t sX = base, sA = sX + kSlice / 64 * kPanel, sB = sA + 2 * kPanel, bar = tc::smem_u32(s_bar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, part = warp >> 2;   // TMEM lanes, and columns
   const int rank = (int)tc::cluster_ctarank();
   uint32_t ctas;
@@ -1243,7 +1244,9 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
   } else {
     if (warp == 0) {
       if (lane == 0) {
-        tc::mbar_init(bar, 1);
+        tc::mbar_init(bar, 1 + stall);
+        tc::mbar_init(bar + 8, 1);
+        s_abort = 0;
         tc::fence_barrier_init();
       }
       __syncwarp();
@@ -1266,6 +1269,7 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
   if (opens) pdl_wait();
   pdl_trigger();
   const uint32_t tmem = kThin ? 0 : s_tmem;
+  const bool issuer = !kThin && warp == 0 && tc::elect_one();   // of every MMA, and of the commits that follow them
   const bool skip = M.skip && *M.skip;   // the same for every thread of the cluster
 
   const int matrix = blockIdx.x / ctas;
@@ -1475,17 +1479,22 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
     } else {
       uint32_t phase = 0;
       // What the threads wrote to shared memory is there for the MMAs that `issue` starts; returns when they are done.
+      // On an expired wait every CTA of the cluster is told: no more MMAs are issued, none waited for, and what
+      // follows is computed on whatever is there, up to the barriers that all have to meet.
       auto products = [&](auto issue) {
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
         __syncthreads();
-        if (warp == 0 && tc::elect_one()) {
+        if (issuer && !*(volatile int*)&s_abort) {
           tc::tc_fence_after();
           issue();
           tc::tc_commit(bar);
         }
         __syncwarp();
-        if (!tc::mbar_wait(bar, phase, nullptr, kWaitNs)) set_error(err, kDevTimeout);
+        if (!tc::mbar_wait(bar, phase, &s_abort, kWaitNs)) {
+          set_error(err, kDevTimeout);
+          for (uint32_t i = 0; i < ctas; ++i) tc::st_peer_u32(tc::map_peer(tc::smem_u32(&s_abort), i), 1u);
+        }
         phase ^= 1u;
         __syncwarp();
         tc::tc_fence_after();
@@ -1606,31 +1615,34 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
       tc::tc_fence_before();
       __syncthreads();
     }
-    // p = p keep - step O, and its bf16 copy; raw: out = O
-    each([&](const At& a, float* p, float*) { get4(M, S, first + a.o, even, a.left, p); },
-         [&](const At& a, const float* p, float* v) {
-           constexpr float back = 1.f / kHeld;
-           if (kThin) {
+    // p = p keep - step O, and its bf16 copy; raw: out = O.  Not after an expired wait of this CTA, or of another
+    // one before the last sums of X X^T, for which the cluster met.
+    const bool whole = kThin || !*(volatile int*)&s_abort;
+    if (whole)
+      each([&](const At& a, float* p, float*) { get4(M, S, first + a.o, even, a.left, p); },
+           [&](const At& a, const float* p, float* v) {
+             constexpr float back = 1.f / kHeld;
+             if (kThin) {
 #pragma unroll
-             for (int x = 0; x < 4; ++x)
-               v[x] = x < a.left ? thin_x[flip ? (a.c + x) * kThinPitch + a.r : a.r * kThinPitch + a.c + x] : 0.f;
-           } else if (flip) {
+               for (int x = 0; x < 4; ++x)
+                 v[x] = x < a.left ? thin_x[flip ? (a.c + x) * kThinPitch + a.r : a.r * kThinPitch + a.c + x] : 0.f;
+             } else if (flip) {
 #pragma unroll
-             for (int x = 0; x < 4; ++x)
-               v[x] = x < a.left
-                          ? __half2float(*reinterpret_cast<const __half*>(X + panel_at(a.c + x, a.r & ~3) + (a.r & 3) * 2)) * back
-                          : 0.f;
-           } else {
-             const uint2 u = *reinterpret_cast<const uint2*>(X + panel_at(a.r, a.c));
-             const __half2* h = reinterpret_cast<const __half2*>(&u);
-             const float2 x = __half22float2(h[0]), y = __half22float2(h[1]);
-             v[0] = x.x * back;
-             v[1] = x.y * back;
-             v[2] = y.x * back;
-             v[3] = y.y * back;
-           }
-           put4(M, S, first + a.o, even, a.left, p, v);
-         });
+               for (int x = 0; x < 4; ++x)
+                 v[x] = x < a.left
+                            ? __half2float(*reinterpret_cast<const __half*>(X + panel_at(a.c + x, a.r & ~3) + (a.r & 3) * 2)) * back
+                            : 0.f;
+             } else {
+               const uint2 u = *reinterpret_cast<const uint2*>(X + panel_at(a.r, a.c));
+               const __half2* h = reinterpret_cast<const __half2*>(&u);
+               const float2 x = __half22float2(h[0]), y = __half22float2(h[1]);
+               v[0] = x.x * back;
+               v[1] = x.y * back;
+               v[2] = y.x * back;
+               v[3] = y.y * back;
+             }
+             put4(M, S, first + a.o, even, a.left, p, v);
+           });
   } else if (ctas > 1) {
     tc::cluster_wait();
   }
@@ -1638,6 +1650,11 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
   __syncwarp();
   if (ctas > 1) tc::cluster_sync();   // no CTA leaves while another may still read its shared memory
   if (!kThin && warp == 0) {
+    // after an expired wait, which may have been the other CTAs', MMAs may still run
+    if (issuer && *(volatile int*)&s_abort) {
+      tc::tc_commit(bar + 8);
+      if (!tc::mbar_wait(bar + 8, 0, nullptr, kWaitNs)) set_error(err, kDevTimeout);
+    }
     __syncwarp();
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
@@ -1831,8 +1848,8 @@ static Segment segment(const moe_muon_tensor& t, int64_t b, int64_t n, int held,
 }
 
 cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int grad_dtype, const moe_muon_params& h,
-                              const OrthogonalRaw* raw, const float* grad_scale, const int32_t* skip, void* ws,
-                              cudaStream_t st) {
+                              const OrthogonalRaw* raw, const float* grad_scale, const int32_t* skip, bool stall,
+                              void* ws, cudaStream_t st) {
   Matrices M = {};
   M.mu = (float)h.momentum;
   M.nesterov = h.nesterov != 0;
@@ -1900,7 +1917,7 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
           const bool now = opens;
           opens = false;
           return launch_kernel(kern, dim3((unsigned)(held * ctas)), dim3(kSmallThreads), smem, st, (unsigned)ctas, M,
-                               (int)h.iterations, now, (int*)ws);
+                               (int)h.iterations, now, stall ? 1 : 0, (int*)ws);
         });
     if (e != cudaSuccess) return e;
   }

@@ -264,6 +264,9 @@ __device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
 __device__ __forceinline__ void st_peer_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // Atomic add into a cluster peer's shared memory (relaxed; visible to it
 // after the next cluster barrier).
 __device__ __forceinline__ void red_peer_add_u32(uint32_t addr, uint32_t v) {
