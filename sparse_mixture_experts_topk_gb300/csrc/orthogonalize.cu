@@ -226,6 +226,7 @@ struct Chain {
   uint64_t limit;
   const int32_t* skip;
   int* err;
+  bool stall;   // testing: each pair's waits run out in one of three ways
 };
 
 // The tiles of a chain in the order in which they are taken.
@@ -404,7 +405,8 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ unsigned long long s_queue[kQueue];
+  __shared__ unsigned long long s_queue[kQueue], s_copies[4];
+  __shared__ uint32_t s_gave_up[2];
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 5];
   const uint32_t sA = (tc::smem_u32(smem_raw) + 1023u) & ~1023u, sB = sA + kStages * kOperand;
   const uint32_t sOut = sB + kStages * kOperandB;
@@ -426,10 +428,13 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
   pdl_wait();
   if (C.beside) pdl_trigger();
   if (C.skip && *C.skip) return;   // every thread of both CTAs
+  // testing: 1 = the first stage's barrier waits for an arrival that nobody makes; the first producer gives up
+  // before it has published a tile (2) or loaded one (3), so that the other CTA's roles, or its copies, are left alone
+  const int stall = C.stall ? 1 + blockIdx.x / 2 % 3 : 0;
   if (warp == 0) {
     if (lane == 0) {
       for (int s = 0; s < kStages; ++s) {
-        tc::mbar_init(full(s), 1);
+        tc::mbar_init(full(s), s == 0 && stall == 1 ? 2 : 1);
         tc::mbar_init(empty(s), 1);
       }
       for (int a = 0; a < 2; ++a) {
@@ -473,13 +478,11 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
   auto before = [&]() { return C.written + (int64_t)(T.p - 1) * C.batch + T.matrix; };
   auto need = [&]() { return T.tiles(T.p - 1) * 2 * kEpiWarps; };
 
-  uint32_t filled = 0, fill_par = 0;
-  bool producer = false;
+  uint32_t filled = 0, fill_par = 0;   // a producer's: stages filled, and the parity of each one's latest
   if (warp == 0 || warp == kSecondProducer) {
     // ------------------------------------------------------------ TMA producers (both CTAs)
     const bool second = warp == kSecondProducer;
     if (tc::elect_one()) {
-      producer = !second;
       int stage = 0, seen_p = 0, seen_m = -1;   // a step and matrix whose operands are known to be written
       uint32_t phase = 0;
       bool ok = true;
@@ -487,6 +490,10 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
       const bool takes = rank == 0 && !second;
       for (int seq = 0; ok; ++seq) {
         int t;
+        if (takes && stall == 2) {
+          ok = false;
+          break;
+        }
         if (takes) {
           // not ahead of time: while it waited here another CTA could have started it
           t = atomicAdd(C.next, 1);
@@ -496,8 +503,8 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
           t = read(seq);
           if (t >= 0) T.seek(t);
         }
-        ok = t != kAborted;
-        if (t < 0) break;
+        ok = t != kAborted && !(takes && stall == 3);
+        if (t < 0 || !ok) break;
         if (T.p > 0 && (T.p != seen_p || T.matrix != seen_m)) {
           ok = wait_written(before(), need(), &s_abort, C.limit);
           if (!ok) break;
@@ -537,6 +544,8 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
         }
       }
       if (!ok) give_up(C.err, &s_abort);
+      tc::st_peer_u64(tc::map_peer(tc::smem_u32(&s_copies[rank * 2 + second]), 0),
+                      (unsigned long long)fill_par << 32 | filled);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -725,19 +734,31 @@ chain_kernel(const __grid_constant__ Chain C, const __grid_constant__ Matrices M
     if (lane == 0 && !tc::mbar_wait(done, 0, nullptr, kWaitNs)) set_error(C.err, kDevTimeout);
     __syncwarp();
   }
-  // after an abort the leader drains its stage barriers, on which both CTAs'
-  // loads complete, before either CTA may leave; loads into a stage that it
-  // had not armed yet are given a millisecond to land
-  if (producer && s_abort) {
-    if (rank == 0)
-      for (int s = 0; s < kStages; ++s)
-        if ((filled >> s) & 1u) tc::mbar_wait(full(s), (fill_par >> s) & 1u, nullptr, kWaitNs);
-    const uint64_t t0 = tc::globaltimer();
-    while (tc::globaltimer() - t0 < 1000000ull) {
-    }
-  }
+  if (threadIdx.x < 2) tc::st_peer_u32(tc::map_peer(tc::smem_u32(&s_gave_up[rank]), threadIdx.x), (uint32_t)s_abort);
   __syncwarp();                     // the cluster's barrier takes whole warps
   tc::cluster_sync();               // neither CTA leaves while the other may still signal it
+  if (s_gave_up[0] | s_gave_up[1]) {
+    // After an abort every copy lands before either CTA leaves.  Both CTAs' are
+    // counted by the leader's stage barriers; where not all four producers have
+    // filled a stage, what is missing is made up for here.
+    if (rank == 0 && threadIdx.x == 0)
+      for (int s = 0; s < kStages; ++s) {
+        const uint32_t parity = tc::mbar_test_wait(full(s), 0) ? 1 : 0;   // of the phase that is not complete
+        uint32_t bytes = 0;
+        bool armed = false;
+        for (int i = 0; i < 4; ++i)
+          if ((s_copies[i] >> s & 1) && (s_copies[i] >> (32 + s) & 1) == parity) {
+            bytes += i & 1 ? kOperandB : kOperand;
+            armed |= i == 0;
+          }
+        if (!bytes) continue;
+        if (!armed) tc::mbar_arrive_expect_tx(full(s), bytes);
+        else if (bytes < 2 * (kOperand + kOperandB)) tc::mbar_complete_tx(full(s), 2 * (kOperand + kOperandB) - bytes);
+        if (!tc::mbar_wait(full(s), parity, nullptr, kWaitNs)) set_error(C.err, kDevTimeout);
+      }
+    __syncwarp();
+    tc::cluster_sync();
+  }
   if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_dealloc_pair(tmem, kTmemCols);
@@ -1718,8 +1739,8 @@ bool leads(const moe_muon_tensor* t, int i) {
   return true;
 }
 
-cudaError_t run_matrices(Matrices& M, const Sizes& z, int n, bool grad_bf16, int iterations, bool beside, char* ws,
-                         cudaStream_t st) {
+cudaError_t run_matrices(Matrices& M, const Sizes& z, int n, bool grad_bf16, int iterations, bool beside, bool stall,
+                         char* ws, cudaStream_t st) {
   int* err = (int*)ws;
   char* at = ws + 256;
   auto take = [&](size_t bytes) {
@@ -1745,6 +1766,7 @@ cudaError_t run_matrices(Matrices& M, const Sizes& z, int n, bool grad_bf16, int
   C.skip = M.skip;
   C.err = err;
   C.beside = beside;
+  C.stall = stall;
   for (int i = 0; i < kBuffers; ++i) {
     const bool x = i <= kY;
     if (!tma_map_16bit_3d(&C.along[i], C.buf[i], n, z.s, x ? z.L : z.s, x ? z.pitch : z.square,
@@ -1897,7 +1919,7 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
     opens = false;
     const cudaError_t e = collect(
         i, z.most(), [&](const moe_muon_tensor& t) { return large(t) && alike(tensors[i], t); },
-        [&]() { return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, i == last, (char*)ws, st); });
+        [&]() { return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, i == last, stall, (char*)ws, st); });
     if (e != cudaSuccess) return e;
   }
   for (int n = 0; n < 8; ++n) {   // the longest first
