@@ -1881,7 +1881,7 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
   M.skip = skip;
   int held = 0;   // matrices in M
   // Collects the matrices of the tensors that `which` names, from tensor i on,
-  // and has `run` run `most` of them at a time.
+  // and has `run` run `most` of them at a time; it is told which time is the last.
   auto collect = [&](int i, int64_t most, auto which, auto run) {
     M.n = held = 0;
     for (int j = i; j < count; ++j) {
@@ -1889,7 +1889,7 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
       if (!which(t)) continue;
       for (int64_t b = 0; b < t.batch;) {
         if (held == most || M.n == kSegments) {
-          const cudaError_t e = run();
+          const cudaError_t e = run(false);
           if (e != cudaSuccess) return e;
           M.n = held = 0;
         }
@@ -1899,7 +1899,7 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
         b += n;
       }
     }
-    return held ? run() : cudaSuccess;
+    return held ? run(true) : cudaSuccess;
   };
   bool opens = true;   // the call with its next launch
   // the last size before the small matrices: those start beside its products
@@ -1919,7 +1919,9 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
     opens = false;
     const cudaError_t e = collect(
         i, z.most(), [&](const moe_muon_tensor& t) { return large(t) && alike(tensors[i], t); },
-        [&]() { return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, i == last, stall, (char*)ws, st); });
+        [&](bool ends) {
+          return run_matrices(M, z, held, grad_dtype == MOE_BF16, h.iterations, i == last && ends, stall, (char*)ws, st);
+        });
     if (e != cudaSuccess) return e;
   }
   for (int n = 0; n < 8; ++n) {   // the longest first
@@ -1930,7 +1932,7 @@ cudaError_t launch_orthogonal(const moe_muon_tensor* tensors, int count, int gra
         [&](const moe_muon_tensor& t) {
           return !empty(t) && small_ctas(t) == ctas && (t.rows <= kThinSide || t.cols <= kThinSide) == thin;
         },
-        [&]() {
+        [&](bool) {
           auto kern = grad_dtype == MOE_BF16 ? thin ? small_kernel<bf16, true> : small_kernel<bf16, false>
                                              : thin ? small_kernel<float, true> : small_kernel<float, false>;
           const size_t smem = thin ? kThinSmem : kSmallSmem;
