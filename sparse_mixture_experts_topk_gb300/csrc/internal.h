@@ -274,6 +274,7 @@ int64_t router_weight_partials(const Shape& s);
 // into dbias.  panels: [T, gate_panel_cols] bf16 and alive as
 // dlogits_kernel writes them.
 int gate_panel_cols(int E);
+bool gate_skips_tiles(int E);   // whether the products leave out tiles by their flags
 int64_t gate_part_floats(const Shape& s);
 cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* panels, const uint8_t* alive,
                            float* part, const float* part_b, int rows_b, int* err, cudaStream_t st);

@@ -562,7 +562,7 @@ cudaError_t launch_router_backward(const Shape& s, const RouterBackward& b, void
   const bool tc = router_gate_on_tensor_cores(s), products = b.dx || b.dWg;
   float* out = b.dlogits || tc || !products ? b.dlogits : (float*)dl;
   bf16* panels = tc && products ? (bf16*)dl : nullptr;
-  uint8_t* alive = panels && b.mask ? (uint8_t*)(panels + s.T * gate_panel_cols(s.E)) : nullptr;
+  uint8_t* alive = panels && b.mask && gate_skips_tiles(s.E) ? (uint8_t*)(panels + s.T * gate_panel_cols(s.E)) : nullptr;
   const int64_t rows = dlogits_partials(s);
   e = by_experts(s.E, [&](auto lanes, auto vecs) {
     return launch_kernel(dlogits_kernel<decltype(lanes)::value, decltype(vecs)::value>, dim3((unsigned)rows),

@@ -80,7 +80,7 @@ struct Plan {
 struct Params {
   CUtensorMap x, wg, panel, dx;   // boxes of 128, 32, 128 and 32 rows
   const uint8_t* mask;
-  const uint8_t* alive;   // with a mask: whether tokens of a tile count
+  const uint8_t* alive;   // whether tokens of a tile count; null: all are taken
   int64_t T;
   int tiles, chunks;
   int E, H;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   constexpr int kPer = kPacked ? 2 : 1, kSlot = kPer * kHalf;
   constexpr int kD2 = 256;   // TMEM columns: D1 at 0 (and 128), D2 twice 128
   constexpr int kFlags = kRun > 1 ? 0 : kGroups == 2 ? 8 : 4;
-  const uint8_t* alive = kFlags ? P.alive : nullptr;
+  const uint8_t* alive = P.alive;
   // the producers' copies: stages filled and the parity of each one's latest
   uint32_t filled = 0, fill_par = 0;
   bool w_loaded = false;
@@ -548,6 +548,8 @@ int64_t gate_part_floats(const Shape& s) {
   return chunks * gate_splits(s) * (Plan(s.E).packed ? 2 : 1) * s.E * kCols;
 }
 int gate_panel_cols(int E) { return Plan(E).panels * 64; }
+// Not where a sum goes over several tiles: there each of them is taken.
+bool gate_skips_tiles(int E) { return E <= 128; }
 
 cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* panels, const uint8_t* alive, float* part,
                            const float* part_b, int rows_b, int* err, cudaStream_t st) {
@@ -563,7 +565,7 @@ cudaError_t launch_gate_tc(const Shape& s, const RouterBackward& b, const void* 
         !tma_map_bf16(&P.panel, panels, T, (uint64_t)plan.panels * 64, kTok))
       return cudaErrorNotSupported;
     P.mask = b.mask;
-    P.alive = b.mask ? alive : nullptr;
+    P.alive = alive;
     P.T = s.T;
     P.tiles = (int)tiles;
     P.chunks = (int)chunks;
