@@ -514,7 +514,8 @@ int moe_router_backward_workspace_size(const moe_desc* desc, size_t* bytes);
  *   dx [T, H] dtype out, or NULL each, not all.  Results are written, not added:
  *   dx goes to moe_dispatch_backward as dx_add.
  * bf16: the products run on the tensor cores, dlogits split in three bf16 parts
- * for dWg (24 bits) and two for dx (16 bits, which is rounded to 8), fp32 sums.
+ * for dWg (24 bits) and two for dx (2^-18 of each left out, less than what dx'
+ * own rounding loses), fp32 sums.
  * fp32 and MOE_FLAG_SIMT_ROUTER: CUDA cores.  Deterministic.
  */
 int moe_router_backward(const moe_desc* desc, const void* x, const void* Wg, const float* logits,

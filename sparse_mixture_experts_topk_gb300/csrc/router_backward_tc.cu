@@ -4,9 +4,12 @@
 // in one pass over x and dx, which are what it has to read and write: the
 // products themselves are E wide.
 //
-// dl comes in bf16 parts whose sum it is: high + middle for dx (16 bits, which
-// is rounded to 8), and low too for dWg (24 bits: dl itself).  A part times a
-// bf16 value is exact in the tensor cores' fp32 sums.  The parts of 64 experts
+// dl comes in bf16 parts whose sum it is: high + middle for dx, and low too for
+// dWg (24 bits: dl itself).  What dx leaves out, 2^-18 of each dl, is under half
+// of its own rounding to 8 bits even where Wg's rows are nearly alike, so that
+// most of the sum cancels (a token's dl add up to zero): rows of bf16 that differ
+// do so by 2^-8 of their size (with the low part, too, 32768 tokens of 64 experts
+// take 99.5 us instead of 98.2).  A part times a bf16 value is exact in the tensor cores' fp32 sums.  The parts of 64 experts
 // are a panel of 64 columns; up to 32 experts high and middle share one.
 //
 // A CTA takes 128 columns of H (a chunk) and walks over tiles of 128 tokens:
