@@ -191,7 +191,7 @@ def _current_stream():
 
 def _stream(stream):
     if stream is None:
-        return _current_stream()
+        return _raw_stream() if _raw_stream is not None else _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -437,19 +437,56 @@ def moe_adamw_step(tensors: AdamwTensors, params: MoeAdamwParams, grad_scale=Non
         _ptr(grad_scale), _ptr(skip), _stream(stream)))
 
 
-def _mask(fn, desc, mask):
-    # an address is taken as it is
-    if mask is not None and not isinstance(mask, int) and (mask.element_size() != 1 or mask.numel() != desc.T):
-        raise ValueError(f"{fn}: mask is not a byte for each of {desc.T} tokens")
-    return _ptr(mask)
+_f32 = _i32 = _bf16 = None
+
+
+def _types():
+    global _f32, _i32, _bf16
+    import torch
+    _f32, _i32, _bf16 = torch.float32, torch.int32, torch.bfloat16
+
+
+def _address(fn, name, t, dtype, n):
+    """The address of a tensor that holds at least n values as the call reads them; an address, or ``None``, is
+    taken as it is."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.is_cuda and t.numel() >= n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+        raise
+    return _reachable(f"{fn}: {name} is not {n} contiguous {dtype} values", t, t.dtype is dtype and t.numel() >= n)
+
+
+def _reachable(what, t, ok):
+    if not (ok and t.is_contiguous()):
+        raise ValueError(what)
+    if not (t.is_cuda or t.is_pinned()):
+        raise ValueError(what + " that the GPU reaches")
+    return t.data_ptr()
+
+
+def _mask(fn, T, mask):
+    if mask is None or isinstance(mask, int):
+        return mask
+    return _reachable(f"{fn}: mask is not a byte for each of {T} tokens, contiguous", mask,
+                      mask.element_size() == 1 and mask.numel() == T)
 
 
 def moe_balance_loss(desc, logits, ids, mask, psum, count, tokens, loss, ws, stream=None):
     """The load-balancing loss over the tokens that ``mask`` ([T] ``bool`` or
     ``uint8``, or ``None``) keeps, with its counts and probability sums."""
-    _check("moe_balance_loss", lib().moe_balance_loss(
-        ctypes.byref(desc), _ptr(logits), _ptr(ids), _mask("moe_balance_loss", desc, mask), _ptr(psum), _ptr(count),
-        _ptr(tokens), _ptr(loss), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+    if _f32 is None:
+        _types()
+    fn, T, E = "moe_balance_loss", desc.T, desc.E
+    # the results' tensors are not looked at: the host's share of a short call is most of its time
+    _check(fn, lib().moe_balance_loss(
+        ctypes.byref(desc), _address(fn, "logits", logits, _f32, T * E), _address(fn, "ids", ids, _i32, T * desc.K),
+        _mask(fn, T, mask), _ptr(psum), _ptr(count), _ptr(tokens), _ptr(loss), _ptr(ws),
+        ws.numel() if ws is not None else 0, _stream(stream)))
 
 
 def moe_router_backward_workspace_size(desc: MoeDesc) -> int:
@@ -473,10 +510,17 @@ def router_backward_workspace(desc: MoeDesc, device=None):
 
 def moe_router_backward(desc, x, Wg, logits, ids, dw, dloss, count, tokens, mask, dlogits, dWg, dgate_bias, dx, ws,
                         stream=None):
-    _check("moe_router_backward", lib().moe_router_backward(
-        ctypes.byref(desc), _ptr(x), _ptr(Wg), _ptr(logits), _ptr(ids), _ptr(dw), _ptr(dloss), _ptr(count),
-        _ptr(tokens), _mask("moe_router_backward", desc, mask), _ptr(dlogits), _ptr(dWg), _ptr(dgate_bias), _ptr(dx), _ptr(ws),
-        ws.numel() if ws is not None else 0, _stream(stream)))
+    """The gradient of the top-k weights and of the balance loss by the scores, the gate's matrix and bias, and x."""
+    if _f32 is None:
+        _types()
+    fn, T, H, E = "moe_router_backward", desc.T, desc.H, desc.E
+    TK, dt = T * desc.K, _bf16 if desc.dtype == MOE_BF16 else _f32
+    _check(fn, lib().moe_router_backward(
+        ctypes.byref(desc), _address(fn, "x", x, dt, T * H), _address(fn, "Wg", Wg, dt, E * H),
+        _address(fn, "logits", logits, _f32, T * E), _address(fn, "ids", ids, _i32, TK), _address(fn, "dw", dw, _f32, TK),
+        _address(fn, "dloss", dloss, _f32, 1), _address(fn, "count", count, _i32, E),
+        _address(fn, "tokens", tokens, _i32, 1), _mask(fn, T, mask), _ptr(dlogits), _ptr(dWg), _ptr(dgate_bias),
+        _ptr(dx), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
 
 
 def moe_orthogonalize_workspace_size(batch: int, rows: int, cols: int) -> int:
