@@ -1500,13 +1500,13 @@ small_kernel(const __grid_constant__ Matrices M, int iterations, bool opens, int
     } else {
       uint32_t phase = 0;
       // What the threads wrote to shared memory is there for the MMAs that `issue` starts; returns when they are done.
-      // On an expired wait every CTA of the cluster is told: no more MMAs are issued, none waited for, and what
-      // follows is computed on whatever is there, up to the barriers that all have to meet.
+      // On an expired wait every CTA of the cluster is told: no more MMAs are waited for, and what follows is computed
+      // on whatever is there, up to the barriers that all have to meet.
       auto products = [&](auto issue) {
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
         __syncthreads();
-        if (issuer && !*(volatile int*)&s_abort) {
+        if (issuer) {
           tc::tc_fence_after();
           issue();
           tc::tc_commit(bar);
