@@ -38,8 +38,9 @@
 //
 // What bounds it is HBM up to 32 experts (32768 tokens, H = 4096: 86 us for
 // 537 MB, 93 % of the copy rate; the prefill layer's 8192 tokens, H = 3584:
-// 20 us for 118 MB), and from 64 on the MMA thread, 2500 of a tile's 2870 cycles
-// with 64 experts (32768 tokens: 102 us).
+// 22 us for 118 MB), and from 64 on the MMA thread, 2500 of a tile's 2870 cycles
+// with 64 experts.  These are this kernel's times; with 32768 tokens of 64, 128
+// and 256 experts it takes 101, 183 and 328 us, and the call 109, 195 and 350.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
@@ -64,9 +65,9 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // How E experts are held: `groups` of 64 columns of D1; panels of a tile, `per`
 // of them in a slot of the ring.  Up to 32 experts a slot holds a tile's two
 // panels and one MMA takes both: its operand x is read from shared memory once
-// for 128 columns instead of for 64 (prefill layer 30.9 -> 28.9 us).  For 64
-// experts the three panels in a slot leave room for two tiles of x only (104.7
-// instead of 102.7 us for 32768 padded tokens), so slots hold one.
+// for 128 columns instead of for 64 (the prefill layer's call 30.9 -> 28.9 us).
+// For 64 experts the three panels in a slot leave room for two tiles of x only
+// (the call on 32768 padded tokens, 102.7 us then, 104.7), so slots hold one.
 struct Plan {
   int E, groups, panels;
   bool packed;      // up to 32 experts: panels [high | middle] and [low | 0]
@@ -206,7 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) gate_kernel(const __grid_constant
   // that kernel.
   if (warp != 0 || P.alive) pdl_wait();
   // No early start for the sums behind it: beside this kernel they cost more
-  // than their launch (32768 tokens 101.7 -> 99.9 us, prefill 29.2 -> 28.4).
+  // than their launch (the call on 32768 padded tokens 99.7 -> 98.3 us, on the
+  // prefill layer 28.9 -> 28.1).
   const uint32_t tmem = s_tmem;
   const int chunk = blockIdx.x % P.chunks, h0 = chunk * kCols;
   const int first = blockIdx.x / P.chunks, splits = gridDim.x / P.chunks;
